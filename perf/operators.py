@@ -1,0 +1,582 @@
+"""The operators of the dense side of a training and serving step, as calls to measure.
+
+Three operators work on what the embedding layer's lookups feed: the attention of a user's event
+sequence to its own recent events (a sliding window) and its first few (sinks), in training form
+forward and backward over ragged CSR sequences and in serving form for one new event per user; the
+norms before and after such a block fused with its gate and residual scale, forward and backward;
+and an AdamW step over all dense weights at once, with fp32 states or states in 8 bits.
+
+`run` computes them in elementary torch operations, or, where `own` is true, by this package's calls.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+if own:
+    from ad_recommendation_amd import dense
+
+DEV = "cuda"
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ---------------------------------------------------------------------------------- the cases
+def listed():
+    return [
+        # one ranking request: the short histories of a few users, where latency counts
+        dict(name="attn_fwd_request", op="attn_fwd", dtype="f16", n_seq=16, max_len=50, q_heads=4,
+             kv_heads=4, dim=32, window=32, sinks=2, packed=True),
+        # lifelong histories in a training step, grouped heads
+        dict(name="attn_fwd_long", op="attn_fwd", dtype="bf16", n_seq=5, max_len=8191, q_heads=16,
+             kv_heads=2, dim=128, window=1024, sinks=4, packed=True),
+        # a training batch of ordinary histories, very ragged
+        dict(name="attn_bwd_history", op="attn_bwd", dtype="f16", n_seq=512, max_len=200,
+             q_heads=8, kv_heads=8, dim=64, window=64, sinks=4, packed=True),
+        # the backward of lifelong histories, grouped heads
+        dict(name="attn_bwd_long", op="attn_bwd", dtype="bf16", n_seq=5, max_len=4095, q_heads=16,
+             kv_heads=8, dim=128, window=1024, sinks=4, packed=False),
+        # one new event for a few users
+        dict(name="decode_few", op="decode", dtype="f16", n_seq=3, capacity=4096, q_heads=8,
+             kv_heads=2, dim=64, window=1000, sinks=4),
+        # one new event for every user of a serving batch
+        dict(name="decode_batch", op="decode", dtype="bf16", n_seq=256, capacity=8192, q_heads=32,
+             kv_heads=8, dim=128, window=4096, sinks=4),
+        # between two blocks of one ranking request
+        dict(name="norm_fwd_request", op="norm_fwd", dtype="f16", rows=100, dim=256, gate="row"),
+        # between two blocks of a training step
+        dict(name="norm_fwd_batch", op="norm_fwd", dtype="bf16", rows=32768, dim=2048, gate="vec"),
+        # its backward in 32 bits at the odd sizes of a ragged batch
+        dict(name="norm_bwd_odd", op="norm_bwd", dtype="f32", rows=5003, dim=333, gate="row"),
+        # its backward in a training step
+        dict(name="norm_bwd_batch", op="norm_bwd", dtype="bf16", rows=20011, dim=2048, gate="vec"),
+        # a ranking tower over 26 fields of 16 columns, all in 32 bits: many small tensors
+        dict(name="adamw_tower", op="adamw", states="f32", grad="f32", copy=False, layers=12,
+             width=416),
+        # the dense weights of a large sequence model, 8-bit states and half-precision copies
+        dict(name="adamw_q8_large", op="adamw", states="q8", grad="bf16", copy=True, layers=8,
+             width=2048),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["attn_fwd", "attn_bwd", "decode", "norm_fwd", "norm_bwd", "adamw"])
+    if op in ("attn_fwd", "attn_bwd"):
+        kv = rng.choice([1, 2, 4, 8])
+        max_len = _log(rng, 20, 4000)
+        return dict(op=op, dtype=rng.choice(["f16", "bf16"]),
+                    n_seq=max(1, min(_log(rng, 1, 512), 12000 // max_len)), max_len=max_len,
+                    q_heads=kv * rng.choice([1, 2]), kv_heads=kv,
+                    dim=rng.choice([16, 32, 40, 64, 80, 128]), window=_log(rng, 1, 2000),
+                    sinks=rng.randint(0, 16), packed=rng.random() < 0.5)
+    if op == "decode":
+        kv = rng.choice([1, 2, 4, 8])
+        return dict(op=op, dtype=rng.choice(["f16", "bf16"]), n_seq=_log(rng, 1, 200),
+                    capacity=_log(rng, 16, 8000), q_heads=kv * rng.choice([1, 2, 3, 4]),
+                    kv_heads=kv, dim=rng.choice([16, 32, 40, 64, 80, 128]),
+                    window=_log(rng, 1, 4000), sinks=rng.randint(0, 16))
+    if op in ("norm_fwd", "norm_bwd"):
+        return dict(op=op, dtype=rng.choice(["f16", "bf16", "f32"]), rows=_log(rng, 1, 16000),
+                    dim=_log(rng, 16, 2500), gate=rng.choice(["vec", "row", "none"]))
+    return dict(op=op, states=rng.choice(["f32", "q8"]), grad=rng.choice(["f32", "f16", "bf16"]),
+                copy=rng.random() < 0.5, layers=rng.randint(1, 12), width=_log(rng, 16, 1500))
+
+
+# ---------------------------------------------------------------------------------- their sizes
+def _lens(case, most):
+    """Lengths spread from none to the longest, in a fixed shuffled order."""
+    n = case["n_seq"]
+    a = np.round(most * ((np.arange(n) + 0.5) / n) ** 1.5).astype(np.int64)
+    a[-1] = most
+    if n > 2:
+        a[0] = 0
+    return np.random.RandomState(n).permutation(a)
+
+
+def _pairs(lens, window, sinks):
+    """Query-key pairs that see each other in causal sequences of these lengths."""
+    total = 0
+    for n in lens.tolist():
+        seen = np.minimum(np.arange(1, n + 1), window)
+        total += int(seen.sum() + np.minimum(np.arange(1, n + 1) - seen, sinks).sum())
+    return total
+
+
+def _shapes(case):
+    """The dense weights: per layer two square matrices, one to four times the width and back, and
+    the vectors beside them."""
+    w = case["width"]
+    per = [(w, w), (w, w), (w, 4 * w), (4 * w, w), (4 * w,), (w,), (w,), (w + 1,)]
+    return per * case["layers"]
+
+
+BLOCK = 128  # the state arrays give every tensor whole blocks of this many elements
+
+
+def _starts(case):
+    sizes = [math.prod(s) for s in _shapes(case)]
+    ends = np.cumsum([-(-n // BLOCK) * BLOCK for n in sizes])
+    return sizes, [0] + ends[:-1].tolist(), int(ends[-1])
+
+
+def work(case):
+    op = case["op"]
+    if op in ("attn_fwd", "attn_bwd"):
+        lens = _lens(case, case["max_len"])
+        t, d = int(lens.sum()), case["dim"]
+        q, kv = t * case["q_heads"] * d * 2, t * case["kv_heads"] * d * 2
+        pairs = _pairs(lens, case["window"], case["sinks"]) * case["q_heads"]
+        lse = t * case["q_heads"] * 4
+        if op == "attn_fwd":
+            return {"bytes": 2 * q + 2 * kv + lse, "flops": 4 * d * pairs}
+        return {"bytes": 4 * q + 4 * kv + lse, "flops": 10 * d * pairs}
+    if op == "decode":
+        lens = _lens(case, case["capacity"])
+        seen = np.minimum(lens, case["window"])
+        seen = int((seen + np.minimum(lens - seen, case["sinks"])).sum())
+        d = case["dim"]
+        return {"bytes": 4 * seen * case["kv_heads"] * d + 4 * case["n_seq"] * case["q_heads"] * d,
+                "flops": 4 * d * seen * case["q_heads"]}
+    if op in ("norm_fwd", "norm_bwd"):
+        e = 4 if case["dtype"] == "f32" else 2
+        n = case["rows"] * case["dim"]
+        rows = (4 if op == "norm_fwd" else 6) * n
+        if case["gate"] == "row":
+            rows += n if op == "norm_fwd" else 2 * n
+        return {"bytes": rows * e + 16 * case["dim"], "flops": (10 if op == "norm_fwd" else 25) * n}
+    n = sum(_starts(case)[0])
+    state = 16 if case["states"] == "f32" else 4 + 4 / BLOCK
+    return {"bytes": n * (8 + (4 if case["grad"] == "f32" else 2) + state + (2 if case["copy"] else 0)),
+            "flops": 15 * n}
+
+
+# ---------------------------------------------------------------------------------- the inputs
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _attn_inputs(case, seed):
+    t = TYPES[case["dtype"]]
+    g = _gen(seed)
+    lens = _lens(case, case["max_len"])
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    n, hq, hk, d = int(off[-1]), case["q_heads"], case["kv_heads"], case["dim"]
+    x = torch.randn(n, hq + 2 * hk, d, generator=g, device=DEV).to(t)
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]  # views of one projection's output
+    if not case["packed"]:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    return dict(case=case, q=q, k=k, v=v, offsets=torch.from_numpy(off).to(DEV),
+                max_len=int(lens.max()), scale=d ** -0.5)
+
+
+def prepare(case, seed):
+    op = case["op"]
+    if op in ("attn_fwd", "attn_bwd"):
+        s = _attn_inputs(case, seed)
+        out_shape = s["q"].shape
+        s["lse"] = torch.empty(out_shape[1], out_shape[0], dtype=torch.float32, device=DEV)
+        s["out"] = torch.empty(out_shape, dtype=s["q"].dtype, device=DEV)
+        if op == "attn_bwd":
+            s["out"], s["lse"] = _attn_fwd(s)
+            s["dout"] = torch.randn(out_shape, generator=_gen(seed + 7), device=DEV).to(s["q"].dtype)
+            s["dq"] = torch.empty(out_shape, dtype=s["q"].dtype, device=DEV)
+            s["dk"] = torch.empty(s["k"].shape, dtype=s["q"].dtype, device=DEV)
+            s["dv"] = torch.empty(s["k"].shape, dtype=s["q"].dtype, device=DEV)
+        return s
+    if op == "decode":
+        t, g = TYPES[case["dtype"]], _gen(seed)
+        n, cap, hk, d = case["n_seq"], case["capacity"], case["kv_heads"], case["dim"]
+        make = lambda *shape: torch.empty(*shape, dtype=t, device=DEV).normal_(generator=g)  # noqa: E731
+        return dict(case=case, q=make(n, case["q_heads"], d), k=make(n, cap, hk, d),
+                    v=make(n, cap, hk, d),
+                    lens=torch.from_numpy(_lens(case, cap).astype(np.int32)).to(DEV),
+                    out=torch.empty(n, case["q_heads"], d, dtype=t, device=DEV), scale=d ** -0.5)
+    if op in ("norm_fwd", "norm_bwd"):
+        t, g, n, d = TYPES[case["dtype"]], _gen(seed), case["rows"], case["dim"]
+        make = lambda *shape: torch.randn(*shape, generator=g, device=DEV).to(t)  # noqa: E731
+        gate = {"vec": lambda: 0.5 * make(d), "row": lambda: 0.5 * make(n, d), "none": lambda: None}
+        s = dict(case=case, y=3 * make(n, d), gate=gate[case["gate"]](), alpha=0.8, eps=1e-6,
+                 w_post=1 + 0.1 * torch.randn(d, generator=g, device=DEV),
+                 w_pre=1 + 0.1 * torch.randn(d, generator=g, device=DEV))
+        new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
+        if op == "norm_fwd":
+            s.update(x=make(n, d), r=new(s["y"]), h=new(s["y"]))
+        else:
+            s.update(r=make(n, d), dr=make(n, d), dh=make(n, d), dx=new(s["y"]), dy=new(s["y"]),
+                     dw_post=new(s["w_post"]), dw_pre=new(s["w_pre"]),
+                     dgate=new(s["w_post"]) if case["gate"] == "vec" else new(s["gate"]))
+        return s
+    g, t = _gen(seed), TYPES[case["grad"]]
+    shapes, (sizes, starts, total) = _shapes(case), _starts(case)
+    w = torch.zeros(total, device=DEV)
+    c = torch.zeros(total, dtype=torch.bfloat16 if t == torch.float32 else t, device=DEV)
+    cut = lambda flat: [flat[a:a + n].view(s) for s, n, a in zip(shapes, sizes, starts)]  # noqa: E731
+    s = dict(case=case, flat=w, weights=cut(w), copy_flat=c if case["copy"] else None,
+             copies=cut(c) if case["copy"] else None, step=10, lr=1e-3, beta1=0.9, beta2=0.999,
+             eps=1e-8, weight_decay=0.01, seed=seed * 1000003, sizes=sizes, starts=starts)
+    for x in s["weights"]:
+        x.normal_(std=0.02, generator=g)
+    s["grads"] = [(torch.randn(x, generator=g, device=DEV) * 1e-3).to(t) for x in shapes]
+    inside = torch.zeros(total, device=DEV)
+    for a, n in zip(starts, sizes):
+        inside[a:a + n] = 1
+    m = torch.empty(total, device=DEV).normal_(std=3e-4, generator=g) * inside
+    r = (torch.empty(total, device=DEV).normal_(std=1e-3, generator=g).abs() + 1e-4) * inside
+    if case["states"] == "f32":
+        s["m"], s["v"] = m, r * r
+    else:  # the first moment and the root of the second, an exponent of two for each block
+        s["m"], s["m_exp"] = _to_blocks(m)
+        s["v"], s["v_exp"] = _to_blocks(r)
+    return s
+
+
+# ---------------------------------------------------------------------------------- plain forms
+def _padded(s):
+    """The sequences side by side: where each place takes its token from, and which places are."""
+    off = s["offsets"].long()
+    at = torch.arange(s["max_len"], device=DEV)
+    there = at < (off[1:] - off[:-1])[:, None]
+    return torch.where(there, off[:-1, None] + at, 0), there
+
+
+def _visible(s, there):
+    at = torch.arange(s["max_len"], device=DEV)
+    back = at[:, None] - at
+    see = (back >= 0) & ((back < s["case"]["window"]) | (at < s["case"]["sinks"]))
+    return see & there[:, None, None, :]
+
+
+def _heads(x, idx, groups):
+    """[tokens, heads, dim] to [sequences, kv heads, group * length, dim] in 32 bits."""
+    b, n = idx.shape
+    x = x[idx].float().reshape(b, n, -1, groups, x.shape[-1])
+    return x.permute(0, 2, 3, 1, 4).reshape(b, x.shape[2], groups * n, x.shape[-1])
+
+
+def _tokens(x, s, there, groups):
+    """The way back."""
+    b, n = there.shape
+    x = x.reshape(b, -1, groups, n, x.shape[-1]).permute(0, 3, 1, 2, 4)
+    return x.reshape(b, n, -1, x.shape[-1])[there].to(s["q"].dtype)
+
+
+def _scores(s):
+    idx, there = _padded(s)
+    groups = s["q"].shape[1] // s["k"].shape[1]
+    q, k, v = _heads(s["q"], idx, groups), _heads(s["k"], idx, 1), _heads(s["v"], idx, 1)
+    see = _visible(s, there).repeat(1, 1, groups, 1)
+    p = (q @ k.transpose(2, 3)).mul_(s["scale"]).masked_fill_(~see, -math.inf)
+    return idx, there, groups, q, k, v, p
+
+
+def _attn_fwd(s):
+    idx, there, groups, q, k, v, p = _scores(s)
+    b, n = there.shape
+    m = p.amax(-1, keepdim=True)
+    m = torch.where(m == -math.inf, 0, m)
+    p = p.sub_(m).exp_()
+    l = p.sum(-1, keepdim=True)
+    out = _tokens(p @ v / torch.where(l == 0, 1, l), s, there, groups)
+    lse = (m + l.log()).reshape(b, -1, groups, n).permute(0, 3, 1, 2).reshape(b, n, -1)[there]
+    return out, lse.t().contiguous()
+
+
+def _attn_bwd(s):
+    idx, there, groups, q, k, v, p = _scores(s)
+    b, n = there.shape
+    lse = s["lse"].t()[idx].reshape(b, n, -1, groups).permute(0, 2, 3, 1).reshape(b, -1, groups * n, 1)
+    p = p.sub_(lse).exp_()
+    live = there[:, None, :, None].repeat(1, 1, groups, 1)
+    do = _heads(s["dout"], idx, groups) * live
+    delta = (do * _heads(s["out"], idx, groups)).sum(-1, keepdim=True)
+    p = p * live
+    dv = p.transpose(2, 3) @ do
+    ds = (do @ v.transpose(2, 3)).sub_(delta).mul_(p).mul_(s["scale"])
+    dq, dk = ds @ k, ds.transpose(2, 3) @ q
+    return _tokens(dq, s, there, groups), _tokens(dk, s, there, 1), _tokens(dv, s, there, 1)
+
+
+def _decode(s):
+    c, lens = s["case"], s["lens"].long()[:, None]
+    n, hk, d = c["n_seq"], c["kv_heads"], c["dim"]
+    first = torch.clamp(lens - c["window"], min=0)
+    sinks = torch.arange(min(c["sinks"], c["capacity"]), device=DEV).expand(n, -1)
+    recent = first + torch.arange(min(c["window"], c["capacity"]), device=DEV)
+    idx = torch.cat([sinks, recent], 1)
+    see = torch.cat([sinks < first, recent < lens], 1)[:, None, None, :]
+    idx = idx.clamp(max=c["capacity"] - 1)
+    rows = torch.arange(n, device=DEV)[:, None]
+    k = s["k"][rows, idx].float().permute(0, 2, 1, 3)
+    v = s["v"][rows, idx].float().permute(0, 2, 1, 3)
+    q = s["q"].float().reshape(n, hk, -1, d)
+    p = (q @ k.transpose(2, 3) * s["scale"]).masked_fill(~see, -math.inf)
+    m = p.amax(-1, keepdim=True)
+    p = (p - torch.where(m == -math.inf, 0, m)).exp()
+    l = p.sum(-1, keepdim=True)
+    return (p @ v / torch.where(l == 0, 1, l)).reshape(n, -1, d).to(s["q"].dtype)
+
+
+def _norm_fwd(s):
+    t = s["y"].dtype
+    y = s["y"].float()
+    y = y * torch.rsqrt((y * y).mean(-1, keepdim=True) + s["eps"]) * s["w_post"]
+    r = s["alpha"] * s["x"].float() + (y if s["gate"] is None else s["gate"].float() * y)
+    h = r * torch.rsqrt((r * r).mean(-1, keepdim=True) + s["eps"]) * s["w_pre"]
+    return r.to(t), h.to(t)
+
+
+def _norm_bwd(s):
+    t = s["y"].dtype
+    r, y, dh = s["r"].float(), s["y"].float(), s["dh"].float()
+    inv = torch.rsqrt((r * r).mean(-1, keepdim=True) + s["eps"])
+    rn, u = r * inv, dh * s["w_pre"]
+    dr = s["dr"].float() + inv * (u - rn * (u * rn).mean(-1, keepdim=True))
+    iny = torch.rsqrt((y * y).mean(-1, keepdim=True) + s["eps"])
+    yn = y * iny
+    dn = dr if s["gate"] is None else s["gate"].float() * dr
+    z = dn * s["w_post"]
+    dy = iny * (z - yn * (z * yn).mean(-1, keepdim=True))
+    got = [(s["alpha"] * dr).to(t), dy.to(t), _rows_sum(dn * yn), _rows_sum(dh * rn)]
+    if s["gate"] is not None:
+        dg = dr * yn * s["w_post"]
+        got.append(_rows_sum(dg) if s["gate"].dim() == 1 else dg.to(t))
+    return got
+
+
+def _rows_sum(x):
+    return x.double().sum(0).float()  # a long sum
+
+
+def _hash(seed, n):
+    """32 random bits for each element of the state arrays, from the seed and its index."""
+    def mix(x):
+        x = ((x ^ (x >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
+        x = ((x ^ (x >> 13)) * 0xC2B2AE35) & 0xFFFFFFFF
+        return x ^ (x >> 16)
+    e = torch.arange(n, device=DEV)
+    lo, hi = seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF
+    base = mix((mix(lo) ^ hi) ^ ((e >> 32) * 0x9E3779B1 & 0xFFFFFFFF))
+    return mix((e + base) & 0xFFFFFFFF)
+
+
+def _to_blocks(x, bits=None, keep=False):
+    """8-bit codes (e4m3) of x and the exponent of two, plus 127, of each block of 128. The values
+    of a block are scaled to below 256; `bits`: 16 random bits that round up or down each value,
+    the nearest without them; `keep`: what is not zero does not become zero."""
+    x = x.reshape(-1, BLOCK)
+    most = x.abs().amax(-1, keepdim=True)
+    k = torch.where(most > 0, torch.frexp(most)[1] - 8, -127).clamp(min=-127)
+    y = torch.ldexp(x.abs(), -k)
+    e = (torch.frexp(y)[1] - 1).clamp(min=-6)
+    u = 0.5 if bits is None else (bits.reshape(-1, BLOCK).float() + 0.5) / 65536
+    q = torch.floor(torch.ldexp(y, 3 - e) + u)
+    if keep:
+        q = torch.where(y > 0, q.clamp(min=1), q)
+    q = torch.ldexp(q, e - 3) * torch.sign(x)
+    return q.reshape(-1).to(torch.float8_e4m3fn), (k.reshape(-1) + 127).to(torch.uint8)
+
+
+def _of_blocks(code, exp):
+    return torch.ldexp(code.float().reshape(-1, BLOCK), exp.int()[:, None] - 127).reshape(-1)
+
+
+def _adamw(s):
+    cat = lambda parts: torch.cat([x for p, n in zip(parts, s["sizes"]) for x in (  # noqa: E731
+        p.reshape(-1), p.new_zeros(-n % BLOCK))])
+    q8 = s["case"]["states"] == "q8"
+    g = cat(s["grads"]).float()
+    m = (_of_blocks(s["m"], s["m_exp"]) if q8 else s["m"]) * s["beta1"] + g * (1 - s["beta1"])
+    v = (_of_blocks(s["v"], s["v_exp"]) ** 2 if q8 else s["v"]) * s["beta2"] + g * g * (1 - s["beta2"])
+    root = v.sqrt()
+    c1, c2 = 1 - s["beta1"] ** s["step"], math.sqrt(1 - s["beta2"] ** s["step"])
+    w = s["flat"]
+    w.sub_(s["lr"] * (m / c1 / (root / c2 + s["eps"]) + s["weight_decay"] * w))
+    if s["copies"] is not None:
+        s["copy_flat"].copy_(w)
+    if not q8:
+        s["m"].copy_(m)
+        s["v"].copy_(v)
+        return
+    bits = _hash(s["seed"] + s["step"], m.numel())
+    for name, x, b, keep in (("m", m, bits & 0xFFFF, False), ("v", root, bits >> 16, True)):
+        code, exp = _to_blocks(x, b, keep)
+        s[name].view(torch.uint8).copy_(code.view(torch.uint8))
+        s[name + "_exp"].copy_(exp)
+
+
+# ---------------------------------------------------------------------------------- one pass
+def run(s):
+    c = s["case"]
+    op = c["op"]
+    if op == "attn_fwd":
+        if own:
+            dense.attn_window_fwd(s["q"], s["k"], s["v"], s["offsets"], c["window"], c["sinks"],
+                                  s["scale"], s["out"], s["lse"])
+            return s["out"], s["lse"]
+        return _attn_fwd(s)
+    if op == "attn_bwd":
+        if own:
+            ws = torch.empty(dense.attn_window_bwd_workspace_bytes(
+                s["q"].shape[0], c["n_seq"], c["q_heads"], c["kv_heads"], c["dim"], c["sinks"]),
+                dtype=torch.uint8, device=DEV)
+            dense.attn_window_bwd(s["q"], s["k"], s["v"], s["offsets"], c["window"], c["sinks"],
+                                  s["scale"], s["out"], s["lse"], s["dout"], s["dq"], s["dk"],
+                                  s["dv"], ws)
+            return s["dq"], s["dk"], s["dv"]
+        return _attn_bwd(s)
+    if op == "decode":
+        if own:
+            ws = torch.empty(dense.attn_window_decode_workspace_bytes(
+                c["n_seq"], c["capacity"], c["q_heads"], c["kv_heads"], c["dim"], c["window"],
+                c["sinks"]), dtype=torch.uint8, device=DEV)
+            dense.attn_window_decode(s["q"], s["k"], s["v"], s["lens"], c["window"], c["sinks"],
+                                     s["scale"], s["out"], ws)
+            return s["out"]
+        return _decode(s)
+    if op == "norm_fwd":
+        if own:
+            dense.norm_gate_residual_fwd(s["x"], s["y"], s["gate"], s["w_post"], s["w_pre"],
+                                         s["alpha"], s["eps"], s["r"], s["h"])
+            return s["r"], s["h"]
+        return _norm_fwd(s)
+    if op == "norm_bwd":
+        if own:
+            ws = torch.empty(dense.norm_gate_residual_bwd_workspace_bytes(c["rows"], c["dim"]),
+                             dtype=torch.uint8, device=DEV)
+            dense.norm_gate_residual_bwd(s["r"], s["y"], s["gate"], s["w_post"], s["w_pre"],
+                                         s["alpha"], s["eps"], s["dr"], s["dh"], s["dx"], s["dy"],
+                                         s["dgate"], s["dw_post"], s["dw_pre"], ws)
+            got = [s["dx"], s["dy"], s["dw_post"], s["dw_pre"]]
+            return got if s["dgate"] is None else got + [s["dgate"]]
+        return _norm_bwd(s)
+    s["step"] += 1
+    if own:
+        more = dict(copies=s["copies"])
+        args = (s["step"], s["lr"], s["beta1"], s["beta2"], s["eps"], s["weight_decay"])
+        if c["states"] == "q8":
+            dense.adamw_step_q8(s["weights"], s["grads"], s["m"], s["m_exp"], s["v"], s["v_exp"],
+                                *args, seed=s["seed"] + s["step"], **more)
+        else:
+            dense.adamw_step(s["weights"], s["grads"], s["m"], s["v"], *args, **more)
+    else:
+        _adamw(s)
+    got = [s["flat"]] if s["copies"] is None else [s["flat"], s["copy_flat"]]
+    if c["states"] == "f32":
+        return got + [s["m"], s["v"]]
+    # a code times a power of two has four significant bits: bf16 holds it as it is
+    for code, exp in ((s["m"], s["m_exp"]), (s["v"], s["v_exp"])):
+        if own:
+            got.append(torch.empty(code.numel(), dtype=torch.bfloat16, device=DEV))
+            dense.adamw_q8_values(code, exp, got[-1])
+        else:
+            got.append(_of_blocks(code, exp).bfloat16())
+    return got
+
+
+# ---------------------------------------------------------------------------------- in 64 bits
+def exact(case, seed):
+    s, op = prepare(case, seed), case["op"]
+    if op in ("attn_fwd", "attn_bwd"):
+        return _exact_attn(case, s, op == "attn_bwd")
+    if op == "decode":
+        out, group = torch.zeros(s["q"].shape, dtype=torch.float64, device=DEV), case["q_heads"] // case["kv_heads"]
+        for b, n in enumerate(s["lens"].tolist()):
+            j = torch.arange(n, device=DEV)
+            j = j[(j >= n - case["window"]) | (j < case["sinks"])]
+            for h in range(case["q_heads"] if n else 0):
+                k, v = s["k"][b, j, h // group].double(), s["v"][b, j, h // group].double()
+                out[b, h] = torch.softmax(k @ s["q"][b, h].double() * s["scale"], 0) @ v
+        return out
+    if op == "norm_fwd":
+        rms = lambda x, w: x / (x.pow(2).mean(1, keepdim=True) + s["eps"]).sqrt() * w.double()  # noqa: E731
+        n = rms(s["y"].double(), s["w_post"])
+        r = s["x"].double() * s["alpha"] + n * (1.0 if s["gate"] is None else s["gate"].double())
+        return r, rms(r, s["w_pre"])
+    if op == "norm_bwd":
+        # by the chain rule of the two norms, each as its Jacobian applied to a vector
+        def back(x, w, d):
+            q = (x.pow(2).mean(1, keepdim=True) + s["eps"]).sqrt()
+            return (d * w) / q - x * ((d * w * x).mean(1, keepdim=True) / q.pow(3)), (d * x / q).sum(0), x / q
+        r, y = s["r"].double(), s["y"].double()
+        into, dw_pre, _ = back(r, s["w_pre"].double(), s["dh"].double())
+        dr = s["dr"].double() + into
+        gate = 1.0 if s["gate"] is None else s["gate"].double()
+        dy, dw_post, unit = back(y, s["w_post"].double(), dr * gate)
+        got = [dr * s["alpha"], dy, dw_post, dw_pre]
+        dg = dr * unit * s["w_post"].double()
+        return got + ([] if s["gate"] is None else [dg.sum(0) if s["gate"].dim() == 1 else dg])
+    return _exact_adamw(case, s)
+
+
+def _exact_attn(case, s, bwd):
+    group, dev = case["q_heads"] // case["kv_heads"], DEV
+    wide = lambda x: torch.zeros(x.shape, dtype=torch.float64, device=dev)  # noqa: E731
+    out, lse, dq, dk, dv = wide(s["q"]), wide(s["lse"]), wide(s["q"]), wide(s["k"]), wide(s["k"])
+    off = s["offsets"].tolist()
+    for a, z in zip(off[:-1], off[1:]):
+        i = torch.arange(z - a, device=dev)
+        hidden = (i[None] > i[:, None]) | ((i[None] <= i[:, None] - case["window"]) & (i[None] >= case["sinks"]))
+        for h in range(case["q_heads"] if z > a else 0):
+            q, k, v = s["q"][a:z, h].double(), s["k"][a:z, h // group].double(), s["v"][a:z, h // group].double()
+            score = (q @ k.T * s["scale"]).masked_fill_(hidden, -math.inf)
+            lse[h, a:z] = torch.logsumexp(score, 1)
+            p = torch.softmax(score, 1)
+            out[a:z, h] = p @ v
+            if bwd:
+                do = s["dout"][a:z, h].double()
+                dp = do @ v.T
+                ds = p * (dp - (p * dp).sum(1, keepdim=True)) * s["scale"]
+                dq[a:z, h] = ds @ k
+                dk[a:z, h // group] += ds.T @ q
+                dv[a:z, h // group] += p.T @ do
+    return (dq, dk, dv) if bwd else (out, lse)
+
+
+def _exact_adamw(case, s):
+    t, q8 = s["step"] + 1, case["states"] == "q8"
+    u = lambda x: x & 0xFFFFFFFF  # noqa: E731
+
+    def finish(x):
+        for shift, factor in ((16, 0x85EBCA6B), (13, 0xC2B2AE35)):
+            x = u((x ^ (x >> shift)) * factor)
+        return x ^ (x >> 16)
+
+    def stored(x, up, keep):
+        """Each block's values rounded to one of the two codes beside them."""
+        x = torch.cat([x, x.new_zeros(-x.numel() % BLOCK)]).view(-1, BLOCK)
+        top = x.abs().amax(1, keepdim=True)
+        scale = torch.where(top > 0, 2.0 ** (torch.floor(torch.log2(top.clamp(min=1e-38))) - 7), 2.0 ** -127)
+        y = x.abs() / scale
+        step = 2.0 ** (torch.floor(torch.log2(y.clamp(min=2.0 ** -6))) - 3)
+        n = torch.floor(y / step + up.view(-1, BLOCK))
+        n = torch.where((y > 0) & (n == 0), 1.0, n) if keep else n
+        return (n * step * scale * torch.sign(x)).view(-1)
+
+    w_all = torch.zeros(s["flat"].numel(), dtype=torch.float64, device=DEV)
+    m_all, v_all = torch.zeros_like(w_all), torch.zeros_like(w_all)
+    base = finish(finish(torch.tensor(u(s["seed"] + t))) ^ u((s["seed"] + t) >> 32)).item()
+    for w, g, a, n in zip(s["weights"], s["grads"], s["starts"], s["sizes"]):
+        end = a + -(-n // BLOCK) * BLOCK
+        w, g = w.reshape(-1).double(), g.reshape(-1).double()
+        if q8:
+            scale = lambda e: 2.0 ** (e[a // BLOCK:end // BLOCK].double() - 127)  # noqa: E731
+            m = (s["m"][a:end].double().view(-1, BLOCK) * scale(s["m_exp"])[:, None]).view(-1)[:n]
+            v = (s["v"][a:end].double().view(-1, BLOCK) * scale(s["v_exp"])[:, None]).view(-1)[:n] ** 2
+        else:
+            m, v = s["m"][a:a + n].double(), s["v"][a:a + n].double()
+        m = m + (g - m) * (1 - s["beta1"])
+        v = v + (g * g - v) * (1 - s["beta2"])
+        mh, vh = m / (1 - s["beta1"] ** t), v / (1 - s["beta2"] ** t)
+        w_all[a:a + n] = w * (1 - s["lr"] * s["weight_decay"]) - s["lr"] * mh / (vh.sqrt() + s["eps"])
+        if q8:  # the arrays hold fewer than 2^32 elements here
+            bits = finish(u(torch.arange(a, end, device=DEV) + base))
+            m_all[a:end] = stored(m, ((bits & 0xFFFF) + 0.5) / 65536, False)
+            v_all[a:end] = stored(v.sqrt(), ((bits >> 16) + 0.5) / 65536, True)
+        else:
+            m_all[a:a + n], v_all[a:a + n] = m, v
+    return ([w_all] if s["copies"] is None else [w_all, w_all]) + [m_all, v_all]
