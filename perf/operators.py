@@ -15,9 +15,6 @@ import torch
 
 own = False
 
-if own:
-    from ad_recommendation_amd import dense
-
 DEV = "cuda"
 TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 
@@ -411,6 +408,8 @@ def _adamw(s):
 
 # ---------------------------------------------------------------------------------- one pass
 def run(s):
+    if own:
+        from ad_recommendation_amd import dense
     c = s["case"]
     op = c["op"]
     if op == "attn_fwd":
