@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,6 +16,9 @@ ARCH = "gfx950"
 
 # Packed fp32 instructions are kept out of all device code.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+# Device sources and host sources of the library, without their endings.
+KERNELS = ["emb_kernels", "dense_attn", "dense_norm", "dense_adamw"]
+HOSTS = ["emb_host", "dense_host"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
@@ -40,15 +44,15 @@ def build(verbose: bool = False) -> str:
     """Compile every source and link libmi355emb.so next to this file; returns its path."""
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
-    k_obj = os.path.join(BUILD, "emb_kernels.o")
-    h_obj = os.path.join(BUILD, "emb_host.o")
-    _run([hipcc, "-x", "hip", f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-c",
-          os.path.join(CSRC, "emb_kernels.hip"), "-o", k_obj], verbose)
-    _run([hipcc, "-x", "c++", *COMMON, "-I", "/opt/rocm/include", "-D__HIP_PLATFORM_AMD__", "-c",
-          os.path.join(CSRC, "emb_host.cpp"), "-o", h_obj], verbose)
+    jobs = [[hipcc, "-x", "hip", f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-c",
+             os.path.join(CSRC, n + ".hip"), "-o", os.path.join(BUILD, n + ".o")] for n in KERNELS]
+    jobs += [[hipcc, "-x", "c++", *COMMON, "-I", "/opt/rocm/include", "-D__HIP_PLATFORM_AMD__", "-c",
+              os.path.join(CSRC, n + ".cpp"), "-o", os.path.join(BUILD, n + ".o")] for n in HOSTS]
+    with ThreadPoolExecutor(4) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
     tmp = LIB + ".tmp"
-    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, k_obj, h_obj,
-          "-lpthread"], verbose)
+    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
+          *(os.path.join(BUILD, n + ".o") for n in KERNELS + HOSTS), "-lpthread"], verbose)
     os.replace(tmp, LIB)
     return LIB
 
@@ -58,22 +62,23 @@ SAN_LIB = os.path.join(BUILD, "san", "libmi355emb_san.so")
 
 def build_sanitized(verbose: bool = False) -> str:
     """The host runtime built with AddressSanitizer and UndefinedBehaviorSanitizer (host code only,
-    compiled by g++; the kernels object is the regular build's), linked into SAN_LIB.  The CPU
+    compiled by g++; the kernels' objects are the regular build's), linked into SAN_LIB.  The CPU
     tests load it in a process started with the ASan runtime preloaded.  Returns its path."""
-    k_obj = os.path.join(BUILD, "emb_kernels.o")
-    if not os.path.exists(k_obj):
+    k_objs = [os.path.join(BUILD, n + ".o") for n in KERNELS]
+    if not all(os.path.exists(o) for o in k_objs):
         build(verbose)
     d = os.path.dirname(SAN_LIB)
     os.makedirs(d, exist_ok=True)
-    h_obj = os.path.join(d, "emb_host_san.o")
+    h_objs = [os.path.join(d, n + "_san.o") for n in HOSTS]
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     san = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
            "-fno-omit-frame-pointer"]
-    _run(["g++", "-std=c++17", "-O1", "-g", "-fPIC", "-Wall", *san, "-I", os.path.join(ROOT, "include"),
-          "-I", CSRC, "-I", os.path.join(rocm, "include"), "-D__HIP_PLATFORM_AMD__", "-c",
-          os.path.join(CSRC, "emb_host.cpp"), "-o", h_obj], verbose)
+    for n, h_obj in zip(HOSTS, h_objs):
+        _run(["g++", "-std=c++17", "-O1", "-g", "-fPIC", "-Wall", *san, "-I",
+              os.path.join(ROOT, "include"), "-I", CSRC, "-I", os.path.join(rocm, "include"),
+              "-D__HIP_PLATFORM_AMD__", "-c", os.path.join(CSRC, n + ".cpp"), "-o", h_obj], verbose)
     tmp = SAN_LIB + ".tmp"
-    _run(["g++", "-shared", "-fPIC", *san[:1], "-o", tmp, k_obj, h_obj,
+    _run(["g++", "-shared", "-fPIC", *san[:1], "-o", tmp, *k_objs, *h_objs,
           "-L", os.path.join(rocm, "lib"), "-Wl,-rpath," + os.path.join(rocm, "lib"), "-lamdhip64",
           "-lpthread"], verbose)
     os.replace(tmp, SAN_LIB)

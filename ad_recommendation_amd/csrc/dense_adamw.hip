@@ -1,0 +1,213 @@
+// AdamW over many weight tensors in one launch, with states in 32 bits or in 8.
+//
+//   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   w = w - lr (m / c1 / (sqrt(v) / sqrt(c2) + eps) + wd w)
+// Bound by HBM.
+//
+// In 8 bits the states are m and s = sqrt(v), each an e4m3 code times a power of two shared by a block
+// of 128: the root halves the exponent range that v needs.  A code is within 1/16 of its value, while
+// b2 = 0.999 moves s by at most 0.05 % a step when g falls to zero, so rounding to the nearest would
+// leave s where it is for good; both states are rounded up or down at random, in proportion, so that
+// their means move as the formula says.
+#include "dense_device.h"
+
+// Products and sums round one by one, as the formula is written: the vector path, the element path
+// and a program that does the same steps give the same bits.
+#pragma clang fp contract(off)
+
+namespace emb {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStep = kThreads * 8;  // elements a workgroup takes at once, eight a thread
+
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {  // the finaliser of MurmurHash3
+  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
+  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {  // over 16 lanes
+#define STEP(C) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, C, 0xF, 0xF, false))
+  STEP(0x128);
+  STEP(0x124);
+  STEP(0x122);
+  STEP(0x121);
+#undef STEP
+  return x;
+}
+
+// Eight codes as values.
+__device__ __forceinline__ f32x8 decode8(uint2 c, int exp) {
+  const f32x2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
+  const f32x2 p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+  const f32x2 p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
+  const f32x2 p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+  f32x8 x = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], exp - 127);
+  return x;
+}
+
+// Eight values of a block, its 16 lanes' 128 in all, as codes; returns the block's exponent + 127.
+// `up`: for each value a number in (0, 1).  KEEP: a value that is not zero gets a code that is not.
+template <bool KEEP>
+__device__ __forceinline__ int encode8(const f32x8& x, const f32x8& up, uint2& codes) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = (uint32_t)__float_as_int(x[i]) & 0x7FFFFFFFu;
+    top = max(top, b < 0x7F800000u ? b : 0u);
+  }
+  top = row_max(top);
+  // floor(log2(top)) - 7, within the exponents that a byte holds
+  const int k = top ? max(__builtin_amdgcn_frexp_expf(__int_as_float((int)top)) - 8, -127) : -127;
+  f32x8 c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = ldexpf(fabsf(x[i]), -k);
+    const int e = max(__builtin_amdgcn_frexp_expf(y) - 1, -6);
+    float q = floorf(ldexpf(y, 3 - e) + up[i]);
+    if (KEEP && y > 0.f) q = fmaxf(q, 1.f);
+    c[i] = copysignf(ldexpf(q, e - 3), x[i]);
+    // infinities and NaN: the one code that e4m3 has for them
+    if (!(y < __builtin_huge_valf())) c[i] = __builtin_nanf("");
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
+  codes = make_uint2((uint32_t)lo, (uint32_t)hi);
+  return k + 127;
+}
+
+// One workgroup takes one chunk of one tensor.  The state arrays hold whole blocks of 128, so 16
+// lanes always share a block and only w, g and the copy have a ragged end.
+template <typename G, typename C, bool COPY, bool Q8>
+__global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
+  uint32_t lo = 0, hi = a.n_tensors;  // the last tensor whose first chunk is not past this one
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (a.t[mid].chunk0 <= blockIdx.x) lo = mid;
+    else hi = mid;
+  }
+  const AdamTensor& t = a.t[lo];
+  float* const w = t.w;
+  const G* const g = static_cast<const G*>(t.g);
+  C* const copy = static_cast<C*>(t.copy);
+  const int64_t n = t.n;
+  const int64_t n_pad = (n + EMB_ADAMW_BLOCK - 1) & ~(int64_t)(EMB_ADAMW_BLOCK - 1);
+  const int64_t s0 = (int64_t)t.block0 * EMB_ADAMW_BLOCK;
+  const float wd = t.wd;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+  const int64_t begin = (int64_t)(blockIdx.x - t.chunk0) * a.chunk;
+  const int64_t end = min(begin + (int64_t)a.chunk, n_pad);
+  const uint32_t seed = mix32(a.seed_lo) ^ a.seed_hi;
+
+  for (int64_t e0 = begin; e0 < end; e0 += kStep) {
+    const int64_t e = e0 + threadIdx.x * 8;
+    const bool in = e < n_pad;                        // the same for the 16 lanes of a block
+    const int left = (int)min(max(n - e, (int64_t)0), (int64_t)8);
+    f32x8 wv = {}, gv = {}, m = {}, v = {};
+    const int64_t s = s0 + e;
+    if (left > 0) {
+      wv = load8(w + e, left);
+      gv = widen(load8(g + e, left));
+    }
+    if (in) {
+      if (Q8) {
+        m = decode8(*reinterpret_cast<const uint2*>(a.m8 + s), a.m_exp[s / EMB_ADAMW_BLOCK]);
+        v = decode8(*reinterpret_cast<const uint2*>(a.v8 + s), a.v_exp[s / EMB_ADAMW_BLOCK]);
+        v = v * v;
+      } else {
+        m = *reinterpret_cast<const f32x8*>(a.m + s);
+        v = *reinterpret_cast<const f32x8*>(a.v + s);
+      }
+    }
+    f32x8 root;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float gi = gv[i] * gs;
+      m[i] = m[i] * a.b1 + gi * a.omb1;
+      v[i] = v[i] * a.b2 + gi * gi * a.omb2;
+      if (i >= left) m[i] = v[i] = 0.f;
+      root[i] = sqrtf(v[i]);
+      const float step = m[i] * a.inv_c1 / (root[i] * a.inv_c2 + a.eps) + wd * wv[i];
+      wv[i] = wv[i] - a.lr * step;
+    }
+    if (left > 0) {
+      store8(w + e, wv, left);
+      if (COPY) store8(copy + e, wv, left);
+    }
+    if (Q8) {
+      const uint32_t base = mix32(seed ^ (uint32_t)((uint64_t)s >> 32) * 0x9E3779B1u);
+      f32x8 up_m, up_v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t r = mix32((uint32_t)(s + i) + base);
+        up_m[i] = ((float)(r & 0xFFFFu) + 0.5f) * (1.f / 65536.f);
+        up_v[i] = ((float)(r >> 16) + 0.5f) * (1.f / 65536.f);
+      }
+      uint2 cm, cv;
+      const int em = encode8<false>(m, up_m, cm);
+      const int ev = encode8<true>(root, up_v, cv);
+      if (in) {
+        *reinterpret_cast<uint2*>(a.m8 + s) = cm;
+        *reinterpret_cast<uint2*>(a.v8 + s) = cv;
+        if ((threadIdx.x & 15) == 0) {
+          a.m_exp[s / EMB_ADAMW_BLOCK] = (uint8_t)em;
+          a.v_exp[s / EMB_ADAMW_BLOCK] = (uint8_t)ev;
+        }
+      }
+    } else if (in) {
+      *reinterpret_cast<f32x8*>(a.m + s) = m;
+      *reinterpret_cast<f32x8*>(a.v + s) = v;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adamw_values(const uint8_t* codes, const uint8_t* exp,
+                                                         int64_t elems, T* out) {
+  const int64_t stride = (int64_t)gridDim.x * kStep;
+  for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; e < elems; e += stride)
+    store8(out + e, decode8(*reinterpret_cast<const uint2*>(codes + e), exp[e / EMB_ADAMW_BLOCK]), 8);
+}
+
+template <typename G, bool Q8>
+void go(const AdamArgs& a, uint32_t chunks, int copy_dtype, hipStream_t st) {
+  const dim3 grid(chunks), block(kThreads);
+  if (copy_dtype == EMB_F16) hipLaunchKernelGGL((adamw<G, _Float16, true, Q8>), grid, block, 0, st, a);
+  else if (copy_dtype == EMB_BF16) hipLaunchKernelGGL((adamw<G, __bf16, true, Q8>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((adamw<G, _Float16, false, Q8>), grid, block, 0, st, a);
+}
+
+template <bool Q8>
+void go_type(const AdamArgs& a, uint32_t chunks, int grad_dtype, int copy_dtype, hipStream_t st) {
+  if (grad_dtype == EMB_F32) go<float, Q8>(a, chunks, copy_dtype, st);
+  else if (grad_dtype == EMB_F16) go<_Float16, Q8>(a, chunks, copy_dtype, st);
+  else go<__bf16, Q8>(a, chunks, copy_dtype, st);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamArgs& a, uint32_t n_chunks, bool q8, int grad_dtype,
+                        int copy_dtype, hipStream_t st) {
+  if (q8) go_type<true>(a, n_chunks, grad_dtype, copy_dtype, st);
+  else go_type<false>(a, n_chunks, grad_dtype, copy_dtype, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw_values(const uint8_t* codes, const uint8_t* exp, int64_t elems, void* out,
+                               int out_dtype, hipStream_t st) {
+  const int64_t blocks = (elems + kStep - 1) / kStep;
+  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536)), block(kThreads);
+  if (out_dtype == EMB_BF16)
+    hipLaunchKernelGGL((adamw_values<__bf16>), grid, block, 0, st, codes, exp, elems, static_cast<__bf16*>(out));
+  else
+    hipLaunchKernelGGL((adamw_values<float>), grid, block, 0, st, codes, exp, elems, static_cast<float*>(out));
+  return hipGetLastError();
+}
+
+}  // namespace emb

@@ -1,0 +1,88 @@
+// Device helpers of the dense side's kernels: element types, vectors of eight, sums over lanes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "dense_internal.h"
+
+namespace emb {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <typename T> struct Vec8;
+template <> struct Vec8<float> { typedef f32x8 t; };
+template <> struct Vec8<_Float16> { typedef f16x8 t; };
+template <> struct Vec8<__bf16> { typedef bf16x8 t; };
+
+// Eight elements at p as they are.  `n` of them exist; the others are zero and are not read.  p need
+// only be aligned to its elements: global memory takes 16-byte accesses at any address.
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::t load8(const T* p, int n) {
+  typedef typename Vec8<T>::t V;
+  typedef V U __attribute__((aligned(sizeof(T))));
+  if (n >= 8) return *reinterpret_cast<const U*>(p);
+  V v = {};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) v[i] = p[i];
+  return v;
+}
+
+// Rounds eight values to T (nearest even) and writes the first n.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, f32x8 x, int n) {
+  typedef typename Vec8<T>::t V;
+  typedef V U __attribute__((aligned(sizeof(T))));
+  const V v = __builtin_convertvector(x, V);
+  if (n >= 8) {
+    *reinterpret_cast<U*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) p[i] = v[i];
+}
+
+template <typename V>
+__device__ __forceinline__ f32x8 widen(V v) {
+  return __builtin_convertvector(v, f32x8);
+}
+
+// ---------------------------------------------------------------- sums over lanes
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float swap16_sum(float x) {  // with the neighbouring row of 16 lanes
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_int(x), __float_as_int(x), false, false);
+  return __int_as_float(r[0]) + __int_as_float(r[1]);
+}
+__device__ __forceinline__ float swap32_sum(float x) {  // with the other half of the wave
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
+  return __int_as_float(r[0]) + __int_as_float(r[1]);
+}
+__device__ __forceinline__ float swap32_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
+  return fmaxf(__int_as_float(r[0]), __int_as_float(r[1]));
+}
+// The sum over each group of N lanes (16, 32 or 64), in every lane of it: rotations within rows of 16
+// lanes on the vector unit, then swaps of rows and halves; no LDS.
+template <int N>
+__device__ __forceinline__ float lanes_sum(float x) {
+  x += dpp<0x128>(x);  // row_ror:8
+  x += dpp<0x124>(x);
+  x += dpp<0x122>(x);
+  x += dpp<0x121>(x);
+  if (N >= 32) x = swap16_sum(x);
+  if (N >= 64) x = swap32_sum(x);
+  return x;
+}
+
+}  // namespace emb

@@ -1,0 +1,364 @@
+// The norm after a block, its gate, the scaled residual and the norm before the next block, forward
+// and backward.  With inv(z) = rsqrt(mean(z^2) + eps) of a row z:
+//   forward   n = w_post * y * inv(y);  r = alpha * x + gate * n;  h = w_pre * r * inv(r)
+//   backward  u = dh * w_pre
+//             dR = dr + inv(r) * (u - r * inv(r)^2 * mean(u * r))
+//             z = gate * dR * w_post;  dx = alpha * dR
+//             dy = inv(y) * (z - y * inv(y)^2 * mean(z * y))
+//             dgate = dR * n;  dw_post = sum over rows of gate * dR * y * inv(y)
+//             dw_pre = sum over rows of dh * r * inv(r)
+// Both are bound by HBM: every row is read once into registers, its sums are taken there, and its
+// results leave from there.
+//
+// The backward needs mean(z * y), where z holds dR and so the row's other means.  dR is linear in
+// them, so with a = gate * w_post * y
+//   sum(z * y) = sum(a * dr) + inv(r) * sum(a * u) - inv(r)^3 * mean(u * r) * sum(a * r)
+// and one exchange of six sums per row is enough, where two exchanges would stand one after the
+// other between a row's loads and its stores.
+#include "dense_device.h"
+
+namespace emb {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sums K values over the row's TPR threads; every thread gets them.  Rows of at most a wave stay on
+// the vector unit; a row of the whole block meets in LDS, in one of two buffers in turn so that one
+// barrier a row is enough.
+template <int TPR, int K>
+__device__ __forceinline__ void row_sums(float (&s)[K], float (*lds)[kThreads / 64][K], int turn) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) s[k] = lanes_sum<(TPR < 64 ? TPR : 64)>(s[k]);
+  if (TPR > 64) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) lds[turn][w][k] = s[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float t = lds[turn][0][k];
+#pragma unroll
+      for (int i = 1; i < kThreads / 64; ++i) t += lds[turn][i][k];
+      s[k] = t;
+    }
+  }
+}
+
+// TPR threads take a row, each NC vectors of eight columns.
+template <typename T, int TPR, int NC>
+__global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
+  __shared__ float lds[2][kThreads / 64][1];
+  constexpr int kRows = kThreads / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int D = a.dim;
+  const T* x = static_cast<const T*>(a.x);
+  const T* y = static_cast<const T*>(a.y);
+  const T* gate = static_cast<const T*>(a.gate);
+  T* r = static_cast<T*>(a.r);
+  T* h = static_cast<T*>(a.h);
+  const float inv_d = 1.f / (float)D;
+
+  // what all rows share: the weights after the block times a gate vector, the weights before
+  f32x8 wg[NC], wp[NC];
+  int n[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int col = (c * TPR + lane) * 8;
+    n[c] = D - col;
+    wg[c] = f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    wp[c] = wg[c];
+    if (n[c] > 0) {
+      if (a.w_post) wg[c] = load8(a.w_post + col, n[c]);
+      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= widen(load8(gate + col, n[c]));
+      if (a.w_pre) wp[c] = load8(a.w_pre + col, n[c]);
+    }
+  }
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  // the same number of turns for every thread of a block: there are barriers inside
+  const int64_t first = (int64_t)blockIdx.x * kRows;
+  int turn = 0;
+  for (int64_t base = first; base < a.rows; base += stride) {
+    const int64_t row = base + threadIdx.x / TPR;
+    const bool live = row < a.rows;
+    const int64_t at = row * D;
+    typename Vec8<T>::t xr[NC], yr[NC], gr[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + lane) * 8;
+      xr[c] = typename Vec8<T>::t{};
+      yr[c] = xr[c];
+      gr[c] = xr[c];
+      if (live && n[c] > 0) {
+        xr[c] = load8(x + at + col, n[c]);
+        if (y) yr[c] = load8(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8(gate + at + col, n[c]);
+      }
+    }
+    float inv_y = 1.f;
+    if (y && a.w_post) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const f32x8 v = widen(yr[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] += v[i] * v[i];
+      }
+      row_sums<TPR, 1>(s, lds, turn);
+      turn ^= 1;
+      inv_y = rsqrtf(s[0] * inv_d + a.eps);
+    }
+    f32x8 rr[NC];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      rr[c] = a.alpha * widen(xr[c]);
+      if (y) {
+        f32x8 v = widen(yr[c]) * inv_y * wg[c];
+        if (a.gate_kind == EMB_GATE_ROWS) v *= widen(gr[c]);
+        rr[c] += v;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += rr[c][i] * rr[c][i];
+    }
+    if (r && live) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if (n[c] > 0) store8(r + at + (c * TPR + lane) * 8, rr[c], n[c]);
+    }
+    if (h) {
+      row_sums<TPR, 1>(s, lds, turn);
+      turn ^= 1;
+      const float inv_r = rsqrtf(s[0] * inv_d + a.eps);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if (live && n[c] > 0) store8(h + at + (c * TPR + lane) * 8, rr[c] * inv_r * wp[c], n[c]);
+    }
+  }
+}
+
+// Rows go round the blocks; a thread keeps the column sums of its columns over the rows it sees in
+// registers, the block's rows then meet in LDS, and the blocks in norm_join.
+template <typename T, int TPR, int NC>
+__global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
+  constexpr int kRows = kThreads / TPR;
+  constexpr int kSums = 6;
+  __shared__ float lds[2][kThreads / 64][kSums];
+  __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * 8 : 1];
+  const int lane = threadIdx.x % TPR;
+  const int D = a.dim;
+  const T* r = static_cast<const T*>(a.r_in);
+  const T* y = static_cast<const T*>(a.y);
+  const T* gate = static_cast<const T*>(a.gate);
+  const T* dr = static_cast<const T*>(a.dr);
+  const T* dh = static_cast<const T*>(a.dh);
+  T* dx = static_cast<T*>(a.dx);
+  T* dy = static_cast<T*>(a.dy);
+  T* dgate = a.gate_kind == EMB_GATE_ROWS ? static_cast<T*>(a.dgate) : nullptr;
+  const float inv_d = 1.f / (float)D;
+  const bool pre = a.w_pre != nullptr;
+
+  f32x8 wg[NC], wp[NC], c_post[NC], c_pre[NC];
+  int n[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int col = (c * TPR + lane) * 8;
+    n[c] = D - col;
+    wg[c] = f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    wp[c] = wg[c];
+    c_post[c] = f32x8{};
+    c_pre[c] = f32x8{};
+    if (n[c] > 0) {
+      if (a.w_post) wg[c] = load8(a.w_post + col, n[c]);
+      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= widen(load8(gate + col, n[c]));
+      if (pre) wp[c] = load8(a.w_pre + col, n[c]);
+    }
+  }
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += (int64_t)gridDim.x * kRows) {
+    const int64_t row = base + threadIdx.x / TPR;
+    const bool live = row < a.rows;
+    const int64_t at = row * D;
+    typename Vec8<T>::t rr[NC], yr[NC], gr[NC], drr[NC], dhr[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + lane) * 8;
+      rr[c] = typename Vec8<T>::t{};
+      yr[c] = rr[c];
+      gr[c] = rr[c];
+      drr[c] = rr[c];
+      dhr[c] = rr[c];
+      if (live && n[c] > 0) {
+        if (pre) {
+          rr[c] = load8(r + at + col, n[c]);
+          dhr[c] = load8(dh + at + col, n[c]);
+        }
+        if (dr) drr[c] = load8(dr + at + col, n[c]);
+        if (y) yr[c] = load8(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8(gate + at + col, n[c]);
+      }
+    }
+    // r^2, u r, y^2, a dr, a u, a r
+    float s[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const f32x8 rv = widen(rr[c]), u = widen(dhr[c]) * wp[c], yv = widen(yr[c]), dv = widen(drr[c]);
+      f32x8 av = yv * wg[c];
+      if (a.gate_kind == EMB_GATE_ROWS) av *= widen(gr[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[0] += rv[i] * rv[i];
+        s[1] += u[i] * rv[i];
+        s[2] += yv[i] * yv[i];
+        s[3] += av[i] * dv[i];
+        s[4] += av[i] * u[i];
+        s[5] += av[i] * rv[i];
+      }
+    }
+    row_sums<TPR, kSums>(s, lds, turn);
+    turn ^= 1;
+    const float inv_r = pre ? rsqrtf(s[0] * inv_d + a.eps) : 0.f;
+    const float back_r = inv_r * inv_r * inv_r * s[1] * inv_d;  // dR = dr + inv_r u - back_r r
+    float inv_y = 1.f, back_y = 0.f;                            // dy = inv_y z - back_y y
+    if (a.w_post) {
+      inv_y = rsqrtf(s[2] * inv_d + a.eps);
+      back_y = inv_y * inv_y * inv_y * (s[3] + inv_r * s[4] - back_r * s[5]) * inv_d;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (n[c] <= 0) continue;
+      const int col = (c * TPR + lane) * 8;
+      const f32x8 rv = widen(rr[c]), dhv = widen(dhr[c]), yv = widen(yr[c]);
+      const f32x8 dR = widen(drr[c]) + inv_r * (dhv * wp[c]) - back_r * rv;
+      f32x8 z = dR * wg[c];
+      f32x8 yn = yv * inv_y;
+      if (a.gate_kind == EMB_GATE_ROWS) {
+        if (dgate && live) {
+          // wg is w_post alone here (or 1)
+          store8(dgate + at + col, dR * yn * wg[c], n[c]);
+        }
+        const f32x8 g = widen(gr[c]);
+        z *= g;
+        yn *= g;
+      }
+      c_post[c] += dR * yn;
+      c_pre[c] += dhv * (rv * inv_r);
+      if (live) {
+        if (dx) store8(dx + at + col, a.alpha * dR, n[c]);
+        if (dy) store8(dy + at + col, inv_y * z - back_y * yv, n[c]);
+      }
+    }
+  }
+  // the block's column sums, [2][D] of its own
+  float* out = a.part + (size_t)blockIdx.x * 2 * D;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + lane) * 8;
+      f32x8 v = k ? c_pre[c] : c_post[c];
+      if (kRows > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cols[threadIdx.x / TPR][lane * 8 + i] = v[i];
+        __syncthreads();
+        if (threadIdx.x < TPR) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float t = 0.f;
+            for (int g = 0; g < kRows; ++g) t += cols[g][lane * 8 + i];
+            v[i] = t;
+          }
+        }
+      }
+      if ((kRows == 1 || threadIdx.x < TPR) && n[c] > 0) store8(out + (size_t)k * D + col, v, n[c]);
+    }
+  }
+}
+
+// Sums the blocks' column sums: 32 columns a workgroup, 8 threads a column, in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) norm_join(NormArgs a) {
+  __shared__ float lds[8][33];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
+  const int part = threadIdx.x >> 5;
+  float t[2] = {0.f, 0.f};
+  if (col < a.dim) {
+    for (int b = part; b < a.blocks; b += 8) {
+      t[0] += a.part[((size_t)b * 2 + 0) * a.dim + col];
+      t[1] += a.part[((size_t)b * 2 + 1) * a.dim + col];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
+    lds[part][threadIdx.x & 31] = t[k];
+    __syncthreads();
+    if (part == 0 && col < a.dim) {
+      float v = 0.f;
+      for (int i = 0; i < 8; ++i) v += lds[i][threadIdx.x & 31];
+      if (k == 1) {
+        if (a.dw_pre) a.dw_pre[col] = v;
+      } else if (a.gate_kind == EMB_GATE_VECTOR) {
+        // the sum is of dR * y * inv(y) alone: the gate and the weights are the same in every row
+        const float g = (float)static_cast<const T*>(a.gate)[col];
+        if (a.dgate) static_cast<float*>(a.dgate)[col] = v * (a.w_post ? a.w_post[col] : 1.f);
+        if (a.dw_post) a.dw_post[col] = v * g;
+      } else if (a.dw_post) {
+        a.dw_post[col] = v;
+      }
+    }
+  }
+}
+
+template <typename T, int TPR, int NC>
+void go_fwd(const NormArgs& a, hipStream_t st) {
+  const int64_t blocks = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
+  hipLaunchKernelGGL((norm_fwd<T, TPR, NC>), dim3((unsigned)(blocks < 2048 ? blocks : 2048)),
+                     dim3(kThreads), 0, st, a);
+}
+template <typename T, int TPR, int NC>
+void go_bwd(const NormArgs& a, hipStream_t st) {
+  if (a.blocks)
+    hipLaunchKernelGGL((norm_bwd<T, TPR, NC>), dim3((unsigned)a.blocks), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((norm_join<T>), dim3((unsigned)((a.dim + 31) / 32)), dim3(kThreads), 0, st, a);
+}
+
+template <typename T>
+void pick(const NormArgs& a, bool bwd, hipStream_t st) {
+#define GO(TPR, NC) (bwd ? go_bwd<T, TPR, NC>(a, st) : go_fwd<T, TPR, NC>(a, st))
+  if (a.dim <= 256) GO(32, 1);
+  else if (a.dim <= 512) GO(64, 1);
+  else if (a.dim <= 2048) GO(256, 1);
+  else if (a.dim <= 4096) GO(256, 2);
+  else GO(256, 4);
+#undef GO
+}
+
+void pick_type(const NormArgs& a, bool bwd, hipStream_t st) {
+  if (a.dtype == EMB_F32) pick<float>(a, bwd, st);
+  else if (a.dtype == EMB_F16) pick<_Float16>(a, bwd, st);
+  else pick<__bf16>(a, bwd, st);
+}
+
+}  // namespace
+
+// Blocks of the backward: 16 rows each where there are few, no more than 1024.
+int norm_bwd_blocks(int64_t rows, int32_t dim) {
+  const int64_t per = dim <= 256 ? 8 : dim <= 512 ? 4 : 1;
+  int64_t b = (rows + per * 4 - 1) / (per * 4);
+  return (int)(b < 1024 ? b : 1024);
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
+  pick_type(a, false, st);
+  return hipGetLastError();
+}
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st) {
+  pick_type(a, true, st);
+  return hipGetLastError();
+}
+
+}  // namespace emb

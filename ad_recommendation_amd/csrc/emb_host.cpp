@@ -191,6 +191,8 @@ void sort_entries(std::vector<Entry>& v, uint32_t n_home) {
 
 }  // namespace
 
+int emb::set_error(int code, const std::string& msg) { return fail(code, msg); }
+
 struct EmbTable {
   // descriptor
   int32_t F = 0;

@@ -10,6 +10,9 @@
 
 namespace emb {
 
+// Sets the calling thread's emb_last_error() message and returns `code`.
+int set_error(int code, const std::string& msg);
+
 constexpr uint64_t kEmpty = ~0ull;             // free-slot marker in the key buckets
 constexpr int kKeysPerBucket = 15;             // 15 keys + 1 metadata word = one 128-byte line
 constexpr int kWordsPerBucket = 16;

@@ -1,0 +1,341 @@
+"""Python binding of the library's dense side (include/emb_dense.h): attention over event sequences
+with a sliding window and sinks, the gated residual norms around a block, and AdamW.  Argument
+marshalling only; the work runs in the library's HIP kernels on the caller's stream.
+
+The functions keep the C names and argument order.  Device arguments are torch CUDA tensors on the
+current device; errors raise EmbError (the library's checks) or TypeError/ValueError (the tensors').
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional
+
+import torch
+
+from .emb import EMB_F16, EMB_F32, _check, _stream, lib as _emb_lib
+
+EMB_BF16 = 2
+ATTN_MAX_SINKS = 32
+ADAMW_BLOCK = 128
+GATE_NONE, GATE_VECTOR, GATE_ROWS = 0, 1, 2
+
+_VP, _I32, _I64, _F = C.c_void_p, C.c_int32, C.c_int64, C.c_float
+_D = C.c_double
+_DTYPE = {torch.float32: EMB_F32, torch.float16: EMB_F16, torch.bfloat16: EMB_BF16}
+
+
+class EmbAttn(C.Structure):
+    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("kv_heads", _I32), ("dim", _I32),
+                ("window", _I32), ("sinks", _I32), ("scale", _F)]
+
+
+class EmbHeads(C.Structure):
+    _fields_ = [("p", _VP), ("seq", _I64), ("tok", _I64), ("head", _I64)]
+
+
+_LIB = None
+_A, _H = C.POINTER(EmbAttn), C.POINTER(EmbHeads)
+_SZ = C.POINTER(C.c_size_t)
+_SIG = {
+    "attn_window_fwd": [_A, _H, _H, _H, _VP, _I64, _I64, _H, _VP, _VP],
+    "attn_window_bwd_workspace_bytes": [_A, _I64, _I64, _SZ],
+    "attn_window_bwd": [_A, _H, _H, _H, _VP, _I64, _I64, _H, _VP, _H, _H, _H, _H, _VP, C.c_size_t,
+                        _VP],
+    "attn_window_decode_workspace_bytes": [_A, _I64, _I64, _SZ],
+    "attn_window_decode": [_A, _H, _H, _H, _VP, _I64, _I64, _H, _VP, C.c_size_t, _VP],
+    "norm_gate_residual_fwd": [_VP, _VP, _VP, _I32, _VP, _VP, _I64, _I32, _I32, _F, _F, _VP, _VP,
+                               _VP],
+    "norm_gate_residual_bwd_workspace_bytes": [_I64, _I32, _SZ],
+    "norm_gate_residual_bwd": [_VP, _VP, _VP, _I32, _VP, _VP, _I64, _I32, _I32, _F, _F, _VP, _VP,
+                               _VP, _VP, _VP, _VP, _VP, _VP, C.c_size_t, _VP],
+    "adamw_state_elems": [_VP, _I32, C.POINTER(_I64)],
+    "adamw_step": [_I32, _VP, _VP, _VP, _I32, _VP, _I32, _VP, _VP, _I64, _I64, _D, _D, _D, _D, _VP,
+                   _VP, _VP],
+    "adamw_step_q8": [_I32, _VP, _VP, _VP, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _I64, _I64, _D, _D,
+                      _D, _D, _VP, _VP, C.c_uint64, _VP],
+    "adamw_q8_values": [_VP, _VP, _I64, _VP, _I32, _VP],
+}
+
+
+def exported_symbols():
+    """Names include/emb_dense.h declares (used by the load test)."""
+    return list(_SIG)
+
+
+def lib() -> C.CDLL:
+    """The HIP library with this module's signatures set."""
+    global _LIB
+    if _LIB is None:
+        L = _emb_lib()
+        for name, args in _SIG.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = C.c_int
+        _LIB = L
+    return _LIB
+
+
+def _ptr(t, name: str, dtype=None, shape=None, optional: bool = False) -> Optional[int]:
+    """Device pointer of a contiguous tensor of this type and shape."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name}: expected a tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _ws(ws):
+    """Pointer and size of a workspace (None where none is needed)."""
+    return (None, 0) if ws is None else (_ptr(ws, "workspace"), ws.numel() * ws.element_size())
+
+
+# ------------------------------------------------------------------ attention
+def _heads(t, name: str, dtype, shape) -> EmbHeads:
+    """[tokens, heads, dim], or [sequences, tokens, heads, dim] of a cache: any strides but the
+    last, which is 1."""
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last dimension's stride must be 1")
+    # the strides of dimensions of one element are never used: 0 passes the library's check of them
+    st = [s if n > 1 else 0 for s, n in zip(st, shape)]
+    return EmbHeads(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+
+
+def _attn(q, kv_heads: int, window: int, sinks: int, scale: float) -> EmbAttn:
+    if q.dim() != 3:
+        raise ValueError("q: expected [tokens, heads, dim]")
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q: expected float16 or bfloat16, got {q.dtype}")
+    # no window past the longest sequence differs from one of 2^31 - 1
+    return EmbAttn(_DTYPE[q.dtype], q.shape[1], kv_heads, q.shape[2], min(int(window), 2**31 - 1),
+                   int(sinks), float(scale))
+
+
+def _kv_shape(q, k):
+    if k.dim() != 3:
+        raise ValueError("k: expected [tokens, heads, dim]")
+    return torch.Size((q.shape[0], k.shape[1], q.shape[2]))
+
+
+def _offsets(offsets):
+    p = _ptr(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets: expected one dimension of n_seq + 1 elements")
+    return p, offsets.numel() - 1
+
+
+def attn_window_fwd(q, k, v, offsets, window: int, sinks: int, scale: float, out, lse=None,
+                    stream=None):
+    """out [tokens, q_heads, dim] and lse [q_heads, tokens] (fp32, optional) of q [tokens, q_heads,
+    dim] and k, v [tokens, kv_heads, dim]; sequence s holds tokens offsets[s] to offsets[s + 1] - 1."""
+    t, kv = q.dtype, _kv_shape(q, k)
+    a = _attn(q, k.shape[1], window, sinks, scale)
+    off, n_seq = _offsets(offsets)
+    _check(lib().attn_window_fwd(
+        C.byref(a), C.byref(_heads(q, "q", t, q.shape)), C.byref(_heads(k, "k", t, kv)),
+        C.byref(_heads(v, "v", t, kv)), off, n_seq, q.shape[0],
+        C.byref(_heads(out, "out", t, q.shape)),
+        _ptr(lse, "lse", torch.float32, torch.Size((q.shape[1], q.shape[0])), optional=True),
+        _stream(stream)))
+
+
+def attn_window_bwd_workspace_bytes(n_tok: int, n_seq: int, q_heads: int, kv_heads: int, dim: int,
+                                    sinks: int) -> int:
+    a, n = EmbAttn(EMB_F16, q_heads, kv_heads, dim, 1, sinks, 1.0), C.c_size_t()
+    _check(lib().attn_window_bwd_workspace_bytes(C.byref(a), n_seq, n_tok, C.byref(n)))
+    return n.value
+
+
+def attn_window_bwd(q, k, v, offsets, window: int, sinks: int, scale: float, out, lse, dout, dq,
+                    dk, dv, ws, stream=None):
+    """dq, dk and dv from the forward's inputs and results and the gradient of out."""
+    t, kv = q.dtype, _kv_shape(q, k)
+    a = _attn(q, k.shape[1], window, sinks, scale)
+    off, n_seq = _offsets(offsets)
+    wp, wb = _ws(ws)
+    _check(lib().attn_window_bwd(
+        C.byref(a), C.byref(_heads(q, "q", t, q.shape)), C.byref(_heads(k, "k", t, kv)),
+        C.byref(_heads(v, "v", t, kv)), off, n_seq, q.shape[0],
+        C.byref(_heads(out, "out", t, q.shape)),
+        _ptr(lse, "lse", torch.float32, torch.Size((q.shape[1], q.shape[0]))),
+        C.byref(_heads(dout, "dout", t, q.shape)), C.byref(_heads(dq, "dq", t, q.shape)),
+        C.byref(_heads(dk, "dk", t, kv)), C.byref(_heads(dv, "dv", t, kv)), wp, wb,
+        _stream(stream)))
+
+
+def attn_window_decode_workspace_bytes(n_seq: int, capacity: int, q_heads: int, kv_heads: int,
+                                       dim: int, window: int, sinks: int) -> int:
+    a, n = EmbAttn(EMB_F16, q_heads, kv_heads, dim, min(int(window), 2**31 - 1), sinks, 1.0), C.c_size_t()
+    _check(lib().attn_window_decode_workspace_bytes(C.byref(a), n_seq, capacity, C.byref(n)))
+    return n.value
+
+
+def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale: float, out, ws,
+                       stream=None):
+    """out [n_seq, q_heads, dim] of one query per sequence, q [n_seq, q_heads, dim], against caches
+    [n_seq, capacity, kv_heads, dim] that hold lens [n_seq] events, the query's own among them."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected [sequences, capacity, heads, dim]")
+    t, (n, cap, kv_heads, _) = q.dtype, k_cache.shape
+    a = _attn(q, kv_heads, window, sinks, scale)
+    cache = torch.Size((q.shape[0], cap, kv_heads, q.shape[2]))
+    wp, wb = _ws(ws)
+    _check(lib().attn_window_decode(
+        C.byref(a), C.byref(_heads(q, "q", t, q.shape)),
+        C.byref(_heads(k_cache, "k_cache", t, cache)), C.byref(_heads(v_cache, "v_cache", t, cache)),
+        _ptr(lens, "lens", torch.int32, torch.Size((q.shape[0],))), q.shape[0], cap,
+        C.byref(_heads(out, "out", t, q.shape)), wp, wb, _stream(stream)))
+
+
+# ------------------------------------------------------------------ norms
+def _gate_kind(gate, shape) -> int:
+    if gate is None:
+        return GATE_NONE
+    return GATE_VECTOR if gate.dim() == 1 else GATE_ROWS
+
+
+def _rows(t):
+    if t.dim() != 2:
+        raise ValueError("expected rows [rows, dim]")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"expected float32, float16 or bfloat16, got {t.dtype}")
+    return t.dtype, t.shape, torch.Size((t.shape[1],))
+
+
+def norm_gate_residual_fwd(x, y, gate, w_post, w_pre, alpha: float, eps: float, r, h, stream=None):
+    """r = alpha x + gate * (w_post * rms(y)), h = w_pre * rms(r).  x, y, r, h [rows, dim]; gate
+    [dim] or [rows, dim]; w_post, w_pre fp32 [dim].  None where a part is left out."""
+    t, s, d = _rows(x)
+    kind = _gate_kind(gate, s)
+    _check(lib().norm_gate_residual_fwd(
+        _ptr(x, "x"), _ptr(y, "y", t, s, True), _ptr(gate, "gate", t, d if kind == 1 else s, True),
+        kind, _ptr(w_post, "w_post", torch.float32, d, True),
+        _ptr(w_pre, "w_pre", torch.float32, d, True), s[0], s[1], _DTYPE[t], float(alpha),
+        float(eps), _ptr(r, "r", t, s, True), _ptr(h, "h", t, s, True), _stream(stream)))
+
+
+def norm_gate_residual_bwd_workspace_bytes(rows: int, dim: int) -> int:
+    n = C.c_size_t()
+    _check(lib().norm_gate_residual_bwd_workspace_bytes(rows, dim, C.byref(n)))
+    return n.value
+
+
+def norm_gate_residual_bwd(r, y, gate, w_post, w_pre, alpha: float, eps: float, dr, dh, dx, dy,
+                           dgate, dw_post, dw_pre, ws, stream=None):
+    """Gradients of norm_gate_residual_fwd from r as stored; None for an output that is not wanted.
+    dgate: fp32 [dim] for a gate vector, like the rows for a gate of rows."""
+    t, s, d = _rows(r)
+    kind = _gate_kind(gate, s)
+    f, wp_wb = torch.float32, _ws(ws)
+    _check(lib().norm_gate_residual_bwd(
+        _ptr(r, "r"), _ptr(y, "y", t, s, True), _ptr(gate, "gate", t, d if kind == 1 else s, True),
+        kind, _ptr(w_post, "w_post", f, d, True), _ptr(w_pre, "w_pre", f, d, True), s[0], s[1],
+        _DTYPE[t], float(alpha), float(eps), _ptr(dr, "dr", t, s, True), _ptr(dh, "dh", t, s, True),
+        _ptr(dx, "dx", t, s, True), _ptr(dy, "dy", t, s, True),
+        _ptr(dgate, "dgate", f if kind == 1 else t, d if kind == 1 else s, True),
+        _ptr(dw_post, "dw_post", f, d, True), _ptr(dw_pre, "dw_pre", f, d, True), *wp_wb,
+        _stream(stream)))
+
+
+# ------------------------------------------------------------------ AdamW
+def adamw_state_elems(weights) -> int:
+    """Elements of a state array for these weight tensors."""
+    n = (_I64 * len(weights))(*[w.numel() for w in weights])
+    out = _I64()
+    _check(lib().adamw_state_elems(n, len(weights), C.byref(out)))
+    return out.value
+
+
+def _tensors(ts, name: str, dtype, sizes):
+    """Host array of the device pointers of contiguous tensors of one type and these sizes."""
+    if len(ts) != len(sizes):
+        raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(ts)}")
+    for t, n in zip(ts, sizes):
+        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+            raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} with the weights' "
+                            f"sizes, got {t.dtype}, {tuple(t.shape)} on {t.device}")
+    return (_VP * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def _adamw_args(weights, grads, copies, weight_decay):
+    sizes = [w.numel() for w in weights]
+    k = len(sizes)
+    g_dtype = grads[0].dtype if k and len(grads) else torch.float32
+    c_dtype = copies[0].dtype if k and copies else torch.bfloat16
+    if g_dtype not in _DTYPE or c_dtype not in _DTYPE:
+        raise TypeError(f"unexpected tensor dtype {g_dtype}, {c_dtype}")
+    if isinstance(weight_decay, (int, float)):
+        wd = (_F * k)(*([weight_decay] * k))
+    else:
+        if len(weight_decay) != k:
+            raise ValueError(f"weight_decay: expected {k} values, got {len(weight_decay)}")
+        wd = (_F * k)(*weight_decay)
+    return (k, (_I64 * k)(*sizes), _tensors(weights, "weights", torch.float32, sizes),
+            _tensors(grads, "grads", g_dtype, sizes), _DTYPE[g_dtype],
+            None if copies is None else _tensors(copies, "copies", c_dtype, sizes),
+            _DTYPE[c_dtype]), wd
+
+
+def _scalar(t):
+    if t is not None and t.numel() != 1:
+        raise ValueError(f"grad_scale: expected one element, got {t.numel()}")
+
+
+def adamw_step(weights, grads, m, v, step: int, lr: float, beta1: float, beta2: float, eps: float,
+               weight_decay, copies=None, grad_scale=None, stream=None):
+    """One AdamW step over lists of tensors, in place.  weights fp32; grads of one type; m, v fp32
+    [adamw_state_elems(weights)]; weight_decay: a number or one per tensor; copies: float16 or
+    bfloat16 tensors that receive the new weights; grad_scale: fp32 device scalar."""
+    args, wd = _adamw_args(weights, grads, copies, weight_decay)
+    f = torch.float32
+    _scalar(grad_scale)
+    _check(lib().adamw_step(
+        *args, _ptr(m, "m", f), _ptr(v, "v", f, m.shape), m.numel(), int(step), lr, beta1, beta2,
+        eps, wd, _ptr(grad_scale, "grad_scale", f, optional=True), _stream(stream)))
+
+
+def _codes(t, name: str, n: int):
+    if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError(f"{name}: expected uint8 or float8_e4m3fn, got {t.dtype}")
+    return _ptr(t, name, shape=torch.Size((n,)))
+
+
+def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta1: float,
+                  beta2: float, eps: float, weight_decay, seed: int, copies=None, grad_scale=None,
+                  stream=None):
+    """adamw_step with states in 8 bits: m, v codes [adamw_state_elems(weights)] (uint8 or
+    float8_e4m3fn), m_exp, v_exp uint8 [that / ADAMW_BLOCK], all zero at first.  `seed`: another one
+    each step."""
+    args, wd = _adamw_args(weights, grads, copies, weight_decay)
+    _scalar(grad_scale)
+    n = m.numel()
+    e = torch.Size((n // ADAMW_BLOCK,))
+    _check(lib().adamw_step_q8(
+        *args, _codes(m, "m", n), _ptr(m_exp, "m_exp", torch.uint8, e), _codes(v, "v", n),
+        _ptr(v_exp, "v_exp", torch.uint8, e), n, int(step), lr, beta1, beta2, eps, wd,
+        _ptr(grad_scale, "grad_scale", torch.float32, optional=True), int(seed) & (2**64 - 1),
+        _stream(stream)))
+
+
+def adamw_q8_values(codes, exp, out, stream=None):
+    """The values that 8-bit state codes stand for, in bfloat16 or float32; v's are its roots."""
+    n = codes.numel()
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
+    _check(lib().adamw_q8_values(
+        _codes(codes, "codes", n), _ptr(exp, "exp", torch.uint8, torch.Size((n // ADAMW_BLOCK,))), n,
+        _ptr(out, "out", shape=torch.Size((n,))), _DTYPE[out.dtype], _stream(stream)))
