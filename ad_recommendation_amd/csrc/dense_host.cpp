@@ -70,9 +70,9 @@ int check_counts(int64_t n_seq, int64_t n_tok) {
   return EMB_OK;
 }
 
-// A launch's grid: one workgroup per (tile slot, head) at the smallest tile of 32 tokens.
+// A launch's grid: tile slots and sink chunks by heads, with room to spare.
 int check_grid(const EmbAttn* a, int64_t n_seq, int64_t n_tok) {
-  DENSE_CHECK((n_tok / 32 + n_seq) * (int64_t)a->q_heads < INT32_MAX, EMB_ERANGE,
+  DENSE_CHECK((n_tok / 32 + 3 * n_seq) * (int64_t)a->q_heads < INT32_MAX, EMB_ERANGE,
               "attention: more tiles than one launch holds");
   return EMB_OK;
 }

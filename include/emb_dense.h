@@ -60,8 +60,8 @@ typedef struct {
  * d_offsets[s + 1] - 1 of n_tok, as the bags of lookup_pool_fwd hold keys (offsets int32,
  * ascending from 0 to n_tok; empty sequences are fine).  Softmax statistics and sums are fp32.
  *   d_lse : nullable; fp32 [q_heads][n_tok], what the backward reads.
- * A key or value that is not finite reaches only the queries that see it and, where they share one
- * tile of 64 keys with it, queries of the same sequence; never another sequence.
+ * A key or value that is not finite reaches only the queries that see it (and in the backward, a
+ * query or gradient only the keys it sees).
  * EMB_VALIDATE=1 checks the offsets first (it synchronises the stream); without it malformed
  * offsets give wrong results but no access outside the n_tok tokens.
  * Errors: EMB_EINVAL for a null pointer, a bad descriptor, alignment or stride; EMB_ERANGE for
