@@ -50,13 +50,13 @@ struct Seq {
   int len, tile;  // tokens; which tile of the sequence this workgroup has
   int index;
 };
-// Tile slot s of a ragged batch: sequence b's tiles start at slot off[b] / tile + extra * b, which
-// leaves every sequence room for ceil(len / tile) + extra - 1 tiles without a pass over the
-// lengths.  64 lanes look for the sequence together.  Offsets are clamped to the tokens.
-__device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int tile, int extra) {
-  auto start = [&](int b) {
-    return min(max((int64_t)a.off[b], (int64_t)0), a.n_tok) / tile + (int64_t)extra * b;
-  };
+// Tile slot s of a ragged batch, where sequence b's tiles start at slot first(begin, b): a function that
+// leaves each sequence room for its tiles without a pass over the lengths (begin / tile + b does: the
+// tiles of a length l that starts anywhere number at most l / tile + 1).  64 lanes look for the
+// sequence together.  Offsets are clamped to the tokens.
+template <typename F>
+__device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, F first) {
+  auto start = [&](int b) { return first(min(max((int64_t)a.off[b], (int64_t)0), a.n_tok), b); };
   int lo = 0, n = a.n_seq;
   while (n > 1) {
     const int step = (n + 63) >> 6, k = lane_id() * step;
@@ -72,47 +72,57 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int tile, 
   s.begin = min(max((int64_t)a.off[lo], (int64_t)0), a.n_tok);
   const int64_t end = min(max((int64_t)a.off[lo + 1], s.begin), a.n_tok);
   s.len = (int)(end - s.begin);
-  s.tile = (int)max((int64_t)slot - (s.begin / tile + (int64_t)extra * lo), (int64_t)-1);
+  s.tile = (int)max((int64_t)slot - (int64_t)first(s.begin, lo), (int64_t)-1);
   return s;
 }
 
-__device__ __forceinline__ bool sees(const AttnArgs& a, int i, int j) {
-  return j <= i && (i - j < a.window || j < a.sinks);
+// Sets x[r] to `hidden` where query i does not see key j0 + row_of(r): the distance i - j, taken as an
+// unsigned number, is below the window, or below all others for a sink.  Few tiles need it; the empty
+// statement keeps the compiler from doing it in all of them and choosing afterwards.
+__device__ __forceinline__ void hide_keys(const AttnArgs& a, int i, int j0, f32x16& x, float hidden) {
+  asm volatile("");
+  const int d = i - j0 - 4 * (lane_id() >> 5);
+  const int sinks = a.sinks - j0 - 4 * (lane_id() >> 5);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int e = 8 * (r >> 2) + (r & 3);
+    const uint32_t limit = e < sinks ? 0x7FFFFFFFu : (uint32_t)a.window;
+    if ((uint32_t)(d - e) >= limit) x[r] = hidden;
+  }
 }
 
 // ---------------------------------------------------------------- LDS tiles
-// Rows of DH elements in 16-byte pieces, a row's pieces exchanged by its number so that the eight or
-// more rows which one read touches lie in different banks.
+// Rows of DH elements, 16 bytes apart from one another, so that the eight rows whose pieces one pass
+// of a read touches lie in different banks and every place within a tile is a constant from a lane's own.
 template <int DH>
 struct Tile {
-  static constexpr int kPieces = DH / 8;
-  static constexpr int kBytes = kStageRows * DH * 2;
-  static constexpr int kRegs = kStageRows * kPieces / kThreads;
-  __device__ static __forceinline__ int at(int row, int piece) {
-    const int x = kPieces >= 8 ? row & 7 : (row >> 1) & 3;
-    return (row * kPieces + (piece ^ x)) * 16;
-  }
+  static constexpr int kPieces = DH / 8;  // of 16 bytes
+  static constexpr int kRow = DH * 2 + 16;
+  static constexpr int kBytes = kStageRows * kRow;
+  __device__ static __forceinline__ int at(int row, int piece) { return row * kRow + piece * 16; }
 };
 
-template <int DH>
+template <int DH, int THREADS>
 struct Staged {
-  u32x4 r[Tile<DH>::kRegs];
+  static constexpr int kPieces = Tile<DH>::kPieces;
+  static constexpr int kRegs = kStageRows * kPieces / THREADS;
+  u32x4 r[kRegs];
   // Rows row0 .. row0 + 63 of a head; zeros past `len` rows and past D columns.
   template <typename T>
   __device__ __forceinline__ void load(const T* base, int64_t stride, int row0, int len, int D) {
 #pragma unroll
-    for (int n = 0; n < Tile<DH>::kRegs; ++n) {
-      const int idx = threadIdx.x + n * kThreads;
-      const int row = row0 + idx / Tile<DH>::kPieces, col = idx % Tile<DH>::kPieces * 8;
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = threadIdx.x + n * THREADS;
+      const int row = row0 + idx / kPieces, col = idx % kPieces * 8;
       r[n] = u32x4{0, 0, 0, 0};
       if (row < len && col < D) r[n] = *reinterpret_cast<const u32x4*>(base + row * stride + col);
     }
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
-    for (int n = 0; n < Tile<DH>::kRegs; ++n) {
-      const int idx = threadIdx.x + n * kThreads;
-      *reinterpret_cast<u32x4*>(lds + Tile<DH>::at(idx / Tile<DH>::kPieces, idx % Tile<DH>::kPieces)) = r[n];
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = threadIdx.x + n * THREADS;
+      *reinterpret_cast<u32x4*>(lds + Tile<DH>::at(idx / kPieces, idx % kPieces)) = r[n];
     }
   }
 };
@@ -121,20 +131,17 @@ struct Staged {
 template <typename T, int DH>
 __device__ __forceinline__ typename Vec8<T>::t left(const char* lds, int row0, int ks) {
   const int l = lane_id();
-  return *reinterpret_cast<const typename Vec8<T>::t*>(lds + Tile<DH>::at(row0 + (l & 31), 2 * ks + (l >> 5)));
+  return *reinterpret_cast<const typename Vec8<T>::t*>(lds + Tile<DH>::at(l & 31, l >> 5) + Tile<DH>::at(row0, 2 * ks));
 }
 // Left operand, transposed: columns 32 db .. 32 db + 31 as rows, rows row0 .. row0 + 15 as k, in the
 // order in which a result's registers hold them.
 template <typename T, int DH>
 __device__ __forceinline__ typename Vec8<T>::t left_t(const char* lds, int row0, int db) {
   const int l = lane_id();
-  const int row = row0 + 4 * (l >> 5) + ((l & 15) >> 2);
-  const int piece = db * 4 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
+  const char* p = lds + Tile<DH>::at(4 * (l >> 5) + ((l & 15) >> 2), ((l >> 4) & 1) * 2) + (l & 3) * 8;
   typedef __attribute__((address_space(3))) i16x4* Lds;
-  const char* p0 = lds + Tile<DH>::at(row, piece) + (l & 1) * 8;
-  const char* p1 = lds + Tile<DH>::at(row + 8, piece) + (l & 1) * 8;
-  const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p0);
-  const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p1);
+  const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + Tile<DH>::at(row0, db * 4)));
+  const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + Tile<DH>::at(row0 + 8, db * 4)));
   const i16x8 v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(typename Vec8<T>::t, v);
 }
@@ -154,8 +161,8 @@ __device__ __forceinline__ void right_row(const EmbHeads& t, int64_t tok, int he
 // Eight registers of a result as the right operand of the next product, rounded to T: a product's
 // operands have 16 bits, and its sum is fp32 again.
 template <typename T>
-__device__ __forceinline__ typename Vec8<T>::t right_of(const float* p) {
-  const f32x8 x = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+__device__ __forceinline__ typename Vec8<T>::t right_of(const f32x16& p, int r) {
+  const f32x8 x = {p[r], p[r + 1], p[r + 2], p[r + 3], p[r + 4], p[r + 5], p[r + 6], p[r + 7]};
   return __builtin_convertvector(x, typename Vec8<T>::t);
 }
 
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
   const int kh = blockIdx.x % a.kv_heads;
   const int rest = blockIdx.x / a.kv_heads;
   const int h = kh * group + rest % group;
-  const Seq s = find_tile(a, rest / group, kQTile, 1);
+  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / kQTile + b; });
   if (s.tile < 0 || (int64_t)s.tile * kQTile >= s.len) return;
   const int i0 = s.tile * kQTile;
   const int iw = __builtin_amdgcn_readfirstlane(i0 + (threadIdx.x >> 6) * 32);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
   const KeyTiles tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
-  Staged<DH> ks_, vs_;
+  Staged<DH, kThreads> ks_, vs_;
   ks_.load(kp, a.k.tok, tiles.key0(0), s.len, a.dim);
   vs_.load(vp, a.v.tok, tiles.key0(0), s.len, a.dim);
 
@@ -344,11 +351,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
       sc[0] = mma(left<T, DH>(kt, 0, ks), q[ks], sc[0]);
       sc[1] = mma(left<T, DH>(kt, 32, ks), q[ks], sc[1]);
     }
-    if (j0 + 63 > iw || j0 < iw + 31 - a.window + 1) {
-#pragma unroll
-      for (int r = 0; r < 32; ++r)
-        if (!sees(a, i, j0 + (r >> 4) * 32 + row_of(r & 15))) sc[r >> 4][r & 15] = -kInf;
-    }
+    if (j0 + 31 > iw || j0 < iw + 31 - a.window + 1) hide_keys(a, i, j0, sc[0], -kInf);
+    if (j0 + 63 > iw || j0 + 32 < iw + 31 - a.window + 1) hide_keys(a, i, j0 + 32, sc[1], -kInf);
     float top = sc[0][0];
 #pragma unroll
     for (int r = 1; r < 32; ++r) top = fmaxf(top, sc[r >> 4][r & 15]);
@@ -364,15 +368,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
       for (int db = 0; db < DH / 32; ++db) o[db] *= by;
     }
     const float off = m == -kInf ? 0.f : m * c;
-    float p[32];
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
-      p[r] = __builtin_amdgcn_exp2f(fmaf(sc[r >> 4][r & 15], c, -off));
-      l += p[r];
+      sc[r >> 4][r & 15] = __builtin_amdgcn_exp2f(fmaf(sc[r >> 4][r & 15], c, -off));
+      l += sc[r >> 4][r & 15];
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const V8 pb = right_of<T>(p + 8 * k);
+      const V8 pb = right_of<T>(sc[k >> 1], 8 * (k & 1));
 #pragma unroll
       for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T, DH>(vt, 16 * k, db), pb, o[db]);
     }
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
   const int kh = blockIdx.x % a.kv_heads;
   const int rest = blockIdx.x / a.kv_heads;
   const int h = kh * group + rest % group;
-  const Seq s = find_tile(a, rest / group, kQTile, 1);
+  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / kQTile + b; });
   if (s.tile < 0 || (int64_t)s.tile * kQTile >= s.len) return;
   const int i0 = s.tile * kQTile;
   const int iw = __builtin_amdgcn_readfirstlane(i0 + (threadIdx.x >> 6) * 32);
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
   const KeyTiles tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
-  Staged<DH> ks_, vs_;
+  Staged<DH, kThreads> ks_, vs_;
   ks_.load(kp, a.k.tok, tiles.key0(0), s.len, a.dim);
   vs_.load(vp, a.v.tok, tiles.key0(0), s.len, a.dim);
 
@@ -450,18 +453,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
         sc = mma(left<T, DH>(kt, 32 * sub, ks), q[ks], sc);
         dp = mma(left<T, DH>(vt, 32 * sub, ks), d[ks], dp);
       }
-      float ds[16];
+      f32x16 ds;
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         ds[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -lse)) * (dp[r] - delta);
-      if (js + 31 > iw || js < iw + 31 - a.window + 1) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (!sees(a, i, js + row_of(r))) ds[r] = 0.f;
-      }
+      if (js + 31 > iw || js < iw + 31 - a.window + 1) hide_keys(a, i, js, ds, 0.f);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const V8 b = right_of<T>(ds + 8 * k);
+        const V8 b = right_of<T>(ds, 8 * k);
 #pragma unroll
         for (int db = 0; db < DH / 32; ++db)
           dq[db] = mma(left_t<T, DH>(kt, 32 * sub + 16 * k, db), b, dq[db]);
@@ -474,60 +473,110 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- backward: dk, dv
-// A workgroup has 128 keys of a key/value head, 32 a wave, and meets the queries of every head of its
-// group that see them; sums stay in registers, so nothing is added up in memory.  The sinks are
-// seen by every later query of their sequence too: those queries, from `reach` on, are cut into
-// chunks, each a workgroup whose four waves take its rows in turn for the first 32 keys; its sums and
-// those of the first key tile go to memory in fp32, and attn_sink_join adds them in order.
+// A workgroup has 128 keys of a key/value head and meets the queries of every head of its group that
+// see them, 64 rows a step; sums stay in registers, so nothing is added up in memory.
+//
+// The sinks are seen by every later query of their sequence too: those queries, from `reach` on, are
+// cut into chunks, each a workgroup whose waves take its rows in turn for the first 32 keys; its
+// sums and those of the first key tile go to memory in fp32, and attn_sink_join adds them in order.
+//
+// Heads of 64 and less: four waves of 32 keys, which hold their keys and values as right operands in
+// registers.  Heads of 128: the sums alone take 128 registers and the operands another 64, which
+// leaves one wave a SIMD; eight waves, two to each 32 keys with half of a step's rows, and keys and
+// values in LDS make it two, at a half more reads of LDS.
 constexpr int kSinkKeys = EMB_ATTN_MAX_SINKS;
 
 __host__ __device__ inline int64_t reach_of(int window) { return (int64_t)kQTile + window - 1; }
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(kThreads, DH == 128 ? 1 : 2)
-    attn_dkv(AttnArgs a, int main_blocks, int chunk) {
-  typedef typename Vec8<T>::t V8;
-  struct Shared {
-    char q[2][Tile<DH>::kBytes], d[2][Tile<DH>::kBytes];
-    float lse[2][kStageRows], delta[2][kStageRows];
-  };
-  __shared__ __attribute__((aligned(16))) Shared sh;
-  const int group = a.q_heads / a.kv_heads;
-  const bool sink = (int)blockIdx.x >= main_blocks;  // the same for the whole workgroup
-  const int block = sink ? blockIdx.x - main_blocks : blockIdx.x;
-  const int kh = block % a.kv_heads, slot = block / a.kv_heads;
-  const Seq s = sink ? find_tile(a, slot, chunk, 2) : find_tile(a, slot, kQTile, 1);
-  const int64_t reach = reach_of(a.window);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int j0, row0, row1;  // first key; the queries met
-  if (s.tile < 0) return;
-  if (sink) {
-    const int64_t r0 = reach + (int64_t)s.tile * chunk;
-    if (r0 >= s.len) return;
-    j0 = 0;
-    row0 = (int)r0;
-    row1 = (int)min(r0 + chunk, (int64_t)s.len);
-  } else {
-    if ((int64_t)s.tile * kQTile >= s.len) return;
-    j0 = s.tile * kQTile;
-    row0 = j0;
-    row1 = (int)min(j0 + reach, (int64_t)s.len);
+// Partial sums of the sinks, [2][sinks][dim] each: first those of the chunks by slot, then those of
+// the first key tiles of sequences longer than reach, of which a batch has at most n_tok / 129.
+// Sequence b's chunks start at slot begin / chunk + begin / (reach + 1): where its length is over
+// reach that leaves room for len / chunk + 1 of them.
+struct SinkSlots {
+  int64_t chunk_slots, first_tiles;
+  __host__ __device__ SinkSlots(int64_t n_tok, int64_t n_seq, int window, int chunk) {
+    chunk_slots = n_tok / chunk + n_tok / (reach_of(window) + 1) + 1;
+    first_tiles = n_seq < n_tok / (kQTile + 1) + 1 ? n_seq : n_tok / (kQTile + 1) + 1;
   }
-  const int jw = sink ? 0 : j0 + 32 * wave;
+};
+__device__ __forceinline__ float* sink_part(const AttnArgs& a, int64_t slot, int kh) {
+  return a.part + (slot * a.kv_heads + kh) * 2 * a.sinks * (int64_t)a.dim;
+}
+__device__ __forceinline__ float* first_tile_part(const AttnArgs& a, int64_t begin, int index, int chunk, int kh) {
+  const SinkSlots n(a.n_tok, a.n_seq, a.window, chunk);
+  return sink_part(a, n.chunk_slots + (n.first_tiles == a.n_seq ? index : begin / (kQTile + 1)), kh);
+}
+
+// Adds the sums of the upper half of `n` waves to those of the lower half, through LDS.
+template <int N>
+__device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave, int n) {
+  __syncthreads();
+  if (wave >= n / 2 && wave < n) {
+#pragma unroll
+    for (int k = 0; k < N * 16; ++k) lds[((wave - n / 2) * N * 16 + k) * 64 + lane_id()] = x[k >> 4][k & 15];
+  }
+  __syncthreads();
+  if (wave < n / 2) {
+#pragma unroll
+    for (int k = 0; k < N * 16; ++k) x[k >> 4][k & 15] += lds[(wave * N * 16 + k) * 64 + lane_id()];
+  }
+}
+
+template <int DH>
+struct DkvShape {
+  static constexpr bool kWide = DH == 128;
+  static constexpr int kWaves = kWide ? 8 : 4;
+  static constexpr int kBlock = kWaves * 64;
+  static constexpr int kShare = kWaves / 4;  // waves that share 32 keys
+};
+
+template <int DH>
+struct DkvShared {
+  static constexpr int kKeyTiles = DkvShape<DH>::kWide ? 2 : 0;
+  char q[2][Tile<DH>::kBytes], d[2][Tile<DH>::kBytes];
+  float lse[2][kStageRows], delta[2][kStageRows];
+  char k[kKeyTiles][Tile<DH>::kBytes], v[kKeyTiles][Tile<DH>::kBytes];
+};
+
+// SINK: rows `row0` to `row1` - 1 against the sinks, the sums to the slot's place; otherwise those rows
+// against the 128 keys from j0.
+template <typename T, int DH, bool SINK>
+__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const Seq& s, int kh, int j0, int row0,
+                                    int row1, int64_t slot, int chunk) {
+  typedef typename Vec8<T>::t V8;
+  typedef DkvShape<DH> P;
+  const int group = a.q_heads / a.kv_heads;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int jrow = SINK ? 0 : 32 * (wave & 3);  // the wave's keys within the tile
+  const int jw = j0 + jrow;
   const int j = jw + (lane_id() & 31);
   const bool live = j < s.len;
+  const uint32_t limit = j < a.sinks ? 0x7FFFFFFFu : (uint32_t)a.window;
 
-  V8 k[DH / 16], v[DH / 16];
-  right_row<T, DH>(a.k, s.begin + j, kh, live, a.dim, k);
-  right_row<T, DH>(a.v, s.begin + j, kh, live, a.dim, v);
+  V8 k[P::kWide ? 1 : DH / 16], v[P::kWide ? 1 : DH / 16];
+  if constexpr (P::kWide) {
+    const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
+    const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      Staged<DH, P::kBlock> ks_, vs_;
+      ks_.load(kp, a.k.tok, j0 + kStageRows * x, s.len, a.dim);
+      vs_.load(vp, a.v.tok, j0 + kStageRows * x, s.len, a.dim);
+      ks_.store(sh.k[x]);
+      vs_.store(sh.v[x]);
+    }
+  } else {
+    right_row<T, DH>(a.k, s.begin + j, kh, live, a.dim, k);
+    right_row<T, DH>(a.v, s.begin + j, kh, live, a.dim, v);
+  }
   const float c = a.scale * kLog2e;
 
   const int n_tiles = (row1 - row0 + kStageRows - 1) / kStageRows;
-  const int steps = n_tiles * group;  // of all heads of the group
-  Staged<DH> qs_, ds_;
+  Staged<DH, P::kBlock> qs_, ds_;
   float stat = 0.f;  // threads 0-63: lse of a row; 64-127: its delta
-  auto load = [&](int step) {
-    const int h = kh * group + step / n_tiles, r0 = row0 + step % n_tiles * kStageRows;
+  int next_h = kh * group, next_r0 = row0;  // what is loaded next
+  auto load = [&]() {
+    const int h = next_h, r0 = next_r0;
     qs_.load(static_cast<const T*>(a.q.p) + s.begin * a.q.tok + h * a.q.head, a.q.tok, r0, row1, a.dim);
     ds_.load(static_cast<const T*>(a.dout.p) + s.begin * a.dout.tok + h * a.dout.head, a.dout.tok,
              r0, row1, a.dim);
@@ -538,35 +587,51 @@ __global__ void __launch_bounds__(kThreads, DH == 128 ? 1 : 2)
       // a row that is not there gets probabilities of zero
       if (threadIdx.x < kStageRows) stat = row < row1 ? stat * kLog2e : kInf;
     }
+    next_r0 += kStageRows;
+    if (next_r0 >= row1) {
+      next_r0 = row0;
+      ++next_h;
+    }
   };
-  load(0);
+  load();
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
-  for (int step = 0; step < steps; ++step) {
+  int r0 = row0;
+  const int steps = n_tiles * group;  // of all heads of the group
+  for (int step = 0; step < steps; ++step, r0 = r0 + kStageRows < row1 ? r0 + kStageRows : row0) {
     const int b = step & 1;
     qs_.store(sh.q[b]);
     ds_.store(sh.d[b]);
     if (threadIdx.x < kStageRows) sh.lse[b][threadIdx.x] = stat;
     else if (threadIdx.x < 2 * kStageRows) sh.delta[b][threadIdx.x - kStageRows] = stat;
-    if (step + 1 < steps) load(step + 1);
+    if (step + 1 < steps) load();
     __syncthreads();
-    const int r0 = row0 + step % n_tiles * kStageRows;
     if (jw >= s.len) continue;
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
+    for (int sub_ = 0; sub_ < 2 / P::kShare; ++sub_) {
+      const int sub = P::kShare == 2 ? wave >> 2 : sub_;
       const int is = r0 + 32 * sub;
       if (is >= row1) continue;
-      if (sink) {
-        if (((step * 2 + sub) & 3) != wave) continue;
+      if (SINK) {
+        if ((P::kShare == 2 ? step & 3 : (step * 2 + sub) & 3) != (wave & 3)) continue;
       } else if (is + 31 < jw || (jw >= a.sinks && is >= jw + 31 + (int64_t)a.window)) {
         continue;
       }
       f32x16 sc = {}, dp = {};
+      if constexpr (P::kWide) {
 #pragma unroll
-      for (int ks = 0; ks < DH / 16; ++ks) {
-        sc = mma(left<T, DH>(sh.q[b], 32 * sub, ks), k[ks], sc);
-        dp = mma(left<T, DH>(sh.d[b], 32 * sub, ks), v[ks], dp);
+        for (int ks = 0; ks < DH / 16; ++ks)
+          sc = mma(left<T, DH>(sh.q[b], 32 * sub, ks), left<T, DH>(sh.k[0], jrow, ks), sc);
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks)
+          dp = mma(left<T, DH>(sh.d[b], 32 * sub, ks), left<T, DH>(sh.v[0], jrow, ks), dp);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks) {
+          sc = mma(left<T, DH>(sh.q[b], 32 * sub, ks), k[ks], sc);
+          dp = mma(left<T, DH>(sh.d[b], 32 * sub, ks), v[ks], dp);
+        }
       }
-      float p[16], ds[16];
+      f32x16 p, ds;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int at = 32 * sub + 8 * g + 4 * (lane_id() >> 5);
@@ -579,13 +644,15 @@ __global__ void __launch_bounds__(kThreads, DH == 128 ? 1 : 2)
         }
       }
       if (is < jw + 31 || (int64_t)is + 31 - jw >= a.window) {
+        asm volatile("");  // see hide_keys
+        const int d = is + 4 * (lane_id() >> 5) - j;
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (!sees(a, is + row_of(r), j)) p[r] = ds[r] = 0.f;
+          if ((uint32_t)(d + 8 * (r >> 2) + (r & 3)) >= limit) p[r] = ds[r] = 0.f;
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const V8 pb = right_of<T>(p + 8 * x), db_ = right_of<T>(ds + 8 * x);
+        const V8 pb = right_of<T>(p, 8 * x), db_ = right_of<T>(ds, 8 * x);
 #pragma unroll
         for (int db = 0; db < DH / 32; ++db) {
           dv[db] = mma(left_t<T, DH>(sh.d[b], 32 * sub + 16 * x, db), pb, dv[db]);
@@ -594,63 +661,67 @@ __global__ void __launch_bounds__(kThreads, DH == 128 ? 1 : 2)
       }
     }
   }
-  // partial sums of the sinks: [slot][kv head][2][sinks][dim], the first key tile's in the slot before
-  // the sequence's chunks' (slots are two a sequence apart for it)
-  const bool split = a.sinks > 0 && reach < s.len;
-  const int64_t first_slot = s.begin / chunk + 2 * (int64_t)s.index;
-  auto partial = [&](int64_t at) {
-    return a.part + (at * a.kv_heads + kh) * 2 * a.sinks * (int64_t)a.dim;
-  };
-  if (!sink) {
-    float* out = partial(first_slot);
-    const EmbHeads row{out, 0, a.dim, 0};
-    uint32_t again = either(live && (not_finite(dk) || not_finite(dv)));
-    if (live && !(again >> (lane_id() & 31) & 1)) {
-      if (!split || j >= a.sinks) {
-        store_row<T, DH>(a.dk, s.begin + j, kh, a.dim, dk, a.scale);
-        store_row<T, DH>(a.dv, s.begin + j, kh, a.dim, dv, 1.f);
-      } else {
-        store_row<float, DH>(row, j, 0, a.dim, dk, 1.f);
-        store_row<float, DH>(row, a.sinks + j, 0, a.dim, dv, 1.f);
+  float* fold = reinterpret_cast<float*>(sh.q);  // q and d: half the waves' sums of one matrix
+  static_assert(sizeof(sh.q) + sizeof(sh.d) >= sizeof(float) * P::kWaves / 2 * 32 * DH, "room to fold");
+  if constexpr (SINK) {
+    const EmbHeads row{sink_part(a, slot, kh), 0, a.dim, 0};
+    auto finish = [&](f32x16 (&x)[DH / 32], int row_at) {
+#pragma unroll
+      for (int n = P::kWaves; n > 1; n /= 2) fold_waves(x, fold, wave, n);
+      if (wave == 0 && j < a.sinks) store_row<float, DH>(row, row_at + j, 0, a.dim, x, 1.f);
+    };
+    finish(dk, 0);
+    finish(dv, a.sinks);
+  } else {
+    const bool split = a.sinks > 0 && reach_of(a.window) < s.len;
+    const EmbHeads row{split ? first_tile_part(a, s.begin, s.index, chunk, kh) : nullptr, 0, a.dim, 0};
+    // one matrix after the other; the rows of each that are not finite
+    auto finish = [&](f32x16 (&x)[DH / 32], const EmbHeads& to, int row_at, float by) -> uint32_t {
+      if constexpr (P::kShare == 2) fold_waves(x, fold, wave, 8);
+      const uint32_t bad = wave < 4 ? either(live && not_finite(x)) : 0;
+      if (wave < 4 && live && !(bad >> (lane_id() & 31) & 1)) {
+        if (!split || j >= a.sinks) store_row<T, DH>(to, s.begin + j, kh, a.dim, x, by);
+        else store_row<float, DH>(row, row_at + j, 0, a.dim, x, 1.f);
       }
-    }
-    for (; again; again &= again - 1) {
-      const int x = jw + __builtin_ctz(again);
+      return bad;
+    };
+    const uint32_t bad_k = finish(dk, a.dk, 0, a.scale);
+    const uint32_t bad_v = finish(dv, a.dv, a.sinks, 1.f);
+    for (uint32_t again = bad_k | bad_v; again; again &= again - 1) {
+      const int n = __builtin_ctz(again), x = jw + n;
+      const bool sum = split && x < a.sinks;
       Pair pk, pv;
       again_dkv<T>(a, s.begin, x, x < a.sinks ? row1 : (int)min((int64_t)x + a.window, (int64_t)s.len),
                    kh, pk, pv);
-      if (!split || x >= a.sinks) {
-        put<T>(a.dk, s.begin + x, kh, a.dim, pk, a.scale);
-        put<T>(a.dv, s.begin + x, kh, a.dim, pv, 1.f);
-      } else {
-        put<float>(row, x, 0, a.dim, pk, 1.f);
-        put<float>(row, a.sinks + x, 0, a.dim, pv, 1.f);
+      if (bad_k >> n & 1) {
+        if (sum) put<float>(row, x, 0, a.dim, pk, 1.f);
+        else put<T>(a.dk, s.begin + x, kh, a.dim, pk, a.scale);
+      }
+      if (bad_v >> n & 1) {
+        if (sum) put<float>(row, a.sinks + x, 0, a.dim, pv, 1.f);
+        else put<T>(a.dv, s.begin + x, kh, a.dim, pv, 1.f);
       }
     }
-    return;
   }
-  // the four waves' sums meet in LDS, one wave after the other
-  float* acc = reinterpret_cast<float*>(sh.q);  // [32][DH] fp32 of one matrix
-  static_assert(sizeof(sh.q) >= sizeof(float) * kSinkKeys * DH, "the sums fit the tiles' LDS");
-  float* out = partial(first_slot + 1 + s.tile);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    for (int w = 0; w < 4; ++w) {
-      __syncthreads();
-      if (wave != w) continue;
-#pragma unroll
-      for (int db = 0; db < DH / 32; ++db) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float* p = acc + (lane_id() & 31) * DH + db * 32 + row_of(r);
-          const float t = x ? dv[db][r] : dk[db][r];
-          *p = w ? *p + t : t;
-        }
-      }
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.sinks * a.dim; e += kThreads)
-      out[x * a.sinks * a.dim + e] = acc[e / a.dim * DH + e % a.dim];
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(DkvShape<DH>::kBlock, 2) attn_dkv(AttnArgs a, int main_blocks, int chunk) {
+  __shared__ __attribute__((aligned(16))) DkvShared<DH> sh;
+  const bool sink = (int)blockIdx.x >= main_blocks;  // the same for the whole workgroup
+  const int block = sink ? blockIdx.x - main_blocks : blockIdx.x;
+  const int kh = block % a.kv_heads, slot = block / a.kv_heads;
+  const int64_t reach = reach_of(a.window);
+  if (sink) {
+    const Seq s = find_tile(a, slot, [&](int64_t t, int) { return t / chunk + t / (reach + 1); });
+    const int64_t r0 = reach + (int64_t)s.tile * chunk;
+    if (s.tile < 0 || r0 >= s.len) return;
+    dkv<T, DH, true>(a, sh, s, kh, 0, (int)r0, (int)min(r0 + chunk, (int64_t)s.len), slot, chunk);
+  } else {
+    const Seq s = find_tile(a, slot, [](int64_t t, int b) { return t / kQTile + b; });
+    if (s.tile < 0 || (int64_t)s.tile * kQTile >= s.len) return;
+    const int j0 = s.tile * kQTile;
+    dkv<T, DH, false>(a, sh, s, kh, j0, j0, (int)min(j0 + reach, (int64_t)s.len), 0, chunk);
   }
 }
 
@@ -662,11 +733,15 @@ __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int chunk
   const int64_t len = min(max((int64_t)a.off[b + 1], begin), a.n_tok) - begin;
   const int64_t reach = reach_of(a.window);
   if (len <= reach) return;
-  const int64_t n = 1 + (len - reach + chunk - 1) / chunk;
-  const int64_t each = 2 * a.sinks * (int64_t)a.dim, first = begin / chunk + 2 * (int64_t)b;
+  const int64_t n = (len - reach + chunk - 1) / chunk;
+  const int64_t first = begin / chunk + begin / (reach + 1);
+  const int64_t each = 2 * a.sinks * (int64_t)a.dim, step = each * a.kv_heads;
+  const float* tile = first_tile_part(a, begin, b, chunk, kh);
+  const float* part = sink_part(a, first, kh);
   for (int e = threadIdx.x; e < each; e += kThreads) {
-    float t = 0.f;
-    for (int64_t x = 0; x < n; ++x) t += a.part[((first + x) * a.kv_heads + kh) * each + e];
+    float t = tile[e];
+#pragma unroll 8
+    for (int64_t x = 0; x < n; ++x) t += part[x * step + e];
     const int row = e / a.dim % a.sinks, col = e % a.dim;
     const bool is_v = e >= a.sinks * a.dim;
     const EmbHeads& to = is_v ? a.dv : a.dk;
@@ -683,7 +758,7 @@ __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int chunk
 template <int DH>
 struct WaveTile {  // 32 rows, of one wave
   static constexpr int kRegs = 32 * Tile<DH>::kPieces / 64;
-  static constexpr int kBytes = 32 * DH * 2;
+  static constexpr int kBytes = 32 * Tile<DH>::kRow;
 };
 
 template <typename T, int DH>
@@ -770,15 +845,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
       for (int db = 0; db < DH / 32; ++db) o[db] *= by;
     }
     const float off = m == -kInf ? 0.f : m * c;
-    float p[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      p[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -off));
-      l += p[r];
+      sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -off));
+      l += sc[r];
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const V8 pb = right_of<T>(p + 8 * k);
+      const V8 pb = right_of<T>(sc, 8 * k);
 #pragma unroll
       for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T, DH>(vt, 16 * k, db), pb, o[db]);
     }
@@ -787,93 +861,100 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
   l = swap32_sum(l);
-  // the waves meet: every wave scales its sums to the common maximum, and they are added in order
+  // the waves meet: each leaves its sums in its own part of LDS, and four rows of a column at a time
+  // are scaled to the common maximum and added in the waves' order
   if (lane < 32) {
     stats[wave][0][lane] = m;
     stats[wave][1][lane] = l;
   }
+  static_assert(sizeof(lds[0]) >= sizeof(float) * 32 * DH, "a wave's sums take its tiles' place");
+  f32x4* mine = reinterpret_cast<f32x4*>(lds[wave]);
+#pragma unroll
+  for (int x = 0; x < DH / 8; ++x) {
+    const f32x16 t = o[x >> 2];
+    const int r = (x & 3) * 4;
+    mine[x * 64 + lane] = f32x4{t[r], t[r + 1], t[r + 2], t[r + 3]};
+  }
   __syncthreads();
-  float top = -kInf, sum = 0.f;
+  float top = -kInf, sum = 0.f, by[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) top = fmaxf(top, stats[w][0][lane & 31]);
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const float mw = stats[w][0][lane & 31];
-    if (mw != -kInf) sum += stats[w][1][lane & 31] * exp2f((mw - top) * c);
+    by[w] = mw == -kInf ? 0.f : exp2f((mw - top) * c);
+    sum += stats[w][1][lane & 31] * by[w];
   }
-  const float by = m == -kInf ? 0.f : exp2f((m - top) * c);
-  float* acc = reinterpret_cast<float*>(lds);  // [32][DH]
-  static_assert(sizeof(lds) >= sizeof(float) * 32 * DH, "the sums fit the tiles' LDS");
-  for (int w = 0; w < 4; ++w) {
-    __syncthreads();
-    if (wave != w) continue;
-#pragma unroll
-    for (int db = 0; db < DH / 32; ++db) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        // a lane's row starts at a piece of its own, so that 32 rows do not share a bank
-        float* x = acc + (lane & 31) * DH + ((db * 32 + row_of(r) + (lane & 31)) & (DH - 1));
-        const float t = o[db][r] * by;
-        *x = w ? *x + t : t;
-      }
-    }
-  }
-  __syncthreads();
   // part: [split][sequence][q head][dim] of unscaled sums, then [..][2] of maximum and sum
-  const int heads = min(group - col * 32, 32);
   const int64_t total = (int64_t)a.n_seq * a.q_heads;
-  if (threadIdx.x < 32) {
-    stats[0][0][threadIdx.x] = top;  // every thread has read them: barriers have passed
-    stats[0][1][threadIdx.x] = sum;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < heads * a.dim; e += kThreads) {
-    const int hd = e / a.dim, d = e % a.dim;
-    const int qh = kh * group + col * 32 + hd;
-    const float x = acc[hd * DH + ((d + hd) & (DH - 1))];
+  const int qh = kh * group + head;
+  const int64_t row = (int64_t)split * total + (int64_t)sq * a.q_heads + qh;
+#pragma unroll
+  for (int y = 0; y < DH / 32; ++y) {
+    const int x = wave + 4 * y;  // which four rows
+    const int d = x * 8 + 4 * (lane >> 5);
+    f32x4 t = {};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const f32x4 ow = reinterpret_cast<const f32x4*>(lds[w])[x * 64 + lane];
+      // a wave without keys has zeros, and so does its factor
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] += ow[e] * by[w];
+    }
+    if (!live || d >= a.dim) continue;
     if (splits == 1) {
-      const float sm = stats[0][1][hd];
-      static_cast<T*>(a.out.p)[sq * a.out.tok + qh * a.out.head + d] = (T)(n_keys > 0 ? x / sm : 0.f);
+      typedef T V __attribute__((ext_vector_type(4)));
+      const float inv = n_keys > 0 ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = n_keys > 0 ? t[e] * inv : 0.f;
+      *reinterpret_cast<V*>(static_cast<T*>(a.out.p) + sq * a.out.tok + qh * a.out.head + d) =
+          __builtin_convertvector(t, V);
     } else {
-      const int64_t row = (int64_t)split * total + (int64_t)sq * a.q_heads + qh;
-      a.part[row * a.dim + d] = x;
-      if (d == 0) {
-        float* st = a.part + (int64_t)splits * total * a.dim + row * 2;
-        st[0] = stats[0][0][hd] * c;
-        st[1] = stats[0][1][hd];
-      }
+      *reinterpret_cast<f32x4*>(a.part + row * a.dim + d) = t;
     }
   }
+  if (splits > 1 && live && threadIdx.x < 32)
+    *reinterpret_cast<f32x2*>(a.part + (int64_t)splits * total * a.dim + row * 2) = f32x2{top * c, sum};
 }
 
-// One wave a (sequence, query head): the splits' sums at their common maximum.
+// One wave a (sequence, query head): the splits' sums at their common maximum.  A lane has one split's
+// maximum and sum (of 64 at a time), then two columns of all.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_decode_join(AttnArgs a, int splits) {
-  const int64_t total = (int64_t)a.n_seq * a.q_heads;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= total) return;
+__global__ void __launch_bounds__(64) attn_decode_join(AttnArgs a, int splits) {
+  const int64_t total = (int64_t)a.n_seq * a.q_heads, row = blockIdx.x;
   const float* st = a.part + (int64_t)splits * total * a.dim;
+  const int lane = lane_id(), d = 2 * lane;
   float top = -kInf, sum = 0.f;
-  for (int x = 0; x < splits; ++x) top = fmaxf(top, st[(x * total + row) * 2]);
-  float o[2] = {0.f, 0.f};
-  for (int x = 0; x < splits; ++x) {
-    const float m = st[(x * total + row) * 2];
-    const float by = m == -kInf ? 0.f : exp2f(m - top);
-    sum += by * st[(x * total + row) * 2 + 1];
+  f32x2 o = {};
+  for (int x0 = 0; x0 < splits; x0 += 64) {
+    f32x2 mine = {-kInf, 0.f};
+    if (x0 + lane < splits) mine = *reinterpret_cast<const f32x2*>(st + ((x0 + lane) * total + row) * 2);
+    float m = mine[0];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int d = lane_id() + 64 * e;
-      if (d < a.dim) o[e] += by * a.part[(x * total + row) * a.dim + d];
+    for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k, 64));
+    const float t = fmaxf(top, m);
+    const float keep = top == -kInf ? 0.f : exp2f(top - t);
+    const float by = mine[0] == -kInf ? 0.f : exp2f(mine[0] - t);
+    top = t;
+    sum = sum * keep + lanes_sum<64>(by * mine[1]);
+    o[0] *= keep;
+    o[1] *= keep;
+    const int n = min(splits - x0, 64);
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) {
+      const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(by), x));
+      f32x2 v = {};
+      if (d < a.dim) v = *reinterpret_cast<const f32x2*>(a.part + ((x0 + x) * total + row) * a.dim + d);
+      o[0] += f * v[0];
+      o[1] += f * v[1];
     }
   }
+  if (d >= a.dim) return;
   const int64_t sq = row / a.q_heads, qh = row % a.q_heads;
   const bool none = a.off[sq] <= 0;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int d = lane_id() + 64 * e;
-    if (d < a.dim)
-      static_cast<T*>(a.out.p)[sq * a.out.tok + qh * a.out.head + d] = (T)(none ? 0.f : o[e] / sum);
-  }
+  T* out = static_cast<T*>(a.out.p) + sq * a.out.tok + qh * a.out.head + d;
+  out[0] = (T)(none ? 0.f : o[0] / sum);
+  out[1] = (T)(none ? 0.f : o[1] / sum);
 }
 
 // ---------------------------------------------------------------- launches
@@ -908,8 +989,10 @@ AttnBwdPlan plan_attn_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok) {
   AttnBwdPlan p{};
   p.off_part = ((size_t)n_tok * a.q_heads * sizeof(float) + 255) & ~(size_t)255;
   p.bytes = p.off_part;
-  if (a.sinks > 0)  // for any window
-    p.bytes += (size_t)(n_tok / sink_chunk(n_tok) + 2 * n_seq + 1) * a.kv_heads * 2 * a.sinks * a.dim * sizeof(float);
+  if (a.sinks > 0) {  // for any window: the smallest reaches the fewest queries
+    const SinkSlots n(n_tok, n_seq, 1, sink_chunk(n_tok));
+    p.bytes += (size_t)(n.chunk_slots + n.first_tiles + 1) * a.kv_heads * 2 * a.sinks * a.dim * sizeof(float);
+  }
   return p;
 }
 
@@ -941,10 +1024,10 @@ hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
                        dim3(kThreads), 0, st, a);
     const int chunk = sink_chunk(a.n_tok);
     const bool sinks = has_sink_chunks(a.sinks, a.window, a.n_tok);
-    const int64_t sink_slots = sinks ? a.n_tok / chunk + 2 * a.n_seq : 0;
+    const int64_t sink_slots = sinks ? SinkSlots(a.n_tok, a.n_seq, a.window, chunk).chunk_slots : 0;
     hipLaunchKernelGGL((attn_dkv<T, decltype(d)::value>),
-                       dim3((unsigned)((slots + sink_slots) * a.kv_heads)), dim3(kThreads), 0, st, a,
-                       (int)(slots * a.kv_heads), chunk);
+                       dim3((unsigned)((slots + sink_slots) * a.kv_heads)),
+                       dim3(DkvShape<decltype(d)::value>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
     if (sinks)
       hipLaunchKernelGGL((attn_sink_join<T>), dim3((unsigned)(a.n_seq * a.kv_heads)), dim3(kThreads), 0,
                          st, a, chunk);
@@ -960,8 +1043,8 @@ hipError_t launch_attn_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStr
                        dim3((unsigned)(a.n_seq * a.kv_heads * cols * p.splits)), dim3(kThreads), 0, st, a,
                        p.splits);
     if (p.splits > 1)
-      hipLaunchKernelGGL((attn_decode_join<T>), dim3((unsigned)(((int64_t)a.n_seq * a.q_heads + 3) / 4)),
-                         dim3(kThreads), 0, st, a, p.splits);
+      hipLaunchKernelGGL((attn_decode_join<T>), dim3((unsigned)((int64_t)a.n_seq * a.q_heads)), dim3(64), 0,
+                         st, a, p.splits);
   });
   return hipGetLastError();
 }

@@ -278,37 +278,33 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   }
 }
 
-// Sums the blocks' column sums: 32 columns a workgroup, 8 threads a column, in a fixed order.
+// Sums the blocks' column sums: 32 columns of one of the two a workgroup, 32 threads a column, in a
+// fixed order.
+constexpr int kJoin = 1024;
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_join(NormArgs a) {
-  __shared__ float lds[8][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
-  const int part = threadIdx.x >> 5;
-  float t[2] = {0.f, 0.f};
+__global__ void __launch_bounds__(kJoin) norm_join(NormArgs a) {
+  __shared__ float lds[32][33];
+  const int x = threadIdx.x & 31, part = threadIdx.x >> 5, k = blockIdx.y;
+  const int col = blockIdx.x * 32 + x;
+  float t = 0.f;
   if (col < a.dim) {
-    for (int b = part; b < a.blocks; b += 8) {
-      t[0] += a.part[((size_t)b * 2 + 0) * a.dim + col];
-      t[1] += a.part[((size_t)b * 2 + 1) * a.dim + col];
-    }
+#pragma unroll 8
+    for (int b = part; b < a.blocks; b += 32) t += a.part[((size_t)b * 2 + k) * a.dim + col];
   }
+  lds[part][x] = t;
+  __syncthreads();
+  if (part == 0 && col < a.dim) {
+    float v = 0.f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    __syncthreads();
-    lds[part][threadIdx.x & 31] = t[k];
-    __syncthreads();
-    if (part == 0 && col < a.dim) {
-      float v = 0.f;
-      for (int i = 0; i < 8; ++i) v += lds[i][threadIdx.x & 31];
-      if (k == 1) {
-        if (a.dw_pre) a.dw_pre[col] = v;
-      } else if (a.gate_kind == EMB_GATE_VECTOR) {
-        // the sum is of dR * y * inv(y) alone: the gate and the weights are the same in every row
-        const float g = (float)static_cast<const T*>(a.gate)[col];
-        if (a.dgate) static_cast<float*>(a.dgate)[col] = v * (a.w_post ? a.w_post[col] : 1.f);
-        if (a.dw_post) a.dw_post[col] = v * g;
-      } else if (a.dw_post) {
-        a.dw_post[col] = v;
-      }
+    for (int i = 0; i < 32; ++i) v += lds[i][x];
+    if (k == 1) {
+      if (a.dw_pre) a.dw_pre[col] = v;
+    } else if (a.gate_kind == EMB_GATE_VECTOR) {
+      // the sum is of dR * y * inv(y) alone: the gate and the weights are the same in every row
+      if (a.dgate) static_cast<float*>(a.dgate)[col] = v * (a.w_post ? a.w_post[col] : 1.f);
+      if (a.dw_post) a.dw_post[col] = v * (float)static_cast<const T*>(a.gate)[col];
+    } else if (a.dw_post) {
+      a.dw_post[col] = v;
     }
   }
 }
@@ -323,7 +319,7 @@ template <typename T, int TPR, int NC>
 void go_bwd(const NormArgs& a, hipStream_t st) {
   if (a.blocks)
     hipLaunchKernelGGL((norm_bwd<T, TPR, NC>), dim3((unsigned)a.blocks), dim3(kThreads), 0, st, a);
-  hipLaunchKernelGGL((norm_join<T>), dim3((unsigned)((a.dim + 31) / 32)), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((norm_join<T>), dim3((unsigned)((a.dim + 31) / 32), 2), dim3(kJoin), 0, st, a);
 }
 
 template <typename T>
@@ -345,11 +341,13 @@ void pick_type(const NormArgs& a, bool bwd, hipStream_t st) {
 
 }  // namespace
 
-// Blocks of the backward: 16 rows each where there are few, no more than 1024.
+// Blocks of the backward: as many as are resident at once (three waves a SIMD by its registers), so
+// that the last ones do not run alone; each writes and norm_join reads 8 dim bytes.
 int norm_bwd_blocks(int64_t rows, int32_t dim) {
   const int64_t per = dim <= 256 ? 8 : dim <= 512 ? 4 : 1;
-  int64_t b = (rows + per * 4 - 1) / (per * 4);
-  return (int)(b < 1024 ? b : 1024);
+  const int64_t most = dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
+  const int64_t b = (rows + per - 1) / per;
+  return (int)(b < most ? b : most);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
