@@ -92,14 +92,19 @@ __device__ __forceinline__ void hide_keys(const AttnArgs& a, int i, int j0, f32x
 }
 
 // ---------------------------------------------------------------- LDS tiles
-// Rows of DH elements, 16 bytes apart from one another, so that the eight rows whose pieces one pass
-// of a read touches lie in different banks and every place within a tile is a constant from a lane's own.
+// Rows of DH elements with 16 bytes between them.  LDS has 64 banks of 4 bytes.  A left operand's read
+// takes one 16-byte piece of 16 rows at once: an odd number of pieces a row puts them into 16 different
+// places.  A transposing read takes four pieces of four rows at once: row r of each 16 lies at place
+// 4 (r % 4) + r / 4, so that those four rows, consecutive ones, are four places and with them four
+// pieces apart.  (In order, they overlapped: half the cycles that the forward kept LDS busy were
+// conflicts.)  Every place within a tile is a constant from a lane's own.
 template <int DH>
 struct Tile {
   static constexpr int kPieces = DH / 8;  // of 16 bytes
   static constexpr int kRow = DH * 2 + 16;
   static constexpr int kBytes = kStageRows * kRow;
-  __device__ static __forceinline__ int at(int row, int piece) { return row * kRow + piece * 16; }
+  __device__ static __forceinline__ int place(int row) { return (row & ~15) | (row & 3) << 2 | (row >> 2 & 3); }
+  __device__ static __forceinline__ int at(int row, int piece) { return place(row) * kRow + piece * 16; }
 };
 
 template <int DH, int THREADS>
@@ -131,7 +136,7 @@ struct Staged {
 template <typename T, int DH>
 __device__ __forceinline__ typename Vec8<T>::t left(const char* lds, int row0, int ks) {
   const int l = lane_id();
-  return *reinterpret_cast<const typename Vec8<T>::t*>(lds + Tile<DH>::at(l & 31, l >> 5) + Tile<DH>::at(row0, 2 * ks));
+  return *reinterpret_cast<const typename Vec8<T>::t*>(lds + Tile<DH>::at(l & 31, l >> 5) + row0 * Tile<DH>::kRow + ks * 32);
 }
 // Left operand, transposed: columns 32 db .. 32 db + 31 as rows, rows row0 .. row0 + 15 as k, in the
 // order in which a result's registers hold them.
@@ -140,8 +145,9 @@ __device__ __forceinline__ typename Vec8<T>::t left_t(const char* lds, int row0,
   const int l = lane_id();
   const char* p = lds + Tile<DH>::at(4 * (l >> 5) + ((l & 15) >> 2), ((l >> 4) & 1) * 2) + (l & 3) * 8;
   typedef __attribute__((address_space(3))) i16x4* Lds;
-  const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + Tile<DH>::at(row0, db * 4)));
-  const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + Tile<DH>::at(row0 + 8, db * 4)));
+  p += row0 * Tile<DH>::kRow + db * 64;
+  const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p);
+  const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 2 * Tile<DH>::kRow));  // eight rows on
   const i16x8 v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(typename Vec8<T>::t, v);
 }
@@ -725,29 +731,27 @@ __global__ void __launch_bounds__(DkvShape<DH>::kBlock, 2) attn_dkv(AttnArgs a, 
   }
 }
 
-// dk and dv of the sinks from the first key tile's sums and every chunk's, in that order.
+// dk and dv of the sinks from the first key tile's sums and every chunk's, in that order: one element a
+// thread.  Only sequences longer than reach have any, and each of those is alone in its tile of
+// reach + 1 tokens.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int chunk) {
-  const int kh = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
-  const int64_t begin = min(max((int64_t)a.off[b], (int64_t)0), a.n_tok);
-  const int64_t len = min(max((int64_t)a.off[b + 1], begin), a.n_tok) - begin;
+  const int kh = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
   const int64_t reach = reach_of(a.window);
-  if (len <= reach) return;
-  const int64_t n = (len - reach + chunk - 1) / chunk;
-  const int64_t first = begin / chunk + begin / (reach + 1);
+  const Seq s = find_tile(a, slot, [&](int64_t t, int) { return t / (reach + 1); });
+  if (s.tile != 0 || s.len <= reach) return;
+  const int e = blockIdx.y * kThreads + threadIdx.x;
   const int64_t each = 2 * a.sinks * (int64_t)a.dim, step = each * a.kv_heads;
-  const float* tile = first_tile_part(a, begin, b, chunk, kh);
-  const float* part = sink_part(a, first, kh);
-  for (int e = threadIdx.x; e < each; e += kThreads) {
-    float t = tile[e];
+  if (e >= each) return;
+  const int64_t n = (s.len - reach + chunk - 1) / chunk;
+  const float* part = sink_part(a, s.begin / chunk + s.begin / (reach + 1), kh) + e;
+  float t = first_tile_part(a, s.begin, s.index, chunk, kh)[e];
 #pragma unroll 8
-    for (int64_t x = 0; x < n; ++x) t += part[x * step + e];
-    const int row = e / a.dim % a.sinks, col = e % a.dim;
-    const bool is_v = e >= a.sinks * a.dim;
-    const EmbHeads& to = is_v ? a.dv : a.dk;
-    T* p = static_cast<T*>(to.p) + (begin + row) * to.tok + kh * to.head;
-    p[col] = (T)(is_v ? t : t * a.scale);
-  }
+  for (int64_t x = 0; x < n; ++x) t += part[x * step];
+  const int row = e / a.dim % a.sinks, col = e % a.dim;
+  const bool is_v = e >= a.sinks * a.dim;
+  const EmbHeads& to = is_v ? a.dv : a.dk;
+  static_cast<T*>(to.p)[(s.begin + row) * to.tok + kh * to.head + col] = (T)(is_v ? t : t * a.scale);
 }
 
 // ---------------------------------------------------------------- one new event
@@ -1029,8 +1033,10 @@ hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
                        dim3((unsigned)((slots + sink_slots) * a.kv_heads)),
                        dim3(DkvShape<decltype(d)::value>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
     if (sinks)
-      hipLaunchKernelGGL((attn_sink_join<T>), dim3((unsigned)(a.n_seq * a.kv_heads)), dim3(kThreads), 0,
-                         st, a, chunk);
+      hipLaunchKernelGGL((attn_sink_join<T>),
+                         dim3((unsigned)((a.n_tok / (reach_of(a.window) + 1) + 1) * a.kv_heads),
+                              (unsigned)((2 * a.sinks * a.dim + kThreads - 1) / kThreads)),
+                         dim3(kThreads), 0, st, a, chunk);
   });
   return hipGetLastError();
 }
