@@ -26,8 +26,18 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_huge_valf();
 constexpr int kThreads = 256;
-constexpr int kQTile = 128;  // tokens of a workgroup: 32 for each of its four waves
-constexpr int kStageRows = 64;  // rows of an LDS tile
+
+// The two shapes of a workgroup in training.  Four waves have 128 tokens, 32 each, and share LDS tiles
+// of 64 rows, two of each so that one barrier a tile is enough.  One wave has 32 tokens and tiles of 32
+// rows to itself: no wave waits for another or is left without tokens by a short sequence, and what the
+// rows next to each other read twice is in the caches; see one_wave().
+template <int WAVES>
+struct Group {
+  static constexpr int kTokens = 32 * WAVES;
+  static constexpr int kThreads = 64 * WAVES;
+  static constexpr int kRows = WAVES == 1 ? 32 : 64;  // of an LDS tile
+  static constexpr int kBuffers = WAVES == 1 ? 1 : 2;
+};
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
@@ -102,17 +112,16 @@ template <int DH>
 struct Tile {
   static constexpr int kPieces = DH / 8;  // of 16 bytes
   static constexpr int kRow = DH * 2 + 16;
-  static constexpr int kBytes = kStageRows * kRow;
   __device__ static __forceinline__ int place(int row) { return (row & ~15) | (row & 3) << 2 | (row >> 2 & 3); }
   __device__ static __forceinline__ int at(int row, int piece) { return place(row) * kRow + piece * 16; }
 };
 
-template <int DH, int THREADS>
+template <int DH, int ROWS, int THREADS>
 struct Staged {
   static constexpr int kPieces = Tile<DH>::kPieces;
-  static constexpr int kRegs = kStageRows * kPieces / THREADS;
+  static constexpr int kRegs = ROWS * kPieces / THREADS;
   u32x4 r[kRegs];
-  // Rows row0 .. row0 + 63 of a head; zeros past `len` rows and past D columns.
+  // Rows row0 .. row0 + ROWS - 1 of a head; zeros past `len` rows and past D columns.
   template <typename T>
   __device__ __forceinline__ void load(const T* base, int64_t stride, int row0, int len, int D) {
 #pragma unroll
@@ -287,33 +296,38 @@ __device__ __forceinline__ void again_dkv(const AttnArgs& a, int64_t begin, int 
 }
 
 // ---------------------------------------------------------------- which keys a query tile meets
-// Tiles of 64 keys: the one that holds the sinks where the window does not reach it, then the
-// window's.
+// The tile that holds the sinks where the window's tiles do not reach it, then the window's.
+template <int WAVES>
 struct KeyTiles {
+  static constexpr int kRows = Group<WAVES>::kRows;
   int first, n, sink;
   __device__ __forceinline__ KeyTiles(const AttnArgs& a, int i0, int len) {
-    const int end = min(len, i0 + kQTile);
-    first = max(i0 - a.window + 1, 0) & ~(kStageRows - 1);
+    const int end = min(len, i0 + Group<WAVES>::kTokens);
+    first = max(i0 - a.window + 1, 0) & ~(kRows - 1);
     sink = a.sinks > 0 && first > 0 ? 1 : 0;
-    n = (end - first + kStageRows - 1) / kStageRows + sink;
+    n = (end - first + kRows - 1) / kRows + sink;
   }
-  __device__ __forceinline__ int key0(int it) const {
-    return it < sink ? 0 : first + (it - sink) * kStageRows;
+  __device__ __forceinline__ int key0(int it) const { return it < sink ? 0 : first + (it - sink) * kRows; }
+  // of a tile that is there for the sinks no other key is looked at
+  __device__ __forceinline__ int end(const AttnArgs& a, int it, int len) const {
+    return it < sink ? min(a.sinks, len) : len;
   }
 };
 
 // ---------------------------------------------------------------- forward
-template <typename T, int DH>
-__global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
+template <typename T, int DH, int WAVES>
+__global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a) {
   typedef typename Vec8<T>::t V8;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][Tile<DH>::kBytes];
+  typedef Group<WAVES> G;
+  constexpr int kSubs = G::kRows / 32;
+  __shared__ __attribute__((aligned(16))) char lds[G::kBuffers][2][G::kRows * Tile<DH>::kRow];
   const int group = a.q_heads / a.kv_heads;
   const int kh = blockIdx.x % a.kv_heads;
   const int rest = blockIdx.x / a.kv_heads;
   const int h = kh * group + rest % group;
-  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / kQTile + b; });
-  if (s.tile < 0 || (int64_t)s.tile * kQTile >= s.len) return;
-  const int i0 = s.tile * kQTile;
+  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
+  if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
+  const int i0 = s.tile * G::kTokens;
   const int iw = __builtin_amdgcn_readfirstlane(i0 + (threadIdx.x >> 6) * 32);
   const int i = iw + (lane_id() & 31);
   const bool live = i < s.len;
@@ -328,40 +342,44 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
   }
   const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
 
-  const KeyTiles tiles(a, i0, s.len);
+  const KeyTiles<WAVES> tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
-  Staged<DH, kThreads> ks_, vs_;
-  ks_.load(kp, a.k.tok, tiles.key0(0), s.len, a.dim);
-  vs_.load(vp, a.v.tok, tiles.key0(0), s.len, a.dim);
+  Staged<DH, G::kRows, G::kThreads> ks_, vs_;
+  auto load = [&](int it) {
+    ks_.load(kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+    vs_.load(vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+  };
+  load(0);
 
   f32x16 o[DH / 32] = {};
   float m = -kInf, l = 0.f;  // the maximum that o and l stand at, and this lane's half of the sum
   for (int it = 0; it < tiles.n; ++it) {
-    char* kt = lds[it & 1][0];
-    char* vt = lds[it & 1][1];
+    char* kt = lds[it & (G::kBuffers - 1)][0];
+    char* vt = lds[it & (G::kBuffers - 1)][1];
+    if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
     ks_.store(kt);
     vs_.store(vt);
-    if (it + 1 < tiles.n) {
-      ks_.load(kp, a.k.tok, tiles.key0(it + 1), s.len, a.dim);
-      vs_.load(vp, a.v.tok, tiles.key0(it + 1), s.len, a.dim);
-    }
+    if (it + 1 < tiles.n) load(it + 1);
     __syncthreads();
     const int j0 = tiles.key0(it);
     if (iw >= s.len || j0 > iw + 31) continue;
-    if (j0 >= a.sinks && j0 + 63 <= iw - a.window) continue;
+    if (j0 >= a.sinks && j0 + G::kRows - 1 <= iw - a.window) continue;
 
-    f32x16 sc[2] = {};
+    f32x16 sc[kSubs] = {};
 #pragma unroll
-    for (int ks = 0; ks < DH / 16; ++ks) {
-      sc[0] = mma(left<T, DH>(kt, 0, ks), q[ks], sc[0]);
-      sc[1] = mma(left<T, DH>(kt, 32, ks), q[ks], sc[1]);
+    for (int ks = 0; ks < DH / 16; ++ks)
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub)
+        sc[sub] = mma(left<T, DH>(kt, 32 * sub, ks), q[ks], sc[sub]);
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub) {
+      const int js = j0 + 32 * sub;
+      if (js + 31 > iw || js < iw + 31 - a.window + 1) hide_keys(a, i, js, sc[sub], -kInf);
     }
-    if (j0 + 31 > iw || j0 < iw + 31 - a.window + 1) hide_keys(a, i, j0, sc[0], -kInf);
-    if (j0 + 63 > iw || j0 + 32 < iw + 31 - a.window + 1) hide_keys(a, i, j0 + 32, sc[1], -kInf);
     float top = sc[0][0];
 #pragma unroll
-    for (int r = 1; r < 32; ++r) top = fmaxf(top, sc[r >> 4][r & 15]);
+    for (int r = 1; r < 16 * kSubs; ++r) top = fmaxf(top, sc[r >> 4][r & 15]);
     top = swap32_max(top);
     // o and l move to a new maximum only when it is over 2^8 times the old one's exponential: below
     // that the probabilities stay small enough for 16 bits and the sums for 32
@@ -375,12 +393,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
     }
     const float off = m == -kInf ? 0.f : m * c;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
+    for (int r = 0; r < 16 * kSubs; ++r) {
       sc[r >> 4][r & 15] = __builtin_amdgcn_exp2f(fmaf(sc[r >> 4][r & 15], c, -off));
       l += sc[r >> 4][r & 15];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2 * kSubs; ++k) {
       const V8 pb = right_of<T>(sc[k >> 1], 8 * (k & 1));
 #pragma unroll
       for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T, DH>(vt, 16 * k, db), pb, o[db]);
@@ -396,27 +414,32 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd(AttnArgs a) {
 
 // ---------------------------------------------------------------- backward: dq
 // As the forward, with dout as a second right operand; also writes delta.
-template <typename T, int DH>
-__global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
+template <typename T, int DH, int WAVES>
+__global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a) {
   typedef typename Vec8<T>::t V8;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][Tile<DH>::kBytes];
+  typedef Group<WAVES> G;
+  constexpr int kSubs = G::kRows / 32;
+  __shared__ __attribute__((aligned(16))) char lds[G::kBuffers][2][G::kRows * Tile<DH>::kRow];
   const int group = a.q_heads / a.kv_heads;
   const int kh = blockIdx.x % a.kv_heads;
   const int rest = blockIdx.x / a.kv_heads;
   const int h = kh * group + rest % group;
-  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / kQTile + b; });
-  if (s.tile < 0 || (int64_t)s.tile * kQTile >= s.len) return;
-  const int i0 = s.tile * kQTile;
+  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
+  if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
+  const int i0 = s.tile * G::kTokens;
   const int iw = __builtin_amdgcn_readfirstlane(i0 + (threadIdx.x >> 6) * 32);
   const int i = iw + (lane_id() & 31);
   const bool live = i < s.len;
 
-  const KeyTiles tiles(a, i0, s.len);
+  const KeyTiles<WAVES> tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
-  Staged<DH, kThreads> ks_, vs_;
-  ks_.load(kp, a.k.tok, tiles.key0(0), s.len, a.dim);
-  vs_.load(vp, a.v.tok, tiles.key0(0), s.len, a.dim);
+  Staged<DH, G::kRows, G::kThreads> ks_, vs_;
+  auto load = [&](int it) {
+    ks_.load(kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+    vs_.load(vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+  };
+  load(0);
 
   V8 q[DH / 16], d[DH / 16];
   right_row<T, DH>(a.q, s.begin + i, h, live, a.dim, q);
@@ -438,19 +461,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
 
   f32x16 dq[DH / 32] = {};
   for (int it = 0; it < tiles.n; ++it) {
-    char* kt = lds[it & 1][0];
-    char* vt = lds[it & 1][1];
+    char* kt = lds[it & (G::kBuffers - 1)][0];
+    char* vt = lds[it & (G::kBuffers - 1)][1];
+    if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
     ks_.store(kt);
     vs_.store(vt);
-    if (it + 1 < tiles.n) {
-      ks_.load(kp, a.k.tok, tiles.key0(it + 1), s.len, a.dim);
-      vs_.load(vp, a.v.tok, tiles.key0(it + 1), s.len, a.dim);
-    }
+    if (it + 1 < tiles.n) load(it + 1);
     __syncthreads();
     const int j0 = tiles.key0(it);
     if (iw >= s.len) continue;
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
+    for (int sub = 0; sub < kSubs; ++sub) {
       const int js = j0 + 32 * sub;
       if (js > iw + 31 || (js >= a.sinks && js + 31 <= iw - a.window)) continue;
       f32x16 sc = {}, dp = {};
@@ -492,25 +513,33 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq(AttnArgs a) {
 // values in LDS make it two, at a half more reads of LDS.
 constexpr int kSinkKeys = EMB_ATTN_MAX_SINKS;
 
-__host__ __device__ inline int64_t reach_of(int window) { return (int64_t)kQTile + window - 1; }
+// Queries from here on see nothing of the first key tile but the sinks.
+__host__ __device__ inline int64_t reach_of(int window, int tokens) { return (int64_t)tokens + window - 1; }
 
-// Partial sums of the sinks, [2][sinks][dim] each: first those of the chunks by slot, then those of
-// the first key tiles of sequences longer than reach, of which a batch has at most n_tok / 129.
-// Sequence b's chunks start at slot begin / chunk + begin / (reach + 1): where its length is over
-// reach that leaves room for len / chunk + 1 of them.
+// Where partial sums of the sinks go, [2][sinks][dim] each: first those of the chunks by slot, then those
+// of the first key tiles.  Only sequences longer than reach have any; each is given a number, its own
+// or, where the batch has more sequences than could be that long, which part of reach + 1 tokens it
+// begins in.  A sequence's chunks start at slot begin / chunk + number, which leaves it room for
+// len / chunk + 1 of them.
 struct SinkSlots {
-  int64_t chunk_slots, first_tiles;
-  __host__ __device__ SinkSlots(int64_t n_tok, int64_t n_seq, int window, int chunk) {
-    chunk_slots = n_tok / chunk + n_tok / (reach_of(window) + 1) + 1;
-    first_tiles = n_seq < n_tok / (kQTile + 1) + 1 ? n_seq : n_tok / (kQTile + 1) + 1;
+  int64_t reach, numbers, chunk_slots;
+  int chunk;
+  bool by_sequence;
+  __host__ __device__ SinkSlots(int64_t n_tok, int64_t n_seq, int window, int tokens, int chunk_) {
+    reach = reach_of(window, tokens);
+    chunk = chunk_;
+    by_sequence = n_seq <= n_tok / (reach + 1);
+    numbers = by_sequence ? n_seq : n_tok / (reach + 1) + 1;
+    chunk_slots = n_tok / chunk + numbers + 1;
   }
+  __host__ __device__ int64_t number(int64_t begin, int b) const { return by_sequence ? b : begin / (reach + 1); }
+  __host__ __device__ int64_t first(int64_t begin, int b) const { return begin / chunk + number(begin, b); }
 };
 __device__ __forceinline__ float* sink_part(const AttnArgs& a, int64_t slot, int kh) {
   return a.part + (slot * a.kv_heads + kh) * 2 * a.sinks * (int64_t)a.dim;
 }
-__device__ __forceinline__ float* first_tile_part(const AttnArgs& a, int64_t begin, int index, int chunk, int kh) {
-  const SinkSlots n(a.n_tok, a.n_seq, a.window, chunk);
-  return sink_part(a, n.chunk_slots + (n.first_tiles == a.n_seq ? index : begin / (kQTile + 1)), kh);
+__device__ __forceinline__ float* first_tile_part(const AttnArgs& a, const SinkSlots& p, const Seq& s, int kh) {
+  return sink_part(a, p.chunk_slots + p.number(s.begin, s.index), kh);
 }
 
 // Adds the sums of the upper half of `n` waves to those of the lower half, through LDS.
@@ -528,29 +557,33 @@ __device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave,
   }
 }
 
-template <int DH>
+template <int DH, int WAVES>
 struct DkvShape {
-  static constexpr bool kWide = DH == 128;
-  static constexpr int kWaves = kWide ? 8 : 4;
+  typedef Group<WAVES> G;
+  static constexpr bool kWide = DH == 128 && WAVES == 4;
+  static constexpr int kWaves = kWide ? 8 : WAVES;
   static constexpr int kBlock = kWaves * 64;
-  static constexpr int kShare = kWaves / 4;  // waves that share 32 keys
+  static constexpr int kShare = kWide ? 2 : 1;  // waves that share 32 keys
+  static constexpr int kTile = G::kRows * Tile<DH>::kRow;
+  static constexpr int kKeyTiles = kWide ? 2 : 0;
 };
-
-template <int DH>
+template <int DH, int WAVES>
 struct DkvShared {
-  static constexpr int kKeyTiles = DkvShape<DH>::kWide ? 2 : 0;
-  char q[2][Tile<DH>::kBytes], d[2][Tile<DH>::kBytes];
-  float lse[2][kStageRows], delta[2][kStageRows];
-  char k[kKeyTiles][Tile<DH>::kBytes], v[kKeyTiles][Tile<DH>::kBytes];
+  typedef DkvShape<DH, WAVES> P;
+  char q[P::G::kBuffers][P::kTile], d[P::G::kBuffers][P::kTile];
+  float lse[P::G::kBuffers][P::G::kRows], delta[P::G::kBuffers][P::G::kRows];
+  char k[P::kKeyTiles][P::kTile], v[P::kKeyTiles][P::kTile];
 };
 
 // SINK: rows `row0` to `row1` - 1 against the sinks, the sums to the slot's place; otherwise those rows
 // against the 128 keys from j0.
-template <typename T, int DH, bool SINK>
-__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const Seq& s, int kh, int j0, int row0,
-                                    int row1, int64_t slot, int chunk) {
+template <typename T, int DH, int WAVES, bool SINK>
+__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh, const SinkSlots& parts,
+                                    const Seq& s, int kh, int j0, int row0, int row1, int64_t slot) {
   typedef typename Vec8<T>::t V8;
-  typedef DkvShape<DH> P;
+  typedef DkvShape<DH, WAVES> P;
+  typedef Group<WAVES> G;
+  constexpr int kRows = G::kRows;
   const int group = a.q_heads / a.kv_heads;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int jrow = SINK ? 0 : 32 * (wave & 3);  // the wave's keys within the tile
@@ -565,9 +598,9 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const 
     const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      Staged<DH, P::kBlock> ks_, vs_;
-      ks_.load(kp, a.k.tok, j0 + kStageRows * x, s.len, a.dim);
-      vs_.load(vp, a.v.tok, j0 + kStageRows * x, s.len, a.dim);
+      Staged<DH, kRows, P::kBlock> ks_, vs_;
+      ks_.load(kp, a.k.tok, j0 + kRows * x, s.len, a.dim);
+      vs_.load(vp, a.v.tok, j0 + kRows * x, s.len, a.dim);
       ks_.store(sh.k[x]);
       vs_.store(sh.v[x]);
     }
@@ -577,23 +610,23 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const 
   }
   const float c = a.scale * kLog2e;
 
-  const int n_tiles = (row1 - row0 + kStageRows - 1) / kStageRows;
-  Staged<DH, P::kBlock> qs_, ds_;
-  float stat = 0.f;  // threads 0-63: lse of a row; 64-127: its delta
+  const int n_tiles = (row1 - row0 + kRows - 1) / kRows;
+  Staged<DH, kRows, P::kBlock> qs_, ds_;
+  float stat = 0.f;  // the first kRows threads: lse of a row; as many after them: its delta
   int next_h = kh * group, next_r0 = row0;  // what is loaded next
   auto load = [&]() {
     const int h = next_h, r0 = next_r0;
     qs_.load(static_cast<const T*>(a.q.p) + s.begin * a.q.tok + h * a.q.head, a.q.tok, r0, row1, a.dim);
     ds_.load(static_cast<const T*>(a.dout.p) + s.begin * a.dout.tok + h * a.dout.head, a.dout.tok,
              r0, row1, a.dim);
-    if (threadIdx.x < 2 * kStageRows) {
-      const int row = r0 + (threadIdx.x & 63);
-      const float* p = threadIdx.x < kStageRows ? a.lse : a.delta;
+    if (threadIdx.x < 2 * kRows) {
+      const int row = r0 + (threadIdx.x & (kRows - 1));
+      const float* p = threadIdx.x < kRows ? a.lse : a.delta;
       stat = row < row1 ? p[(int64_t)h * a.n_tok + s.begin + row] : 0.f;
       // a row that is not there gets probabilities of zero
-      if (threadIdx.x < kStageRows) stat = row < row1 ? stat * kLog2e : kInf;
+      if (threadIdx.x < kRows) stat = row < row1 ? stat * kLog2e : kInf;
     }
-    next_r0 += kStageRows;
+    next_r0 += kRows;
     if (next_r0 >= row1) {
       next_r0 = row0;
       ++next_h;
@@ -603,22 +636,24 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const 
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
   int r0 = row0;
   const int steps = n_tiles * group;  // of all heads of the group
-  for (int step = 0; step < steps; ++step, r0 = r0 + kStageRows < row1 ? r0 + kStageRows : row0) {
-    const int b = step & 1;
+  for (int step = 0; step < steps; ++step, r0 = r0 + kRows < row1 ? r0 + kRows : row0) {
+    const int b = step & (G::kBuffers - 1);
+    if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
     qs_.store(sh.q[b]);
     ds_.store(sh.d[b]);
-    if (threadIdx.x < kStageRows) sh.lse[b][threadIdx.x] = stat;
-    else if (threadIdx.x < 2 * kStageRows) sh.delta[b][threadIdx.x - kStageRows] = stat;
+    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat;
+    else if (threadIdx.x < 2 * kRows) sh.delta[b][threadIdx.x - kRows] = stat;
     if (step + 1 < steps) load();
     __syncthreads();
     if (jw >= s.len) continue;
 #pragma unroll
-    for (int sub_ = 0; sub_ < 2 / P::kShare; ++sub_) {
+    for (int sub_ = 0; sub_ < kRows / 32 / P::kShare; ++sub_) {
       const int sub = P::kShare == 2 ? wave >> 2 : sub_;
       const int is = r0 + 32 * sub;
       if (is >= row1) continue;
       if (SINK) {
-        if ((P::kShare == 2 ? step & 3 : (step * 2 + sub) & 3) != (wave & 3)) continue;
+        // rows go round the waves: by steps where a wave has a fixed half of each
+        if (P::kWaves > 1 && ((P::kShare == 2 ? step : step * 2 + sub) & 3) != (wave & 3)) continue;
       } else if (is + 31 < jw || (jw >= a.sinks && is >= jw + 31 + (int64_t)a.window)) {
         continue;
       }
@@ -679,8 +714,8 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const 
     finish(dk, 0);
     finish(dv, a.sinks);
   } else {
-    const bool split = a.sinks > 0 && reach_of(a.window) < s.len;
-    const EmbHeads row{split ? first_tile_part(a, s.begin, s.index, chunk, kh) : nullptr, 0, a.dim, 0};
+    const bool split = a.sinks > 0 && parts.reach < s.len;
+    const EmbHeads row{split ? first_tile_part(a, parts, s, kh) : nullptr, 0, a.dim, 0};
     // one matrix after the other; the rows of each that are not finite
     auto finish = [&](f32x16 (&x)[DH / 32], const EmbHeads& to, int row_at, float by) -> uint32_t {
       if constexpr (P::kShare == 2) fold_waves(x, fold, wave, 8);
@@ -711,41 +746,42 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH>& sh, const 
   }
 }
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(DkvShape<DH>::kBlock, 2) attn_dkv(AttnArgs a, int main_blocks, int chunk) {
-  __shared__ __attribute__((aligned(16))) DkvShared<DH> sh;
+template <typename T, int DH, int WAVES>
+__global__ void __launch_bounds__((DkvShape<DH, WAVES>::kBlock), 2)
+    attn_dkv(AttnArgs a, int main_blocks, int chunk) {
+  __shared__ __attribute__((aligned(16))) DkvShared<DH, WAVES> sh;
+  constexpr int kTokens = Group<WAVES>::kTokens;
   const bool sink = (int)blockIdx.x >= main_blocks;  // the same for the whole workgroup
   const int block = sink ? blockIdx.x - main_blocks : blockIdx.x;
   const int kh = block % a.kv_heads, slot = block / a.kv_heads;
-  const int64_t reach = reach_of(a.window);
+  const SinkSlots parts(a.n_tok, a.n_seq, a.window, kTokens, chunk);
   if (sink) {
-    const Seq s = find_tile(a, slot, [&](int64_t t, int) { return t / chunk + t / (reach + 1); });
-    const int64_t r0 = reach + (int64_t)s.tile * chunk;
+    const Seq s = find_tile(a, slot, [&](int64_t t, int b) { return parts.first(t, b); });
+    const int64_t r0 = parts.reach + (int64_t)s.tile * chunk;
     if (s.tile < 0 || r0 >= s.len) return;
-    dkv<T, DH, true>(a, sh, s, kh, 0, (int)r0, (int)min(r0 + chunk, (int64_t)s.len), slot, chunk);
+    dkv<T, DH, WAVES, true>(a, sh, parts, s, kh, 0, (int)r0, (int)min(r0 + chunk, (int64_t)s.len), slot);
   } else {
-    const Seq s = find_tile(a, slot, [](int64_t t, int b) { return t / kQTile + b; });
-    if (s.tile < 0 || (int64_t)s.tile * kQTile >= s.len) return;
-    const int j0 = s.tile * kQTile;
-    dkv<T, DH, false>(a, sh, s, kh, j0, j0, (int)min(j0 + reach, (int64_t)s.len), 0, chunk);
+    const Seq s = find_tile(a, slot, [](int64_t t, int b) { return t / kTokens + b; });
+    if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
+    const int j0 = s.tile * kTokens;
+    dkv<T, DH, WAVES, false>(a, sh, parts, s, kh, j0, j0, (int)min(j0 + parts.reach, (int64_t)s.len), 0);
   }
 }
 
 // dk and dv of the sinks from the first key tile's sums and every chunk's, in that order: one element a
-// thread.  Only sequences longer than reach have any, and each of those is alone in its tile of
-// reach + 1 tokens.
+// thread, a number (see SinkSlots) a workgroup.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int chunk) {
+__global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int tokens, int chunk) {
   const int kh = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
-  const int64_t reach = reach_of(a.window);
-  const Seq s = find_tile(a, slot, [&](int64_t t, int) { return t / (reach + 1); });
-  if (s.tile != 0 || s.len <= reach) return;
+  const SinkSlots parts(a.n_tok, a.n_seq, a.window, tokens, chunk);
+  const Seq s = find_tile(a, slot, [&](int64_t t, int b) { return parts.number(t, b); });
+  if (s.tile != 0 || s.len <= parts.reach) return;
   const int e = blockIdx.y * kThreads + threadIdx.x;
   const int64_t each = 2 * a.sinks * (int64_t)a.dim, step = each * a.kv_heads;
   if (e >= each) return;
-  const int64_t n = (s.len - reach + chunk - 1) / chunk;
-  const float* part = sink_part(a, s.begin / chunk + s.begin / (reach + 1), kh) + e;
-  float t = first_tile_part(a, s.begin, s.index, chunk, kh)[e];
+  const int64_t n = (s.len - parts.reach + chunk - 1) / chunk;
+  const float* part = sink_part(a, parts.first(s.begin, s.index), kh) + e;
+  float t = first_tile_part(a, parts, s, kh)[e];
 #pragma unroll 8
   for (int64_t x = 0; x < n; ++x) t += part[x * step];
   const int row = e / a.dim % a.sinks, col = e % a.dim;
@@ -962,6 +998,8 @@ __global__ void __launch_bounds__(64) attn_decode_join(AttnArgs a, int splits) {
 }
 
 // ---------------------------------------------------------------- launches
+constexpr int64_t kOneWave = 160;
+
 template <typename F>
 void by_shape(const AttnArgs& a, F f) {
   // the widths that kernels are built for; a head of another is padded with zeros in LDS
@@ -982,9 +1020,10 @@ int sink_chunk(int64_t n_tok) {
   while (n_tok / c > 1024) c *= 2;
   return (int)c;
 }
-// Whether a sequence of this batch can be longer than what its first key tile meets.
-bool has_sink_chunks(int32_t sinks, int32_t window, int64_t n_tok) {
-  return sinks > 0 && n_tok > reach_of(window);
+// Whether one wave a workgroup is the better shape: see the comment at its measurements below.
+bool one_wave(const AttnArgs& a) {
+  const int64_t mean = a.n_tok / a.n_seq;
+  return a.dim <= 64 && std::min<int64_t>(mean, a.window) <= kOneWave;
 }
 
 }  // namespace
@@ -993,9 +1032,9 @@ AttnBwdPlan plan_attn_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok) {
   AttnBwdPlan p{};
   p.off_part = ((size_t)n_tok * a.q_heads * sizeof(float) + 255) & ~(size_t)255;
   p.bytes = p.off_part;
-  if (a.sinks > 0) {  // for any window: the smallest reaches the fewest queries
-    const SinkSlots n(n_tok, n_seq, 1, sink_chunk(n_tok));
-    p.bytes += (size_t)(n.chunk_slots + n.first_tiles + 1) * a.kv_heads * 2 * a.sinks * a.dim * sizeof(float);
+  if (a.sinks > 0) {  // for any window and shape: the smallest leave the most sequences longer than reach
+    const SinkSlots n(n_tok, n_seq, 1, 32, sink_chunk(n_tok));
+    p.bytes += (size_t)(n.chunk_slots + n.numbers + 1) * a.kv_heads * 2 * a.sinks * a.dim * sizeof(float);
   }
   return p;
 }
@@ -1012,31 +1051,49 @@ AttnDecodePlan plan_attn_decode(const EmbAttn& a, int64_t n_seq, int64_t capacit
   return p;
 }
 
+template <typename T, int DH, int WAVES>
+void go_fwd(const AttnArgs& a, hipStream_t st) {
+  typedef Group<WAVES> G;
+  const unsigned grid = (unsigned)((a.n_tok / G::kTokens + a.n_seq) * a.q_heads);
+  hipLaunchKernelGGL((attn_fwd<T, DH, WAVES>), dim3(grid), dim3(G::kThreads), 0, st, a);
+}
+
+template <typename T, int DH, int WAVES>
+void go_bwd(const AttnArgs& a, hipStream_t st) {
+  typedef Group<WAVES> G;
+  const int64_t slots = a.n_tok / G::kTokens + a.n_seq;
+  hipLaunchKernelGGL((attn_dq<T, DH, WAVES>), dim3((unsigned)(slots * a.q_heads)), dim3(G::kThreads), 0, st, a);
+  const int chunk = sink_chunk(a.n_tok);
+  const SinkSlots n(a.n_tok, a.n_seq, a.window, G::kTokens, chunk);
+  const bool sinks = a.sinks > 0 && a.n_tok > n.reach;  // a sequence may be longer than reach
+  hipLaunchKernelGGL((attn_dkv<T, DH, WAVES>),
+                     dim3((unsigned)((slots + (sinks ? n.chunk_slots : 0)) * a.kv_heads)),
+                     dim3(DkvShape<DH, WAVES>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
+  if (sinks)
+    hipLaunchKernelGGL((attn_sink_join<T>),
+                       dim3((unsigned)(n.numbers * a.kv_heads),
+                            (unsigned)((2 * a.sinks * a.dim + kThreads - 1) / kThreads)),
+                       dim3(kThreads), 0, st, a, G::kTokens, chunk);
+}
+
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st) {
   by_shape(a, [&](auto t, auto d) {
-    const unsigned grid = (unsigned)((a.n_tok / kQTile + a.n_seq) * a.q_heads);
-    hipLaunchKernelGGL((attn_fwd<decltype(t), decltype(d)::value>), dim3(grid), dim3(kThreads), 0, st, a);
+    constexpr int DH = decltype(d)::value;
+    if constexpr (DH < 128) {
+      if (one_wave(a)) return go_fwd<decltype(t), DH, 1>(a, st);
+    }
+    go_fwd<decltype(t), DH, 4>(a, st);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
   by_shape(a, [&](auto t, auto d) {
-    typedef decltype(t) T;
-    const int64_t slots = a.n_tok / kQTile + a.n_seq;
-    hipLaunchKernelGGL((attn_dq<T, decltype(d)::value>), dim3((unsigned)(slots * a.q_heads)),
-                       dim3(kThreads), 0, st, a);
-    const int chunk = sink_chunk(a.n_tok);
-    const bool sinks = has_sink_chunks(a.sinks, a.window, a.n_tok);
-    const int64_t sink_slots = sinks ? SinkSlots(a.n_tok, a.n_seq, a.window, chunk).chunk_slots : 0;
-    hipLaunchKernelGGL((attn_dkv<T, decltype(d)::value>),
-                       dim3((unsigned)((slots + sink_slots) * a.kv_heads)),
-                       dim3(DkvShape<decltype(d)::value>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
-    if (sinks)
-      hipLaunchKernelGGL((attn_sink_join<T>),
-                         dim3((unsigned)((a.n_tok / (reach_of(a.window) + 1) + 1) * a.kv_heads),
-                              (unsigned)((2 * a.sinks * a.dim + kThreads - 1) / kThreads)),
-                         dim3(kThreads), 0, st, a, chunk);
+    constexpr int DH = decltype(d)::value;
+    if constexpr (DH < 128) {
+      if (one_wave(a)) return go_bwd<decltype(t), DH, 1>(a, st);
+    }
+    go_bwd<decltype(t), DH, 4>(a, st);
   });
   return hipGetLastError();
 }

@@ -72,7 +72,7 @@ int check_counts(int64_t n_seq, int64_t n_tok) {
 
 // A launch's grid: tile slots and sink chunks by heads, with room to spare.
 int check_grid(const EmbAttn* a, int64_t n_seq, int64_t n_tok) {
-  DENSE_CHECK((n_tok / 32 + 3 * n_seq) * (int64_t)a->q_heads < INT32_MAX, EMB_ERANGE,
+  DENSE_CHECK((n_tok / 16 + 3 * n_seq + 2) * (int64_t)a->q_heads < INT32_MAX, EMB_ERANGE,
               "attention: more tiles than one launch holds");
   return EMB_OK;
 }

@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from .emb import EMB_F16, EMB_F32, _check, _stream, lib as _emb_lib
+from .emb import EMB_F16, EMB_F32, _check, _stream as _emb_stream, lib as _emb_lib
 
 EMB_BF16 = 2
 ATTN_MAX_SINKS = 32
@@ -73,6 +73,16 @@ def lib() -> C.CDLL:
             fn.restype = C.c_int
         _LIB = L
     return _LIB
+
+
+# the current stream's handle without the Stream object around it, which costs 3 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return _emb_stream(stream)
 
 
 def _ptr(t, name: str, dtype=None, shape=None, optional: bool = False) -> Optional[int]:
@@ -265,7 +275,7 @@ def _tensors(ts, name: str, dtype, sizes):
     if len(ts) != len(sizes):
         raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(ts)}")
     for t, n in zip(ts, sizes):
-        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        if t.numel() != n or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
             raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} with the weights' "
                             f"sizes, got {t.dtype}, {tuple(t.shape)} on {t.device}")
     return (_VP * len(ts))(*[t.data_ptr() for t in ts])
