@@ -126,8 +126,6 @@ def _heads(t, name: str, dtype, shape) -> EmbHeads:
 
 
 def _attn(q, kv_heads: int, window: int, sinks: int, scale: float) -> EmbAttn:
-    if q.dim() != 3:
-        raise ValueError("q: expected [tokens, heads, dim]")
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q: expected float16 or bfloat16, got {q.dtype}")
     # no window past the longest sequence differs from one of 2^31 - 1
@@ -136,8 +134,8 @@ def _attn(q, kv_heads: int, window: int, sinks: int, scale: float) -> EmbAttn:
 
 
 def _kv_shape(q, k):
-    if k.dim() != 3:
-        raise ValueError("k: expected [tokens, heads, dim]")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k: expected [tokens, heads, dim]")
     return torch.Size((q.shape[0], k.shape[1], q.shape[2]))
 
 
@@ -198,8 +196,8 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
                        stream=None):
     """out [n_seq, q_heads, dim] of one query per sequence, q [n_seq, q_heads, dim], against caches
     [n_seq, capacity, kv_heads, dim] that hold lens [n_seq] events, the query's own among them."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: expected [sequences, capacity, heads, dim]")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("expected q [sequences, heads, dim], k_cache [sequences, capacity, heads, dim]")
     t, (n, cap, kv_heads, _) = q.dtype, k_cache.shape
     a = _attn(q, kv_heads, window, sinks, scale)
     cache = torch.Size((q.shape[0], cap, kv_heads, q.shape[2]))
@@ -272,8 +270,6 @@ def adamw_state_elems(weights) -> int:
 
 def _tensors(ts, name: str, dtype, sizes):
     """Host array of the device pointers of contiguous tensors of one type and these sizes."""
-    if len(ts) != len(sizes):
-        raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(ts)}")
     for t, n in zip(ts, sizes):
         if t.numel() != n or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
             raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} with the weights' "
@@ -284,7 +280,9 @@ def _tensors(ts, name: str, dtype, sizes):
 def _adamw_args(weights, grads, copies, weight_decay):
     sizes = [w.numel() for w in weights]
     k = len(sizes)
-    g_dtype = grads[0].dtype if k and len(grads) else torch.float32
+    if len(grads) != k or (copies is not None and len(copies) != k):
+        raise ValueError(f"expected {k} tensors in grads and copies")
+    g_dtype = grads[0].dtype if k else torch.float32
     c_dtype = copies[0].dtype if k and copies else torch.bfloat16
     if g_dtype not in _DTYPE or c_dtype not in _DTYPE:
         raise TypeError(f"unexpected tensor dtype {g_dtype}, {c_dtype}")

@@ -187,12 +187,19 @@ def hash_bits(seed: int, index):
     return mix((index + base) & 0xFFFFFFFF)
 
 
+def pow2(k):
+    """2^k for whole k, exact (a library's power need not be)."""
+    return ((k.long() + 1023) << 52).view(torch.float64)
+
+
+def values(codes, exp):
+    """What e4m3 codes with block exponents (plus 127) stand for."""
+    return (codes.view(torch.float8_e4m3fn).double().reshape(-1, BLOCK) * pow2(exp.int() - 127)[:, None]).reshape(-1)
+
+
 def e4m3_neighbours(x):
     """The e4m3-like codes below and above |x| (values), with four significant bits down to 2^-9."""
-    e = torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6)))
-    # log2 may round up to the next integer just below a power of two
-    e = torch.where(2.0 ** e > x.abs().clamp(min=2.0 ** -6), e - 1, e)
-    step = 2.0 ** (e - 3)
+    step = pow2(torch.frexp(x.abs().clamp(min=2.0 ** -6))[1] - 4)
     low = torch.floor(x.abs() / step) * step
     return low, low + step, step
 
@@ -206,10 +213,11 @@ def block_exponents(x):
 def to_codes(x, bits, keep):
     """Values of codes and block exponents of fp32 x with 16 random bits an element."""
     k = block_exponents(x)
-    y = torch.ldexp(x.double().reshape(-1, BLOCK), -k[:, None].double())
+    y = x.double().reshape(-1, BLOCK) * pow2(-k)[:, None]
     low, high, step = e4m3_neighbours(y)
     up = (bits.reshape(-1, BLOCK).double() + 0.5) / 65536
-    c = torch.floor(y.abs() / step + up) * step
+    # the place between two codes is exact in fp32, and the sum is one of fp32
+    c = torch.floor((y.abs() / step).float() + up.float()).double() * step
     if keep:
         c = torch.where((y != 0) & (c == 0), 2.0 ** -9, c)
-    return torch.ldexp(c * torch.sign(y), k[:, None].double()).reshape(-1), k
+    return (c * torch.sign(y) * pow2(k)[:, None]).reshape(-1), k

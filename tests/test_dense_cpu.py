@@ -1,0 +1,324 @@
+"""The dense side's C ABI on the CPU: it exports what its header declares and refuses bad arguments
+with the documented codes before any device work; the Python binding refuses bad tensors.  The
+oracle that the GPU tests compare with is itself checked against differences and closed forms."""
+import ctypes as C
+import math
+import os
+import re
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from ad_recommendation_amd import dense, emb  # noqa: E402
+from oracle import dense_oracle as O  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 0x10000  # stands for device memory: nothing here reaches it
+F16, BF16, F32 = emb.EMB_F16, dense.EMB_BF16, emb.EMB_F32
+
+
+def test_library_exports_every_declared_symbol():
+    src = open(os.path.join(ROOT, "include", "emb_dense.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    names = re.findall(r"^int\s+(\w+)\s*\(", src, flags=re.M)
+    assert set(names) == set(dense.exported_symbols()) and len(names) >= 10
+    for n in names:
+        assert hasattr(emb.lib(), n), n
+    assert int(re.search(r"#define EMB_ATTN_MAX_SINKS (\d+)", src).group(1)) == dense.ATTN_MAX_SINKS
+    assert int(re.search(r"#define EMB_ADAMW_BLOCK (\d+)", src).group(1)) == dense.ADAMW_BLOCK == O.BLOCK
+
+
+def refused(rc, code, text=""):
+    msg = emb.lib().emb_last_error().decode()
+    assert emb._STATUS[rc] == code and text in msg, (rc, msg)
+
+
+# ---------------------------------------------------------------------------------- attention
+def attn(dtype=F16, q_heads=4, kv_heads=2, dim=64, window=8, sinks=2, scale=1.0):
+    return dense.EmbAttn(dtype, q_heads, kv_heads, dim, window, sinks, scale)
+
+
+def heads(p=P, seq=64, tok=256, head=64):
+    return dense.EmbHeads(p, seq, tok, head)
+
+
+def fwd(a=None, n_seq=2, n_tok=10, off=P, lse=P, **t):
+    h = {k: C.byref(t.get(k, heads())) if t.get(k, 0) is not None else None for k in ("q", "k", "v", "out")}
+    return dense.lib().attn_window_fwd(C.byref(a or attn()), h["q"], h["k"], h["v"], off, n_seq, n_tok,
+                                       h["out"], lse, None)
+
+
+def bwd(a=None, n_seq=2, n_tok=10, ws=P, ws_bytes=1 << 20, lse=P, **t):
+    h = {k: C.byref(t.get(k, heads())) for k in ("q", "k", "v", "out", "dout", "dq", "dk", "dv")}
+    return dense.lib().attn_window_bwd(C.byref(a or attn()), h["q"], h["k"], h["v"], P, n_seq, n_tok,
+                                       h["out"], lse, h["dout"], h["dq"], h["dk"], h["dv"], ws, ws_bytes, None)
+
+
+def dec(a=None, n_seq=2, cap=100, lens=P, ws=P, ws_bytes=1 << 20, **t):
+    h = {k: C.byref(t.get(k, heads())) for k in ("q", "k", "v", "out")}
+    return dense.lib().attn_window_decode(C.byref(a or attn()), h["q"], h["k"], h["v"], lens, n_seq, cap,
+                                          h["out"], ws, ws_bytes, None)
+
+
+BAD_ATTN = [(dict(dtype=F32), "dtype"), (dict(dtype=3), "dtype"), (dict(q_heads=3), "multiple"),
+            (dict(kv_heads=0), "multiple"), (dict(q_heads=0), "multiple"), (dict(q_heads=-4), "multiple"),
+            (dict(dim=0), "dim"), (dict(dim=4), "dim"), (dict(dim=20), "dim"), (dict(dim=136), "dim"),
+            (dict(window=0), "window"), (dict(window=-1), "window"), (dict(sinks=-1), "sinks"),
+            (dict(sinks=33), "sinks"), (dict(scale=math.inf), "scale"), (dict(scale=math.nan), "scale")]
+
+
+@pytest.mark.parametrize("bad,text", BAD_ATTN)
+@pytest.mark.parametrize("call", [fwd, bwd, dec])
+def test_bad_descriptors_are_refused(call, bad, text):
+    refused(call(attn(**bad)), "EMB_EINVAL", text)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, dec])
+def test_bad_attention_arguments_are_refused(call):
+    for name in ("q", "k", "v", "out") + (("dout", "dq", "dk", "dv") if call is bwd else ()):
+        refused(call(**{name: heads(p=None)}), "EMB_EINVAL", "null")
+        refused(call(**{name: heads(p=P + 8)}), "EMB_EINVAL", "aligned")
+        refused(call(**{name: heads(tok=100)}), "EMB_EINVAL", "stride")
+        refused(call(**{name: heads(head=33)}), "EMB_EINVAL", "stride")
+    refused(call(n_seq=-1), "EMB_EINVAL", "negative")
+    refused(call(n_seq=2 ** 31), "EMB_ERANGE")
+    if call is dec:
+        refused(call(cap=-1), "EMB_EINVAL", "negative")
+        refused(call(cap=2 ** 31), "EMB_ERANGE")
+        refused(call(lens=None), "EMB_EINVAL", "lens")
+        refused(call(cap=4096, a=attn(window=4096), ws=None), "EMB_EINVAL", "workspace")
+        refused(call(cap=4096, a=attn(window=4096), ws_bytes=16), "EMB_ENOSPACE")
+        refused(call(n_seq=2 ** 30), "EMB_ERANGE")
+        assert call(n_seq=0) == 0
+    else:
+        refused(call(n_tok=-1), "EMB_EINVAL", "negative")
+        refused(call(n_tok=2 ** 31), "EMB_ERANGE")
+        refused(call(a=attn(q_heads=4096), n_tok=2 ** 30), "EMB_ERANGE")
+        refused(call(lse=P + 2), "EMB_EINVAL", "aligned")
+        assert call(n_seq=0, n_tok=0) == 0 and call(n_tok=0) == 0
+    if call is fwd:
+        refused(call(off=None), "EMB_EINVAL", "offsets")
+        refused(call(q=None), "EMB_EINVAL", "null")
+    if call is bwd:
+        refused(call(lse=None), "EMB_EINVAL", "null")
+        refused(call(ws=None), "EMB_EINVAL", "null")
+        refused(call(ws=P + 4), "EMB_EINVAL", "misaligned")
+        refused(call(ws_bytes=100), "EMB_ENOSPACE")
+
+
+def test_workspaces_cover_every_window():
+    L = dense.lib()
+    n = C.c_size_t()
+    for n_tok, n_seq in ((1, 1), (1000, 3), (1000, 1000), (5_000_000, 7), (1 << 24, 1 << 20)):
+        sizes = []
+        for w in (1, 2, 100, 4096, 2 ** 31 - 1):
+            assert L.attn_window_bwd_workspace_bytes(C.byref(attn(window=w)), n_seq, n_tok, C.byref(n)) == 0
+            sizes.append(n.value)
+        assert len(set(sizes)) == 1 and sizes[0] >= 4 * 4 * n_tok
+    refused(L.attn_window_bwd_workspace_bytes(C.byref(attn()), 1, 1, None), "EMB_EINVAL")
+    refused(L.attn_window_decode_workspace_bytes(C.byref(attn(dim=7)), 1, 1, C.byref(n)), "EMB_EINVAL")
+    # enough sequences fill the GPU without splitting their keys
+    assert dense.attn_window_decode_workspace_bytes(1024, 8192, 4, 2, 64, 4096, 4) == 0
+    assert dense.attn_window_decode_workspace_bytes(1, 8192, 4, 2, 64, 4096, 4) > 0
+
+
+# ---------------------------------------------------------------------------------- norms
+def norm_fwd(x=P, y=P, gate=None, kind=0, w_post=P, w_pre=P, rows=3, dim=16, dtype=F16, alpha=1.0, eps=1e-6,
+             r=P, h=P):
+    return dense.lib().norm_gate_residual_fwd(x, y, gate, kind, w_post, w_pre, rows, dim, dtype, alpha, eps, r,
+                                              h, None)
+
+
+def norm_bwd(r=P, y=P, gate=None, kind=0, w_post=P, w_pre=P, rows=3, dim=16, dtype=F16, alpha=1.0, eps=1e-6,
+             dr=P, dh=P, dx=P, dy=P, dgate=None, dw_post=P, dw_pre=P, ws=P, ws_bytes=1 << 20):
+    return dense.lib().norm_gate_residual_bwd(r, y, gate, kind, w_post, w_pre, rows, dim, dtype, alpha, eps, dr,
+                                              dh, dx, dy, dgate, dw_post, dw_pre, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [norm_fwd, norm_bwd])
+def test_bad_norm_arguments_are_refused(call):
+    refused(call(dtype=3), "EMB_EINVAL", "dtype")
+    for d in (0, -1, 8193):
+        refused(call(dim=d), "EMB_EINVAL", "dim")
+    refused(call(rows=-1), "EMB_EINVAL", "negative")
+    refused(call(rows=2 ** 41), "EMB_ERANGE")
+    refused(call(kind=3), "EMB_EINVAL", "gate")
+    refused(call(kind=1), "EMB_EINVAL", "gate")
+    refused(call(kind=2), "EMB_EINVAL", "gate")
+    refused(call(gate=P), "EMB_EINVAL", "gate")
+    refused(call(y=None), "EMB_EINVAL", "without y")
+    refused(call(eps=0.0), "EMB_EINVAL", "eps")
+    refused(call(eps=math.nan), "EMB_EINVAL", "eps")
+    refused(call(alpha=math.inf), "EMB_EINVAL", "alpha")
+    refused(call(y=P + 1), "EMB_EINVAL", "aligned")
+    refused(call(w_pre=P + 2), "EMB_EINVAL", "aligned")
+
+
+def test_parts_of_the_norm_go_together():
+    refused(norm_fwd(x=None), "EMB_EINVAL", "null")
+    refused(norm_fwd(h=None), "EMB_EINVAL", "w_pre")
+    refused(norm_fwd(w_pre=None), "EMB_EINVAL", "w_pre")
+    refused(norm_fwd(w_pre=None, h=None, r=None), "EMB_EINVAL", "neither")
+    assert norm_fwd(rows=0, x=None, r=None, h=None) == 0
+    refused(norm_bwd(dh=None), "EMB_EINVAL", "w_pre")
+    refused(norm_bwd(w_pre=None, dw_pre=None), "EMB_EINVAL", "w_pre")
+    refused(norm_bwd(w_pre=None, dh=None, dr=None, dw_pre=None), "EMB_EINVAL", "neither")
+    refused(norm_bwd(r=None), "EMB_EINVAL", "null")
+    refused(norm_bwd(y=None, w_post=None, dw_post=None), "EMB_EINVAL", "dy")
+    refused(norm_bwd(dgate=P), "EMB_EINVAL", "gate")
+    refused(norm_bwd(w_post=None), "EMB_EINVAL", "dw_post")
+    refused(norm_bwd(w_pre=None, dh=None), "EMB_EINVAL", "dw_pre")
+    refused(norm_bwd(ws=None), "EMB_EINVAL", "workspace")
+    refused(norm_bwd(ws_bytes=64), "EMB_ENOSPACE")
+    n = C.c_size_t()
+    refused(dense.lib().norm_gate_residual_bwd_workspace_bytes(1, 0, C.byref(n)), "EMB_EINVAL")
+    refused(dense.lib().norm_gate_residual_bwd_workspace_bytes(1, 8, None), "EMB_EINVAL")
+    assert dense.norm_gate_residual_bwd_workspace_bytes(0, 64) == 0
+
+
+# ---------------------------------------------------------------------------------- AdamW
+def adam(q8, n=(10, 20), w=(P, P), g=(P, P), grad_dtype=F32, copies=None, copy_dtype=F16, states=P, elems=256,
+         step=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=(0.0, 0.0), scale=None, count=None):
+    arr = lambda x: None if x is None else (C.c_void_p * len(x))(*x)  # noqa: E731
+    args = [len(n) if count is None else count, (C.c_int64 * len(n))(*n), arr(w), arr(g), grad_dtype, arr(copies),
+            copy_dtype]
+    tail = [elems, step, lr, b1, b2, eps, None if wd is None else (C.c_float * len(wd))(*wd), scale]
+    if q8:
+        return dense.lib().adamw_step_q8(*args, states, P, P, P, *tail, 1, None)
+    return dense.lib().adamw_step(*args, states, P, *tail, None)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_bad_adamw_arguments_are_refused(q8):
+    bad = [dict(count=-1), dict(w=None), dict(g=None), dict(wd=None), dict(grad_dtype=3), dict(step=0),
+           dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=math.nan), dict(eps=0.0), dict(eps=math.inf),
+           dict(lr=math.nan), dict(n=(-1, 20)), dict(wd=(math.nan, 0.0)), dict(w=(P, None)), dict(g=(None, P)),
+           dict(w=(P + 2, P)), dict(g=(P + 2, P)), dict(copies=(P, None)), dict(copies=(P, P + 1)),
+           dict(copies=(P, P), copy_dtype=F32), dict(states=None), dict(states=P + 4), dict(elems=128),
+           dict(elems=384), dict(scale=P + 1)]
+    for b in bad:
+        refused(adam(q8, **b), "EMB_EINVAL", "adamw")
+    refused(adam(q8, n=(2 ** 32, 1)), "EMB_ERANGE")
+    assert adam(q8, n=(0, 0), elems=0, states=None, w=(None, None), g=(None, None)) == 0
+    assert adam(q8, n=(), w=(), g=(), wd=(), elems=0) == 0
+
+
+def test_state_sizes_and_values():
+    n = C.c_int64()
+    assert dense.lib().adamw_state_elems((C.c_int64 * 4)(0, 1, 128, 129), 4, C.byref(n)) == 0 and n.value == 512
+    refused(dense.lib().adamw_state_elems(None, 1, C.byref(n)), "EMB_EINVAL")
+    refused(dense.lib().adamw_state_elems((C.c_int64 * 1)(-1), 1, C.byref(n)), "EMB_EINVAL")
+    L = dense.lib().adamw_q8_values
+    refused(L(P, P, 100, P, F32, None), "EMB_EINVAL", "multiple")
+    refused(L(P, P, -128, P, F32, None), "EMB_EINVAL")
+    refused(L(P, P, 128, P, F16, None), "EMB_EINVAL", "EMB_BF16")
+    refused(L(None, P, 128, P, F32, None), "EMB_EINVAL", "null")
+    refused(L(P + 8, P, 128, P, F32, None), "EMB_EINVAL", "aligned")
+    assert L(None, None, 0, None, F32, None) == 0
+
+
+# ---------------------------------------------------------------------------------- the binding
+def test_binding_refuses_bad_tensors():
+    x = torch.zeros(4, 2, 8, dtype=torch.float16)
+    off = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="CUDA"):
+        dense.attn_window_fwd(x, x, x, off, 1, 0, 1.0, x)
+    with pytest.raises(TypeError, match="float16 or bfloat16"):
+        dense.attn_window_fwd(x.float(), x, x, off, 1, 0, 1.0, x)
+    with pytest.raises(ValueError, match="tokens, heads, dim"):
+        dense.attn_window_fwd(x[0], x, x, off, 1, 0, 1.0, x)
+    with pytest.raises(ValueError, match="capacity"):
+        dense.attn_window_decode(x, x, x, off, 1, 0, 1.0, x, None)
+    with pytest.raises(ValueError, match="rows"):
+        dense.norm_gate_residual_fwd(x, None, None, None, None, 1.0, 1e-6, x, None)
+    with pytest.raises(TypeError, match="CUDA"):
+        dense.norm_gate_residual_fwd(x[0], None, None, None, None, 1.0, 1e-6, x[0], None)
+    w = [torch.zeros(3)]
+    with pytest.raises(ValueError, match="tensors"):
+        dense.adamw_step(w, [], w[0], w[0], 1, 1e-3, 0.9, 0.99, 1e-8, 0.0)
+    with pytest.raises(TypeError, match="CUDA"):
+        dense.adamw_step(w, w, w[0], w[0], 1, 1e-3, 0.9, 0.99, 1e-8, 0.0)
+    with pytest.raises(ValueError, match="weight_decay"):
+        dense.adamw_step(w, w, w[0], w[0], 1, 1e-3, 0.9, 0.99, 1e-8, [0.0, 0.0])
+    assert dense.adamw_state_elems([torch.zeros(5), torch.zeros(200)]) == 384
+
+
+# ---------------------------------------------------------------------------------- the oracle
+def test_attention_oracle_against_differences():
+    g = torch.Generator().manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    off, w, s, scale = torch.tensor([0, 5, 5, 12]), 3, 2, 0.4
+    x = dict(q=rand(12, 4, 8), k=rand(12, 2, 8), v=rand(12, 2, 8))
+    dout = rand(12, 4, 8)
+    f = lambda: (O.attn_fwd(x["q"], x["k"], x["v"], off, w, s, scale)[0] * dout).sum().item()  # noqa: E731
+    out, lse = O.attn_fwd(x["q"], x["k"], x["v"], off, w, s, scale)[:2]
+    grads = O.attn_bwd(x["q"], x["k"], x["v"], off, w, s, scale, out, lse, dout)[:3]
+    for name, grad in zip(("q", "k", "v"), grads):
+        d = rand(*x[name].shape)
+        keep, h = x[name], 1e-5
+        x[name] = keep + h * d
+        up = f()
+        x[name] = keep - h * d
+        down = f()
+        x[name] = keep
+        # an error of h^2 of the third derivative and 1e-16 / h of rounding
+        assert abs((up - down) / (2 * h) - (grad * d).sum().item()) < 1e-7
+    # the definition, pair by pair
+    i, h = 11, 3
+    seen = [j for j in range(7) if j <= 6 and (6 - j < w or j < s)]
+    sc = torch.tensor([scale * (x["q"][i, h] @ x["k"][5 + j, 1]).item() for j in seen], dtype=torch.float64)
+    want = sum(p * x["v"][5 + j, 1] for p, j in zip(torch.softmax(sc, 0), seen))
+    assert torch.allclose(out[i, h], want) and seen == [0, 1, 4, 5, 6]
+
+
+def test_decode_oracle_is_the_forward_of_the_newest():
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn(9, h, 8, generator=g, dtype=torch.float32).half() for h in (4, 2, 2))
+    out = O.attn_fwd(q, k, v, torch.tensor([0, 9]), 4, 1, 0.3)[0]
+    got = O.attn_decode(q[8:], k[None], v[None], torch.tensor([9]), 4, 1, 0.3)[0]
+    assert torch.allclose(got[0], out[8], atol=1e-12)
+
+
+@pytest.mark.parametrize("gate", ["none", "vec", "row"])
+def test_norm_oracle_against_differences(gate):
+    g = torch.Generator().manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    t = dict(x=rand(4, 6), y=rand(4, 6), gate={"none": None, "vec": rand(6), "row": rand(4, 6)}[gate],
+             w_post=rand(6), w_pre=rand(6))
+    alpha, eps, cr, ch = 0.7, 1e-3, rand(4, 6), rand(4, 6)
+
+    def f():
+        r, h = O.norm_fwd(t["x"], t["y"], t["gate"], t["w_post"], t["w_pre"], alpha, eps)
+        return ((r * cr).sum() + (h * ch).sum()).item()
+    r = O.norm_fwd(t["x"], t["y"], t["gate"], t["w_post"], t["w_pre"], alpha, eps)[0]
+    got = dict(zip(("x", "y", "gate", "w_post", "w_pre"),
+                   O.norm_bwd(r, t["y"], t["gate"], t["w_post"], t["w_pre"], alpha, eps, cr, ch)))
+    for name, grad in got.items():
+        if t[name] is None:
+            continue
+        d, keep, h = rand(*t[name].shape), t[name], 1e-5
+        t[name] = keep + h * d
+        up = f()
+        t[name] = keep - h * d
+        down = f()
+        t[name] = keep
+        assert abs((up - down) / (2 * h) - (grad * d).sum().item()) < 1e-6, name
+
+
+def test_adamw_oracle_first_step_and_codes():
+    w, m, v = O.adamw(torch.tensor([1.0]).double(), torch.tensor([0.5]).double(), 0.0, 0.0, 1, 0.1, 0.9, 0.99, 0.0, 0.2)
+    assert abs(w.item() - (1.0 - 0.1 * (1.0 + 0.2))) < 1e-12 and abs(m.item() - 0.05) < 1e-12
+    # every e4m3 value keeps itself, whatever the bits; a value between two becomes one of them
+    codes = torch.arange(0, 0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    x = torch.cat([codes[codes < 256], torch.zeros(128)])[:128]
+    x[127] = 240.0  # the block's largest lies in [128, 256)
+    for bits in (0, 0x7FFF, 0xFFFF):
+        got, k = O.to_codes(x, torch.full((128,), bits), False)
+        assert k.item() == 0 and torch.equal(got.float(), x)
+    low, high, _ = O.e4m3_neighbours(torch.tensor([17.0, 0.5, 0.001, 255.0]).double())
+    assert low.tolist() == [16.0, 0.5, 0.0, 240.0] and high.tolist() == [18.0, 0.5625, 2.0 ** -9, 256.0]
+    bits = O.hash_bits(5, torch.arange(1 << 16))
+    for part in (bits & 0xFFFF, bits >> 16):  # a mean of 65536 even draws: 1/2 within 4 deviations
+        assert abs((part.double() / 65536).mean().item() - 0.5) < 4 * 0.29 / 256
+    assert not torch.equal(bits, O.hash_bits(6, torch.arange(1 << 16)))

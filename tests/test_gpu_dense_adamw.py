@@ -1,0 +1,247 @@
+"""AdamW over many tensors against the formula in 64 bits, and its 8-bit states bit by bit against
+the oracle's codes: every type, sizes around blocks and chunks, tensors aligned to their elements
+alone, more tensors than one launch takes."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from ad_recommendation_amd import dense  # noqa: E402
+from oracle import dense_oracle as O  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+E = 2.0 ** -24
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+SIZES = [1, 7, 8, 127, 128, 129, 0, 2047, 2048, 2049, 20000, 3, 70001]
+
+
+def tensors(sizes, dtype, seed, by=1.0, offset=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [(by * torch.randn(n + offset, generator=g, device="cuda")).to(dtype)[offset:] for n in sizes]
+
+
+def starts(sizes):
+    at, out = 0, []
+    for n in sizes:
+        out.append(at)
+        at += -(-n // O.BLOCK) * O.BLOCK
+    return out, at
+
+
+def args(step=5, **kw):
+    h = {**HYPER, **kw}
+    return step, h["lr"], h["beta1"], h["beta2"], h["eps"]
+
+
+def close(got, want, bound, what):
+    err = (got.double() - want).abs()
+    worst = (err - bound).max().item() if err.numel() else -1.0
+    assert worst <= 0, f"{what}: {worst:.3g} over its bound"
+
+
+def check_weights(w, w0, g, m, v, step, wd, c, copy=None):
+    """Weights from the new m and v as they are (the kernel's own): an error of the update of 16
+    roundings, one of the weight."""
+    mh, vh = m.double() / (1 - c["beta1"] ** step), v.double() / (1 - c["beta2"] ** step)
+    up = c["lr"] * (mh / (vh.sqrt() + c["eps"]) + wd * w0.double())
+    size = c["lr"] * (mh.abs() / (vh.sqrt() + c["eps"]) + abs(wd) * w0.double().abs())
+    want = w0.double() - up
+    close(w, want, E * want.abs() + 16 * E * size, "weights")
+    if copy is not None:
+        assert torch.equal(copy, w.to(copy.dtype))
+
+
+@pytest.mark.parametrize("copy", [None, F16, BF16], ids=str)
+@pytest.mark.parametrize("grad", [F32, F16, BF16], ids=str)
+def test_fp32_states(grad, copy):
+    at, total = starts(SIZES)
+    w, g = tensors(SIZES, F32, 1), tensors(SIZES, grad, 2, 0.1)
+    assert dense.adamw_state_elems(w) == total
+    m, v = torch.randn(total, device="cuda") * 0.1, torch.rand(total, device="cuda")
+    copies = None if copy is None else [torch.full_like(x, 7, dtype=copy) for x in w]
+    wd = [0.01 * (i % 3) for i in range(len(SIZES))]
+    w0, m0, v0 = [x.clone() for x in w], m.clone(), v.clone()
+    scale = torch.tensor(0.5, device="cuda")
+    dense.adamw_step(w, g, m, v, *args(), wd, copies=copies, grad_scale=scale)
+    for i, n in enumerate(SIZES):
+        a, z = at[i], at[i] + n
+        gg = g[i].double() * 0.5
+        m1, v1 = 0.9 * m0[a:z].double() + 0.1 * gg, 0.99 * v0[a:z].double() + 0.01 * gg * gg
+        close(m[a:z], m1, 3 * E * (0.9 * m0[a:z].double().abs() + 0.1 * gg.abs()), "m")
+        close(v[a:z], v1, 4 * E * v1, "v")
+        check_weights(w[i], w0[i], gg, m[a:z], v[a:z], 5, wd[i], HYPER, copies and copies[i])
+        pad = m[z:at[i + 1] if i + 1 < len(SIZES) else total]
+        assert (pad == 0).all()
+
+
+def test_many_steps_follow_the_formula():
+    """A hundred steps in fp32 against 64 bits: errors of m and v shrink by their betas each step."""
+    w, m, v = tensors([500], F32, 3), torch.zeros(512, device="cuda"), torch.zeros(512, device="cuda")
+    ww, mm, vv = w[0].double(), torch.zeros(500, dtype=torch.float64, device="cuda"), torch.zeros(500, dtype=torch.float64, device="cuda")
+    for t in range(1, 101):
+        g = tensors([500], F32, 100 + t)
+        dense.adamw_step(w, g, m, v, *args(t), 0.01)
+        ww, mm, vv = O.adamw(ww, g[0].double(), mm, vv, t, HYPER["lr"], 0.9, 0.99, 1e-8, 0.01)
+    close(m[:500], mm, 10 * 4 * E * torch.full_like(mm, 4.0), "m")
+    close(v[:500], vv, 100 * 4 * E * vv, "v")
+    # each step's update of about lr is off by a relative 16 E and what m and v carry: 400 E of them
+    close(w[0], ww, 100 * (E * ww.abs().clamp(min=1.0) + HYPER["lr"] * 500 * E), "weights")
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("q8", [False, True])
+def test_tensors_aligned_to_their_elements_alone(q8, offset):
+    sizes = [5, 300, 4099]
+    w, g = tensors(sizes, F32, 4, offset=offset), tensors(sizes, BF16, 5, offset=offset)
+    aw, ag = [x.clone() for x in w], [x.clone() for x in g]
+    copies = [torch.zeros(n + offset, dtype=F16, device="cuda")[offset:] for n in sizes]
+    total = dense.adamw_state_elems(w)
+
+    def run(w, g, copies):
+        if q8:
+            s = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (total, total // 128) * 2]
+            dense.adamw_step_q8(w, g, *s, *args(1), 0.1, seed=9, copies=copies)
+        else:
+            s = [torch.zeros(total, device="cuda") for _ in range(2)]
+            dense.adamw_step(w, g, *s, *args(1), 0.1, copies=copies)
+        return list(w) + s
+    a, b = run(w, g, copies), run(aw, ag, None)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert all(torch.equal(c, x.half()) for c, x in zip(copies, w))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_more_tensors_than_one_launch_takes(q8):
+    sizes = [(i * 37) % 300 for i in range(250)]
+    w, g = tensors(sizes, F32, 6), tensors(sizes, F32, 7)
+    at, total = starts(sizes)
+    w0 = [x.clone() for x in w]
+    if q8:
+        s = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (total, total // 128) * 2]
+        dense.adamw_step_q8(w, g, *s, *args(1), 0.0, seed=1)
+    else:
+        s = [torch.zeros(total, device="cuda") for _ in range(2)]
+        dense.adamw_step(w, g, *s, *args(1), 0.0)
+    for x, y, gg in zip(w, w0, g):  # the first step is lr against the gradient's sign
+        close(x, y.double() - HYPER["lr"] * gg.double() / (gg.double().abs() + 1e-8),
+              E * y.double().abs() + 1e-3 * 32 * E, "weights")
+
+
+# ---------------------------------------------------------------------------------- 8 bits
+def q8_state(x):
+    """Codes and exponents nearest to x, by the oracle."""
+    val, k = O.to_codes(x, torch.full(x.shape, 0x7FFF, device=x.device), False)
+    codes = (val.reshape(-1, O.BLOCK) * O.pow2(-k)[:, None]).reshape(-1).float()
+    return codes.to(torch.float8_e4m3fn), (k + 127).to(torch.uint8)
+
+
+@pytest.mark.parametrize("grad", [F32, BF16], ids=str)
+@pytest.mark.parametrize("seed", [0, 12345, (7 << 32) + 3, 2 ** 64 - 1])
+def test_codes_bit_by_bit(seed, grad):
+    at, total = starts(SIZES)
+    w, g = tensors(SIZES, F32, 8), tensors(SIZES, grad, 9, 0.1)
+    inside = torch.zeros(total, device="cuda")
+    for a, n in zip(at, SIZES):
+        inside[a:a + n] = 1
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    spread = torch.exp(3 * torch.randn(total, generator=gen, device="cuda"))  # values far apart in a block
+    m, me = q8_state(torch.randn(total, generator=gen, device="cuda") * spread * inside * 0.01)
+    v, ve = q8_state(spread * inside * 0.1)
+    old = [O.values(c, e).float() for c, e in ((m, me), (v, ve))]
+    w0 = [x.clone() for x in w]
+    dense.adamw_step_q8(w, g, m, me, v, ve, *args(5), 0.01, seed=seed)
+    flat = torch.zeros(total, device="cuda")
+    for a, n, x in zip(at, SIZES, g):
+        flat[a:a + n] = x.float()
+    # the formula's products and sums one by one in fp32
+    m1 = old[0] * 0.9 + flat * (1 - 0.9)
+    v1 = old[1] * old[1] * 0.99 + flat * flat * (1 - 0.99)
+    root = v1.cpu().sqrt().cuda()
+    bits = O.hash_bits(seed, torch.arange(total, device="cuda"))
+    for codes, exp, x, b, keep in ((m, me, m1, bits & 0xFFFF, False), (v, ve, root, bits >> 16, True)):
+        want, k = O.to_codes(x, b, keep)
+        assert torch.equal(exp.int() - 127, k.int())
+        got = torch.empty(total, device="cuda")
+        dense.adamw_q8_values(codes, exp, got)
+        assert torch.equal(got.double(), want)
+        half = torch.empty(total, dtype=BF16, device="cuda")
+        dense.adamw_q8_values(codes, exp, half)
+        assert torch.equal(half.float(), got)
+    for i, n in enumerate(SIZES):
+        a = at[i]
+        check_weights(w[i], w0[i], None, m1[a:a + n], v1[a:a + n], 5, 0.01, HYPER)
+
+
+def test_the_means_move_as_the_formula_says():
+    """Without gradients the root of v shrinks by sqrt(beta2) a step, though each step is far less
+    than a code; m's mean follows a constant gradient."""
+    n, steps, b2 = 1 << 16, 300, 0.999
+    w, g = [torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")]
+    m, me = q8_state(torch.zeros(n, device="cuda"))
+    v, ve = q8_state(torch.ones(n, device="cuda"))
+    for t in range(steps):
+        dense.adamw_step_q8(w, g, m, me, v, ve, *args(t + 1, beta2=b2), 0.0, seed=t)
+    x = torch.empty(n, device="cuda")
+    dense.adamw_q8_values(v, ve, x)
+    want = b2 ** (steps / 2)
+    # a step changes a root by one code (at most 1/8 of it) or not: 300 steps of 65536 roots leave
+    # their mean within 1/8 sqrt(300 / 65536) < 0.9 % at one deviation of the worst case
+    assert abs(x.mean().item() / want - 1) < 0.03
+    assert x.unique().numel() > 1
+    g[0].fill_(0.37)
+    for t in range(100):
+        dense.adamw_step_q8(w, g, m, me, v, ve, *args(t + 1, beta2=b2), 0.0, seed=1000 + t)
+    dense.adamw_q8_values(m, me, x)
+    assert abs(x.mean().item() / 0.37 - 1) < 0.01
+
+
+def test_what_is_not_finite_is_held_as_nan_beside_sound_values():
+    n = 256
+    w, g = [torch.zeros(n, device="cuda")], [torch.ones(n, device="cuda")]
+    g[0][3], g[0][200] = float("inf"), float("nan")
+    s = [torch.zeros(k, dtype=torch.uint8, device="cuda") for k in (n, n // 128) * 2]
+    dense.adamw_step_q8(w, g, *s, *args(1), 0.0, seed=4)
+    for c, e, near in ((s[0], s[1], 0.1), (s[2], s[3], 0.1)):
+        x = torch.empty(n, device="cuda")
+        dense.adamw_q8_values(c, e, x)
+        bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+        bad[[3, 200]] = True
+        assert x[bad].isnan().all()
+        assert ((x[~bad] - near).abs() <= near / 8).all()
+
+
+def test_small_roots_beside_large_ones_do_not_vanish():
+    n = 128
+    w, g = [torch.zeros(n, device="cuda")], [torch.full((n,), 1e-9, device="cuda")]
+    g[0][0] = 1e6
+    s = [torch.zeros(k, dtype=torch.uint8, device="cuda") for k in (n, 1) * 2]
+    dense.adamw_step_q8(w, g, *s, *args(1), 0.0, seed=4)
+    assert (s[2] != 0).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_in_a_graph(q8):
+    sizes = [1000, 77]
+    w, g = tensors(sizes, F32, 11), tensors(sizes, F16, 12)
+    total = dense.adamw_state_elems(w)
+    s = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (total, total // 128) * 2] if q8 else \
+        [torch.zeros(total, device="cuda") for _ in range(2)]
+
+    def step(w, s):
+        if q8:
+            dense.adamw_step_q8(w, g, *s, *args(3), 0.1, seed=2)
+        else:
+            dense.adamw_step(w, g, *s, *args(3), 0.1)
+    step(w, s)
+    torch.cuda.synchronize()
+    w2, s2 = [x.clone() for x in w], [x.clone() for x in s]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(w, s)
+    for turn in range(3):
+        for x, y in zip(g, tensors(sizes, F16, 20 + turn)):
+            x.copy_(y)
+        graph.replay()
+        step(w2, s2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(w + s, w2 + s2))
