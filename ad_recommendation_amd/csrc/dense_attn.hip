@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
 // ---------------------------------------------------------------- backward: dq
 // As the forward, with dout as a second right operand; also writes delta.
 template <typename T, int DH, int WAVES>
-__global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a) {
+__global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) attn_dq(AttnArgs a) {
   typedef typename Vec8<T>::t V8;
   typedef Group<WAVES> G;
   constexpr int kSubs = G::kRows / 32;
@@ -532,8 +532,13 @@ struct SinkSlots {
     numbers = by_sequence ? n_seq : n_tok / (reach + 1) + 1;
     chunk_slots = n_tok / chunk + numbers + 1;
   }
-  __host__ __device__ int64_t number(int64_t begin, int b) const { return by_sequence ? b : begin / (reach + 1); }
-  __host__ __device__ int64_t first(int64_t begin, int b) const { return begin / chunk + number(begin, b); }
+  // in 32 bits: tokens are fewer than 2^31, and reach + 1 at most 2^31 + 127
+  __host__ __device__ int64_t number(int64_t begin, int b) const {
+    return by_sequence ? b : (uint32_t)begin / (uint32_t)(reach + 1);
+  }
+  __host__ __device__ int64_t first(int64_t begin, int b) const {
+    return (uint32_t)begin / (uint32_t)chunk + number(begin, b);
+  }
 };
 __device__ __forceinline__ float* sink_part(const AttnArgs& a, int64_t slot, int kh) {
   return a.part + (slot * a.kv_heads + kh) * 2 * a.sinks * (int64_t)a.dim;
@@ -768,26 +773,31 @@ __global__ void __launch_bounds__((DkvShape<DH, WAVES>::kBlock), 2)
   }
 }
 
-// dk and dv of the sinks from the first key tile's sums and every chunk's, in that order: one element a
-// thread, a number (see SinkSlots) a workgroup.
+// dk and dv of the sinks from the first key tile's sums and every chunk's, in that order: up to four
+// elements a thread, a number (see SinkSlots) a row of workgroups.
+constexpr int kJoinEach = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int tokens, int chunk) {
-  const int kh = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
   const SinkSlots parts(a.n_tok, a.n_seq, a.window, tokens, chunk);
-  const Seq s = find_tile(a, slot, [&](int64_t t, int b) { return parts.number(t, b); });
+  const Seq s = find_tile(a, blockIdx.x, [&](int64_t t, int b) { return parts.number(t, b); });
   if (s.tile != 0 || s.len <= parts.reach) return;
-  const int e = blockIdx.y * kThreads + threadIdx.x;
-  const int64_t each = 2 * a.sinks * (int64_t)a.dim, step = each * a.kv_heads;
-  if (e >= each) return;
-  const int64_t n = (s.len - parts.reach + chunk - 1) / chunk;
-  const float* part = sink_part(a, parts.first(s.begin, s.index), kh) + e;
-  float t = first_tile_part(a, parts, s, kh)[e];
-#pragma unroll 8
-  for (int64_t x = 0; x < n; ++x) t += part[x * step];
-  const int row = e / a.dim % a.sinks, col = e % a.dim;
-  const bool is_v = e >= a.sinks * a.dim;
-  const EmbHeads& to = is_v ? a.dv : a.dk;
-  static_cast<T*>(to.p)[(s.begin + row) * to.tok + kh * to.head + col] = (T)(is_v ? t : t * a.scale);
+  const int n = (int)((s.len - parts.reach + chunk - 1) / chunk);
+  const int each = 2 * a.sinks * a.dim, all = each * a.kv_heads;
+  const float* tile = first_tile_part(a, parts, s, 0);
+  const float* part = sink_part(a, parts.first(s.begin, s.index), 0);
+#pragma unroll
+  for (int k = 0; k < kJoinEach; ++k) {
+    const int at = (blockIdx.y * kJoinEach + k) * kThreads + threadIdx.x;
+    if (at >= all) return;
+    float t = tile[at];
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) t += part[(int64_t)x * all + at];
+    const int kh = at / each, e = at % each;
+    const int row = e / a.dim % a.sinks, col = e % a.dim;
+    const bool is_v = e >= a.sinks * a.dim;
+    const EmbHeads& to = is_v ? a.dv : a.dk;
+    static_cast<T*>(to.p)[(s.begin + row) * to.tok + kh * to.head + col] = (T)(is_v ? t : t * a.scale);
+  }
 }
 
 // ---------------------------------------------------------------- one new event
@@ -1071,8 +1081,9 @@ void go_bwd(const AttnArgs& a, hipStream_t st) {
                      dim3(DkvShape<DH, WAVES>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
   if (sinks)
     hipLaunchKernelGGL((attn_sink_join<T>),
-                       dim3((unsigned)(n.numbers * a.kv_heads),
-                            (unsigned)((2 * a.sinks * a.dim + kThreads - 1) / kThreads)),
+                       dim3((unsigned)n.numbers,
+                            (unsigned)((2 * a.sinks * a.dim * a.kv_heads + kThreads * kJoinEach - 1) /
+                                       (kThreads * kJoinEach))),
                        dim3(kThreads), 0, st, a, G::kTokens, chunk);
 }
 

@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
       yr[c] = xr[c];
       gr[c] = xr[c];
       if (live && n[c] > 0) {
-        xr[c] = load8(x + at + col, n[c]);
-        if (y) yr[c] = load8(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8(gate + at + col, n[c]);
+        xr[c] = load8<T, true>(x + at + col, n[c]);
+        if (y) yr[c] = load8<T, true>(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, true>(gate + at + col, n[c]);
       }
     }
     float inv_y = 1.f;
@@ -192,12 +192,12 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       dhr[c] = rr[c];
       if (live && n[c] > 0) {
         if (pre) {
-          rr[c] = load8(r + at + col, n[c]);
-          dhr[c] = load8(dh + at + col, n[c]);
+          rr[c] = load8<T, true>(r + at + col, n[c]);
+          dhr[c] = load8<T, true>(dh + at + col, n[c]);
         }
-        if (dr) drr[c] = load8(dr + at + col, n[c]);
-        if (y) yr[c] = load8(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8(gate + at + col, n[c]);
+        if (dr) drr[c] = load8<T, true>(dr + at + col, n[c]);
+        if (y) yr[c] = load8<T, true>(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, true>(gate + at + col, n[c]);
       }
     }
     // r^2, u r, y^2, a dr, a u, a r
