@@ -2,9 +2,9 @@
 //
 //   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
 //   w = w - lr (m / c1 / (sqrt(v) / sqrt(c2) + eps) + wd w)
-// Bound by HBM: everything is read and written once a step, and by nontemporal accesses, since the
-// next to read it comes a step later (an fp32 step over 96 tensors of 21M elements: 123 -> 114 us,
-// 5.1 TB/s; a plain device copy reaches 4.7).
+// Bound by HBM: everything is read and written once a step, past the caches where it is more than they
+// hold (an fp32 step over 96 tensors of 21M elements: 123 -> 114 us, 5.1 TB/s; a plain device copy
+// reaches 4.7).
 //
 // In 8 bits the states are m and s = sqrt(v), each an e4m3 code times a power of two shared by a block
 // of 128: the root halves the exponent range that v needs.  A code is within 1/16 of its value, while
@@ -97,7 +97,7 @@ __device__ __forceinline__ float update(const AdamArgs& a, float g, float wd, bo
 
 // One workgroup takes one chunk of one tensor.  The state arrays hold whole blocks of 128, so only w, g
 // and the copy have a ragged end.
-template <typename G, typename C, bool COPY, bool Q8>
+template <typename G, typename C, bool COPY, bool Q8, bool ONCE>
 __global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
   uint32_t lo = 0, hi = a.n_tensors;  // the last tensor whose first chunk is not past this one
   while (hi - lo > 1) {
@@ -127,10 +127,10 @@ __global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
         const int64_t e = e0 + k * (kStep / 2) + threadIdx.x * 4;
         left[k] = (int)min(max(n - e, (int64_t)0), (int64_t)4);
         if (left[k] > 0) {
-          wv[k] = load4(w + e, left[k]);
-          gv[k] = load4(g + e, left[k]);
-          m[k] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.m + s0 + e));
-          v[k] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.v + s0 + e));
+          wv[k] = load4<float, ONCE>(w + e, left[k]);
+          gv[k] = load4<G, ONCE>(g + e, left[k]);
+          m[k] = load4<float, ONCE>(a.m + s0 + e, 4);
+          v[k] = load4<float, ONCE>(a.v + s0 + e, 4);
         }
       }
 #pragma unroll
@@ -145,12 +145,12 @@ __global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
           wv[k][i] = wi;
         }
         if (left[k] > 0) {
-          store4(w + e, wv[k], left[k]);
-          if (COPY) store4(copy + e, wv[k], left[k]);
+          store4<float, ONCE>(w + e, wv[k], left[k]);
+          if (COPY) store4<C, ONCE>(copy + e, wv[k], left[k]);
         }
         if (e < n_pad) {
-          __builtin_nontemporal_store(m[k], reinterpret_cast<f32x4*>(a.m + s0 + e));
-          __builtin_nontemporal_store(v[k], reinterpret_cast<f32x4*>(a.v + s0 + e));
+          store4<float, ONCE>(a.m + s0 + e, m[k], 4);
+          store4<float, ONCE>(a.v + s0 + e, v[k], 4);
         }
       }
     }
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
       const int left = (int)min(max(n - e, (int64_t)0), (int64_t)8);
       f32x8 wv = {}, gv = {}, m = {}, v = {}, root;
       if (left > 0) {
-        wv = load8<float, true>(w + e, left);
-        gv = widen(load8<G, true>(g + e, left));
+        wv = load8<float, ONCE>(w + e, left);
+        gv = widen(load8<G, ONCE>(g + e, left));
       }
       if (in) {
         m = decode8(*reinterpret_cast<const uint2*>(a.m8 + s), a.m_exp[s / EMB_ADAMW_BLOCK]);
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
         wv[i] = wi;
       }
       if (left > 0) {
-        store8<float, true>(w + e, wv, left);
-        if (COPY) store8<C, true>(copy + e, wv, left);
+        store8<float, ONCE>(w + e, wv, left);
+        if (COPY) store8<C, ONCE>(copy + e, wv, left);
       }
       const uint32_t base = mix32(seed ^ (uint32_t)((uint64_t)s >> 32) * 0x9E3779B1u);
       f32x8 up_m, up_v;
@@ -212,25 +212,32 @@ __global__ void __launch_bounds__(kThreads) adamw_values(const uint8_t* codes, c
     store8<T, true>(out + e, decode8(*reinterpret_cast<const uint2*>(codes + e), exp[e / EMB_ADAMW_BLOCK]), 8);
 }
 
+template <typename G, typename C, bool COPY, bool Q8>
+void go(const AdamArgs& a, uint32_t chunks, hipStream_t st) {
+  if (a.once) hipLaunchKernelGGL((adamw<G, C, COPY, Q8, true>), dim3(chunks), dim3(kThreads), 0, st, a);
+  else hipLaunchKernelGGL((adamw<G, C, COPY, Q8, false>), dim3(chunks), dim3(kThreads), 0, st, a);
+}
+
 template <typename G, bool Q8>
-void go(const AdamArgs& a, uint32_t chunks, int copy_dtype, hipStream_t st) {
-  const dim3 grid(chunks), block(kThreads);
-  if (copy_dtype == EMB_F16) hipLaunchKernelGGL((adamw<G, _Float16, true, Q8>), grid, block, 0, st, a);
-  else if (copy_dtype == EMB_BF16) hipLaunchKernelGGL((adamw<G, __bf16, true, Q8>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((adamw<G, _Float16, false, Q8>), grid, block, 0, st, a);
+void go_copy(const AdamArgs& a, uint32_t chunks, int copy_dtype, hipStream_t st) {
+  if (copy_dtype == EMB_F16) go<G, _Float16, true, Q8>(a, chunks, st);
+  else if (copy_dtype == EMB_BF16) go<G, __bf16, true, Q8>(a, chunks, st);
+  else go<G, _Float16, false, Q8>(a, chunks, st);
 }
 
 template <bool Q8>
 void go_type(const AdamArgs& a, uint32_t chunks, int grad_dtype, int copy_dtype, hipStream_t st) {
-  if (grad_dtype == EMB_F32) go<float, Q8>(a, chunks, copy_dtype, st);
-  else if (grad_dtype == EMB_F16) go<_Float16, Q8>(a, chunks, copy_dtype, st);
-  else go<__bf16, Q8>(a, chunks, copy_dtype, st);
+  if (grad_dtype == EMB_F32) go_copy<float, Q8>(a, chunks, copy_dtype, st);
+  else if (grad_dtype == EMB_F16) go_copy<_Float16, Q8>(a, chunks, copy_dtype, st);
+  else go_copy<__bf16, Q8>(a, chunks, copy_dtype, st);
 }
 
 }  // namespace
 
-hipError_t launch_adamw(const AdamArgs& a, uint32_t n_chunks, bool q8, int grad_dtype,
+hipError_t launch_adamw(AdamArgs& a, int64_t elems, uint32_t n_chunks, bool q8, int grad_dtype,
                         int copy_dtype, hipStream_t st) {
+  const int each = 8 + (q8 ? 4 : 16) + (grad_dtype == EMB_F32 ? 4 : 2) + (copy_dtype >= 0 ? 2 : 0);
+  a.once = elems * each > kOnceBytes;
   if (q8) go_type<true>(a, n_chunks, grad_dtype, copy_dtype, st);
   else go_type<false>(a, n_chunks, grad_dtype, copy_dtype, st);
   return hipGetLastError();

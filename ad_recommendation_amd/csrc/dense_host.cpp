@@ -206,7 +206,7 @@ int run_adamw(const AdamCall& c, AdamArgs& a, bool q8, hipStream_t st) {
     }
     if (k == 0) break;
     a.n_tensors = k;
-    DENSE_TRY(done(launch_adamw(a, (uint32_t)chunks, q8, c.grad_dtype,
+    DENSE_TRY(done(launch_adamw(a, total, (uint32_t)chunks, q8, c.grad_dtype,
                                 c.copies ? c.copy_dtype : -1, st),
                    "adamw"));
   }

@@ -72,9 +72,11 @@ struct AdamArgs {
   const float* grad_scale;
   float lr, b1, b2, omb1, omb2, inv_c1, inv_c2, eps;
   uint32_t seed_lo, seed_hi, n_tensors, chunk;  // chunk: elements a workgroup takes
+  uint32_t once;  // more data than the caches hold
 };
 static_assert(sizeof(AdamArgs) <= 4096, "the argument block of a launch");
-hipError_t launch_adamw(const AdamArgs& a, uint32_t n_chunks, bool q8, int grad_dtype,
+// elems: of the whole call, which may be several launches.
+hipError_t launch_adamw(AdamArgs& a, int64_t elems, uint32_t n_chunks, bool q8, int grad_dtype,
                         int copy_dtype, hipStream_t st);
 hipError_t launch_adamw_values(const uint8_t* codes, const uint8_t* exp, int64_t elems, void* out,
                                int out_dtype, hipStream_t st);

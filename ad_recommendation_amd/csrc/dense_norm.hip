@@ -48,7 +48,7 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float (*lds)[kThreads / 
 }
 
 // TPR threads take a row, each NC vectors of eight columns.
-template <typename T, int TPR, int NC>
+template <typename T, int TPR, int NC, bool ONCE>
 __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
   __shared__ float lds[2][kThreads / 64][1];
   constexpr int kRows = kThreads / TPR;
@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
       yr[c] = xr[c];
       gr[c] = xr[c];
       if (live && n[c] > 0) {
-        xr[c] = load8<T, true>(x + at + col, n[c]);
-        if (y) yr[c] = load8<T, true>(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, true>(gate + at + col, n[c]);
+        xr[c] = load8<T, ONCE>(x + at + col, n[c]);
+        if (y) yr[c] = load8<T, ONCE>(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, ONCE>(gate + at + col, n[c]);
       }
     }
     float inv_y = 1.f;
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
     if (r && live) {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (n[c] > 0) store8(r + at + (c * TPR + lane) * 8, rr[c], n[c]);
+        if (n[c] > 0) store8<T, ONCE>(r + at + (c * TPR + lane) * 8, rr[c], n[c]);
     }
     if (h) {
       row_sums<TPR, 1>(s, lds, turn);
@@ -134,14 +134,14 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
       const float inv_r = rsqrtf(s[0] * inv_d + a.eps);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (live && n[c] > 0) store8(h + at + (c * TPR + lane) * 8, rr[c] * inv_r * wp[c], n[c]);
+        if (live && n[c] > 0) store8<T, ONCE>(h + at + (c * TPR + lane) * 8, rr[c] * inv_r * wp[c], n[c]);
     }
   }
 }
 
 // Rows go round the blocks; a thread keeps the column sums of its columns over the rows it sees in
 // registers, the block's rows then meet in LDS, and the blocks in norm_join.
-template <typename T, int TPR, int NC>
+template <typename T, int TPR, int NC, bool ONCE>
 __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   constexpr int kRows = kThreads / TPR;
   constexpr int kSums = 6;
@@ -192,12 +192,12 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       dhr[c] = rr[c];
       if (live && n[c] > 0) {
         if (pre) {
-          rr[c] = load8<T, true>(r + at + col, n[c]);
-          dhr[c] = load8<T, true>(dh + at + col, n[c]);
+          rr[c] = load8<T, ONCE>(r + at + col, n[c]);
+          dhr[c] = load8<T, ONCE>(dh + at + col, n[c]);
         }
-        if (dr) drr[c] = load8<T, true>(dr + at + col, n[c]);
-        if (y) yr[c] = load8<T, true>(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, true>(gate + at + col, n[c]);
+        if (dr) drr[c] = load8<T, ONCE>(dr + at + col, n[c]);
+        if (y) yr[c] = load8<T, ONCE>(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, ONCE>(gate + at + col, n[c]);
       }
     }
     // r^2, u r, y^2, a dr, a u, a r
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       if (a.gate_kind == EMB_GATE_ROWS) {
         if (dgate && live) {
           // wg is w_post alone here (or 1)
-          store8(dgate + at + col, dR * yn * wg[c], n[c]);
+          store8<T, ONCE>(dgate + at + col, dR * yn * wg[c], n[c]);
         }
         const f32x8 g = widen(gr[c]);
         z *= g;
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       c_post[c] += dR * yn;
       c_pre[c] += dhv * (rv * inv_r);
       if (live) {
-        if (dx) store8(dx + at + col, a.alpha * dR, n[c]);
-        if (dy) store8(dy + at + col, inv_y * z - back_y * yv, n[c]);
+        if (dx) store8<T, ONCE>(dx + at + col, a.alpha * dR, n[c]);
+        if (dy) store8<T, ONCE>(dy + at + col, inv_y * z - back_y * yv, n[c]);
       }
     }
   }
@@ -309,16 +309,22 @@ __global__ void __launch_bounds__(kJoin) norm_join(NormArgs a) {
   }
 }
 
+template <typename T>
+bool once(const NormArgs& a, int rows_of_data) {
+  return a.rows * a.dim * (int64_t)sizeof(T) * rows_of_data > kOnceBytes;
+}
 template <typename T, int TPR, int NC>
 void go_fwd(const NormArgs& a, hipStream_t st) {
   const int64_t blocks = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
-  hipLaunchKernelGGL((norm_fwd<T, TPR, NC>), dim3((unsigned)(blocks < 2048 ? blocks : 2048)),
-                     dim3(kThreads), 0, st, a);
+  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048)), block(kThreads);
+  if (once<T>(a, 4)) hipLaunchKernelGGL((norm_fwd<T, TPR, NC, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((norm_fwd<T, TPR, NC, false>), grid, block, 0, st, a);
 }
 template <typename T, int TPR, int NC>
 void go_bwd(const NormArgs& a, hipStream_t st) {
-  if (a.blocks)
-    hipLaunchKernelGGL((norm_bwd<T, TPR, NC>), dim3((unsigned)a.blocks), dim3(kThreads), 0, st, a);
+  const dim3 grid((unsigned)a.blocks), block(kThreads);
+  if (a.blocks && once<T>(a, 6)) hipLaunchKernelGGL((norm_bwd<T, TPR, NC, true>), grid, block, 0, st, a);
+  else if (a.blocks) hipLaunchKernelGGL((norm_bwd<T, TPR, NC, false>), grid, block, 0, st, a);
   hipLaunchKernelGGL((norm_join<T>), dim3((unsigned)((a.dim + 31) / 32), 2), dim3(kJoin), 0, st, a);
 }
 
