@@ -15,6 +15,7 @@
 // stands at which k is free as long as the left operand agrees, and the left operand comes out of
 // LDS by transposing reads, four rows at any address at a time.
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "dense_device.h"
@@ -102,61 +103,129 @@ __device__ __forceinline__ void hide_keys(const AttnArgs& a, int i, int j0, f32x
 }
 
 // ---------------------------------------------------------------- LDS tiles
-// Rows of DH elements with 16 bytes between them.  LDS has 64 banks of 4 bytes.  A left operand's read
-// takes one 16-byte piece of 16 rows at once: an odd number of pieces a row puts them into 16 different
-// places.  A transposing read takes four pieces of four rows at once: row r of each 16 lies at place
-// 4 (r % 4) + r / 4, so that those four rows, consecutive ones, are four places and with them four
-// pieces apart.  (In order, they overlapped: half the cycles that the forward kept LDS busy were
-// conflicts.)  Every place within a tile is a constant from a lane's own.
-template <int DH>
-struct Tile {
-  static constexpr int kPieces = DH / 8;  // of 16 bytes
-  static constexpr int kRow = DH * 2 + 16;
-  __device__ static __forceinline__ int place(int row) { return (row & ~15) | (row & 3) << 2 | (row >> 2 & 3); }
-  __device__ static __forceinline__ int at(int row, int piece) { return place(row) * kRow + piece * 16; }
-};
-
-template <int DH, int ROWS, int THREADS>
-struct Staged {
-  static constexpr int kPieces = Tile<DH>::kPieces;
+// Rows of a head in LDS, read in two ways: 16-byte pieces of 16 rows at once (left operands) and, by the
+// transposing reads, four pieces of four consecutive rows at once.  LDS has 64 banks of 4 bytes, so
+// both are without conflict if the 16 rows' pieces, and the four rows' four pieces, lie in 16 different
+// places of 256 bytes.  (With rows in order and 16 bytes between them the second kind met itself: half
+// the cycles that the forward kept LDS busy.)
+//
+// Through registers: an odd number of pieces a row, row r of each 16 at place 4 (r % 4) + r / 4.
+// Zeros past the last row and column.
+template <typename T, int DH, int ROWS, int THREADS>
+struct RegisterTile {
+  static constexpr int kPieces = DH / 8, kRow = DH * 2 + 16, kBytes = ROWS * kRow;
   static constexpr int kRegs = ROWS * kPieces / THREADS;
+  __device__ static __forceinline__ int at(int row, int piece) {
+    return ((row & ~15) | (row & 3) << 2 | (row >> 2 & 3)) * kRow + piece * 16;
+  }
+  struct Reads {  // where a lane reads in a tile
+    int l, t;
+    __device__ __forceinline__ Reads() {
+      const int n = lane_id();
+      l = at(n & 31, n >> 5);
+      t = at(4 * (n >> 5) + ((n & 15) >> 2), ((n >> 4) & 1) * 2) + (n & 3) * 8;
+    }
+    __device__ __forceinline__ int left(int row0, int ks) const { return l + row0 * kRow + ks * 32; }
+    __device__ __forceinline__ int left_t(int row0, int db, int half) const {
+      return t + (row0 + 2 * half) * kRow + db * 64;  // eight rows on are two places
+    }
+  };
   u32x4 r[kRegs];
-  // Rows row0 .. row0 + ROWS - 1 of a head; zeros past `len` rows and past D columns.
-  template <typename T>
-  __device__ __forceinline__ void load(const T* base, int64_t stride, int row0, int len, int D) {
+  // Rows row0 .. row0 + ROWS - 1 of a head, which has `end` of them.
+  __device__ __forceinline__ void load(char*, const T* base, int64_t stride, int row0, int end, int D) {
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
       const int idx = threadIdx.x + n * THREADS;
       const int row = row0 + idx / kPieces, col = idx % kPieces * 8;
       r[n] = u32x4{0, 0, 0, 0};
-      if (row < len && col < D) r[n] = *reinterpret_cast<const u32x4*>(base + row * stride + col);
+      if (row < end && col < D) r[n] = *reinterpret_cast<const u32x4*>(base + row * stride + col);
     }
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
       const int idx = threadIdx.x + n * THREADS;
-      *reinterpret_cast<u32x4*>(lds + Tile<DH>::at(idx / kPieces, idx % kPieces)) = r[n];
+      *reinterpret_cast<u32x4*>(lds + at(idx / kPieces, idx % kPieces)) = r[n];
     }
+  }
+  __device__ static __forceinline__ void arrived() {}
+};
+
+// Straight from memory to LDS, where heads have DH columns: a wave's load fills 1024 bytes in order, so a
+// row's pieces are exchanged by its number instead of set apart, by the address that a lane loads from.
+// The last row stands for those past it; no query sees them, and no row past `end` is read.
+template <typename T, int DH, int ROWS, int THREADS>
+struct DirectTile {
+  static constexpr int kPieces = DH / 8, kRow = DH * 2, kBytes = ROWS * kRow;
+  static constexpr int kSpan = 16 / kPieces;  // rows in 256 bytes
+  static constexpr int kAtOnce = 64 / kPieces;  // rows of a wave's load
+  static constexpr int kLoads = ROWS / kAtOnce / (THREADS / 64);
+  static_assert(kLoads * kAtOnce * (THREADS / 64) == ROWS, "whole loads");
+  __device__ static __forceinline__ int exchange(int row) { return (row & 3) / kSpan << 2 | (row >> 2 & 3); }
+  struct Reads {
+    int l[DH / 16], t[DH / 32][2];
+    __device__ __forceinline__ Reads() {
+      const int n = lane_id(), row = n & 31;
+#pragma unroll
+      for (int ks = 0; ks < DH / 16; ++ks) l[ks] = row * kRow + ((2 * ks + (n >> 5)) ^ exchange(row)) * 16;
+#pragma unroll
+      for (int db = 0; db < DH / 32; ++db)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = 4 * (n >> 5) + ((n & 15) >> 2) + 8 * half;
+          const int piece = db * 4 + ((n >> 4) & 1) * 2 + ((n & 3) >> 1);
+          t[db][half] = r * kRow + (piece ^ exchange(r)) * 16 + (n & 1) * 8;
+        }
+    }
+    __device__ __forceinline__ int left(int row0, int ks) const { return l[ks] + row0 * kRow; }
+    __device__ __forceinline__ int left_t(int row0, int db, int half) const { return t[db][half] + row0 * kRow; }
+  };
+  // The compiler would wait for every load to LDS that is under way before each transposing read, of
+  // whichever buffer; it is told nothing, and arrived() waits.  The load has no register to write.
+  __device__ static __forceinline__ void load_piece(const char* p, uint32_t off, char* lds) {
+    typedef __attribute__((address_space(3))) char* Lds;
+    const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(Lds)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(off), "s"(p)
+                 : "memory", "m0");
+  }
+  __device__ __forceinline__ void load(char* lds, const T* base, int64_t stride, int row0, int end, int) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+    const int from = min(row0, end - 1), last = end - 1 - from;
+    const char* p = reinterpret_cast<const char*>(base + from * stride);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int first = (wave + n * (THREADS / 64)) * kAtOnce, row = first + lane / kPieces;
+      const int piece = (lane % kPieces) ^ exchange(row);
+      // a tile's rows are within 2^31 bytes of one another: see direct()
+      const uint32_t off = (uint32_t)(min(row, last) * ((int)stride * 2) + piece * 16);
+      load_piece(p, off, lds + first * kRow);
+    }
+  }
+  __device__ __forceinline__ void store(char*) const {}
+  // A barrier does not wait for loads to LDS.
+  __device__ static __forceinline__ void arrived() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   }
 };
 
+template <typename T, int DH, int ROWS, int THREADS, bool DIRECT>
+using TileOf = std::conditional_t<DIRECT, DirectTile<T, DH, ROWS, THREADS>, RegisterTile<T, DH, ROWS, THREADS>>;
+
 // Left operand: rows row0 .. row0 + 31, columns 16 ks .. 16 ks + 15 as k.
-template <typename T, int DH>
-__device__ __forceinline__ typename Vec8<T>::t left(const char* lds, int row0, int ks) {
-  const int l = lane_id();
-  return *reinterpret_cast<const typename Vec8<T>::t*>(lds + Tile<DH>::at(l & 31, l >> 5) + row0 * Tile<DH>::kRow + ks * 32);
+template <typename T, typename R>
+__device__ __forceinline__ typename Vec8<T>::t left(const char* lds, const R& r, int row0, int ks) {
+  return *reinterpret_cast<const typename Vec8<T>::t*>(lds + r.left(row0, ks));
 }
 // Left operand, transposed: columns 32 db .. 32 db + 31 as rows, rows row0 .. row0 + 15 as k, in the
 // order in which a result's registers hold them.
-template <typename T, int DH>
-__device__ __forceinline__ typename Vec8<T>::t left_t(const char* lds, int row0, int db) {
-  const int l = lane_id();
-  const char* p = lds + Tile<DH>::at(4 * (l >> 5) + ((l & 15) >> 2), ((l >> 4) & 1) * 2) + (l & 3) * 8;
+template <typename T, typename R>
+__device__ __forceinline__ typename Vec8<T>::t left_t(const char* lds, const R& r, int row0, int db) {
   typedef __attribute__((address_space(3))) i16x4* Lds;
-  p += row0 * Tile<DH>::kRow + db * 64;
-  const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p);
-  const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 2 * Tile<DH>::kRow));  // eight rows on
+  const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(lds + r.left_t(row0, db, 0)));
+  const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(lds + r.left_t(row0, db, 1)));
   const i16x8 v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(typename Vec8<T>::t, v);
 }
@@ -296,6 +365,10 @@ __device__ __forceinline__ void again_dkv(const AttnArgs& a, int64_t begin, int 
 }
 
 // ---------------------------------------------------------------- which keys a query tile meets
+// Workgroups of four waves take query tiles from the last to the first: a sequence's first tiles meet the
+// fewest keys, and short work at the end leaves fewer units idle (16.4k tokens, 16 heads of 128, window
+// 1024: 193 -> 190 us; those of one wave, all short, are 4 us slower that way).
+
 // The tile that holds the sinks where the window's tiles do not reach it, then the window's.
 template <int WAVES>
 struct KeyTiles {
@@ -315,15 +388,17 @@ struct KeyTiles {
 };
 
 // ---------------------------------------------------------------- forward
-template <typename T, int DH, int WAVES>
+template <typename T, int DH, int WAVES, bool DIRECT>
 __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a) {
   typedef typename Vec8<T>::t V8;
   typedef Group<WAVES> G;
+  typedef TileOf<T, DH, G::kRows, G::kThreads, DIRECT> Tile;
   constexpr int kSubs = G::kRows / 32;
-  __shared__ __attribute__((aligned(16))) char lds[G::kBuffers][2][G::kRows * Tile<DH>::kRow];
+  __shared__ __attribute__((aligned(1024))) char lds[G::kBuffers][2][Tile::kBytes];
   const int group = a.q_heads / a.kv_heads;
-  const int kh = blockIdx.x % a.kv_heads;
-  const int rest = blockIdx.x / a.kv_heads;
+  const int block = WAVES == 1 ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
+  const int kh = block % a.kv_heads;
+  const int rest = block / a.kv_heads;
   const int h = kh * group + rest % group;
   const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
   if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
@@ -345,33 +420,36 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
   const KeyTiles<WAVES> tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
-  Staged<DH, G::kRows, G::kThreads> ks_, vs_;
-  auto load = [&](int it) {
-    ks_.load(kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
-    vs_.load(vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+  Tile kl, vl;
+  auto load = [&](int it, char (*to)[Tile::kBytes]) {
+    kl.load(to[0], kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+    vl.load(to[1], vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
   };
-  load(0);
+  load(0, lds[0]);
+  const typename Tile::Reads at;
 
   f32x16 o[DH / 32] = {};
   float m = -kInf, l = 0.f;  // the maximum that o and l stand at, and this lane's half of the sum
-  for (int it = 0; it < tiles.n; ++it) {
-    char* kt = lds[it & (G::kBuffers - 1)][0];
-    char* vt = lds[it & (G::kBuffers - 1)][1];
+  auto meet = [&](int it, char (*lds_now)[Tile::kBytes], char (*lds_next)[Tile::kBytes]) {
+    const char* kt = lds_now[0];
+    const char* vt = lds_now[1];
     if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
-    ks_.store(kt);
-    vs_.store(vt);
-    if (it + 1 < tiles.n) load(it + 1);
-    __syncthreads();
+    kl.store(lds_now[0]);
+    vl.store(lds_now[1]);
+    if (!DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
+    Tile::arrived();
+    __syncthreads();  // this tile is there, and the other buffer is no longer read
+    if (DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
     const int j0 = tiles.key0(it);
-    if (iw >= s.len || j0 > iw + 31) continue;
-    if (j0 >= a.sinks && j0 + G::kRows - 1 <= iw - a.window) continue;
+    if (iw >= s.len || j0 > iw + 31) return;
+    if (j0 >= a.sinks && j0 + G::kRows - 1 <= iw - a.window) return;
 
     f32x16 sc[kSubs] = {};
 #pragma unroll
     for (int ks = 0; ks < DH / 16; ++ks)
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub)
-        sc[sub] = mma(left<T, DH>(kt, 32 * sub, ks), q[ks], sc[sub]);
+        sc[sub] = mma(left<T>(kt, at, 32 * sub, ks), q[ks], sc[sub]);
 #pragma unroll
     for (int sub = 0; sub < kSubs; ++sub) {
       const int js = j0 + 32 * sub;
@@ -401,8 +479,13 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
     for (int k = 0; k < 2 * kSubs; ++k) {
       const V8 pb = right_of<T>(sc[k >> 1], 8 * (k & 1));
 #pragma unroll
-      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T, DH>(vt, 16 * k, db), pb, o[db]);
+      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(vt, at, 16 * k, db), pb, o[db]);
     }
+  };
+  // two tiles a turn, so that the buffers' places are constants
+  for (int it = 0; it < tiles.n; it += 2) {
+    meet(it, lds[0], lds[G::kBuffers - 1]);
+    if (it + 1 < tiles.n) meet(it + 1, lds[G::kBuffers - 1], lds[0]);
   }
   l = swap32_sum(l);
   uint32_t again = either(live && not_finite(o));
@@ -414,15 +497,17 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
 
 // ---------------------------------------------------------------- backward: dq
 // As the forward, with dout as a second right operand; also writes delta.
-template <typename T, int DH, int WAVES>
+template <typename T, int DH, int WAVES, bool DIRECT>
 __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) attn_dq(AttnArgs a) {
   typedef typename Vec8<T>::t V8;
   typedef Group<WAVES> G;
+  typedef TileOf<T, DH, G::kRows, G::kThreads, DIRECT> Tile;
   constexpr int kSubs = G::kRows / 32;
-  __shared__ __attribute__((aligned(16))) char lds[G::kBuffers][2][G::kRows * Tile<DH>::kRow];
+  __shared__ __attribute__((aligned(1024))) char lds[G::kBuffers][2][Tile::kBytes];
   const int group = a.q_heads / a.kv_heads;
-  const int kh = blockIdx.x % a.kv_heads;
-  const int rest = blockIdx.x / a.kv_heads;
+  const int block = WAVES == 1 ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
+  const int kh = block % a.kv_heads;
+  const int rest = block / a.kv_heads;
   const int h = kh * group + rest % group;
   const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
   if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
@@ -434,12 +519,13 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
   const KeyTiles<WAVES> tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
-  Staged<DH, G::kRows, G::kThreads> ks_, vs_;
-  auto load = [&](int it) {
-    ks_.load(kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
-    vs_.load(vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+  Tile kl, vl;
+  auto load = [&](int it, char (*to)[Tile::kBytes]) {
+    kl.load(to[0], kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+    vl.load(to[1], vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
   };
-  load(0);
+  load(0, lds[0]);
+  const typename Tile::Reads at;
 
   V8 q[DH / 16], d[DH / 16];
   right_row<T, DH>(a.q, s.begin + i, h, live, a.dim, q);
@@ -460,16 +546,18 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
   const float lse = live ? a.lse[stat] * kLog2e : kInf;
 
   f32x16 dq[DH / 32] = {};
-  for (int it = 0; it < tiles.n; ++it) {
-    char* kt = lds[it & (G::kBuffers - 1)][0];
-    char* vt = lds[it & (G::kBuffers - 1)][1];
+  auto meet = [&](int it, char (*lds_now)[Tile::kBytes], char (*lds_next)[Tile::kBytes]) {
+    const char* kt = lds_now[0];
+    const char* vt = lds_now[1];
     if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
-    ks_.store(kt);
-    vs_.store(vt);
-    if (it + 1 < tiles.n) load(it + 1);
-    __syncthreads();
+    kl.store(lds_now[0]);
+    vl.store(lds_now[1]);
+    if (!DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
+    Tile::arrived();
+    __syncthreads();  // this tile is there, and the other buffer is no longer read
+    if (DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
     const int j0 = tiles.key0(it);
-    if (iw >= s.len) continue;
+    if (iw >= s.len) return;
 #pragma unroll
     for (int sub = 0; sub < kSubs; ++sub) {
       const int js = j0 + 32 * sub;
@@ -477,8 +565,8 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
       f32x16 sc = {}, dp = {};
 #pragma unroll
       for (int ks = 0; ks < DH / 16; ++ks) {
-        sc = mma(left<T, DH>(kt, 32 * sub, ks), q[ks], sc);
-        dp = mma(left<T, DH>(vt, 32 * sub, ks), d[ks], dp);
+        sc = mma(left<T>(kt, at, 32 * sub, ks), q[ks], sc);
+        dp = mma(left<T>(vt, at, 32 * sub, ks), d[ks], dp);
       }
       f32x16 ds;
 #pragma unroll
@@ -490,9 +578,14 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
         const V8 b = right_of<T>(ds, 8 * k);
 #pragma unroll
         for (int db = 0; db < DH / 32; ++db)
-          dq[db] = mma(left_t<T, DH>(kt, 32 * sub + 16 * k, db), b, dq[db]);
+          dq[db] = mma(left_t<T>(kt, at, 32 * sub + 16 * k, db), b, dq[db]);
       }
     }
+  };
+  // two tiles a turn, so that the buffers' places are constants
+  for (int it = 0; it < tiles.n; it += 2) {
+    meet(it, lds[0], lds[G::kBuffers - 1]);
+    if (it + 1 < tiles.n) meet(it + 1, lds[G::kBuffers - 1], lds[0]);
   }
   uint32_t again = either(live && not_finite(dq));
   if (live && !(again >> (lane_id() & 31) & 1)) store_row<T, DH>(a.dq, s.begin + i, h, a.dim, dq, a.scale);
@@ -562,31 +655,33 @@ __device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave,
   }
 }
 
-template <int DH, int WAVES>
+template <typename T, int DH, int WAVES, bool DIRECT>
 struct DkvShape {
   typedef Group<WAVES> G;
   static constexpr bool kWide = DH == 128 && WAVES == 4;
   static constexpr int kWaves = kWide ? 8 : WAVES;
   static constexpr int kBlock = kWaves * 64;
   static constexpr int kShare = kWide ? 2 : 1;  // waves that share 32 keys
-  static constexpr int kTile = G::kRows * Tile<DH>::kRow;
   static constexpr int kKeyTiles = kWide ? 2 : 0;
+  typedef TileOf<T, DH, G::kRows, kBlock, DIRECT> Tile;
 };
-template <int DH, int WAVES>
+template <typename T, int DH, int WAVES, bool DIRECT>
 struct DkvShared {
-  typedef DkvShape<DH, WAVES> P;
-  char q[P::G::kBuffers][P::kTile], d[P::G::kBuffers][P::kTile];
+  typedef DkvShape<T, DH, WAVES, DIRECT> P;
+  static constexpr int kTile = P::Tile::kBytes;
+  char q[P::G::kBuffers][kTile], d[P::G::kBuffers][kTile];
+  char k[P::kKeyTiles][kTile], v[P::kKeyTiles][kTile];
   float lse[P::G::kBuffers][P::G::kRows], delta[P::G::kBuffers][P::G::kRows];
-  char k[P::kKeyTiles][P::kTile], v[P::kKeyTiles][P::kTile];
 };
 
 // SINK: rows `row0` to `row1` - 1 against the sinks, the sums to the slot's place; otherwise those rows
 // against the 128 keys from j0.
-template <typename T, int DH, int WAVES, bool SINK>
-__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh, const SinkSlots& parts,
+template <typename T, int DH, int WAVES, bool DIRECT, bool SINK>
+__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, DIRECT>& sh, const SinkSlots& parts,
                                     const Seq& s, int kh, int j0, int row0, int row1, int64_t slot) {
   typedef typename Vec8<T>::t V8;
-  typedef DkvShape<DH, WAVES> P;
+  typedef DkvShape<T, DH, WAVES, DIRECT> P;
+  typedef typename P::Tile Tile;
   typedef Group<WAVES> G;
   constexpr int kRows = G::kRows;
   const int group = a.q_heads / a.kv_heads;
@@ -603,11 +698,11 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh,
     const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      Staged<DH, kRows, P::kBlock> ks_, vs_;
-      ks_.load(kp, a.k.tok, j0 + kRows * x, s.len, a.dim);
-      vs_.load(vp, a.v.tok, j0 + kRows * x, s.len, a.dim);
-      ks_.store(sh.k[x]);
-      vs_.store(sh.v[x]);
+      Tile kl, vl;
+      kl.load(sh.k[x], kp, a.k.tok, j0 + kRows * x, s.len, a.dim);
+      vl.load(sh.v[x], vp, a.v.tok, j0 + kRows * x, s.len, a.dim);
+      kl.store(sh.k[x]);
+      vl.store(sh.v[x]);
     }
   } else {
     right_row<T, DH>(a.k, s.begin + j, kh, live, a.dim, k);
@@ -616,20 +711,21 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh,
   const float c = a.scale * kLog2e;
 
   const int n_tiles = (row1 - row0 + kRows - 1) / kRows;
-  Staged<DH, kRows, P::kBlock> qs_, ds_;
+  Tile ql, dl;
+  const typename Tile::Reads at;
   float stat = 0.f;  // the first kRows threads: lse of a row; as many after them: its delta
   int next_h = kh * group, next_r0 = row0;  // what is loaded next
-  auto load = [&]() {
+  auto load = [&](int b) {
     const int h = next_h, r0 = next_r0;
-    qs_.load(static_cast<const T*>(a.q.p) + s.begin * a.q.tok + h * a.q.head, a.q.tok, r0, row1, a.dim);
-    ds_.load(static_cast<const T*>(a.dout.p) + s.begin * a.dout.tok + h * a.dout.head, a.dout.tok,
-             r0, row1, a.dim);
+    ql.load(sh.q[b], static_cast<const T*>(a.q.p) + s.begin * a.q.tok + h * a.q.head, a.q.tok, r0, row1, a.dim);
+    dl.load(sh.d[b], static_cast<const T*>(a.dout.p) + s.begin * a.dout.tok + h * a.dout.head, a.dout.tok, r0,
+            row1, a.dim);
     if (threadIdx.x < 2 * kRows) {
       const int row = r0 + (threadIdx.x & (kRows - 1));
       const float* p = threadIdx.x < kRows ? a.lse : a.delta;
-      stat = row < row1 ? p[(int64_t)h * a.n_tok + s.begin + row] : 0.f;
       // a row that is not there gets probabilities of zero
-      if (threadIdx.x < kRows) stat = row < row1 ? stat * kLog2e : kInf;
+      stat = threadIdx.x < kRows ? kInf : 0.f;
+      if (row < row1) stat = p[(int64_t)h * a.n_tok + s.begin + row];
     }
     next_r0 += kRows;
     if (next_r0 >= row1) {
@@ -637,19 +733,22 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh,
       ++next_h;
     }
   };
-  load();
+  load(0);
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
   int r0 = row0;
   const int steps = n_tiles * group;  // of all heads of the group
   for (int step = 0; step < steps; ++step, r0 = r0 + kRows < row1 ? r0 + kRows : row0) {
     const int b = step & (G::kBuffers - 1);
     if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
-    qs_.store(sh.q[b]);
-    ds_.store(sh.d[b]);
-    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat;
+    ql.store(sh.q[b]);
+    dl.store(sh.d[b]);
+    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat * kLog2e;
     else if (threadIdx.x < 2 * kRows) sh.delta[b][threadIdx.x - kRows] = stat;
-    if (step + 1 < steps) load();
-    __syncthreads();
+    const int other = b ^ (G::kBuffers - 1);
+    if (!DIRECT && step + 1 < steps) load(other);
+    Tile::arrived();
+    __syncthreads();  // this step's rows are there, and the other buffer is no longer read
+    if (DIRECT && step + 1 < steps) load(other);
     if (jw >= s.len) continue;
 #pragma unroll
     for (int sub_ = 0; sub_ < kRows / 32 / P::kShare; ++sub_) {
@@ -666,15 +765,15 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh,
       if constexpr (P::kWide) {
 #pragma unroll
         for (int ks = 0; ks < DH / 16; ++ks)
-          sc = mma(left<T, DH>(sh.q[b], 32 * sub, ks), left<T, DH>(sh.k[0], jrow, ks), sc);
+          sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), left<T>(sh.k[jrow >> 6], at, jrow & 63, ks), sc);
 #pragma unroll
         for (int ks = 0; ks < DH / 16; ++ks)
-          dp = mma(left<T, DH>(sh.d[b], 32 * sub, ks), left<T, DH>(sh.v[0], jrow, ks), dp);
+          dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), left<T>(sh.v[jrow >> 6], at, jrow & 63, ks), dp);
       } else {
 #pragma unroll
         for (int ks = 0; ks < DH / 16; ++ks) {
-          sc = mma(left<T, DH>(sh.q[b], 32 * sub, ks), k[ks], sc);
-          dp = mma(left<T, DH>(sh.d[b], 32 * sub, ks), v[ks], dp);
+          sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), k[ks], sc);
+          dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), v[ks], dp);
         }
       }
       f32x16 p, ds;
@@ -701,8 +800,8 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh,
         const V8 pb = right_of<T>(p, 8 * x), db_ = right_of<T>(ds, 8 * x);
 #pragma unroll
         for (int db = 0; db < DH / 32; ++db) {
-          dv[db] = mma(left_t<T, DH>(sh.d[b], 32 * sub + 16 * x, db), pb, dv[db]);
-          dk[db] = mma(left_t<T, DH>(sh.q[b], 32 * sub + 16 * x, db), db_, dk[db]);
+          dv[db] = mma(left_t<T>(sh.d[b], at, 32 * sub + 16 * x, db), pb, dv[db]);
+          dk[db] = mma(left_t<T>(sh.q[b], at, 32 * sub + 16 * x, db), db_, dk[db]);
         }
       }
     }
@@ -751,10 +850,10 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<DH, WAVES>& sh,
   }
 }
 
-template <typename T, int DH, int WAVES>
-__global__ void __launch_bounds__((DkvShape<DH, WAVES>::kBlock), 2)
+template <typename T, int DH, int WAVES, bool DIRECT>
+__global__ void __launch_bounds__((DkvShape<T, DH, WAVES, DIRECT>::kBlock), 2)
     attn_dkv(AttnArgs a, int main_blocks, int chunk) {
-  __shared__ __attribute__((aligned(16))) DkvShared<DH, WAVES> sh;
+  __shared__ __attribute__((aligned(1024))) DkvShared<T, DH, WAVES, DIRECT> sh;
   constexpr int kTokens = Group<WAVES>::kTokens;
   const bool sink = (int)blockIdx.x >= main_blocks;  // the same for the whole workgroup
   const int block = sink ? blockIdx.x - main_blocks : blockIdx.x;
@@ -764,12 +863,12 @@ __global__ void __launch_bounds__((DkvShape<DH, WAVES>::kBlock), 2)
     const Seq s = find_tile(a, slot, [&](int64_t t, int b) { return parts.first(t, b); });
     const int64_t r0 = parts.reach + (int64_t)s.tile * chunk;
     if (s.tile < 0 || r0 >= s.len) return;
-    dkv<T, DH, WAVES, true>(a, sh, parts, s, kh, 0, (int)r0, (int)min(r0 + chunk, (int64_t)s.len), slot);
+    dkv<T, DH, WAVES, DIRECT, true>(a, sh, parts, s, kh, 0, (int)r0, (int)min(r0 + chunk, (int64_t)s.len), slot);
   } else {
     const Seq s = find_tile(a, slot, [](int64_t t, int b) { return t / kTokens + b; });
     if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
     const int j0 = s.tile * kTokens;
-    dkv<T, DH, WAVES, false>(a, sh, parts, s, kh, j0, j0, (int)min(j0 + parts.reach, (int64_t)s.len), 0);
+    dkv<T, DH, WAVES, DIRECT, false>(a, sh, parts, s, kh, j0, j0, (int)min(j0 + parts.reach, (int64_t)s.len), 0);
   }
 }
 
@@ -807,14 +906,15 @@ __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int token
 // columns of one product, so keys and values are read once.  Memory bound.
 template <int DH>
 struct WaveTile {  // 32 rows, of one wave
-  static constexpr int kRegs = 32 * Tile<DH>::kPieces / 64;
-  static constexpr int kBytes = 32 * Tile<DH>::kRow;
+  static constexpr int kPieces = DH / 8, kRegs = 32 * kPieces / 64;
 };
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int splits) {
   typedef typename Vec8<T>::t V8;
-  __shared__ __attribute__((aligned(16))) char lds[4][2][WaveTile<DH>::kBytes];
+  typedef RegisterTile<T, DH, 32, 64> Tile;
+  const typename Tile::Reads reads;
+  __shared__ __attribute__((aligned(16))) char lds[4][2][Tile::kBytes];
   __shared__ float stats[4][2][32];
   const int group = a.q_heads / a.kv_heads;
   const int kh = blockIdx.x % a.kv_heads;
@@ -846,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
 #pragma unroll
     for (int n = 0; n < WaveTile<DH>::kRegs; ++n) {
       const int idx = lane + n * 64;
-      const int u = t0 + idx / Tile<DH>::kPieces, cl = idx % Tile<DH>::kPieces * 8;
+      const int u = t0 + idx / Tile::kPieces, cl = idx % Tile::kPieces * 8;
       kr[n] = vr[n] = u32x4{0, 0, 0, 0};
       if (u < u1 && cl < a.dim) {
         const int64_t key = u < n_sink ? u : first + (u - n_sink);
@@ -865,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
 #pragma unroll
     for (int n = 0; n < WaveTile<DH>::kRegs; ++n) {
       const int idx = lane + n * 64;
-      const int at = Tile<DH>::at(idx / Tile<DH>::kPieces, idx % Tile<DH>::kPieces);
+      const int at = Tile::at(idx / Tile::kPieces, idx % Tile::kPieces);
       *reinterpret_cast<u32x4*>(kt + at) = kr[n];
       *reinterpret_cast<u32x4*>(vt + at) = vr[n];
     }
@@ -876,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     f32x16 sc = {};
 #pragma unroll
-    for (int ks = 0; ks < DH / 16; ++ks) sc = mma(left<T, DH>(kt, 0, ks), q[ks], sc);
+    for (int ks = 0; ks < DH / 16; ++ks) sc = mma(left<T>(kt, reads, 0, ks), q[ks], sc);
     if (t0 + 32 > u1) {
 #pragma unroll
       for (int r = 0; r < 16; ++r)
@@ -904,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
     for (int k = 0; k < 2; ++k) {
       const V8 pb = right_of<T>(sc, 8 * k);
 #pragma unroll
-      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T, DH>(vt, 16 * k, db), pb, o[db]);
+      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(vt, reads, 16 * k, db), pb, o[db]);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -1061,24 +1161,25 @@ AttnDecodePlan plan_attn_decode(const EmbAttn& a, int64_t n_seq, int64_t capacit
   return p;
 }
 
-template <typename T, int DH, int WAVES>
+template <typename T, int DH, int WAVES, bool DIRECT>
 void go_fwd(const AttnArgs& a, hipStream_t st) {
   typedef Group<WAVES> G;
   const unsigned grid = (unsigned)((a.n_tok / G::kTokens + a.n_seq) * a.q_heads);
-  hipLaunchKernelGGL((attn_fwd<T, DH, WAVES>), dim3(grid), dim3(G::kThreads), 0, st, a);
+  hipLaunchKernelGGL((attn_fwd<T, DH, WAVES, DIRECT>), dim3(grid), dim3(G::kThreads), 0, st, a);
 }
 
-template <typename T, int DH, int WAVES>
+template <typename T, int DH, int WAVES, bool DIRECT>
 void go_bwd(const AttnArgs& a, hipStream_t st) {
   typedef Group<WAVES> G;
   const int64_t slots = a.n_tok / G::kTokens + a.n_seq;
-  hipLaunchKernelGGL((attn_dq<T, DH, WAVES>), dim3((unsigned)(slots * a.q_heads)), dim3(G::kThreads), 0, st, a);
+  hipLaunchKernelGGL((attn_dq<T, DH, WAVES, DIRECT>), dim3((unsigned)(slots * a.q_heads)), dim3(G::kThreads), 0,
+                     st, a);
   const int chunk = sink_chunk(a.n_tok);
   const SinkSlots n(a.n_tok, a.n_seq, a.window, G::kTokens, chunk);
   const bool sinks = a.sinks > 0 && a.n_tok > n.reach;  // a sequence may be longer than reach
-  hipLaunchKernelGGL((attn_dkv<T, DH, WAVES>),
+  hipLaunchKernelGGL((attn_dkv<T, DH, WAVES, DIRECT>),
                      dim3((unsigned)((slots + (sinks ? n.chunk_slots : 0)) * a.kv_heads)),
-                     dim3(DkvShape<DH, WAVES>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
+                     dim3(DkvShape<T, DH, WAVES, DIRECT>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
   if (sinks)
     hipLaunchKernelGGL((attn_sink_join<T>),
                        dim3((unsigned)n.numbers,
@@ -1087,24 +1188,36 @@ void go_bwd(const AttnArgs& a, hipStream_t st) {
                        dim3(kThreads), 0, st, a, G::kTokens, chunk);
 }
 
+// Whether tiles may be loaded straight to LDS: whole rows of the kernel's width, and a tile's rows
+// within 2^31 bytes of one another.
+bool direct(const AttnArgs& a, int width, std::initializer_list<const EmbHeads*> heads) {
+  for (const EmbHeads* h : heads)
+    if (h->tok < 0 || h->tok > ((int64_t)1 << 23)) return false;
+  return a.dim == width;
+}
+
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st) {
   by_shape(a, [&](auto t, auto d) {
+    typedef decltype(t) T;
     constexpr int DH = decltype(d)::value;
     if constexpr (DH < 128) {
-      if (one_wave(a)) return go_fwd<decltype(t), DH, 1>(a, st);
+      if (one_wave(a)) return go_fwd<T, DH, 1, false>(a, st);
     }
-    go_fwd<decltype(t), DH, 4>(a, st);
+    if (direct(a, DH, {&a.k, &a.v})) go_fwd<T, DH, 4, true>(a, st);
+    else go_fwd<T, DH, 4, false>(a, st);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
   by_shape(a, [&](auto t, auto d) {
+    typedef decltype(t) T;
     constexpr int DH = decltype(d)::value;
     if constexpr (DH < 128) {
-      if (one_wave(a)) return go_bwd<decltype(t), DH, 1>(a, st);
+      if (one_wave(a)) return go_bwd<T, DH, 1, false>(a, st);
     }
-    go_bwd<decltype(t), DH, 4>(a, st);
+    if (direct(a, DH, {&a.q, &a.k, &a.v, &a.dout})) go_bwd<T, DH, 4, true>(a, st);
+    else go_bwd<T, DH, 4, false>(a, st);
   });
   return hipGetLastError();
 }
