@@ -162,19 +162,20 @@ struct DirectTile {
   static constexpr int kLoads = ROWS / kAtOnce / (THREADS / 64);
   static_assert(kLoads * kAtOnce * (THREADS / 64) == ROWS, "whole loads");
   __device__ static __forceinline__ int exchange(int row) { return (row & 3) / kSpan << 2 | (row >> 2 & 3); }
+  __device__ static __forceinline__ int at(int row, int piece) { return row * kRow + (piece ^ exchange(row)) * 16; }
   struct Reads {
     int l[DH / 16], t[DH / 32][2];
     __device__ __forceinline__ Reads() {
       const int n = lane_id(), row = n & 31;
 #pragma unroll
-      for (int ks = 0; ks < DH / 16; ++ks) l[ks] = row * kRow + ((2 * ks + (n >> 5)) ^ exchange(row)) * 16;
+      for (int ks = 0; ks < DH / 16; ++ks) l[ks] = at(row, 2 * ks + (n >> 5));
 #pragma unroll
       for (int db = 0; db < DH / 32; ++db)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int r = 4 * (n >> 5) + ((n & 15) >> 2) + 8 * half;
           const int piece = db * 4 + ((n >> 4) & 1) * 2 + ((n & 3) >> 1);
-          t[db][half] = r * kRow + (piece ^ exchange(r)) * 16 + (n & 1) * 8;
+          t[db][half] = at(r, piece) + (n & 1) * 8;
         }
     }
     __device__ __forceinline__ int left(int row0, int ks) const { return l[ks] + row0 * kRow; }
@@ -249,6 +250,68 @@ __device__ __forceinline__ typename Vec8<T>::t right_of(const f32x16& p, int r) 
   const f32x8 x = {p[r], p[r + 1], p[r + 2], p[r + 3], p[r + 4], p[r + 5], p[r + 6], p[r + 7]};
   return __builtin_convertvector(x, typename Vec8<T>::t);
 }
+
+// The 32 rows of a wave, to right operands and from results.  A lane has a row of its own there, 16 or
+// 8 bytes at a time, which in memory are scattered pieces of 32 rows; so rows pass through the wave's
+// part of LDS (`part`, from row `first` of a tile on) and memory sees whole ones.  Backward of 512 short
+// histories: writing results piece by piece took 23 of dq's 92 us.
+template <typename T, int DH, typename TILE>
+struct WaveRows {
+  static constexpr int kPieces = DH / 8, kRegs = 32 * kPieces / 64;
+  u32x4 r[kRegs];
+  // the first `rows` of the 32 from token tok on; zeros past them and past D columns
+  __device__ __forceinline__ void load(const EmbHeads& t, int64_t tok, int head, int rows, int D) {
+    const T* p = static_cast<const T*>(t.p) + tok * t.tok + head * t.head;
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane_id() + n * 64, row = idx / kPieces, col = idx % kPieces * 8;
+      r[n] = u32x4{0, 0, 0, 0};
+      if (row < rows && col < D) r[n] = *reinterpret_cast<const u32x4*>(p + row * t.tok + col);
+    }
+  }
+  __device__ __forceinline__ void to_right(char* part, int first, const typename TILE::Reads& at,
+                                           typename Vec8<T>::t (&f)[DH / 16]) const {
+    wave_sync();
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane_id() + n * 64;
+      *reinterpret_cast<u32x4*>(part + TILE::at(first + idx / kPieces, idx % kPieces)) = r[n];
+    }
+    wave_sync();
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks) f[ks] = left<T>(part, at, first, ks);
+  }
+  // Rows of results that hold them as columns (one per 32 of their elements), but those in `skip`.
+  __device__ static __forceinline__ void store(const EmbHeads& t, int64_t tok, int head, int rows, int D,
+                                               char* part, int first, const f32x16 (&x)[DH / 32], float by,
+                                               uint32_t skip) {
+    typedef T V __attribute__((ext_vector_type(4)));
+    const int own = lane_id() & 31, half = lane_id() >> 5;
+    wave_sync();
+#pragma unroll
+    for (int db = 0; db < DH / 32; ++db) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 v = {x[db][4 * g] * by, x[db][4 * g + 1] * by, x[db][4 * g + 2] * by, x[db][4 * g + 3] * by};
+        *reinterpret_cast<V*>(part + TILE::at(first + own, db * 4 + g) + half * 8) = __builtin_convertvector(v, V);
+      }
+    }
+    wave_sync();
+    T* p = static_cast<T*>(t.p) + tok * t.tok + head * t.head;
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane_id() + n * 64, row = idx / kPieces, col = idx % kPieces * 8;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(part + TILE::at(first + row, idx % kPieces));
+      if (row < rows && col < D && !(skip >> row & 1)) *reinterpret_cast<u32x4*>(p + row * t.tok + col) = v;
+    }
+  }
+  // LDS accesses of one wave are carried out in order; this keeps the compiler to that order.
+  __device__ static __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+};
 
 // Writes a lane's row from results that hold it as a column (one per 32 of its elements).
 template <typename T, int DH>
@@ -407,15 +470,10 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
   const int i = iw + (lane_id() & 31);
   const bool live = i < s.len;
 
-  V8 q[DH / 16];
-  right_row<T, DH>(a.q, s.begin + i, h, live && a.scale != 0.f, a.dim, q);
-  // the running maximum is one of q . k, so a negative scale turns q around and a scale of zero
-  // leaves zeros
-  if (a.scale < 0.f) {
-#pragma unroll
-    for (int ks = 0; ks < DH / 16; ++ks) q[ks] = -q[ks];
-  }
-  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+  const int rows = s.len - iw;  // of the wave's 32 queries
+  typedef WaveRows<T, DH, Tile> Rows;
+  Rows ql;
+  ql.load(a.q, s.begin + iw, h, a.scale != 0.f ? rows : 0, a.dim);
 
   const KeyTiles<WAVES> tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
@@ -427,6 +485,17 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
   };
   load(0, lds[0]);
   const typename Tile::Reads at;
+  // the wave's own part of the buffers: of the last one before the tiles, of the first one after them
+  const int part = WAVES == 1 ? 0 : threadIdx.x >> 7, first = WAVES == 1 ? 0 : 32 * (threadIdx.x >> 6 & 1);
+  V8 q[DH / 16];
+  ql.to_right(lds[G::kBuffers - 1][part], first, at, q);
+  // the running maximum is one of q . k, so a negative scale turns q around and a scale of zero
+  // leaves zeros
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks) q[ks] = -q[ks];
+  }
+  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
 
   f32x16 o[DH / 32] = {};
   float m = -kInf, l = 0.f;  // the maximum that o and l stand at, and this lane's half of the sum
@@ -489,7 +558,8 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
   }
   l = swap32_sum(l);
   uint32_t again = either(live && not_finite(o));
-  if (live && !(again >> (lane_id() & 31) & 1)) store_row<T, DH>(a.out, s.begin + i, h, a.dim, o, 1.f / l);
+  __syncthreads();  // the tiles are done with
+  Rows::store(a.out, s.begin + iw, h, rows, a.dim, lds[0][part], first, o, 1.f / l, again);
   if (live && a.lse && lane_id() < 32)
     a.lse[(int64_t)h * a.n_tok + s.begin + i] = m * c * kLn2 + logf(l);
   for (; again; again &= again - 1) again_fwd<T>(a, s.begin, iw + __builtin_ctz(again), h, kh);
@@ -516,6 +586,12 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
   const int i = iw + (lane_id() & 31);
   const bool live = i < s.len;
 
+  const int rows = s.len - iw;  // of the wave's 32 queries
+  typedef WaveRows<T, DH, Tile> Rows;
+  Rows ql, dl, ol;
+  ql.load(a.q, s.begin + iw, h, rows, a.dim);
+  dl.load(a.dout, s.begin + iw, h, rows, a.dim);
+  ol.load(a.out, s.begin + iw, h, rows, a.dim);
   const KeyTiles<WAVES> tiles(a, i0, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
@@ -527,13 +603,14 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
   load(0, lds[0]);
   const typename Tile::Reads at;
 
+  const int part = WAVES == 1 ? 0 : threadIdx.x >> 7, first = WAVES == 1 ? 0 : 32 * (threadIdx.x >> 6 & 1);
   V8 q[DH / 16], d[DH / 16];
-  right_row<T, DH>(a.q, s.begin + i, h, live, a.dim, q);
-  right_row<T, DH>(a.dout, s.begin + i, h, live, a.dim, d);
+  ql.to_right(lds[G::kBuffers - 1][part], first, at, q);
+  dl.to_right(lds[G::kBuffers - 1][part], first, at, d);
   float delta = 0.f;
   {
     V8 out[DH / 16];
-    right_row<T, DH>(a.out, s.begin + i, h, live, a.dim, out);
+    ol.to_right(lds[G::kBuffers - 1][part], first, at, out);
 #pragma unroll
     for (int ks = 0; ks < DH / 16; ++ks)
 #pragma unroll
@@ -588,7 +665,8 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) at
     if (it + 1 < tiles.n) meet(it + 1, lds[G::kBuffers - 1], lds[0]);
   }
   uint32_t again = either(live && not_finite(dq));
-  if (live && !(again >> (lane_id() & 31) & 1)) store_row<T, DH>(a.dq, s.begin + i, h, a.dim, dq, a.scale);
+  __syncthreads();  // the tiles are done with
+  Rows::store(a.dq, s.begin + iw, h, rows, a.dim, lds[0][part], first, dq, a.scale, again);
   for (; again; again &= again - 1) again_dq<T>(a, s.begin, iw + __builtin_ctz(again), h, kh);
 }
 
@@ -692,6 +770,12 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
   const bool live = j < s.len;
   const uint32_t limit = j < a.sinks ? 0x7FFFFFFFu : (uint32_t)a.window;
 
+  const typename Tile::Reads at;
+  typedef WaveRows<T, DH, Tile> Rows;
+  // the wave's own part of LDS, before the steps and after them: where keys and values have their
+  // tiles, or half of a buffer of queries or gradients
+  char* const part = P::kWide ? (wave & 2 ? sh.v[0] : sh.k[0]) : (wave & 2 ? sh.d : sh.q)[G::kBuffers - 1];
+  const int first = WAVES == 1 ? 0 : 32 * (wave & 1);
   V8 k[P::kWide ? 1 : DH / 16], v[P::kWide ? 1 : DH / 16];
   if constexpr (P::kWide) {
     const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
@@ -705,14 +789,17 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
       vl.store(sh.v[x]);
     }
   } else {
-    right_row<T, DH>(a.k, s.begin + j, kh, live, a.dim, k);
-    right_row<T, DH>(a.v, s.begin + j, kh, live, a.dim, v);
+    // through the buffers that the first step does not use
+    Rows kl, vl;
+    kl.load(a.k, s.begin + jw, kh, s.len - jw, a.dim);
+    vl.load(a.v, s.begin + jw, kh, s.len - jw, a.dim);
+    kl.to_right(part, first, at, k);
+    vl.to_right(part, first, at, v);
   }
   const float c = a.scale * kLog2e;
 
   const int n_tiles = (row1 - row0 + kRows - 1) / kRows;
   Tile ql, dl;
-  const typename Tile::Reads at;
   float stat = 0.f;  // the first kRows threads: lse of a row; as many after them: its delta
   int next_h = kh * group, next_r0 = row0;  // what is loaded next
   auto load = [&](int b) {
@@ -821,13 +908,16 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
     const bool split = a.sinks > 0 && parts.reach < s.len;
     const EmbHeads row{split ? first_tile_part(a, parts, s, kh) : nullptr, 0, a.dim, 0};
     // one matrix after the other; the rows of each that are not finite
+    if (P::kShare == 1) __syncthreads();  // the tiles are done with; folding sees to it otherwise
     auto finish = [&](f32x16 (&x)[DH / 32], const EmbHeads& to, int row_at, float by) -> uint32_t {
       if constexpr (P::kShare == 2) fold_waves(x, fold, wave, 8);
-      const uint32_t bad = wave < 4 ? either(live && not_finite(x)) : 0;
-      if (wave < 4 && live && !(bad >> (lane_id() & 31) & 1)) {
-        if (!split || j >= a.sinks) store_row<T, DH>(to, s.begin + j, kh, a.dim, x, by);
-        else store_row<float, DH>(row, row_at + j, 0, a.dim, x, 1.f);
-      }
+      if (wave >= 4) return 0;
+      const uint32_t bad = either(live && not_finite(x));
+      // sinks of a sequence with chunks go to their sums
+      const uint32_t sums = split && jw == 0 ? (a.sinks == 32 ? ~0u : (1u << a.sinks) - 1) : 0;
+      if (sums >> (lane_id() & 31) & ~bad >> (lane_id() & 31) & 1)
+        store_row<float, DH>(row, row_at + j, 0, a.dim, x, 1.f);
+      Rows::store(to, s.begin + jw, kh, s.len - jw, a.dim, part, first, x, by, bad | sums);
       return bad;
     };
     const uint32_t bad_k = finish(dk, a.dk, 0, a.scale);
