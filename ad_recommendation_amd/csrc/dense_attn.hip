@@ -61,6 +61,15 @@ struct Seq {
   int len, tile;  // tokens; which tile of the sequence this workgroup has
   int index;
 };
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, int tile) {
+  Seq s;
+  s.index = b;
+  s.begin = min(max((int64_t)a.off[b], (int64_t)0), a.n_tok);
+  const int64_t end = min(max((int64_t)a.off[b + 1], s.begin), a.n_tok);
+  s.len = (int)(end - s.begin);
+  s.tile = tile;
+  return s;
+}
 // Tile slot s of a ragged batch, where sequence b's tiles start at slot first(begin, b): a function that
 // leaves each sequence room for its tiles without a pass over the lengths (begin / tile + b does: the
 // tiles of a length l that starts anywhere number at most l / tile + 1).  64 lanes look for the
@@ -78,11 +87,7 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, F first) {
     lo = __builtin_amdgcn_readfirstlane(lo);
     n = __builtin_amdgcn_readfirstlane(n);
   }
-  Seq s;
-  s.index = lo;
-  s.begin = min(max((int64_t)a.off[lo], (int64_t)0), a.n_tok);
-  const int64_t end = min(max((int64_t)a.off[lo + 1], s.begin), a.n_tok);
-  s.len = (int)(end - s.begin);
+  Seq s = sequence(a, lo, 0);
   s.tile = (int)max((int64_t)slot - (int64_t)first(s.begin, lo), (int64_t)-1);
   return s;
 }
@@ -153,7 +158,9 @@ struct RegisterTile {
 
 // Straight from memory to LDS, where heads have DH columns: a wave's load fills 1024 bytes in order, so a
 // row's pieces are exchanged by its number instead of set apart, by the address that a lane loads from.
-// The last row stands for those past it; no query sees them, and no row past `end` is read.
+// The last row stands for those past it; no query sees them, and no row past `end` is read.  Against
+// registers: no moves, no LDS writes, 32 registers fewer; forward of 16.4k tokens, 16 heads of 128,
+// window 1024: 193 -> 172 us.
 template <typename T, int DH, int ROWS, int THREADS>
 struct DirectTile {
   static constexpr int kPieces = DH / 8, kRow = DH * 2, kBytes = ROWS * kRow;
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
 // ---------------------------------------------------------------- backward: dq
 // As the forward, with dout as a second right operand; also writes delta.
 template <typename T, int DH, int WAVES, bool DIRECT>
-__global__ void __launch_bounds__(Group<WAVES>::kThreads, WAVES == 1 ? 3 : 2) attn_dq(AttnArgs a) {
+__global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a) {
   typedef typename Vec8<T>::t V8;
   typedef Group<WAVES> G;
   typedef TileOf<T, DH, G::kRows, G::kThreads, DIRECT> Tile;
@@ -689,8 +696,8 @@ __host__ __device__ inline int64_t reach_of(int window, int tokens) { return (in
 
 // Where partial sums of the sinks go, [2][sinks][dim] each: first those of the chunks by slot, then those
 // of the first key tiles.  Only sequences longer than reach have any; each is given a number, its own
-// or, where the batch has more sequences than could be that long, which part of reach + 1 tokens it
-// begins in.  A sequence's chunks start at slot begin / chunk + number, which leaves it room for
+// or, where the batch has over twice the sequences that could be that long, which part of reach + 1
+// tokens it begins in.  A sequence's chunks start at slot begin / chunk + number, which leaves it room for
 // len / chunk + 1 of them.
 struct SinkSlots {
   int64_t reach, numbers, chunk_slots;
@@ -699,8 +706,9 @@ struct SinkSlots {
   __host__ __device__ SinkSlots(int64_t n_tok, int64_t n_seq, int window, int tokens, int chunk_) {
     reach = reach_of(window, tokens);
     chunk = chunk_;
-    by_sequence = n_seq <= n_tok / (reach + 1);
-    numbers = by_sequence ? n_seq : n_tok / (reach + 1) + 1;
+    const int64_t most = n_tok / (reach + 1) + 1;
+    by_sequence = n_seq <= 2 * most;
+    numbers = by_sequence ? n_seq : most;
     chunk_slots = n_tok / chunk + numbers + 1;
   }
   // in 32 bits: tokens are fewer than 2^31, and reach + 1 at most 2^31 + 127
@@ -968,7 +976,9 @@ constexpr int kJoinEach = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int tokens, int chunk) {
   const SinkSlots parts(a.n_tok, a.n_seq, a.window, tokens, chunk);
-  const Seq s = find_tile(a, blockIdx.x, [&](int64_t t, int b) { return parts.number(t, b); });
+  const int number = blockIdx.x;
+  const Seq s = parts.by_sequence ? sequence(a, number, 0)
+                                  : find_tile(a, number, [&](int64_t t, int b) { return parts.number(t, b); });
   if (s.tile != 0 || s.len <= parts.reach) return;
   const int n = (int)((s.len - parts.reach + chunk - 1) / chunk);
   const int each = 2 * a.sinks * a.dim, all = each * a.kv_heads;
@@ -991,21 +1001,21 @@ __global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int token
 
 // ---------------------------------------------------------------- one new event
 // The keys that the newest event sees, in one row: the sinks outside the window, then the window.
-// A workgroup has a part of them for one key/value head; its waves take tiles of 32 in turn, each
-// with a softmax of its own, and meet in LDS at the end.  All query heads of the group are the
+// A workgroup has them, or a part, for one key/value head; its waves take tiles of 32 in turn, each with a
+// softmax of its own, and meet in LDS at the end.  All query heads of the group are the
 // columns of one product, so keys and values are read once.  Memory bound.
 template <int DH>
 struct WaveTile {  // 32 rows, of one wave
   static constexpr int kPieces = DH / 8, kRegs = 32 * kPieces / 64;
 };
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int splits) {
+template <typename T, int DH, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) attn_decode(AttnArgs a, int splits) {
   typedef typename Vec8<T>::t V8;
   typedef RegisterTile<T, DH, 32, 64> Tile;
   const typename Tile::Reads reads;
-  __shared__ __attribute__((aligned(16))) char lds[4][2][Tile::kBytes];
-  __shared__ float stats[4][2][32];
+  __shared__ __attribute__((aligned(16))) char lds[WAVES][2][Tile::kBytes];
+  __shared__ float stats[WAVES][2][32];
   const int group = a.q_heads / a.kv_heads;
   const int kh = blockIdx.x % a.kv_heads;
   int rest = blockIdx.x / a.kv_heads;
@@ -1051,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
   float m = -kInf, l = 0.f;
   int t0 = u0 + wave * 32;
   if (t0 < u1) load(t0);
-  for (; t0 < u1; t0 += 128) {
+  for (; t0 < u1; t0 += 32 * WAVES) {
 #pragma unroll
     for (int n = 0; n < WaveTile<DH>::kRegs; ++n) {
       const int idx = lane + n * 64;
@@ -1059,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
       *reinterpret_cast<u32x4*>(kt + at) = kr[n];
       *reinterpret_cast<u32x4*>(vt + at) = vr[n];
     }
-    if (t0 + 128 < u1) load(t0 + 128);
+    if (t0 + 32 * WAVES < u1) load(t0 + 32 * WAVES);
     // the tile is the wave's own: its LDS accesses are carried out in order
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -1116,11 +1126,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
     mine[x * 64 + lane] = f32x4{t[r], t[r + 1], t[r + 2], t[r + 3]};
   }
   __syncthreads();
-  float top = -kInf, sum = 0.f, by[4];
+  float top = -kInf, sum = 0.f, by[WAVES];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, stats[w][0][lane & 31]);
+  for (int w = 0; w < WAVES; ++w) top = fmaxf(top, stats[w][0][lane & 31]);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const float mw = stats[w][0][lane & 31];
     by[w] = mw == -kInf ? 0.f : exp2f((mw - top) * c);
     sum += stats[w][1][lane & 31] * by[w];
@@ -1130,12 +1140,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode(AttnArgs a, int split
   const int qh = kh * group + head;
   const int64_t row = (int64_t)split * total + (int64_t)sq * a.q_heads + qh;
 #pragma unroll
-  for (int y = 0; y < DH / 32; ++y) {
-    const int x = wave + 4 * y;  // which four rows
+  for (int x = wave; x < DH / 8; x += WAVES) {  // which four rows
     const int d = x * 8 + 4 * (lane >> 5);
     f32x4 t = {};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       const f32x4 ow = reinterpret_cast<const f32x4*>(lds[w])[x * 64 + lane];
       // a wave without keys has zeros, and so does its factor
 #pragma unroll
@@ -1198,8 +1207,6 @@ __global__ void __launch_bounds__(64) attn_decode_join(AttnArgs a, int splits) {
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int64_t kOneWave = 160;
-
 template <typename F>
 void by_shape(const AttnArgs& a, F f) {
   // the widths that kernels are built for; a head of another is padded with zeros in LDS
@@ -1220,7 +1227,12 @@ int sink_chunk(int64_t n_tok) {
   while (n_tok / c > 1024) c *= 2;
   return (int)c;
 }
-// Whether one wave a workgroup is the better shape: see the comment at its measurements below.
+// Whether one wave a workgroup is the better shape, by what most queries see: their window or, in short
+// sequences, what there is.  40k tokens, 8 heads of 64, fp16, four waves against one, forward / backward
+// us: 20 tokens a sequence 93 / 311 and 37 / 125; 74 tokens, window 64: 43 / 147 and 36 / 122; 400 tokens,
+// window 128: 49 / 168 and 43 / 150, 256: 50 / 176 and 53 / 166, 512: 50 / 168 and 56 / 174; 2000
+// tokens, 128: 45 / 155 and 46 / 162, 256: 55 / 186 and 63 / 205.
+constexpr int64_t kOneWave = 128;
 bool one_wave(const AttnArgs& a) {
   const int64_t mean = a.n_tok / a.n_seq;
   return a.dim <= 64 && std::min<int64_t>(mean, a.window) <= kOneWave;
@@ -1239,14 +1251,23 @@ AttnBwdPlan plan_attn_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok) {
   return p;
 }
 
-// Parts of a sequence's keys: where sequences and heads alone leave compute units idle, up to four
-// tiles (one a wave) each.
+// How a sequence's keys are shared out.  Many sequences and heads: a workgroup of four waves each.  Few:
+// one workgroup of as many waves as LDS has room for while that is two tiles a wave, or while there is
+// one for every other unit; more keys, parts of at least a tile to each of four waves, whose sums a
+// second kernel joins.  One sequence, 2 key/value heads of 64: 1024 keys 8.8 us in one workgroup, 8.6 in
+// parts; 512 keys 7.1 and 7.7; 4000 keys 18.9 and 14.8.  32 sequences, 8 heads of 128, 1024 keys: 24.6 and 29.5.
+constexpr int kOneGroupTiles = 2;
 AttnDecodePlan plan_attn_decode(const EmbAttn& a, int64_t n_seq, int64_t capacity) {
-  AttnDecodePlan p{};
+  AttnDecodePlan p{4, 1, 0};
   const int64_t keys = std::min<int64_t>(capacity, (int64_t)a.window + a.sinks);
   const int64_t group = a.q_heads / a.kv_heads, base = std::max<int64_t>(n_seq * a.kv_heads * ((group + 31) / 32), 1);
-  const int64_t most = std::max<int64_t>((keys + 127) / 128, 1);
-  p.splits = (int32_t)std::min<int64_t>(most, std::max<int64_t>(1024 / base, 1));
+  if (base >= 512 || keys <= 128) return p;
+  const int most = a.dim <= 64 ? 16 : 8;
+  if (base <= 256 && (base > 128 || keys <= 32 * most * kOneGroupTiles)) {
+    p.waves = most;
+    return p;
+  }
+  p.splits = (int32_t)std::min<int64_t>((keys + 127) / 128, 1024 / base);
   p.bytes = p.splits > 1 ? (size_t)p.splits * n_seq * a.q_heads * (a.dim + 2) * sizeof(float) : 0;
   return p;
 }
@@ -1312,13 +1333,19 @@ hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <typename T, int DH, int WAVES>
+void go_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStream_t st) {
+  const int64_t cols = (a.q_heads / a.kv_heads + 31) / 32;
+  hipLaunchKernelGGL((attn_decode<T, DH, WAVES>), dim3((unsigned)(a.n_seq * a.kv_heads * cols * p.splits)),
+                     dim3(64 * WAVES), 0, st, a, p.splits);
+}
+
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStream_t st) {
   by_shape(a, [&](auto t, auto d) {
     typedef decltype(t) T;
-    const int64_t cols = (a.q_heads / a.kv_heads + 31) / 32;
-    hipLaunchKernelGGL((attn_decode<T, decltype(d)::value>),
-                       dim3((unsigned)(a.n_seq * a.kv_heads * cols * p.splits)), dim3(kThreads), 0, st, a,
-                       p.splits);
+    constexpr int DH = decltype(d)::value, kMost = DH <= 64 ? 16 : 8;
+    if (p.waves == kMost) go_decode<T, DH, kMost>(a, p, st);
+    else go_decode<T, DH, 4>(a, p, st);
     if (p.splits > 1)
       hipLaunchKernelGGL((attn_decode_join<T>), dim3((unsigned)((int64_t)a.n_seq * a.q_heads)), dim3(64), 0,
                          st, a, p.splits);

@@ -27,6 +27,7 @@ struct AttnBwdPlan {
 };
 AttnBwdPlan plan_attn_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok);
 struct AttnDecodePlan {
+  int32_t waves;   // of a workgroup
   int32_t splits;  // of a sequence's visible keys
   size_t bytes;
 };

@@ -91,11 +91,9 @@ def _ptr(t, name: str, dtype=None, shape=None, optional: bool = False) -> Option
         if optional:
             return None
         raise TypeError(f"{name}: expected a tensor")
-    if not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor")
-    if not t.is_contiguous():
-        raise TypeError(f"{name}: expected a contiguous tensor")
-    if dtype is not None and t.dtype != dtype:
+    if not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous CUDA tensor")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -111,18 +109,19 @@ def _ws(ws):
 def _heads(t, name: str, dtype, shape) -> EmbHeads:
     """[tokens, heads, dim], or [sequences, tokens, heads, dim] of a cache: any strides but the
     last, which is 1."""
-    if not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dtype is not dtype or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
         raise ValueError(f"{name}: the last dimension's stride must be 1")
-    # the strides of dimensions of one element are never used: 0 passes the library's check of them
-    st = [s if n > 1 else 0 for s, n in zip(st, shape)]
-    return EmbHeads(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    if 1 in shape:
+        # the strides of dimensions of one element are never used: 0 passes the library's check of them
+        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
+    if len(st) == 3:
+        return EmbHeads(t.data_ptr(), 0, st[0], st[1])
+    return EmbHeads(t.data_ptr(), st[0], st[1], st[2])
 
 
 def _attn(q, kv_heads: int, window: int, sinks: int, scale: float) -> EmbAttn:
@@ -136,7 +135,8 @@ def _attn(q, kv_heads: int, window: int, sinks: int, scale: float) -> EmbAttn:
 def _kv_shape(q, k):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k: expected [tokens, heads, dim]")
-    return torch.Size((q.shape[0], k.shape[1], q.shape[2]))
+    n, _, d = q.shape
+    return n, k.shape[1], d
 
 
 def _offsets(offsets):
@@ -154,10 +154,10 @@ def attn_window_fwd(q, k, v, offsets, window: int, sinks: int, scale: float, out
     a = _attn(q, k.shape[1], window, sinks, scale)
     off, n_seq = _offsets(offsets)
     _check(lib().attn_window_fwd(
-        C.byref(a), C.byref(_heads(q, "q", t, q.shape)), C.byref(_heads(k, "k", t, kv)),
-        C.byref(_heads(v, "v", t, kv)), off, n_seq, q.shape[0],
-        C.byref(_heads(out, "out", t, q.shape)),
-        _ptr(lse, "lse", torch.float32, torch.Size((q.shape[1], q.shape[0])), optional=True),
+        a, _heads(q, "q", t, q.shape), _heads(k, "k", t, kv),
+        _heads(v, "v", t, kv), off, n_seq, q.shape[0],
+        _heads(out, "out", t, q.shape),
+        _ptr(lse, "lse", torch.float32, (q.shape[1], q.shape[0]), optional=True),
         _stream(stream)))
 
 
@@ -176,12 +176,12 @@ def attn_window_bwd(q, k, v, offsets, window: int, sinks: int, scale: float, out
     off, n_seq = _offsets(offsets)
     wp, wb = _ws(ws)
     _check(lib().attn_window_bwd(
-        C.byref(a), C.byref(_heads(q, "q", t, q.shape)), C.byref(_heads(k, "k", t, kv)),
-        C.byref(_heads(v, "v", t, kv)), off, n_seq, q.shape[0],
-        C.byref(_heads(out, "out", t, q.shape)),
-        _ptr(lse, "lse", torch.float32, torch.Size((q.shape[1], q.shape[0]))),
-        C.byref(_heads(dout, "dout", t, q.shape)), C.byref(_heads(dq, "dq", t, q.shape)),
-        C.byref(_heads(dk, "dk", t, kv)), C.byref(_heads(dv, "dv", t, kv)), wp, wb,
+        a, _heads(q, "q", t, q.shape), _heads(k, "k", t, kv),
+        _heads(v, "v", t, kv), off, n_seq, q.shape[0],
+        _heads(out, "out", t, q.shape),
+        _ptr(lse, "lse", torch.float32, (q.shape[1], q.shape[0])),
+        _heads(dout, "dout", t, q.shape), _heads(dq, "dq", t, q.shape),
+        _heads(dk, "dk", t, kv), _heads(dv, "dv", t, kv), wp, wb,
         _stream(stream)))
 
 
@@ -200,13 +200,13 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
         raise ValueError("expected q [sequences, heads, dim], k_cache [sequences, capacity, heads, dim]")
     t, (n, cap, kv_heads, _) = q.dtype, k_cache.shape
     a = _attn(q, kv_heads, window, sinks, scale)
-    cache = torch.Size((q.shape[0], cap, kv_heads, q.shape[2]))
+    cache = (q.shape[0], cap, kv_heads, q.shape[2])
     wp, wb = _ws(ws)
     _check(lib().attn_window_decode(
-        C.byref(a), C.byref(_heads(q, "q", t, q.shape)),
-        C.byref(_heads(k_cache, "k_cache", t, cache)), C.byref(_heads(v_cache, "v_cache", t, cache)),
-        _ptr(lens, "lens", torch.int32, torch.Size((q.shape[0],))), q.shape[0], cap,
-        C.byref(_heads(out, "out", t, q.shape)), wp, wb, _stream(stream)))
+        a, _heads(q, "q", t, q.shape),
+        _heads(k_cache, "k_cache", t, cache), _heads(v_cache, "v_cache", t, cache),
+        _ptr(lens, "lens", torch.int32, (q.shape[0],)), q.shape[0], cap,
+        _heads(out, "out", t, q.shape), wp, wb, _stream(stream)))
 
 
 # ------------------------------------------------------------------ norms
@@ -221,7 +221,7 @@ def _rows(t):
         raise ValueError("expected rows [rows, dim]")
     if t.dtype not in _DTYPE:
         raise TypeError(f"expected float32, float16 or bfloat16, got {t.dtype}")
-    return t.dtype, t.shape, torch.Size((t.shape[1],))
+    return t.dtype, t.shape, (t.shape[1],)
 
 
 def norm_gate_residual_fwd(x, y, gate, w_post, w_pre, alpha: float, eps: float, r, h, stream=None):
@@ -319,7 +319,7 @@ def adamw_step(weights, grads, m, v, step: int, lr: float, beta1: float, beta2: 
 def _codes(t, name: str, n: int):
     if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError(f"{name}: expected uint8 or float8_e4m3fn, got {t.dtype}")
-    return _ptr(t, name, shape=torch.Size((n,)))
+    return _ptr(t, name, shape=(n,))
 
 
 def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta1: float,
@@ -331,7 +331,7 @@ def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta
     args, wd = _adamw_args(weights, grads, copies, weight_decay)
     _scalar(grad_scale)
     n = m.numel()
-    e = torch.Size((n // ADAMW_BLOCK,))
+    e = (n // ADAMW_BLOCK,)
     _check(lib().adamw_step_q8(
         *args, _codes(m, "m", n), _ptr(m_exp, "m_exp", torch.uint8, e), _codes(v, "v", n),
         _ptr(v_exp, "v_exp", torch.uint8, e), n, int(step), lr, beta1, beta2, eps, wd,
@@ -345,5 +345,5 @@ def adamw_q8_values(codes, exp, out, stream=None):
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
     _check(lib().adamw_q8_values(
-        _codes(codes, "codes", n), _ptr(exp, "exp", torch.uint8, torch.Size((n // ADAMW_BLOCK,))), n,
-        _ptr(out, "out", shape=torch.Size((n,))), _DTYPE[out.dtype], _stream(stream)))
+        _codes(codes, "codes", n), _ptr(exp, "exp", torch.uint8, (n // ADAMW_BLOCK,)), n,
+        _ptr(out, "out", shape=(n,)), _DTYPE[out.dtype], _stream(stream)))
