@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a)
 constexpr int kSinkKeys = EMB_ATTN_MAX_SINKS;
 
 // Queries from here on see nothing of the first key tile but the sinks.
-__host__ __device__ inline int64_t reach_of(int window, int tokens) { return (int64_t)tokens + window - 1; }
+inline int64_t reach_of(int window, int tokens) { return (int64_t)tokens + window - 1; }
 
 // Where partial sums of the sinks go, [2][sinks][dim] each: first those of the chunks by slot, then those
 // of the first key tiles.  Only sequences longer than reach have any; each is given a number, its own
@@ -703,7 +703,7 @@ struct SinkSlots {
   int64_t reach, numbers, chunk_slots;
   int chunk;
   bool by_sequence;
-  __host__ __device__ SinkSlots(int64_t n_tok, int64_t n_seq, int window, int tokens, int chunk_) {
+  SinkSlots(int64_t n_tok, int64_t n_seq, int window, int tokens, int chunk_) {
     reach = reach_of(window, tokens);
     chunk = chunk_;
     const int64_t most = n_tok / (reach + 1) + 1;
@@ -712,10 +712,10 @@ struct SinkSlots {
     chunk_slots = n_tok / chunk + numbers + 1;
   }
   // in 32 bits: tokens are fewer than 2^31, and reach + 1 at most 2^31 + 127
-  __host__ __device__ int64_t number(int64_t begin, int b) const {
+  __device__ int64_t number(int64_t begin, int b) const {
     return by_sequence ? b : (uint32_t)begin / (uint32_t)(reach + 1);
   }
-  __host__ __device__ int64_t first(int64_t begin, int b) const {
+  __device__ int64_t first(int64_t begin, int b) const {
     return (uint32_t)begin / (uint32_t)chunk + number(begin, b);
   }
 };
@@ -950,18 +950,17 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
 
 template <typename T, int DH, int WAVES, bool DIRECT>
 __global__ void __launch_bounds__((DkvShape<T, DH, WAVES, DIRECT>::kBlock), 2)
-    attn_dkv(AttnArgs a, int main_blocks, int chunk) {
+    attn_dkv(AttnArgs a, int main_blocks, SinkSlots parts) {
   __shared__ __attribute__((aligned(1024))) DkvShared<T, DH, WAVES, DIRECT> sh;
   constexpr int kTokens = Group<WAVES>::kTokens;
   const bool sink = (int)blockIdx.x >= main_blocks;  // the same for the whole workgroup
   const int block = sink ? blockIdx.x - main_blocks : blockIdx.x;
   const int kh = block % a.kv_heads, slot = block / a.kv_heads;
-  const SinkSlots parts(a.n_tok, a.n_seq, a.window, kTokens, chunk);
   if (sink) {
     const Seq s = find_tile(a, slot, [&](int64_t t, int b) { return parts.first(t, b); });
-    const int64_t r0 = parts.reach + (int64_t)s.tile * chunk;
+    const int64_t r0 = parts.reach + (int64_t)s.tile * parts.chunk;
     if (s.tile < 0 || r0 >= s.len) return;
-    dkv<T, DH, WAVES, DIRECT, true>(a, sh, parts, s, kh, 0, (int)r0, (int)min(r0 + chunk, (int64_t)s.len), slot);
+    dkv<T, DH, WAVES, DIRECT, true>(a, sh, parts, s, kh, 0, (int)r0, (int)min(r0 + parts.chunk, (int64_t)s.len), slot);
   } else {
     const Seq s = find_tile(a, slot, [](int64_t t, int b) { return t / kTokens + b; });
     if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
@@ -974,28 +973,33 @@ __global__ void __launch_bounds__((DkvShape<T, DH, WAVES, DIRECT>::kBlock), 2)
 // elements a thread, a number (see SinkSlots) a row of workgroups.
 constexpr int kJoinEach = 4;
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, int tokens, int chunk) {
-  const SinkSlots parts(a.n_tok, a.n_seq, a.window, tokens, chunk);
+__global__ void __launch_bounds__(kThreads) attn_sink_join(AttnArgs a, SinkSlots parts) {
   const int number = blockIdx.x;
   const Seq s = parts.by_sequence ? sequence(a, number, 0)
                                   : find_tile(a, number, [&](int64_t t, int b) { return parts.number(t, b); });
   if (s.tile != 0 || s.len <= parts.reach) return;
-  const int n = (int)((s.len - parts.reach + chunk - 1) / chunk);
+  const int n = (int)((uint32_t)(s.len - (int)parts.reach + parts.chunk - 1) / (uint32_t)parts.chunk);
   const int each = 2 * a.sinks * a.dim, all = each * a.kv_heads;
   const float* tile = first_tile_part(a, parts, s, 0);
   const float* part = sink_part(a, parts.first(s.begin, s.index), 0);
+  const int at0 = blockIdx.y * kJoinEach * kThreads + threadIdx.x;
+  float t[kJoinEach];
+#pragma unroll
+  for (int k = 0; k < kJoinEach; ++k) t[k] = tile[min(at0 + k * kThreads, all - 1)];
+#pragma unroll 2
+  for (int x = 0; x < n; ++x) {
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) t[k] += part[(int64_t)x * all + min(at0 + k * kThreads, all - 1)];
+  }
 #pragma unroll
   for (int k = 0; k < kJoinEach; ++k) {
-    const int at = (blockIdx.y * kJoinEach + k) * kThreads + threadIdx.x;
+    const int at = at0 + k * kThreads;
     if (at >= all) return;
-    float t = tile[at];
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) t += part[(int64_t)x * all + at];
     const int kh = at / each, e = at % each;
     const int row = e / a.dim % a.sinks, col = e % a.dim;
     const bool is_v = e >= a.sinks * a.dim;
     const EmbHeads& to = is_v ? a.dv : a.dk;
-    static_cast<T*>(to.p)[(s.begin + row) * to.tok + kh * to.head + col] = (T)(is_v ? t : t * a.scale);
+    static_cast<T*>(to.p)[(s.begin + row) * to.tok + kh * to.head + col] = (T)(is_v ? t[k] : t[k] * a.scale);
   }
 }
 
@@ -1285,18 +1289,17 @@ void go_bwd(const AttnArgs& a, hipStream_t st) {
   const int64_t slots = a.n_tok / G::kTokens + a.n_seq;
   hipLaunchKernelGGL((attn_dq<T, DH, WAVES, DIRECT>), dim3((unsigned)(slots * a.q_heads)), dim3(G::kThreads), 0,
                      st, a);
-  const int chunk = sink_chunk(a.n_tok);
-  const SinkSlots n(a.n_tok, a.n_seq, a.window, G::kTokens, chunk);
+  const SinkSlots n(a.n_tok, a.n_seq, a.window, G::kTokens, sink_chunk(a.n_tok));
   const bool sinks = a.sinks > 0 && a.n_tok > n.reach;  // a sequence may be longer than reach
   hipLaunchKernelGGL((attn_dkv<T, DH, WAVES, DIRECT>),
                      dim3((unsigned)((slots + (sinks ? n.chunk_slots : 0)) * a.kv_heads)),
-                     dim3(DkvShape<T, DH, WAVES, DIRECT>::kBlock), 0, st, a, (int)(slots * a.kv_heads), chunk);
+                     dim3(DkvShape<T, DH, WAVES, DIRECT>::kBlock), 0, st, a, (int)(slots * a.kv_heads), n);
   if (sinks)
     hipLaunchKernelGGL((attn_sink_join<T>),
                        dim3((unsigned)n.numbers,
                             (unsigned)((2 * a.sinks * a.dim * a.kv_heads + kThreads * kJoinEach - 1) /
                                        (kThreads * kJoinEach))),
-                       dim3(kThreads), 0, st, a, G::kTokens, chunk);
+                       dim3(kThreads), 0, st, a, n);
 }
 
 // Whether tiles may be loaded straight to LDS: whole rows of the kernel's width, and a tile's rows
