@@ -1,6 +1,7 @@
 """AdamW over many tensors against the formula in 64 bits, and its 8-bit states bit by bit against
 the oracle's codes: every type, sizes around blocks and chunks, tensors aligned to their elements
 alone, more tensors than one launch takes."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -127,6 +128,20 @@ def test_more_tensors_than_one_launch_takes(q8):
               E * y.double().abs() + 1e-3 * 32 * E, "weights")
 
 
+def test_more_data_than_the_caches_hold():
+    """Over 256 MB the kernels pass the caches by; every element is as in smaller calls, bit by bit."""
+    n, half = 10_000_128, 5_000_064
+    w, g, m, v = (tensors([n], F32, s)[0] for s in (1, 2, 3, 4))
+    v.abs_()
+    whole = [x.clone() for x in (w, m, v)]
+    dense.adamw_step([whole[0]], [g], whole[1], whole[2], *args(), 0.1)
+    parts = [x.clone() for x in (w, m, v)]
+    for a in (0, half):
+        x = [p[a:a + half] for p in parts]
+        dense.adamw_step([x[0]], [g[a:a + half]], x[1], x[2], *args(), 0.1)
+    assert all(torch.equal(a, b) for a, b in zip(whole, parts))
+
+
 # ---------------------------------------------------------------------------------- 8 bits
 def q8_state(x):
     """Codes and exponents nearest to x, by the oracle."""
@@ -136,12 +151,13 @@ def q8_state(x):
 
 
 @pytest.mark.parametrize("grad", [F32, BF16], ids=str)
-@pytest.mark.parametrize("seed", [0, 12345, (7 << 32) + 3, 2 ** 64 - 1])
-def test_codes_bit_by_bit(seed, grad):
-    at, total = starts(SIZES)
-    w, g = tensors(SIZES, F32, 8), tensors(SIZES, grad, 9, 0.1)
+@pytest.mark.parametrize("seed,sizes", [(0, SIZES), (12345, SIZES), ((7 << 32) + 3, SIZES), (2 ** 64 - 1, SIZES),
+                                        (5, [17_000_001, 3])], ids=["0", "small", "high", "all", "past_caches"])
+def test_codes_bit_by_bit(seed, sizes, grad):
+    at, total = starts(sizes)
+    w, g = tensors(sizes, F32, 8), tensors(sizes, grad, 9, 0.1)
     inside = torch.zeros(total, device="cuda")
-    for a, n in zip(at, SIZES):
+    for a, n in zip(at, sizes):
         inside[a:a + n] = 1
     gen = torch.Generator(device="cuda").manual_seed(10)
     spread = torch.exp(3 * torch.randn(total, generator=gen, device="cuda"))  # values far apart in a block
@@ -151,12 +167,12 @@ def test_codes_bit_by_bit(seed, grad):
     w0 = [x.clone() for x in w]
     dense.adamw_step_q8(w, g, m, me, v, ve, *args(5), 0.01, seed=seed)
     flat = torch.zeros(total, device="cuda")
-    for a, n, x in zip(at, SIZES, g):
+    for a, n, x in zip(at, sizes, g):
         flat[a:a + n] = x.float()
     # the formula's products and sums one by one in fp32
     m1 = old[0] * 0.9 + flat * (1 - 0.9)
     v1 = old[1] * old[1] * 0.99 + flat * flat * (1 - 0.99)
-    root = v1.cpu().sqrt().cuda()
+    root = torch.from_numpy(np.sqrt(v1.cpu().numpy())).cuda()  # torch's on the CPU is not always the nearest
     bits = O.hash_bits(seed, torch.arange(total, device="cuda"))
     for codes, exp, x, b, keep in ((m, me, m1, bits & 0xFFFF, False), (v, ve, root, bits >> 16, True)):
         want, k = O.to_codes(x, b, keep)
@@ -167,7 +183,7 @@ def test_codes_bit_by_bit(seed, grad):
         half = torch.empty(total, dtype=BF16, device="cuda")
         dense.adamw_q8_values(codes, exp, half)
         assert torch.equal(half.float(), got)
-    for i, n in enumerate(SIZES):
+    for i, n in enumerate(sizes):
         a = at[i]
         check_weights(w[i], w0[i], None, m1[a:a + n], v1[a:a + n], 5, 0.01, HYPER)
 

@@ -53,6 +53,10 @@ SHAPES = [
     ([1400, 700], 2, 2, 128, 129, 1),
     ([400, 129, 64], 2, 2, 24, BIG, 5),
     ([513, 640], 3, 1, 104, 512, 0),
+    ([700, 300], 4, 2, 32, 300, 3),
+    ([1500, 0, 220], 4, 2, 64, 200, 7),
+    ([650], 2, 1, 48, 200, 32),
+    ([900, 100], 2, 2, 32, 150, 32),
     ([0, 0], 2, 2, 32, 4, 2),
     ([5] * 70 + [0] * 70 + [40] * 70, 2, 1, 32, 7, 2),
 ]
@@ -84,6 +88,34 @@ def test_forward_and_backward(lens, hq, hk, d, window, sinks, dtype):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
     for g, again in zip(got, bwd(q, k, v, off, window, sinks, scale, out, lse, dout)):
         assert torch.equal(g, again)
+
+
+@pytest.mark.parametrize("d,window", [(32, 40), (64, BIG), (128, 2)])
+def test_tokens_far_apart(d, window):
+    """Strides over which a tile of rows spans more than 2^31 bytes, and orders of heads and tokens."""
+    n = 300
+    off = offsets([n])
+    big = torch.empty(n, (1 << 23) + 8, dtype=F16, device="cuda")
+    q, k, v, dout = (big[:, 1024 * x:1024 * x + 2 * d].unflatten(1, (2, d)) for x in range(4))
+    dense_of = [rand(n, 2, d, dtype=F16, seed=x) for x in range(4)]
+    for t, x in zip((q, k, v, dout), dense_of):
+        t.copy_(x)
+
+    def run(q, k, v, dout):
+        out, lse = torch.empty(n, 2, d, dtype=F16, device="cuda"), torch.empty(2, n, device="cuda")
+        dense.attn_window_fwd(q, k, v, off, window, 3, 0.1, out, lse)
+        return [out, lse, *bwd(q, k, v, off, window, 3, 0.1, out, lse, dout)]
+    got, want = run(q, k, v, dout), run(*dense_of)
+    del big, q, k, v, dout
+    o, l, bo, bl = O.attn_fwd(*dense_of[:3], off, window, 3, 0.1)
+    within(got[0], o, bo, "out")
+    grads = O.attn_bwd(*dense_of[:3], off, window, 3, 0.1, want[0], want[1], dense_of[3])
+    for g, w, b in zip(got[2:], grads[:3], grads[3:]):
+        within(g, w, 3 * b, "gradient")  # from another rounding of out
+    # heads before tokens
+    heads_first = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in dense_of]
+    assert heads_first[0].stride() == (d, n * d, 1)
+    assert all(torch.equal(a, b) for a, b in zip(run(*heads_first), want))
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2])

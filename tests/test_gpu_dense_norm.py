@@ -138,6 +138,27 @@ def test_a_training_batch_of_rows(dtype):
     check_bwd(t)
 
 
+def test_more_data_than_the_caches_hold():
+    """Over 256 MB the kernels pass the caches by; every row is as in smaller calls, bit by bit."""
+    rows, dim, part = 36000, 1001, 9000
+    t = make(rows, dim, BF16, "vec", seed=2)
+    r, h = torch.empty_like(t["x"]), torch.empty_like(t["x"])
+    dense.norm_gate_residual_fwd(t["x"], t["y"], t["gate"], t["w_post"], t["w_pre"], 0.8, 1e-6, r, h)
+    res = run_bwd(t, 0.8, 1e-6)
+    sums = {k: 0.0 for k in ("dw_post", "dw_pre", "dgate")}
+    for a in range(0, rows, part):
+        p = {k: v[a:a + part] if v is not None and v.dim() == 2 else v for k, v in t.items()}
+        r2, h2 = torch.empty_like(p["x"]), torch.empty_like(p["x"])
+        dense.norm_gate_residual_fwd(p["x"], p["y"], p["gate"], p["w_post"], p["w_pre"], 0.8, 1e-6, r2, h2)
+        assert torch.equal(r2, r[a:a + part]) and torch.equal(h2, h[a:a + part])
+        res2 = run_bwd(p, 0.8, 1e-6)
+        assert torch.equal(res2["dx"], res["dx"][a:a + part]) and torch.equal(res2["dy"], res["dy"][a:a + part])
+        sums = {k: s + res2[k].double() for k, s in sums.items()}
+    # column sums of 36000 terms, each about one: additions in a block and of the blocks
+    for k, s in sums.items():
+        assert ((res[k].double() - s).abs() <= 2 * (rows / 768 + 128) * E * rows * 4).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, F16], ids=str)
 @pytest.mark.parametrize("offset", [1, 3])
 def test_rows_aligned_to_their_elements_alone(offset, dtype):
