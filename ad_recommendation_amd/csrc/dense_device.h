@@ -26,68 +26,56 @@ template <> struct Vec8<float> { typedef f32x8 t; };
 template <> struct Vec8<_Float16> { typedef f16x8 t; };
 template <> struct Vec8<__bf16> { typedef bf16x8 t; };
 
-// Eight elements at p as they are.  `n` of them exist; the others are zero and are not read.  p need
-// only be aligned to its elements: global memory takes 16-byte accesses at any address.
+template <typename T, int N> using Vec = T __attribute__((ext_vector_type(N)));
+
+// N elements at p as they are.  `n` of them exist; the others are zero and are not read.  p need only be
+// aligned to its elements: global memory takes 16-byte accesses at any address.
 // ONCE: what nothing reads again soon, and what the caches need not keep (a nontemporal access).
-template <typename T, bool ONCE = false>
-__device__ __forceinline__ typename Vec8<T>::t load8(const T* p, int n) {
-  typedef typename Vec8<T>::t V;
+template <int N, typename T, bool ONCE = false>
+__device__ __forceinline__ Vec<T, N> load_vec(const T* p, int n) {
+  typedef Vec<T, N> V;
   typedef V U __attribute__((aligned(sizeof(T))));
-  if (n >= 8) {
+  if (n >= N) {
     if (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const U*>(p));
     return *reinterpret_cast<const U*>(p);
   }
   V v = {};
 #pragma unroll
-  for (int i = 0; i < 7; ++i)
+  for (int i = 0; i < N - 1; ++i)
     if (i < n) v[i] = p[i];
   return v;
 }
-
-// Rounds eight values to T (nearest even) and writes the first n.
-template <typename T, bool ONCE = false>
-__device__ __forceinline__ void store8(T* p, f32x8 x, int n) {
-  typedef typename Vec8<T>::t V;
+// Rounds N values to T (nearest even) and writes the first n.
+template <int N, typename T, bool ONCE = false>
+__device__ __forceinline__ void store_vec(T* p, Vec<float, N> x, int n) {
+  typedef Vec<T, N> V;
   typedef V U __attribute__((aligned(sizeof(T))));
   const V v = __builtin_convertvector(x, V);
-  if (n >= 8) {
+  if (n >= N) {
     if (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<U*>(p));
     else *reinterpret_cast<U*>(p) = v;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 7; ++i)
+  for (int i = 0; i < N - 1; ++i)
     if (i < n) p[i] = v[i];
 }
+template <typename T, bool ONCE = false>
+__device__ __forceinline__ typename Vec8<T>::t load8(const T* p, int n) {
+  return load_vec<8, T, ONCE>(p, n);
+}
+template <typename T, bool ONCE = false>
+__device__ __forceinline__ void store8(T* p, f32x8 x, int n) {
+  store_vec<8, T, ONCE>(p, x, n);
+}
 
-// Four elements, likewise.
 template <typename T, bool ONCE>
 __device__ __forceinline__ f32x4 load4(const T* p, int n) {
-  typedef T V __attribute__((ext_vector_type(4)));
-  typedef V U __attribute__((aligned(sizeof(T))));
-  if (n >= 4) {
-    if (ONCE) return __builtin_convertvector(__builtin_nontemporal_load(reinterpret_cast<const U*>(p)), f32x4);
-    return __builtin_convertvector(*reinterpret_cast<const U*>(p), f32x4);
-  }
-  f32x4 v = {};
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i < n) v[i] = (float)p[i];
-  return v;
+  return __builtin_convertvector((load_vec<4, T, ONCE>(p, n)), f32x4);
 }
 template <typename T, bool ONCE>
 __device__ __forceinline__ void store4(T* p, f32x4 x, int n) {
-  typedef T V __attribute__((ext_vector_type(4)));
-  typedef V U __attribute__((aligned(sizeof(T))));
-  const V v = __builtin_convertvector(x, V);
-  if (n >= 4) {
-    if (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<U*>(p));
-    else *reinterpret_cast<U*>(p) = v;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i < n) p[i] = v[i];
+  store_vec<4, T, ONCE>(p, x, n);
 }
 
 template <typename V>

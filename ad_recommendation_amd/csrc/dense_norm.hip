@@ -47,11 +47,21 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float (*lds)[kThreads / 
   }
 }
 
-// TPR threads take a row, each NC vectors of eight columns.
+// Columns of a vector: 16 bytes of the rows' type, so that neighbouring threads read neighbouring 16 bytes.
+template <typename T> constexpr int kVec = 16 / sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ Vec<float, kVec<T>> wide(Vec<T, kVec<T>> v) {
+  return __builtin_convertvector(v, Vec<float, kVec<T>>);
+}
+
+// TPR threads take a row, each NC vectors of kVec columns.
 template <typename T, int TPR, int NC, bool ONCE>
 __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
   __shared__ float lds[2][kThreads / 64][1];
-  constexpr int kRows = kThreads / TPR;
+  constexpr int kRows = kThreads / TPR, W = kVec<T>;
+  typedef Vec<T, W> V;
+  typedef Vec<float, W> F;
   const int lane = threadIdx.x % TPR;
   const int D = a.dim;
   const T* x = static_cast<const T*>(a.x);
@@ -62,18 +72,18 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
   const float inv_d = 1.f / (float)D;
 
   // what all rows share: the weights after the block times a gate vector, the weights before
-  f32x8 wg[NC], wp[NC];
+  F wg[NC], wp[NC];
   int n[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + lane) * 8;
+    const int col = (c * TPR + lane) * W;
     n[c] = D - col;
-    wg[c] = f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    wg[c] = F(1.f);
     wp[c] = wg[c];
     if (n[c] > 0) {
-      if (a.w_post) wg[c] = load8(a.w_post + col, n[c]);
-      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= widen(load8(gate + col, n[c]));
-      if (a.w_pre) wp[c] = load8(a.w_pre + col, n[c]);
+      if (a.w_post) wg[c] = load_vec<W>(a.w_post + col, n[c]);
+      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= wide<T>(load_vec<W>(gate + col, n[c]));
+      if (a.w_pre) wp[c] = load_vec<W>(a.w_pre + col, n[c]);
     }
   }
   const int64_t stride = (int64_t)gridDim.x * kRows;
@@ -84,17 +94,17 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
     const int64_t row = base + threadIdx.x / TPR;
     const bool live = row < a.rows;
     const int64_t at = row * D;
-    typename Vec8<T>::t xr[NC], yr[NC], gr[NC];
+    V xr[NC], yr[NC], gr[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + lane) * 8;
-      xr[c] = typename Vec8<T>::t{};
+      const int col = (c * TPR + lane) * W;
+      xr[c] = V{};
       yr[c] = xr[c];
       gr[c] = xr[c];
       if (live && n[c] > 0) {
-        xr[c] = load8<T, ONCE>(x + at + col, n[c]);
-        if (y) yr[c] = load8<T, ONCE>(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, ONCE>(gate + at + col, n[c]);
+        xr[c] = load_vec<W, T, ONCE>(x + at + col, n[c]);
+        if (y) yr[c] = load_vec<W, T, ONCE>(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load_vec<W, T, ONCE>(gate + at + col, n[c]);
       }
     }
     float inv_y = 1.f;
@@ -102,31 +112,31 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
       float s[1] = {0.f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const f32x8 v = widen(yr[c]);
+        const F v = wide<T>(yr[c]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += v[i] * v[i];
+        for (int i = 0; i < W; ++i) s[0] += v[i] * v[i];
       }
       row_sums<TPR, 1>(s, lds, turn);
       turn ^= 1;
       inv_y = rsqrtf(s[0] * inv_d + a.eps);
     }
-    f32x8 rr[NC];
+    F rr[NC];
     float s[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      rr[c] = a.alpha * widen(xr[c]);
+      rr[c] = a.alpha * wide<T>(xr[c]);
       if (y) {
-        f32x8 v = widen(yr[c]) * inv_y * wg[c];
-        if (a.gate_kind == EMB_GATE_ROWS) v *= widen(gr[c]);
+        F v = wide<T>(yr[c]) * inv_y * wg[c];
+        if (a.gate_kind == EMB_GATE_ROWS) v *= wide<T>(gr[c]);
         rr[c] += v;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += rr[c][i] * rr[c][i];
+      for (int i = 0; i < W; ++i) s[0] += rr[c][i] * rr[c][i];
     }
     if (r && live) {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (n[c] > 0) store8<T, ONCE>(r + at + (c * TPR + lane) * 8, rr[c], n[c]);
+        if (n[c] > 0) store_vec<W, T, ONCE>(r + at + (c * TPR + lane) * W, rr[c], n[c]);
     }
     if (h) {
       row_sums<TPR, 1>(s, lds, turn);
@@ -134,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
       const float inv_r = rsqrtf(s[0] * inv_d + a.eps);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (live && n[c] > 0) store8<T, ONCE>(h + at + (c * TPR + lane) * 8, rr[c] * inv_r * wp[c], n[c]);
+        if (live && n[c] > 0) store_vec<W, T, ONCE>(h + at + (c * TPR + lane) * W, rr[c] * inv_r * wp[c], n[c]);
     }
   }
 }
@@ -143,10 +153,12 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
 // registers, the block's rows then meet in LDS, and the blocks in norm_join.
 template <typename T, int TPR, int NC, bool ONCE>
 __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
-  constexpr int kRows = kThreads / TPR;
+  constexpr int kRows = kThreads / TPR, W = kVec<T>;
+  typedef Vec<T, W> V;
+  typedef Vec<float, W> F;
   constexpr int kSums = 6;
   __shared__ float lds[2][kThreads / 64][kSums];
-  __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * 8 : 1];
+  __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * W : 1];
   const int lane = threadIdx.x % TPR;
   const int D = a.dim;
   const T* r = static_cast<const T*>(a.r_in);
@@ -160,20 +172,20 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   const float inv_d = 1.f / (float)D;
   const bool pre = a.w_pre != nullptr;
 
-  f32x8 wg[NC], wp[NC], c_post[NC], c_pre[NC];
+  F wg[NC], wp[NC], c_post[NC], c_pre[NC];
   int n[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + lane) * 8;
+    const int col = (c * TPR + lane) * W;
     n[c] = D - col;
-    wg[c] = f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    wg[c] = F(1.f);
     wp[c] = wg[c];
-    c_post[c] = f32x8{};
-    c_pre[c] = f32x8{};
+    c_post[c] = F{};
+    c_pre[c] = F{};
     if (n[c] > 0) {
-      if (a.w_post) wg[c] = load8(a.w_post + col, n[c]);
-      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= widen(load8(gate + col, n[c]));
-      if (pre) wp[c] = load8(a.w_pre + col, n[c]);
+      if (a.w_post) wg[c] = load_vec<W>(a.w_post + col, n[c]);
+      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= wide<T>(load_vec<W>(gate + col, n[c]));
+      if (pre) wp[c] = load_vec<W>(a.w_pre + col, n[c]);
     }
   }
   int turn = 0;
@@ -181,34 +193,34 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
     const int64_t row = base + threadIdx.x / TPR;
     const bool live = row < a.rows;
     const int64_t at = row * D;
-    typename Vec8<T>::t rr[NC], yr[NC], gr[NC], drr[NC], dhr[NC];
+    V rr[NC], yr[NC], gr[NC], drr[NC], dhr[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + lane) * 8;
-      rr[c] = typename Vec8<T>::t{};
+      const int col = (c * TPR + lane) * W;
+      rr[c] = V{};
       yr[c] = rr[c];
       gr[c] = rr[c];
       drr[c] = rr[c];
       dhr[c] = rr[c];
       if (live && n[c] > 0) {
         if (pre) {
-          rr[c] = load8<T, ONCE>(r + at + col, n[c]);
-          dhr[c] = load8<T, ONCE>(dh + at + col, n[c]);
+          rr[c] = load_vec<W, T, ONCE>(r + at + col, n[c]);
+          dhr[c] = load_vec<W, T, ONCE>(dh + at + col, n[c]);
         }
-        if (dr) drr[c] = load8<T, ONCE>(dr + at + col, n[c]);
-        if (y) yr[c] = load8<T, ONCE>(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load8<T, ONCE>(gate + at + col, n[c]);
+        if (dr) drr[c] = load_vec<W, T, ONCE>(dr + at + col, n[c]);
+        if (y) yr[c] = load_vec<W, T, ONCE>(y + at + col, n[c]);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load_vec<W, T, ONCE>(gate + at + col, n[c]);
       }
     }
     // r^2, u r, y^2, a dr, a u, a r
     float s[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const f32x8 rv = widen(rr[c]), u = widen(dhr[c]) * wp[c], yv = widen(yr[c]), dv = widen(drr[c]);
-      f32x8 av = yv * wg[c];
-      if (a.gate_kind == EMB_GATE_ROWS) av *= widen(gr[c]);
+      const F rv = wide<T>(rr[c]), u = wide<T>(dhr[c]) * wp[c], yv = wide<T>(yr[c]), dv = wide<T>(drr[c]);
+      F av = yv * wg[c];
+      if (a.gate_kind == EMB_GATE_ROWS) av *= wide<T>(gr[c]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < W; ++i) {
         s[0] += rv[i] * rv[i];
         s[1] += u[i] * rv[i];
         s[2] += yv[i] * yv[i];
@@ -229,25 +241,25 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (n[c] <= 0) continue;
-      const int col = (c * TPR + lane) * 8;
-      const f32x8 rv = widen(rr[c]), dhv = widen(dhr[c]), yv = widen(yr[c]);
-      const f32x8 dR = widen(drr[c]) + inv_r * (dhv * wp[c]) - back_r * rv;
-      f32x8 z = dR * wg[c];
-      f32x8 yn = yv * inv_y;
+      const int col = (c * TPR + lane) * W;
+      const F rv = wide<T>(rr[c]), dhv = wide<T>(dhr[c]), yv = wide<T>(yr[c]);
+      const F dR = wide<T>(drr[c]) + inv_r * (dhv * wp[c]) - back_r * rv;
+      F z = dR * wg[c];
+      F yn = yv * inv_y;
       if (a.gate_kind == EMB_GATE_ROWS) {
         if (dgate && live) {
           // wg is w_post alone here (or 1)
-          store8<T, ONCE>(dgate + at + col, dR * yn * wg[c], n[c]);
+          store_vec<W, T, ONCE>(dgate + at + col, dR * yn * wg[c], n[c]);
         }
-        const f32x8 g = widen(gr[c]);
+        const F g = wide<T>(gr[c]);
         z *= g;
         yn *= g;
       }
       c_post[c] += dR * yn;
       c_pre[c] += dhv * (rv * inv_r);
       if (live) {
-        if (dx) store8<T, ONCE>(dx + at + col, a.alpha * dR, n[c]);
-        if (dy) store8<T, ONCE>(dy + at + col, inv_y * z - back_y * yv, n[c]);
+        if (dx) store_vec<W, T, ONCE>(dx + at + col, a.alpha * dR, n[c]);
+        if (dy) store_vec<W, T, ONCE>(dy + at + col, inv_y * z - back_y * yv, n[c]);
       }
     }
   }
@@ -257,23 +269,23 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + lane) * 8;
-      f32x8 v = k ? c_pre[c] : c_post[c];
+      const int col = (c * TPR + lane) * W;
+      F v = k ? c_pre[c] : c_post[c];
       if (kRows > 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cols[threadIdx.x / TPR][lane * 8 + i] = v[i];
+        for (int i = 0; i < W; ++i) cols[threadIdx.x / TPR][lane * W + i] = v[i];
         __syncthreads();
         if (threadIdx.x < TPR) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < W; ++i) {
             float t = 0.f;
-            for (int g = 0; g < kRows; ++g) t += cols[g][lane * 8 + i];
+            for (int g = 0; g < kRows; ++g) t += cols[g][lane * W + i];
             v[i] = t;
           }
         }
       }
-      if ((kRows == 1 || threadIdx.x < TPR) && n[c] > 0) store8(out + (size_t)k * D + col, v, n[c]);
+      if ((kRows == 1 || threadIdx.x < TPR) && n[c] > 0) store_vec<W>(out + (size_t)k * D + col, v, n[c]);
     }
   }
 }
@@ -328,14 +340,35 @@ void go_bwd(const NormArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((norm_join<T>), dim3((unsigned)((a.dim + 31) / 32), 2), dim3(kJoin), 0, st, a);
 }
 
+// How many threads take a row of `dim` columns, and in how many vectors each.
+struct RowShape {
+  int threads, vectors;
+};
+RowShape row_shape(int32_t dim, int vec) {
+  if (dim <= 32 * vec) return {32, 1};
+  if (dim <= 64 * vec) return {64, 1};
+  if (dim <= 64 * vec * 2 && vec == 4) return {64, 2};
+  if (dim <= 256 * vec) return {256, 1};
+  if (dim <= 256 * vec * 2) return {256, 2};
+  if (dim <= 256 * vec * 4) return {256, 4};
+  return {256, 8};  // fp32 alone
+}
+
 template <typename T>
 void pick(const NormArgs& a, bool bwd, hipStream_t st) {
-#define GO(TPR, NC) (bwd ? go_bwd<T, TPR, NC>(a, st) : go_fwd<T, TPR, NC>(a, st))
-  if (a.dim <= 256) GO(32, 1);
-  else if (a.dim <= 512) GO(64, 1);
-  else if (a.dim <= 2048) GO(256, 1);
-  else if (a.dim <= 4096) GO(256, 2);
-  else GO(256, 4);
+#define GO(TPR, NC)                                                       \
+  if (s.threads == TPR && s.vectors == NC)                                \
+    return bwd ? go_bwd<T, TPR, NC>(a, st) : go_fwd<T, TPR, NC>(a, st)
+  const RowShape s = row_shape(a.dim, kVec<T>);
+  GO(32, 1);
+  GO(64, 1);
+  GO(256, 1);
+  GO(256, 2);
+  GO(256, 4);
+  if constexpr (kVec<T> == 4) {
+    GO(64, 2);
+    GO(256, 8);
+  }
 #undef GO
 }
 
@@ -348,9 +381,10 @@ void pick_type(const NormArgs& a, bool bwd, hipStream_t st) {
 }  // namespace
 
 // Blocks of the backward: as many as are resident at once (three waves a SIMD by its registers), so
-// that the last ones do not run alone; each writes and norm_join reads 8 dim bytes.
+// that the last ones do not run alone; each writes and norm_join reads 8 dim bytes.  For any type: the
+// workspace is asked for without it.
 int norm_bwd_blocks(int64_t rows, int32_t dim) {
-  const int64_t per = dim <= 256 ? 8 : dim <= 512 ? 4 : 1;
+  const int64_t per = kThreads / row_shape(dim, 8).threads;
   const int64_t most = dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
   const int64_t b = (rows + per - 1) / per;
   return (int)(b < most ? b : most);
