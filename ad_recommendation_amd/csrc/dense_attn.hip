@@ -390,7 +390,8 @@ __device__ __forceinline__ void again_fwd(const AttnArgs& a, int64_t begin, int 
     const float s = dot(q, get<T>(a.k, begin + j, kh, a.dim)) * a.scale;
     const Pair v = get<T>(a.v, begin + j, kh, a.dim);
     const float mn = fmaxf(m, s);
-    const float by = m == -kInf ? 0.f : expf(m - mn), p = expf(s - mn);
+    const float by = m == -kInf ? 0.f : expf(m - mn);
+    const float p = s == -kInf ? 0.f : expf(s - mn);  // mn may be -inf as well
     o.a = o.a * by + p * v.a;
     o.b = o.b * by + p * v.b;
     l = l * by + p;

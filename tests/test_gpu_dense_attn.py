@@ -197,6 +197,40 @@ def test_what_is_not_finite_reaches_only_what_sees_it(at, d):
         x[at] = keep
 
 
+@pytest.mark.parametrize("d", [32, 128])
+def test_a_score_of_minus_infinity_weighs_nothing(d):
+    n, window, dtype = 200, 20, F16
+    off = offsets([n])
+    q, k, v = (rand(n, 1, d, dtype=dtype, seed=s) for s in range(3))
+    q[:, 0, 0] = 1
+    k[[0, 60], 0, 0] = -float("inf")
+    v[150] = float("nan")  # hidden from most, in a tile with many that do not see it
+    v[1] = float("inf")
+    out, lse = torch.empty_like(q), torch.empty(1, n, device="cuda")
+    dense.attn_window_fwd(q, k, v, off, window, 0, 0.2, out, lse)
+    with_zeros = k.clone()
+    with_zeros[[0, 60]] = 0
+    s = q[:, 0].double() @ with_zeros[:, 0].double().T * 0.2
+    see = O.visible(n, window, 0, "cuda")
+    see[:, [0, 60]] = False
+    rel = 2 * (d + 8) * O.F32 * (q[:, 0].abs().double() @ with_zeros[:, 0].abs().double().T * 0.2).max() + \
+        (16 + n) * O.F32
+    p = torch.softmax(s.masked_fill(~see, -float("inf")), -1)
+    fine = torch.ones(n, dtype=torch.bool, device="cuda")
+    fine[0] = False  # sees key 0 alone: 0 / 0
+    fine[1:1 + window] = False
+    fine[150:150 + window] = False
+    vv = v[:, 0].double().nan_to_num(0, 0, 0)
+    want, u = (p @ vv)[fine], O.U[dtype]
+    bound = u * want.abs() + (u + 2 * rel) * (1 + u) * (p @ vv.abs())[fine] + \
+        O.TINY[dtype] * (1 + (see.double() @ vv.abs())[fine])
+    within(out[fine, 0], want, bound, "out")
+    assert not out[~fine].isfinite().all(-1).any()
+    assert out[0].isnan().all()
+    # key 1's value is +inf and key 0 weighs nothing: the sums are +inf, not NaN
+    assert (out[1:1 + window] == float("inf")).all()
+
+
 # ---------------------------------------------------------------------------------- one new event
 def decode(q, kc, vc, lens, window, sinks, scale):
     n, hq, d = q.shape
