@@ -65,8 +65,9 @@ int check_heads(const EmbHeads* t, const char* name) {
 
 int check_counts(int64_t n_seq, int64_t n_tok) {
   DENSE_CHECK(n_seq >= 0 && n_tok >= 0, EMB_EINVAL, "attention: negative size");
-  DENSE_CHECK(n_seq < INT32_MAX && n_tok < INT32_MAX, EMB_ERANGE,
-              "attention: 2^31 - 1 or more sequences or tokens");
+  // the kernels count tokens in 32 bits, with tiles past the last one
+  DENSE_CHECK(n_seq <= (1 << 30) && n_tok <= (1 << 30), EMB_ERANGE,
+              "attention: more than 2^30 sequences or tokens");
   return EMB_OK;
 }
 

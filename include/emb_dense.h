@@ -65,7 +65,7 @@ typedef struct {
  * EMB_VALIDATE=1 checks the offsets first (it synchronises the stream); without it malformed
  * offsets give wrong results but no access outside the n_tok tokens.
  * Errors: EMB_EINVAL for a null pointer, a bad descriptor, alignment or stride; EMB_ERANGE for
- * n_tok or n_seq of 2^31 - 1 or more, or more tiles than a launch can hold.
+ * n_tok or n_seq (or a cache's capacity) over 2^30, or more tiles than a launch can hold.
  */
 int attn_window_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
                     const int32_t* d_offsets, int64_t n_seq, int64_t n_tok, const EmbHeads* out,

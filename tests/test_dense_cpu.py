@@ -82,10 +82,10 @@ def test_bad_attention_arguments_are_refused(call):
         refused(call(**{name: heads(tok=100)}), "EMB_EINVAL", "stride")
         refused(call(**{name: heads(head=33)}), "EMB_EINVAL", "stride")
     refused(call(n_seq=-1), "EMB_EINVAL", "negative")
-    refused(call(n_seq=2 ** 31), "EMB_ERANGE")
+    refused(call(n_seq=2 ** 30 + 1), "EMB_ERANGE")
     if call is dec:
         refused(call(cap=-1), "EMB_EINVAL", "negative")
-        refused(call(cap=2 ** 31), "EMB_ERANGE")
+        refused(call(cap=2 ** 30 + 1), "EMB_ERANGE")
         refused(call(lens=None), "EMB_EINVAL", "lens")
         refused(call(cap=4096, a=attn(window=4096), ws=None), "EMB_EINVAL", "workspace")
         refused(call(cap=4096, a=attn(window=4096), ws_bytes=16), "EMB_ENOSPACE")
@@ -93,7 +93,7 @@ def test_bad_attention_arguments_are_refused(call):
         assert call(n_seq=0) == 0
     else:
         refused(call(n_tok=-1), "EMB_EINVAL", "negative")
-        refused(call(n_tok=2 ** 31), "EMB_ERANGE")
+        refused(call(n_tok=2 ** 30 + 1), "EMB_ERANGE")
         refused(call(a=attn(q_heads=4096), n_tok=2 ** 30), "EMB_ERANGE")
         refused(call(lse=P + 2), "EMB_EINVAL", "aligned")
         assert call(n_seq=0, n_tok=0) == 0 and call(n_tok=0) == 0
