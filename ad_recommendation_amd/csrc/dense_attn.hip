@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a)
 // registers.  Heads of 128: the sums alone take 128 registers and the operands another 64, which
 // leaves one wave a SIMD; eight waves, two to each 32 keys with half of a step's rows, and keys and
 // values in LDS make it two, at a half more reads of LDS.
-constexpr int kSinkKeys = EMB_ATTN_MAX_SINKS;
+static_assert(EMB_ATTN_MAX_SINKS <= 32, "the sinks lie in the first 32 keys");
 
 // Queries from here on see nothing of the first key tile but the sinks.
 inline int64_t reach_of(int window, int tokens) { return (int64_t)tokens + window - 1; }

@@ -8,6 +8,7 @@ current device; errors raise EmbError (the library's checks) or TypeError/ValueE
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from typing import Optional
 
 import torch
@@ -33,8 +34,11 @@ class EmbHeads(C.Structure):
     _fields_ = [("p", _VP), ("seq", _I64), ("tok", _I64), ("head", _I64)]
 
 
+# The same as bytes, which the calls take as well: a Structure costs 0.3 us more, of which a call has up to nine.
+_pack_attn, _pack_heads = struct.Struct("6if").pack, struct.Struct("P3q").pack
+
 _LIB = None
-_A, _H = C.POINTER(EmbAttn), C.POINTER(EmbHeads)
+_A = _H = _VP
 _SZ = C.POINTER(C.c_size_t)
 _SIG = {
     "attn_window_fwd": [_A, _H, _H, _H, _VP, _I64, _I64, _H, _VP, _VP],
@@ -75,13 +79,15 @@ def lib() -> C.CDLL:
     return _LIB
 
 
-# the current stream's handle without the Stream object around it, which costs 3 us
+# the current stream's handle without the Stream object around it, which costs 3 us, and the device's
+# number without a look at whether there is a device, which a CUDA tensor has answered
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return _emb_stream(stream)
 
 
@@ -106,9 +112,9 @@ def _ws(ws):
 
 
 # ------------------------------------------------------------------ attention
-def _heads(t, name: str, dtype, shape) -> EmbHeads:
-    """[tokens, heads, dim], or [sequences, tokens, heads, dim] of a cache: any strides but the
-    last, which is 1."""
+def _heads(t, name: str, dtype, shape) -> bytes:
+    """EmbHeads of [tokens, heads, dim], or [sequences, tokens, heads, dim] of a cache: any strides
+    but the last, which is 1."""
     if t.dtype is not dtype or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
     if t.shape != shape:
@@ -120,75 +126,78 @@ def _heads(t, name: str, dtype, shape) -> EmbHeads:
         # the strides of dimensions of one element are never used: 0 passes the library's check of them
         st = [s if n > 1 else 0 for s, n in zip(st, shape)]
     if len(st) == 3:
-        return EmbHeads(t.data_ptr(), 0, st[0], st[1])
-    return EmbHeads(t.data_ptr(), st[0], st[1], st[2])
+        return _pack_heads(t.data_ptr(), 0, st[0], st[1])
+    return _pack_heads(t.data_ptr(), st[0], st[1], st[2])
 
 
-def _attn(q, kv_heads: int, window: int, sinks: int, scale: float) -> EmbAttn:
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q: expected float16 or bfloat16, got {q.dtype}")
-    # no window past the longest sequence differs from one of 2^31 - 1
-    return EmbAttn(_DTYPE[q.dtype], q.shape[1], kv_heads, q.shape[2], min(int(window), 2**31 - 1),
-                   int(sinks), float(scale))
+def _attn(dtype, shape, kv_heads: int, window: int, sinks: int, scale: float) -> bytes:
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"q: expected float16 or bfloat16, got {dtype}")
+    try:
+        # no window past the longest sequence differs from one of 2^31 - 1
+        return _pack_attn(_DTYPE[dtype], shape[1], kv_heads, shape[2], min(int(window), 2**31 - 1),
+                          int(sinks), float(scale))
+    except struct.error:
+        raise ValueError("window, sinks: a value that 32 bits do not hold") from None
 
 
-def _kv_shape(q, k):
-    if q.dim() != 3 or k.dim() != 3:
+def _shapes(q, k):
+    """q's, and that of keys and values."""
+    shape = q.shape
+    if len(shape) != 3 or k.dim() != 3:
         raise ValueError("q, k: expected [tokens, heads, dim]")
-    n, _, d = q.shape
-    return n, k.shape[1], d
+    return shape, (shape[0], k.shape[1], shape[2])
 
 
 def _offsets(offsets):
     p = _ptr(offsets, "offsets", torch.int32)
-    if offsets.dim() != 1 or offsets.numel() < 1:
+    n = offsets.numel()
+    if offsets.dim() != 1 or n < 1:
         raise ValueError("offsets: expected one dimension of n_seq + 1 elements")
-    return p, offsets.numel() - 1
+    return p, n - 1
 
 
 def attn_window_fwd(q, k, v, offsets, window: int, sinks: int, scale: float, out, lse=None,
                     stream=None):
     """out [tokens, q_heads, dim] and lse [q_heads, tokens] (fp32, optional) of q [tokens, q_heads,
     dim] and k, v [tokens, kv_heads, dim]; sequence s holds tokens offsets[s] to offsets[s + 1] - 1."""
-    t, kv = q.dtype, _kv_shape(q, k)
-    a = _attn(q, k.shape[1], window, sinks, scale)
+    t, (qs, kv) = q.dtype, _shapes(q, k)
+    a = _attn(t, qs, kv[1], window, sinks, scale)
     off, n_seq = _offsets(offsets)
     _check(lib().attn_window_fwd(
-        a, _heads(q, "q", t, q.shape), _heads(k, "k", t, kv),
-        _heads(v, "v", t, kv), off, n_seq, q.shape[0],
-        _heads(out, "out", t, q.shape),
-        _ptr(lse, "lse", torch.float32, (q.shape[1], q.shape[0]), optional=True),
+        a, _heads(q, "q", t, qs), _heads(k, "k", t, kv), _heads(v, "v", t, kv), off, n_seq, qs[0],
+        _heads(out, "out", t, qs),
+        _ptr(lse, "lse", torch.float32, (qs[1], qs[0]), optional=True),
         _stream(stream)))
 
 
 def attn_window_bwd_workspace_bytes(n_tok: int, n_seq: int, q_heads: int, kv_heads: int, dim: int,
                                     sinks: int) -> int:
-    a, n = EmbAttn(EMB_F16, q_heads, kv_heads, dim, 1, sinks, 1.0), C.c_size_t()
-    _check(lib().attn_window_bwd_workspace_bytes(C.byref(a), n_seq, n_tok, C.byref(n)))
+    a, n = _attn(torch.float16, (n_tok, q_heads, dim), kv_heads, 1, sinks, 1.0), C.c_size_t()
+    _check(lib().attn_window_bwd_workspace_bytes(a, n_seq, n_tok, C.byref(n)))
     return n.value
 
 
 def attn_window_bwd(q, k, v, offsets, window: int, sinks: int, scale: float, out, lse, dout, dq,
                     dk, dv, ws, stream=None):
     """dq, dk and dv from the forward's inputs and results and the gradient of out."""
-    t, kv = q.dtype, _kv_shape(q, k)
-    a = _attn(q, k.shape[1], window, sinks, scale)
+    t, (qs, kv) = q.dtype, _shapes(q, k)
+    a = _attn(t, qs, kv[1], window, sinks, scale)
     off, n_seq = _offsets(offsets)
     wp, wb = _ws(ws)
     _check(lib().attn_window_bwd(
-        a, _heads(q, "q", t, q.shape), _heads(k, "k", t, kv),
-        _heads(v, "v", t, kv), off, n_seq, q.shape[0],
-        _heads(out, "out", t, q.shape),
-        _ptr(lse, "lse", torch.float32, (q.shape[1], q.shape[0])),
-        _heads(dout, "dout", t, q.shape), _heads(dq, "dq", t, q.shape),
+        a, _heads(q, "q", t, qs), _heads(k, "k", t, kv), _heads(v, "v", t, kv), off, n_seq, qs[0],
+        _heads(out, "out", t, qs),
+        _ptr(lse, "lse", torch.float32, (qs[1], qs[0])),
+        _heads(dout, "dout", t, qs), _heads(dq, "dq", t, qs),
         _heads(dk, "dk", t, kv), _heads(dv, "dv", t, kv), wp, wb,
         _stream(stream)))
 
 
 def attn_window_decode_workspace_bytes(n_seq: int, capacity: int, q_heads: int, kv_heads: int,
                                        dim: int, window: int, sinks: int) -> int:
-    a, n = EmbAttn(EMB_F16, q_heads, kv_heads, dim, min(int(window), 2**31 - 1), sinks, 1.0), C.c_size_t()
-    _check(lib().attn_window_decode_workspace_bytes(C.byref(a), n_seq, capacity, C.byref(n)))
+    a, n = _attn(torch.float16, (n_seq, q_heads, dim), kv_heads, window, sinks, 1.0), C.c_size_t()
+    _check(lib().attn_window_decode_workspace_bytes(a, n_seq, capacity, C.byref(n)))
     return n.value
 
 
@@ -196,39 +205,40 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
                        stream=None):
     """out [n_seq, q_heads, dim] of one query per sequence, q [n_seq, q_heads, dim], against caches
     [n_seq, capacity, kv_heads, dim] that hold lens [n_seq] events, the query's own among them."""
-    if q.dim() != 3 or k_cache.dim() != 4:
+    t, qs = q.dtype, q.shape
+    if len(qs) != 3 or k_cache.dim() != 4:
         raise ValueError("expected q [sequences, heads, dim], k_cache [sequences, capacity, heads, dim]")
-    t, (n, cap, kv_heads, _) = q.dtype, k_cache.shape
-    a = _attn(q, kv_heads, window, sinks, scale)
-    cache = (q.shape[0], cap, kv_heads, q.shape[2])
+    _, cap, kv_heads, _ = k_cache.shape
+    a = _attn(t, qs, kv_heads, window, sinks, scale)
+    cache = (qs[0], cap, kv_heads, qs[2])
     wp, wb = _ws(ws)
     _check(lib().attn_window_decode(
-        a, _heads(q, "q", t, q.shape),
-        _heads(k_cache, "k_cache", t, cache), _heads(v_cache, "v_cache", t, cache),
-        _ptr(lens, "lens", torch.int32, (q.shape[0],)), q.shape[0], cap,
-        _heads(out, "out", t, q.shape), wp, wb, _stream(stream)))
+        a, _heads(q, "q", t, qs), _heads(k_cache, "k_cache", t, cache),
+        _heads(v_cache, "v_cache", t, cache), _ptr(lens, "lens", torch.int32, (qs[0],)), qs[0], cap,
+        _heads(out, "out", t, qs), wp, wb, _stream(stream)))
 
 
 # ------------------------------------------------------------------ norms
-def _gate_kind(gate, shape) -> int:
+def _gate_kind(gate) -> int:
     if gate is None:
         return GATE_NONE
     return GATE_VECTOR if gate.dim() == 1 else GATE_ROWS
 
 
 def _rows(t):
-    if t.dim() != 2:
+    dtype, shape = t.dtype, t.shape
+    if len(shape) != 2:
         raise ValueError("expected rows [rows, dim]")
-    if t.dtype not in _DTYPE:
-        raise TypeError(f"expected float32, float16 or bfloat16, got {t.dtype}")
-    return t.dtype, t.shape, (t.shape[1],)
+    if dtype not in _DTYPE:
+        raise TypeError(f"expected float32, float16 or bfloat16, got {dtype}")
+    return dtype, shape, shape[1:]
 
 
 def norm_gate_residual_fwd(x, y, gate, w_post, w_pre, alpha: float, eps: float, r, h, stream=None):
     """r = alpha x + gate * (w_post * rms(y)), h = w_pre * rms(r).  x, y, r, h [rows, dim]; gate
     [dim] or [rows, dim]; w_post, w_pre fp32 [dim].  None where a part is left out."""
     t, s, d = _rows(x)
-    kind = _gate_kind(gate, s)
+    kind = _gate_kind(gate)
     _check(lib().norm_gate_residual_fwd(
         _ptr(x, "x"), _ptr(y, "y", t, s, True), _ptr(gate, "gate", t, d if kind == 1 else s, True),
         kind, _ptr(w_post, "w_post", torch.float32, d, True),
@@ -247,7 +257,7 @@ def norm_gate_residual_bwd(r, y, gate, w_post, w_pre, alpha: float, eps: float, 
     """Gradients of norm_gate_residual_fwd from r as stored; None for an output that is not wanted.
     dgate: fp32 [dim] for a gate vector, like the rows for a gate of rows."""
     t, s, d = _rows(r)
-    kind = _gate_kind(gate, s)
+    kind = _gate_kind(gate)
     f, wp_wb = torch.float32, _ws(ws)
     _check(lib().norm_gate_residual_bwd(
         _ptr(r, "r"), _ptr(y, "y", t, s, True), _ptr(gate, "gate", t, d if kind == 1 else s, True),

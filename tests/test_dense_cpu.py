@@ -230,6 +230,13 @@ def test_binding_refuses_bad_tensors():
         dense.attn_window_fwd(x[0], x, x, off, 1, 0, 1.0, x)
     with pytest.raises(ValueError, match="capacity"):
         dense.attn_window_decode(x, x, x, off, 1, 0, 1.0, x, None)
+    for window, sinks in ((-2 ** 40, 0), (1, 2 ** 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            dense.attn_window_fwd(x, x, x, off, window, sinks, 1.0, x)
+    with pytest.raises(ValueError, match="32 bits"):
+        dense.attn_window_bwd_workspace_bytes(4, 1, 2, 2, 8, 2 ** 32)
+    with pytest.raises(emb.EmbError):
+        dense.attn_window_decode_workspace_bytes(4, 1, 2, 2, 8, 0, 2)
     with pytest.raises(ValueError, match="rows"):
         dense.norm_gate_residual_fwd(x, None, None, None, None, 1.0, 1e-6, x, None)
     with pytest.raises(TypeError, match="CUDA"):
