@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import struct
+from operator import attrgetter
 from typing import Optional
 
 import torch
@@ -272,23 +273,30 @@ def norm_gate_residual_bwd(r, y, gate, w_post, w_pre, alpha: float, eps: float, 
 # ------------------------------------------------------------------ AdamW
 def adamw_state_elems(weights) -> int:
     """Elements of a state array for these weight tensors."""
-    n = (_I64 * len(weights))(*[w.numel() for w in weights])
     out = _I64()
-    _check(lib().adamw_state_elems(n, len(weights), C.byref(out)))
+    _check(lib().adamw_state_elems(struct.pack(f"{len(weights)}q", *map(_numel, weights)), len(weights),
+                                   C.byref(out)))
     return out.value
 
 
-def _tensors(ts, name: str, dtype, sizes):
+# looked up once: a step of a hundred small tensors is bound by what is asked of each of them
+_numel, _data_ptr, _contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+_dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")
+
+
+def _tensors(ts, name: str, dtype, sizes) -> bytes:
     """Host array of the device pointers of contiguous tensors of one type and these sizes."""
-    for t, n in zip(ts, sizes):
-        if t.numel() != n or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} with the weights' "
-                            f"sizes, got {t.dtype}, {tuple(t.shape)} on {t.device}")
-    return (_VP * len(ts))(*[t.data_ptr() for t in ts])
+    if not (list(map(_numel, ts)) == sizes and set(map(_dtype_of, ts)) <= {dtype} and
+            all(map(_is_cuda, ts)) and all(map(_contiguous, ts))):
+        got = [(t.dtype, tuple(t.shape), str(t.device)) for t, n in zip(ts, sizes) if t.numel() != n or
+               t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()]
+        raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} with the weights' "
+                        f"sizes, got {got[0]}")
+    return struct.pack(f"{len(ts)}P", *map(_data_ptr, ts))
 
 
 def _adamw_args(weights, grads, copies, weight_decay):
-    sizes = [w.numel() for w in weights]
+    sizes = list(map(_numel, weights))
     k = len(sizes)
     if len(grads) != k or (copies is not None and len(copies) != k):
         raise ValueError(f"expected {k} tensors in grads and copies")
@@ -297,15 +305,13 @@ def _adamw_args(weights, grads, copies, weight_decay):
     if g_dtype not in _DTYPE or c_dtype not in _DTYPE:
         raise TypeError(f"unexpected tensor dtype {g_dtype}, {c_dtype}")
     if isinstance(weight_decay, (int, float)):
-        wd = (_F * k)(*([weight_decay] * k))
-    else:
-        if len(weight_decay) != k:
-            raise ValueError(f"weight_decay: expected {k} values, got {len(weight_decay)}")
-        wd = (_F * k)(*weight_decay)
-    return (k, (_I64 * k)(*sizes), _tensors(weights, "weights", torch.float32, sizes),
+        weight_decay = [weight_decay] * k
+    elif len(weight_decay) != k:
+        raise ValueError(f"weight_decay: expected {k} values, got {len(weight_decay)}")
+    return (k, struct.pack(f"{k}q", *sizes), _tensors(weights, "weights", torch.float32, sizes),
             _tensors(grads, "grads", g_dtype, sizes), _DTYPE[g_dtype],
             None if copies is None else _tensors(copies, "copies", c_dtype, sizes),
-            _DTYPE[c_dtype]), wd
+            _DTYPE[c_dtype]), struct.pack(f"{k}f", *weight_decay)
 
 
 def _scalar(t):
