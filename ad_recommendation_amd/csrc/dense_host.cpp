@@ -184,15 +184,12 @@ int run_adamw(const AdamCall& c, AdamArgs& a, bool q8, hipStream_t st) {
   a.inv_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(c.b2, (double)c.step)));
   a.eps = (float)c.eps;
   a.grad_scale = c.scale;
-  // Elements a workgroup takes: enough workgroups for every CU at small totals, fewer and longer
-  // ones at large totals.
-  a.chunk = total <= (int64_t)16 << 20 ? 2048 : 8192;
   uint32_t block0 = 0;
   int32_t i = 0;
   while (i < c.n_tensors) {
     uint32_t k = 0;
     uint64_t chunks = 0;
-    for (; i < c.n_tensors && k < (uint32_t)kAdamMax && chunks < (1u << 30); ++i) {
+    for (; i < c.n_tensors && k < (uint32_t)kAdamMax && chunks < kAdamChunks; ++i) {
       if (c.n[i] == 0) continue;
       AdamTensor& t = a.t[k++];
       t.w = static_cast<float*>(c.w[i]);
@@ -203,7 +200,7 @@ int run_adamw(const AdamCall& c, AdamArgs& a, bool q8, hipStream_t st) {
       t.chunk0 = (uint32_t)chunks;
       t.wd = c.wd[i];
       block0 += (uint32_t)(padded(c.n[i]) / EMB_ADAMW_BLOCK);
-      chunks += ((uint64_t)c.n[i] + a.chunk - 1) / a.chunk;
+      chunks += ((uint64_t)c.n[i] + kAdamChunk - 1) / kAdamChunk;
     }
     if (k == 0) break;
     a.n_tensors = k;

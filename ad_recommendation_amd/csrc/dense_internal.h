@@ -66,13 +66,18 @@ struct AdamTensor {
   float wd;
 };
 constexpr int kAdamMax = 96;
+// Elements of a workgroup: what its threads hold at once.  With more, taken in turn, the loads of a turn
+// wait for the stores of the one before: 20.8M elements in fp32 98 us, 8192 a workgroup 115; 335.6M with
+// 8-bit states 1054 and 1070.
+constexpr int kAdamChunk = 2048;
+constexpr uint32_t kAdamChunks = 1 << 23;  // of a launch, which has fewer than 2^32 threads
 struct AdamArgs {
   AdamTensor t[kAdamMax];
   float *m, *v;
   uint8_t *m8, *m_exp, *v8, *v_exp;
   const float* grad_scale;
   float lr, b1, b2, omb1, omb2, inv_c1, inv_c2, eps;
-  uint32_t seed_lo, seed_hi, n_tensors, chunk;  // chunk: elements a workgroup takes
+  uint32_t seed_lo, seed_hi, n_tensors;
   uint32_t once;  // more data than the caches hold
 };
 static_assert(sizeof(AdamArgs) <= 4096, "the argument block of a launch");
