@@ -100,10 +100,15 @@ __device__ __forceinline__ float swap32_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
   return fmaxf(__int_as_float(r[0]), __int_as_float(r[1]));
 }
-// The sum over each group of N lanes (16, 32 or 64), in every lane of it: rotations within rows of 16
-// lanes on the vector unit, then swaps of rows and halves; no LDS.
+// The sum over each group of N lanes (8, 16, 32 or 64), in every lane of it and the same bits there:
+// exchanges within rows of 16 lanes on the vector unit, then swaps of rows and halves; no LDS.
 template <int N>
 __device__ __forceinline__ float lanes_sum(float x) {
+  if (N == 8) {
+    x += dpp<0x141>(x);  // row_half_mirror: with lane 7 - i of the eight
+    x += dpp<0xB1>(x);   // quad_perm: with lane i ^ 1
+    return x + dpp<0x4E>(x);  // i ^ 2
+  }
   x += dpp<0x128>(x);  // row_ror:8
   x += dpp<0x124>(x);
   x += dpp<0x122>(x);

@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -377,7 +378,8 @@ int norm_gate_residual_bwd_workspace_bytes(int64_t rows, int32_t dim, size_t* by
   DENSE_CHECK(dim >= 1 && dim <= 8192, EMB_EINVAL, "norm: dim must lie in [1, 8192]");
   DENSE_CHECK(rows >= 0, EMB_EINVAL, "norm: negative row count");
   DENSE_CHECK(bytes, EMB_EINVAL, "norm: null pointer: bytes");
-  *bytes = (size_t)norm_bwd_blocks(rows, dim) * 2 * (size_t)dim * sizeof(float);
+  const int blocks = std::max(norm_bwd_blocks(rows, dim, EMB_F32), norm_bwd_blocks(rows, dim, EMB_F16));
+  *bytes = (size_t)blocks * 2 * (size_t)dim * sizeof(float);
   return EMB_OK;
 }
 
@@ -401,7 +403,7 @@ int norm_gate_residual_bwd(const void* r, const void* y, const void* gate, int32
                   aligned(dw_post, 4) && aligned(dw_pre, 4),
               EMB_EINVAL, "norm: a tensor is not aligned to its elements");
   NormArgs a{};
-  a.blocks = norm_bwd_blocks(rows, dim);
+  a.blocks = norm_bwd_blocks(rows, dim, dtype);
   const size_t need = (size_t)a.blocks * 2 * (size_t)dim * sizeof(float);
   DENSE_CHECK(ws_bytes >= need, EMB_ENOSPACE, "norm: workspace too small");
   DENSE_CHECK(need == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL,

@@ -49,7 +49,7 @@ struct NormArgs {
   int32_t dim, gate_kind, dtype, blocks;
   float alpha, eps;
 };
-int norm_bwd_blocks(int64_t rows, int32_t dim);
+int norm_bwd_blocks(int64_t rows, int32_t dim, int32_t dtype);
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st);
 

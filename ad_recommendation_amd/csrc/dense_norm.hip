@@ -55,8 +55,40 @@ __device__ __forceinline__ Vec<float, kVec<T>> wide(Vec<T, kVec<T>> v) {
   return __builtin_convertvector(v, Vec<float, kVec<T>>);
 }
 
-// TPR threads take a row, each NC vectors of kVec columns.  32768 x 2048 in bf16, a block a row: 99 us,
-// 5.4 TB/s; 100 x 256 in fp16, eight rows a block: 3.2 us.
+// Which columns a thread has: vector c of kVec at col[c].  The last vector of a row whose width is no multiple
+// of kVec ends where the row does, so that it is a whole one: its first `twice[c]` columns are the thread
+// before's as well.  Both compute them, from the same sums, and write the same bits; sums over the row leave
+// them out.  Element by element the end of a row costs seven loads and stores of every wave: 24M
+// elements in rows of 500, fp16, forward / backward 50 / 122 us, this way 41 / 60.
+// Rows shorter than a vector are read by elements.
+template <int W, int TPR, int NC>
+struct Columns {
+  int col[NC], twice[NC];
+  bool some[NC];  // whether there are any
+  int width;      // of a vector, the same for all threads
+  __device__ __forceinline__ Columns(int D, int lane) {
+    width = min(D, W);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * TPR + lane) * W;
+      some[c] = at < D;
+      col[c] = min(at, D - width);
+      twice[c] = at - col[c];
+    }
+  }
+};
+// The sum of the squares of the columns that are this thread's alone.
+template <int W>
+__device__ __forceinline__ float squares(Vec<float, W> x, int twice) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (i >= W - 1 || i >= twice) s += x[i] * x[i];
+  return s;
+}
+
+// TPR threads take a row, each NC vectors of kVec columns.  32768 x 2048 in bf16, a block a row: 93 us,
+// 5.8 TB/s; 100 x 256 in fp16, eight rows a block: 3.2 us.
 template <typename T, int TPR, int NC, bool ONCE>
 __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
   __shared__ float lds[2][kThreads / 64][1];
@@ -73,18 +105,16 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
   const float inv_d = 1.f / (float)D;
 
   // what all rows share: the weights after the block times a gate vector, the weights before
+  const Columns<W, TPR, NC> cl(D, lane);
   F wg[NC], wp[NC];
-  int n[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + lane) * W;
-    n[c] = D - col;
     wg[c] = F(1.f);
     wp[c] = wg[c];
-    if (n[c] > 0) {
-      if (a.w_post) wg[c] = load_vec<W>(a.w_post + col, n[c]);
-      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= wide<T>(load_vec<W>(gate + col, n[c]));
-      if (a.w_pre) wp[c] = load_vec<W>(a.w_pre + col, n[c]);
+    if (cl.some[c]) {
+      if (a.w_post) wg[c] = load_vec<W>(a.w_post + cl.col[c], cl.width);
+      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= wide<T>(load_vec<W>(gate + cl.col[c], cl.width));
+      if (a.w_pre) wp[c] = load_vec<W>(a.w_pre + cl.col[c], cl.width);
     }
   }
   const int64_t stride = (int64_t)gridDim.x * kRows;
@@ -98,28 +128,26 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
     V xr[NC], yr[NC], gr[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + lane) * W;
+      const int64_t e = at + cl.col[c];
       xr[c] = V{};
       yr[c] = xr[c];
       gr[c] = xr[c];
-      if (live && n[c] > 0) {
-        xr[c] = load_vec<W, T, ONCE>(x + at + col, n[c]);
-        if (y) yr[c] = load_vec<W, T, ONCE>(y + at + col, n[c]);
-        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load_vec<W, T, ONCE>(gate + at + col, n[c]);
+      if (live && cl.some[c]) {
+        xr[c] = load_vec<W, T, ONCE>(x + e, cl.width);
+        if (y) yr[c] = load_vec<W, T, ONCE>(y + e, cl.width);
+        if (a.gate_kind == EMB_GATE_ROWS) gr[c] = load_vec<W, T, ONCE>(gate + e, cl.width);
       }
     }
     float inv_y = 1.f;
     if (y && a.w_post) {
       float s[1] = {0.f};
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const F v = wide<T>(yr[c]);
-#pragma unroll
-        for (int i = 0; i < W; ++i) s[0] += v[i] * v[i];
-      }
+      for (int c = 0; c < NC; ++c) s[0] += squares<W>(wide<T>(yr[c]), cl.twice[c]);
       row_sums<TPR, 1>(s, lds, turn);
       turn ^= 1;
       inv_y = rsqrtf(s[0] * inv_d + a.eps);
+    } else if (TPR > 64) {
+      __syncthreads();  // r may be x's buffer: what two waves have is read by both before it is written
     }
     F rr[NC];
     float s[1] = {0.f};
@@ -131,13 +159,12 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
         if (a.gate_kind == EMB_GATE_ROWS) v *= wide<T>(gr[c]);
         rr[c] += v;
       }
-#pragma unroll
-      for (int i = 0; i < W; ++i) s[0] += rr[c][i] * rr[c][i];
+      s[0] += squares<W>(rr[c], cl.twice[c]);
     }
     if (r && live) {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (n[c] > 0) store_vec<W, T, ONCE>(r + at + (c * TPR + lane) * W, rr[c], n[c]);
+        if (cl.some[c]) store_vec<W, T, ONCE>(r + at + cl.col[c], rr[c], cl.width);
     }
     if (h) {
       row_sums<TPR, 1>(s, lds, turn);
@@ -145,14 +172,14 @@ __global__ void __launch_bounds__(kThreads) norm_fwd(NormArgs a) {
       const float inv_r = rsqrtf(s[0] * inv_d + a.eps);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (live && n[c] > 0) store_vec<W, T, ONCE>(h + at + (c * TPR + lane) * W, rr[c] * inv_r * wp[c], n[c]);
+        if (live && cl.some[c]) store_vec<W, T, ONCE>(h + at + cl.col[c], rr[c] * inv_r * wp[c], cl.width);
     }
   }
 }
 
 // Rows go round the blocks; a thread keeps the column sums of its columns over the rows it sees in
 // registers, the block's rows then meet in LDS, and the blocks in norm_join.  20011 x 2048 in bf16: 88 us,
-// 5.6 TB/s; 5003 x 333 in fp32: 14.8 us.
+// 5.6 TB/s; 5003 x 333 in fp32: 12 us beside the 4 of norm_join.
 template <typename T, int TPR, int NC, bool ONCE>
 __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   constexpr int kRows = kThreads / TPR, W = kVec<T>;
@@ -160,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   typedef Vec<float, W> F;
   constexpr int kSums = 6;
   __shared__ float lds[2][kThreads / 64][kSums];
-  __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * W : 1];
+  __shared__ __attribute__((aligned(16))) float cols[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * W : 4];
   const int lane = threadIdx.x % TPR;
   const int D = a.dim;
   const T* r = static_cast<const T*>(a.r_in);
@@ -174,20 +201,18 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   const float inv_d = 1.f / (float)D;
   const bool pre = a.w_pre != nullptr;
 
+  const Columns<W, TPR, NC> cl(D, lane);
   F wg[NC], wp[NC], c_post[NC], c_pre[NC];
-  int n[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + lane) * W;
-    n[c] = D - col;
     wg[c] = F(1.f);
     wp[c] = wg[c];
     c_post[c] = F{};
     c_pre[c] = F{};
-    if (n[c] > 0) {
-      if (a.w_post) wg[c] = load_vec<W>(a.w_post + col, n[c]);
-      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= wide<T>(load_vec<W>(gate + col, n[c]));
-      if (pre) wp[c] = load_vec<W>(a.w_pre + col, n[c]);
+    if (cl.some[c]) {
+      if (a.w_post) wg[c] = load_vec<W>(a.w_post + cl.col[c], cl.width);
+      if (a.gate_kind == EMB_GATE_VECTOR) wg[c] *= wide<T>(load_vec<W>(gate + cl.col[c], cl.width));
+      if (pre) wp[c] = load_vec<W>(a.w_pre + cl.col[c], cl.width);
     }
   }
   // A row's data as it is.  Rows of a wave or less are loaded while the row before is computed (5003 x 333
@@ -201,16 +226,16 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
     const int64_t row = base + threadIdx.x / TPR, at = row * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + lane) * W;
+      const int64_t e = at + cl.col[c];
       x[c] = Row{};
-      if (row >= a.rows || n[c] <= 0) continue;
+      if (row >= a.rows || !cl.some[c]) continue;
       if (pre) {
-        x[c].r = load_vec<W, T, ONCE>(r + at + col, n[c]);
-        x[c].dh = load_vec<W, T, ONCE>(dh + at + col, n[c]);
+        x[c].r = load_vec<W, T, ONCE>(r + e, cl.width);
+        x[c].dh = load_vec<W, T, ONCE>(dh + e, cl.width);
       }
-      if (dr) x[c].dr = load_vec<W, T, ONCE>(dr + at + col, n[c]);
-      if (y) x[c].y = load_vec<W, T, ONCE>(y + at + col, n[c]);
-      if (a.gate_kind == EMB_GATE_ROWS) x[c].g = load_vec<W, T, ONCE>(gate + at + col, n[c]);
+      if (dr) x[c].dr = load_vec<W, T, ONCE>(dr + e, cl.width);
+      if (y) x[c].y = load_vec<W, T, ONCE>(y + e, cl.width);
+      if (a.gate_kind == EMB_GATE_ROWS) x[c].g = load_vec<W, T, ONCE>(gate + e, cl.width);
     }
   };
   int turn = 0;
@@ -232,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       if (a.gate_kind == EMB_GATE_ROWS) av *= wide<T>(now[c].g);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
+        if (i < W - 1 && i < cl.twice[c]) continue;
         s[0] += rv[i] * rv[i];
         s[1] += u[i] * rv[i];
         s[2] += yv[i] * yv[i];
@@ -251,8 +277,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (n[c] <= 0) continue;
-      const int col = (c * TPR + lane) * W;
+      if (!cl.some[c]) continue;
+      const int64_t e = at + cl.col[c];
       const F rv = wide<T>(now[c].r), dhv = wide<T>(now[c].dh), yv = wide<T>(now[c].y);
       const F dR = wide<T>(now[c].dr) + inv_r * (dhv * wp[c]) - back_r * rv;
       F z = dR * wg[c];
@@ -260,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       if (a.gate_kind == EMB_GATE_ROWS) {
         if (dgate && live) {
           // wg is w_post alone here (or 1)
-          store_vec<W, T, ONCE>(dgate + at + col, dR * yn * wg[c], n[c]);
+          store_vec<W, T, ONCE>(dgate + e, dR * yn * wg[c], cl.width);
         }
         const F g = wide<T>(now[c].g);
         z *= g;
@@ -269,8 +295,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       c_post[c] += dR * yn;
       c_pre[c] += dhv * (rv * inv_r);
       if (live) {
-        if (dx) store_vec<W, T, ONCE>(dx + at + col, a.alpha * dR, n[c]);
-        if (dy) store_vec<W, T, ONCE>(dy + at + col, inv_y * z - back_y * yv, n[c]);
+        if (dx) store_vec<W, T, ONCE>(dx + e, a.alpha * dR, cl.width);
+        if (dy) store_vec<W, T, ONCE>(dy + e, inv_y * z - back_y * yv, cl.width);
       }
     }
 #pragma unroll
@@ -283,29 +309,27 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + lane) * W;
-      F v = k ? c_pre[c] : c_post[c];
-      if (kRows > 1) {
+      const F v = k ? c_pre[c] : c_post[c];
+      if constexpr (kRows == 1) {
+        if (cl.some[c]) store_vec<W>(out + (size_t)k * D + cl.col[c], v, cl.width);
+      } else {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < W; ++i) cols[threadIdx.x / TPR][lane * W + i] = v[i];
+        *reinterpret_cast<F*>(&cols[threadIdx.x / TPR][lane * W]) = v;
         __syncthreads();
-        if (threadIdx.x < TPR) {
+        for (int x = threadIdx.x; x < TPR * W; x += kThreads) {
+          float t = 0.f;
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            float t = 0.f;
-            for (int g = 0; g < kRows; ++g) t += cols[g][lane * W + i];
-            v[i] = t;
-          }
+          for (int g = 0; g < kRows; ++g) t += cols[g][x];
+          const int at = c * TPR * W + x / W * W, i = x % W;
+          if (at < D && i < cl.width) out[(size_t)k * D + min(at, D - cl.width) + i] = t;
         }
       }
-      if ((kRows == 1 || threadIdx.x < TPR) && n[c] > 0) store_vec<W>(out + (size_t)k * D + col, v, n[c]);
     }
   }
 }
 
 // Sums the blocks' column sums: 32 columns of one of the two a workgroup, 32 threads a column, in a
-// fixed order.  768 blocks of 2048 columns: 4.6 us, of which a launch is most.
+// fixed order.  768 blocks of 2048 columns: 4.7 us, of which a launch is most.
 constexpr int kJoin = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kJoin) norm_join(NormArgs a) {
@@ -335,14 +359,36 @@ __global__ void __launch_bounds__(kJoin) norm_join(NormArgs a) {
   }
 }
 
+// How many threads take a row of `dim` columns, and in how many vectors each.
+struct RowShape {
+  int threads, vectors;
+};
+RowShape row_shape(int32_t dim, int vec) {
+  if (dim <= 8 * vec) return {8, 1};
+  if (dim <= 16 * vec) return {16, 1};
+  if (dim <= 32 * vec) return {32, 1};
+  if (dim <= 64 * vec) return {64, 1};
+  if (dim <= 64 * vec * 2) return {64, 2};
+  if (dim <= 256 * vec) return {256, 1};
+  if (dim <= 256 * vec * 2) return {256, 2};
+  if (dim <= 256 * vec * 4) return {256, 4};
+  return {256, 8};  // fp32 alone
+}
+
 template <typename T>
 bool once(const NormArgs& a, int rows_of_data) {
   return a.rows * a.dim * (int64_t)sizeof(T) * rows_of_data > kOnceBytes;
 }
+// Blocks of the forward.  Loads of a block's turn wait for the stores of its turn before, so many blocks with
+// few turns are better; but each loads the weights, which weighs more where a thread has more of a row.
+// 24M elements in rows of 200 in fp32, 1024 / 2048 / 8192 / 16384 blocks: 70 / 79 / 71 / 66 us; 500 in fp16:
+// 38 / 41 / 37 / 38; 8192 in fp16, 512 / 1024 / 2048 / 8192: 40 / 43 / 45 / 48.
 template <typename T, int TPR, int NC>
 void go_fwd(const NormArgs& a, hipStream_t st) {
+  constexpr int kFloats = NC * kVec<T>;  // of a row, in a thread
+  constexpr int64_t kMost = kFloats <= 4 ? 16384 : kFloats <= 8 ? 8192 : 512;
   const int64_t blocks = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
-  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048)), block(kThreads);
+  const dim3 grid((unsigned)(blocks < kMost ? blocks : kMost)), block(kThreads);
   if (once<T>(a, 4)) hipLaunchKernelGGL((norm_fwd<T, TPR, NC, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((norm_fwd<T, TPR, NC, false>), grid, block, 0, st, a);
 }
@@ -354,35 +400,21 @@ void go_bwd(const NormArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((norm_join<T>), dim3((unsigned)((a.dim + 31) / 32), 2), dim3(kJoin), 0, st, a);
 }
 
-// How many threads take a row of `dim` columns, and in how many vectors each.
-struct RowShape {
-  int threads, vectors;
-};
-RowShape row_shape(int32_t dim, int vec) {
-  if (dim <= 32 * vec) return {32, 1};
-  if (dim <= 64 * vec) return {64, 1};
-  if (dim <= 64 * vec * 2 && vec == 4) return {64, 2};
-  if (dim <= 256 * vec) return {256, 1};
-  if (dim <= 256 * vec * 2) return {256, 2};
-  if (dim <= 256 * vec * 4) return {256, 4};
-  return {256, 8};  // fp32 alone
-}
-
 template <typename T>
 void pick(const NormArgs& a, bool bwd, hipStream_t st) {
 #define GO(TPR, NC)                                                       \
   if (s.threads == TPR && s.vectors == NC)                                \
     return bwd ? go_bwd<T, TPR, NC>(a, st) : go_fwd<T, TPR, NC>(a, st)
   const RowShape s = row_shape(a.dim, kVec<T>);
+  GO(8, 1);
+  GO(16, 1);
   GO(32, 1);
   GO(64, 1);
+  GO(64, 2);
   GO(256, 1);
   GO(256, 2);
   GO(256, 4);
-  if constexpr (kVec<T> == 4) {
-    GO(64, 2);
-    GO(256, 8);
-  }
+  if constexpr (kVec<T> == 4) GO(256, 8);
 #undef GO
 }
 
@@ -394,12 +426,16 @@ void pick_type(const NormArgs& a, bool bwd, hipStream_t st) {
 
 }  // namespace
 
-// Blocks of the backward: as many as are resident at once (three waves a SIMD by its registers), so
-// that the last ones do not run alone; each writes and norm_join reads 8 dim bytes.  For any type: the
-// workspace is asked for without it.
-int norm_bwd_blocks(int64_t rows, int32_t dim) {
-  const int64_t per = kThreads / row_shape(dim, 8).threads;
-  const int64_t most = dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
+// Blocks of the backward, at most what is resident at once, so that the last ones do not run alone; each
+// writes and norm_join reads 8 dim bytes.  24M elements, 512 / 768 / 1024 blocks: rows of 300 in fp16 86 / 74 /
+// 88 us, of 700 64 / 79 / 71, of 500 in fp32 108 / 121 / 115, of 16 in fp32, where a block's own sums
+// are most of the end, 136 / 110 / 104; rows of 8192 in fp16, 256 / 512: 79 / 87.
+int norm_bwd_blocks(int64_t rows, int32_t dim, int32_t dtype) {
+  const int vec = dtype == EMB_F32 ? 4 : 8;
+  const RowShape s = row_shape(dim, vec);
+  const int floats = s.vectors * vec;
+  const int64_t per = kThreads / s.threads;
+  const int64_t most = s.threads == 8 || (vec == 8 && floats == 8) ? 768 : floats < 32 ? 512 : 256;
   const int64_t b = (rows + per - 1) / per;
   return (int)(b < most ? b : most);
 }

@@ -222,6 +222,30 @@ def test_in_place():
     assert torch.equal(dr, res["dx"]) and torch.equal(dh, res["dy"]) and torch.equal(dw, res["dw_post"])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("dim", [1, 9, 17, 63, 121, 333, 777, 1501, 2051, 4093, 8191])
+def test_in_place_where_a_vector_ends_with_the_row(dim, dtype):
+    rows = 700
+    t = make(rows, dim, dtype, "row", seed=dim)
+    r, h = check_fwd(t)
+    x, y = t["x"].clone(), t["y"].clone()
+    dense.norm_gate_residual_fwd(x, y, t["gate"], t["w_post"], t["w_pre"], 0.8, 1e-6, x, y)
+    assert torch.equal(x, r) and torch.equal(y, h)
+    # no sum before r is written
+    first, x = torch.empty_like(x), t["x"].clone()
+    dense.norm_gate_residual_fwd(t["x"], None, None, None, None, 0.8, 1e-6, first, None)
+    dense.norm_gate_residual_fwd(x, None, None, None, None, 0.8, 1e-6, x, None)
+    assert torch.equal(x, first)
+    res = check_bwd(t)
+    dr, dh = t["dr"].clone(), t["dh"].clone()
+    dw, dw_pre = torch.empty(2, dim, device="cuda")
+    ws = torch.empty(dense.norm_gate_residual_bwd_workspace_bytes(rows, dim), dtype=torch.uint8, device="cuda")
+    dense.norm_gate_residual_bwd(t["r"], t["y"], t["gate"], t["w_post"], t["w_pre"], 0.8, 1e-6, dr, dh,
+                                 dr, dh, None, dw, dw_pre, ws)
+    assert torch.equal(dr, res["dx"]) and torch.equal(dh, res["dy"])
+    assert torch.equal(dw, res["dw_post"]) and torch.equal(dw_pre, res["dw_pre"])
+
+
 def test_no_rows_give_no_sums():
     t = make(0, 77, F16, "vec", seed=7)
     res = run_bwd(t, 1.0, 1e-6)
