@@ -51,7 +51,19 @@ __device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+// AGAIN, here and below: not 0 in what a kernel computes once more because its sums were not finite.  The compiler
+// would keep what both ways have in common (each address) in registers all along and spill; a lane's number that
+// comes about in another way is the second way's own.
+template <int AGAIN = 0>
+__device__ __forceinline__ int lane_id() {
+  if (AGAIN) return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 64 * AGAIN)) - 64 * AGAIN;
+  return threadIdx.x & 63;
+}
+template <int AGAIN>
+__device__ __forceinline__ int thread_id() {
+  if (AGAIN) return (__builtin_amdgcn_readfirstlane(threadIdx.x) & ~63) + lane_id<AGAIN>();
+  return threadIdx.x;
+}
 // The row of a result that register r of this lane holds.
 __device__ __forceinline__ int row_of(int r) { return 8 * (r >> 2) + 4 * (lane_id() >> 5) + (r & 3); }
 
@@ -116,7 +128,7 @@ __device__ __forceinline__ void hide_keys(const AttnArgs& a, int i, int j0, f32x
 //
 // Through registers: an odd number of pieces a row, row r of each 16 at place 4 (r % 4) + r / 4.
 // Zeros past the last row and column.
-template <typename T, int DH, int ROWS, int THREADS>
+template <typename T, int DH, int ROWS, int THREADS, int AGAIN = 0>
 struct RegisterTile {
   static constexpr int kPieces = DH / 8, kRow = DH * 2 + 16, kBytes = ROWS * kRow;
   static constexpr int kRegs = ROWS * kPieces / THREADS;
@@ -126,7 +138,7 @@ struct RegisterTile {
   struct Reads {  // where a lane reads in a tile
     int l, t;
     __device__ __forceinline__ Reads() {
-      const int n = lane_id();
+      const int n = lane_id<AGAIN>();
       l = at(n & 31, n >> 5);
       t = at(4 * (n >> 5) + ((n & 15) >> 2), ((n >> 4) & 1) * 2) + (n & 3) * 8;
     }
@@ -140,7 +152,7 @@ struct RegisterTile {
   __device__ __forceinline__ void load(char*, const T* base, int64_t stride, int row0, int end, int D) {
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
-      const int idx = threadIdx.x + n * THREADS;
+      const int idx = thread_id<AGAIN>() + n * THREADS;
       const int row = row0 + idx / kPieces, col = idx % kPieces * 8;
       r[n] = u32x4{0, 0, 0, 0};
       if (row < end && col < D) r[n] = *reinterpret_cast<const u32x4*>(base + row * stride + col);
@@ -149,7 +161,7 @@ struct RegisterTile {
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
-      const int idx = threadIdx.x + n * THREADS;
+      const int idx = thread_id<AGAIN>() + n * THREADS;
       *reinterpret_cast<u32x4*>(lds + at(idx / kPieces, idx % kPieces)) = r[n];
     }
   }
@@ -161,7 +173,7 @@ struct RegisterTile {
 // The last row stands for those past it; no query sees them, and no row past `end` is read.  Against
 // registers: no moves, no LDS writes, 32 registers fewer; forward of 16.4k tokens, 16 heads of 128,
 // window 1024: 193 -> 172 us.
-template <typename T, int DH, int ROWS, int THREADS>
+template <typename T, int DH, int ROWS, int THREADS, int AGAIN = 0>
 struct DirectTile {
   static constexpr int kPieces = DH / 8, kRow = DH * 2, kBytes = ROWS * kRow;
   static constexpr int kSpan = 16 / kPieces;  // rows in 256 bytes
@@ -173,7 +185,7 @@ struct DirectTile {
   struct Reads {
     int l[DH / 16], t[DH / 32][2];
     __device__ __forceinline__ Reads() {
-      const int n = lane_id(), row = n & 31;
+      const int n = lane_id<AGAIN>(), row = n & 31;
 #pragma unroll
       for (int ks = 0; ks < DH / 16; ++ks) l[ks] = at(row, 2 * ks + (n >> 5));
 #pragma unroll
@@ -199,7 +211,7 @@ struct DirectTile {
                  : "memory", "m0");
   }
   __device__ __forceinline__ void load(char* lds, const T* base, int64_t stride, int row0, int end, int) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(thread_id<AGAIN>() >> 6), lane = lane_id<AGAIN>();
     const int from = min(row0, end - 1), last = end - 1 - from;
     const char* p = reinterpret_cast<const char*>(base + from * stride);
 #pragma unroll
@@ -219,8 +231,9 @@ struct DirectTile {
   }
 };
 
-template <typename T, int DH, int ROWS, int THREADS, bool DIRECT>
-using TileOf = std::conditional_t<DIRECT, DirectTile<T, DH, ROWS, THREADS>, RegisterTile<T, DH, ROWS, THREADS>>;
+template <typename T, int DH, int ROWS, int THREADS, bool DIRECT, int AGAIN = 0>
+using TileOf = std::conditional_t<DIRECT, DirectTile<T, DH, ROWS, THREADS, AGAIN>,
+                                  RegisterTile<T, DH, ROWS, THREADS, AGAIN>>;
 
 // Left operand: rows row0 .. row0 + 31, columns 16 ks .. 16 ks + 15 as k.
 template <typename T, typename R>
@@ -262,7 +275,7 @@ __device__ __forceinline__ typename Vec8<T>::t right_of(const f32x16& p, int r) 
 // 8 bytes at a time, which in memory are scattered pieces of 32 rows; so rows pass through the wave's
 // part of LDS (`part`, from row `first` of a tile on) and memory sees whole ones.  Backward of 512 short
 // histories: writing results piece by piece took 23 of dq's 92 us.
-template <typename T, int DH, typename TILE>
+template <typename T, int DH, typename TILE, int AGAIN = 0>
 struct WaveRows {
   static constexpr int kPieces = DH / 8, kRegs = 32 * kPieces / 64;
   u32x4 r[kRegs];
@@ -271,7 +284,7 @@ struct WaveRows {
     const T* p = static_cast<const T*>(t.p) + tok * t.tok + head * t.head;
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
-      const int idx = lane_id() + n * 64, row = idx / kPieces, col = idx % kPieces * 8;
+      const int idx = lane_id<AGAIN>() + n * 64, row = idx / kPieces, col = idx % kPieces * 8;
       r[n] = u32x4{0, 0, 0, 0};
       if (row < rows && col < D) r[n] = *reinterpret_cast<const u32x4*>(p + row * t.tok + col);
     }
@@ -281,7 +294,7 @@ struct WaveRows {
     wave_sync();
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
-      const int idx = lane_id() + n * 64;
+      const int idx = lane_id<AGAIN>() + n * 64;
       *reinterpret_cast<u32x4*>(part + TILE::at(first + idx / kPieces, idx % kPieces)) = r[n];
     }
     wave_sync();
@@ -293,7 +306,7 @@ struct WaveRows {
                                                char* part, int first, const f32x16 (&x)[DH / 32], float by,
                                                uint32_t skip) {
     typedef T V __attribute__((ext_vector_type(4)));
-    const int own = lane_id() & 31, half = lane_id() >> 5;
+    const int own = lane_id<AGAIN>() & 31, half = lane_id<AGAIN>() >> 5;
     wave_sync();
 #pragma unroll
     for (int db = 0; db < DH / 32; ++db) {
@@ -307,7 +320,7 @@ struct WaveRows {
     T* p = static_cast<T*>(t.p) + tok * t.tok + head * t.head;
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
-      const int idx = lane_id() + n * 64, row = idx / kPieces, col = idx % kPieces * 8;
+      const int idx = lane_id<AGAIN>() + n * 64, row = idx / kPieces, col = idx % kPieces * 8;
       const u32x4 v = *reinterpret_cast<const u32x4*>(part + TILE::at(first + row, idx % kPieces));
       if (row < rows && col < D && !(skip >> row & 1)) *reinterpret_cast<u32x4*>(p + row * t.tok + col) = v;
     }
@@ -321,7 +334,7 @@ struct WaveRows {
 };
 
 // Writes a lane's row from results that hold it as a column (one per 32 of its elements).
-template <typename T, int DH>
+template <typename T, int DH, int AGAIN = 0>
 __device__ __forceinline__ void store_row(const EmbHeads& t, int64_t tok, int head, int D,
                                           const f32x16 (&x)[DH / 32], float by) {
   typedef T V __attribute__((ext_vector_type(4)));
@@ -330,7 +343,7 @@ __device__ __forceinline__ void store_row(const EmbHeads& t, int64_t tok, int he
   for (int db = 0; db < DH / 32; ++db) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int col = db * 32 + 8 * g + 4 * (lane_id() >> 5);
+      const int col = db * 32 + 8 * g + 4 * (lane_id<AGAIN>() >> 5);
       const f32x4 v = {x[db][4 * g] * by, x[db][4 * g + 1] * by, x[db][4 * g + 2] * by, x[db][4 * g + 3] * by};
       if (col < D) *reinterpret_cast<V*>(p + col) = __builtin_convertvector(v, V);
     }
@@ -339,8 +352,9 @@ __device__ __forceinline__ void store_row(const EmbHeads& t, int64_t tok, int he
 
 // ---------------------------------------------------------------- what is not finite
 // A product adds 0 * x for a pair that does not see each other, which is NaN where x is not finite.
-// A row whose sums come out not finite is therefore computed once more from the pairs that see each
-// other alone, by the whole wave, two dimensions a lane: it costs nothing while values are finite.
+// A row of out or dq whose sums come out not finite is therefore computed once more from the pairs that see
+// each other alone, by the whole wave, two dimensions a lane; dk and dv of a workgroup with add_seen, on the matrix
+// cores.  It costs nothing while values are finite.
 struct Pair {
   float a, b;
 };
@@ -374,6 +388,69 @@ __device__ __forceinline__ bool not_finite(const f32x16 (&x)[N]) {
 __device__ __forceinline__ uint32_t either(bool b) {
   const uint64_t m = __ballot(b);
   return (uint32_t)m | (uint32_t)(m >> 32);
+}
+
+// Whether any wave of a workgroup says so, and a barrier.
+template <int WAVES>
+__device__ __forceinline__ bool any_wave(bool b, uint32_t (&said)[WAVES]) {
+  const uint32_t mine = __any(b);
+  if (lane_id() == 0) said[threadIdx.x >> 6] = mine;
+  __syncthreads();
+  uint32_t all = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) all |= said[w];
+  return __builtin_amdgcn_readfirstlane(all) != 0;
+}
+
+// sum += A B over the pairs that see each other: `see` is 1 for those and 0 for the others, where B is 0 as well.
+// What A has finite goes through the product as it is.  For the rest a product of small whole numbers gives, for
+// each element, 256 times how many of its pairs see something not finite, plus the signs of what they give: +1
+// or -1 for an infinity times a number, 0 for what is NaN.
+template <typename T>
+__device__ __forceinline__ void add_seen(f32x16& sum, typename Vec8<T>::t a, typename Vec8<T>::t b,
+                                         typename Vec8<T>::t see) {
+  typedef typename Vec8<T>::t V8;
+  constexpr short kTop = std::is_same<T, _Float16>::value ? 0x7C00 : 0x7F80;  // the exponent of what is not finite
+  constexpr short kOne = std::is_same<T, _Float16>::value ? 0x3C00 : 0x3F80, kMany = kOne + 8 * (0x8000 - kTop);  // 256
+  const i16x8 x = __builtin_bit_cast(i16x8, a), y = __builtin_bit_cast(i16x8, b);
+  const i16x8 xs = x & 0x7FFF, ys = y & 0x7FFF, sign = x & (short)0x8000;
+  const i16x8 odd = xs >= kTop;  // all ones where it is so
+  sum = mma(__builtin_bit_cast(V8, (i16x8)(x & ~odd)), b, sum);
+  const u32x4 some = __builtin_bit_cast(u32x4, odd);
+  if (!__any(some[0] | some[1] | some[2] | some[3])) return;
+  f32x16 n = mma(__builtin_bit_cast(V8, (i16x8)(odd & kMany)), see, f32x16{});
+  n = mma(__builtin_bit_cast(V8, (i16x8)((xs == kTop) & (kOne | sign))),
+          __builtin_bit_cast(V8, (i16x8)((ys != 0) & (ys <= kTop) & (kOne | (y & (short)0x8000)))), n);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const float count = rintf(n[r] * (1.f / 256.f)), signs = n[r] - 256.f * count;
+    if (count > 0.f) sum[r] += fabsf(signs) == count ? copysignf(kInf, signs) : __builtin_nanf("");
+  }
+}
+// Brings gradients of scores into the range of 16 bits: x times 2^-by, and sums of such products that stand at
+// 2^-by already.  A lane has a query or a key, whose sums are its own and its partner's, so `by` is of the two;
+// it grows with the largest so far, as a running maximum does.  bf16 has the range of fp32.
+template <typename T, int N>
+__device__ __forceinline__ void fit(f32x16& x, f32x16 (&sums)[N], int& by) {
+  if constexpr (std::is_same<T, _Float16>::value) {
+    float top = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]) < kInf ? fabsf(x[r]) : 0.f);
+    const int more = max(__builtin_amdgcn_frexp_expf(swap32_max(top)) - 15 - by, 0);
+    by += more;
+    const float down = ldexpf(1.f, -more);
+#pragma unroll
+    for (int n = 0; n < N; ++n) sums[n] *= down;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[r] = ldexpf(x[r], -by);
+  }
+}
+template <int N>
+__device__ __forceinline__ void unfit(f32x16 (&sums)[N], int by) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sums[n][r] = ldexpf(sums[n][r], by);
 }
 
 // The next key that row i sees after j.
@@ -414,27 +491,6 @@ __device__ __forceinline__ void again_dq(const AttnArgs& a, int64_t begin, int i
   }
   put<T>(a.dq, begin + i, h, a.dim, o, a.scale);
 }
-// Key j's unscaled sums over rows j .. end - 1, of which it is seen by all.
-template <typename T>
-__device__ __forceinline__ void again_dkv(const AttnArgs& a, int64_t begin, int j, int end, int kh,
-                                          Pair& dk, Pair& dv) {
-  const Pair k = get<T>(a.k, begin + j, kh, a.dim), v = get<T>(a.v, begin + j, kh, a.dim);
-  const int group = a.q_heads / a.kv_heads;
-  dk = dv = Pair{0.f, 0.f};
-  for (int h = kh * group; h < (kh + 1) * group; ++h) {
-    for (int i = j; i < end; ++i) {
-      const Pair q = get<T>(a.q, begin + i, h, a.dim), d = get<T>(a.dout, begin + i, h, a.dim);
-      const int64_t stat = (int64_t)h * a.n_tok + begin + i;
-      const float p = expf(dot(q, k) * a.scale - a.lse[stat]);
-      const float ds = p * (dot(d, v) - a.delta[stat]);
-      dv.a += p * d.a;
-      dv.b += p * d.b;
-      dk.a += ds * q.a;
-      dk.b += ds * q.b;
-    }
-  }
-}
-
 // ---------------------------------------------------------------- which keys a query tile meets
 // Workgroups of four waves take query tiles from the last to the first: a sequence's first tiles meet the
 // fewest keys, and short work at the end leaves fewer units idle (16.4k tokens, 16 heads of 128, window
@@ -737,21 +793,21 @@ __device__ __forceinline__ float* first_tile_part(const AttnArgs& a, const SinkS
 }
 
 // Adds the sums of the upper half of `n` waves to those of the lower half, through LDS.
-template <int N>
+template <int AGAIN, int N>
 __device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave, int n) {
   __syncthreads();
   if (wave >= n / 2 && wave < n) {
 #pragma unroll
-    for (int k = 0; k < N * 16; ++k) lds[((wave - n / 2) * N * 16 + k) * 64 + lane_id()] = x[k >> 4][k & 15];
+    for (int k = 0; k < N * 16; ++k) lds[((wave - n / 2) * N * 16 + k) * 64 + lane_id<AGAIN>()] = x[k >> 4][k & 15];
   }
   __syncthreads();
   if (wave < n / 2) {
 #pragma unroll
-    for (int k = 0; k < N * 16; ++k) x[k >> 4][k & 15] += lds[(wave * N * 16 + k) * 64 + lane_id()];
+    for (int k = 0; k < N * 16; ++k) x[k >> 4][k & 15] += lds[(wave * N * 16 + k) * 64 + lane_id<AGAIN>()];
   }
 }
 
-template <typename T, int DH, int WAVES, bool DIRECT>
+template <typename T, int DH, int WAVES, bool DIRECT, int AGAIN = 0>
 struct DkvShape {
   typedef Group<WAVES> G;
   static constexpr bool kWide = DH == 128 && WAVES == 4;
@@ -759,7 +815,7 @@ struct DkvShape {
   static constexpr int kBlock = kWaves * 64;
   static constexpr int kShare = kWide ? 2 : 1;  // waves that share 32 keys
   static constexpr int kKeyTiles = kWide ? 2 : 0;
-  typedef TileOf<T, DH, G::kRows, kBlock, DIRECT> Tile;
+  typedef TileOf<T, DH, G::kRows, kBlock, DIRECT, AGAIN> Tile;
 };
 template <typename T, int DH, int WAVES, bool DIRECT>
 struct DkvShared {
@@ -768,15 +824,27 @@ struct DkvShared {
   char q[P::G::kBuffers][kTile], d[P::G::kBuffers][kTile];
   char k[P::kKeyTiles][kTile], v[P::kKeyTiles][kTile];
   float lse[P::G::kBuffers][P::G::kRows], delta[P::G::kBuffers][P::G::kRows];
+  uint32_t said[P::kWaves];
+  // A wave's own part, before the steps and after them: where keys and values have their tiles, or half of a
+  // buffer of queries or gradients that the first step does not use.
+  __device__ __forceinline__ char* part(int wave) {
+    if (P::kWide) return wave & 2 ? v[0] : k[0];
+    return (wave & 2 ? d : q)[P::G::kBuffers - 1];
+  }
 };
 
-// SINK: rows `row0` to `row1` - 1 against the sinks, the sums to the slot's place; otherwise those rows
-// against the 128 keys from j0.
-template <typename T, int DH, int WAVES, bool DIRECT, bool SINK>
-__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, DIRECT>& sh, const SinkSlots& parts,
-                                    const Seq& s, int kh, int j0, int row0, int row1, int64_t slot) {
+// The sums of rows `row0` to `row1` - 1 against the 128 keys from j0 (SINK: the sinks), which the first kFirst
+// waves have in the end.  Of both; or, where they came out not finite, of dk or dv AGAIN, one at a time to have
+// the registers, so that they are what the pairs that see each other make them: without the products with zero
+// of those that do not, and in fp16 with gradients of scores past 65504 brought into range.
+enum { kBoth, kDkAgain, kDvAgain };
+template <typename T, int DH, int WAVES, bool DIRECT, bool SINK, int WHAT>
+__device__ __forceinline__ void dkv_sums(const AttnArgs& a, DkvShared<T, DH, WAVES, DIRECT>& sh, const Seq& s, int kh,
+                                         int j0, int row0, int row1, f32x16 (&dk)[DH / 32], f32x16 (&dv)[DH / 32]) {
   typedef typename Vec8<T>::t V8;
-  typedef DkvShape<T, DH, WAVES, DIRECT> P;
+  constexpr int AGAIN = WHAT;
+  constexpr bool DK = WHAT != kDvAgain, DV = WHAT != kDkAgain;
+  typedef DkvShape<T, DH, WAVES, DIRECT, AGAIN> P;
   typedef typename P::Tile Tile;
   typedef Group<WAVES> G;
   constexpr int kRows = G::kRows;
@@ -784,18 +852,15 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int jrow = SINK ? 0 : 32 * (wave & 3);  // the wave's keys within the tile
   const int jw = j0 + jrow;
-  const int j = jw + (lane_id() & 31);
-  const bool live = j < s.len;
+  const int j = jw + (lane_id<AGAIN>() & 31);
   const uint32_t limit = j < a.sinks ? 0x7FFFFFFFu : (uint32_t)a.window;
 
   const typename Tile::Reads at;
-  typedef WaveRows<T, DH, Tile> Rows;
-  // the wave's own part of LDS, before the steps and after them: where keys and values have their
-  // tiles, or half of a buffer of queries or gradients
-  char* const part = P::kWide ? (wave & 2 ? sh.v[0] : sh.k[0]) : (wave & 2 ? sh.d : sh.q)[G::kBuffers - 1];
-  const int first = WAVES == 1 ? 0 : 32 * (wave & 1);
+  typedef WaveRows<T, DH, Tile, AGAIN> Rows;
   V8 k[P::kWide ? 1 : DH / 16], v[P::kWide ? 1 : DH / 16];
-  if constexpr (P::kWide) {
+  if constexpr (P::kWide && AGAIN) {
+    // they are still there
+  } else if constexpr (P::kWide) {
     const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
     const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
 #pragma unroll
@@ -808,6 +873,8 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
     }
   } else {
     // through the buffers that the first step does not use
+    char* const part = sh.part(wave);
+    const int first = WAVES == 1 ? 0 : 32 * (wave & 1);
     Rows kl, vl;
     kl.load(a.k, s.begin + jw, kh, s.len - jw, a.dim);
     vl.load(a.v, s.begin + jw, kh, s.len - jw, a.dim);
@@ -825,11 +892,11 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
     ql.load(sh.q[b], static_cast<const T*>(a.q.p) + s.begin * a.q.tok + h * a.q.head, a.q.tok, r0, row1, a.dim);
     dl.load(sh.d[b], static_cast<const T*>(a.dout.p) + s.begin * a.dout.tok + h * a.dout.head, a.dout.tok, r0,
             row1, a.dim);
-    if (threadIdx.x < 2 * kRows) {
-      const int row = r0 + (threadIdx.x & (kRows - 1));
-      const float* p = threadIdx.x < kRows ? a.lse : a.delta;
+    if (thread_id<AGAIN>() < 2 * kRows) {
+      const int row = r0 + (thread_id<AGAIN>() & (kRows - 1));
+      const float* p = thread_id<AGAIN>() < kRows ? a.lse : a.delta;
       // a row that is not there gets probabilities of zero
-      stat = threadIdx.x < kRows ? kInf : 0.f;
+      stat = thread_id<AGAIN>() < kRows ? kInf : 0.f;
       if (row < row1) stat = p[(int64_t)h * a.n_tok + s.begin + row];
     }
     next_r0 += kRows;
@@ -838,124 +905,151 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
       ++next_h;
     }
   };
-  load(0);
-  f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
-  int r0 = row0;
-  const int steps = n_tiles * group;  // of all heads of the group
-  for (int step = 0; step < steps; ++step, r0 = r0 + kRows < row1 ? r0 + kRows : row0) {
-    const int b = step & (G::kBuffers - 1);
-    if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
-    ql.store(sh.q[b]);
-    dl.store(sh.d[b]);
-    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat * kLog2e;
-    else if (threadIdx.x < 2 * kRows) sh.delta[b][threadIdx.x - kRows] = stat;
-    const int other = b ^ (G::kBuffers - 1);
-    if (!DIRECT && step + 1 < steps) load(other);
-    Tile::arrived();
-    __syncthreads();  // this step's rows are there, and the other buffer is no longer read
-    if (DIRECT && step + 1 < steps) load(other);
-    if (jw >= s.len) continue;
 #pragma unroll
-    for (int sub_ = 0; sub_ < kRows / 32 / P::kShare; ++sub_) {
-      const int sub = P::kShare == 2 ? wave >> 2 : sub_;
-      const int is = r0 + 32 * sub;
-      if (is >= row1) continue;
-      if (SINK) {
-        // rows go round the waves: by steps where a wave has a fixed half of each
-        if (P::kWaves > 1 && ((P::kShare == 2 ? step : step * 2 + sub) & 3) != (wave & 3)) continue;
-      } else if (is + 31 < jw || (jw >= a.sinks && is >= jw + 31 + (int64_t)a.window)) {
-        continue;
-      }
-      f32x16 sc = {}, dp = {};
-      if constexpr (P::kWide) {
-#pragma unroll
-        for (int ks = 0; ks < DH / 16; ++ks)
-          sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), left<T>(sh.k[jrow >> 6], at, jrow & 63, ks), sc);
-#pragma unroll
-        for (int ks = 0; ks < DH / 16; ++ks)
-          dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), left<T>(sh.v[jrow >> 6], at, jrow & 63, ks), dp);
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < DH / 16; ++ks) {
-          sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), k[ks], sc);
-          dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), v[ks], dp);
-        }
-      }
-      f32x16 p, ds;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = 32 * sub + 8 * g + 4 * (lane_id() >> 5);
-        const f32x4 lse = *reinterpret_cast<const f32x4*>(&sh.lse[b][at]);
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(&sh.delta[b][at]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -lse[e]));
-          ds[4 * g + e] = p[4 * g + e] * (dp[4 * g + e] - delta[e]);
-        }
-      }
-      if (is < jw + 31 || (int64_t)is + 31 - jw >= a.window) {
-        asm volatile("");  // see hide_keys
-        const int d = is + 4 * (lane_id() >> 5) - j;
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if ((uint32_t)(d + 8 * (r >> 2) + (r & 3)) >= limit) p[r] = ds[r] = 0.f;
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const V8 pb = right_of<T>(p, 8 * x), db_ = right_of<T>(ds, 8 * x);
-#pragma unroll
-        for (int db = 0; db < DH / 32; ++db) {
-          dv[db] = mma(left_t<T>(sh.d[b], at, 32 * sub + 16 * x, db), pb, dv[db]);
-          dk[db] = mma(left_t<T>(sh.q[b], at, 32 * sub + 16 * x, db), db_, dk[db]);
-        }
-      }
-    }
+  for (int db = 0; db < DH / 32; ++db) {
+    if (DK) dk[db] = f32x16{};
+    if (DV) dv[db] = f32x16{};
   }
+  int by = 0;  // AGAIN, in fp16: dk stands at 2^-by
   float* fold = reinterpret_cast<float*>(sh.q);  // q and d: half the waves' sums of one matrix
   static_assert(sizeof(sh.q) + sizeof(sh.d) >= sizeof(float) * P::kWaves / 2 * 32 * DH, "room to fold");
-  if constexpr (SINK) {
-    const EmbHeads row{sink_part(a, slot, kh), 0, a.dim, 0};
-    auto finish = [&](f32x16 (&x)[DH / 32], int row_at) {
+  constexpr int kFirst = SINK ? 1 : P::kWaves / P::kShare;
+  {
+    load(0);
+    int r0 = row0;
+    const int steps = n_tiles * group;  // of all heads of the group
+    for (int step = 0; step < steps; ++step, r0 = r0 + kRows < row1 ? r0 + kRows : row0) {
+      const int b = step & (G::kBuffers - 1);
+      if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
+      ql.store(sh.q[b]);
+      dl.store(sh.d[b]);
+      if (thread_id<AGAIN>() < kRows) sh.lse[b][thread_id<AGAIN>()] = stat * kLog2e;
+      else if (thread_id<AGAIN>() < 2 * kRows) sh.delta[b][thread_id<AGAIN>() - kRows] = stat;
+      const int other = b ^ (G::kBuffers - 1);
+      if (!DIRECT && step + 1 < steps) load(other);
+      Tile::arrived();
+      __syncthreads();  // this step's rows are there, and the other buffer is no longer read
+      if (DIRECT && step + 1 < steps) load(other);
+      if (jw >= s.len) continue;
 #pragma unroll
-      for (int n = P::kWaves; n > 1; n /= 2) fold_waves(x, fold, wave, n);
-      if (wave == 0 && j < a.sinks) store_row<float, DH>(row, row_at + j, 0, a.dim, x, 1.f);
-    };
-    finish(dk, 0);
-    finish(dv, a.sinks);
-  } else {
-    const bool split = a.sinks > 0 && parts.reach < s.len;
-    const EmbHeads row{split ? first_tile_part(a, parts, s, kh) : nullptr, 0, a.dim, 0};
-    // one matrix after the other; the rows of each that are not finite
-    if (P::kShare == 1) __syncthreads();  // the tiles are done with; folding sees to it otherwise
-    auto finish = [&](f32x16 (&x)[DH / 32], const EmbHeads& to, int row_at, float by) -> uint32_t {
-      if constexpr (P::kShare == 2) fold_waves(x, fold, wave, 8);
-      if (wave >= 4) return 0;
-      const uint32_t bad = either(live && not_finite(x));
-      // sinks of a sequence with chunks go to their sums
-      const uint32_t sums = split && jw == 0 ? (a.sinks == 32 ? ~0u : (1u << a.sinks) - 1) : 0;
-      if (sums >> (lane_id() & 31) & ~bad >> (lane_id() & 31) & 1)
-        store_row<float, DH>(row, row_at + j, 0, a.dim, x, 1.f);
-      Rows::store(to, s.begin + jw, kh, s.len - jw, a.dim, part, first, x, by, bad | sums);
-      return bad;
-    };
-    const uint32_t bad_k = finish(dk, a.dk, 0, a.scale);
-    const uint32_t bad_v = finish(dv, a.dv, a.sinks, 1.f);
-    for (uint32_t again = bad_k | bad_v; again; again &= again - 1) {
-      const int n = __builtin_ctz(again), x = jw + n;
-      const bool sum = split && x < a.sinks;
-      Pair pk, pv;
-      again_dkv<T>(a, s.begin, x, x < a.sinks ? row1 : (int)min((int64_t)x + a.window, (int64_t)s.len),
-                   kh, pk, pv);
-      if (bad_k >> n & 1) {
-        if (sum) put<float>(row, x, 0, a.dim, pk, 1.f);
-        else put<T>(a.dk, s.begin + x, kh, a.dim, pk, a.scale);
-      }
-      if (bad_v >> n & 1) {
-        if (sum) put<float>(row, a.sinks + x, 0, a.dim, pv, 1.f);
-        else put<T>(a.dv, s.begin + x, kh, a.dim, pv, 1.f);
+      for (int sub_ = 0; sub_ < kRows / 32 / P::kShare; ++sub_) {
+        const int sub = P::kShare == 2 ? wave >> 2 : sub_;
+        const int is = r0 + 32 * sub;
+        if (is >= row1) continue;
+        if (SINK) {
+          // rows go round the waves: by steps where a wave has a fixed half of each
+          if (P::kWaves > 1 && ((P::kShare == 2 ? step : step * 2 + sub) & 3) != (wave & 3)) continue;
+        } else if (is + 31 < jw || (jw >= a.sinks && is >= jw + 31 + (int64_t)a.window)) {
+          continue;
+        }
+        f32x16 sc = {}, dp = {};
+        if constexpr (P::kWide) {
+#pragma unroll
+          for (int ks = 0; ks < DH / 16; ++ks)
+            sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), left<T>(sh.k[jrow >> 6], at, jrow & 63, ks), sc);
+#pragma unroll
+          for (int ks = 0; ks < DH / 16; ++ks)
+            dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), left<T>(sh.v[jrow >> 6], at, jrow & 63, ks), dp);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < DH / 16; ++ks) {
+            sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), k[ks], sc);
+            dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), v[ks], dp);
+          }
+        }
+        f32x16 p, ds;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int at = 32 * sub + 8 * g + 4 * (lane_id<AGAIN>() >> 5);
+          const f32x4 lse = *reinterpret_cast<const f32x4*>(&sh.lse[b][at]);
+          const f32x4 delta = *reinterpret_cast<const f32x4*>(&sh.delta[b][at]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -lse[e]));
+            ds[4 * g + e] = p[4 * g + e] * (dp[4 * g + e] - delta[e]);
+          }
+        }
+        if constexpr (AGAIN) {
+          const int d = is + 4 * (lane_id<AGAIN>() >> 5) - j, last = row1 - 1 - j;
+          f32x16 x = DK ? ds : p;
+          V8 see[2];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int e = d + 8 * (r >> 2) + (r & 3);
+            const bool seen = (uint32_t)e < limit && e <= last;
+            see[r >> 3][r & 7] = (T)(seen ? 1.f : 0.f);
+            if (!seen) x[r] = 0.f;
+          }
+          if (DK) fit<T>(x, dk, by);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const V8 xb = right_of<T>(x, 8 * n);
+#pragma unroll
+            for (int db = 0; db < DH / 32; ++db) {
+              const V8 xa = left_t<T>(DK ? sh.q[b] : sh.d[b], at, 32 * sub + 16 * n, db);
+              add_seen<T>(DK ? dk[db] : dv[db], xa, xb, see[n]);
+            }
+          }
+          continue;
+        }
+        if (is < jw + 31 || (int64_t)is + 31 - jw >= a.window) {
+          asm volatile("");  // see hide_keys
+          const int d = is + 4 * (lane_id<AGAIN>() >> 5) - j;
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if ((uint32_t)(d + 8 * (r >> 2) + (r & 3)) >= limit) p[r] = ds[r] = 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const V8 pb = right_of<T>(p, 8 * x), db_ = right_of<T>(ds, 8 * x);
+#pragma unroll
+          for (int db = 0; db < DH / 32; ++db) {
+            dv[db] = mma(left_t<T>(sh.d[b], at, 32 * sub + 16 * x, db), pb, dv[db]);
+            dk[db] = mma(left_t<T>(sh.q[b], at, 32 * sub + 16 * x, db), db_, dk[db]);
+          }
+        }
       }
     }
   }
+  if (AGAIN && DK) unfit(dk, by);
+  // the waves' sums of the same keys, to the first of them
+#pragma unroll
+  for (int n = P::kWaves; n > kFirst; n /= 2) {
+    if (DK) fold_waves<AGAIN>(dk, fold, wave, n);
+    if (DV) fold_waves<AGAIN>(dv, fold, wave, n);
+  }
+}
+
+template <typename T, int DH, int WAVES, bool DIRECT, bool SINK>
+__device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, DIRECT>& sh, const SinkSlots& parts,
+                                    const Seq& s, int kh, int j0, int row0, int row1, int64_t slot) {
+  typedef DkvShape<T, DH, WAVES, DIRECT> P;
+  constexpr int kFirst = SINK ? 1 : P::kWaves / P::kShare;
+  f32x16 dk[DH / 32], dv[DH / 32];
+  dkv_sums<T, DH, WAVES, DIRECT, SINK, kBoth>(a, sh, s, kh, j0, row0, row1, dk, dv);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int jw = SINK ? 0 : j0 + 32 * (wave & 3), j = jw + (lane_id() & 31);
+  const bool bad = wave < kFirst && j < (SINK ? a.sinks : s.len) && (not_finite(dk) || not_finite(dv));
+  if (any_wave(bad, sh.said)) {
+    dkv_sums<T, DH, WAVES, DIRECT, SINK, kDkAgain>(a, sh, s, kh, j0, row0, row1, dk, dv);
+    __syncthreads();  // its tiles are done with
+    dkv_sums<T, DH, WAVES, DIRECT, SINK, kDvAgain>(a, sh, s, kh, j0, row0, row1, dk, dv);
+    __syncthreads();
+  }
+  if (wave >= kFirst) return;
+  // sinks of a sequence with chunks go to their sums
+  const bool split = SINK || (a.sinks > 0 && parts.reach < s.len);
+  const uint32_t sums = split && jw == 0 ? (a.sinks == 32 ? ~0u : (1u << a.sinks) - 1) : 0;
+  if (sums >> (lane_id() & 31) & 1) {
+    const EmbHeads row{SINK ? sink_part(a, slot, kh) : first_tile_part(a, parts, s, kh), 0, a.dim, 0};
+    store_row<float, DH>(row, j, 0, a.dim, dk, 1.f);
+    store_row<float, DH>(row, a.sinks + j, 0, a.dim, dv, 1.f);
+  }
+  if (SINK) return;
+  typedef WaveRows<T, DH, typename P::Tile> Rows;
+  const int first = WAVES == 1 ? 0 : 32 * (wave & 1);
+  Rows::store(a.dk, s.begin + jw, kh, s.len - jw, a.dim, sh.part(wave), first, dk, a.scale, sums);
+  Rows::store(a.dv, s.begin + jw, kh, s.len - jw, a.dim, sh.part(wave), first, dv, 1.f, sums);
 }
 
 template <typename T, int DH, int WAVES, bool DIRECT>
@@ -970,12 +1064,13 @@ __global__ void __launch_bounds__((DkvShape<T, DH, WAVES, DIRECT>::kBlock), 2)
     const Seq s = find_tile(a, slot, [&](int64_t t, int b) { return parts.first(t, b); });
     const int64_t r0 = parts.reach + (int64_t)s.tile * parts.chunk;
     if (s.tile < 0 || r0 >= s.len) return;
-    dkv<T, DH, WAVES, DIRECT, true>(a, sh, parts, s, kh, 0, (int)r0, (int)min(r0 + parts.chunk, (int64_t)s.len), slot);
+    const int row1 = (int)min(r0 + parts.chunk, (int64_t)s.len);
+    dkv<T, DH, WAVES, DIRECT, true>(a, sh, parts, s, kh, 0, (int)r0, row1, slot);
   } else {
     const Seq s = find_tile(a, slot, [](int64_t t, int b) { return t / kTokens + b; });
     if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
-    const int j0 = s.tile * kTokens;
-    dkv<T, DH, WAVES, DIRECT, false>(a, sh, parts, s, kh, j0, j0, (int)min(j0 + parts.reach, (int64_t)s.len), 0);
+    const int j0 = s.tile * kTokens, row1 = (int)min(j0 + parts.reach, (int64_t)s.len);
+    dkv<T, DH, WAVES, DIRECT, false>(a, sh, parts, s, kh, j0, j0, row1, 0);
   }
 }
 

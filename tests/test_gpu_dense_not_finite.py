@@ -1,0 +1,115 @@
+"""What is not finite in the attention's inputs, and what passes the largest number of 16 bits on the way to
+a finite result: gradients of scores over 65504 in fp16, minus infinity in a sink's key, and how long a
+call takes when nothing of its data is finite."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from ad_recommendation_amd import dense  # noqa: E402
+from oracle import dense_oracle as O  # noqa: E402
+from tests.test_gpu_dense_attn import BF16, BIG, F16, bwd, offsets, rand, within  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def forward(q, k, v, off, window, sinks, scale):
+    out, lse = torch.empty_like(q), torch.empty(q.shape[1], q.shape[0], device="cuda")
+    dense.attn_window_fwd(q, k, v, off, window, sinks, scale, out, lse)
+    return out, lse
+
+
+def largest_gradient_of_a_score(q, k, v, off, window, sinks, scale, out, lse, dout):
+    """Of p (dout . v - delta), which the kernels round to 16 bits."""
+    most, g = 0.0, q.shape[1] // k.shape[1]
+    for a, z in zip(off[:-1].tolist(), off[1:].tolist()):
+        see = O.visible(z - a, window, sinks, "cuda")
+        for h in range(q.shape[1]):
+            s = q[a:z, h].double() @ k[a:z, h // g].double().T * scale
+            p = torch.exp(s - lse[h, a:z].double()[:, None]).masked_fill(~see, 0.0)
+            do, o = dout[a:z, h].double(), out[a:z, h].double()
+            ds = p * (do @ v[a:z, h // g].double().T - (do * o).sum(1, keepdim=True))
+            most = max(most, ds.abs().max().item())
+    return most
+
+
+def test_score_gradients_past_fp16_in_rows_that_see_a_sink_alone():
+    """One window of one event and a sink: every row's gradient of the sink's score is 153600."""
+    n = 400
+    off = offsets([n])
+    q = torch.full((n, 1, 64), 0.001, dtype=F16, device="cuda")
+    k = torch.zeros_like(q)
+    v = torch.full_like(q, -8)
+    v[0] = 8
+    dout = torch.full_like(q, 600)
+    out, lse = forward(q, k, v, off, 1, 1, 0.125)
+    assert largest_gradient_of_a_score(q, k, v, off, 1, 1, 0.125, out, lse, dout) > 1.5e5
+    want = O.attn_bwd(q, k, v, off, 1, 1, 0.125, out, lse, dout)
+    got = bwd(q, k, v, off, 1, 1, 0.125, out, lse, dout)
+    within(got[0], want[0], want[3], "dq")
+    within(got[1], want[1], want[4], "dk")
+    # the sink's dv itself, 1.2e5, is past the largest number of fp16
+    assert (got[2][0] == float("inf")).all()
+    within(got[2][1:], want[2][1:], want[5][1:], "dv")
+
+
+# one wave a workgroup, four, and eight for the widest heads; tiles through registers and straight to LDS;
+# sequences that end within the sinks' reach, in it and chunks past it
+@pytest.mark.parametrize("lens,hq,hk,d,window,sinks", [
+    ([700, 40], 2, 1, 64, 40, 3), ([333], 2, 2, 24, 50, 5), ([1000, 90], 2, 1, 64, 200, 4), ([900], 1, 1, 40, 180, 2),
+    ([1300], 2, 1, 128, 60, 4), ([1250, 64], 4, 2, 104, 50, 32), ([2000], 1, 1, 32, 30, 1)])
+def test_score_gradients_past_fp16(lens, hq, hk, d, window, sinks):
+    print(f"[attn] {lens} heads {hq}/{hk} dim {d} window {window} sinks {sinks}", flush=True)
+    off = offsets(lens)
+    n = sum(lens)
+    # the results' own deviations: dv at most 1.2e4, dq and dk 1e4 (a sequence's first rows see few keys)
+    q, k = rand(n, hq, d, dtype=F16, seed=1) * 0.01, rand(n, hk, d, dtype=F16, seed=2) * 0.02
+    v, dout = rand(n, hk, d, dtype=F16, seed=3) * 60, rand(n, hq, d, dtype=F16, seed=4) * 6000
+    scale = 0.125
+    out, lse = forward(q, k, v, off, window, sinks, scale)
+    assert largest_gradient_of_a_score(q, k, v, off, window, sinks, scale, out, lse, dout) > 65504
+    want = O.attn_bwd(q, k, v, off, window, sinks, scale, out, lse, dout)
+    got = bwd(q, k, v, off, window, sinks, scale, out, lse, dout)
+    for name, g, w, b in zip(("dq", "dk", "dv"), got, want[:3], want[3:]):
+        assert w.abs().max() < 65504
+        within(g, w, b, name)
+    for g, again in zip(got, bwd(q, k, v, off, window, sinks, scale, out, lse, dout)):
+        assert torch.equal(g, again)
+
+
+@pytest.mark.parametrize("n", [608, 609, 623, 640, 700])
+@pytest.mark.parametrize("d,window", [(32, 30), (40, 150), (64, 150), (128, 30)])
+def test_minus_infinity_in_the_key_of_a_sink(d, window, n):
+    """Its score is minus infinity in every row, so it has gradients of zero, wherever its sequence ends."""
+    off = offsets([n])
+    q, k, v, dout = (rand(n, 2, d, dtype=BF16, seed=s) for s in range(4))
+    q[:, :, 0] = 1
+    k[1, :, 0] = -float("inf")
+    out, lse = forward(q, k, v, off, window, 2, 0.2)
+    assert out.isfinite().all() and lse.isfinite().all()
+    dq, dk, dv = bwd(q, k, v, off, window, 2, 0.2, out, lse, dout)
+    assert (dk[1] == 0).all() and (dv[1] == 0).all()
+    k[1] = 0
+    want = O.attn_bwd(q, k, v, off, window, 2, 0.2, out, lse, dout)
+    rest = torch.arange(n, device="cuda") != 1
+    within(dk[rest], want[1][rest], want[4][rest], "dk")
+    within(dv[rest], want[2][rest], want[5][rest], "dv")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("d,window", [(32, 30), (64, 150), (128, 30)])
+def test_a_gradient_that_is_not_finite_reaches_a_sink_from_afar(d, window, bad):
+    n, at = 900, 851
+    off = offsets([n, 100])
+    q, k, v, dout = (rand(n + 100, 2, d, dtype=BF16, seed=s) for s in range(4))
+    out, lse = forward(q, k, v, off, window, 2, 0.2)
+    want = O.attn_bwd(q, k, v, off, window, 2, 0.2, out, lse, dout)
+    dout[at, :, 3] = bad
+    dq, dk, dv = bwd(q, k, v, off, window, 2, 0.2, out, lse, dout)
+    rows = torch.arange(n + 100, device="cuda")
+    seen = (rows <= at) & ((at - rows < window) | (rows < 2))
+    within(dk[~seen], want[1][~seen], want[4][~seen], "dk")
+    within(dv[~seen], want[2][~seen], want[5][~seen], "dv")
+    within(dq[rows != at], want[0][rows != at], want[3][rows != at], "dq")
+    assert not dk[seen].isfinite().any() and not dv[seen][:, :, 3].isfinite().any()
+    others = torch.arange(d, device="cuda") != 3  # the columns of dv that are finite in every row
+    within(dv[seen][:, :, others], want[2][seen][:, :, others], want[5][seen][:, :, others], "dv")
