@@ -107,16 +107,22 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, F first) {
 // Sets x[r] to `hidden` where query i does not see key j0 + row_of(r): the distance i - j, taken as an
 // unsigned number, is below the window, or below all others for a sink.  Few tiles need it; the empty
 // statement keeps the compiler from doing it in all of them and choosing afterwards.
-__device__ __forceinline__ void hide_keys(const AttnArgs& a, int i, int j0, f32x16& x, float hidden) {
+// Returns a bit for each register whose key it sees.
+template <int AGAIN>
+__device__ __forceinline__ uint32_t hide_keys(const AttnArgs& a, int i, int j0, f32x16& x, float hidden) {
   asm volatile("");
-  const int d = i - j0 - 4 * (lane_id() >> 5);
-  const int sinks = a.sinks - j0 - 4 * (lane_id() >> 5);
+  const int half = lane_id<AGAIN>() >> 5, d = i - j0 - 4 * half, sinks = a.sinks - j0 - 4 * half;
+  uint32_t see = 0xFFFF;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     const int e = 8 * (r >> 2) + (r & 3);
     const uint32_t limit = e < sinks ? 0x7FFFFFFFu : (uint32_t)a.window;
-    if ((uint32_t)(d - e) >= limit) x[r] = hidden;
+    if ((uint32_t)(d - e) >= limit) {
+      x[r] = hidden;
+      see &= ~(1u << r);
+    }
   }
+  return see;
 }
 
 // ---------------------------------------------------------------- LDS tiles
@@ -351,49 +357,29 @@ __device__ __forceinline__ void store_row(const EmbHeads& t, int64_t tok, int he
 }
 
 // ---------------------------------------------------------------- what is not finite
-// A product adds 0 * x for a pair that does not see each other, which is NaN where x is not finite.
-// A row of out or dq whose sums come out not finite is therefore computed once more from the pairs that see
-// each other alone, by the whole wave, two dimensions a lane; dk and dv of a workgroup with add_seen, on the matrix
-// cores.  It costs nothing while values are finite.
-struct Pair {
-  float a, b;
-};
-template <typename T>
-__device__ __forceinline__ Pair get(const EmbHeads& t, int64_t tok, int h, int D) {
-  const int d = lane_id() * 2;
-  if (d >= D) return Pair{0.f, 0.f};
-  const T* p = static_cast<const T*>(t.p) + tok * t.tok + h * t.head + d;
-  return Pair{(float)p[0], (float)p[1]};
-}
-template <typename T>
-__device__ __forceinline__ void put(const EmbHeads& t, int64_t tok, int h, int D, Pair x, float by) {
-  const int d = lane_id() * 2;
-  if (d >= D) return;
-  T* p = static_cast<T*>(t.p) + tok * t.tok + h * t.head + d;
-  p[0] = (T)(x.a * by);
-  p[1] = (T)(x.b * by);
-}
-__device__ __forceinline__ float dot(Pair x, Pair y) { return lanes_sum<64>(x.a * y.a + x.b * y.b); }
-
+// A product adds 0 * x for a pair that does not see each other, which is NaN where x is not finite; and in fp16
+// the gradient of a score, which is rounded to 16 bits before its product, is infinite past 65504.  So where sums of
+// a workgroup come out not finite it computes them once more, still on the matrix cores, from the pairs that
+// see each other alone: what is finite with finite_of and fit, and what is not with add_odd.  It costs a look at
+// the sums while they are finite.  8614 tokens, 16 and 8 heads of 128, window 1024, bf16, with an infinity in
+// each row of dout, or of v: backward 1.30 ms, forward 0.43; 81 and 31 by one wave that goes over a row's pairs.
 template <int N>
 __device__ __forceinline__ bool not_finite(const f32x16 (&x)[N]) {
-  float z = 0.f;
+  float z[4] = {0.f, 0.f, 0.f, 0.f};  // four chains: a wave waits for each addition
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) z = fmaf(x[n][r], 0.f, z);
-  return z != 0.f;
+    for (int r = 0; r < 16; ++r) z[r & 3] = fmaf(x[n][r], 0.f, z[r & 3]);
+  return z[0] + z[1] + (z[2] + z[3]) != 0.f;
 }
-// Whether a lane or its partner says so: one bit for each of the 32 rows or columns.
-__device__ __forceinline__ uint32_t either(bool b) {
-  const uint64_t m = __ballot(b);
-  return (uint32_t)m | (uint32_t)(m >> 32);
-}
-
 // Whether any wave of a workgroup says so, and a barrier.
 template <int WAVES>
 __device__ __forceinline__ bool any_wave(bool b, uint32_t (&said)[WAVES]) {
   const uint32_t mine = __any(b);
+  if (WAVES == 1) {
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(mine) != 0;
+  }
   if (lane_id() == 0) said[threadIdx.x >> 6] = mine;
   __syncthreads();
   uint32_t all = 0;
@@ -402,29 +388,43 @@ __device__ __forceinline__ bool any_wave(bool b, uint32_t (&said)[WAVES]) {
   return __builtin_amdgcn_readfirstlane(all) != 0;
 }
 
-// sum += A B over the pairs that see each other: `see` is 1 for those and 0 for the others, where B is 0 as well.
-// What A has finite goes through the product as it is.  For the rest a product of small whole numbers gives, for
-// each element, 256 times how many of its pairs see something not finite, plus the signs of what they give: +1
-// or -1 for an infinity times a number, 0 for what is NaN.
+// Which of a vector's elements are not finite (all ones), and the vector without them.
+template <typename T> constexpr short kTop = std::is_same<T, _Float16>::value ? 0x7C00 : 0x7F80;  // an infinity's bits
 template <typename T>
-__device__ __forceinline__ void add_seen(f32x16& sum, typename Vec8<T>::t a, typename Vec8<T>::t b,
-                                         typename Vec8<T>::t see) {
+__device__ __forceinline__ i16x8 odd_of(typename Vec8<T>::t x) {
+  return (__builtin_bit_cast(i16x8, x) & 0x7FFF) >= kTop<T>;
+}
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::t finite_of(typename Vec8<T>::t x) {
+  return __builtin_bit_cast(typename Vec8<T>::t, (i16x8)(__builtin_bit_cast(i16x8, x) & ~odd_of<T>(x)));
+}
+// Ones where the pairs see each other, for registers r0 to r0 + 7: `see` has a bit for each.
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::t ones(uint32_t see, int r0) {
+  typename Vec8<T>::t x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (T)(see >> (r0 + i) & 1 ? 1.f : 0.f);
+  return x;
+}
+// To sum += A B, what A's elements that are not finite add.  Of B it takes `one`, 1 for the pairs that see each
+// other and 0 for the rest, and `signs`, 0 for a B of zero or of no known sign.  A product of small whole numbers
+// gives, for each element of the sum, 256 times how many of its pairs see something not finite, plus the signs of
+// what they add: +1 or -1 for an infinity times a number, 0 for what is NaN.
+template <typename T>
+__device__ __forceinline__ void add_odd(f32x16& sum, typename Vec8<T>::t a, typename Vec8<T>::t one,
+                                        typename Vec8<T>::t signs) {
   typedef typename Vec8<T>::t V8;
-  constexpr short kTop = std::is_same<T, _Float16>::value ? 0x7C00 : 0x7F80;  // the exponent of what is not finite
-  constexpr short kOne = std::is_same<T, _Float16>::value ? 0x3C00 : 0x3F80, kMany = kOne + 8 * (0x8000 - kTop);  // 256
-  const i16x8 x = __builtin_bit_cast(i16x8, a), y = __builtin_bit_cast(i16x8, b);
-  const i16x8 xs = x & 0x7FFF, ys = y & 0x7FFF, sign = x & (short)0x8000;
-  const i16x8 odd = xs >= kTop;  // all ones where it is so
-  sum = mma(__builtin_bit_cast(V8, (i16x8)(x & ~odd)), b, sum);
+  constexpr short kOne = std::is_same<T, _Float16>::value ? 0x3C00 : 0x3F80;
+  constexpr short kMany = kOne + 8 * (0x8000 - kTop<T>);  // 256
+  const i16x8 odd = odd_of<T>(a), x = __builtin_bit_cast(i16x8, a);
   const u32x4 some = __builtin_bit_cast(u32x4, odd);
   if (!__any(some[0] | some[1] | some[2] | some[3])) return;
-  f32x16 n = mma(__builtin_bit_cast(V8, (i16x8)(odd & kMany)), see, f32x16{});
-  n = mma(__builtin_bit_cast(V8, (i16x8)((xs == kTop) & (kOne | sign))),
-          __builtin_bit_cast(V8, (i16x8)((ys != 0) & (ys <= kTop) & (kOne | (y & (short)0x8000)))), n);
+  f32x16 n = mma(__builtin_bit_cast(V8, (i16x8)(odd & kMany)), one, f32x16{});
+  n = mma(__builtin_bit_cast(V8, (i16x8)(((x & 0x7FFF) == kTop<T>) & (kOne | (x & (short)0x8000)))), signs, n);
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const float count = rintf(n[r] * (1.f / 256.f)), signs = n[r] - 256.f * count;
-    if (count > 0.f) sum[r] += fabsf(signs) == count ? copysignf(kInf, signs) : __builtin_nanf("");
+    const float count = rintf(n[r] * (1.f / 256.f)), sign = n[r] - 256.f * count;
+    if (count > 0.f) sum[r] += fabsf(sign) == count ? copysignf(kInf, sign) : __builtin_nanf("");
   }
 }
 // Brings gradients of scores into the range of 16 bits: x times 2^-by, and sums of such products that stand at
@@ -453,44 +453,6 @@ __device__ __forceinline__ void unfit(f32x16 (&sums)[N], int by) {
     for (int r = 0; r < 16; ++r) sums[n][r] = ldexpf(sums[n][r], by);
 }
 
-// The next key that row i sees after j.
-__device__ __forceinline__ int next_key(const AttnArgs& a, int i, int j) {
-  ++j;
-  return j >= a.sinks && i - j >= a.window ? i - a.window + 1 : j;
-}
-template <typename T>
-__device__ __forceinline__ void again_fwd(const AttnArgs& a, int64_t begin, int i, int h, int kh) {
-  const Pair q = get<T>(a.q, begin + i, h, a.dim);
-  Pair o{0.f, 0.f};
-  float m = -kInf, l = 0.f;
-  for (int j = next_key(a, i, -1); j <= i; j = next_key(a, i, j)) {
-    const float s = dot(q, get<T>(a.k, begin + j, kh, a.dim)) * a.scale;
-    const Pair v = get<T>(a.v, begin + j, kh, a.dim);
-    const float mn = fmaxf(m, s);
-    const float by = m == -kInf ? 0.f : expf(m - mn);
-    const float p = s == -kInf ? 0.f : expf(s - mn);  // mn may be -inf as well
-    o.a = o.a * by + p * v.a;
-    o.b = o.b * by + p * v.b;
-    l = l * by + p;
-    m = mn;
-  }
-  put<T>(a.out, begin + i, h, a.dim, o, 1.f / l);
-}
-template <typename T>
-__device__ __forceinline__ void again_dq(const AttnArgs& a, int64_t begin, int i, int h, int kh) {
-  const Pair q = get<T>(a.q, begin + i, h, a.dim), d = get<T>(a.dout, begin + i, h, a.dim);
-  const int64_t stat = (int64_t)h * a.n_tok + begin + i;
-  const float delta = dot(d, get<T>(a.out, begin + i, h, a.dim)), lse = a.lse[stat];
-  Pair o{0.f, 0.f};
-  for (int j = next_key(a, i, -1); j <= i; j = next_key(a, i, j)) {
-    const Pair k = get<T>(a.k, begin + j, kh, a.dim);
-    const float p = expf(dot(q, k) * a.scale - lse);
-    const float ds = p * (dot(d, get<T>(a.v, begin + j, kh, a.dim)) - delta);
-    o.a += ds * k.a;
-    o.b += ds * k.b;
-  }
-  put<T>(a.dq, begin + i, h, a.dim, o, a.scale);
-}
 // ---------------------------------------------------------------- which keys a query tile meets
 // Workgroups of four waves take query tiles from the last to the first: a sequence's first tiles meet the
 // fewest keys, and short work at the end leaves fewer units idle (16.4k tokens, 16 heads of 128, window
@@ -515,68 +477,111 @@ struct KeyTiles {
 };
 
 // ---------------------------------------------------------------- forward
-// One pass over the keys with a running maximum and sum for each query; keys and values come by tiles
-// through LDS, queries stay in registers.  Long sequences are bound by matrix cores and exponentials, which
-// are about equally busy: 16.4k tokens, 16 query and 2 key/value heads of 128, window 1024, bf16: 164 us,
-// 780 TFLOP/s of the pairs that see each other.
+// LDS of the forward and of dq.
 template <typename T, int DH, int WAVES, bool DIRECT>
-__global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a) {
+struct QueryShared {
+  typedef Group<WAVES> G;
+  __attribute__((aligned(256))) char tile[G::kBuffers][2][RegisterTile<T, DH, G::kRows, G::kThreads>::kBytes];
+  uint32_t said[WAVES];
+  // A wave's own part of the buffers' tiles: of the last one before the steps, of the first one after them.
+  __device__ __forceinline__ char* part(int buffer) { return tile[buffer][WAVES == 1 ? 0 : wave() >> 1]; }
+  __device__ static __forceinline__ int first() { return WAVES == 1 ? 0 : 32 * (wave() & 1); }
+  __device__ static __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+};
+
+// To the wave's 32 queries' sums of what they see of x, the keys or the values, what its elements that are not
+// finite add: by weights over zero (SIGN), or by weights that are not finite either, which makes NaN.  (The score
+// of a key that is not finite is not; a value's weight of zero counts as one over zero.)
+template <typename T, int DH, int WAVES, bool DIRECT, bool SIGN>
+__device__ __forceinline__ void add_odd_seen(const AttnArgs& a, const EmbHeads& x,
+                                             QueryShared<T, DH, WAVES, DIRECT>& sh, const Seq& s, int kh, int iw,
+                                             f32x16 (&sums)[DH / 32]) {
   typedef typename Vec8<T>::t V8;
   typedef Group<WAVES> G;
-  typedef TileOf<T, DH, G::kRows, G::kThreads, DIRECT> Tile;
+  typedef TileOf<T, DH, G::kRows, G::kThreads, false, 2> Tile;
+  const int i = iw + (lane_id<2>() & 31);
+  const KeyTiles<WAVES> tiles(a, s.tile * G::kTokens, s.len);
+  const T* p = static_cast<const T*>(x.p) + s.begin * x.tok + kh * x.head;
+  const typename Tile::Reads at;
+  for (int it = 0; it < tiles.n; ++it) {
+    Tile tile;
+    __syncthreads();  // the tile before is done with
+    tile.load(sh.tile[0][0], p, x.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
+    tile.store(sh.tile[0][0]);
+    Tile::arrived();
+    __syncthreads();
+    if (iw >= s.len) continue;
+    for (int sub = 0; sub < G::kRows / 32; ++sub) {
+      f32x16 none;
+      const uint32_t see = hide_keys<2>(a, i, tiles.key0(it) + 32 * sub, none, 0.f);
+      for (int k = 0; k < 2; ++k) {
+        const V8 one = ones<T>(see >> 8 * k, 0);
+#pragma unroll
+        for (int db = 0; db < DH / 32; ++db)
+          add_odd<T>(sums[db], left_t<T>(sh.tile[0][0], at, 32 * sub + 16 * k, db), one, SIGN ? one : V8{});
+      }
+    }
+  }
+}
+
+// The sums of the values that the wave's 32 queries from iw on see, weighed by exp(score - m), and of the weights:
+// one pass over the keys with a running maximum and sum for each query.  Keys and values come by tiles through
+// LDS, queries stay in registers.  Long sequences are bound by matrix cores and exponentials, which
+// are about equally busy: 16.4k tokens, 16 query and 2 key/value heads of 128, window 1024, bf16: 164 us,
+// 780 TFLOP/s of the pairs that see each other.
+template <typename T, int DH, int WAVES, bool DIRECT, int AGAIN>
+__device__ __forceinline__ void fwd_sums(const AttnArgs& a, QueryShared<T, DH, WAVES, DIRECT>& sh, const Seq& s, int h,
+                                         int kh, int iw, float c, f32x16 (&o)[DH / 32], float& m, float& l) {
+  typedef typename Vec8<T>::t V8;
+  typedef Group<WAVES> G;
+  constexpr bool kDirect = DIRECT && !AGAIN;
+  typedef TileOf<T, DH, G::kRows, G::kThreads, kDirect, AGAIN> Tile;
+  constexpr int kBytes = sizeof(sh.tile[0][0]);
   constexpr int kSubs = G::kRows / 32;
-  __shared__ __attribute__((aligned(1024))) char lds[G::kBuffers][2][Tile::kBytes];
-  const int group = a.q_heads / a.kv_heads;
-  const int block = WAVES == 1 ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
-  const int kh = block % a.kv_heads;
-  const int rest = block / a.kv_heads;
-  const int h = kh * group + rest % group;
-  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
-  if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
-  const int i0 = s.tile * G::kTokens;
-  const int iw = __builtin_amdgcn_readfirstlane(i0 + (threadIdx.x >> 6) * 32);
-  const int i = iw + (lane_id() & 31);
-  const bool live = i < s.len;
-
-  const int rows = s.len - iw;  // of the wave's 32 queries
-  typedef WaveRows<T, DH, Tile> Rows;
+  const int i = iw + (lane_id<AGAIN>() & 31);
+  typedef WaveRows<T, DH, Tile, AGAIN> Rows;
   Rows ql;
-  ql.load(a.q, s.begin + iw, h, a.scale != 0.f ? rows : 0, a.dim);
+  ql.load(a.q, s.begin + iw, h, a.scale != 0.f ? s.len - iw : 0, a.dim);
 
-  const KeyTiles<WAVES> tiles(a, i0, s.len);
+  const KeyTiles<WAVES> tiles(a, s.tile * G::kTokens, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
   Tile kl, vl;
-  auto load = [&](int it, char (*to)[Tile::kBytes]) {
+  auto load = [&](int it, char (*to)[kBytes]) {
     kl.load(to[0], kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
     vl.load(to[1], vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
   };
-  load(0, lds[0]);
+  load(0, sh.tile[0]);
   const typename Tile::Reads at;
-  // the wave's own part of the buffers: of the last one before the tiles, of the first one after them
-  const int part = WAVES == 1 ? 0 : threadIdx.x >> 7, first = WAVES == 1 ? 0 : 32 * (threadIdx.x >> 6 & 1);
   V8 q[DH / 16];
-  ql.to_right(lds[G::kBuffers - 1][part], first, at, q);
+  ql.to_right(sh.part(G::kBuffers - 1), sh.first(), at, q);
   // the running maximum is one of q . k, so a negative scale turns q around and a scale of zero
   // leaves zeros
   if (a.scale < 0.f) {
 #pragma unroll
     for (int ks = 0; ks < DH / 16; ++ks) q[ks] = -q[ks];
   }
-  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
 
-  f32x16 o[DH / 32] = {};
-  float m = -kInf, l = 0.f;  // the maximum that o and l stand at, and this lane's half of the sum
-  auto meet = [&](int it, char (*lds_now)[Tile::kBytes], char (*lds_next)[Tile::kBytes]) {
+#pragma unroll
+  for (int db = 0; db < DH / 32; ++db) o[db] = f32x16{};
+  m = -kInf;  // the maximum that o and l stand at
+  l = 0.f;    // this lane's half of the sum
+  auto meet = [&](int it, char (*lds_now)[kBytes], char (*lds_next)[kBytes]) {
     const char* kt = lds_now[0];
     const char* vt = lds_now[1];
     if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
+    if (AGAIN && it) load(it, lds_now);
     kl.store(lds_now[0]);
+    if constexpr (AGAIN != 0) {
+#pragma unroll
+      for (int x = 0; x < Tile::kRegs; ++x)
+        vl.r[x] = __builtin_bit_cast(u32x4, finite_of<T>(__builtin_bit_cast(V8, vl.r[x])));
+    }
     vl.store(lds_now[1]);
-    if (!DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
+    if (!kDirect && !AGAIN && it + 1 < tiles.n) load(it + 1, lds_next);
     Tile::arrived();
     __syncthreads();  // this tile is there, and the other buffer is no longer read
-    if (DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
+    if (kDirect && it + 1 < tiles.n) load(it + 1, lds_next);
     const int j0 = tiles.key0(it);
     if (iw >= s.len || j0 > iw + 31) return;
     if (j0 >= a.sinks && j0 + G::kRows - 1 <= iw - a.window) return;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
 #pragma unroll
     for (int sub = 0; sub < kSubs; ++sub) {
       const int js = j0 + 32 * sub;
-      if (js + 31 > iw || js < iw + 31 - a.window + 1) hide_keys(a, i, js, sc[sub], -kInf);
+      if (js + 31 > iw || js < iw + 31 - a.window + 1) hide_keys<AGAIN>(a, i, js, sc[sub], -kInf);
     }
     float top = sc[0][0];
 #pragma unroll
@@ -621,29 +626,23 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_fwd(AttnArgs a
   };
   // two tiles a turn, so that the buffers' places are constants
   for (int it = 0; it < tiles.n; it += 2) {
-    meet(it, lds[0], lds[G::kBuffers - 1]);
-    if (it + 1 < tiles.n) meet(it + 1, lds[G::kBuffers - 1], lds[0]);
+    meet(it, sh.tile[0], sh.tile[G::kBuffers - 1]);
+    if (it + 1 < tiles.n) meet(it + 1, sh.tile[G::kBuffers - 1], sh.tile[0]);
   }
   l = swap32_sum(l);
-  uint32_t again = either(live && not_finite(o));
-  __syncthreads();  // the tiles are done with
-  Rows::store(a.out, s.begin + iw, h, rows, a.dim, lds[0][part], first, o, 1.f / l, again);
-  if (live && a.lse && lane_id() < 32)
-    a.lse[(int64_t)h * a.n_tok + s.begin + i] = m * c * kLn2 + logf(l);
-  for (; again; again &= again - 1) again_fwd<T>(a, s.begin, iw + __builtin_ctz(again), h, kh);
 }
 
-// ---------------------------------------------------------------- backward: dq
-// As the forward, with dout as a second right operand; also writes delta.  8.2k tokens, 16 and 8 heads of
-// 128, window 1024, bf16: 114 us, 790 TFLOP/s, bound as the forward is.  512 histories of up to 200, 8 heads
-// of 64, window 64, fp16: 70 us, 3.3 TB/s.  (Three waves a SIMD there, by four registers spilled: 74 us.)
+// Waves of a SIMD that the forward and dq have registers for without their second way, whose code would otherwise
+// take more: 400 events a sequence, window 300, 8 heads of 64, forward 70 us instead of 51.
+template <int DH, int WAVES, bool DIRECT>
+constexpr int fwd_waves = DH == 128 ? 2 : DH == 64 ? (WAVES == 4 && DIRECT ? 4 : 3) : WAVES == 1 ? 5 : 4;
+template <int DH>
+constexpr int dq_waves = DH == 128 ? 2 : DH == 64 ? 3 : 4;
+
 template <typename T, int DH, int WAVES, bool DIRECT>
-__global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a) {
-  typedef typename Vec8<T>::t V8;
+__global__ void __launch_bounds__(Group<WAVES>::kThreads, (fwd_waves<DH, WAVES, DIRECT>)) attn_fwd(AttnArgs a) {
   typedef Group<WAVES> G;
-  typedef TileOf<T, DH, G::kRows, G::kThreads, DIRECT> Tile;
-  constexpr int kSubs = G::kRows / 32;
-  __shared__ __attribute__((aligned(1024))) char lds[G::kBuffers][2][Tile::kBytes];
+  __shared__ QueryShared<T, DH, WAVES, DIRECT> sh;
   const int group = a.q_heads / a.kv_heads;
   const int block = WAVES == 1 ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
   const int kh = block % a.kv_heads;
@@ -651,36 +650,64 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a)
   const int h = kh * group + rest % group;
   const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
   if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
-  const int i0 = s.tile * G::kTokens;
-  const int iw = __builtin_amdgcn_readfirstlane(i0 + (threadIdx.x >> 6) * 32);
+  const int iw = __builtin_amdgcn_readfirstlane(s.tile * G::kTokens + (threadIdx.x >> 6) * 32);
+  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+  f32x16 o[DH / 32];
+  float m, l;
+  fwd_sums<T, DH, WAVES, DIRECT, 0>(a, sh, s, h, kh, iw, c, o, m, l);
   const int i = iw + (lane_id() & 31);
+  if (any_wave(i < s.len && not_finite(o), sh.said)) {
+    fwd_sums<T, DH, WAVES, DIRECT, 1>(a, sh, s, h, kh, iw, c, o, m, l);
+    add_odd_seen<T, DH, WAVES, DIRECT, true>(a, a.v, sh, s, kh, iw, o);
+    __syncthreads();  // the tiles are done with
+  }
+  constexpr int kOwn = DIRECT ? 3 : 0;  // addresses of its own: the kernel of 64-wide heads has no register over
+  typedef WaveRows<T, DH, TileOf<T, DH, G::kRows, G::kThreads, DIRECT, kOwn>, kOwn> Rows;
+  Rows::store(a.out, s.begin + iw, h, s.len - iw, a.dim, sh.part(0), sh.first(), o, 1.f / l, 0);
+  if (i < s.len && a.lse && lane_id() < 32) a.lse[(int64_t)h * a.n_tok + s.begin + i] = m * c * kLn2 + logf(l);
+}
+
+// ---------------------------------------------------------------- backward: dq
+// As the forward, with dout as a second right operand: unscaled sums of the gradients that the wave's 32 queries
+// from iw on have; also writes delta.  8.2k tokens, 16 and 8 heads of 128, window 1024, bf16: 114 us, 790 TFLOP/s,
+// bound as the forward is.  512 histories of up to 200, 8 heads of 64, window 64, fp16: 70 us, 3.3 TB/s.
+template <typename T, int DH, int WAVES, bool DIRECT, int AGAIN>
+__device__ __forceinline__ void dq_sums(const AttnArgs& a, QueryShared<T, DH, WAVES, DIRECT>& sh, const Seq& s, int h,
+                                        int kh, int iw, f32x16 (&dq)[DH / 32]) {
+  typedef typename Vec8<T>::t V8;
+  typedef Group<WAVES> G;
+  constexpr bool kDirect = DIRECT && !AGAIN;
+  typedef TileOf<T, DH, G::kRows, G::kThreads, kDirect, AGAIN> Tile;
+  constexpr int kBytes = sizeof(sh.tile[0][0]);
+  constexpr int kSubs = G::kRows / 32;
+  const int i = iw + (lane_id<AGAIN>() & 31);
   const bool live = i < s.len;
 
   const int rows = s.len - iw;  // of the wave's 32 queries
-  typedef WaveRows<T, DH, Tile> Rows;
+  typedef WaveRows<T, DH, Tile, AGAIN> Rows;
   Rows ql, dl, ol;
   ql.load(a.q, s.begin + iw, h, rows, a.dim);
   dl.load(a.dout, s.begin + iw, h, rows, a.dim);
   ol.load(a.out, s.begin + iw, h, rows, a.dim);
-  const KeyTiles<WAVES> tiles(a, i0, s.len);
+  const KeyTiles<WAVES> tiles(a, s.tile * G::kTokens, s.len);
   const T* kp = static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head;
   Tile kl, vl;
-  auto load = [&](int it, char (*to)[Tile::kBytes]) {
+  auto load = [&](int it, char (*to)[kBytes]) {
     kl.load(to[0], kp, a.k.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
     vl.load(to[1], vp, a.v.tok, tiles.key0(it), tiles.end(a, it, s.len), a.dim);
   };
-  load(0, lds[0]);
+  load(0, sh.tile[0]);
   const typename Tile::Reads at;
 
-  const int part = WAVES == 1 ? 0 : threadIdx.x >> 7, first = WAVES == 1 ? 0 : 32 * (threadIdx.x >> 6 & 1);
+  char* const part = sh.part(G::kBuffers - 1);
   V8 q[DH / 16], d[DH / 16];
-  ql.to_right(lds[G::kBuffers - 1][part], first, at, q);
-  dl.to_right(lds[G::kBuffers - 1][part], first, at, d);
+  ql.to_right(part, sh.first(), at, q);
+  dl.to_right(part, sh.first(), at, d);
   float delta = 0.f;
   {
     V8 out[DH / 16];
-    ol.to_right(lds[G::kBuffers - 1][part], first, at, out);
+    ol.to_right(part, sh.first(), at, out);
 #pragma unroll
     for (int ks = 0; ks < DH / 16; ++ks)
 #pragma unroll
@@ -688,21 +715,24 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a)
     delta = swap32_sum(delta);
   }
   const int64_t stat = (int64_t)h * a.n_tok + s.begin + i;
-  if (live && lane_id() < 32) a.delta[stat] = delta;
+  if (live && lane_id<AGAIN>() < 32) a.delta[stat] = delta;
   const float c = a.scale * kLog2e;
   const float lse = live ? a.lse[stat] * kLog2e : kInf;
 
-  f32x16 dq[DH / 32] = {};
-  auto meet = [&](int it, char (*lds_now)[Tile::kBytes], char (*lds_next)[Tile::kBytes]) {
+#pragma unroll
+  for (int db = 0; db < DH / 32; ++db) dq[db] = f32x16{};
+  int by = 0;  // AGAIN, in fp16: dq stands at 2^-by
+  auto meet = [&](int it, char (*lds_now)[kBytes], char (*lds_next)[kBytes]) {
     const char* kt = lds_now[0];
     const char* vt = lds_now[1];
     if (G::kBuffers == 1) __syncthreads();  // of one wave: its reads of the tile before have ended
+    if (AGAIN && it) load(it, lds_now);
     kl.store(lds_now[0]);
     vl.store(lds_now[1]);
-    if (!DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
+    if (!kDirect && !AGAIN && it + 1 < tiles.n) load(it + 1, lds_next);
     Tile::arrived();
     __syncthreads();  // this tile is there, and the other buffer is no longer read
-    if (DIRECT && it + 1 < tiles.n) load(it + 1, lds_next);
+    if (kDirect && it + 1 < tiles.n) load(it + 1, lds_next);
     const int j0 = tiles.key0(it);
     if (iw >= s.len) return;
 #pragma unroll
@@ -719,25 +749,49 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, 2) attn_dq(AttnArgs a)
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         ds[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -lse)) * (dp[r] - delta);
-      if (js + 31 > iw || js < iw + 31 - a.window + 1) hide_keys(a, i, js, ds, 0.f);
+      if (js + 31 > iw || js < iw + 31 - a.window + 1) hide_keys<AGAIN>(a, i, js, ds, 0.f);
+      if constexpr (AGAIN != 0) fit<T>(ds, dq, by);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const V8 b = right_of<T>(ds, 8 * k);
 #pragma unroll
-        for (int db = 0; db < DH / 32; ++db)
-          dq[db] = mma(left_t<T>(kt, at, 32 * sub + 16 * k, db), b, dq[db]);
+        for (int db = 0; db < DH / 32; ++db) {
+          V8 x = left_t<T>(kt, at, 32 * sub + 16 * k, db);
+          if (AGAIN) x = finite_of<T>(x);
+          dq[db] = mma(x, b, dq[db]);
+        }
       }
     }
   };
   // two tiles a turn, so that the buffers' places are constants
   for (int it = 0; it < tiles.n; it += 2) {
-    meet(it, lds[0], lds[G::kBuffers - 1]);
-    if (it + 1 < tiles.n) meet(it + 1, lds[G::kBuffers - 1], lds[0]);
+    meet(it, sh.tile[0], sh.tile[G::kBuffers - 1]);
+    if (it + 1 < tiles.n) meet(it + 1, sh.tile[G::kBuffers - 1], sh.tile[0]);
   }
-  uint32_t again = either(live && not_finite(dq));
-  __syncthreads();  // the tiles are done with
-  Rows::store(a.dq, s.begin + iw, h, rows, a.dim, lds[0][part], first, dq, a.scale, again);
-  for (; again; again &= again - 1) again_dq<T>(a, s.begin, iw + __builtin_ctz(again), h, kh);
+  if constexpr (AGAIN != 0) unfit(dq, by);
+}
+
+template <typename T, int DH, int WAVES, bool DIRECT>
+__global__ void __launch_bounds__(Group<WAVES>::kThreads, (dq_waves<DH>)) attn_dq(AttnArgs a) {
+  typedef Group<WAVES> G;
+  __shared__ QueryShared<T, DH, WAVES, DIRECT> sh;
+  const int group = a.q_heads / a.kv_heads;
+  const int block = WAVES == 1 ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
+  const int kh = block % a.kv_heads;
+  const int rest = block / a.kv_heads;
+  const int h = kh * group + rest % group;
+  const Seq s = find_tile(a, rest / group, [](int64_t t, int b) { return t / G::kTokens + b; });
+  if (s.tile < 0 || (int64_t)s.tile * G::kTokens >= s.len) return;
+  const int iw = __builtin_amdgcn_readfirstlane(s.tile * G::kTokens + (threadIdx.x >> 6) * 32);
+  f32x16 dq[DH / 32];
+  dq_sums<T, DH, WAVES, DIRECT, 0>(a, sh, s, h, kh, iw, dq);
+  if (__builtin_expect(any_wave(iw + (lane_id() & 31) < s.len && not_finite(dq), sh.said), 0)) {
+    dq_sums<T, DH, WAVES, DIRECT, 1>(a, sh, s, h, kh, iw, dq);
+    add_odd_seen<T, DH, WAVES, DIRECT, false>(a, a.k, sh, s, kh, iw, dq);
+    __syncthreads();  // the tiles are done with
+  }
+  typedef WaveRows<T, DH, TileOf<T, DH, G::kRows, G::kThreads, DIRECT, 3>, 3> Rows;
+  Rows::store(a.dq, s.begin + iw, h, s.len - iw, a.dim, sh.part(0), sh.first(), dq, a.scale, 0);
 }
 
 // ---------------------------------------------------------------- backward: dk, dv
@@ -972,22 +1026,26 @@ __device__ __forceinline__ void dkv_sums(const AttnArgs& a, DkvShared<T, DH, WAV
         if constexpr (AGAIN) {
           const int d = is + 4 * (lane_id<AGAIN>() >> 5) - j, last = row1 - 1 - j;
           f32x16 x = DK ? ds : p;
-          V8 see[2];
+          uint32_t see = 0;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int e = d + 8 * (r >> 2) + (r & 3);
-            const bool seen = (uint32_t)e < limit && e <= last;
-            see[r >> 3][r & 7] = (T)(seen ? 1.f : 0.f);
-            if (!seen) x[r] = 0.f;
+            if ((uint32_t)e < limit && e <= last) see |= 1u << r;
+            else x[r] = 0.f;
           }
           if (DK) fit<T>(x, dk, by);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const V8 xb = right_of<T>(x, 8 * n);
+            const V8 xb = right_of<T>(x, 8 * n), one = ones<T>(see, 8 * n);
+            V8 signs;  // in fp32 a small weight is not 0
+#pragma unroll
+            for (int e = 0; e < 8; ++e) signs[e] = (T)(x[8 * n + e] > 0.f ? 1.f : x[8 * n + e] < 0.f ? -1.f : 0.f);
 #pragma unroll
             for (int db = 0; db < DH / 32; ++db) {
+              f32x16& sum = DK ? dk[db] : dv[db];
               const V8 xa = left_t<T>(DK ? sh.q[b] : sh.d[b], at, 32 * sub + 16 * n, db);
-              add_seen<T>(DK ? dk[db] : dv[db], xa, xb, see[n]);
+              sum = mma(finite_of<T>(xa), xb, sum);
+              add_odd<T>(sum, xa, one, signs);
             }
           }
           continue;
@@ -1029,8 +1087,8 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
   dkv_sums<T, DH, WAVES, DIRECT, SINK, kBoth>(a, sh, s, kh, j0, row0, row1, dk, dv);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int jw = SINK ? 0 : j0 + 32 * (wave & 3), j = jw + (lane_id() & 31);
-  const bool bad = wave < kFirst && j < (SINK ? a.sinks : s.len) && (not_finite(dk) || not_finite(dv));
-  if (any_wave(bad, sh.said)) {
+  const bool odd = not_finite(dk) | not_finite(dv), bad = wave < kFirst && j < (SINK ? a.sinks : s.len) && odd;
+  if (__builtin_expect(any_wave(bad, sh.said), 0)) {
     dkv_sums<T, DH, WAVES, DIRECT, SINK, kDkAgain>(a, sh, s, kh, j0, row0, row1, dk, dv);
     __syncthreads();  // its tiles are done with
     dkv_sums<T, DH, WAVES, DIRECT, SINK, kDvAgain>(a, sh, s, kh, j0, row0, row1, dk, dv);

@@ -113,3 +113,97 @@ def test_a_gradient_that_is_not_finite_reaches_a_sink_from_afar(d, window, bad):
     assert not dk[seen].isfinite().any() and not dv[seen][:, :, 3].isfinite().any()
     others = torch.arange(d, device="cuda") != 3  # the columns of dv that are finite in every row
     within(dv[seen][:, :, others], want[2][seen][:, :, others], want[5][seen][:, :, others], "dv")
+
+
+def sprinkled(x, seed):
+    """x with infinities of either sign and NaN in one element of fifty, and where: +1, -1, 2 for NaN."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    kind = torch.randint(0, 150, x.shape, generator=g, device="cuda")
+    bad = torch.where(kind == 0, 1, torch.where(kind == 1, -1, torch.where(kind == 2, 2, 0)))
+    inf, nan = torch.full_like(x, float("inf")), torch.full_like(x, float("nan"))
+    return torch.where(bad == 1, inf, torch.where(bad == -1, -inf, torch.where(bad == 2, nan, x))), bad
+
+
+def check_sprinkled(got, want, bound, see, bad, what):
+    """got [rows, dim] sums over what `see` [rows, others] shows each row, each with a weight over zero, of `bad`
+    [others, dim]: finite where a row sees nothing else, infinite where it sees infinities of one sign."""
+    n = lambda k: (see.double() @ (bad == k).double()) > 0  # noqa: E731
+    plus, minus, nan = n(1), n(-1), n(2)
+    fine = ~(plus | minus | nan)
+    assert fine.any() and plus.any() and minus.any() and nan.any()
+    assert got[fine].isfinite().all(), what
+    err = (got.double() - want).abs() - bound
+    assert err[fine].max() <= 0, what
+    assert (got[plus & ~minus & ~nan] == float("inf")).all() and (got[minus & ~plus & ~nan] == -float("inf")).all(), what
+    assert got[nan | (plus & minus)].isnan().all(), what
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("n,d,window,sinks", [(300, 32, 9, 1), (450, 64, 40, 0), (700, 64, 140, 2), (600, 40, 150, 1),
+                                              (400, 128, 17, 1), (333, 104, 60, 0)])
+def test_many_elements_that_are_not_finite(n, d, window, sinks, dtype):
+    """Each reaches its column of the rows that see it, as the formula has it, and nothing else."""
+    off = offsets([50, n])
+    q, k, v, dout = (rand(50 + n, 2, d, dtype=dtype, seed=s) for s in range(4))
+    see = torch.zeros(50 + n, 50 + n, dtype=torch.bool, device="cuda")
+    see[:50, :50], see[50:, 50:] = O.visible(50, window, sinks, "cuda"), O.visible(n, window, sinks, "cuda")
+    scale = 0.1 * d ** -0.5
+    out, lse = forward(q, k, v, off, window, sinks, scale)
+    odd, bad = sprinkled(v, 7)
+    got, lse2 = forward(q, k, odd, off, window, sinks, scale)
+    assert torch.equal(lse, lse2)
+    for h in range(2):
+        only = torch.where(bad == 0, v, 0)
+        want, _, bound, _ = O.attn_fwd(q, k, only, off, window, sinks, scale)
+        check_sprinkled(got[:, h], want[:, h], bound[:, h], see, bad[:, h], "out")
+    odd, bad = sprinkled(dout, 8)
+    dq, dk, dv = bwd(q, k, v, off, window, sinks, scale, out, lse, odd)
+    rows = (bad == 0).all(-1)
+    assert rows.any() and not rows.all()
+    finite = torch.where(rows[:, :, None], dout, 0)
+    want = O.attn_bwd(q, k, v, off, window, sinks, scale, out, lse, finite)
+    only = torch.where(bad == 0, dout, 0)
+    values = O.attn_bwd(q, k, v, off, window, sinks, scale, out, lse, only)
+    for h in range(2):
+        within(dq[rows[:, h], h], want[0][rows[:, h], h], want[3][rows[:, h], h], "dq")
+        assert not dq[~rows[:, h], h].isfinite().any()
+        check_sprinkled(dv[:, h], values[2][:, h], values[5][:, h], see.T, bad[:, h], "dv")
+        fine = ~(see.T.double() @ (~rows[:, h]).double()).bool()
+        if fine.any():
+            within(dk[fine, h], want[1][fine, h], want[4][fine, h], "dk")
+        assert not dk[~fine, h].isfinite().any()
+
+
+def milliseconds(f):
+    f()
+    best = float("inf")
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,window,dtype", [
+    ([1500], 4, 4, 64, BIG, F16), ([2000, 900], 8, 2, 128, 512, BF16), ([80] * 200, 4, 4, 64, 64, F16)])
+def test_calls_on_what_is_not_finite_are_not_slow(lens, hq, hk, d, window, dtype):
+    """A step whose gradients overflowed, or whose weights are NaN: a few passes over the data instead of one
+    (pair by pair by one wave it was some hundreds)."""
+    n, off = sum(lens), offsets(lens)
+    q, k, v, dout = (rand(n, h, d, dtype=dtype, seed=s) for s, h in enumerate((hq, hk, hk, hq)))
+    out, lse = forward(q, k, v, off, window, 3, 0.1)
+    res = [torch.empty_like(x) for x in (q, k, v)]
+    ws = torch.empty(dense.attn_window_bwd_workspace_bytes(n, len(lens), hq, hk, d, 3), dtype=torch.uint8, device="cuda")
+    fwd = lambda: dense.attn_window_fwd(q, k, v, off, window, 3, 0.1, out, lse)  # noqa: E731
+    back = lambda: dense.attn_window_bwd(q, k, v, off, window, 3, 0.1, out, lse, dout, *res, ws)  # noqa: E731
+    usual = milliseconds(fwd), milliseconds(back)
+    dout[:, :, 5] = float("inf")
+    assert milliseconds(back) < 12 * usual[1] + 0.1
+    v[:, :, 3] = float("inf")
+    assert milliseconds(fwd) < 12 * usual[0] + 0.1
+    q.fill_(float("nan"))
+    assert milliseconds(fwd) < 12 * usual[0] + 0.1
+    assert milliseconds(back) < 12 * usual[1] + 0.1
