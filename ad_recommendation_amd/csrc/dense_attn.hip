@@ -1410,6 +1410,27 @@ bool one_wave(const AttnArgs& a) {
 
 }  // namespace
 
+// Whether a sequence of the batch may be longer than reach.
+bool has_chunks(const AttnArgs& a, const SinkSlots& n) { return a.sinks > 0 && a.n_tok > n.reach; }
+
+// Threads of a call's largest launch: two for each token that a slot has room for, four in dk/dv of wide heads.
+int64_t attn_fwd_threads(const AttnArgs& a) {
+  const int64_t tokens = one_wave(a) ? 32 : 128;
+  return (a.n_tok / tokens + a.n_seq) * a.q_heads * 2 * tokens;
+}
+int64_t attn_bwd_threads(const AttnArgs& a) {
+  const int64_t tokens = one_wave(a) ? 32 : 128;
+  const SinkSlots n(a.n_tok, a.n_seq, a.window, (int)tokens, sink_chunk(a.n_tok));
+  const int64_t slots = a.n_tok / tokens + a.n_seq + (has_chunks(a, n) ? n.chunk_slots : 0);
+  const int64_t dkv = slots * a.kv_heads * (a.dim <= 64 ? 2 : 4) * tokens;
+  const int64_t join = has_chunks(a, n) ? n.numbers * kThreads : 0;
+  return std::max({attn_fwd_threads(a), dkv, join});
+}
+int64_t attn_decode_threads(const AttnArgs& a, const AttnDecodePlan& p) {
+  const int64_t cols = (a.q_heads / a.kv_heads + 31) / 32;
+  return (int64_t)a.n_seq * 64 * std::max<int64_t>(a.kv_heads * cols * p.splits * p.waves, a.q_heads);
+}
+
 AttnBwdPlan plan_attn_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok) {
   AttnBwdPlan p{};
   p.off_part = ((size_t)n_tok * a.q_heads * sizeof(float) + 255) & ~(size_t)255;
@@ -1449,23 +1470,30 @@ void go_fwd(const AttnArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((attn_fwd<T, DH, WAVES, DIRECT>), dim3(grid), dim3(G::kThreads), 0, st, a);
 }
 
+// A launch that fails is the last one: what comes after it would read what it did not write.
 template <typename T, int DH, int WAVES, bool DIRECT>
-void go_bwd(const AttnArgs& a, hipStream_t st) {
+hipError_t go_bwd(const AttnArgs& a, hipStream_t st) {
   typedef Group<WAVES> G;
   const int64_t slots = a.n_tok / G::kTokens + a.n_seq;
   hipLaunchKernelGGL((attn_dq<T, DH, WAVES, DIRECT>), dim3((unsigned)(slots * a.q_heads)), dim3(G::kThreads), 0,
                      st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const SinkSlots n(a.n_tok, a.n_seq, a.window, G::kTokens, sink_chunk(a.n_tok));
-  const bool sinks = a.sinks > 0 && a.n_tok > n.reach;  // a sequence may be longer than reach
+  const bool sinks = has_chunks(a, n);
   hipLaunchKernelGGL((attn_dkv<T, DH, WAVES, DIRECT>),
                      dim3((unsigned)((slots + (sinks ? n.chunk_slots : 0)) * a.kv_heads)),
                      dim3(DkvShape<T, DH, WAVES, DIRECT>::kBlock), 0, st, a, (int)(slots * a.kv_heads), n);
-  if (sinks)
+  e = hipGetLastError();
+  if (sinks && e == hipSuccess) {
     hipLaunchKernelGGL((attn_sink_join<T>),
                        dim3((unsigned)n.numbers,
                             (unsigned)((2 * a.sinks * a.dim * a.kv_heads + kThreads * kJoinEach - 1) /
                                        (kThreads * kJoinEach))),
                        dim3(kThreads), 0, st, a, n);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 // Whether tiles may be loaded straight to LDS: whole rows of the kernel's width, and a tile's rows
@@ -1490,16 +1518,20 @@ hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
+  hipError_t e = hipSuccess;
   by_shape(a, [&](auto t, auto d) {
     typedef decltype(t) T;
     constexpr int DH = decltype(d)::value;
     if constexpr (DH < 128) {
-      if (one_wave(a)) return go_bwd<T, DH, 1, false>(a, st);
+      if (one_wave(a)) {
+        e = go_bwd<T, DH, 1, false>(a, st);
+        return;
+      }
     }
-    if (direct(a, DH, {&a.q, &a.k, &a.v, &a.dout})) go_bwd<T, DH, 4, true>(a, st);
-    else go_bwd<T, DH, 4, false>(a, st);
+    if (direct(a, DH, {&a.q, &a.k, &a.v, &a.dout})) e = go_bwd<T, DH, 4, true>(a, st);
+    else e = go_bwd<T, DH, 4, false>(a, st);
   });
-  return hipGetLastError();
+  return e;
 }
 
 template <typename T, int DH, int WAVES>
@@ -1510,16 +1542,20 @@ void go_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStream_t st) {
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStream_t st) {
+  hipError_t e = hipSuccess;
   by_shape(a, [&](auto t, auto d) {
     typedef decltype(t) T;
     constexpr int DH = decltype(d)::value, kMost = DH <= 64 ? 16 : 8;
     if (p.waves == kMost) go_decode<T, DH, kMost>(a, p, st);
     else go_decode<T, DH, 4>(a, p, st);
-    if (p.splits > 1)
+    e = hipGetLastError();
+    if (p.splits > 1 && e == hipSuccess) {
       hipLaunchKernelGGL((attn_decode_join<T>), dim3((unsigned)((int64_t)a.n_seq * a.q_heads)), dim3(64), 0,
                          st, a, p.splits);
+      e = hipGetLastError();
+    }
   });
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace emb

@@ -72,10 +72,8 @@ int check_counts(int64_t n_seq, int64_t n_tok) {
   return EMB_OK;
 }
 
-// A launch's grid: tile slots and sink chunks by heads, with room to spare.
-int check_grid(const EmbAttn* a, int64_t n_seq, int64_t n_tok) {
-  DENSE_CHECK((n_tok / 16 + 3 * n_seq + 2) * (int64_t)a->q_heads < INT32_MAX, EMB_ERANGE,
-              "attention: more tiles than one launch holds");
+int check_launch(int64_t threads) {
+  DENSE_CHECK(threads <= (int64_t)UINT32_MAX, EMB_ERANGE, "attention: more tiles than one launch holds");
   return EMB_OK;
 }
 
@@ -229,10 +227,10 @@ int attn_window_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   DENSE_CHECK(d_offsets, EMB_EINVAL, "attention: null pointer: offsets");
   DENSE_CHECK(aligned(d_offsets, 4) && aligned(d_lse, 4), EMB_EINVAL,
               "attention: offsets or lse not 4-byte aligned");
-  DENSE_TRY(check_grid(a, n_seq, n_tok));
+  AttnArgs x = attn_args(a, q, k, v, d_offsets, n_seq, n_tok);
+  DENSE_TRY(check_launch(attn_fwd_threads(x)));
   hipStream_t st = static_cast<hipStream_t>(stream);
   DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
-  AttnArgs x = attn_args(a, q, k, v, d_offsets, n_seq, n_tok);
   x.out = *out;
   x.lse = d_lse;
   return done(launch_attn_fwd(x, st), "attn_window_fwd");
@@ -266,12 +264,12 @@ int attn_window_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
               "attention: null pointer: offsets, lse or workspace");
   DENSE_CHECK(aligned(d_offsets, 4) && aligned(d_lse, 4) && aligned(d_ws, 16), EMB_EINVAL,
               "attention: misaligned offsets, lse or workspace");
-  DENSE_TRY(check_grid(a, n_seq, n_tok));
+  AttnArgs x = attn_args(a, q, k, v, d_offsets, n_seq, n_tok);
+  DENSE_TRY(check_launch(attn_bwd_threads(x)));
   const AttnBwdPlan p = plan_attn_bwd(*a, n_seq, n_tok);
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   hipStream_t st = static_cast<hipStream_t>(stream);
   DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
-  AttnArgs x = attn_args(a, q, k, v, d_offsets, n_seq, n_tok);
   x.out = *out;
   x.lse = const_cast<float*>(d_lse);
   x.dout = *dout;
@@ -310,14 +308,13 @@ int attn_window_decode(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k_ca
   DENSE_CHECK(d_lens, EMB_EINVAL, "attention: null pointer: lens");
   DENSE_CHECK(aligned(d_lens, 4), EMB_EINVAL, "attention: lens not 4-byte aligned");
   const AttnDecodePlan p = plan_attn_decode(*a, n_seq, capacity);
-  DENSE_CHECK((int64_t)n_seq * a->q_heads * p.splits < INT32_MAX, EMB_ERANGE,
-              "attention: more tiles than one launch holds");
+  AttnArgs x = attn_args(a, q, k_cache, v_cache, d_lens, n_seq, capacity);
+  DENSE_TRY(check_launch(attn_decode_threads(x, p)));
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL,
               "attention: null or misaligned workspace");
   hipStream_t st = static_cast<hipStream_t>(stream);
   DENSE_TRY(validate_offsets(d_lens, n_seq, capacity, true, st));
-  AttnArgs x = attn_args(a, q, k_cache, v_cache, d_lens, n_seq, capacity);
   x.out = *out;
   x.part = static_cast<float*>(d_ws);
   return done(launch_attn_decode(x, p, st), "attn_window_decode");

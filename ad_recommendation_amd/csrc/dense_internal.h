@@ -33,6 +33,11 @@ struct AttnDecodePlan {
 };
 AttnDecodePlan plan_attn_decode(const EmbAttn& a, int64_t n_seq, int64_t capacity);
 
+// Threads of a call's largest launch, of which there have to be fewer than 2^32.
+int64_t attn_fwd_threads(const AttnArgs& a);
+int64_t attn_bwd_threads(const AttnArgs& a);
+int64_t attn_decode_threads(const AttnArgs& a, const AttnDecodePlan& p);
+
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStream_t st);
