@@ -12,7 +12,7 @@
 //
 // The backward needs mean(z * y), where z holds dR and so the row's other means.  dR is linear in
 // them, so with a = gate * w_post * y
-//   sum(z * y) = sum(a * dr) + inv(r) * sum(a * u) - inv(r)^3 * mean(u * r) * sum(a * r)
+//   sum(z * y) = sum(a * dr) + inv(r) * (sum(a * u) - inv(r)^2 * mean(u * r) * sum(a * r))
 // and one exchange of six sums per row is enough, where two exchanges would stand one after the
 // other between a row's loads and its stores.
 #include "dense_device.h"
@@ -269,18 +269,20 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
     row_sums<TPR, kSums>(s, lds, turn);
     turn ^= 1;
     const float inv_r = pre ? rsqrtf(s[0] * inv_d + a.eps) : 0.f;
-    const float back_r = inv_r * inv_r * inv_r * s[1] * inv_d;  // dR = dr + inv_r u - back_r r
-    float inv_y = 1.f, back_y = 0.f;                            // dy = inv_y z - back_y y
+    // dR = dr + inv_r (u - back_r r) and dy = inv_y (z - back_y y): a cube of an inverse is zero for rows of
+    // about 1e15, and infinite for rows of zeros with an eps below 1e-25
+    const float back_r = s[1] * inv_r * inv_d * inv_r;
+    float inv_y = 1.f, back_y = 0.f;
     if (a.w_post) {
       inv_y = rsqrtf(s[2] * inv_d + a.eps);
-      back_y = inv_y * inv_y * inv_y * (s[3] + inv_r * s[4] - back_r * s[5]) * inv_d;
+      back_y = (s[3] + inv_r * (s[4] - back_r * s[5])) * inv_y * inv_d * inv_y;
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (!cl.some[c]) continue;
       const int64_t e = at + cl.col[c];
       const F rv = wide<T>(now[c].r), dhv = wide<T>(now[c].dh), yv = wide<T>(now[c].y);
-      const F dR = wide<T>(now[c].dr) + inv_r * (dhv * wp[c]) - back_r * rv;
+      const F dR = wide<T>(now[c].dr) + inv_r * (dhv * wp[c] - back_r * rv);
       F z = dR * wg[c];
       F yn = yv * inv_y;
       if (a.gate_kind == EMB_GATE_ROWS) {
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd(NormArgs a) {
       c_pre[c] += dhv * (rv * inv_r);
       if (live) {
         if (dx) store_vec<W, T, ONCE>(dx + e, a.alpha * dR, cl.width);
-        if (dy) store_vec<W, T, ONCE>(dy + e, inv_y * z - back_y * yv, cl.width);
+        if (dy) store_vec<W, T, ONCE>(dy + e, inv_y * (z - back_y * yv), cl.width);
       }
     }
 #pragma unroll

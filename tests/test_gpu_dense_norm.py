@@ -193,6 +193,28 @@ def test_values_far_from_one_and_rows_of_zeros():
     check_bwd(t)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("dim", [8, 320, 2048])
+@pytest.mark.parametrize("by", [1e13, 1e14, 1e15, 1e16, 1e17])
+def test_rows_so_large_that_the_cube_of_their_inverse_is_zero(by, dim, dtype):
+    """Without a gradient of r beside it, what the norms subtract is as large as what they subtract it from."""
+    t = make(24, dim, dtype, "vec", seed=9)
+    t["r"] *= by
+    t["dr"] = None
+    check_bwd(t)
+    t["y"] *= by
+    check_bwd(t)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_rows_of_zeros_with_an_eps_whose_inverse_cubed_is_infinite(dtype):
+    t = make(24, 320, dtype, "row", seed=10)
+    t["r"][3] = 0
+    t["y"][5] = 0
+    check_fwd(t, eps=1e-30)
+    check_bwd(t, eps=1e-30)
+
+
 def test_what_is_not_finite_stays_in_its_row():
     t = make(40, 320, F32, "row", seed=5)
     r, h = check_fwd(t)
