@@ -86,20 +86,29 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream):
+def _current() -> int:
+    """The device that a call runs on, asked for once: every tensor has to be there."""
+    try:
+        return _device()
+    except RuntimeError:  # there is none
+        return -2
+
+
+def _stream(dev: int, stream):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(_device())
+        return _raw_stream(dev)
     return _emb_stream(stream)
 
 
-def _ptr(t, name: str, dtype=None, shape=None, optional: bool = False) -> Optional[int]:
+def _ptr(dev: int, t, name: str, dtype=None, shape=None, optional: bool = False) -> Optional[int]:
     """Device pointer of a contiguous tensor of this type and shape."""
     if t is None:
         if optional:
             return None
         raise TypeError(f"{name}: expected a tensor")
-    if not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous CUDA tensor of the current device, got one on {t.device} "
+                        f"with strides {t.stride()}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -107,17 +116,17 @@ def _ptr(t, name: str, dtype=None, shape=None, optional: bool = False) -> Option
     return t.data_ptr()
 
 
-def _ws(ws):
+def _ws(dev: int, ws):
     """Pointer and size of a workspace (None where none is needed)."""
-    return (None, 0) if ws is None else (_ptr(ws, "workspace"), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (_ptr(dev, ws, "workspace"), ws.numel() * ws.element_size())
 
 
 # ------------------------------------------------------------------ attention
-def _heads(t, name: str, dtype, shape) -> bytes:
+def _heads(dev: int, t, name: str, dtype, shape) -> bytes:
     """EmbHeads of [tokens, heads, dim], or [sequences, tokens, heads, dim] of a cache: any strides
     but the last, which is 1."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name}: expected a CUDA tensor of {dtype} on the current device, got {t.dtype} on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
@@ -150,8 +159,8 @@ def _shapes(q, k):
     return shape, (shape[0], k.shape[1], shape[2])
 
 
-def _offsets(offsets):
-    p = _ptr(offsets, "offsets", torch.int32)
+def _offsets(dev: int, offsets):
+    p = _ptr(dev, offsets, "offsets", torch.int32)
     n = offsets.numel()
     if offsets.dim() != 1 or n < 1:
         raise ValueError("offsets: expected one dimension of n_seq + 1 elements")
@@ -164,12 +173,13 @@ def attn_window_fwd(q, k, v, offsets, window: int, sinks: int, scale: float, out
     dim] and k, v [tokens, kv_heads, dim]; sequence s holds tokens offsets[s] to offsets[s + 1] - 1."""
     t, (qs, kv) = q.dtype, _shapes(q, k)
     a = _attn(t, qs, kv[1], window, sinks, scale)
-    off, n_seq = _offsets(offsets)
+    dev = _current()
+    off, n_seq = _offsets(dev, offsets)
     _check(lib().attn_window_fwd(
-        a, _heads(q, "q", t, qs), _heads(k, "k", t, kv), _heads(v, "v", t, kv), off, n_seq, qs[0],
-        _heads(out, "out", t, qs),
-        _ptr(lse, "lse", torch.float32, (qs[1], qs[0]), optional=True),
-        _stream(stream)))
+        a, _heads(dev, q, "q", t, qs), _heads(dev, k, "k", t, kv), _heads(dev, v, "v", t, kv), off, n_seq, qs[0],
+        _heads(dev, out, "out", t, qs),
+        _ptr(dev, lse, "lse", torch.float32, (qs[1], qs[0]), optional=True),
+        _stream(dev, stream)))
 
 
 def attn_window_bwd_workspace_bytes(n_tok: int, n_seq: int, q_heads: int, kv_heads: int, dim: int,
@@ -184,15 +194,16 @@ def attn_window_bwd(q, k, v, offsets, window: int, sinks: int, scale: float, out
     """dq, dk and dv from the forward's inputs and results and the gradient of out."""
     t, (qs, kv) = q.dtype, _shapes(q, k)
     a = _attn(t, qs, kv[1], window, sinks, scale)
-    off, n_seq = _offsets(offsets)
-    wp, wb = _ws(ws)
+    dev = _current()
+    off, n_seq = _offsets(dev, offsets)
+    wp, wb = _ws(dev, ws)
     _check(lib().attn_window_bwd(
-        a, _heads(q, "q", t, qs), _heads(k, "k", t, kv), _heads(v, "v", t, kv), off, n_seq, qs[0],
-        _heads(out, "out", t, qs),
-        _ptr(lse, "lse", torch.float32, (qs[1], qs[0])),
-        _heads(dout, "dout", t, qs), _heads(dq, "dq", t, qs),
-        _heads(dk, "dk", t, kv), _heads(dv, "dv", t, kv), wp, wb,
-        _stream(stream)))
+        a, _heads(dev, q, "q", t, qs), _heads(dev, k, "k", t, kv), _heads(dev, v, "v", t, kv), off, n_seq, qs[0],
+        _heads(dev, out, "out", t, qs),
+        _ptr(dev, lse, "lse", torch.float32, (qs[1], qs[0])),
+        _heads(dev, dout, "dout", t, qs), _heads(dev, dq, "dq", t, qs),
+        _heads(dev, dk, "dk", t, kv), _heads(dev, dv, "dv", t, kv), wp, wb,
+        _stream(dev, stream)))
 
 
 def attn_window_decode_workspace_bytes(n_seq: int, capacity: int, q_heads: int, kv_heads: int,
@@ -211,12 +222,12 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
         raise ValueError("expected q [sequences, heads, dim], k_cache [sequences, capacity, heads, dim]")
     _, cap, kv_heads, _ = k_cache.shape
     a = _attn(t, qs, kv_heads, window, sinks, scale)
-    cache = (qs[0], cap, kv_heads, qs[2])
-    wp, wb = _ws(ws)
+    cache, dev = (qs[0], cap, kv_heads, qs[2]), _current()
+    wp, wb = _ws(dev, ws)
     _check(lib().attn_window_decode(
-        a, _heads(q, "q", t, qs), _heads(k_cache, "k_cache", t, cache),
-        _heads(v_cache, "v_cache", t, cache), _ptr(lens, "lens", torch.int32, (qs[0],)), qs[0], cap,
-        _heads(out, "out", t, qs), wp, wb, _stream(stream)))
+        a, _heads(dev, q, "q", t, qs), _heads(dev, k_cache, "k_cache", t, cache),
+        _heads(dev, v_cache, "v_cache", t, cache), _ptr(dev, lens, "lens", torch.int32, (qs[0],)), qs[0], cap,
+        _heads(dev, out, "out", t, qs), wp, wb, _stream(dev, stream)))
 
 
 # ------------------------------------------------------------------ norms
@@ -239,12 +250,12 @@ def norm_gate_residual_fwd(x, y, gate, w_post, w_pre, alpha: float, eps: float, 
     """r = alpha x + gate * (w_post * rms(y)), h = w_pre * rms(r).  x, y, r, h [rows, dim]; gate
     [dim] or [rows, dim]; w_post, w_pre fp32 [dim].  None where a part is left out."""
     t, s, d = _rows(x)
-    kind = _gate_kind(gate)
+    kind, dev = _gate_kind(gate), _current()
     _check(lib().norm_gate_residual_fwd(
-        _ptr(x, "x"), _ptr(y, "y", t, s, True), _ptr(gate, "gate", t, d if kind == 1 else s, True),
-        kind, _ptr(w_post, "w_post", torch.float32, d, True),
-        _ptr(w_pre, "w_pre", torch.float32, d, True), s[0], s[1], _DTYPE[t], float(alpha),
-        float(eps), _ptr(r, "r", t, s, True), _ptr(h, "h", t, s, True), _stream(stream)))
+        _ptr(dev, x, "x"), _ptr(dev, y, "y", t, s, True), _ptr(dev, gate, "gate", t, d if kind == 1 else s, True),
+        kind, _ptr(dev, w_post, "w_post", torch.float32, d, True),
+        _ptr(dev, w_pre, "w_pre", torch.float32, d, True), s[0], s[1], _DTYPE[t], float(alpha),
+        float(eps), _ptr(dev, r, "r", t, s, True), _ptr(dev, h, "h", t, s, True), _stream(dev, stream)))
 
 
 def norm_gate_residual_bwd_workspace_bytes(rows: int, dim: int) -> int:
@@ -258,16 +269,16 @@ def norm_gate_residual_bwd(r, y, gate, w_post, w_pre, alpha: float, eps: float, 
     """Gradients of norm_gate_residual_fwd from r as stored; None for an output that is not wanted.
     dgate: fp32 [dim] for a gate vector, like the rows for a gate of rows."""
     t, s, d = _rows(r)
-    kind = _gate_kind(gate)
-    f, wp_wb = torch.float32, _ws(ws)
+    kind, dev = _gate_kind(gate), _current()
+    f, wp_wb = torch.float32, _ws(dev, ws)
     _check(lib().norm_gate_residual_bwd(
-        _ptr(r, "r"), _ptr(y, "y", t, s, True), _ptr(gate, "gate", t, d if kind == 1 else s, True),
-        kind, _ptr(w_post, "w_post", f, d, True), _ptr(w_pre, "w_pre", f, d, True), s[0], s[1],
-        _DTYPE[t], float(alpha), float(eps), _ptr(dr, "dr", t, s, True), _ptr(dh, "dh", t, s, True),
-        _ptr(dx, "dx", t, s, True), _ptr(dy, "dy", t, s, True),
-        _ptr(dgate, "dgate", f if kind == 1 else t, d if kind == 1 else s, True),
-        _ptr(dw_post, "dw_post", f, d, True), _ptr(dw_pre, "dw_pre", f, d, True), *wp_wb,
-        _stream(stream)))
+        _ptr(dev, r, "r"), _ptr(dev, y, "y", t, s, True), _ptr(dev, gate, "gate", t, d if kind == 1 else s, True),
+        kind, _ptr(dev, w_post, "w_post", f, d, True), _ptr(dev, w_pre, "w_pre", f, d, True), s[0], s[1],
+        _DTYPE[t], float(alpha), float(eps), _ptr(dev, dr, "dr", t, s, True), _ptr(dev, dh, "dh", t, s, True),
+        _ptr(dev, dx, "dx", t, s, True), _ptr(dev, dy, "dy", t, s, True),
+        _ptr(dev, dgate, "dgate", f if kind == 1 else t, d if kind == 1 else s, True),
+        _ptr(dev, dw_post, "dw_post", f, d, True), _ptr(dev, dw_pre, "dw_pre", f, d, True), *wp_wb,
+        _stream(dev, stream)))
 
 
 # ------------------------------------------------------------------ AdamW
@@ -281,21 +292,21 @@ def adamw_state_elems(weights) -> int:
 
 # looked up once: a step of a hundred small tensors is bound by what is asked of each of them
 _numel, _data_ptr, _contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
-_dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")
+_dtype_of, _device_of = attrgetter("dtype"), torch.Tensor.get_device
 
 
-def _tensors(ts, name: str, dtype, sizes) -> bytes:
+def _tensors(dev: int, ts, name: str, dtype, sizes) -> bytes:
     """Host array of the device pointers of contiguous tensors of one type and these sizes."""
     if not (list(map(_numel, ts)) == sizes and set(map(_dtype_of, ts)) <= {dtype} and
-            all(map(_is_cuda, ts)) and all(map(_contiguous, ts))):
+            set(map(_device_of, ts)) <= {dev} and all(map(_contiguous, ts))):
         got = [(t.dtype, tuple(t.shape), str(t.device)) for t, n in zip(ts, sizes) if t.numel() != n or
-               t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()]
-        raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} with the weights' "
-                        f"sizes, got {got[0]}")
+               t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()]
+        raise TypeError(f"{name}: expected contiguous CUDA tensors of {dtype} on the current device with the "
+                        f"weights' sizes, got {got[0]}")
     return struct.pack(f"{len(ts)}P", *map(_data_ptr, ts))
 
 
-def _adamw_args(weights, grads, copies, weight_decay):
+def _adamw_args(dev: int, weights, grads, copies, weight_decay):
     sizes = list(map(_numel, weights))
     k = len(sizes)
     if len(grads) != k or (copies is not None and len(copies) != k):
@@ -308,9 +319,9 @@ def _adamw_args(weights, grads, copies, weight_decay):
         weight_decay = [weight_decay] * k
     elif len(weight_decay) != k:
         raise ValueError(f"weight_decay: expected {k} values, got {len(weight_decay)}")
-    return (k, struct.pack(f"{k}q", *sizes), _tensors(weights, "weights", torch.float32, sizes),
-            _tensors(grads, "grads", g_dtype, sizes), _DTYPE[g_dtype],
-            None if copies is None else _tensors(copies, "copies", c_dtype, sizes),
+    return (k, struct.pack(f"{k}q", *sizes), _tensors(dev, weights, "weights", torch.float32, sizes),
+            _tensors(dev, grads, "grads", g_dtype, sizes), _DTYPE[g_dtype],
+            None if copies is None else _tensors(dev, copies, "copies", c_dtype, sizes),
             _DTYPE[c_dtype]), struct.pack(f"{k}f", *weight_decay)
 
 
@@ -324,18 +335,19 @@ def adamw_step(weights, grads, m, v, step: int, lr: float, beta1: float, beta2: 
     """One AdamW step over lists of tensors, in place.  weights fp32; grads of one type; m, v fp32
     [adamw_state_elems(weights)]; weight_decay: a number or one per tensor; copies: float16 or
     bfloat16 tensors that receive the new weights; grad_scale: fp32 device scalar."""
-    args, wd = _adamw_args(weights, grads, copies, weight_decay)
+    dev = _current()
+    args, wd = _adamw_args(dev, weights, grads, copies, weight_decay)
     f = torch.float32
     _scalar(grad_scale)
     _check(lib().adamw_step(
-        *args, _ptr(m, "m", f), _ptr(v, "v", f, m.shape), m.numel(), int(step), lr, beta1, beta2,
-        eps, wd, _ptr(grad_scale, "grad_scale", f, optional=True), _stream(stream)))
+        *args, _ptr(dev, m, "m", f), _ptr(dev, v, "v", f, m.shape), m.numel(), int(step), lr, beta1, beta2,
+        eps, wd, _ptr(dev, grad_scale, "grad_scale", f, optional=True), _stream(dev, stream)))
 
 
-def _codes(t, name: str, n: int):
+def _codes(dev: int, t, name: str, n: int):
     if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError(f"{name}: expected uint8 or float8_e4m3fn, got {t.dtype}")
-    return _ptr(t, name, shape=(n,))
+    return _ptr(dev, t, name, shape=(n,))
 
 
 def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta1: float,
@@ -344,22 +356,23 @@ def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta
     """adamw_step with states in 8 bits: m, v codes [adamw_state_elems(weights)] (uint8 or
     float8_e4m3fn), m_exp, v_exp uint8 [that / ADAMW_BLOCK], all zero at first.  `seed`: another one
     each step."""
-    args, wd = _adamw_args(weights, grads, copies, weight_decay)
+    dev = _current()
+    args, wd = _adamw_args(dev, weights, grads, copies, weight_decay)
     _scalar(grad_scale)
     n = m.numel()
     e = (n // ADAMW_BLOCK,)
     _check(lib().adamw_step_q8(
-        *args, _codes(m, "m", n), _ptr(m_exp, "m_exp", torch.uint8, e), _codes(v, "v", n),
-        _ptr(v_exp, "v_exp", torch.uint8, e), n, int(step), lr, beta1, beta2, eps, wd,
-        _ptr(grad_scale, "grad_scale", torch.float32, optional=True), int(seed) & (2**64 - 1),
-        _stream(stream)))
+        *args, _codes(dev, m, "m", n), _ptr(dev, m_exp, "m_exp", torch.uint8, e), _codes(dev, v, "v", n),
+        _ptr(dev, v_exp, "v_exp", torch.uint8, e), n, int(step), lr, beta1, beta2, eps, wd,
+        _ptr(dev, grad_scale, "grad_scale", torch.float32, optional=True), int(seed) & (2**64 - 1),
+        _stream(dev, stream)))
 
 
 def adamw_q8_values(codes, exp, out, stream=None):
     """The values that 8-bit state codes stand for, in bfloat16 or float32; v's are its roots."""
-    n = codes.numel()
+    n, dev = codes.numel(), _current()
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
     _check(lib().adamw_q8_values(
-        _codes(codes, "codes", n), _ptr(exp, "exp", torch.uint8, (n // ADAMW_BLOCK,)), n,
-        _ptr(out, "out", shape=(n,)), _DTYPE[out.dtype], _stream(stream)))
+        _codes(dev, codes, "codes", n), _ptr(dev, exp, "exp", torch.uint8, (n // ADAMW_BLOCK,)), n,
+        _ptr(dev, out, "out", shape=(n,)), _DTYPE[out.dtype], _stream(dev, stream)))
