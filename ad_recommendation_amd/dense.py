@@ -84,14 +84,8 @@ def lib() -> C.CDLL:
 # number without a look at whether there is a device, which a CUDA tensor has answered
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _current() -> int:
-    """The device that a call runs on, asked for once: every tensor has to be there."""
-    try:
-        return _device()
-    except RuntimeError:  # there is none
-        return -2
+# The device that a call runs on is asked for once, where one of its tensors is on some GPU; each has to be there.
+_NONE = -2
 
 
 def _stream(dev: int, stream):
@@ -173,7 +167,7 @@ def attn_window_fwd(q, k, v, offsets, window: int, sinks: int, scale: float, out
     dim] and k, v [tokens, kv_heads, dim]; sequence s holds tokens offsets[s] to offsets[s + 1] - 1."""
     t, (qs, kv) = q.dtype, _shapes(q, k)
     a = _attn(t, qs, kv[1], window, sinks, scale)
-    dev = _current()
+    dev = _device() if q.is_cuda else _NONE
     off, n_seq = _offsets(dev, offsets)
     _check(lib().attn_window_fwd(
         a, _heads(dev, q, "q", t, qs), _heads(dev, k, "k", t, kv), _heads(dev, v, "v", t, kv), off, n_seq, qs[0],
@@ -194,7 +188,7 @@ def attn_window_bwd(q, k, v, offsets, window: int, sinks: int, scale: float, out
     """dq, dk and dv from the forward's inputs and results and the gradient of out."""
     t, (qs, kv) = q.dtype, _shapes(q, k)
     a = _attn(t, qs, kv[1], window, sinks, scale)
-    dev = _current()
+    dev = _device() if q.is_cuda else _NONE
     off, n_seq = _offsets(dev, offsets)
     wp, wb = _ws(dev, ws)
     _check(lib().attn_window_bwd(
@@ -222,7 +216,7 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
         raise ValueError("expected q [sequences, heads, dim], k_cache [sequences, capacity, heads, dim]")
     _, cap, kv_heads, _ = k_cache.shape
     a = _attn(t, qs, kv_heads, window, sinks, scale)
-    cache, dev = (qs[0], cap, kv_heads, qs[2]), _current()
+    cache, dev = (qs[0], cap, kv_heads, qs[2]), _device() if q.is_cuda else _NONE
     wp, wb = _ws(dev, ws)
     _check(lib().attn_window_decode(
         a, _heads(dev, q, "q", t, qs), _heads(dev, k_cache, "k_cache", t, cache),
@@ -250,7 +244,7 @@ def norm_gate_residual_fwd(x, y, gate, w_post, w_pre, alpha: float, eps: float, 
     """r = alpha x + gate * (w_post * rms(y)), h = w_pre * rms(r).  x, y, r, h [rows, dim]; gate
     [dim] or [rows, dim]; w_post, w_pre fp32 [dim].  None where a part is left out."""
     t, s, d = _rows(x)
-    kind, dev = _gate_kind(gate), _current()
+    kind, dev = _gate_kind(gate), _device() if x.is_cuda else _NONE
     _check(lib().norm_gate_residual_fwd(
         _ptr(dev, x, "x"), _ptr(dev, y, "y", t, s, True), _ptr(dev, gate, "gate", t, d if kind == 1 else s, True),
         kind, _ptr(dev, w_post, "w_post", torch.float32, d, True),
@@ -269,7 +263,7 @@ def norm_gate_residual_bwd(r, y, gate, w_post, w_pre, alpha: float, eps: float, 
     """Gradients of norm_gate_residual_fwd from r as stored; None for an output that is not wanted.
     dgate: fp32 [dim] for a gate vector, like the rows for a gate of rows."""
     t, s, d = _rows(r)
-    kind, dev = _gate_kind(gate), _current()
+    kind, dev = _gate_kind(gate), _device() if r.is_cuda else _NONE
     f, wp_wb = torch.float32, _ws(dev, ws)
     _check(lib().norm_gate_residual_bwd(
         _ptr(dev, r, "r"), _ptr(dev, y, "y", t, s, True), _ptr(dev, gate, "gate", t, d if kind == 1 else s, True),
@@ -335,7 +329,7 @@ def adamw_step(weights, grads, m, v, step: int, lr: float, beta1: float, beta2: 
     """One AdamW step over lists of tensors, in place.  weights fp32; grads of one type; m, v fp32
     [adamw_state_elems(weights)]; weight_decay: a number or one per tensor; copies: float16 or
     bfloat16 tensors that receive the new weights; grad_scale: fp32 device scalar."""
-    dev = _current()
+    dev = _device() if m.is_cuda else _NONE
     args, wd = _adamw_args(dev, weights, grads, copies, weight_decay)
     f = torch.float32
     _scalar(grad_scale)
@@ -356,7 +350,7 @@ def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta
     """adamw_step with states in 8 bits: m, v codes [adamw_state_elems(weights)] (uint8 or
     float8_e4m3fn), m_exp, v_exp uint8 [that / ADAMW_BLOCK], all zero at first.  `seed`: another one
     each step."""
-    dev = _current()
+    dev = _device() if m.is_cuda else _NONE
     args, wd = _adamw_args(dev, weights, grads, copies, weight_decay)
     _scalar(grad_scale)
     n = m.numel()
@@ -370,7 +364,7 @@ def adamw_step_q8(weights, grads, m, m_exp, v, v_exp, step: int, lr: float, beta
 
 def adamw_q8_values(codes, exp, out, stream=None):
     """The values that 8-bit state codes stand for, in bfloat16 or float32; v's are its roots."""
-    n, dev = codes.numel(), _current()
+    n, dev = codes.numel(), _device() if codes.is_cuda else _NONE
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
     _check(lib().adamw_q8_values(
