@@ -22,6 +22,12 @@ namespace {
     if (!(cond)) return set_error(code, msg);         \
   } while (0)
 
+#define DENSE_TRY(expr)              \
+  do {                               \
+    const int rc_ = (expr);          \
+    if (rc_ != EMB_OK) return rc_;   \
+  } while (0)
+
 // The failed call's code must not stay behind as the thread's last error (see emb_host.cpp).
 int done(hipError_t e, const char* what) {
   if (e == hipSuccess) return EMB_OK;
@@ -61,6 +67,15 @@ int check_heads(const EmbHeads* t, const char* name) {
               std::string("attention: not 16-byte aligned: ") + name);
   DENSE_CHECK(t->seq % 8 == 0 && t->tok % 8 == 0 && t->head % 8 == 0, EMB_EINVAL,
               std::string("attention: a stride is not a multiple of 8: ") + name);
+  return EMB_OK;
+}
+
+// Of an output: no element may have two places in the tensor, of which the last written would win.
+int check_written(const EmbHeads* t, int64_t tokens, int32_t heads, int32_t dim, const char* name) {
+  DENSE_TRY(check_heads(t, name));
+  const auto apart = [&](int64_t stride, int64_t n) { return n <= 1 || stride >= dim || stride <= -dim; };
+  DENSE_CHECK(apart(t->tok, tokens) && apart(t->head, heads), EMB_EINVAL,
+              std::string("attention: tokens or heads of an output overlap: ") + name);
   return EMB_OK;
 }
 
@@ -118,12 +133,6 @@ AttnArgs attn_args(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const
   x.scale = a->scale;
   return x;
 }
-
-#define DENSE_TRY(expr)              \
-  do {                               \
-    const int rc_ = (expr);          \
-    if (rc_ != EMB_OK) return rc_;   \
-  } while (0)
 
 // ---------------------------------------------------------------- AdamW
 struct AdamCall {
@@ -223,7 +232,7 @@ int attn_window_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   DENSE_TRY(check_heads(q, "q"));
   DENSE_TRY(check_heads(k, "k"));
   DENSE_TRY(check_heads(v, "v"));
-  DENSE_TRY(check_heads(out, "out"));
+  DENSE_TRY(check_written(out, n_tok, a->q_heads, a->dim, "out"));
   DENSE_CHECK(d_offsets, EMB_EINVAL, "attention: null pointer: offsets");
   DENSE_CHECK(aligned(d_offsets, 4) && aligned(d_lse, 4), EMB_EINVAL,
               "attention: offsets or lse not 4-byte aligned");
@@ -257,9 +266,9 @@ int attn_window_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   DENSE_TRY(check_heads(v, "v"));
   DENSE_TRY(check_heads(out, "out"));
   DENSE_TRY(check_heads(dout, "dout"));
-  DENSE_TRY(check_heads(dq, "dq"));
-  DENSE_TRY(check_heads(dk, "dk"));
-  DENSE_TRY(check_heads(dv, "dv"));
+  DENSE_TRY(check_written(dq, n_tok, a->q_heads, a->dim, "dq"));
+  DENSE_TRY(check_written(dk, n_tok, a->kv_heads, a->dim, "dk"));
+  DENSE_TRY(check_written(dv, n_tok, a->kv_heads, a->dim, "dv"));
   DENSE_CHECK(d_offsets && d_lse && d_ws, EMB_EINVAL,
               "attention: null pointer: offsets, lse or workspace");
   DENSE_CHECK(aligned(d_offsets, 4) && aligned(d_lse, 4) && aligned(d_ws, 16), EMB_EINVAL,
@@ -298,7 +307,7 @@ int attn_window_decode(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k_ca
   DENSE_TRY(check_counts(n_seq, capacity));
   if (n_seq == 0) return EMB_OK;
   DENSE_TRY(check_heads(q, "q"));
-  DENSE_TRY(check_heads(out, "out"));
+  DENSE_TRY(check_written(out, n_seq, a->q_heads, a->dim, "out"));
   if (capacity > 0) {  // an empty cache has nothing to point at
     DENSE_TRY(check_heads(k_cache, "k_cache"));
     DENSE_TRY(check_heads(v_cache, "v_cache"));

@@ -48,7 +48,8 @@ typedef struct {
 /*
  * Heads of tokens in device memory: element (s, t, h, d) at p + s * seq + t * tok + h * head + d,
  * strides in elements.  p must be 16-byte aligned and the strides multiples of 8 (EMB_EINVAL), so
- * views of one projection's output may be passed as they are.  `seq` is read for a cache only.
+ * views of one projection's output may be passed as they are.  `seq` is read for a cache only.  Inputs may
+ * repeat (a stride of 0); tokens or heads of an output less than dim apart are refused (EMB_EINVAL).
  */
 typedef struct {
   void* p;

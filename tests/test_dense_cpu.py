@@ -107,19 +107,27 @@ def test_bad_attention_arguments_are_refused(call):
         refused(call(ws_bytes=100), "EMB_ENOSPACE")
 
 
+@pytest.mark.parametrize("call", [fwd, bwd, dec])
+def test_outputs_that_overlap_are_refused(call):
+    for name in ("out",) if call is not bwd else ("dq", "dk", "dv"):
+        for bad in (dict(tok=0), dict(head=0), dict(head=56), dict(tok=-8)):
+            refused(call(**{name: heads(**bad)}), "EMB_EINVAL", "overlap: " + name)
+
+
 def test_calls_past_what_a_launch_holds_are_refused():
     """A launch has fewer than 2^32 threads, 256 for each 128 tokens, sequence and query head (64 and 32 where
     sequences are short and heads at most 64 wide), 512 in dk/dv of wider heads, 256 a sequence in its join."""
     wide = attn(q_heads=16, kv_heads=2, dim=128)
+    apart = {k: heads(tok=2048, head=128) for k in ("out", "dq", "dk", "dv")}
     for call in (fwd, bwd):
-        refused(call(wide, n_seq=2 ** 20 + 2 ** 14, n_tok=5 * 2 ** 20, **({} if call is fwd else {"ws_bytes": 2 ** 50})),
-                "EMB_ERANGE", "launch")
+        refused(call(wide, n_seq=2 ** 20 + 2 ** 14, n_tok=5 * 2 ** 20, **apart,
+                     **({} if call is fwd else {"ws_bytes": 2 ** 50})), "EMB_ERANGE", "launch")
         narrow = attn(q_heads=64, kv_heads=64, dim=64)
         refused(call(narrow, n_seq=2 ** 20, n_tok=2 ** 20, **({} if call is fwd else {"ws_bytes": 2 ** 50})),
                 "EMB_ERANGE", "launch")
     # the forward's and dq's launch holds these, dk/dv's does not, nor the sinks' join
-    refused(bwd(attn(q_heads=4, kv_heads=4, dim=128, sinks=0), n_seq=2 ** 21 + 1, n_tok=2 ** 21 + 1, ws_bytes=2 ** 50),
-            "EMB_ERANGE", "launch")
+    refused(bwd(attn(q_heads=4, kv_heads=4, dim=128, sinks=0), n_seq=2 ** 21 + 1, n_tok=2 ** 21 + 1, ws_bytes=2 ** 50,
+                **apart), "EMB_ERANGE", "launch")
     refused(bwd(attn(q_heads=1, kv_heads=1, dim=8, window=1, sinks=1), n_seq=2 ** 24, n_tok=2 ** 29, ws_bytes=2 ** 50),
             "EMB_ERANGE", "launch")
     refused(dec(attn(q_heads=64, kv_heads=64, window=1), n_seq=2 ** 18, cap=100), "EMB_ERANGE", "launch")
