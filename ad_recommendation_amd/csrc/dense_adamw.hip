@@ -72,7 +72,9 @@ __device__ __forceinline__ int encode8(const f32x8& x, const f32x8& up, uint2& c
   for (int i = 0; i < 8; ++i) {
     const float y = ldexpf(fabsf(x[i]), -k);
     const int e = max(__builtin_amdgcn_frexp_expf(y) - 1, -6);
-    // the upper of two codes where the place between them and `up` add up to more than one
+    // The upper of two codes where the place between them and `up` add up to more than one.  On exactly one, which
+    // keeps the mean as well either way, the lower: a program that scales its values by a power of two that is a
+    // unit in the last place short, as a library's power function may be, gets the same code.
     float q = ceilf(ldexpf(y, 3 - e) + up[i]) - 1.f;
     if (KEEP && y > 0.f) q = fmaxf(q, 1.f);
     c[i] = copysignf(ldexpf(q, e - 3), x[i]);

@@ -169,6 +169,7 @@ int adamw_step(int32_t n_tensors, const int64_t* n, void* const* w, const void* 
  * A value becomes one of the two codes beside it, the upper one with the probability that keeps the
  * mean, by 16 bits of a hash of `seed` and the element's index in the state array: with rounding to
  * the nearest a second moment would never move, since a step changes its root by less than half a code.
+ * Exactly: at a place p in [0, 1) between the two, with bits b, the upper one where p + (b + 0.5) / 65536 > 1.
  * `seed` is to differ from step to step.  A root that is not zero does not become zero.  What is
  * not finite is held as NaN.  The weights are updated from the states before they are rounded.
  */
