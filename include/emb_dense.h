@@ -62,7 +62,8 @@ typedef struct {
  * ascending from 0 to n_tok; empty sequences are fine).  Softmax statistics and sums are fp32.
  *   d_lse : nullable; fp32 [q_heads][n_tok], what the backward reads.
  * A key or value that is not finite reaches only the queries that see it (and in the backward, a
- * query or gradient only the keys it sees).
+ * query or gradient only the keys it sees).  Sums that are not finite, in EMB_F16 also those of score gradients
+ * over 65504, are computed once more: such a call takes a few times as long.
  * EMB_VALIDATE=1 checks the offsets first (it synchronises the stream); without it malformed
  * offsets give wrong results but no access outside the n_tok tokens.
  * Errors: EMB_EINVAL for a null pointer, a bad descriptor, alignment or stride; EMB_ERANGE for
@@ -86,7 +87,10 @@ int attn_window_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
                     const EmbHeads* dk, const EmbHeads* dv, void* d_ws, size_t ws_bytes,
                     emb_stream_t stream);
 
-/* Workspace of attn_window_decode for a cache of `capacity` tokens a sequence (host only). */
+/*
+ * Workspace of attn_window_decode for n_seq sequences with caches of `capacity` tokens (host only).  Fewer
+ * sequences may need more: the keys of each are split over more of the GPU.
+ */
 int attn_window_decode_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t capacity,
                                        size_t* bytes);
 
