@@ -55,9 +55,9 @@ __device__ __forceinline__ f32x8 decode8(uint2 c, int exp) {
 }
 
 // Eight values of a block, its 16 lanes' 128 in all, as codes; returns the block's exponent + 127.
-// `up`: for each value a number in (0, 1).  KEEP: a value that is not zero gets a code that is not.
+// `down`: for each value a number in (0, 1), a multiple of 2^-17.  KEEP: a value that is not zero gets a code that is not.
 template <bool KEEP>
-__device__ __forceinline__ int encode8(const f32x8& x, const f32x8& up, uint2& codes) {
+__device__ __forceinline__ int encode8(const f32x8& x, const f32x8& down, uint2& codes) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -72,10 +72,12 @@ __device__ __forceinline__ int encode8(const f32x8& x, const f32x8& up, uint2& c
   for (int i = 0; i < 8; ++i) {
     const float y = ldexpf(fabsf(x[i]), -k);
     const int e = max(__builtin_amdgcn_frexp_expf(y) - 1, -6);
-    // The upper of two codes where the place between them and `up` add up to more than one.  On exactly one, which
-    // keeps the mean as well either way, the lower: a program that scales its values by a power of two that is a
-    // unit in the last place short, as a library's power function may be, gets the same code.
-    float q = ceilf(ldexpf(y, 3 - e) + up[i]) - 1.f;
+    // The upper of two codes where the place between them is past `down`.  Both are exact in fp32; a sum with
+    // 1 - down would be rounded, onto the border now and then.  On the border itself, which keeps the mean as well
+    // either way, the lower.
+    const float t = ldexpf(y, 3 - e);
+    float q = floorf(t);
+    q += t - q > down[i] ? 1.f : 0.f;
     if (KEEP && y > 0.f) q = fmaxf(q, 1.f);
     c[i] = copysignf(ldexpf(q, e - 3), x[i]);
     // infinities and NaN: the one code that e4m3 has for them
@@ -182,16 +184,16 @@ __global__ void __launch_bounds__(kThreads) adamw(const AdamArgs a) {
       if (COPY) store8<C, ONCE>(copy + e, wv, left);
     }
     const uint32_t base = mix32(seed ^ (uint32_t)((uint64_t)s >> 32) * 0x9E3779B1u);
-    f32x8 up_m, up_v;
+    f32x8 down_m, down_v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t r = mix32((uint32_t)(s + i) + base);
-      up_m[i] = ((float)(r & 0xFFFFu) + 0.5f) * (1.f / 65536.f);
-      up_v[i] = ((float)(r >> 16) + 0.5f) * (1.f / 65536.f);
+      down_m[i] = (65535.5f - (float)(r & 0xFFFFu)) * (1.f / 65536.f);
+      down_v[i] = (65535.5f - (float)(r >> 16)) * (1.f / 65536.f);
     }
     uint2 cm, cv;
-    const int em = encode8<false>(m, up_m, cm);
-    const int ev = encode8<true>(root, up_v, cv);
+    const int em = encode8<false>(m, down_m, cm);
+    const int ev = encode8<true>(root, down_v, cv);
     if (in) {
       *reinterpret_cast<uint2*>(a.m8 + s) = cm;
       *reinterpret_cast<uint2*>(a.v8 + s) = cv;

@@ -216,8 +216,8 @@ def to_codes(x, bits, keep):
     y = x.double().reshape(-1, BLOCK) * pow2(-k)[:, None]
     low, high, step = e4m3_neighbours(y)
     up = (bits.reshape(-1, BLOCK).double() + 0.5) / 65536
-    # the place between two codes is exact in fp32, and the sum is one of fp32
-    c = (torch.ceil((y.abs() / step).float() + up.float()).double() - 1) * step
+    # the upper where the place between two codes and `up` are over one; 64 bits hold that sum
+    c = (torch.ceil(y.abs() / step + up) - 1) * step
     if keep:
         c = torch.where((y != 0) & (c == 0), 2.0 ** -9, c)
     return (c * torch.sign(y) * pow2(k)[:, None]).reshape(-1), k

@@ -188,6 +188,28 @@ def test_codes_bit_by_bit(seed, sizes, grad):
         check_weights(w[i], w0[i], None, m1[a:a + n], v1[a:a + n], 5, 0.01, HYPER)
 
 
+@pytest.mark.parametrize("seed", [1, 2, 3])
+@pytest.mark.parametrize("base,scale,ulp", [(15.0, 1.0, 2.0 ** -20), (8.0, 1.0, 2.0 ** -20), (0.0, 2.0 ** -9, 2.0 ** -24)])
+def test_values_on_the_border_of_two_codes_and_beside_it(base, scale, ulp, seed):
+    """Without betas m is the gradient.  At p between two codes with bits b, the upper where p + (b + 0.5) / 65536 > 1:
+    not on one, and a unit in the last place on either side; codes of whole numbers from 8 to 16, and the smallest."""
+    n = 128
+    up = ((O.hash_bits(seed, torch.arange(n, device="cuda")) & 0xFFFF).double() + 0.5) / 65536
+    side = torch.arange(n, device="cuda") % 3 - 1
+    x = (base + (1 - up) + side * ulp) * scale
+    use = (1 - up > 0.5) & (1 - up < 1 - 2.0 ** -16) & (torch.arange(n, device="cuda") < n - 1)
+    x = torch.where(use, x, 0.0)
+    x[n - 1] = 240.0  # the block's exponent is 0
+    g = [x.float()]
+    assert torch.equal(g[0].double(), x) and use.sum() > 30
+    s = [torch.zeros(k, dtype=torch.uint8, device="cuda") for k in (n, 1) * 2]
+    dense.adamw_step_q8([torch.zeros(n, device="cuda")], g, *s, *args(1, beta1=0.0, beta2=0.0), 0.0, seed=seed)
+    got = torch.empty(n, device="cuda")
+    dense.adamw_q8_values(s[0], s[1], got)
+    want = torch.where(side > 0, base + 1, base) * scale
+    assert torch.equal(got[use].double(), want[use])
+
+
 def test_the_means_move_as_the_formula_says():
     """Without gradients the root of v shrinks by sqrt(beta2) a step, though each step is far less
     than a code; m's mean follows a constant gradient."""
