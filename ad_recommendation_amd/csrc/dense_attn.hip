@@ -177,7 +177,7 @@ struct RegisterTile {
 // Straight from memory to LDS, where heads have DH columns: a wave's load fills 1024 bytes in order, so a
 // row's pieces are exchanged by its number instead of set apart, by the address that a lane loads from.
 // The last row stands for those past it; no query sees them, and no row past `end` is read.  Against
-// registers: no moves, no LDS writes, 32 registers fewer; forward of 16.4k tokens, 16 heads of 128,
+// registers: no moves, no LDS writes, 32 registers fewer; forward of 17.2k tokens, 16 heads of 128,
 // window 1024: 193 -> 172 us.
 template <typename T, int DH, int ROWS, int THREADS, int AGAIN = 0>
 struct DirectTile {
@@ -455,7 +455,7 @@ __device__ __forceinline__ void unfit(f32x16 (&sums)[N], int by) {
 
 // ---------------------------------------------------------------- which keys a query tile meets
 // Workgroups of four waves take query tiles from the last to the first: a sequence's first tiles meet the
-// fewest keys, and short work at the end leaves fewer units idle (16.4k tokens, 16 heads of 128, window
+// fewest keys, and short work at the end leaves fewer units idle (17.2k tokens, 16 heads of 128, window
 // 1024: 193 -> 190 us; those of one wave, all short, are 4 us slower that way).
 
 // The tile that holds the sinks where the window's tiles do not reach it, then the window's.
@@ -527,8 +527,8 @@ __device__ __forceinline__ void add_odd_seen(const AttnArgs& a, const EmbHeads& 
 // The sums of the values that the wave's 32 queries from iw on see, weighed by exp(score - m), and of the weights:
 // one pass over the keys with a running maximum and sum for each query.  Keys and values come by tiles through
 // LDS, queries stay in registers.  Long sequences are bound by matrix cores and exponentials, which
-// are about equally busy: 16.4k tokens, 16 query and 2 key/value heads of 128, window 1024, bf16: 164 us,
-// 780 TFLOP/s of the pairs that see each other.
+// are about equally busy (39 and 47 % of the time): 17.2k tokens, 16 query and 2 key/value heads of 128, window
+// 1024, bf16: 172 us, 740 TFLOP/s of the pairs that see each other.
 template <typename T, int DH, int WAVES, bool DIRECT, int AGAIN>
 __device__ __forceinline__ void fwd_sums(const AttnArgs& a, QueryShared<T, DH, WAVES, DIRECT>& sh, const Seq& s, int h,
                                          int kh, int iw, float c, f32x16 (&o)[DH / 32], float& m, float& l) {
@@ -669,8 +669,9 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, (fwd_waves<DH, WAVES, 
 
 // ---------------------------------------------------------------- backward: dq
 // As the forward, with dout as a second right operand: unscaled sums of the gradients that the wave's 32 queries
-// from iw on have; also writes delta.  8.2k tokens, 16 and 8 heads of 128, window 1024, bf16: 114 us, 790 TFLOP/s,
-// bound as the forward is.  512 histories of up to 200, 8 heads of 64, window 64, fp16: 70 us, 3.3 TB/s.
+// from iw on have; also writes delta.  8.6k tokens, 16 and 8 heads of 128, window 1024, bf16: 114 us, 730 TFLOP/s of
+// three products, bound as the forward is.  512 histories of up to 200, 8 heads of 64, window 64, fp16: 69 us,
+// 3.7 TB/s.
 template <typename T, int DH, int WAVES, bool DIRECT, int AGAIN>
 __device__ __forceinline__ void dq_sums(const AttnArgs& a, QueryShared<T, DH, WAVES, DIRECT>& sh, const Seq& s, int h,
                                         int kh, int iw, f32x16 (&dq)[DH / 32]) {
@@ -807,8 +808,9 @@ __global__ void __launch_bounds__(Group<WAVES>::kThreads, (dq_waves<DH>)) attn_d
 // leaves one wave a SIMD; eight waves, two to each 32 keys with half of a step's rows, and keys and
 // values in LDS make it two, at a half more reads of LDS.
 //
-// 8.2k tokens, 16 and 8 heads of 128, window 1024, bf16: 187 us, 640 TFLOP/s, a tenth of it the uneven
-// end of one workgroup a unit.  512 histories of up to 200, 8 heads of 64, window 64, fp16: 70 us, 3.3 TB/s.
+// 8.6k tokens, 16 and 8 heads of 128, window 1024, bf16: 188 us, 590 TFLOP/s of four products: matrix cores, vector
+// unit and LDS are busy 29, 23 and 28 % of the time, and half of a wave's time it waits.  512 histories of up to 200,
+// 8 heads of 64, window 64, fp16: 70 us, 3.6 TB/s.
 static_assert(EMB_ATTN_MAX_SINKS <= 32, "the sinks lie in the first 32 keys");
 
 // Queries from here on see nothing of the first key tile but the sinks.
@@ -1399,9 +1401,9 @@ int sink_chunk(int64_t n_tok) {
 }
 // Whether one wave a workgroup is the better shape, by what most queries see: their window or, in short
 // sequences, what there is.  40k tokens, 8 heads of 64, fp16, four waves against one, forward / backward
-// us: 20 tokens a sequence 93 / 311 and 37 / 125; 74 tokens, window 64: 43 / 147 and 36 / 122; 400 tokens,
-// window 128: 49 / 168 and 43 / 150, 256: 50 / 176 and 53 / 166, 512: 50 / 168 and 56 / 174; 2000
-// tokens, 128: 45 / 155 and 46 / 162, 256: 55 / 186 and 63 / 205.
+// us: 20 tokens a sequence 91 / 318 and 38 / 112; 74 tokens, window 64: 44 / 143 and 34 / 108; 400 tokens,
+// window 128: 48 / 167 and 44 / 138, 256: 51 / 172 and 53 / 156, 512: 49 / 162 and 57 / 162; 2000
+// tokens, 128: 45 / 155 and 45 / 150, 256: 57 / 177 and 64 / 192.
 constexpr int64_t kOneWave = 128;
 bool one_wave(const AttnArgs& a) {
   const int64_t mean = a.n_tok / a.n_seq;

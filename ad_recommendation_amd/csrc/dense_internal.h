@@ -72,8 +72,8 @@ struct AdamTensor {
 };
 constexpr int kAdamMax = 96;
 // Elements of a workgroup: what its threads hold at once.  With more, taken in turn, the loads of a turn
-// wait for the stores of the one before: 20.8M elements in fp32 98 us, 8192 a workgroup 115; 335.6M with
-// 8-bit states 1054 and 1070.
+// wait for the stores of the one before: 20.8M elements in fp32 97 us, 8192 a workgroup 115; 335.6M with
+// 8-bit states 994, 8192 a workgroup 1.5 % more.
 constexpr int kAdamChunk = 2048;
 constexpr uint32_t kAdamChunks = 1 << 23;  // of a launch, which has fewer than 2^32 threads
 struct AdamArgs {
