@@ -1089,7 +1089,8 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, DkvShared<T, DH, WAVES, D
   dkv_sums<T, DH, WAVES, DIRECT, SINK, kBoth>(a, sh, s, kh, j0, row0, row1, dk, dv);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int jw = SINK ? 0 : j0 + 32 * (wave & 3), j = jw + (lane_id() & 31);
-  const bool odd = not_finite(dk) | not_finite(dv), bad = wave < kFirst && j < (SINK ? a.sinks : s.len) && odd;
+  const int odd = (int)not_finite(dk) | (int)not_finite(dv);  // no branch between the two
+  const bool bad = wave < kFirst && j < (SINK ? a.sinks : s.len) && odd;
   if (__builtin_expect(any_wave(bad, sh.said), 0)) {
     dkv_sums<T, DH, WAVES, DIRECT, SINK, kDkAgain>(a, sh, s, kh, j0, row0, row1, dk, dv);
     __syncthreads();  // its tiles are done with
