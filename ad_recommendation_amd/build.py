@@ -17,7 +17,7 @@ ARCH = "gfx950"
 # Packed fp32 instructions are kept out of all device code.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # Device sources and host sources of the library, without their endings.
-KERNELS = ["emb_kernels", "dense_attn", "dense_norm", "dense_adamw"]
+KERNELS = ["emb_kernels", "dense_attn", "dense_shared", "dense_cache", "dense_norm", "dense_adamw"]
 HOSTS = ["emb_host", "dense_host"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
@@ -48,7 +48,7 @@ def build(verbose: bool = False) -> str:
              os.path.join(CSRC, n + ".hip"), "-o", os.path.join(BUILD, n + ".o")] for n in KERNELS]
     jobs += [[hipcc, "-x", "c++", *COMMON, "-I", "/opt/rocm/include", "-D__HIP_PLATFORM_AMD__", "-c",
               os.path.join(CSRC, n + ".cpp"), "-o", os.path.join(BUILD, n + ".o")] for n in HOSTS]
-    with ThreadPoolExecutor(4) as pool:
+    with ThreadPoolExecutor(8) as pool:
         list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
     tmp = LIB + ".tmp"
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,

@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "dense_internal.h"
@@ -79,6 +80,22 @@ int check_written(const EmbHeads* t, int64_t tokens, int32_t heads, int32_t dim,
   return EMB_OK;
 }
 
+// Of an output with three strides: that no two of its places are one. Every stride has to pass what the smaller
+// ones span.
+int check_apart(const EmbHeads* t, int64_t n_seq, int64_t tokens, int64_t heads, int64_t dim, const std::string& name) {
+  const auto size = [](int64_t x) { return x >= 0 ? x : x > -INT64_MAX ? -x : INT64_MAX; };
+  std::pair<int64_t, int64_t> by[3] = {{size(t->seq), n_seq}, {size(t->tok), tokens}, {size(t->head), heads}};
+  std::sort(by, by + 3);
+  int64_t span = dim;
+  for (const auto& x : by) {
+    if (x.second <= 1) continue;
+    DENSE_CHECK(x.first >= span, EMB_EINVAL, "attention: places of an output overlap: " + name);
+    // past 2^62 nothing else fits between
+    span = x.first > ((int64_t)1 << 62) / x.second ? INT64_MAX : span + (x.second - 1) * x.first;
+  }
+  return EMB_OK;
+}
+
 int check_counts(int64_t n_seq, int64_t n_tok) {
   DENSE_CHECK(n_seq >= 0 && n_tok >= 0, EMB_EINVAL, "attention: negative size");
   // the kernels count tokens in 32 bits, with tiles past the last one
@@ -132,6 +149,188 @@ AttnArgs attn_args(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const
   x.dtype = a->dtype;
   x.scale = a->scale;
   return x;
+}
+
+// ---------------------------------------------------------------- caches in 8 bits
+int check_codes(const EmbHeads* t, const EmbHeads* e, const char* name) {
+  DENSE_CHECK(t && t->p && e && e->p, EMB_EINVAL, std::string("cache: null pointer: ") + name);
+  DENSE_CHECK(aligned(t->p, 8) && t->seq % 8 == 0 && t->tok % 8 == 0 && t->head % 8 == 0, EMB_EINVAL,
+              std::string("cache: codes not 8-byte aligned, or a stride no multiple of 8: ") + name);
+  return EMB_OK;
+}
+
+// ---------------------------------------------------------------- attention of candidates
+// The tokens of requests and what they see of their own.
+struct SharedCall {
+  const EmbAttn* a;
+  const EmbHeads *q, *k, *v;
+  const int32_t *off, *first;
+  int64_t n_seq, n_tok;
+};
+// The checks that every form has in common.
+int check_shared(const SharedCall& c) {
+  DENSE_TRY(check_heads(c.q, "q"));
+  DENSE_TRY(check_heads(c.k, "k"));
+  DENSE_TRY(check_heads(c.v, "v"));
+  DENSE_CHECK(c.off, EMB_EINVAL, "attention: null pointer: offsets");
+  DENSE_CHECK(aligned(c.off, 4) && aligned(c.first, 4), EMB_EINVAL, "attention: offsets or first not 4-byte aligned");
+  return EMB_OK;
+}
+SharedArgs shared_args(const SharedCall& c) {
+  SharedArgs x{};
+  static_cast<AttnArgs&>(x) = attn_args(c.a, c.q, c.k ? c.k : c.q, c.v ? c.v : c.q, c.off, c.n_seq, c.n_tok);
+  x.group = c.a->q_heads / c.a->kv_heads;
+  x.first = c.first;
+  x.own = c.first ? kOwnTiles : kOwnSelf;
+  x.back = c.a->window - 1;  // a candidate's place is the one after the last event
+  return x;
+}
+// EMB_VALIDATE=1: that `first` names a candidate's first token for each token.
+int validate_first(const SharedCall& c, hipStream_t st) {
+  if (!validate_on() || !c.first) return EMB_OK;
+  try {
+    std::vector<int32_t> f((size_t)c.n_tok), off((size_t)c.n_seq + 1);
+    hipError_t e = hipMemcpyAsync(f.data(), c.first, f.size() * 4, hipMemcpyDeviceToHost, st);
+    if (e == hipSuccess) e = hipMemcpyAsync(off.data(), c.off, off.size() * 4, hipMemcpyDeviceToHost, st);
+    if (e == hipSuccess) e = hipStreamSynchronize(st);
+    if (e != hipSuccess) return done(e, "attention: reading first");
+    for (int64_t s = 0; s < c.n_seq; ++s) {
+      for (int64_t i = off[s]; i < off[s + 1]; ++i) {
+        DENSE_CHECK(f[i] >= off[s] && f[i] <= i && f[f[i]] == f[i] && (i == off[s] || f[i] == i || f[i] == f[i - 1]),
+                    EMB_EINVAL, "attention: first does not name the first token of a candidate");
+      }
+    }
+  } catch (const std::bad_alloc&) {
+    return set_error(EMB_ENOMEM, "attention: host memory");
+  }
+  return EMB_OK;
+}
+
+// The serving forms: histories are caches, in 16 bits or (k_exp) in 8.
+int shared_cache(const SharedCall& c, const EmbHeads* hk, const EmbHeads* ke, const EmbHeads* hv, const EmbHeads* ve,
+                 const int32_t* d_lens, int64_t capacity, bool q8, const EmbHeads* out, void* d_ws, size_t ws_bytes,
+                 emb_stream_t stream, const char* what) {
+  DENSE_TRY(check_attn(c.a));
+  DENSE_TRY(check_counts(c.n_seq, c.n_tok));
+  DENSE_TRY(check_counts(c.n_seq, capacity));
+  if (c.n_seq == 0 || c.n_tok == 0) return EMB_OK;
+  DENSE_TRY(check_shared(c));
+  DENSE_TRY(check_written(out, c.n_tok, c.a->q_heads, c.a->dim, "out"));
+  EmbHeads one = *out;
+  one.seq = 0;
+  DENSE_TRY(check_apart(&one, 1, c.n_tok, c.a->q_heads, c.a->dim, "out"));
+  DENSE_CHECK(hk && hv && (!q8 || (ke && ve)), EMB_EINVAL, "attention: null pointer: cache");
+  if (capacity > 0) {  // an empty cache has nothing to point at
+    if (q8) {
+      DENSE_TRY(check_codes(hk, ke, "k_cache"));
+      DENSE_TRY(check_codes(hv, ve, "v_cache"));
+    } else {
+      DENSE_TRY(check_heads(hk, "k_cache"));
+      DENSE_TRY(check_heads(hv, "v_cache"));
+    }
+  }
+  DENSE_CHECK(d_lens, EMB_EINVAL, "attention: null pointer: lens");
+  DENSE_CHECK(aligned(d_lens, 4), EMB_EINVAL, "attention: lens not 4-byte aligned");
+  SharedArgs x = shared_args(c);
+  x.hk = *hk;
+  x.hv = *hv;
+  if (q8) {
+    x.ke = *ke;
+    x.ve = *ve;
+  }
+  x.hist = d_lens;
+  x.n_hist = capacity;
+  const SharedPlan p = plan_shared(*c.a, c.n_seq, c.n_tok, capacity, false);
+  DENSE_TRY(check_launch(shared_threads(x, p)));
+  DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
+  DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  DENSE_TRY(validate_offsets(c.off, c.n_seq, c.n_tok, false, st));
+  DENSE_TRY(validate_offsets(d_lens, c.n_seq, capacity, true, st));
+  DENSE_TRY(validate_first(c, st));
+  x.out = *out;
+  x.part = static_cast<float*>(d_ws);
+  return done(launch_shared(x, p, q8, st), what);
+}
+
+// The training forms' checks of packed histories.
+int check_packed(const SharedCall& c, const EmbHeads* hk, const EmbHeads* hv, const int32_t* hist_off, int64_t n_hist) {
+  DENSE_TRY(check_shared(c));
+  if (n_hist > 0) {
+    DENSE_TRY(check_heads(hk, "hist_k"));
+    DENSE_TRY(check_heads(hv, "hist_v"));
+  } else {
+    DENSE_CHECK(hk && hv, EMB_EINVAL, "attention: null pointer: history");
+  }
+  DENSE_CHECK(hist_off, EMB_EINVAL, "attention: null pointer: hist_offsets");
+  DENSE_CHECK(aligned(hist_off, 4), EMB_EINVAL, "attention: hist_offsets not 4-byte aligned");
+  return EMB_OK;
+}
+SharedArgs packed_args(const SharedCall& c, const EmbHeads* hk, const EmbHeads* hv, const int32_t* hist_off,
+                       int64_t n_hist) {
+  SharedArgs x = shared_args(c);
+  x.hk = *hk;
+  x.hv = *hv;
+  x.hist = hist_off;
+  x.n_hist = n_hist;
+  x.packed = 1;
+  return x;
+}
+int64_t mean_of(int64_t n, int64_t count) {
+  count = std::max<int64_t>(count, 1);
+  return (n + count - 1) / count;
+}
+
+int cache_call(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k, const EmbHeads* v,
+               const int32_t* d_offsets, const int32_t* d_start, int64_t n_seq, int64_t n_tok, const EmbHeads* kc,
+               const EmbHeads* ke, const EmbHeads* vc, const EmbHeads* ve, int64_t capacity, bool write,
+               hipStream_t st, const char* what) {
+  DENSE_CHECK(dtype_ok(dtype), EMB_EINVAL, "cache: bad dtype");
+  DENSE_CHECK(kv_heads >= 1 && kv_heads <= 4096, EMB_EINVAL, "cache: kv_heads must lie in [1, 4096]");
+  DENSE_CHECK(dim >= 8 && dim <= 128 && dim % 8 == 0, EMB_EINVAL, "cache: dim must be a multiple of 8 from 8 to 128");
+  DENSE_TRY(check_counts(n_seq, n_tok));
+  DENSE_TRY(check_counts(n_seq, capacity));
+  if (n_seq == 0 || n_tok == 0 || (write && capacity == 0)) return EMB_OK;
+  DENSE_TRY(check_heads(k, "k"));
+  DENSE_TRY(check_heads(v, "v"));
+  if (capacity > 0) {
+    DENSE_TRY(check_codes(kc, ke, "k_cache"));
+    DENSE_TRY(check_codes(vc, ve, "v_cache"));
+  } else {
+    DENSE_CHECK(kc && ke && vc && ve, EMB_EINVAL, "cache: null pointer: cache");
+  }
+  if (write) {
+    DENSE_TRY(check_apart(kc, n_seq, capacity, kv_heads, dim, "k_cache"));
+    DENSE_TRY(check_apart(vc, n_seq, capacity, kv_heads, dim, "v_cache"));
+    DENSE_TRY(check_apart(ke, n_seq, capacity, kv_heads, 1, "k_exp"));
+    DENSE_TRY(check_apart(ve, n_seq, capacity, kv_heads, 1, "v_exp"));
+  } else {
+    for (const EmbHeads* t : {k, v}) {
+      EmbHeads one = *t;
+      one.seq = 0;
+      DENSE_TRY(check_apart(&one, 1, n_tok, kv_heads, dim, t == k ? "k" : "v"));
+    }
+  }
+  DENSE_CHECK(d_offsets || n_tok == n_seq, EMB_EINVAL, "cache: without offsets every sequence has one token");
+  DENSE_CHECK(aligned(d_offsets, 4) && aligned(d_start, 4), EMB_EINVAL, "cache: offsets or start not 4-byte aligned");
+  CacheArgs x{};
+  x.x[0] = *k;
+  x.x[1] = *v;
+  x.code[0] = *kc;
+  x.code[1] = *vc;
+  x.exp[0] = *ke;
+  x.exp[1] = *ve;
+  x.off = d_offsets;
+  x.start = d_start;
+  x.n_tok = n_tok;
+  x.capacity = capacity;
+  x.n_seq = (int32_t)n_seq;
+  x.heads = kv_heads;
+  x.dim = dim;
+  x.dtype = dtype;
+  DENSE_TRY(check_launch(cache_threads(x)));
+  if (d_offsets) DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
+  return done(launch_cache(x, write, st), what);
 }
 
 // ---------------------------------------------------------------- AdamW
@@ -327,6 +526,133 @@ int attn_window_decode(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k_ca
   x.out = *out;
   x.part = static_cast<float*>(d_ws);
   return done(launch_attn_decode(x, p, st), "attn_window_decode");
+}
+
+int attn_window_decode_q8_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t capacity, size_t* bytes) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, capacity));
+  DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
+  *bytes = plan_shared(*a, n_seq, n_seq, capacity, true).bytes;
+  return EMB_OK;
+}
+
+int attn_window_decode_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k_cache, const EmbHeads* k_exp,
+                          const EmbHeads* v_cache, const EmbHeads* v_exp, const int32_t* d_lens, int64_t n_seq,
+                          int64_t capacity, const EmbHeads* out, void* d_ws, size_t ws_bytes, emb_stream_t stream) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, capacity));
+  if (n_seq == 0) return EMB_OK;
+  DENSE_TRY(check_heads(q, "q"));
+  DENSE_TRY(check_written(out, n_seq, a->q_heads, a->dim, "out"));
+  EmbHeads one = *out;
+  one.seq = 0;
+  DENSE_TRY(check_apart(&one, 1, n_seq, a->q_heads, a->dim, "out"));
+  DENSE_CHECK(k_cache && v_cache && k_exp && v_exp, EMB_EINVAL, "attention: null pointer: cache");
+  if (capacity > 0) {  // an empty cache has nothing to point at
+    DENSE_TRY(check_codes(k_cache, k_exp, "k_cache"));
+    DENSE_TRY(check_codes(v_cache, v_exp, "v_cache"));
+  }
+  DENSE_CHECK(d_lens, EMB_EINVAL, "attention: null pointer: lens");
+  DENSE_CHECK(aligned(d_lens, 4), EMB_EINVAL, "attention: lens not 4-byte aligned");
+  SharedArgs x = shared_args({a, q, nullptr, nullptr, nullptr, nullptr, n_seq, n_seq});
+  x.own = kOwnNone;
+  x.back = a->window;  // the query is at the last cached event
+  x.hk = *k_cache;
+  x.hv = *v_cache;
+  x.ke = *k_exp;
+  x.ve = *v_exp;
+  x.hist = d_lens;
+  x.n_hist = capacity;
+  const SharedPlan p = plan_shared(*a, n_seq, n_seq, capacity, true);
+  DENSE_TRY(check_launch(shared_threads(x, p)));
+  DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
+  DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  DENSE_TRY(validate_offsets(d_lens, n_seq, capacity, true, st));
+  x.out = *out;
+  x.part = static_cast<float*>(d_ws);
+  return done(launch_shared(x, p, true, st), "attn_window_decode_q8");
+}
+
+int attn_shared_fwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t n_hist, size_t* bytes) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, n_tok));
+  DENSE_TRY(check_counts(n_seq, n_hist));
+  DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
+  *bytes = plan_shared(*a, n_seq, n_tok, mean_of(n_hist, n_seq), false).bytes;
+  return EMB_OK;
+}
+
+int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v, const EmbHeads* hist_k,
+                    const EmbHeads* hist_v, const int32_t* d_offsets, const int32_t* d_first,
+                    const int32_t* d_hist_offsets, int64_t n_seq, int64_t n_tok, int64_t n_hist, const EmbHeads* out,
+                    float* d_lse, void* d_ws, size_t ws_bytes, emb_stream_t stream) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, n_tok));
+  DENSE_TRY(check_counts(n_seq, n_hist));
+  if (n_seq == 0 || n_tok == 0) return EMB_OK;
+  const SharedCall c{a, q, k, v, d_offsets, d_first, n_seq, n_tok};
+  DENSE_TRY(check_packed(c, hist_k, hist_v, d_hist_offsets, n_hist));
+  DENSE_TRY(check_written(out, n_tok, a->q_heads, a->dim, "out"));
+  EmbHeads one = *out;
+  one.seq = 0;
+  DENSE_TRY(check_apart(&one, 1, n_tok, a->q_heads, a->dim, "out"));
+  DENSE_CHECK(aligned(d_lse, 4), EMB_EINVAL, "attention: lse not 4-byte aligned");
+  SharedArgs x = packed_args(c, hist_k, hist_v, d_hist_offsets, n_hist);
+  const SharedPlan p = plan_shared(*a, n_seq, n_tok, mean_of(n_hist, n_seq), false);
+  DENSE_TRY(check_launch(shared_threads(x, p)));
+  DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
+  DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
+  DENSE_TRY(validate_offsets(d_hist_offsets, n_seq, n_hist, false, st));
+  DENSE_TRY(validate_first(c, st));
+  x.out = *out;
+  x.lse = d_lse;
+  x.part = static_cast<float*>(d_ws);
+  return done(launch_shared(x, p, false, st), "attn_shared_fwd");
+}
+
+int attn_shared_cache_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t capacity, size_t* bytes) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, n_tok));
+  DENSE_TRY(check_counts(n_seq, capacity));
+  DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
+  *bytes = plan_shared(*a, n_seq, n_tok, capacity, false).bytes;
+  return EMB_OK;
+}
+
+int attn_shared_cache(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
+                      const EmbHeads* k_cache, const EmbHeads* v_cache, const int32_t* d_offsets,
+                      const int32_t* d_first, const int32_t* d_lens, int64_t n_seq, int64_t n_tok, int64_t capacity,
+                      const EmbHeads* out, void* d_ws, size_t ws_bytes, emb_stream_t stream) {
+  return shared_cache({a, q, k, v, d_offsets, d_first, n_seq, n_tok}, k_cache, nullptr, v_cache, nullptr, d_lens,
+                      capacity, false, out, d_ws, ws_bytes, stream, "attn_shared_cache");
+}
+
+int attn_shared_cache_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
+                         const EmbHeads* k_cache, const EmbHeads* k_exp, const EmbHeads* v_cache,
+                         const EmbHeads* v_exp, const int32_t* d_offsets, const int32_t* d_first,
+                         const int32_t* d_lens, int64_t n_seq, int64_t n_tok, int64_t capacity, const EmbHeads* out,
+                         void* d_ws, size_t ws_bytes, emb_stream_t stream) {
+  return shared_cache({a, q, k, v, d_offsets, d_first, n_seq, n_tok}, k_cache, k_exp, v_cache, v_exp, d_lens, capacity,
+                      true, out, d_ws, ws_bytes, stream, "attn_shared_cache_q8");
+}
+
+int cache_q8_write(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k, const EmbHeads* v,
+                   const int32_t* d_offsets, const int32_t* d_start, int64_t n_seq, int64_t n_tok,
+                   const EmbHeads* k_cache, const EmbHeads* k_exp, const EmbHeads* v_cache, const EmbHeads* v_exp,
+                   int64_t capacity, emb_stream_t stream) {
+  return cache_call(kv_heads, dim, dtype, k, v, d_offsets, d_start, n_seq, n_tok, k_cache, k_exp, v_cache, v_exp,
+                    capacity, true, static_cast<hipStream_t>(stream), "cache_q8_write");
+}
+
+int cache_q8_read(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k_cache, const EmbHeads* k_exp,
+                  const EmbHeads* v_cache, const EmbHeads* v_exp, int64_t capacity, const int32_t* d_offsets,
+                  const int32_t* d_start, int64_t n_seq, int64_t n_tok, const EmbHeads* k, const EmbHeads* v,
+                  emb_stream_t stream) {
+  return cache_call(kv_heads, dim, dtype, k, v, d_offsets, d_start, n_seq, n_tok, k_cache, k_exp, v_cache, v_exp,
+                    capacity, false, static_cast<hipStream_t>(stream), "cache_q8_read");
 }
 
 static int check_norm(const void* y, const void* gate, int32_t gate_kind, const float* w_post,

@@ -1,5 +1,6 @@
 // Internal declarations shared by the dense side's host entry points (dense_host.cpp) and its gfx950
-// kernels (dense_attn.hip, dense_norm.hip, dense_adamw.hip).  Not part of the public C ABI.
+// kernels (dense_attn.hip, dense_shared.hip, dense_shared_bwd.hip, dense_cache.hip, dense_norm.hip,
+// dense_adamw.hip).  Not part of the public C ABI.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -41,6 +42,52 @@ int64_t attn_decode_threads(const AttnArgs& a, const AttnDecodePlan& p);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnDecodePlan& p, hipStream_t st);
+
+// ---------------------------------------------------------------- attention of candidates
+// What a query row sees of its request's own tokens: nothing (a newest event, which is cached), its token
+// alone, or its candidate's tokens up to its own.
+enum { kOwnNone, kOwnSelf, kOwnTiles };
+struct SharedArgs : AttnArgs {  // off: tokens of requests, null for one token each
+  EmbHeads hk, hv;              // history; in 8 bits its codes
+  EmbHeads ke, ve;              // their exponents
+  EmbHeads dhk, dhv;
+  const int32_t* hist;          // packed: offsets of n_hist events; caches: lengths up to n_hist
+  const int32_t* first;         // kOwnTiles
+  float* self;                  // backward, kOwnSelf: p and ds of each row with itself, [2][q_heads][n_tok]
+  int64_t n_hist;
+  int32_t group;                // query heads of a key/value head
+  int32_t back;                 // history events of the window
+  int32_t packed, own;
+};
+struct SharedPlan {
+  int32_t rows;    // of a tile: 32, whose keys the waves share out, or 128, 32 a wave
+  int32_t waves;   // of 32 rows: of a workgroup
+  int32_t splits;  // of a tile's keys
+  size_t bytes;
+};
+// hist: events that a history may have, or has on average.  one: one token a request, without offsets.
+SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, bool one);
+int64_t shared_threads(const SharedArgs& a, const SharedPlan& p);
+hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipStream_t st);
+
+struct SharedBwdPlan {
+  size_t off_self, bytes;
+};
+SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_tok);
+int64_t shared_bwd_threads(const SharedArgs& a);
+hipError_t launch_shared_bwd(const SharedArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------- caches in 8 bits
+struct CacheArgs {
+  EmbHeads x[2];       // keys and values of packed tokens
+  EmbHeads code[2], exp[2];
+  const int32_t* off;  // null: one token a sequence
+  const int32_t* start;  // null: 0
+  int64_t n_tok, capacity;
+  int32_t n_seq, heads, dim, dtype;
+};
+int64_t cache_threads(const CacheArgs& a);
+hipError_t launch_cache(const CacheArgs& a, bool write, hipStream_t st);
 
 // ---------------------------------------------------------------- norms
 struct NormArgs {

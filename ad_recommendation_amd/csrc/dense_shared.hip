@@ -1,0 +1,578 @@
+// Attention of many candidates of a request to its one history and to their own tokens; and of a newest event to
+// a cache in 8 bits, which is the same with one query token a request and nothing of its own.
+//
+//   see(i, j) = j of the request's history, inside its window or a sink; or j of i's candidate, j <= i
+//   s_ij = scale q_i . k_j;  p_i = softmax(s_i);  out_i = sum_j p_ij v_j;  lse_i = log sum_j exp(s_ij)
+//
+// One pass over the keys with a running maximum and sum for each query row; rows are (token, head of the group),
+// so a history is read once for every candidate and head that shares it.  Two shapes: 128 rows a workgroup, 32 a
+// wave, which share tiles of 64 keys in LDS (bound by matrix cores and exponentials); and, where a request has few
+// rows, 32 rows a workgroup whose waves take tiles of 32 keys in turn, each with a softmax of its own, and meet in
+// LDS (bound by reading the history).  Either may share a request's keys out over several workgroups, whose sums a
+// second kernel joins.
+#include <algorithm>
+#include <initializer_list>
+
+#include "dense_shared_device.h"
+
+namespace emb {
+
+namespace {
+
+// The maximum m that o and l stand at moves to that of the scores as well, only when it is over 2^8 times the old
+// one's exponential: below that the probabilities stay small enough for 16 bits and the sums for 32.  Scores
+// become probabilities, their sum goes to l (a lane's half of it).
+template <int N, int DB>
+__device__ __forceinline__ void soften(f32x16 (&sc)[N], f32x16 (&o)[DB], float& m, float& l, float c) {
+  float top = sc[0][0];
+#pragma unroll
+  for (int r = 1; r < 16 * N; ++r) top = fmaxf(top, sc[r >> 4][r & 15]);
+  top = swap32_max(top);
+  if (__any((top - m) * c > 8.f)) {
+    const float mn = fmaxf(m, top);
+    const float by = m == -kInf ? 0.f : exp2f((m - mn) * c);
+    m = mn;
+    l *= by;
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[db] *= by;
+  }
+  const float off = m == -kInf ? 0.f : m * c;
+#pragma unroll
+  for (int r = 0; r < 16 * N; ++r) {
+    sc[r >> 4][r & 15] = __builtin_amdgcn_exp2f(fmaf(sc[r >> 4][r & 15], c, -off));
+    l += sc[r >> 4][r & 15];
+  }
+}
+
+// Sums o and l at the maximum m after the history meet the row's own tokens.  They come after the loop over the
+// history and share no address with it (AGAIN, see lane_id), so that it keeps its registers.
+//
+// A token alone: its score and value on the vector unit, so nothing that is not finite reaches another row.  A
+// score of minus infinity has no weight beside others; one that is not finite otherwise makes the sum NaN.
+template <typename T, int DH>
+__device__ __forceinline__ void meet_self(const SharedArgs& a, int64_t tok, int kh, bool live,
+                                          const typename Vec8<T>::t (&q)[DH / 16], float c, f32x16 (&o)[DH / 32],
+                                          float& m, float& l) {
+  const float s = dot_row<T, DH, 3>(q, static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head, live, a.dim);
+  if (!live || s == -kInf) return;
+  const float mn = fmaxf(m, s), by = m == -kInf ? 0.f : exp2f((m - mn) * c), p = exp2f((s - mn) * c);
+  m = mn;
+  l = l * by + (lane_id<3>() < 32 ? p : 0.f);
+  typedef T V __attribute__((ext_vector_type(4)));
+  const T* v = static_cast<const T*>(a.v.p) + tok * a.v.tok + kh * a.v.head;
+#pragma unroll
+  for (int db = 0; db < DH / 32; ++db) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int col = db * 32 + 8 * g + 4 * (lane_id<3>() >> 5);
+      f32x4 x = {};
+      if (col < a.dim) x = __builtin_convertvector(*reinterpret_cast<const V*>(v + col), f32x4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[db][4 * g + e] = o[db][4 * g + e] * by + p * x[e];
+    }
+  }
+}
+
+// 32 own tokens from j0 on, keys and values in LDS at row `at0`, of which a row sees lo to hi: pairs that do not
+// see each other have probabilities of zero, whose products with what is not finite are left out.
+template <typename T, int DH, typename R>
+__device__ __forceinline__ void meet_own(const char* kt, const char* vt, const R& at, int at0, int lo, int hi, int j0,
+                                         const typename Vec8<T>::t (&q)[DH / 16], float c, f32x16 (&o)[DH / 32],
+                                         float& m, float& l) {
+  typedef typename Vec8<T>::t V8;
+  f32x16 sc[1] = {};
+#pragma unroll
+  for (int ks = 0; ks < DH / 16; ++ks) sc[0] = mma(left<T>(kt, at, at0, ks), q[ks], sc[0]);
+  const uint32_t see = hide_outside<3>(lo, hi, j0, sc[0], -kInf);
+  soften(sc, o, m, l, c);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const V8 pb = right_of<T>(sc[0], 8 * k), one = ones<T>(see, 8 * k);
+#pragma unroll
+    for (int db = 0; db < DH / 32; ++db) {
+      const V8 v = left_t<T>(vt, at, at0 + 16 * k, db);
+      o[db] = mma(finite_of<T>(v), pb, o[db]);
+      add_odd<T>(o[db], v, one, one);
+    }
+  }
+}
+
+// Where sums of split keys go: [split][token][q head][dim], then [..][2] of maximum (in powers of two) and sum.
+__device__ __forceinline__ float* part_of(const SharedArgs& a, int split) {
+  return a.part + (int64_t)split * a.n_tok * a.q_heads * a.dim;
+}
+__device__ __forceinline__ float* part_stats(const SharedArgs& a, int splits, int split, int64_t tok, int qh) {
+  return part_of(a, splits) + (((int64_t)split * a.n_tok + tok) * a.q_heads + qh) * 2;
+}
+
+// ---------------------------------------------------------------- 128 rows
+enum { kByRegisters, kDirect, kCodes };  // how tiles of history get to LDS
+
+// Tiles of keys or values in 8 bits through registers: codes are converted on their way to LDS.
+template <typename T, int DH, int ROWS, int THREADS>
+struct CodesTile : RegisterTile<T, DH, ROWS, THREADS> {
+  typedef RegisterTile<T, DH, ROWS, THREADS> R;
+  u32x2 code[R::kRegs];
+  uint32_t exps[R::kRegs];
+  __device__ __forceinline__ void load(const uint8_t* base, int64_t stride, const uint8_t* exp, int64_t exp_stride,
+                                       int row0, int end, int D) {
+#pragma unroll
+    for (int n = 0; n < R::kRegs; ++n) {
+      const int idx = threadIdx.x + n * THREADS;
+      const int row = row0 + idx / R::kPieces, col = idx % R::kPieces * 8;
+      code[n] = u32x2{0, 0};
+      exps[n] = 0;
+      if (row < end && col < D) {
+        code[n] = *reinterpret_cast<const u32x2*>(base + row * stride + col);
+        exps[n] = exp[row * exp_stride];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int n = 0; n < R::kRegs; ++n) {
+      const int idx = threadIdx.x + n * THREADS;
+      *reinterpret_cast<typename Vec8<T>::t*>(lds + R::at(idx / R::kPieces, idx % R::kPieces)) =
+          of_codes<T>(code[n], exps[n]);
+    }
+  }
+};
+
+template <typename T, int DH, int HOW>
+struct WideTile {
+  static constexpr int kRows = 64, kThreads = 256;
+  typedef std::conditional_t<HOW == kDirect, DirectTile<T, DH, kRows, kThreads>,
+                             std::conditional_t<HOW == kCodes, CodesTile<T, DH, kRows, kThreads>,
+                                                RegisterTile<T, DH, kRows, kThreads>>> t;
+};
+
+template <int DH, int HOW>
+constexpr int wide_waves = DH == 128 ? 2 : DH == 64 ? 3 : 4;
+
+template <typename T, int DH, int HOW>
+__global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(SharedArgs a, int splits) {
+  typedef typename Vec8<T>::t V8;
+  typedef typename WideTile<T, DH, HOW>::t Tile;
+  constexpr int kRows = 64, kTile = 128;
+  constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
+  __shared__ __attribute__((aligned(256))) char lds[2][2][kBytes];
+  int block = blockIdx.x;
+  const int kh = block % a.kv_heads;
+  block /= a.kv_heads;
+  const int split = block % splits;
+  const Seq s = find_rows<kTile>(a, block / splits);
+  const int rows = s.len * a.group;
+  if (s.tile < 0 || (int64_t)s.tile * kTile >= rows) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r0 = s.tile * kTile, rw = r0 + wave * 32, h0 = kh * a.group;
+  const int last = min(r0 + kTile, rows) - 1;  // of the workgroup's rows
+
+  typedef PackedRows<T, DH, Tile> Rows;
+  Rows ql;
+  ql.load(a, a.q, s.begin, h0, rw, a.scale != 0.f ? rows : 0);
+  const History hist = history(a, s.index);
+  const HistoryTiles<kRows> tiles(hist);
+  const int per = (tiles.total + splits - 1) / splits;
+  const int it0 = min(split * per, tiles.total), it1 = min(it0 + per, tiles.total);
+
+  typedef std::conditional_t<HOW == kCodes, uint8_t, T> H;
+  const H* hk = history_of<H>(a, a.hk, hist, s.index, kh);
+  const H* hv = history_of<H>(a, a.hv, hist, s.index, kh);
+  const uint8_t* ke = HOW == kCodes ? history_of<uint8_t>(a, a.ke, hist, s.index, kh) : nullptr;
+  const uint8_t* ve = HOW == kCodes ? history_of<uint8_t>(a, a.ve, hist, s.index, kh) : nullptr;
+  Tile kl, vl;
+  auto load = [&](int it, char (*to)[kBytes]) {
+    const int j0 = tiles.key0(it), end = tiles.end(it);
+    if constexpr (HOW == kCodes) {
+      kl.load(hk, a.hk.tok, ke, a.ke.tok, j0, end, a.dim);
+      vl.load(hv, a.hv.tok, ve, a.ve.tok, j0, end, a.dim);
+    } else {
+      kl.load(to[0], hk, a.hk.tok, j0, end, a.dim);
+      vl.load(to[1], hv, a.hv.tok, j0, end, a.dim);
+    }
+  };
+  if (it0 < it1) load(it0, lds[0]);
+  const typename Tile::Reads at;
+  V8 q[DH / 16];
+  char* const part = lds[1][wave >> 1];  // a wave's own part of the tiles that the first step does not use
+  const int part0 = 32 * (wave & 1);
+  ql.to_right(part, part0, at, q);
+  // the running maximum is one of q . k, so a negative scale turns q around and a scale of zero
+  // leaves zeros
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks) q[ks] = -q[ks];
+  }
+  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+
+  f32x16 o[DH / 32] = {};
+  float m = -kInf, l = 0.f;  // the maximum that o and l stand at; this lane's half of the sum
+  auto meet = [&](int it, char (*now)[kBytes], char (*next)[kBytes]) {
+    kl.store(now[0]);
+    vl.store(now[1]);
+    if (HOW != kDirect && it + 1 < it1) load(it + 1, next);
+    Tile::arrived();
+    __syncthreads();  // this tile is there, and the other buffer is no longer read
+    if (HOW == kDirect && it + 1 < it1) load(it + 1, next);
+    if (rw >= rows) return;
+    f32x16 sc[2] = {};
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) sc[sub] = mma(left<T>(now[0], at, 32 * sub, ks), q[ks], sc[sub]);
+    const int n = tiles.end(it) - tiles.key0(it);
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+      if (32 * sub + 32 > n) hide_from(n, 32 * sub, sc[sub], -kInf);
+    soften(sc, o, m, l, c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const V8 pb = right_of<T>(sc[k >> 1], 8 * (k & 1));
+#pragma unroll
+      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(now[1], at, 16 * k, db), pb, o[db]);
+    }
+  };
+  // two tiles a turn, so that the buffers' places are constants
+  for (int it = it0; it < it1; it += 2) {
+    meet(it, lds[0], lds[1]);
+    if (it + 1 < it1) meet(it + 1, lds[1], lds[0]);
+  }
+
+  const int r = rw + (lane_id<3>() & 31);
+  const bool live = r < rows;
+  const Row row = row_at(a, live ? r : last);
+  if (split == splits - 1) {
+    if (a.own == kOwnSelf) {
+      meet_self<T, DH>(a, s.begin + row.tok, kh, live, q, c, o, m, l);
+    } else {
+      typedef RegisterTile<T, DH, kRows, 256, 3> OwnTile;
+      const typename OwnTile::Reads own_at;
+      const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
+      for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)); j0 < end; j0 += kRows) {
+        OwnTile x, y;
+        x.load(nullptr, static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head, a.k.tok, j0, end, a.dim);
+        y.load(nullptr, static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head, a.v.tok, j0, end, a.dim);
+        __syncthreads();  // the tile before is done with
+        x.store(lds[0][0]);
+        y.store(lds[0][1]);
+        __syncthreads();
+        if (rw >= rows) continue;
+        for (int sub = 0; sub < 2; ++sub)
+          if (j0 + 32 * sub < end)
+            meet_own<T, DH>(lds[0][0], lds[0][1], own_at, 32 * sub, lo, row.tok, j0 + 32 * sub, q, c, o, m, l);
+      }
+    }
+  }
+  l = swap32_sum(l);
+  const int64_t tok = s.begin + row.tok;
+  if (splits > 1) {
+    if (!live) return;
+    const EmbHeads to{part_of(a, split), 0, (int64_t)a.q_heads * a.dim, a.dim};
+    store_row<float, DH>(to, tok, h0 + row.g, a.dim, o, 1.f);
+    if (lane_id() < 32) *reinterpret_cast<f32x2*>(part_stats(a, splits, split, tok, h0 + row.g)) = f32x2{m * c, l};
+    return;
+  }
+  __syncthreads();  // the tiles are done with
+  if (rw >= rows) return;
+  PackedRows<T, DH, Tile, 3>::store(a, a.out, s.begin, h0, rw, rows, lds[1][wave >> 1], part0, o, 1.f / l);
+  if (live && a.lse && lane_id() < 32) a.lse[(int64_t)(h0 + row.g) * a.n_tok + tok] = m * c * kLn2 + logf(l);
+}
+
+// ---------------------------------------------------------------- 32 rows
+// The waves' tiles come through registers, the next one under way while one is computed.
+template <typename T, int DH, int WAVES, bool CODES>
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow(SharedArgs a, int splits) {
+  typedef typename Vec8<T>::t V8;
+  typedef RegisterTile<T, DH, 32, 64> Tile;
+  constexpr int kRegs = Tile::kRegs, kPieces = Tile::kPieces;
+  __shared__ __attribute__((aligned(16))) char lds[WAVES][2][Tile::kBytes];
+  __shared__ float stats[WAVES][2][32];
+  int block = blockIdx.x;
+  const int kh = block % a.kv_heads;
+  block /= a.kv_heads;
+  const int split = block % splits;
+  const Seq s = find_rows<32>(a, block / splits);
+  const int rows = s.len * a.group;
+  if (s.tile < 0 || (int64_t)s.tile * 32 >= rows) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+  const int r0 = s.tile * 32, h0 = kh * a.group, last = min(r0 + 32, rows) - 1;
+  const int r = r0 + (lane & 31);
+  const bool live = r < rows;
+  const Row row = row_at(a, live ? r : last);
+  const int64_t tok = s.begin + row.tok;
+
+  V8 q[DH / 16];
+  right_row<T, DH>(a.q, tok, h0 + row.g, live && a.scale != 0.f, a.dim, q);
+  const History hist = history(a, s.index);
+  const HistoryTiles<32> tiles(hist);
+  const int per = (tiles.total + splits - 1) / splits;
+  const int it0 = min(split * per, tiles.total), it1 = min(it0 + per, tiles.total);
+
+  typedef std::conditional_t<CODES, uint8_t, T> H;
+  typedef std::conditional_t<CODES, u32x2, u32x4> Piece;
+  const H* hk = history_of<H>(a, a.hk, hist, s.index, kh);
+  const H* hv = history_of<H>(a, a.hv, hist, s.index, kh);
+  const uint8_t* ke = CODES ? history_of<uint8_t>(a, a.ke, hist, s.index, kh) : nullptr;
+  const uint8_t* ve = CODES ? history_of<uint8_t>(a, a.ve, hist, s.index, kh) : nullptr;
+  Piece kr[kRegs], vr[kRegs];
+  uint32_t kx[CODES ? kRegs : 1], vx[CODES ? kRegs : 1];
+  auto load = [&](int it) {
+    const int j0 = tiles.key0(it), end = tiles.end(it);
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane + n * 64, j = j0 + idx / kPieces, cl = idx % kPieces * 8;
+      kr[n] = vr[n] = Piece{};
+      if (CODES) kx[n] = vx[n] = 0;
+      if (j < end && cl < a.dim) {
+        kr[n] = *reinterpret_cast<const Piece*>(hk + j * a.hk.tok + cl);
+        vr[n] = *reinterpret_cast<const Piece*>(hv + j * a.hv.tok + cl);
+        if (CODES) {
+          kx[n] = ke[j * a.ke.tok];
+          vx[n] = ve[j * a.ve.tok];
+        }
+      }
+    }
+  };
+  int it = it0 + wave;
+  if (it < it1) load(it);
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks) q[ks] = -q[ks];
+  }
+  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+  f32x16 o[DH / 32] = {};
+  float m = -kInf, l = 0.f;
+  const typename Tile::Reads at;
+  char* kt = lds[wave][0];
+  char* vt = lds[wave][1];
+  for (; it < it1; it += WAVES) {
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane + n * 64, to = Tile::at(idx / kPieces, idx % kPieces);
+      if constexpr (CODES) {
+        *reinterpret_cast<V8*>(kt + to) = of_codes<T>(kr[n], kx[n]);
+        *reinterpret_cast<V8*>(vt + to) = of_codes<T>(vr[n], vx[n]);
+      } else {
+        *reinterpret_cast<u32x4*>(kt + to) = kr[n];
+        *reinterpret_cast<u32x4*>(vt + to) = vr[n];
+      }
+    }
+    if (it + WAVES < it1) load(it + WAVES);
+    // the tile is the wave's own: its LDS accesses are carried out in order
+    WaveRows<T, DH, Tile>::wave_sync();
+    f32x16 sc[1] = {};
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks) sc[0] = mma(left<T>(kt, at, 0, ks), q[ks], sc[0]);
+    const int n = tiles.end(it) - tiles.key0(it);
+    if (n < 32) hide_from(n, 0, sc[0], -kInf);
+    soften(sc, o, m, l, c);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const V8 pb = right_of<T>(sc[0], 8 * k);
+#pragma unroll
+      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(vt, at, 16 * k, db), pb, o[db]);
+    }
+    WaveRows<T, DH, Tile>::wave_sync();
+  }
+  if (split == splits - 1) {
+    if (a.own == kOwnSelf) {
+      if (wave == 0) meet_self<T, DH>(a, tok, kh, live, q, c, o, m, l);
+    } else if (a.own == kOwnTiles) {
+      typedef WaveRows<T, DH, Tile, 3> OwnRows;
+      const typename RegisterTile<T, DH, 32, 64, 3>::Reads own_at;
+      const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
+      for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)) + 32 * wave; j0 < end; j0 += 32 * WAVES) {
+        OwnRows::wave_sync();
+        for (int x = 0; x < 2; ++x) {  // one after the other: there are few, and two would not fit the registers
+          OwnRows rows_;
+          rows_.load(x ? a.v : a.k, s.begin + j0, kh, end - j0, a.dim);
+#pragma unroll
+          for (int n = 0; n < kRegs; ++n) {
+            const int idx = lane_id<3>() + n * 64;
+            *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = rows_.r[n];
+          }
+        }
+        OwnRows::wave_sync();
+        meet_own<T, DH>(kt, vt, own_at, 0, lo, row.tok, j0, q, c, o, m, l);
+      }
+    }
+  }
+  l = swap32_sum(l);
+  // the waves meet: each leaves its sums in its own part of LDS, and four rows of a column at a time
+  // are scaled to the common maximum and added in the waves' order
+  if (lane < 32) {
+    stats[wave][0][lane] = m;
+    stats[wave][1][lane] = l;
+  }
+  static_assert(sizeof(lds[0]) >= sizeof(float) * 32 * DH, "a wave's sums take its tiles' place");
+  f32x4* mine = reinterpret_cast<f32x4*>(lds[wave]);
+#pragma unroll
+  for (int x = 0; x < DH / 8; ++x) {
+    const f32x16 t = o[x >> 2];
+    const int e = (x & 3) * 4;
+    mine[x * 64 + lane] = f32x4{t[e], t[e + 1], t[e + 2], t[e + 3]};
+  }
+  __syncthreads();
+  float top = -kInf, sum = 0.f, by[WAVES];
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const float mw = stats[w][0][lane & 31];
+    top = mw > top || mw != mw ? mw : top;  // NaN stays
+  }
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const float mw = stats[w][0][lane & 31];
+    by[w] = mw == -kInf ? 0.f : mw == top ? 1.f : exp2f((mw - top) * c);
+    sum += stats[w][1][lane & 31] * by[w];
+  }
+#pragma unroll
+  for (int x = wave; x < DH / 8; x += WAVES) {  // which four rows
+    const int d = x * 8 + 4 * (lane >> 5);
+    f32x4 t = {};
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const f32x4 ow = reinterpret_cast<const f32x4*>(lds[w])[x * 64 + lane];
+      // a wave without keys has zeros, and so does its factor
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] += ow[e] * by[w];
+    }
+    if (!live || d >= a.dim) continue;
+    if (splits > 1) {
+      *reinterpret_cast<f32x4*>(part_of(a, split) + (tok * a.q_heads + h0 + row.g) * a.dim + d) = t;
+      continue;
+    }
+    typedef T V __attribute__((ext_vector_type(4)));
+    const bool none = tiles.total == 0 && a.own == kOwnNone;
+    const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = none ? 0.f : t[e] * inv;
+    *reinterpret_cast<V*>(row_ptr<T>(a.out, s.begin, h0, row) + d) = __builtin_convertvector(t, V);
+  }
+  if (!live || threadIdx.x >= 32) return;
+  if (splits > 1) *reinterpret_cast<f32x2*>(part_stats(a, splits, split, tok, h0 + row.g)) = f32x2{top * c, sum};
+  else if (a.lse) a.lse[(int64_t)(h0 + row.g) * a.n_tok + tok] = top * c * kLn2 + logf(sum);
+}
+
+// One wave a (token, query head): the splits' sums at their common maximum.  A lane has one split's maximum and
+// sum (of 64 at a time), then two columns of all.
+template <typename T>
+__global__ void __launch_bounds__(64) shared_join(SharedArgs a, int splits) {
+  const int64_t total = a.n_tok * a.q_heads, row = blockIdx.x;
+  const float* st = a.part + (int64_t)splits * total * a.dim;
+  const int lane = lane_id(), d = 2 * lane;
+  float top = -kInf, sum = 0.f;
+  f32x2 o = {};
+  for (int x0 = 0; x0 < splits; x0 += 64) {
+    f32x2 mine = {-kInf, 0.f};
+    if (x0 + lane < splits) mine = *reinterpret_cast<const f32x2*>(st + ((x0 + lane) * total + row) * 2);
+    float m = mine[0];
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k, 64));
+    const float t = fmaxf(top, m);
+    const float keep = top == -kInf ? 0.f : exp2f(top - t);
+    const float by = mine[0] == -kInf ? 0.f : mine[0] == t ? 1.f : exp2f(mine[0] - t);
+    top = t;
+    sum = sum * keep + lanes_sum<64>(by * mine[1]);
+    o[0] *= keep;
+    o[1] *= keep;
+    const int n = min(splits - x0, 64);
+    for (int x = 0; x < n; ++x) {
+      const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(by), x));
+      f32x2 v = {};
+      if (d < a.dim) v = *reinterpret_cast<const f32x2*>(a.part + ((x0 + x) * total + row) * a.dim + d);
+      o[0] += f * v[0];
+      o[1] += f * v[1];
+    }
+  }
+  const int64_t tok = row / a.q_heads, qh = row % a.q_heads;
+  if (lane == 0 && a.lse) a.lse[qh * a.n_tok + tok] = top * kLn2 + logf(sum);
+  if (d >= a.dim) return;
+  const bool none = sum == 0.f;
+  T* out = static_cast<T*>(a.out.p) + tok * a.out.tok + qh * a.out.head + d;
+  out[0] = (T)(none ? 0.f : o[0] / sum);
+  out[1] = (T)(none ? 0.f : o[1] / sum);
+}
+
+// ---------------------------------------------------------------- launches
+template <typename F>
+void by_type(const SharedArgs& a, F f) {
+  if (a.dtype == EMB_F16) f(_Float16{});
+  else f(__bf16{});
+}
+template <typename F>
+void by_width(const SharedArgs& a, F f) {
+  // the widths that kernels are built for; a head of another is padded with zeros in LDS
+  if (a.dim <= 32) f(std::integral_constant<int, 32>{});
+  else if (a.dim <= 64) f(std::integral_constant<int, 64>{});
+  else f(std::integral_constant<int, 128>{});
+}
+
+// Whether tiles may be loaded straight to LDS: whole rows of the kernel's width, and a tile's rows
+// within 2^31 bytes of one another.
+bool direct(const SharedArgs& a, int width) {
+  for (const EmbHeads* h : {&a.k, &a.v, &a.hk, &a.hv})
+    if (h->tok < 0 || h->tok > ((int64_t)1 << 23)) return false;
+  return a.dim == width;
+}
+
+int64_t slots(const SharedArgs& a, int rows) {
+  if (!a.off) return (int64_t)a.n_seq * ((a.group + rows - 1) / rows);
+  return a.n_tok * a.group / rows + a.n_seq;
+}
+
+}  // namespace
+
+SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, bool one) {
+  SharedPlan p{32, 4, 1, 0};
+  const int64_t group = a.q_heads / a.kv_heads, keys = std::min<int64_t>(hist, (int64_t)a.window + a.sinks);
+  n_seq = std::max<int64_t>(n_seq, 1);
+  if (!one && n_tok * group > 48 * n_seq) p.rows = 128;
+  const int64_t tiles = one ? n_seq * ((group + 31) / 32) : std::max(n_tok * group / p.rows, n_seq);
+  const int64_t base = std::max<int64_t>(tiles * a.kv_heads, 1);
+  if (p.rows == 128) {
+    if (base < 512) p.splits = (int32_t)std::max<int64_t>(1, std::min((keys + 255) / 256, 512 / base));
+  } else if (base < 512 && keys > 128) {
+    const int most = a.dim <= 64 ? 16 : 8;
+    if (base <= 256 && (base > 128 || keys <= 64 * most)) p.waves = most;
+    else p.splits = (int32_t)std::min<int64_t>((keys + 127) / 128, 1024 / base);
+  }
+  p.bytes = p.splits > 1 ? (size_t)p.splits * n_tok * a.q_heads * (a.dim + 2) * sizeof(float) : 0;
+  return p;
+}
+
+// Threads of a call's largest launch.
+int64_t shared_threads(const SharedArgs& a, const SharedPlan& p) {
+  const int64_t groups = slots(a, p.rows) * a.kv_heads * p.splits;
+  return std::max(groups * (p.rows == 128 ? 256 : 64 * p.waves), a.n_tok * a.q_heads * 64);
+}
+
+hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipStream_t st) {
+  hipError_t e = hipSuccess;
+  const dim3 grid((unsigned)(slots(a, p.rows) * a.kv_heads * p.splits));
+  by_type(a, [&](auto t) {
+    typedef decltype(t) T;
+    by_width(a, [&](auto d) {
+      constexpr int DH = decltype(d)::value, kMost = DH <= 64 ? 16 : 8;
+      if (p.rows == 128) {
+        if (q8) hipLaunchKernelGGL((shared_wide<T, DH, kCodes>), grid, dim3(256), 0, st, a, p.splits);
+        else if (direct(a, DH)) hipLaunchKernelGGL((shared_wide<T, DH, kDirect>), grid, dim3(256), 0, st, a, p.splits);
+        else hipLaunchKernelGGL((shared_wide<T, DH, kByRegisters>), grid, dim3(256), 0, st, a, p.splits);
+      } else if (p.waves == kMost) {
+        const dim3 threads(64 * kMost);
+        if (q8) hipLaunchKernelGGL((shared_narrow<T, DH, kMost, true>), grid, threads, 0, st, a, p.splits);
+        else hipLaunchKernelGGL((shared_narrow<T, DH, kMost, false>), grid, threads, 0, st, a, p.splits);
+      } else {
+        if (q8) hipLaunchKernelGGL((shared_narrow<T, DH, 4, true>), grid, dim3(256), 0, st, a, p.splits);
+        else hipLaunchKernelGGL((shared_narrow<T, DH, 4, false>), grid, dim3(256), 0, st, a, p.splits);
+      }
+    });
+    e = hipGetLastError();
+    if (p.splits > 1 && e == hipSuccess) {
+      hipLaunchKernelGGL((shared_join<T>), dim3((unsigned)(a.n_tok * a.q_heads)), dim3(64), 0, st, a, p.splits);
+      e = hipGetLastError();
+    }
+  });
+  return e;
+}
+
+}  // namespace emb

@@ -1,0 +1,213 @@
+// What the kernels of candidates' attention share: where a request's history is, which tiles of keys its
+// query rows meet, rows of (token, head of the group), and history in 8 bits.
+#pragma once
+
+#include "dense_attn_device.h"
+
+namespace emb {
+
+// Query rows of one key/value head: row r of a request is its token r / group, head r % group of the heads that
+// share the keys, so that a few candidates fill a tile of rows and every key is read once for all of them.
+struct Row {
+  int tok, g;  // of the request; of the group
+};
+__device__ __forceinline__ Row row_at(const SharedArgs& a, int r) {
+  const int t = (uint32_t)r / (uint32_t)a.group;
+  return {t, r - t * a.group};
+}
+template <typename T>
+__device__ __forceinline__ T* row_ptr(const EmbHeads& t, int64_t begin, int h0, Row r) {
+  return static_cast<T*>(t.p) + (begin + r.tok) * t.tok + (h0 + r.g) * t.head;
+}
+
+// A value that every lane has, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ Seq uniform(Seq s) {
+  s.begin = uniform((int)s.begin);  // at most 2^30
+  s.len = uniform(s.len);
+  s.tile = uniform(s.tile);
+  s.index = uniform(s.index);
+  return s;
+}
+
+// The request that tile slot `slot` of TOKENS query rows belongs to, and which tile of it.
+template <int ROWS>
+__device__ __forceinline__ Seq find_rows(const SharedArgs& a, int slot) {
+  if (!a.off) {  // one token a request
+    const int tiles = (a.group + ROWS - 1) / ROWS;
+    Seq s;
+    s.index = slot / tiles;
+    s.begin = s.index;
+    s.len = 1;
+    s.tile = slot % tiles;
+    return uniform(s);
+  }
+  const int group = a.group;
+  return uniform(find_tile(a, slot, [group](int64_t t, int b) { return t * group / ROWS + b; }));
+}
+
+// The history of a request, and what of it is seen: the sinks outside the window, then the window.
+struct History {
+  int64_t row;             // packed: the first event's row
+  int n, sinks, first;     // events; of them seen before the window; where the window begins
+};
+__device__ __forceinline__ History history(const SharedArgs& a, int b) {
+  History h;
+  h.row = 0;
+  if (a.packed) {
+    h.row = uniform((int)min(max((int64_t)a.hist[b], (int64_t)0), a.n_hist));  // at most 2^30
+    h.n = uniform((int)(min(max((int64_t)a.hist[b + 1], h.row), a.n_hist) - h.row));
+  } else {
+    h.n = uniform((int)min(max((int64_t)a.hist[b], (int64_t)0), a.n_hist));
+  }
+  h.first = max(h.n - a.back, 0);
+  h.sinks = min(a.sinks, h.first);
+  return h;
+}
+template <typename T>
+__device__ __forceinline__ const T* history_of(const SharedArgs& a, const EmbHeads& t, const History& h, int b, int kh) {
+  return static_cast<const T*>(t.p) + (a.packed ? h.row * t.tok : b * t.seq) + kh * t.head;
+}
+
+// Tiles of ROWS keys of a history that are seen: one of the sinks, then those of the window.
+template <int ROWS>
+struct HistoryTiles {
+  int sinks, sink_end, first, n, total;
+  __device__ __forceinline__ HistoryTiles(const History& h) {
+    sinks = h.sinks > 0;
+    sink_end = h.sinks;
+    first = h.first;
+    n = h.n;
+    total = sinks + (n - first + ROWS - 1) / ROWS;
+  }
+  __device__ __forceinline__ int key0(int it) const { return it < sinks ? 0 : first + (it - sinks) * ROWS; }
+  __device__ __forceinline__ int end(int it) const { return it < sinks ? sink_end : n; }
+};
+
+// The first token of a token's candidate; what no valid array holds leaves the token itself at least.
+__device__ __forceinline__ int first_of(const SharedArgs& a, const Seq& s, int tok) {
+  const int64_t f = (int64_t)a.first[s.begin + tok] - s.begin;
+  return (int)min(max(f, (int64_t)0), (int64_t)tok);
+}
+
+// Sets x[r] to `hidden` where key j0 + row_of(r) is not one of lo to hi; a bit for each register whose key is.
+template <int AGAIN = 0>
+__device__ __forceinline__ uint32_t hide_outside(int lo, int hi, int j0, f32x16& x, float hidden) {
+  const int d = j0 + 4 * (lane_id<AGAIN>() >> 5);
+  uint32_t see = 0;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int j = d + 8 * (r >> 2) + (r & 3);
+    if (j >= lo && j <= hi) see |= 1u << r;
+    else x[r] = hidden;
+  }
+  return see;
+}
+// The same of the keys from `end` on, of which few tiles have any; see hide_keys.
+__device__ __forceinline__ void hide_from(int end, int j0, f32x16& x, float hidden) {
+  asm volatile("");
+  const int n = end - j0 - 4 * (lane_id() >> 5);
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    if (8 * (r >> 2) + (r & 3) >= n) x[r] = hidden;
+}
+
+// ---------------------------------------------------------------- 8 bits
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Eight e4m3 codes times 2^(exp - 127), as T.
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::t of_codes(u32x2 c, uint32_t exp);
+template <>
+__device__ __forceinline__ f16x8 of_codes<_Float16>(u32x2 c, uint32_t exp) {
+  const float by = __uint_as_float(exp << 23);  // the instruction reads the exponent's bits alone
+  const f16x2 x[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[0], by, false),
+                      __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[0], by, true),
+                      __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[1], by, false),
+                      __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[1], by, true)};
+  return f16x8{x[0][0], x[0][1], x[1][0], x[1][1], x[2][0], x[2][1], x[3][0], x[3][1]};
+}
+template <>
+__device__ __forceinline__ bf16x8 of_codes<__bf16>(u32x2 c, uint32_t exp) {
+  const float by = __uint_as_float(exp << 23);
+  const bf16x2 x[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], by, false),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], by, true),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], by, false),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], by, true)};
+  return bf16x8{x[0][0], x[0][1], x[1][0], x[1][1], x[2][0], x[2][1], x[3][0], x[3][1]};
+}
+
+// ---------------------------------------------------------------- rows of a wave
+// As WaveRows, of rows of (token, head of the group).
+template <typename T, int DH, typename TILE, int AGAIN = 0>
+struct PackedRows : WaveRows<T, DH, TILE, AGAIN> {
+  typedef WaveRows<T, DH, TILE, AGAIN> W;
+  // rows r0 to r0 + 31 of a request; zeros past the last row and past D columns
+  __device__ __forceinline__ void load(const SharedArgs& a, const EmbHeads& t, int64_t begin, int h0, int r0, int rows) {
+#pragma unroll
+    for (int n = 0; n < W::kRegs; ++n) {
+      const int idx = lane_id<AGAIN>() + n * 64, row = r0 + idx / W::kPieces, col = idx % W::kPieces * 8;
+      W::r[n] = u32x4{0, 0, 0, 0};
+      if (row < rows && col < a.dim)
+        W::r[n] = *reinterpret_cast<const u32x4*>(row_ptr<const T>(t, begin, h0, row_at(a, row)) + col);
+    }
+  }
+  // Rows of results that hold them as columns (one per 32 of their elements).
+  __device__ static __forceinline__ void store(const SharedArgs& a, const EmbHeads& t, int64_t begin, int h0, int r0,
+                                               int rows, char* part, int first, const f32x16 (&x)[DH / 32], float by) {
+    typedef T V __attribute__((ext_vector_type(4)));
+    const int own = lane_id<AGAIN>() & 31, half = lane_id<AGAIN>() >> 5;
+    W::wave_sync();
+#pragma unroll
+    for (int db = 0; db < DH / 32; ++db) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 v = {x[db][4 * g] * by, x[db][4 * g + 1] * by, x[db][4 * g + 2] * by, x[db][4 * g + 3] * by};
+        *reinterpret_cast<V*>(part + TILE::at(first + own, db * 4 + g) + half * 8) = __builtin_convertvector(v, V);
+      }
+    }
+    W::wave_sync();
+#pragma unroll
+    for (int n = 0; n < W::kRegs; ++n) {
+      const int idx = lane_id<AGAIN>() + n * 64, row = r0 + idx / W::kPieces, col = idx % W::kPieces * 8;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(part + TILE::at(first + idx / W::kPieces, idx % W::kPieces));
+      if (row < rows && col < a.dim)
+        *reinterpret_cast<u32x4*>(row_ptr<T>(t, begin, h0, row_at(a, row)) + col) = v;
+    }
+  }
+};
+
+// A token's own key or value in the layout of a result's column: four elements at a time.
+template <typename T, int DH, int AGAIN = 0>
+__device__ __forceinline__ void column(const T* p, bool live, int D, f32x16 (&x)[DH / 32]) {
+  typedef T V __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int db = 0; db < DH / 32; ++db) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int col = db * 32 + 8 * g + 4 * (lane_id<AGAIN>() >> 5);
+      f32x4 v = {};
+      if (live && col < D) v = __builtin_convertvector(*reinterpret_cast<const V*>(p + col), f32x4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[db][4 * g + e] = v[e];
+    }
+  }
+}
+// The product of a lane's row, as right operands, with a row at p; in both halves' lanes.
+template <typename T, int DH, int AGAIN = 0>
+__device__ __forceinline__ float dot_row(const typename Vec8<T>::t (&f)[DH / 16], const T* p, bool live, int D) {
+  float s = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < DH / 16; ++ks) {
+    const int col = ks * 16 + (lane_id<AGAIN>() >> 5) * 8;
+    typename Vec8<T>::t x = {};
+    if (live && col < D) x = *reinterpret_cast<const typename Vec8<T>::t*>(p + col);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf((float)f[ks][e], (float)x[e], s);
+  }
+  return swap32_sum(s);
+}
+
+}  // namespace emb

@@ -1,5 +1,6 @@
 """Python binding of the library's dense side (include/emb_dense.h): attention over event sequences
-with a sliding window and sinks, the gated residual norms around a block, and AdamW.  Argument
+with a sliding window and sinks, attention of candidates that share a history, caches in 8 bits, the gated residual
+norms around a block, and AdamW.  Argument
 marshalling only; the work runs in the library's HIP kernels on the caller's stream.
 
 The functions keep the C names and argument order.  Device arguments are torch CUDA tensors on the
@@ -48,6 +49,16 @@ _SIG = {
                         _VP],
     "attn_window_decode_workspace_bytes": [_A, _I64, _I64, _SZ],
     "attn_window_decode": [_A, _H, _H, _H, _VP, _I64, _I64, _H, _VP, C.c_size_t, _VP],
+    "attn_window_decode_q8_workspace_bytes": [_A, _I64, _I64, _SZ],
+    "attn_window_decode_q8": [_A, _H, _H, _H, _H, _H, _VP, _I64, _I64, _H, _VP, C.c_size_t, _VP],
+    "attn_shared_fwd_workspace_bytes": [_A, _I64, _I64, _I64, _SZ],
+    "attn_shared_fwd": [_A, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, _VP, C.c_size_t, _VP],
+    "attn_shared_cache_workspace_bytes": [_A, _I64, _I64, _I64, _SZ],
+    "attn_shared_cache": [_A, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, C.c_size_t, _VP],
+    "attn_shared_cache_q8": [_A, _H, _H, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, C.c_size_t,
+                             _VP],
+    "cache_q8_write": [_I32, _I32, _I32, _H, _H, _VP, _VP, _I64, _I64, _H, _H, _H, _H, _I64, _VP],
+    "cache_q8_read": [_I32, _I32, _I32, _H, _H, _H, _H, _I64, _VP, _VP, _I64, _I64, _H, _H, _VP],
     "norm_gate_residual_fwd": [_VP, _VP, _VP, _I32, _VP, _VP, _I64, _I32, _I32, _F, _F, _VP, _VP,
                                _VP],
     "norm_gate_residual_bwd_workspace_bytes": [_I64, _I32, _SZ],
@@ -221,6 +232,159 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
     _check(lib().attn_window_decode(
         a, _heads(dev, q, "q", t, qs), _heads(dev, k_cache, "k_cache", t, cache),
         _heads(dev, v_cache, "v_cache", t, cache), _ptr(dev, lens, "lens", torch.int32, (qs[0],)), qs[0], cap,
+        _heads(dev, out, "out", t, qs), wp, wb, _stream(dev, stream)))
+
+
+# ------------------------------------------------------------------ caches in 8 bits
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _q8(dev: int, codes, exp, name: str, shape):
+    """EmbHeads of codes [sequences, capacity, heads, dim] and of their exponents [sequences, heads, capacity],
+    both of any strides but the codes' last, which is 1."""
+    if codes.dtype not in _CODES:
+        raise TypeError(f"{name}_cache: expected uint8 or float8_e4m3fn, got {codes.dtype}")
+    c = _heads(dev, codes, f"{name}_cache", codes.dtype, shape)
+    if exp.dtype is not torch.uint8 or exp.get_device() != dev:
+        raise TypeError(f"{name}_exp: expected a CUDA tensor of uint8 on the current device, got {exp.dtype} on {exp.device}")
+    if exp.shape != (shape[0], shape[2], shape[1]):
+        raise ValueError(f"{name}_exp: expected shape {(shape[0], shape[2], shape[1])}, got {tuple(exp.shape)}")
+    seq, head, tok = exp.stride()
+    return c, _pack_heads(exp.data_ptr(), seq, tok, head)
+
+
+def _cache(k, v, offsets, start, k_cache):
+    if k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("expected k [tokens, heads, dim], k_cache [sequences, capacity, heads, dim]")
+    if k.dtype not in _DTYPE:
+        raise TypeError(f"k: expected float32, float16 or bfloat16, got {k.dtype}")
+    dev, t, kv, cache = _device() if k.is_cuda else _NONE, k.dtype, k.shape, k_cache.shape
+    if cache[2:] != kv[1:]:
+        raise ValueError(f"k_cache: expected heads and dim {tuple(kv[1:])}, got {tuple(cache[2:])}")
+    off = None
+    if offsets is not None:
+        off, n_seq = _offsets(dev, offsets)
+        if n_seq != cache[0]:
+            raise ValueError(f"offsets: expected {cache[0] + 1} elements, got {n_seq + 1}")
+    return (dev, cache, (kv[1], kv[2], _DTYPE[t]), (_heads(dev, k, "k", t, kv), _heads(dev, v, "v", t, kv)),
+            (off, _ptr(dev, start, "start", torch.int32, cache[:1], optional=True), cache[0], kv[0]))
+
+
+def cache_q8_write(k, v, offsets, start, k_cache, k_exp, v_cache, v_exp, stream=None):
+    """Writes keys and values of new events, k, v [tokens, kv_heads, dim], in 8 bits: sequence s's, tokens offsets[s]
+    to offsets[s + 1] - 1 (None: token s), to places start[s] (None: 0) and on of k_cache, v_cache [n_seq, capacity,
+    kv_heads, dim] (uint8 or float8_e4m3fn) and k_exp, v_exp uint8 [n_seq, kv_heads, capacity]."""
+    dev, cache, what, kv, where = _cache(k, v, offsets, start, k_cache)
+    _check(lib().cache_q8_write(*what, *kv, *where, *_q8(dev, k_cache, k_exp, "k", cache),
+                                *_q8(dev, v_cache, v_exp, "v", cache), cache[1], _stream(dev, stream)))
+
+
+def cache_q8_read(k_cache, k_exp, v_cache, v_exp, offsets, start, k, v, stream=None):
+    """The way back: places start[s] and on, as many as offsets says, to k, v [tokens, kv_heads, dim]."""
+    dev, cache, what, kv, where = _cache(k, v, offsets, start, k_cache)
+    _check(lib().cache_q8_read(*what, *_q8(dev, k_cache, k_exp, "k", cache), *_q8(dev, v_cache, v_exp, "v", cache),
+                               cache[1], *where, *kv, _stream(dev, stream)))
+
+
+def attn_window_decode_q8_workspace_bytes(n_seq: int, capacity: int, q_heads: int, kv_heads: int, dim: int,
+                                          window: int, sinks: int) -> int:
+    a, n = _attn(torch.float16, (n_seq, q_heads, dim), kv_heads, window, sinks, 1.0), C.c_size_t()
+    _check(lib().attn_window_decode_q8_workspace_bytes(a, n_seq, capacity, C.byref(n)))
+    return n.value
+
+
+def attn_window_decode_q8(q, k_cache, k_exp, v_cache, v_exp, lens, window: int, sinks: int, scale: float, out, ws,
+                          stream=None):
+    """attn_window_decode against caches in 8 bits, as cache_q8_write leaves them."""
+    t, qs = q.dtype, q.shape
+    if len(qs) != 3 or k_cache.dim() != 4:
+        raise ValueError("expected q [sequences, heads, dim], k_cache [sequences, capacity, heads, dim]")
+    _, cap, kv_heads, _ = k_cache.shape
+    a = _attn(t, qs, kv_heads, window, sinks, scale)
+    cache, dev = (qs[0], cap, kv_heads, qs[2]), _device() if q.is_cuda else _NONE
+    wp, wb = _ws(dev, ws)
+    _check(lib().attn_window_decode_q8(
+        a, _heads(dev, q, "q", t, qs), *_q8(dev, k_cache, k_exp, "k", cache), *_q8(dev, v_cache, v_exp, "v", cache),
+        _ptr(dev, lens, "lens", torch.int32, (qs[0],)), qs[0], cap, _heads(dev, out, "out", t, qs), wp, wb,
+        _stream(dev, stream)))
+
+
+# ------------------------------------------------------------------ attention of candidates
+def _shared_bytes(fn, n_tok: int, n_seq: int, hist: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    a, n = _attn(torch.float16, (n_tok, q_heads, dim), kv_heads, 2**31 - 1, 0, 1.0), C.c_size_t()
+    _check(fn(a, n_seq, n_tok, hist, C.byref(n)))
+    return n.value
+
+
+def attn_shared_fwd_workspace_bytes(n_tok: int, n_seq: int, n_hist: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    return _shared_bytes(lib().attn_shared_fwd_workspace_bytes, n_tok, n_seq, n_hist, q_heads, kv_heads, dim)
+
+
+def attn_shared_cache_workspace_bytes(n_tok: int, n_seq: int, capacity: int, q_heads: int, kv_heads: int,
+                                      dim: int) -> int:
+    return _shared_bytes(lib().attn_shared_cache_workspace_bytes, n_tok, n_seq, capacity, q_heads, kv_heads, dim)
+
+
+def _packed(q, k, v, hist_k, hist_v, offsets, first, hist_offsets, window, sinks, scale):
+    """What the training calls begin with: the descriptor, the inputs and the sizes."""
+    t, (qs, kv) = q.dtype, _shapes(q, k)
+    if hist_k.dim() != 3:
+        raise ValueError("hist_k: expected [events, heads, dim]")
+    a = _attn(t, qs, kv[1], window, sinks, scale)
+    dev, n_hist = _device() if q.is_cuda else _NONE, hist_k.shape[0]
+    (off, n_seq), (hist, n) = _offsets(dev, offsets), _offsets(dev, hist_offsets)
+    if n != n_seq:
+        raise ValueError(f"hist_offsets: expected {n_seq + 1} elements, got {n + 1}")
+    h = (n_hist, kv[1], kv[2])
+    return dev, t, qs, kv, h, (
+        a, _heads(dev, q, "q", t, qs), _heads(dev, k, "k", t, kv), _heads(dev, v, "v", t, kv),
+        _heads(dev, hist_k, "hist_k", t, h), _heads(dev, hist_v, "hist_v", t, h), off,
+        _ptr(dev, first, "first", torch.int32, qs[:1], optional=True), hist, n_seq, qs[0], n_hist)
+
+
+def attn_shared_fwd(q, k, v, hist_k, hist_v, offsets, first, hist_offsets, window: int, sinks: int, scale: float, out,
+                    lse=None, ws=None, stream=None):
+    """out [tokens, q_heads, dim] and lse [q_heads, tokens] (fp32, optional) of candidates' tokens q [tokens, q_heads,
+    dim], k, v [tokens, kv_heads, dim]: request s has tokens offsets[s] to offsets[s + 1] - 1 and the history
+    hist_k, hist_v [events, kv_heads, dim] from hist_offsets[s] to hist_offsets[s + 1] - 1.  first [tokens]: the first
+    token of each token's candidate, None where every token is a candidate."""
+    dev, t, qs, _, _, args = _packed(q, k, v, hist_k, hist_v, offsets, first, hist_offsets, window, sinks, scale)
+    wp, wb = _ws(dev, ws)
+    _check(lib().attn_shared_fwd(
+        *args, _heads(dev, out, "out", t, qs), _ptr(dev, lse, "lse", torch.float32, (qs[1], qs[0]), optional=True),
+        wp, wb, _stream(dev, stream)))
+
+
+def _against_cache(q, k, v, k_cache, offsets, first, lens, window, sinks, scale):
+    t, (qs, kv) = q.dtype, _shapes(q, k)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected [requests, capacity, heads, dim]")
+    a = _attn(t, qs, kv[1], window, sinks, scale)
+    dev, cap = _device() if q.is_cuda else _NONE, k_cache.shape[1]
+    off, n_seq = _offsets(dev, offsets)
+    return dev, t, qs, (n_seq, cap, kv[1], kv[2]), (
+        a, _heads(dev, q, "q", t, qs), _heads(dev, k, "k", t, kv), _heads(dev, v, "v", t, kv)), (
+        off, _ptr(dev, first, "first", torch.int32, qs[:1], optional=True),
+        _ptr(dev, lens, "lens", torch.int32, (n_seq,)), n_seq, qs[0], cap)
+
+
+def attn_shared_cache(q, k, v, k_cache, v_cache, offsets, first, lens, window: int, sinks: int, scale: float, out,
+                      ws=None, stream=None):
+    """attn_shared_fwd's out against caches [requests, capacity, kv_heads, dim] that hold lens [requests] events."""
+    dev, t, qs, cache, own, rest = _against_cache(q, k, v, k_cache, offsets, first, lens, window, sinks, scale)
+    wp, wb = _ws(dev, ws)
+    _check(lib().attn_shared_cache(
+        *own, _heads(dev, k_cache, "k_cache", t, cache), _heads(dev, v_cache, "v_cache", t, cache), *rest,
+        _heads(dev, out, "out", t, qs), wp, wb, _stream(dev, stream)))
+
+
+def attn_shared_cache_q8(q, k, v, k_cache, k_exp, v_cache, v_exp, offsets, first, lens, window: int, sinks: int,
+                         scale: float, out, ws=None, stream=None):
+    """attn_shared_cache against caches in 8 bits, as cache_q8_write leaves them."""
+    dev, t, qs, cache, own, rest = _against_cache(q, k, v, k_cache, offsets, first, lens, window, sinks, scale)
+    wp, wb = _ws(dev, ws)
+    _check(lib().attn_shared_cache_q8(
+        *own, *_q8(dev, k_cache, k_exp, "k", cache), *_q8(dev, v_cache, v_exp, "v", cache), *rest,
         _heads(dev, out, "out", t, qs), wp, wb, _stream(dev, stream)))
 
 

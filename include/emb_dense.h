@@ -3,6 +3,10 @@
  *   - attn_window_*: attention over ragged event sequences in which an event sees the last `window`
  *     events of its sequence, itself among them, and the sequence's first `sinks` events; forward,
  *     backward, and the serving form of one new event per sequence against a cache.
+ *   - attn_shared_*: attention of the many candidates of a request to its one history and their own tokens;
+ *     forward, backward, and the serving form against caches.
+ *   - cache_q8_*: caches of keys and values in 8 bits, written as events come in and read back;
+ *     attn_shared_cache_q8 and attn_window_decode_q8 read them as they are.
  *   - norm_gate_residual_*: the norm after a block, its gate, the scaled residual and the norm
  *     before the next block in one pass; forward and backward.
  *   - adamw_step, adamw_step_q8: an AdamW step over many weight tensors at once, with fp32 states
@@ -104,6 +108,89 @@ int attn_window_decode(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k_ca
                        const EmbHeads* v_cache, const int32_t* d_lens, int64_t n_seq,
                        int64_t capacity, const EmbHeads* out, void* d_ws, size_t ws_bytes,
                        emb_stream_t stream);
+
+/* ------------------------------------------------------------------ caches in 8 bits
+ *
+ * A cache holds the keys and values of n_seq sequences of up to `capacity` events as e4m3 codes (OCP, uint8) with
+ * one power of two for each event's head: codes at (s, t, h, d) as EmbHeads says, exponents, a byte each, at
+ * p + s * seq + t * tok + h * head of an EmbHeads of their own, in any order of dimensions (tok = 1 is read fastest).
+ * The value of a code is code * 2^(exponent - 127).  The power of two brings the row's largest finite value into
+ * [128, 256); a value becomes the nearest code, halfway the even one, but no code past the largest number of the
+ * type that it came in.  What is not finite is held as NaN; a row of zeros has exponent 0.  An exponent of 255,
+ * which no write makes, stands for NaN.
+ * Codes are 8-byte aligned, their strides multiples of 8.  dim: a multiple of 8, 8 to 128.  kv_heads: 1 to 4096.
+ */
+
+/*
+ * Writes keys and values of new events: sequence s's are tokens d_offsets[s] to d_offsets[s + 1] - 1 of n_tok (or
+ * token s alone, without offsets: n_tok == n_seq), and go to places d_start[s] (0 without it) and on.  Places
+ * outside [0, capacity) are left out.  dtype: EMB_F32, EMB_F16 or EMB_BF16, of k and v.  Nothing else of the
+ * cache is touched.  Errors: EMB_EINVAL for a bad argument, alignment or stride, or places that overlap.
+ */
+int cache_q8_write(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k, const EmbHeads* v,
+                   const int32_t* d_offsets, const int32_t* d_start, int64_t n_seq, int64_t n_tok,
+                   const EmbHeads* k_cache, const EmbHeads* k_exp, const EmbHeads* v_cache,
+                   const EmbHeads* v_exp, int64_t capacity, emb_stream_t stream);
+
+/*
+ * The way back: the values of places d_start[s] and on to tokens of k and v in dtype (exact but in EMB_F16 past
+ * its range: infinities, and below its smallest numbers).  A place outside the cache gives zeros.
+ */
+int cache_q8_read(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k_cache, const EmbHeads* k_exp,
+                  const EmbHeads* v_cache, const EmbHeads* v_exp, int64_t capacity, const int32_t* d_offsets,
+                  const int32_t* d_start, int64_t n_seq, int64_t n_tok, const EmbHeads* k, const EmbHeads* v,
+                  emb_stream_t stream);
+
+/* attn_window_decode against a cache in 8 bits, whose values it reads as a->dtype. */
+int attn_window_decode_q8_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t capacity, size_t* bytes);
+int attn_window_decode_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k_cache, const EmbHeads* k_exp,
+                          const EmbHeads* v_cache, const EmbHeads* v_exp, const int32_t* d_lens, int64_t n_seq,
+                          int64_t capacity, const EmbHeads* out, void* d_ws, size_t ws_bytes, emb_stream_t stream);
+
+/* ------------------------------------------------------------------ attention of candidates
+ *
+ * A request has a history of events and any number of candidates, each of one or more tokens.  Token i of a
+ * candidate sees the history and its candidate's tokens up to itself; no candidate sees another.  A candidate
+ * stands at the place after the history's n events: event j is seen when n - j < window or j < sinks, as the next
+ * event of that sequence would see it in attn_window_fwd.  window and sinks say nothing about a candidate's own
+ * tokens.  Otherwise as there: scores, softmax, heads that share keys, EmbAttn and its limits.
+ *
+ * Requests are ragged: request s holds tokens d_offsets[s] to d_offsets[s + 1] - 1 of q, k and v (int32, ascending
+ * from 0 to n_tok).  d_first (nullable: every token is a candidate of its own): int32 [n_tok], for each token the
+ * first token of its candidate; a candidate's tokens stand together.
+ */
+
+/*
+ * Training: histories are packed, request s's are events d_hist_offsets[s] to d_hist_offsets[s + 1] - 1 of hist_k
+ * and hist_v (int32, ascending from 0 to n_hist).
+ *   d_lse : nullable; fp32 [q_heads][n_tok], what the backward reads.
+ *   d_ws  : 16-byte aligned, at least attn_shared_fwd_workspace_bytes (EMB_ENOSPACE otherwise); null where that is 0.
+ * What is not finite reaches only the tokens that see it.  EMB_VALIDATE=1 checks offsets and first (it synchronises
+ * the stream); without it malformed ones give wrong results but no access outside the tokens and events.
+ * Errors: as attn_window_fwd's.
+ */
+int attn_shared_fwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t n_hist, size_t* bytes);
+int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
+                    const EmbHeads* hist_k, const EmbHeads* hist_v, const int32_t* d_offsets, const int32_t* d_first,
+                    const int32_t* d_hist_offsets, int64_t n_seq, int64_t n_tok, int64_t n_hist,
+                    const EmbHeads* out, float* d_lse, void* d_ws, size_t ws_bytes, emb_stream_t stream);
+
+/*
+ * Serving: the history of request s is the first d_lens[s] (int32, clamped to [0, capacity]) events of its cache.
+ * Cache places at and past the length are not read.  The workspace is enough for any window.
+ */
+int attn_shared_cache_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t capacity,
+                                      size_t* bytes);
+int attn_shared_cache(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
+                      const EmbHeads* k_cache, const EmbHeads* v_cache, const int32_t* d_offsets,
+                      const int32_t* d_first, const int32_t* d_lens, int64_t n_seq, int64_t n_tok,
+                      int64_t capacity, const EmbHeads* out, void* d_ws, size_t ws_bytes, emb_stream_t stream);
+/* The same against a cache in 8 bits (q, k and v have a->dtype), with the same workspace. */
+int attn_shared_cache_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
+                         const EmbHeads* k_cache, const EmbHeads* k_exp, const EmbHeads* v_cache,
+                         const EmbHeads* v_exp, const int32_t* d_offsets, const int32_t* d_first,
+                         const int32_t* d_lens, int64_t n_seq, int64_t n_tok, int64_t capacity, const EmbHeads* out,
+                         void* d_ws, size_t ws_bytes, emb_stream_t stream);
 
 /* ------------------------------------------------------------------ norms, gate, residual
  *

@@ -97,6 +97,102 @@ def attn_bwd(q, k, v, offsets, window, sinks, scale, out, lse, dout):
     return dq, dk, dv, fin(dq, bq), fin(dk, bk), fin(dv, bv)
 
 
+def shared_sees(n_hist: int, first, window: int, sinks: int, device="cpu"):
+    """Which of the history's events, then of its own tokens, each token of a request sees.  first: of each token, by
+    its place in the request."""
+    i = torch.arange(len(first), device=device)[:, None]
+    j = torch.arange(n_hist, device=device)
+    hist = ((n_hist - j < window) | (j < sinks)).expand(len(first), -1)
+    j = torch.arange(len(first), device=device)
+    return torch.cat([hist, (j <= i) & (j >= first[:, None])], 1)
+
+
+def _requests(q, k, v, hk, hv, offsets, first, hist_offsets, window, sinks):
+    """Of each request with tokens and each query head: tokens, history events, heads, what they see, and q, k, v."""
+    g = q.shape[1] // k.shape[1]
+    for a, z, ha, hz in zip(offsets.tolist()[:-1], offsets.tolist()[1:], hist_offsets.tolist()[:-1], hist_offsets.tolist()[1:]):
+        f = torch.arange(z - a, device=q.device) if first is None else first[a:z].long() - a
+        see = shared_sees(hz - ha, f, window, sinks, q.device)
+        for h in range(q.shape[1] if z > a else 0):
+            x = h // g
+            yield (slice(a, z), slice(ha, hz), h, x, see, q[a:z, h].double(),
+                   torch.cat([hk[ha:hz, x], k[a:z, x]]).double(), torch.cat([hv[ha:hz, x], v[a:z, x]]).double())
+
+
+def attn_shared_fwd(q, k, v, hk, hv, offsets, first, hist_offsets, window, sinks, scale):
+    """out, lse, and the bounds of a kernel's error at them, as attn_fwd's."""
+    dt = q.dtype
+    u, tiny = U.get(dt, 0.0), TINY.get(dt, 0.0)
+    out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
+    lse = torch.zeros((q.shape[1], q.shape[0]), dtype=torch.float64, device=q.device)
+    b_out, b_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    for t, _, h, _, see, qq, kk, vv in _requests(q, k, v, hk, hv, offsets, first, hist_offsets, window, sinks):
+        s, rel = _head(qq, kk, scale)
+        p, l = _softmax(s, see)
+        o = p @ vv
+        # parts of a request's keys have maxima of their own, as in attn_decode
+        rel += len(kk) * F32
+        out[t, h], lse[h, t] = o, l
+        b_out[t, h] = u * o.abs() + (u + 2 * rel) * (1 + u) * (p @ vv.abs()) + tiny * see.double() @ vv.abs() + tiny
+        b_lse[h, t] = 2 * rel + 4 * F32 * l.abs()
+    return out, lse, b_out, b_lse
+
+
+def attn_shared_bwd(q, k, v, hk, hv, offsets, first, hist_offsets, window, sinks, scale, out, lse, dout):
+    """dq, dk, dv and the history's dk and dv, then the bounds of a kernel's error at each, as attn_bwd's."""
+    dt = q.dtype
+    u, tiny = U.get(dt, 0.0), TINY.get(dt, 0.0)
+    got = [torch.zeros(x.shape, dtype=torch.float64, device=q.device) for x in (q, k, v, hk, hv)]
+    bound = [torch.zeros_like(x) for x in got]
+    for t, j, h, x, see, qq, kk, vv in _requests(q, k, v, hk, hv, offsets, first, hist_offsets, window, sinks):
+        n = j.stop - j.start
+        do, oo = dout[t, h].double(), out[t, h].double()
+        s, rel = _head(qq, kk, scale)
+        rel += 8 * F32 * lse[h, t].abs().max().item()
+        p = torch.exp(s - lse[h, t].double()[:, None]).masked_fill(~see, 0.0)
+        dp = do @ vv.T
+        delta = (do * oo).sum(1, keepdim=True)
+        ds = p * (dp - delta)
+        e = (q.shape[2] + 8) * F32 * (do.abs() @ vv.abs().T + (do * oo).abs().sum(1, keepdim=True))
+        eds = p * e + ((u + 2 * rel + len(kk) * F32) * ds.abs() + tiny) * see * (1 + u)
+        ep = ((u + 2 * rel + len(kk) * F32) * p + tiny) * see
+        got[0][t, h] = ds @ kk * scale
+        bound[0][t, h] = eds @ kk.abs() * abs(scale)
+        dk, dv, bk, bv = ds.T @ qq * scale, p.T @ do, eds.T @ qq.abs() * abs(scale), ep.T @ do.abs()
+        for to, own, hist, y in ((got, 1, 3, dk), (got, 2, 4, dv), (bound, 1, 3, bk), (bound, 2, 4, bv)):
+            to[hist][j, x] += y[:n]
+            to[own][t, x] += y[n:]
+    return got, [b * (1 + u) + u * x.abs() + tiny for x, b in zip(got, bound)]
+
+
+def power(exp):
+    """2^(exp - 127) in 64 bits."""
+    return (exp.long() - 127 + 1023 << 52).view(torch.float64)
+
+
+def quantise(x):
+    """e4m3 codes (uint8) and the exponent of each row of x [..., dim], by search: the nearest of all codes, halfway
+    the even one."""
+    dt, x = x.dtype, x.double()
+    fine = x.isfinite()
+    top = torch.where(fine, x.abs(), 0.0).amax(-1)
+    k = torch.where(top > 0, torch.frexp(top)[1] - 8, -127).clamp(min=-127)
+    y = x / power(k + 127)[..., None]
+    most = {torch.float16: 8}.get(dt, 120)
+    values = torch.arange(127, dtype=torch.uint8, device=x.device).view(torch.float8_e4m3fn).double()  # ascending
+    at = torch.searchsorted(values, y.abs().contiguous()).clamp(1, 126)  # the first not below
+    up, down = values[at] - y.abs(), y.abs() - values[at - 1]
+    code = torch.where((up < down) | ((up == down) & (at % 2 == 0)), at, at - 1)
+    code = torch.where((k == most)[..., None], code.clamp(max=int((values <= 240).sum()) - 1), code)
+    code = torch.where(torch.signbit(x), code + 128, code)
+    return torch.where(fine, code, 127).to(torch.uint8), (k + 127).to(torch.uint8)
+
+
+def values_of(codes, exp):
+    """What codes and their rows' exponents stand for; an exponent of 255 is NaN."""
+    return codes.view(torch.float8_e4m3fn).double() * torch.where(exp == 255, math.nan, power(exp))[..., None]
+
+
 def attn_decode(q, k, v, lens, window, sinks, scale):
     dt = q.dtype
     u, tiny = U[dt], TINY[dt]

@@ -1,0 +1,183 @@
+"""Attention of candidates that share a history against the 64-bit oracle: training and serving forms, histories
+in 16 and 8 bits, and the newest event against a cache in 8 bits, at lengths, head layouts, widths and strides where
+the kernels' tiles end; within bounds that count the 16-bit roundings of results, probabilities and their gradients."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from ad_recommendation_amd import dense  # noqa: E402
+from oracle import dense_oracle as O  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+U8 = torch.uint8
+BIG = 2 ** 31 - 1
+
+
+def offsets(lens):
+    return torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+
+
+def rand(*shape, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def within(got, want, bound, what):
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all(), what
+    worst = (err - bound).max().item() if err.numel() else -1.0
+    assert worst <= 0, f"{what}: {worst:.3g} over its bound, largest error {err.max().item():.3g}"
+
+
+def candidates(lens, tokens):
+    """first: candidates of 1 to 2 * tokens - 1 tokens, in turn; None for one token each."""
+    if tokens == 1:
+        return None
+    first, at = [], 0
+    for n in lens:
+        i, size = 0, 1
+        while i < n:
+            m = min(size, n - i)
+            first += [at + i] * m
+            i += m
+            size = size % (2 * tokens - 1) + 1
+        at += n
+    return torch.tensor(first, dtype=torch.int32, device="cuda")
+
+
+def workspace(n):
+    """Bytes that are NaN where they are not written, and some behind them that are to stay."""
+    return torch.full((n + 64,), 0xFF, dtype=U8, device="cuda")
+
+
+def inputs(c, h, hq, hk, d, dtype, seed=0):
+    n, m = sum(c), sum(h)
+    x = rand(n, hq + 2 * hk, d, dtype=dtype, seed=seed + n + d)
+    y = rand(m, 2 * hk, d, dtype=dtype, seed=seed + m + d + 1)
+    return x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], y[:, :hk], y[:, hk:]
+
+
+def fwd(q, k, v, hk, hv, off, first, hoff, window, sinks, scale, lse=True):
+    n, hq, d = q.shape
+    out = torch.full((n, hq, d), 7, dtype=q.dtype, device="cuda")
+    l = torch.full((hq, n), 7.0, device="cuda") if lse else None
+    nb = dense.attn_shared_fwd_workspace_bytes(n, off.numel() - 1, hk.shape[0], hq, k.shape[1], d)
+    ws = workspace(nb)
+    dense.attn_shared_fwd(q, k, v, hk, hv, off, first, hoff, window, sinks, scale, out, l, ws[:nb])
+    assert (ws[nb:] == 0xFF).all()
+    return (out, l) if lse else out
+
+
+def cached(x, h, cap):
+    """Packed histories in caches, with what must not be read behind them."""
+    y = torch.full((len(h), cap, *x.shape[1:]), float("nan"), dtype=x.dtype, device="cuda")
+    at = 0
+    for s, n in enumerate(h):
+        y[s, :n] = x[at:at + n]
+        at += n
+    return y
+
+
+def in_8_bits(x):
+    """Codes and exponents of a cache, and the values."""
+    c, e = O.quantise(x)
+    return c, e.transpose(1, 2).contiguous(), O.values_of(c, e).to(x.dtype)
+
+
+# candidates' tokens, histories, q heads, kv heads, dim, window, sinks, tokens of a candidate
+SHAPES = [
+    ([1], [0], 1, 1, 8, BIG, 0, 1),
+    ([1], [1], 1, 1, 16, BIG, 0, 1),
+    ([0, 3, 2, 0, 1], [4, 0, 1, 0, 33], 2, 1, 16, BIG, 0, 2),
+    ([5, 8], [31, 32], 4, 4, 32, BIG, 0, 1),
+    ([6, 1, 9], [33, 63, 64], 4, 2, 64, 20, 3, 1),
+    ([6, 1, 9], [65, 127, 300], 6, 2, 40, 1, 5, 3),
+    ([10], [1000], 8, 1, 128, BIG, 0, 1),
+    ([30], [1500], 8, 2, 64, 700, 4, 4),
+    ([16, 0, 17, 15], [500, 3, 129, 0], 2, 2, 24, 128, 0, 1),
+    ([127, 128, 129], [64, 0, 65], 2, 1, 64, BIG, 0, 1),
+    ([200, 3, 0, 257], [128, 500, 9, 31], 6, 2, 40, 100, 32, 5),
+    ([300], [777], 4, 1, 128, BIG, 0, 1),
+    ([70, 400], [1029, 450], 4, 4, 128, 300, 2, 70),
+    ([513], [2000], 1, 1, 80, 1999, 1, 1),
+    ([90, 33], [400, 600], 3, 1, 104, 256, 0, 2),
+    ([64] * 40, [70] * 40, 2, 2, 32, 65, 7, 1),
+    ([3] * 150, [5] * 150, 3, 3, 48, BIG, 0, 2),
+    ([40], [50], 40, 1, 32, BIG, 0, 1),
+    ([0, 0], [3, 0], 2, 2, 32, 4, 2, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("c,h,hq,hk,d,window,sinks,tokens", SHAPES)
+def test_forward_forms(c, h, hq, hk, d, window, sinks, tokens, dtype):
+    print(f"[shared] {c[:6]} {h[:6]} heads {hq}/{hk} dim {d} window {window} sinks {sinks} tokens {tokens} {dtype}",
+          flush=True)
+    q, k, v, kh, vh = inputs(c, h, hq, hk, d, dtype)
+    off, hoff, first, scale = offsets(c), offsets(h), candidates(c, tokens), 1.3 * d ** -0.5
+    out, lse = fwd(q, k, v, kh, vh, off, first, hoff, window, sinks, scale)
+    o, l, bo, bl = O.attn_shared_fwd(q, k, v, kh, vh, off, first, hoff, window, sinks, scale)
+    within(out, o, bo, "out")
+    within(lse, l, bl, "lse")
+    again = fwd(q, k, v, kh, vh, off, first, hoff, window, sinks, scale)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])  # the same bits again
+    assert torch.equal(out, fwd(q, k, v, kh, vh, off, first, hoff, window, sinks, scale, lse=False))
+    # against caches
+    cap, lens = max(h) + 3, torch.tensor(h, dtype=torch.int32, device="cuda")
+    kc, vc = cached(kh, h, cap), cached(vh, h, cap)
+    n = sum(c)
+    nb = dense.attn_shared_cache_workspace_bytes(n, len(c), cap, hq, hk, d)
+    ws, got = workspace(nb), torch.full((n, hq, d), 7, dtype=dtype, device="cuda")
+    dense.attn_shared_cache(q, k, v, kc, vc, off, first, lens, window, sinks, scale, got, ws[:nb])
+    assert (ws[nb:] == 0xFF).all()
+    within(got, o, bo, "out from caches")
+    # in 8 bits
+    kq, ke, kv_ = in_8_bits(kh.unsqueeze(0).float().to(dtype))
+    vq, ve, vv_ = in_8_bits(vh.unsqueeze(0).float().to(dtype))
+    o, _, bo, _ = O.attn_shared_fwd(q, k, v, kv_[0], vv_[0], off, first, hoff, window, sinks, scale)
+    codes = [torch.full((len(c), cap, hk, d), 0x7F, dtype=U8, device="cuda") for _ in range(2)]
+    exps = [torch.full((len(c), hk, cap), 0xFF, dtype=U8, device="cuda") for _ in range(2)]
+    at = 0
+    for s, m in enumerate(h):
+        for x, y, a, b in ((codes[0], exps[0], kq, ke), (codes[1], exps[1], vq, ve)):
+            x[s, :m], y[s, :, :m] = a[0, at:at + m], b[0, :, at:at + m]
+        at += m
+    ws, got = workspace(nb), torch.full((n, hq, d), 7, dtype=dtype, device="cuda")
+    dense.attn_shared_cache_q8(q, k, v, codes[0], exps[0], codes[1], exps[1], off, first, lens, window, sinks, scale,
+                               got, ws[:nb])
+    assert (ws[nb:] == 0xFF).all()
+    within(got, o, bo, "out from 8 bits")
+
+
+# sequences' lengths, q heads, kv heads, dim, window, sinks
+DECODE = [
+    ([0, 1, 2, 31, 32, 33], 2, 1, 8, BIG, 0),
+    ([5, 700, 64], 8, 2, 64, 100, 4),
+    ([4000], 4, 1, 128, BIG, 0),
+    ([1500, 0, 37], 3, 3, 40, 64, 32),
+    ([300] * 70, 8, 8, 32, 129, 1),
+    ([90, 2000], 66, 2, 80, 1000, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("lens,hq,hk,d,window,sinks", DECODE)
+def test_newest_event_in_8_bits(lens, hq, hk, d, window, sinks, dtype):
+    print(f"[decode q8] {lens[:6]} heads {hq}/{hk} dim {d} window {window} sinks {sinks} {dtype}", flush=True)
+    n, cap, scale = len(lens), max(lens) + 5, 1.3 * d ** -0.5
+    q = rand(n, hq, d, dtype=dtype, seed=1)
+    kq, ke, kv = in_8_bits(rand(n, cap, hk, d, dtype=dtype, seed=2))
+    vq, ve, vv = in_8_bits(rand(n, cap, hk, d, dtype=dtype, seed=3))
+    for s, m in enumerate(lens):  # not to be read
+        kq[s, m:], vq[s, m:], ke[s, :, m:], ve[s, :, m:] = 0x7F, 0x7F, 0xFF, 0xFF
+    l = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    nb = dense.attn_window_decode_q8_workspace_bytes(n, cap, hq, hk, d, window, sinks)
+    ws, out = workspace(nb), torch.full_like(q, 7)
+    dense.attn_window_decode_q8(q, kq, ke, vq, ve, l, window, sinks, scale, out, ws[:nb])
+    assert (ws[nb:] == 0xFF).all()
+    o, bo = O.attn_decode(q, kv, vv, l, window, sinks, scale)
+    within(out, o, bo, "out")
+    again = torch.full_like(q, 7)
+    dense.attn_window_decode_q8(q, kq, ke, vq, ve, l, window, sinks, scale, again, ws[:nb])
+    assert torch.equal(out, again)
