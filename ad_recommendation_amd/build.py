@@ -17,7 +17,7 @@ ARCH = "gfx950"
 # Packed fp32 instructions are kept out of all device code.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # Device sources and host sources of the library, without their endings.
-KERNELS = ["emb_kernels", "dense_attn", "dense_shared", "dense_cache", "dense_norm", "dense_adamw"]
+KERNELS = ["emb_kernels", "dense_attn", "dense_shared", "dense_shared_bwd", "dense_cache", "dense_norm", "dense_adamw"]
 HOSTS = ["emb_host", "dense_host"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 

@@ -613,6 +613,79 @@ int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   return done(launch_shared(x, p, false, st), "attn_shared_fwd");
 }
 
+int attn_shared_bwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t n_hist, size_t* bytes) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, n_tok));
+  DENSE_TRY(check_counts(n_seq, n_hist));
+  DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
+  *bytes = plan_shared_bwd(*a, n_tok).bytes;
+  return EMB_OK;
+}
+
+int attn_shared_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v, const EmbHeads* hist_k,
+                    const EmbHeads* hist_v, const int32_t* d_offsets, const int32_t* d_first,
+                    const int32_t* d_hist_offsets, int64_t n_seq, int64_t n_tok, int64_t n_hist, const EmbHeads* out,
+                    const float* d_lse, const EmbHeads* dout, const EmbHeads* dq, const EmbHeads* dk,
+                    const EmbHeads* dv, const EmbHeads* dhist_k, const EmbHeads* dhist_v, void* d_ws, size_t ws_bytes,
+                    emb_stream_t stream) {
+  DENSE_TRY(check_attn(a));
+  DENSE_TRY(check_counts(n_seq, n_tok));
+  DENSE_TRY(check_counts(n_seq, n_hist));
+  if (n_seq == 0 || (n_tok == 0 && n_hist == 0)) return EMB_OK;
+  const SharedCall c{a, q, k, v, d_offsets, d_first, n_seq, n_tok};
+  // without tokens the history's gradients are zeros, and what the tokens' arrays point at is not read
+  if (n_tok > 0) {
+    DENSE_TRY(check_packed(c, hist_k, hist_v, d_hist_offsets, n_hist));
+    DENSE_TRY(check_heads(out, "out"));
+    DENSE_TRY(check_heads(dout, "dout"));
+    DENSE_CHECK(d_lse && d_ws, EMB_EINVAL, "attention: null pointer: lse or workspace");
+    DENSE_CHECK(aligned(d_lse, 4) && aligned(d_ws, 16), EMB_EINVAL, "attention: misaligned lse or workspace");
+  } else {
+    DENSE_CHECK(q && k && v && out && dout && dq && dk && dv && d_offsets && d_hist_offsets, EMB_EINVAL,
+                "attention: null pointer");
+    DENSE_TRY(check_heads(hist_k, "hist_k"));
+    DENSE_TRY(check_heads(hist_v, "hist_v"));
+    DENSE_CHECK(aligned(d_offsets, 4) && aligned(d_hist_offsets, 4), EMB_EINVAL, "attention: misaligned offsets");
+  }
+  const struct {
+    const EmbHeads* t;
+    int64_t n;
+    int32_t heads;
+    const char* name;
+  } written[] = {{dq, n_tok, a->q_heads, "dq"},
+                 {dk, n_tok, a->kv_heads, "dk"},
+                 {dv, n_tok, a->kv_heads, "dv"},
+                 {dhist_k, n_hist, a->kv_heads, "dhist_k"},
+                 {dhist_v, n_hist, a->kv_heads, "dhist_v"}};
+  for (const auto& w : written) {
+    DENSE_CHECK(w.t, EMB_EINVAL, std::string("attention: null pointer: ") + w.name);
+    if (w.n == 0) continue;
+    DENSE_TRY(check_heads(w.t, w.name));
+    EmbHeads one = *w.t;
+    one.seq = 0;
+    DENSE_TRY(check_apart(&one, 1, w.n, w.heads, a->dim, w.name));
+  }
+  SharedArgs x = packed_args(c, hist_k, hist_v, d_hist_offsets, n_hist);
+  DENSE_TRY(check_launch(shared_bwd_threads(x)));
+  const SharedBwdPlan p = plan_shared_bwd(*a, n_tok);
+  DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
+  DENSE_TRY(validate_offsets(d_hist_offsets, n_seq, n_hist, false, st));
+  DENSE_TRY(validate_first(c, st));
+  x.out = *out;
+  x.lse = const_cast<float*>(d_lse);
+  x.dout = *dout;
+  x.dq = *dq;
+  x.dk = *dk;
+  x.dv = *dv;
+  x.dhk = *dhist_k;
+  x.dhv = *dhist_v;
+  x.delta = static_cast<float*>(d_ws);
+  x.self = reinterpret_cast<float*>(static_cast<char*>(d_ws) + p.off_self);
+  return done(launch_shared_bwd(x, st), "attn_shared_bwd");
+}
+
 int attn_shared_cache_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t capacity, size_t* bytes) {
   DENSE_TRY(check_attn(a));
   DENSE_TRY(check_counts(n_seq, n_tok));

@@ -1,0 +1,702 @@
+// Backward of the attention of candidates that share a history (see dense_shared.hip):
+//
+//   delta_i = out_i . dout_i;  p_ij = exp(s_ij - lse_i);  ds_ij = scale p_ij (dout_i . v_j - delta_i)
+//   dq_i = sum_j ds_ij k_j;  dk_j = sum_i ds_ij q_i;  dv_j = sum_i p_ij dout_i
+//
+// dq by query rows as the forward has them; dk and dv of a history by tiles of its keys, which meet every row
+// (token, head of the group) of the request, so sums stay in registers and nothing is added up in memory; those of
+// own tokens by tiles of them, or, where every token is a candidate, one element at a time from p and ds of the row
+// with itself.
+//
+// In fp16 a score's gradient past 65504 does not fit the second product: sums then go on at a power of two below
+// (fit), looked for in every tile by one more maximum.
+#include <algorithm>
+#include <initializer_list>
+
+#include "dense_shared_device.h"
+
+namespace emb {
+
+namespace {
+
+// Gradients of 32 x 32 scores into 16 bits' range; `some`: whether sums of the wave stand at a power of two by now.
+template <typename T, int N>
+__device__ __forceinline__ void fit_if(f32x16& x, f32x16 (&sums)[N], int& by, bool& some) {
+  if constexpr (std::is_same<T, _Float16>::value) {
+    float top = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
+    if (some || __any(top > 65504.f)) {
+      some = true;
+      fit<T>(x, sums, by);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- dq
+// What a lane's row has throughout: its operands, delta and lse; also writes delta.
+template <typename T, int DH>
+struct QueryRow {
+  typename Vec8<T>::t q[DH / 16], d[DH / 16];
+  float delta, lse;
+};
+template <typename T, int DH>
+__device__ __forceinline__ float row_delta(const typename Vec8<T>::t (&out)[DH / 16],
+                                           const typename Vec8<T>::t (&d)[DH / 16]) {
+  float s = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < DH / 16; ++ks)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += (float)out[ks][e] * (float)d[ks][e];
+  return swap32_sum(s);
+}
+
+// A tile of 32 keys at row at0 of LDS tiles: dq += ds k.  OWN: of keys j0 on the row sees lo to hi; pairs that do not
+// see each other are left out.  Otherwise the first n are there, and seen.
+template <typename T, int DH, bool OWN, typename R>
+__device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R& at, int at0, int n, int lo, int hi,
+                                        int j0, const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int& by,
+                                        bool& some) {
+  typedef typename Vec8<T>::t V8;
+  f32x16 sc = {}, dp = {};
+#pragma unroll
+  for (int ks = 0; ks < DH / 16; ++ks) {
+    sc = mma(left<T>(kt, at, at0, ks), w.q[ks], sc);
+    dp = mma(left<T>(vt, at, at0, ks), w.d[ks], dp);
+  }
+  f32x16 ds;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) ds[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -w.lse)) * (dp[r] - w.delta);
+  uint32_t see = 0;
+  if (OWN) see = hide_outside<3>(lo, hi, j0, ds, 0.f);
+  else if (n < 32) hide_from(n, 0, ds, 0.f);
+  fit_if<T>(ds, dq, by, some);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const V8 b = right_of<T>(ds, 8 * k);
+#pragma unroll
+    for (int db = 0; db < DH / 32; ++db) {
+      const V8 x = left_t<T>(kt, at, at0 + 16 * k, db);
+      if (OWN) {
+        dq[db] = mma(finite_of<T>(x), b, dq[db]);
+        add_odd<T>(dq[db], x, ones<T>(see, 8 * k), V8{});
+      } else {
+        dq[db] = mma(x, b, dq[db]);
+      }
+    }
+  }
+}
+
+// The row's own token alone, on the vector unit; p and ds go to a.self for that token's dk and dv.
+template <typename T, int DH>
+__device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh, int qh, bool live,
+                                        const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int by) {
+  const T* kp = static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head;
+  const T* vp = static_cast<const T*>(a.v.p) + tok * a.v.tok + kh * a.v.head;
+  const float s = dot_row<T, DH, 3>(w.q, kp, live, a.dim), dp = dot_row<T, DH, 3>(w.d, vp, live, a.dim);
+  if (!live) return;
+  const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -w.lse)), ds = p * (dp - w.delta), x = ldexpf(ds, -by);
+  const int64_t at = (int64_t)qh * a.n_tok + tok;
+  if (lane_id<3>() < 32) a.self[at] = p;
+  else a.self[(int64_t)a.q_heads * a.n_tok + at] = ds;
+  typedef T V __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int db = 0; db < DH / 32; ++db) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int col = db * 32 + 8 * g + 4 * (lane_id<3>() >> 5);
+      f32x4 k = {};
+      if (col < a.dim) k = __builtin_convertvector(*reinterpret_cast<const V*>(kp + col), f32x4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dq[db][4 * g + e] += x * k[e];
+    }
+  }
+}
+
+// 128 rows a workgroup, 32 a wave, tiles of 64 keys in LDS, as in the forward.
+template <typename T, int DH, bool DIRECT>
+__global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) shared_dq(SharedArgs a) {
+  typedef TileOf<T, DH, 64, 256, DIRECT> Tile;
+  constexpr int kRows = 64, kTile = 128;
+  constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
+  __shared__ __attribute__((aligned(256))) char lds[2][2][kBytes];
+  const int kh = blockIdx.x % a.kv_heads;
+  const Seq s = find_rows<kTile>(a, blockIdx.x / a.kv_heads);
+  const int rows = s.len * a.group;
+  if (s.tile < 0 || (int64_t)s.tile * kTile >= rows) return;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int r0 = s.tile * kTile, rw = r0 + wave * 32, h0 = kh * a.group, last = min(r0 + kTile, rows) - 1;
+
+  typedef PackedRows<T, DH, Tile> Rows;
+  Rows ql, dl, ol;
+  ql.load(a, a.q, s.begin, h0, rw, rows);
+  dl.load(a, a.dout, s.begin, h0, rw, rows);
+  ol.load(a, a.out, s.begin, h0, rw, rows);
+  const History hist = history(a, s.index);
+  const HistoryTiles<kRows> tiles(hist);
+  const T* hk = history_of<T>(a, a.hk, hist, s.index, kh);
+  const T* hv = history_of<T>(a, a.hv, hist, s.index, kh);
+  Tile kl, vl;
+  auto load = [&](int it, char (*to)[kBytes]) {
+    kl.load(to[0], hk, a.hk.tok, tiles.key0(it), tiles.end(it), a.dim);
+    vl.load(to[1], hv, a.hv.tok, tiles.key0(it), tiles.end(it), a.dim);
+  };
+  if (tiles.total > 0) load(0, lds[0]);
+  const typename Tile::Reads at;
+  char* const part = lds[1][wave >> 1];  // a wave's own part of the tiles that the first step does not use
+  const int part0 = 32 * (wave & 1);
+  QueryRow<T, DH> w;
+  ql.to_right(part, part0, at, w.q);
+  dl.to_right(part, part0, at, w.d);
+  {
+    typename Vec8<T>::t out[DH / 16];
+    ol.to_right(part, part0, at, out);
+    w.delta = row_delta<T, DH>(out, w.d);
+  }
+  const float c = a.scale * kLog2e;
+  {
+    const int r = rw + (lane_id() & 31);
+    const Row row = row_at(a, min(r, last));
+    const int64_t stat = (int64_t)(h0 + row.g) * a.n_tok + s.begin + row.tok;
+    if (r < rows && lane_id() < 32) a.delta[stat] = w.delta;
+    w.lse = r < rows ? a.lse[stat] * kLog2e : kInf;
+  }
+  f32x16 dq[DH / 32] = {};
+  int by = 0;  // in fp16 dq stands at 2^-by
+  bool some = false;
+  auto meet = [&](int it, char (*now)[kBytes], char (*next)[kBytes]) {
+    kl.store(now[0]);
+    vl.store(now[1]);
+    if (!DIRECT && it + 1 < tiles.total) load(it + 1, next);
+    Tile::arrived();
+    __syncthreads();  // this tile is there, and the other buffer is no longer read
+    if (DIRECT && it + 1 < tiles.total) load(it + 1, next);
+    if (rw >= rows) return;
+    const int n = tiles.end(it) - tiles.key0(it);
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+      if (32 * sub < n)
+        dq_meet<T, DH, false>(now[0], now[1], at, 32 * sub, n - 32 * sub, 0, 0, 0, w, c, dq, by, some);
+  };
+  // two tiles a turn, so that the buffers' places are constants
+  for (int it = 0; it < tiles.total; it += 2) {
+    meet(it, lds[0], lds[1]);
+    if (it + 1 < tiles.total) meet(it + 1, lds[1], lds[0]);
+  }
+
+  const int r = rw + (lane_id<3>() & 31);
+  const bool live = r < rows;
+  const Row row = row_at(a, live ? r : last);
+  if (a.own == kOwnSelf) {
+    dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
+  } else {
+    typedef RegisterTile<T, DH, kRows, 256, 3> OwnTile;
+    const typename OwnTile::Reads own_at;
+    const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
+    for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)); j0 < end; j0 += kRows) {
+      OwnTile x, y;
+      x.load(nullptr, static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head, a.k.tok, j0, end, a.dim);
+      y.load(nullptr, static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head, a.v.tok, j0, end, a.dim);
+      __syncthreads();  // the tile before is done with
+      x.store(lds[0][0]);
+      y.store(lds[0][1]);
+      __syncthreads();
+      if (rw >= rows) continue;
+      for (int sub = 0; sub < 2; ++sub)
+        if (j0 + 32 * sub < end)
+          dq_meet<T, DH, true>(lds[0][0], lds[0][1], own_at, 32 * sub, 0, lo, row.tok, j0 + 32 * sub, w, c, dq, by,
+                               some);
+    }
+  }
+  __syncthreads();  // the tiles are done with
+  if (rw >= rows) return;
+  if constexpr (std::is_same<T, _Float16>::value) {
+    if (some) unfit(dq, by);
+  }
+  PackedRows<T, DH, Tile, 3>::store(a, a.dq, s.begin, h0, rw, rows, lds[1][wave >> 1], part0, dq, a.scale);
+}
+
+// 32 rows a workgroup, where a request has few: its four waves take tiles of 32 keys in turn, and their sums meet
+// in LDS.
+template <typename T, int DH>
+__global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
+  typedef RegisterTile<T, DH, 32, 64> Tile;
+  constexpr int kWaves = 4, kRegs = Tile::kRegs, kPieces = Tile::kPieces;
+  __shared__ __attribute__((aligned(256))) char lds[kWaves][2][Tile::kBytes];
+  const int kh = blockIdx.x % a.kv_heads;
+  const Seq s = find_rows<32>(a, blockIdx.x / a.kv_heads);
+  const int rows = s.len * a.group;
+  if (s.tile < 0 || (int64_t)s.tile * 32 >= rows) return;
+  const int wave = uniform(threadIdx.x >> 6), lane = lane_id();
+  const int r0 = s.tile * 32, h0 = kh * a.group, last = min(r0 + 32, rows) - 1;
+  const History hist = history(a, s.index);
+  const HistoryTiles<32> tiles(hist);
+  const T* hk = history_of<T>(a, a.hk, hist, s.index, kh);
+  const T* hv = history_of<T>(a, a.hv, hist, s.index, kh);
+  u32x4 kr[kRegs], vr[kRegs];
+  auto load = [&](int it) {
+    const int j0 = tiles.key0(it), end = tiles.end(it);
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane + n * 64, j = j0 + idx / kPieces, cl = idx % kPieces * 8;
+      kr[n] = vr[n] = u32x4{0, 0, 0, 0};
+      if (j < end && cl < a.dim) {
+        kr[n] = *reinterpret_cast<const u32x4*>(hk + j * a.hk.tok + cl);
+        vr[n] = *reinterpret_cast<const u32x4*>(hv + j * a.hv.tok + cl);
+      }
+    }
+  };
+  const typename Tile::Reads at;
+  char* kt = lds[wave][0];
+  char* vt = lds[wave][1];
+  QueryRow<T, DH> w;
+  {
+    typedef PackedRows<T, DH, Tile> Rows;
+    Rows x, y;
+    typename Vec8<T>::t out[DH / 16];
+    x.load(a, a.dout, s.begin, h0, r0, rows);
+    y.load(a, a.out, s.begin, h0, r0, rows);
+    x.to_right(kt, 0, at, w.d);
+    y.to_right(kt, 0, at, out);
+    w.delta = row_delta<T, DH>(out, w.d);
+    x.load(a, a.q, s.begin, h0, r0, rows);
+    x.to_right(kt, 0, at, w.q);
+    Rows::W::wave_sync();
+  }
+  int it = wave;
+  if (it < tiles.total) load(it);
+  const float c = a.scale * kLog2e;
+  {
+    const int r = r0 + (lane & 31);
+    const Row row = row_at(a, min(r, last));
+    const int64_t stat = (int64_t)(h0 + row.g) * a.n_tok + s.begin + row.tok;
+    if (r < rows && threadIdx.x < 32) a.delta[stat] = w.delta;
+    w.lse = r < rows ? a.lse[stat] * kLog2e : kInf;
+  }
+  f32x16 dq[DH / 32] = {};
+  int by = 0;
+  bool some = false;
+  for (; it < tiles.total; it += kWaves) {
+#pragma unroll
+    for (int n = 0; n < kRegs; ++n) {
+      const int idx = lane + n * 64, to = Tile::at(idx / kPieces, idx % kPieces);
+      *reinterpret_cast<u32x4*>(kt + to) = kr[n];
+      *reinterpret_cast<u32x4*>(vt + to) = vr[n];
+    }
+    if (it + kWaves < tiles.total) load(it + kWaves);
+    WaveRows<T, DH, Tile>::wave_sync();
+    dq_meet<T, DH, false>(kt, vt, at, 0, tiles.end(it) - tiles.key0(it), 0, 0, 0, w, c, dq, by, some);
+    WaveRows<T, DH, Tile>::wave_sync();
+  }
+  const int r = r0 + (lane_id<3>() & 31);
+  const bool live = r < rows;
+  const Row row = row_at(a, live ? r : last);
+  if (a.own == kOwnSelf) {
+    if (wave == 0) dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
+  } else {
+    typedef WaveRows<T, DH, Tile, 3> OwnRows;
+    const typename RegisterTile<T, DH, 32, 64, 3>::Reads own_at;
+    const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
+    for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)) + 32 * wave; j0 < end; j0 += 32 * kWaves) {
+      OwnRows::wave_sync();
+      for (int x = 0; x < 2; ++x) {
+        OwnRows rows_;
+        rows_.load(x ? a.v : a.k, s.begin + j0, kh, end - j0, a.dim);
+#pragma unroll
+        for (int n = 0; n < kRegs; ++n) {
+          const int idx = lane_id<3>() + n * 64;
+          *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = rows_.r[n];
+        }
+      }
+      OwnRows::wave_sync();
+      dq_meet<T, DH, true>(kt, vt, own_at, 0, 0, lo, row.tok, j0, w, c, dq, by, some);
+    }
+  }
+  if constexpr (std::is_same<T, _Float16>::value) {
+    if (some) unfit(dq, by);
+  }
+  // the waves meet, as in the forward
+  static_assert(sizeof(lds[0]) >= sizeof(float) * 32 * DH, "a wave's sums take its tiles' place");
+  f32x4* mine = reinterpret_cast<f32x4*>(lds[wave]);
+  WaveRows<T, DH, Tile>::wave_sync();
+#pragma unroll
+  for (int x = 0; x < DH / 8; ++x) {
+    const f32x16 t = dq[x >> 2];
+    const int e = (x & 3) * 4;
+    mine[x * 64 + lane] = f32x4{t[e], t[e + 1], t[e + 2], t[e + 3]};
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = wave; x < DH / 8; x += kWaves) {  // which four rows
+    const int d = x * 8 + 4 * (lane >> 5);
+    f32x4 t = {};
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) {
+      const f32x4 o = reinterpret_cast<const f32x4*>(lds[v])[x * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] += o[e];
+    }
+    if (!live || d >= a.dim) continue;
+    typedef T V __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] *= a.scale;
+    *reinterpret_cast<V*>(row_ptr<T>(a.dq, s.begin, h0, row) + d) = __builtin_convertvector(t, V);
+  }
+}
+
+// dk and dv of tokens that are candidates of their own, from p and ds of their rows with themselves: a thread has
+// eight columns of a token's key/value head and goes over the heads of the group.
+template <typename T>
+__global__ void __launch_bounds__(256) shared_self(SharedArgs a) {
+  typedef typename Vec8<T>::t V8;
+  const int pieces = a.dim / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, unit = i / pieces;
+  const int col = (int)(i - unit * pieces) * 8;
+  const int64_t tok = unit / a.kv_heads;
+  const int kh = (int)(unit - tok * a.kv_heads);
+  if (tok >= a.n_tok) return;
+  f32x8 dk = {}, dv = {};
+  for (int g = 0; g < a.group; ++g) {
+    const int h = kh * a.group + g;
+    const int64_t at = (int64_t)h * a.n_tok + tok;
+    const float p = a.self[at], ds = a.self[(int64_t)a.q_heads * a.n_tok + at];
+    const f32x8 q = widen(*reinterpret_cast<const V8*>(static_cast<const T*>(a.q.p) + tok * a.q.tok + h * a.q.head + col));
+    const f32x8 d = widen(*reinterpret_cast<const V8*>(static_cast<const T*>(a.dout.p) + tok * a.dout.tok +
+                                                       h * a.dout.head + col));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dk[e] = fmaf(ds, q[e], dk[e]);
+      dv[e] = fmaf(p, d[e], dv[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dk[e] *= a.scale;
+  *reinterpret_cast<V8*>(static_cast<T*>(a.dk.p) + tok * a.dk.tok + kh * a.dk.head + col) = __builtin_convertvector(dk, V8);
+  *reinterpret_cast<V8*>(static_cast<T*>(a.dv.p) + tok * a.dv.tok + kh * a.dv.head + col) = __builtin_convertvector(dv, V8);
+}
+
+// ---------------------------------------------------------------- dk, dv
+// A workgroup has 128 keys, of a history or of a request's own tokens, for a key/value head and meets the request's
+// rows, 64 a step.  Heads of 64 and less: four waves of 32 keys, which hold them as right operands in registers.
+// Heads of 128: eight waves, two to each 32 keys with half of a step's rows, and keys and values in LDS.
+
+// 64 rows (token, head of the group) to LDS.
+template <typename T, int DH, int THREADS, bool DIRECT>
+struct RowsTile : TileOf<T, DH, 64, THREADS, DIRECT> {
+  typedef TileOf<T, DH, 64, THREADS, DIRECT> B;
+  __device__ __forceinline__ void load(char* lds, const SharedArgs& a, const EmbHeads& t, int64_t begin, int h0, int r0,
+                                       int rows) {
+    if constexpr (DIRECT) {
+      const int wave = uniform(threadIdx.x >> 6), lane = lane_id();
+      const int from = min(r0, rows - 1), t0 = uniform(row_at(a, from).tok);
+      const char* p = reinterpret_cast<const char*>(static_cast<const T*>(t.p) + (begin + t0) * t.tok + h0 * t.head);
+#pragma unroll
+      for (int n = 0; n < B::kLoads; ++n) {
+        const int first = (wave + n * (THREADS / 64)) * B::kAtOnce, row = first + lane / B::kPieces;
+        const int piece = (lane % B::kPieces) ^ B::exchange(row);
+        const Row x = row_at(a, min(r0 + row, rows - 1));
+        const uint32_t off = (uint32_t)((x.tok - t0) * ((int)t.tok * 2) + x.g * ((int)t.head * 2) + piece * 16);
+        B::load_piece(p, off, lds + first * B::kRow);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < B::kRegs; ++n) {
+        const int idx = threadIdx.x + n * THREADS, row = r0 + idx / B::kPieces, col = idx % B::kPieces * 8;
+        B::r[n] = u32x4{0, 0, 0, 0};
+        if (row < rows && col < a.dim)
+          B::r[n] = *reinterpret_cast<const u32x4*>(row_ptr<const T>(t, begin, h0, row_at(a, row)) + col);
+      }
+    }
+  }
+};
+
+template <typename T, int DH, bool DIRECT>
+struct DkvTiles {
+  static constexpr bool kWide = DH == 128;
+  static constexpr int kWaves = kWide ? 8 : 4, kThreads = 64 * kWaves, kShare = kWide ? 2 : 1;
+  typedef TileOf<T, DH, 64, kThreads, DIRECT> Tile;
+  static constexpr int kBytes = Tile::kBytes;
+  char q[2][kBytes], d[2][kBytes];
+  char k[kWide ? 2 : 0][kBytes], v[kWide ? 2 : 0][kBytes];
+  float lse[2][64], delta[2][64];
+  int first[2][64], tok[2][64];  // of a row: its candidate's first token, its own
+  __device__ __forceinline__ char* part(int wave) {
+    if (kWide) return wave & 2 ? v[0] : k[0];
+    return (wave & 2 ? d : q)[1];
+  }
+};
+
+// Adds the sums of the upper half of eight waves to those of the lower half, through LDS.
+template <int N>
+__device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave) {
+  __syncthreads();
+  if (wave >= 4) {
+#pragma unroll
+    for (int k = 0; k < N * 16; ++k) lds[((wave - 4) * N * 16 + k) * 64 + lane_id()] = x[k >> 4][k & 15];
+  }
+  __syncthreads();
+  if (wave < 4) {
+#pragma unroll
+    for (int k = 0; k < N * 16; ++k) x[k >> 4][k & 15] += lds[(wave * N * 16 + k) * 64 + lane_id()];
+  }
+}
+
+// OWN: keys are the request's tokens j0 to j1 - 1, met by the rows of their candidates.
+template <typename T, int DH, bool DIRECT, bool OWN>
+__device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>& sh, const Seq& s, const History& hist,
+                                    int kh, int j0, int j1) {
+  typedef typename Vec8<T>::t V8;
+  typedef DkvTiles<T, DH, DIRECT> P;
+  typedef typename P::Tile Tile;
+  constexpr int kRows = 64;
+  const int wave = uniform(threadIdx.x >> 6), h0 = kh * a.group;
+  const int jrow = 32 * (wave & 3), jw = j0 + jrow, j = jw + (lane_id() & 31);
+  const int rows = s.len * a.group, row0 = OWN ? j0 * a.group : 0;
+  const EmbHeads &kx = OWN ? a.k : a.hk, &vx = OWN ? a.v : a.hv;
+  const int64_t begin = OWN ? s.begin : hist.row;
+
+  const typename Tile::Reads at;
+  typedef WaveRows<T, DH, Tile> Rows;
+  V8 k[P::kWide ? 1 : DH / 16], v[P::kWide ? 1 : DH / 16];
+  if constexpr (P::kWide) {
+    const T* kp = static_cast<const T*>(kx.p) + begin * kx.tok + kh * kx.head;
+    const T* vp = static_cast<const T*>(vx.p) + begin * vx.tok + kh * vx.head;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      Tile kl, vl;
+      kl.load(sh.k[x], kp, kx.tok, j0 + kRows * x, j1, a.dim);
+      vl.load(sh.v[x], vp, vx.tok, j0 + kRows * x, j1, a.dim);
+      kl.store(sh.k[x]);
+      vl.store(sh.v[x]);
+    }
+  } else {
+    // through the buffers that the first step does not use
+    Rows kl, vl;
+    kl.load(kx, begin + jw, kh, j1 - jw, a.dim);
+    vl.load(vx, begin + jw, kh, j1 - jw, a.dim);
+    kl.to_right(sh.part(wave), 32 * (wave & 1), at, k);
+    vl.to_right(sh.part(wave), 32 * (wave & 1), at, v);
+  }
+  const float c = a.scale * kLog2e;
+  RowsTile<T, DH, P::kThreads, DIRECT> ql, dl;
+  float stat = 0.f;  // the first 64 threads: lse of a row; as many after them: its delta
+  int tok = 0, first = 0;
+  auto load = [&](int b, int r0) {
+    ql.load(sh.q[b], a, a.q, s.begin, h0, r0, rows);
+    dl.load(sh.d[b], a, a.dout, s.begin, h0, r0, rows);
+    if (threadIdx.x < 2 * kRows) {
+      const int r = r0 + (threadIdx.x & (kRows - 1));
+      const float* p = threadIdx.x < kRows ? a.lse : a.delta;
+      // a row that is not there gets probabilities of zero, and sees no token
+      stat = threadIdx.x < kRows ? kInf : 0.f;
+      tok = -1;
+      first = 0;
+      if (r < rows) {
+        const Row x = row_at(a, r);
+        stat = p[(int64_t)(h0 + x.g) * a.n_tok + s.begin + x.tok];
+        if (OWN) {
+          tok = x.tok;
+          first = first_of(a, s, x.tok);
+        }
+      }
+    }
+  };
+  f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
+  int by = 0;  // in fp16 dk stands at 2^-by
+  bool some = false;
+  if (row0 < rows) load(0, row0);
+  for (int r0 = row0, b = 0; r0 < rows; r0 += kRows, b ^= 1) {
+    ql.store(sh.q[b]);
+    dl.store(sh.d[b]);
+    if (threadIdx.x < kRows) {
+      sh.lse[b][threadIdx.x] = stat * kLog2e;
+      if (OWN) {
+        sh.first[b][threadIdx.x] = first;
+        sh.tok[b][threadIdx.x] = tok;
+      }
+    } else if (threadIdx.x < 2 * kRows) {
+      sh.delta[b][threadIdx.x - kRows] = stat;
+    }
+    if (!DIRECT && r0 + kRows < rows) load(b ^ 1, r0 + kRows);
+    Tile::arrived();
+    __syncthreads();  // this step's rows are there, and the other buffer is no longer read
+    // candidates from here on begin after the last key
+    if (OWN && sh.first[b][0] >= j1) break;
+    if (DIRECT && r0 + kRows < rows) load(b ^ 1, r0 + kRows);
+    if (jw >= j1) continue;
+#pragma unroll
+    for (int sub_ = 0; sub_ < 2 / P::kShare; ++sub_) {
+      const int sub = P::kShare == 2 ? wave >> 2 : sub_;
+      if (r0 + 32 * sub >= rows) continue;
+      f32x16 sc = {}, dp = {};
+      if constexpr (P::kWide) {
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks)
+          sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), left<T>(sh.k[jrow >> 6], at, jrow & 63, ks), sc);
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks)
+          dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), left<T>(sh.v[jrow >> 6], at, jrow & 63, ks), dp);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks) {
+          sc = mma(left<T>(sh.q[b], at, 32 * sub, ks), k[ks], sc);
+          dp = mma(left<T>(sh.d[b], at, 32 * sub, ks), v[ks], dp);
+        }
+      }
+      f32x16 p, ds;
+      uint32_t see = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int i = 32 * sub + 8 * g + 4 * (lane_id() >> 5);
+        const f32x4 lse = *reinterpret_cast<const f32x4*>(&sh.lse[b][i]);
+        const f32x4 delta = *reinterpret_cast<const f32x4*>(&sh.delta[b][i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -lse[e]));
+          ds[4 * g + e] = p[4 * g + e] * (dp[4 * g + e] - delta[e]);
+          if (OWN) {
+            if (j >= sh.first[b][i + e] && j <= sh.tok[b][i + e]) see |= 1u << (4 * g + e);
+            else p[4 * g + e] = ds[4 * g + e] = 0.f;
+          }
+        }
+      }
+      fit_if<T>(ds, dk, by, some);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const V8 pb = right_of<T>(p, 8 * x), dsb = right_of<T>(ds, 8 * x);
+#pragma unroll
+        for (int db = 0; db < DH / 32; ++db) {
+          const V8 dt = left_t<T>(sh.d[b], at, 32 * sub + 16 * x, db);
+          const V8 qt = left_t<T>(sh.q[b], at, 32 * sub + 16 * x, db);
+          if (OWN) {
+            const V8 one = ones<T>(see, 8 * x);
+            dv[db] = mma(finite_of<T>(dt), pb, dv[db]);
+            add_odd<T>(dv[db], dt, one, one);
+            dk[db] = mma(finite_of<T>(qt), dsb, dk[db]);
+            add_odd<T>(dk[db], qt, one, V8{});
+          } else {
+            dv[db] = mma(dt, pb, dv[db]);
+            dk[db] = mma(qt, dsb, dk[db]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (std::is_same<T, _Float16>::value) {
+    if (some) unfit(dk, by);
+  }
+  Tile::arrived();  // of a step that was left early
+  if (P::kWide) {
+    float* fold = reinterpret_cast<float*>(sh.q);
+    static_assert(!P::kWide || sizeof(sh.q) + sizeof(sh.d) >= sizeof(float) * 4 * 32 * DH, "room to fold");
+    fold_waves(dk, fold, wave);
+    fold_waves(dv, fold, wave);
+  } else {
+    __syncthreads();  // the tiles are done with
+  }
+  if (wave >= 4) return;
+  // what no row sees, of a history, gets zeros
+  if (!OWN && (rows == 0 || (j < hist.first && j >= hist.sinks))) {
+#pragma unroll
+    for (int db = 0; db < DH / 32; ++db) dk[db] = dv[db] = f32x16{};
+  }
+  const EmbHeads &dkx = OWN ? a.dk : a.dhk, &dvx = OWN ? a.dv : a.dhv;
+  Rows::store(dkx, begin + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dk, a.scale, 0);
+  Rows::store(dvx, begin + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dv, 1.f, 0);
+}
+
+struct HistoryBatch {  // of find_tile
+  const int32_t* off;
+  int64_t n_tok;
+  int32_t n_seq;
+};
+
+template <typename T, int DH, bool DIRECT>
+__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), 2) shared_dkv(SharedArgs a, int hist_blocks) {
+  __shared__ __attribute__((aligned(1024))) DkvTiles<T, DH, DIRECT> sh;
+  constexpr int kTokens = 128;
+  const bool own = (int)blockIdx.x >= hist_blocks;  // the same for the whole workgroup
+  const int block = own ? blockIdx.x - hist_blocks : blockIdx.x;
+  const int kh = block % a.kv_heads, slot = block / a.kv_heads;
+  const auto first = [](int64_t t, int b) { return t / kTokens + b; };
+  if (own) {
+    const Seq s = uniform(find_tile(a, slot, first));
+    if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
+    const int j0 = s.tile * kTokens;
+    dkv<T, DH, DIRECT, true>(a, sh, s, History{}, kh, j0, min(j0 + kTokens, s.len));
+  } else {
+    const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot, first));
+    if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
+    const History hist = history(a, h.index);
+    Seq s = uniform(sequence(a, h.index, 0));
+    const int j0 = h.tile * kTokens;
+    // a tile that no row sees has none
+    if (j0 >= hist.sinks && j0 + kTokens <= hist.first) s.len = 0;
+    dkv<T, DH, DIRECT, false>(a, sh, s, hist, kh, j0, min(j0 + kTokens, hist.n));
+  }
+}
+
+// ---------------------------------------------------------------- launches
+// Whether tiles may be loaded straight to LDS: whole rows of the kernel's width, and a tile's rows
+// within 2^31 bytes of one another.
+bool direct(const SharedArgs& a, int width, std::initializer_list<const EmbHeads*> heads) {
+  for (const EmbHeads* h : heads) {
+    if (h->tok < 0 || h->tok > ((int64_t)1 << 22) || h->head < 0 || h->head * (int64_t)a.group > ((int64_t)1 << 28))
+      return false;
+  }
+  return a.dim == width;
+}
+// Rows of a request, on average, from which 128 rows a workgroup are the better shape of dq.
+bool few_rows(const SharedArgs& a) { return a.n_tok * a.group <= 48 * (int64_t)a.n_seq; }
+int64_t dq_slots(const SharedArgs& a) { return a.n_tok * a.group / (few_rows(a) ? 32 : 128) + a.n_seq; }
+int64_t hist_slots(const SharedArgs& a) { return a.n_hist / 128 + a.n_seq; }
+int64_t own_slots(const SharedArgs& a) { return a.own == kOwnTiles ? a.n_tok / 128 + a.n_seq : 0; }
+int64_t self_threads(const SharedArgs& a) { return (a.n_tok * a.kv_heads * (a.dim / 8) + 255) / 256 * 256; }
+
+template <typename T, int DH, bool DIRECT>
+hipError_t go(const SharedArgs& a, hipStream_t st) {
+  if (a.n_tok > 0) {
+    const dim3 grid((unsigned)(dq_slots(a) * a.kv_heads));
+    if (few_rows(a)) hipLaunchKernelGGL((shared_dq_few<T, DH>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((shared_dq<T, DH, DIRECT>), grid, dim3(256), 0, st, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;  // what comes after it would read what it did not write
+  const int64_t hist = hist_slots(a) * a.kv_heads;
+  hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT>), dim3((unsigned)(hist + own_slots(a) * a.kv_heads)),
+                     dim3(DkvTiles<T, DH, DIRECT>::kThreads), 0, st, a, (int)hist);
+  e = hipGetLastError();
+  if (e != hipSuccess || a.own == kOwnTiles || a.n_tok == 0) return e;
+  hipLaunchKernelGGL((shared_self<T>), dim3((unsigned)(self_threads(a) / 256)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_tok) {
+  SharedBwdPlan p{};
+  p.off_self = ((size_t)n_tok * a.q_heads * sizeof(float) + 255) & ~(size_t)255;
+  p.bytes = p.off_self + 2 * (size_t)n_tok * a.q_heads * sizeof(float);
+  return p;
+}
+
+int64_t shared_bwd_threads(const SharedArgs& a) {
+  const int64_t dkv = (hist_slots(a) + own_slots(a)) * a.kv_heads * (a.dim <= 64 ? 256 : 512);
+  return std::max({dq_slots(a) * a.kv_heads * 256, dkv, self_threads(a)});
+}
+
+hipError_t launch_shared_bwd(const SharedArgs& a, hipStream_t st) {
+  auto by_width = [&](auto t) {
+    typedef decltype(t) T;
+    auto by_tiles = [&](auto d) {
+      constexpr int DH = decltype(d)::value;
+      return direct(a, DH, {&a.q, &a.k, &a.v, &a.dout, &a.hk, &a.hv}) ? go<T, DH, true>(a, st) : go<T, DH, false>(a, st);
+    };
+    return a.dim <= 32   ? by_tiles(std::integral_constant<int, 32>{})
+           : a.dim <= 64 ? by_tiles(std::integral_constant<int, 64>{})
+                         : by_tiles(std::integral_constant<int, 128>{});
+  };
+  return a.dtype == EMB_F16 ? by_width(_Float16{}) : by_width(__bf16{});
+}
+
+}  // namespace emb

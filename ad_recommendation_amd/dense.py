@@ -53,6 +53,9 @@ _SIG = {
     "attn_window_decode_q8": [_A, _H, _H, _H, _H, _H, _VP, _I64, _I64, _H, _VP, C.c_size_t, _VP],
     "attn_shared_fwd_workspace_bytes": [_A, _I64, _I64, _I64, _SZ],
     "attn_shared_fwd": [_A, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, _VP, C.c_size_t, _VP],
+    "attn_shared_bwd_workspace_bytes": [_A, _I64, _I64, _I64, _SZ],
+    "attn_shared_bwd": [_A, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, _H, _H, _H, _H, _H, _H, _VP,
+                        C.c_size_t, _VP],
     "attn_shared_cache_workspace_bytes": [_A, _I64, _I64, _I64, _SZ],
     "attn_shared_cache": [_A, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, C.c_size_t, _VP],
     "attn_shared_cache_q8": [_A, _H, _H, _H, _H, _H, _H, _H, _VP, _VP, _VP, _I64, _I64, _I64, _H, _VP, C.c_size_t,
@@ -320,6 +323,10 @@ def attn_shared_fwd_workspace_bytes(n_tok: int, n_seq: int, n_hist: int, q_heads
     return _shared_bytes(lib().attn_shared_fwd_workspace_bytes, n_tok, n_seq, n_hist, q_heads, kv_heads, dim)
 
 
+def attn_shared_bwd_workspace_bytes(n_tok: int, n_seq: int, n_hist: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    return _shared_bytes(lib().attn_shared_bwd_workspace_bytes, n_tok, n_seq, n_hist, q_heads, kv_heads, dim)
+
+
 def attn_shared_cache_workspace_bytes(n_tok: int, n_seq: int, capacity: int, q_heads: int, kv_heads: int,
                                       dim: int) -> int:
     return _shared_bytes(lib().attn_shared_cache_workspace_bytes, n_tok, n_seq, capacity, q_heads, kv_heads, dim)
@@ -352,6 +359,18 @@ def attn_shared_fwd(q, k, v, hist_k, hist_v, offsets, first, hist_offsets, windo
     wp, wb = _ws(dev, ws)
     _check(lib().attn_shared_fwd(
         *args, _heads(dev, out, "out", t, qs), _ptr(dev, lse, "lse", torch.float32, (qs[1], qs[0]), optional=True),
+        wp, wb, _stream(dev, stream)))
+
+
+def attn_shared_bwd(q, k, v, hist_k, hist_v, offsets, first, hist_offsets, window: int, sinks: int, scale: float, out,
+                    lse, dout, dq, dk, dv, dhist_k, dhist_v, ws, stream=None):
+    """Gradients of attn_shared_fwd from its inputs and results and the gradient of out."""
+    dev, t, qs, kv, h, args = _packed(q, k, v, hist_k, hist_v, offsets, first, hist_offsets, window, sinks, scale)
+    wp, wb = _ws(dev, ws)
+    _check(lib().attn_shared_bwd(
+        *args, _heads(dev, out, "out", t, qs), _ptr(dev, lse, "lse", torch.float32, (qs[1], qs[0])),
+        _heads(dev, dout, "dout", t, qs), _heads(dev, dq, "dq", t, qs), _heads(dev, dk, "dk", t, kv),
+        _heads(dev, dv, "dv", t, kv), _heads(dev, dhist_k, "dhist_k", t, h), _heads(dev, dhist_v, "dhist_v", t, h),
         wp, wb, _stream(dev, stream)))
 
 

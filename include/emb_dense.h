@@ -176,6 +176,20 @@ int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
                     const EmbHeads* out, float* d_lse, void* d_ws, size_t ws_bytes, emb_stream_t stream);
 
 /*
+ * The backward: gradients with respect to q, k, v and the history, from the forward's inputs, out and lse and the
+ * gradient of out.  The history's are summed over the request's tokens and the query heads that share a head; events
+ * that no token sees get zeros.  In EMB_F16 gradients of scores over 65504 do no harm.
+ * d_ws (16-byte aligned): at least attn_shared_bwd_workspace_bytes (EMB_ENOSPACE otherwise).
+ */
+int attn_shared_bwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t n_hist, size_t* bytes);
+int attn_shared_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, const EmbHeads* v,
+                    const EmbHeads* hist_k, const EmbHeads* hist_v, const int32_t* d_offsets, const int32_t* d_first,
+                    const int32_t* d_hist_offsets, int64_t n_seq, int64_t n_tok, int64_t n_hist,
+                    const EmbHeads* out, const float* d_lse, const EmbHeads* dout, const EmbHeads* dq,
+                    const EmbHeads* dk, const EmbHeads* dv, const EmbHeads* dhist_k, const EmbHeads* dhist_v,
+                    void* d_ws, size_t ws_bytes, emb_stream_t stream);
+
+/*
  * Serving: the history of request s is the first d_lens[s] (int32, clamped to [0, capacity]) events of its cache.
  * Cache places at and past the length are not read.  The workspace is enough for any window.
  */

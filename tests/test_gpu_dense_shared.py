@@ -150,6 +150,37 @@ def test_forward_forms(c, h, hq, hk, d, window, sinks, tokens, dtype):
     within(got, o, bo, "out from 8 bits")
 
 
+def bwd(q, k, v, hk, hv, off, first, hoff, window, sinks, scale, out, lse, dout):
+    n, hq, d = q.shape
+    got = [torch.full(x.shape, 7, dtype=x.dtype, device="cuda") for x in (q, k, v, hk, hv)]
+    nb = dense.attn_shared_bwd_workspace_bytes(n, off.numel() - 1, hk.shape[0], hq, k.shape[1], d)
+    ws = workspace(nb)
+    dense.attn_shared_bwd(q, k, v, hk, hv, off, first, hoff, window, sinks, scale, out, lse, dout, *got, ws[:nb])
+    assert (ws[nb:] == 0xFF).all()
+    return got
+
+
+NAMES = ("dq", "dk", "dv", "dhist_k", "dhist_v")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("c,h,hq,hk,d,window,sinks,tokens", SHAPES)
+def test_backward(c, h, hq, hk, d, window, sinks, tokens, dtype):
+    print(f"[shared bwd] {c[:6]} {h[:6]} heads {hq}/{hk} dim {d} window {window} sinks {sinks} tokens {tokens} {dtype}",
+          flush=True)
+    q, k, v, kh, vh = inputs(c, h, hq, hk, d, dtype)
+    off, hoff, first, scale = offsets(c), offsets(h), candidates(c, tokens), 1.3 * d ** -0.5
+    args = q, k, v, kh, vh, off, first, hoff, window, sinks, scale
+    out, lse = fwd(*args)
+    dout = rand(sum(c), hq, d, dtype=dtype, seed=9)
+    got = bwd(*args, out, lse, dout)
+    want, bound = O.attn_shared_bwd(*args, out, lse, dout)
+    for name, g, w, b in zip(NAMES, got, want, bound):
+        within(g, w, b, name)
+    for g, again in zip(got, bwd(*args, out, lse, dout)):
+        assert torch.equal(g, again)
+
+
 # sequences' lengths, q heads, kv heads, dim, window, sinks
 DECODE = [
     ([0, 1, 2, 31, 32, 33], 2, 1, 8, BIG, 0),
