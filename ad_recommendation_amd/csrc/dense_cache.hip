@@ -25,36 +25,39 @@ __device__ __forceinline__ float lanes_max(float x) {
   return x;
 }
 
-struct Place {
-  int64_t tok;   // packed
-  int64_t at;    // in the cache, or -1
-  int seq, head, which;
+// A lane's rows of a workgroup's tokens: heads of keys, heads of values, then the next token's; `step` rows on each
+// time, without a division.
+struct Walk {
+  int t, x;       // token of the workgroup's, row of the token
+  int dt, dx, per;
+  __device__ __forceinline__ Walk(int row, int step, int heads) {
+    per = 2 * heads;
+    t = (uint32_t)row / (uint32_t)per;
+    x = row - t * per;
+    dt = (uint32_t)step / (uint32_t)per;
+    dx = step - dt * per;
+  }
+  __device__ __forceinline__ void next() {
+    t += dt;
+    x += dx;
+    if (x >= per) {
+      x -= per;
+      ++t;
+    }
+  }
 };
-// Row `row` of a workgroup's tokens: heads of keys, heads of values, then the next token's.
-__device__ __forceinline__ Place place_of(const CacheArgs& a, const Seq& s, int64_t start, int tile, int row) {
-  const int per = 2 * a.heads, t = row / per, x = row - t * per;
-  Place p;
-  p.which = x >= a.heads;
-  p.head = x - p.which * a.heads;
-  p.seq = s.index;
-  const int64_t i = (int64_t)s.tile * tile + t;
-  p.tok = s.begin + i;
-  p.at = start + i;
-  if (p.at < 0 || p.at >= a.capacity) p.at = -1;
-  return p;
-}
 
 template <typename T> constexpr int kTopExp = std::is_same<T, _Float16>::value ? 8 : 120;
 
-// Tokens of a workgroup: the same for every width and type.
-constexpr int kTokens = 8;
+// Tokens of a workgroup: enough rows that finding its sequence costs little.
+constexpr int kTokens = 32;
 
-template <typename T, int LANES, bool WRITE>
+template <typename T, int LANES, bool WRITE, bool ONCE>
 __global__ void __launch_bounds__(256) cache_q8(CacheArgs a) {
   typedef typename Vec8<T>::t V8;
   Seq s;
   if (a.off) {
-    s = find_tile(a, blockIdx.x, [](int64_t t, int b) { return t / kTokens + b; });
+    s = uniform(find_tile(a, blockIdx.x, [](int64_t t, int b) { return t / kTokens + b; }));
     if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
   } else {
     s.index = blockIdx.x;
@@ -62,27 +65,35 @@ __global__ void __launch_bounds__(256) cache_q8(CacheArgs a) {
     s.len = 1;
     s.tile = 0;
   }
-  const int64_t start = a.start ? a.start[s.index] : 0;
-  const int rows = min(kTokens, s.len - s.tile * kTokens) * 2 * a.heads;
+  const int t0 = s.tile * kTokens, tokens = min(kTokens, s.len - t0);
+  const int64_t tok0 = s.begin + t0, at0 = (a.start ? uniform(a.start[s.index]) : 0) + (int64_t)t0;
   constexpr int kGroups = 256 / LANES;
-  const int group = threadIdx.x / LANES, col = threadIdx.x % LANES * 8;
+  const int col = threadIdx.x % LANES * 8;
   const bool inside = col < a.dim;
-  for (int row0 = group; row0 < rows; row0 += kGroups * kRowsAtOnce) {
+  Walk here(threadIdx.x / LANES, kGroups, a.heads);
+  auto in_cache = [&](const Walk& w) { return at0 + w.t >= 0 && at0 + w.t < a.capacity; };
+  auto value_at = [&](const Walk& w) {
+    const bool v = w.x >= a.heads;
+    const EmbHeads& h = a.x[v];
+    return static_cast<T*>(h.p) + (tok0 + w.t) * h.tok + (w.x - (v ? a.heads : 0)) * h.head + col;
+  };
+  auto cached = [&](const EmbHeads* c, const Walk& w) {
+    const bool v = w.x >= a.heads;
+    const EmbHeads& h = c[v];
+    return static_cast<uint8_t*>(h.p) + s.index * h.seq + (at0 + w.t) * h.tok + (w.x - (v ? a.heads : 0)) * h.head;
+  };
+  while (here.t < tokens) {
+    Walk w = here;
     if constexpr (WRITE) {
       V8 x[kRowsAtOnce];
 #pragma unroll
       for (int n = 0; n < kRowsAtOnce; ++n) {
-        const int row = row0 + n * kGroups;
         x[n] = V8{};
-        if (row < rows && inside) {
-          const Place p = place_of(a, s, start, kTokens, row);
-          const EmbHeads& h = a.x[p.which];
-          x[n] = *reinterpret_cast<const V8*>(static_cast<const T*>(h.p) + p.tok * h.tok + p.head * h.head + col);
-        }
+        if (w.t < tokens && inside) x[n] = load8<T, ONCE>(value_at(w), 8);
+        w.next();
       }
 #pragma unroll
       for (int n = 0; n < kRowsAtOnce; ++n) {
-        const int row = row0 + n * kGroups;
         f32x8 y = widen(x[n]);
         float top = 0.f;
 #pragma unroll
@@ -98,47 +109,43 @@ __global__ void __launch_bounds__(256) cache_q8(CacheArgs a) {
         }
         u32x2 c;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w], y[4 * w + 1], 0, false);
-          c[w] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w + 2], y[4 * w + 3], lo, true);
+        for (int i = 0; i < 2; ++i) {
+          const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+          c[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], lo, true);
         }
-        if (row >= rows) continue;
-        const Place p = place_of(a, s, start, kTokens, row);
-        if (p.at < 0) continue;
-        const EmbHeads &h = a.code[p.which], &g = a.exp[p.which];
-        if (inside)
-          *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(h.p) + p.seq * h.seq + p.at * h.tok + p.head * h.head +
-                                    col) = c;
-        if (col == 0) static_cast<uint8_t*>(g.p)[p.seq * g.seq + p.at * g.tok + p.head * g.head] = (uint8_t)(k + 127);
+        if (here.t < tokens && in_cache(here)) {
+          if (inside) {
+            u32x2* to = reinterpret_cast<u32x2*>(cached(a.code, here) + col);
+            if (ONCE) __builtin_nontemporal_store(c, to);
+            else *to = c;
+          }
+          if (col == 0) *cached(a.exp, here) = (uint8_t)(k + 127);
+        }
+        here.next();
       }
     } else {
       u32x2 c[kRowsAtOnce];
       uint32_t ex[kRowsAtOnce];
 #pragma unroll
       for (int n = 0; n < kRowsAtOnce; ++n) {
-        const int row = row0 + n * kGroups;
         c[n] = u32x2{0, 0};
         ex[n] = 0;
-        if (row >= rows || !inside) continue;
-        const Place p = place_of(a, s, start, kTokens, row);
-        if (p.at < 0) continue;
-        const EmbHeads &h = a.code[p.which], &g = a.exp[p.which];
-        c[n] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(h.p) + p.seq * h.seq + p.at * h.tok +
-                                               p.head * h.head + col);
-        ex[n] = static_cast<const uint8_t*>(g.p)[p.seq * g.seq + p.at * g.tok + p.head * g.head];
+        if (w.t < tokens && inside && in_cache(w)) {
+          const u32x2* from = reinterpret_cast<const u32x2*>(cached(a.code, w) + col);
+          c[n] = ONCE ? __builtin_nontemporal_load(from) : *from;
+          ex[n] = *cached(a.exp, w);
+        }
+        w.next();
       }
 #pragma unroll
       for (int n = 0; n < kRowsAtOnce; ++n) {
-        const int row = row0 + n * kGroups;
-        if (row >= rows || !inside) continue;
-        const Place p = place_of(a, s, start, kTokens, row);
         V8 y;
         if constexpr (std::is_same<T, float>::value) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const f32x2 u = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[n][w], false);
-            const f32x2 v = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[n][w], true);
-            y[4 * w] = u[0], y[4 * w + 1] = u[1], y[4 * w + 2] = v[0], y[4 * w + 3] = v[1];
+          for (int i = 0; i < 2; ++i) {
+            const f32x2 u = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[n][i], false);
+            const f32x2 v = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[n][i], true);
+            y[4 * i] = u[0], y[4 * i + 1] = u[1], y[4 * i + 2] = v[0], y[4 * i + 3] = v[1];
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -146,8 +153,12 @@ __global__ void __launch_bounds__(256) cache_q8(CacheArgs a) {
         } else {
           y = of_codes<T>(c[n], ex[n]);
         }
-        const EmbHeads& h = a.x[p.which];
-        *reinterpret_cast<V8*>(static_cast<T*>(h.p) + p.tok * h.tok + p.head * h.head + col) = y;
+        if (here.t < tokens && inside) {
+          V8* to = reinterpret_cast<V8*>(value_at(here));
+          if (ONCE) __builtin_nontemporal_store(y, to);
+          else *to = y;
+        }
+        here.next();
       }
     }
   }
@@ -164,8 +175,11 @@ hipError_t launch_cache(const CacheArgs& a, bool write, hipStream_t st) {
   auto go = [&](auto t, auto lanes) {
     typedef decltype(t) T;
     constexpr int LANES = decltype(lanes)::value;
-    if (write) hipLaunchKernelGGL((cache_q8<T, LANES, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((cache_q8<T, LANES, false>), grid, dim3(256), 0, st, a);
+    const bool once = 2 * a.n_tok * a.heads * a.dim * (int64_t)(sizeof(T) + 1) > kOnceBytes;
+    if (write && once) hipLaunchKernelGGL((cache_q8<T, LANES, true, true>), grid, dim3(256), 0, st, a);
+    else if (write) hipLaunchKernelGGL((cache_q8<T, LANES, true, false>), grid, dim3(256), 0, st, a);
+    else if (once) hipLaunchKernelGGL((cache_q8<T, LANES, false, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((cache_q8<T, LANES, false, false>), grid, dim3(256), 0, st, a);
   };
   auto by_lanes = [&](auto t) {
     if (a.dim <= 8) go(t, std::integral_constant<int, 1>{});

@@ -206,6 +206,16 @@ int validate_first(const SharedCall& c, hipStream_t st) {
   return EMB_OK;
 }
 
+// What is known of histories: their mean, and of caches how long they may be.  A packed one over four times the
+// mean is shared out as one of four times is.
+SharedPlan packed_plan(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t n_hist) {
+  const int64_t mean = (n_hist + std::max<int64_t>(n_seq, 1) - 1) / std::max<int64_t>(n_seq, 1);
+  return plan_shared(a, n_seq, n_tok, mean, std::min(4 * mean, n_hist), false);
+}
+SharedPlan cache_plan(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t capacity) {
+  return plan_shared(a, n_seq, n_tok, capacity / 2, capacity, false);
+}
+
 // The serving forms: histories are caches, in 16 bits or (k_exp) in 8.
 int shared_cache(const SharedCall& c, const EmbHeads* hk, const EmbHeads* ke, const EmbHeads* hv, const EmbHeads* ve,
                  const int32_t* d_lens, int64_t capacity, bool q8, const EmbHeads* out, void* d_ws, size_t ws_bytes,
@@ -240,7 +250,7 @@ int shared_cache(const SharedCall& c, const EmbHeads* hk, const EmbHeads* ke, co
   }
   x.hist = d_lens;
   x.n_hist = capacity;
-  const SharedPlan p = plan_shared(*c.a, c.n_seq, c.n_tok, capacity, false);
+  const SharedPlan p = cache_plan(*c.a, c.n_seq, c.n_tok, capacity);
   DENSE_TRY(check_launch(shared_threads(x, p)));
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
@@ -276,11 +286,6 @@ SharedArgs packed_args(const SharedCall& c, const EmbHeads* hk, const EmbHeads* 
   x.packed = 1;
   return x;
 }
-int64_t mean_of(int64_t n, int64_t count) {
-  count = std::max<int64_t>(count, 1);
-  return (n + count - 1) / count;
-}
-
 int cache_call(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k, const EmbHeads* v,
                const int32_t* d_offsets, const int32_t* d_start, int64_t n_seq, int64_t n_tok, const EmbHeads* kc,
                const EmbHeads* ke, const EmbHeads* vc, const EmbHeads* ve, int64_t capacity, bool write,
@@ -532,7 +537,7 @@ int attn_window_decode_q8_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64
   DENSE_TRY(check_attn(a));
   DENSE_TRY(check_counts(n_seq, capacity));
   DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
-  *bytes = plan_shared(*a, n_seq, n_seq, capacity, true).bytes;
+  *bytes = plan_shared(*a, n_seq, n_seq, capacity, capacity, true).bytes;
   return EMB_OK;
 }
 
@@ -563,7 +568,7 @@ int attn_window_decode_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k
   x.ve = *v_exp;
   x.hist = d_lens;
   x.n_hist = capacity;
-  const SharedPlan p = plan_shared(*a, n_seq, n_seq, capacity, true);
+  const SharedPlan p = plan_shared(*a, n_seq, n_seq, capacity, capacity, true);
   DENSE_TRY(check_launch(shared_threads(x, p)));
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
@@ -579,7 +584,7 @@ int attn_shared_fwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_t
   DENSE_TRY(check_counts(n_seq, n_tok));
   DENSE_TRY(check_counts(n_seq, n_hist));
   DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
-  *bytes = plan_shared(*a, n_seq, n_tok, mean_of(n_hist, n_seq), false).bytes;
+  *bytes = packed_plan(*a, n_seq, n_tok, n_hist).bytes;
   return EMB_OK;
 }
 
@@ -599,7 +604,7 @@ int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   DENSE_TRY(check_apart(&one, 1, n_tok, a->q_heads, a->dim, "out"));
   DENSE_CHECK(aligned(d_lse, 4), EMB_EINVAL, "attention: lse not 4-byte aligned");
   SharedArgs x = packed_args(c, hist_k, hist_v, d_hist_offsets, n_hist);
-  const SharedPlan p = plan_shared(*a, n_seq, n_tok, mean_of(n_hist, n_seq), false);
+  const SharedPlan p = packed_plan(*a, n_seq, n_tok, n_hist);
   DENSE_TRY(check_launch(shared_threads(x, p)));
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
@@ -691,7 +696,7 @@ int attn_shared_cache_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n
   DENSE_TRY(check_counts(n_seq, n_tok));
   DENSE_TRY(check_counts(n_seq, capacity));
   DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
-  *bytes = plan_shared(*a, n_seq, n_tok, capacity, false).bytes;
+  *bytes = cache_plan(*a, n_seq, n_tok, capacity).bytes;
   return EMB_OK;
 }
 

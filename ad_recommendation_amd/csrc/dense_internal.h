@@ -62,11 +62,12 @@ struct SharedArgs : AttnArgs {  // off: tokens of requests, null for one token e
 struct SharedPlan {
   int32_t rows;    // of a tile: 32, whose keys the waves share out, or 128, 32 a wave
   int32_t waves;   // of 32 rows: of a workgroup
-  int32_t splits;  // of a tile's keys
+  int32_t splits;  // workgroups that may share a request's keys, so that each has `unit` tiles of them
+  int32_t unit;
   size_t bytes;
 };
-// hist: events that a history may have, or has on average.  one: one token a request, without offsets.
-SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, bool one);
+// hist: events that a history has on average; most: that one may have.  one: one token a request, without offsets.
+SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, int64_t most, bool one);
 int64_t shared_threads(const SharedArgs& a, const SharedPlan& p);
 hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipStream_t st);
 

@@ -97,14 +97,6 @@ __device__ __forceinline__ void meet_own(const char* kt, const char* vt, const R
   }
 }
 
-// Where sums of split keys go: [split][token][q head][dim], then [..][2] of maximum (in powers of two) and sum.
-__device__ __forceinline__ float* part_of(const SharedArgs& a, int split) {
-  return a.part + (int64_t)split * a.n_tok * a.q_heads * a.dim;
-}
-__device__ __forceinline__ float* part_stats(const SharedArgs& a, int splits, int split, int64_t tok, int qh) {
-  return part_of(a, splits) + (((int64_t)split * a.n_tok + tok) * a.q_heads + qh) * 2;
-}
-
 // ---------------------------------------------------------------- 128 rows
 enum { kByRegisters, kDirect, kCodes };  // how tiles of history get to LDS
 
@@ -150,7 +142,7 @@ template <int DH, int HOW>
 constexpr int wide_waves = DH == 128 ? 2 : DH == 64 ? 3 : 4;
 
 template <typename T, int DH, int HOW>
-__global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(SharedArgs a, int splits) {
+__global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(SharedArgs a, int splits, int unit) {
   typedef typename Vec8<T>::t V8;
   typedef typename WideTile<T, DH, HOW>::t Tile;
   constexpr int kRows = 64, kTile = 128;
@@ -172,8 +164,9 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
   ql.load(a, a.q, s.begin, h0, rw, a.scale != 0.f ? rows : 0);
   const History hist = history(a, s.index);
   const HistoryTiles<kRows> tiles(hist);
-  const int per = (tiles.total + splits - 1) / splits;
-  const int it0 = min(split * per, tiles.total), it1 = min(it0 + per, tiles.total);
+  const Share share = share_of(tiles.total, splits, unit, split);
+  if (split >= share.count) return;
+  const int it0 = share.first, it1 = share.end;
 
   typedef std::conditional_t<HOW == kCodes, uint8_t, T> H;
   const H* hk = history_of<H>(a, a.hk, hist, s.index, kh);
@@ -241,7 +234,7 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
   const int r = rw + (lane_id<3>() & 31);
   const bool live = r < rows;
   const Row row = row_at(a, live ? r : last);
-  if (split == splits - 1) {
+  if (split == share.count - 1) {
     if (a.own == kOwnSelf) {
       meet_self<T, DH>(a, s.begin + row.tok, kh, live, q, c, o, m, l);
     } else {
@@ -265,7 +258,8 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
   }
   l = swap32_sum(l);
   const int64_t tok = s.begin + row.tok;
-  if (splits > 1) {
+  if (splits > 1 && split == 0 && live && lane_id() < 32) *part_count(a, splits, tok, h0 + row.g) = share.count;
+  if (share.count > 1) {
     if (!live) return;
     const EmbHeads to{part_of(a, split), 0, (int64_t)a.q_heads * a.dim, a.dim};
     store_row<float, DH>(to, tok, h0 + row.g, a.dim, o, 1.f);
@@ -280,8 +274,8 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
 
 // ---------------------------------------------------------------- 32 rows
 // The waves' tiles come through registers, the next one under way while one is computed.
-template <typename T, int DH, int WAVES, bool CODES>
-__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow(SharedArgs a, int splits) {
+template <typename T, int DH, int WAVES, bool CODES, bool TILES>
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow(SharedArgs a, int splits, int unit) {
   typedef typename Vec8<T>::t V8;
   typedef RegisterTile<T, DH, 32, 64> Tile;
   constexpr int kRegs = Tile::kRegs, kPieces = Tile::kPieces;
@@ -305,8 +299,9 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
   right_row<T, DH>(a.q, tok, h0 + row.g, live && a.scale != 0.f, a.dim, q);
   const History hist = history(a, s.index);
   const HistoryTiles<32> tiles(hist);
-  const int per = (tiles.total + splits - 1) / splits;
-  const int it0 = min(split * per, tiles.total), it1 = min(it0 + per, tiles.total);
+  const Share share = share_of(tiles.total, splits, unit, split);
+  if (split >= share.count) return;
+  const int it0 = share.first, it1 = share.end;
 
   typedef std::conditional_t<CODES, uint8_t, T> H;
   typedef std::conditional_t<CODES, u32x2, u32x4> Piece;
@@ -374,10 +369,10 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
     }
     WaveRows<T, DH, Tile>::wave_sync();
   }
-  if (split == splits - 1) {
-    if (a.own == kOwnSelf) {
-      if (wave == 0) meet_self<T, DH>(a, tok, kh, live, q, c, o, m, l);
-    } else if (a.own == kOwnTiles) {
+  if (split == share.count - 1) {
+    if constexpr (!TILES) {
+      if (a.own == kOwnSelf && wave == 0) meet_self<T, DH>(a, tok, kh, live, q, c, o, m, l);
+    } else {
       typedef WaveRows<T, DH, Tile, 3> OwnRows;
       const typename RegisterTile<T, DH, 32, 64, 3>::Reads own_at;
       const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
@@ -437,7 +432,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
       for (int e = 0; e < 4; ++e) t[e] += ow[e] * by[w];
     }
     if (!live || d >= a.dim) continue;
-    if (splits > 1) {
+    if (share.count > 1) {
       *reinterpret_cast<f32x4*>(part_of(a, split) + (tok * a.q_heads + h0 + row.g) * a.dim + d) = t;
       continue;
     }
@@ -449,22 +444,81 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
     *reinterpret_cast<V*>(row_ptr<T>(a.out, s.begin, h0, row) + d) = __builtin_convertvector(t, V);
   }
   if (!live || threadIdx.x >= 32) return;
-  if (splits > 1) *reinterpret_cast<f32x2*>(part_stats(a, splits, split, tok, h0 + row.g)) = f32x2{top * c, sum};
+  if (splits > 1 && split == 0) *part_count(a, splits, tok, h0 + row.g) = share.count;
+  if (share.count > 1) *reinterpret_cast<f32x2*>(part_stats(a, splits, split, tok, h0 + row.g)) = f32x2{top * c, sum};
   else if (a.lse) a.lse[(int64_t)(h0 + row.g) * a.n_tok + tok] = top * c * kLn2 + logf(sum);
 }
 
-// One wave a (token, query head): the splits' sums at their common maximum.  A lane has one split's maximum and
-// sum (of 64 at a time), then two columns of all.
+// The sums of a row's parts at their common maximum.  Nothing is read after something else: what is read of parts
+// that are not there is left out.
+//
+// Few parts: a thread has four columns of a row, all its parts' loads under way at once.
+constexpr int kFewParts = 8;
 template <typename T>
-__global__ void __launch_bounds__(64) shared_join(SharedArgs a, int splits) {
-  const int64_t total = a.n_tok * a.q_heads, row = blockIdx.x;
-  const float* st = a.part + (int64_t)splits * total * a.dim;
-  const int lane = lane_id(), d = 2 * lane;
+__global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits) {
+  const int pieces = a.dim / 4;
+  const int64_t total = a.n_tok * a.q_heads, i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / pieces;
+  const int d = (int)(i - row * pieces) * 4;
+  if (row >= total) return;
+  const float* st = part_of(a, splits);
+  const int64_t tok = row / a.q_heads;
+  const int qh = (int)(row - tok * a.q_heads), count = *part_count(a, splits, tok, qh);
+  f32x2 stat[kFewParts];
+  f32x4 v[kFewParts];
+#pragma unroll
+  for (int x = 0; x < kFewParts; ++x) {
+    if (x >= splits) break;
+    stat[x] = *reinterpret_cast<const f32x2*>(st + (x * total + row) * 2);
+    v[x] = *reinterpret_cast<const f32x4*>(a.part + (x * total + row) * a.dim + d);
+  }
+  if (count <= 1) return;  // it has its result
+  float top = -kInf, sum = 0.f;
+#pragma unroll
+  for (int x = 0; x < kFewParts; ++x)
+    if (x < count) top = stat[x][0] > top || stat[x][0] != stat[x][0] ? stat[x][0] : top;  // NaN stays
+  f32x4 o = {};
+#pragma unroll
+  for (int x = 0; x < kFewParts; ++x) {
+    if (x >= count) break;
+    const float by = stat[x][0] == -kInf ? 0.f : stat[x][0] == top ? 1.f : exp2f(stat[x][0] - top);
+    sum += by * stat[x][1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += by * v[x][e];
+  }
+  if (d == 0 && a.lse) a.lse[qh * a.n_tok + tok] = top * kLn2 + logf(sum);
+  typedef T V __attribute__((ext_vector_type(4)));
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = sum == 0.f ? 0.f : o[e] * inv;
+  *reinterpret_cast<V*>(static_cast<T*>(a.out.p) + tok * a.out.tok + qh * a.out.head + d) = __builtin_convertvector(o, V);
+}
+
+// Many: a workgroup has a row, and its waves every fourth part.  A lane has one part's maximum and sum (of 64 at a
+// time), then two columns, eight parts' loads under way at once.  16 parts of 24 rows 3.5 us, a launch's latency and
+// one of memory; by one wave, its loads one after the other, 7.0.
+constexpr int kJoinAtOnce = 8;
+template <typename T>
+__global__ void __launch_bounds__(256) shared_join(SharedArgs a, int splits) {
+  __shared__ f32x2 sums[4][64];
+  const int64_t total = a.n_tok * a.q_heads, row = blockIdx.x, tok = row / a.q_heads;
+  const int wave = uniform(threadIdx.x >> 6), lane = lane_id(), d = 2 * lane, qh = (int)(row - tok * a.q_heads);
+  const float* st = part_of(a, splits);
+  const int count = *part_count(a, splits, tok, qh);
   float top = -kInf, sum = 0.f;
   f32x2 o = {};
   for (int x0 = 0; x0 < splits; x0 += 64) {
-    f32x2 mine = {-kInf, 0.f};
-    if (x0 + lane < splits) mine = *reinterpret_cast<const f32x2*>(st + ((x0 + lane) * total + row) * 2);
+    f32x2 mine = *reinterpret_cast<const f32x2*>(st + ((int64_t)min(x0 + lane, splits - 1) * total + row) * 2);
+    f32x2 v[kJoinAtOnce];
+    auto load = [&](int y) {
+#pragma unroll
+      for (int k = 0; k < kJoinAtOnce; ++k) {
+        const int x = min(x0 + y + 4 * k, splits - 1);
+        v[k] = f32x2{};
+        if (d < a.dim) v[k] = *reinterpret_cast<const f32x2*>(a.part + (x * total + row) * a.dim + d);
+      }
+    };
+    load(wave);
+    if (x0 + lane >= count) mine = f32x2{-kInf, 0.f};
     float m = mine[0];
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k, 64));
@@ -475,16 +529,25 @@ __global__ void __launch_bounds__(64) shared_join(SharedArgs a, int splits) {
     sum = sum * keep + lanes_sum<64>(by * mine[1]);
     o[0] *= keep;
     o[1] *= keep;
-    const int n = min(splits - x0, 64);
-    for (int x = 0; x < n; ++x) {
-      const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(by), x));
-      f32x2 v = {};
-      if (d < a.dim) v = *reinterpret_cast<const f32x2*>(a.part + ((x0 + x) * total + row) * a.dim + d);
-      o[0] += f * v[0];
-      o[1] += f * v[1];
+    const int n = min(count - x0, 64);
+    for (int y = wave; y < n; y += 4 * kJoinAtOnce) {
+      if (y != wave) load(y);
+#pragma unroll
+      for (int k = 0; k < kJoinAtOnce; ++k) {
+        const int x = y + 4 * k;
+        if (x >= n) break;
+        const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(by), x));
+        o[0] += f * v[k][0];
+        o[1] += f * v[k][1];
+      }
     }
+    if (x0 + 64 >= count) break;
   }
-  const int64_t tok = row / a.q_heads, qh = row % a.q_heads;
+  sums[wave][lane] = o;
+  __syncthreads();
+  if (wave != 0 || count <= 1) return;  // one part: it has its result
+#pragma unroll
+  for (int w = 1; w < 4; ++w) o += sums[w][lane];
   if (lane == 0 && a.lse) a.lse[qh * a.n_tok + tok] = top * kLn2 + logf(sum);
   if (d >= a.dim) return;
   const bool none = sum == 0.f;
@@ -522,28 +585,64 @@ int64_t slots(const SharedArgs& a, int rows) {
 
 }  // namespace
 
-SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, bool one) {
-  SharedPlan p{32, 4, 1, 0};
-  const int64_t group = a.q_heads / a.kv_heads, keys = std::min<int64_t>(hist, (int64_t)a.window + a.sinks);
+// How a request's keys are shared out: over so many workgroups that there are about `want`, each of `least` tiles
+// at least.
+static void share_out(SharedPlan& p, int64_t base, int64_t tiles, int64_t most, int64_t want, int64_t least) {
+  if (base >= want) return;
+  p.unit = (int32_t)std::max<int64_t>(least, (base * tiles + want - 1) / want);
+  p.splits = (int32_t)std::min<int64_t>((most + p.unit - 1) / p.unit, 4096);
+}
+
+SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, int64_t most, bool one) {
+  SharedPlan p{32, 4, 1, 1, 0};
   n_seq = std::max<int64_t>(n_seq, 1);
+  const int64_t group = a.q_heads / a.kv_heads, seen = (int64_t)a.window + a.sinks;
   if (!one && n_tok * group > 48 * n_seq) p.rows = 128;
-  const int64_t tiles = one ? n_seq * ((group + 31) / 32) : std::max(n_tok * group / p.rows, n_seq);
-  const int64_t base = std::max<int64_t>(tiles * a.kv_heads, 1);
-  if (p.rows == 128) {
-    if (base < 512) p.splits = (int32_t)std::max<int64_t>(1, std::min((keys + 255) / 256, 512 / base));
-  } else if (base < 512 && keys > 128) {
-    const int most = a.dim <= 64 ? 16 : 8;
-    if (base <= 256 && (base > 128 || keys <= 64 * most)) p.waves = most;
-    else p.splits = (int32_t)std::min<int64_t>((keys + 127) / 128, 1024 / base);
-  }
-  p.bytes = p.splits > 1 ? (size_t)p.splits * n_tok * a.q_heads * (a.dim + 2) * sizeof(float) : 0;
+  const int64_t slots = one ? n_seq * ((group + 31) / 32) : std::max(n_tok * group / p.rows, n_seq);
+  const int64_t base = std::max<int64_t>(slots * a.kv_heads, 1);
+  auto shared = [&](int64_t keys, int64_t longest) {
+    if (p.rows == 128) {
+      share_out(p, base, (keys + 63) / 64, (longest + 63) / 64, 512, 4);
+    } else if (base < 512 && keys > 128) {
+      const int waves = a.dim <= 64 ? 16 : 8;
+      if (base <= 256 && (base > 128 || keys <= 64 * waves)) p.waves = waves;
+      else share_out(p, base, (keys + 31) / 32, (longest + 31) / 32, 1024, 4);
+    }
+    return p.splits;
+  };
+  SharedPlan none = p;
+  const int32_t whole = shared(hist, most);
+  std::swap(p, none);
+  // what is enough without a window is enough with one
+  p.splits = std::min(shared(std::min(hist, seen), std::min(most, seen)), whole);
+  if (p.splits > 1) p.bytes = (size_t)n_tok * a.q_heads * (p.splits * (size_t)(a.dim + 2) + 1) * sizeof(float);
   return p;
 }
 
+static int64_t join_threads(const SharedArgs& a, const SharedPlan& p) {
+  const int64_t rows = a.n_tok * a.q_heads;
+  return p.splits > kFewParts ? rows * 256 : (rows * (a.dim / 4) + 255) / 256 * 256;
+}
 // Threads of a call's largest launch.
 int64_t shared_threads(const SharedArgs& a, const SharedPlan& p) {
   const int64_t groups = slots(a, p.rows) * a.kv_heads * p.splits;
-  return std::max(groups * (p.rows == 128 ? 256 : 64 * p.waves), a.n_tok * a.q_heads * 64);
+  return std::max(groups * (p.rows == 128 ? 256 : 64 * p.waves), p.splits > 1 ? join_threads(a, p) : 0);
+}
+
+template <typename T, int DH, bool CODES>
+void go_narrow(const SharedArgs& a, const SharedPlan& p, dim3 grid, hipStream_t st) {
+  constexpr int kMost = DH <= 64 ? 16 : 8;
+  auto go = [&](auto waves, auto tiles) {
+    constexpr int WAVES = decltype(waves)::value;
+    hipLaunchKernelGGL((shared_narrow<T, DH, WAVES, CODES, decltype(tiles)::value>), grid, dim3(64 * WAVES), 0, st, a,
+                       p.splits, p.unit);
+  };
+  auto by_own = [&](auto waves) {
+    if (a.own == kOwnTiles) go(waves, std::true_type{});
+    else go(waves, std::false_type{});
+  };
+  if (p.waves == kMost) by_own(std::integral_constant<int, kMost>{});
+  else by_own(std::integral_constant<int, 4>{});
 }
 
 hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipStream_t st) {
@@ -552,23 +651,24 @@ hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipS
   by_type(a, [&](auto t) {
     typedef decltype(t) T;
     by_width(a, [&](auto d) {
-      constexpr int DH = decltype(d)::value, kMost = DH <= 64 ? 16 : 8;
+      constexpr int DH = decltype(d)::value;
+      auto wide = [&](auto how) {
+        hipLaunchKernelGGL((shared_wide<T, DH, decltype(how)::value>), grid, dim3(256), 0, st, a, p.splits, p.unit);
+      };
       if (p.rows == 128) {
-        if (q8) hipLaunchKernelGGL((shared_wide<T, DH, kCodes>), grid, dim3(256), 0, st, a, p.splits);
-        else if (direct(a, DH)) hipLaunchKernelGGL((shared_wide<T, DH, kDirect>), grid, dim3(256), 0, st, a, p.splits);
-        else hipLaunchKernelGGL((shared_wide<T, DH, kByRegisters>), grid, dim3(256), 0, st, a, p.splits);
-      } else if (p.waves == kMost) {
-        const dim3 threads(64 * kMost);
-        if (q8) hipLaunchKernelGGL((shared_narrow<T, DH, kMost, true>), grid, threads, 0, st, a, p.splits);
-        else hipLaunchKernelGGL((shared_narrow<T, DH, kMost, false>), grid, threads, 0, st, a, p.splits);
+        if (q8) wide(std::integral_constant<int, kCodes>{});
+        else if (direct(a, DH)) wide(std::integral_constant<int, kDirect>{});
+        else wide(std::integral_constant<int, kByRegisters>{});
       } else {
-        if (q8) hipLaunchKernelGGL((shared_narrow<T, DH, 4, true>), grid, dim3(256), 0, st, a, p.splits);
-        else hipLaunchKernelGGL((shared_narrow<T, DH, 4, false>), grid, dim3(256), 0, st, a, p.splits);
+        if (q8) go_narrow<T, DH, true>(a, p, grid, st);
+        else go_narrow<T, DH, false>(a, p, grid, st);
       }
     });
     e = hipGetLastError();
     if (p.splits > 1 && e == hipSuccess) {
-      hipLaunchKernelGGL((shared_join<T>), dim3((unsigned)(a.n_tok * a.q_heads)), dim3(64), 0, st, a, p.splits);
+      const int64_t rows = a.n_tok * a.q_heads, threads = join_threads(a, p);
+      if (p.splits > kFewParts) hipLaunchKernelGGL((shared_join<T>), dim3((unsigned)rows), dim3(256), 0, st, a, p.splits);
+      else hipLaunchKernelGGL((shared_join_few<T>), dim3((unsigned)(threads / 256)), dim3(256), 0, st, a, p.splits);
       e = hipGetLastError();
     }
   });

@@ -114,7 +114,7 @@ __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh
 }
 
 // 128 rows a workgroup, 32 a wave, tiles of 64 keys in LDS, as in the forward.
-template <typename T, int DH, bool DIRECT>
+template <typename T, int DH, bool DIRECT, bool TILES>
 __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) shared_dq(SharedArgs a) {
   typedef TileOf<T, DH, 64, 256, DIRECT> Tile;
   constexpr int kRows = 64, kTile = 128;
@@ -187,19 +187,20 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   const int r = rw + (lane_id<3>() & 31);
   const bool live = r < rows;
   const Row row = row_at(a, live ? r : last);
-  if (a.own == kOwnSelf) {
+  if constexpr (!TILES) {
     dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
   } else {
     typedef RegisterTile<T, DH, kRows, 256, 3> OwnTile;
     const typename OwnTile::Reads own_at;
     const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
     for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)); j0 < end; j0 += kRows) {
-      OwnTile x, y;
-      x.load(nullptr, static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head, a.k.tok, j0, end, a.dim);
-      y.load(nullptr, static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head, a.v.tok, j0, end, a.dim);
       __syncthreads();  // the tile before is done with
-      x.store(lds[0][0]);
-      y.store(lds[0][1]);
+      for (int x = 0; x < 2; ++x) {  // one after the other: two would not fit the registers
+        const EmbHeads& t = x ? a.v : a.k;
+        OwnTile tile;
+        tile.load(nullptr, static_cast<const T*>(t.p) + s.begin * t.tok + kh * t.head, t.tok, j0, end, a.dim);
+        tile.store(lds[0][x]);
+      }
       __syncthreads();
       if (rw >= rows) continue;
       for (int sub = 0; sub < 2; ++sub)
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
 
 // 32 rows a workgroup, where a request has few: its four waves take tiles of 32 keys in turn, and their sums meet
 // in LDS.
-template <typename T, int DH>
+template <typename T, int DH, bool TILES>
 __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
   typedef RegisterTile<T, DH, 32, 64> Tile;
   constexpr int kWaves = 4, kRegs = Tile::kRegs, kPieces = Tile::kPieces;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
   const int r = r0 + (lane_id<3>() & 31);
   const bool live = r < rows;
   const Row row = row_at(a, live ? r : last);
-  if (a.own == kOwnSelf) {
+  if constexpr (!TILES) {
     if (wave == 0) dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
   } else {
     typedef WaveRows<T, DH, Tile, 3> OwnRows;
@@ -611,15 +612,13 @@ struct HistoryBatch {  // of find_tile
   int32_t n_seq;
 };
 
-template <typename T, int DH, bool DIRECT>
-__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), 2) shared_dkv(SharedArgs a, int hist_blocks) {
+template <typename T, int DH, bool DIRECT, bool OWN>
+__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), 2) shared_dkv(SharedArgs a) {
   __shared__ __attribute__((aligned(1024))) DkvTiles<T, DH, DIRECT> sh;
   constexpr int kTokens = 128;
-  const bool own = (int)blockIdx.x >= hist_blocks;  // the same for the whole workgroup
-  const int block = own ? blockIdx.x - hist_blocks : blockIdx.x;
-  const int kh = block % a.kv_heads, slot = block / a.kv_heads;
+  const int kh = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
   const auto first = [](int64_t t, int b) { return t / kTokens + b; };
-  if (own) {
+  if constexpr (OWN) {
     const Seq s = uniform(find_tile(a, slot, first));
     if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
     const int j0 = s.tile * kTokens;
@@ -650,24 +649,31 @@ bool direct(const SharedArgs& a, int width, std::initializer_list<const EmbHeads
 bool few_rows(const SharedArgs& a) { return a.n_tok * a.group <= 48 * (int64_t)a.n_seq; }
 int64_t dq_slots(const SharedArgs& a) { return a.n_tok * a.group / (few_rows(a) ? 32 : 128) + a.n_seq; }
 int64_t hist_slots(const SharedArgs& a) { return a.n_hist / 128 + a.n_seq; }
-int64_t own_slots(const SharedArgs& a) { return a.own == kOwnTiles ? a.n_tok / 128 + a.n_seq : 0; }
+int64_t own_slots(const SharedArgs& a) { return a.n_tok / 128 + a.n_seq; }
 int64_t self_threads(const SharedArgs& a) { return (a.n_tok * a.kv_heads * (a.dim / 8) + 255) / 256 * 256; }
 
-template <typename T, int DH, bool DIRECT>
+template <typename T, int DH, bool DIRECT, bool TILES>
 hipError_t go(const SharedArgs& a, hipStream_t st) {
   if (a.n_tok > 0) {
     const dim3 grid((unsigned)(dq_slots(a) * a.kv_heads));
-    if (few_rows(a)) hipLaunchKernelGGL((shared_dq_few<T, DH>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((shared_dq<T, DH, DIRECT>), grid, dim3(256), 0, st, a);
+    if (few_rows(a)) hipLaunchKernelGGL((shared_dq_few<T, DH, TILES>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((shared_dq<T, DH, DIRECT, TILES>), grid, dim3(256), 0, st, a);
   }
+  // a launch that fails is the last one: what comes after it would read what it did not write
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;  // what comes after it would read what it did not write
-  const int64_t hist = hist_slots(a) * a.kv_heads;
-  hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT>), dim3((unsigned)(hist + own_slots(a) * a.kv_heads)),
-                     dim3(DkvTiles<T, DH, DIRECT>::kThreads), 0, st, a, (int)hist);
-  e = hipGetLastError();
-  if (e != hipSuccess || a.own == kOwnTiles || a.n_tok == 0) return e;
-  hipLaunchKernelGGL((shared_self<T>), dim3((unsigned)(self_threads(a) / 256)), dim3(256), 0, st, a);
+  if (e != hipSuccess) return e;
+  const dim3 threads(DkvTiles<T, DH, DIRECT>::kThreads);
+  if (a.n_hist > 0) {
+    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT, false>), dim3((unsigned)(hist_slots(a) * a.kv_heads)), threads, 0, st,
+                       a);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess || a.n_tok == 0) return e;
+  if (TILES) {
+    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT, true>), dim3((unsigned)(own_slots(a) * a.kv_heads)), threads, 0, st, a);
+  } else {
+    hipLaunchKernelGGL((shared_self<T>), dim3((unsigned)(self_threads(a) / 256)), dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 
@@ -681,7 +687,7 @@ SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_tok) {
 }
 
 int64_t shared_bwd_threads(const SharedArgs& a) {
-  const int64_t dkv = (hist_slots(a) + own_slots(a)) * a.kv_heads * (a.dim <= 64 ? 256 : 512);
+  const int64_t dkv = std::max(hist_slots(a), own_slots(a)) * a.kv_heads * (a.dim <= 64 ? 256 : 512);
   return std::max({dq_slots(a) * a.kv_heads * 256, dkv, self_threads(a)});
 }
 
@@ -690,7 +696,9 @@ hipError_t launch_shared_bwd(const SharedArgs& a, hipStream_t st) {
     typedef decltype(t) T;
     auto by_tiles = [&](auto d) {
       constexpr int DH = decltype(d)::value;
-      return direct(a, DH, {&a.q, &a.k, &a.v, &a.dout, &a.hk, &a.hv}) ? go<T, DH, true>(a, st) : go<T, DH, false>(a, st);
+      const bool straight = direct(a, DH, {&a.q, &a.k, &a.v, &a.dout, &a.hk, &a.hv});
+      if (a.own == kOwnTiles) return straight ? go<T, DH, true, true>(a, st) : go<T, DH, false, true>(a, st);
+      return straight ? go<T, DH, true, false>(a, st) : go<T, DH, false, false>(a, st);
     };
     return a.dim <= 32   ? by_tiles(std::integral_constant<int, 32>{})
            : a.dim <= 64 ? by_tiles(std::integral_constant<int, 64>{})

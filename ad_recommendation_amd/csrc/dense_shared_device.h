@@ -84,6 +84,32 @@ struct HistoryTiles {
   __device__ __forceinline__ int end(int it) const { return it < sinks ? sink_end : n; }
 };
 
+// ---------------------------------------------------------------- work shared out
+// A request's tiles of keys may go to several workgroups: as many as leave each `unit` tiles, at most `splits`. Their
+// sums go to memory in fp32, [split][token][q head][dim], and a second kernel adds them; a row's count of them
+// follows behind all sums and statistics.
+struct Share {
+  int count, first, end;  // workgroups that share; this one's tiles
+};
+__device__ __forceinline__ Share share_of(int total, int splits, int unit, int split) {
+  Share s;
+  s.count = max(min(splits, (int)(((uint32_t)total + unit - 1) / (uint32_t)unit)), 1);
+  const int per = (total + s.count - 1) / s.count;
+  s.first = min(split * per, total);
+  s.end = min(s.first + per, total);
+  return s;
+}
+__device__ __forceinline__ float* part_of(const SharedArgs& a, int split) {
+  return a.part + (int64_t)split * a.n_tok * a.q_heads * a.dim;
+}
+// Maximum (in powers of two) and sum.
+__device__ __forceinline__ float* part_stats(const SharedArgs& a, int splits, int split, int64_t tok, int qh) {
+  return part_of(a, splits) + (((int64_t)split * a.n_tok + tok) * a.q_heads + qh) * 2;
+}
+__device__ __forceinline__ int* part_count(const SharedArgs& a, int splits, int64_t tok, int qh) {
+  return reinterpret_cast<int*>(part_stats(a, splits, splits, 0, 0)) + tok * a.q_heads + qh;
+}
+
 // The first token of a token's candidate; what no valid array holds leaves the token itself at least.
 __device__ __forceinline__ int first_of(const SharedArgs& a, const Seq& s, int tok) {
   const int64_t f = (int64_t)a.first[s.begin + tok] - s.begin;
