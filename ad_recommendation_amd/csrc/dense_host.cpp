@@ -623,7 +623,7 @@ int attn_shared_bwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_t
   DENSE_TRY(check_counts(n_seq, n_tok));
   DENSE_TRY(check_counts(n_seq, n_hist));
   DENSE_CHECK(bytes, EMB_EINVAL, "attention: null pointer: bytes");
-  *bytes = plan_shared_bwd(*a, n_tok).bytes;
+  *bytes = plan_shared_bwd(*a, n_seq, n_tok, n_hist).bytes;
   return EMB_OK;
 }
 
@@ -671,8 +671,8 @@ int attn_shared_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
     DENSE_TRY(check_apart(&one, 1, w.n, w.heads, a->dim, w.name));
   }
   SharedArgs x = packed_args(c, hist_k, hist_v, d_hist_offsets, n_hist);
-  DENSE_TRY(check_launch(shared_bwd_threads(x)));
-  const SharedBwdPlan p = plan_shared_bwd(*a, n_tok);
+  const SharedBwdPlan p = plan_shared_bwd(*a, n_seq, n_tok, n_hist);
+  DENSE_TRY(check_launch(shared_bwd_threads(x, p)));
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   hipStream_t st = static_cast<hipStream_t>(stream);
   DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
@@ -688,7 +688,8 @@ int attn_shared_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   x.dhv = *dhist_v;
   x.delta = static_cast<float*>(d_ws);
   x.self = reinterpret_cast<float*>(static_cast<char*>(d_ws) + p.off_self);
-  return done(launch_shared_bwd(x, st), "attn_shared_bwd");
+  x.part = reinterpret_cast<float*>(static_cast<char*>(d_ws) + p.off_part);
+  return done(launch_shared_bwd(x, p, st), "attn_shared_bwd");
 }
 
 int attn_shared_cache_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t capacity, size_t* bytes) {

@@ -72,11 +72,12 @@ int64_t shared_threads(const SharedArgs& a, const SharedPlan& p);
 hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipStream_t st);
 
 struct SharedBwdPlan {
-  size_t off_self, bytes;
+  int32_t rows, splits, unit;  // of dq, as the forward's
+  size_t off_self, off_part, bytes;
 };
-SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_tok);
-int64_t shared_bwd_threads(const SharedArgs& a);
-hipError_t launch_shared_bwd(const SharedArgs& a, hipStream_t st);
+SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t n_hist);
+int64_t shared_bwd_threads(const SharedArgs& a, const SharedBwdPlan& p);
+hipError_t launch_shared_bwd(const SharedArgs& a, const SharedBwdPlan& p, hipStream_t st);
 
 // ---------------------------------------------------------------- caches in 8 bits
 struct CacheArgs {

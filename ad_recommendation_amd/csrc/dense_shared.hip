@@ -73,30 +73,23 @@ __device__ __forceinline__ void meet_self(const SharedArgs& a, int64_t tok, int 
   }
 }
 
-// 32 own tokens from j0 on, keys and values in LDS at row `at0`, of which a row sees lo to hi: pairs that do not
-// see each other have probabilities of zero, whose products with what is not finite are left out.
+// 32 own tokens from j0 on, keys and values in LDS at row `at0`, of which a row sees lo to hi.
 template <typename T, int DH, typename R>
 __device__ __forceinline__ void meet_own(const char* kt, const char* vt, const R& at, int at0, int lo, int hi, int j0,
                                          const typename Vec8<T>::t (&q)[DH / 16], float c, f32x16 (&o)[DH / 32],
                                          float& m, float& l) {
-  typedef typename Vec8<T>::t V8;
   f32x16 sc[1] = {};
 #pragma unroll
   for (int ks = 0; ks < DH / 16; ++ks) sc[0] = mma(left<T>(kt, at, at0, ks), q[ks], sc[0]);
-  const uint32_t see = hide_outside<3>(lo, hi, j0, sc[0], -kInf);
+  hide_outside<3>(lo, hi, j0, sc[0], -kInf);
   soften(sc, o, m, l, c);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const V8 pb = right_of<T>(sc[0], 8 * k), one = ones<T>(see, 8 * k);
+    const typename Vec8<T>::t pb = right_of<T>(sc[0], 8 * k);
 #pragma unroll
-    for (int db = 0; db < DH / 32; ++db) {
-      const V8 v = left_t<T>(vt, at, at0 + 16 * k, db);
-      o[db] = mma(finite_of<T>(v), pb, o[db]);
-      add_odd<T>(o[db], v, one, one);
-    }
+    for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(vt, at, at0 + 16 * k, db), pb, o[db]);
   }
 }
-
 // ---------------------------------------------------------------- 128 rows
 enum { kByRegisters, kDirect, kCodes };  // how tiles of history get to LDS
 
@@ -148,6 +141,7 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
   constexpr int kRows = 64, kTile = 128;
   constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
   __shared__ __attribute__((aligned(256))) char lds[2][2][kBytes];
+  __shared__ uint32_t said[4];
   int block = blockIdx.x;
   const int kh = block % a.kv_heads;
   block /= a.kv_heads;
@@ -159,14 +153,14 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
   const int r0 = s.tile * kTile, rw = r0 + wave * 32, h0 = kh * a.group;
   const int last = min(r0 + kTile, rows) - 1;  // of the workgroup's rows
 
-  typedef PackedRows<T, DH, Tile> Rows;
-  Rows ql;
-  ql.load(a, a.q, s.begin, h0, rw, a.scale != 0.f ? rows : 0);
   const History hist = history(a, s.index);
   const HistoryTiles<kRows> tiles(hist);
   const Share share = share_of(tiles.total, splits, unit, split);
   if (split >= share.count) return;
   const int it0 = share.first, it1 = share.end;
+  typedef PackedRows<T, DH, Tile> Rows;
+  Rows ql;
+  ql.load(a, a.q, s.begin, h0, rw, a.scale != 0.f ? rows : 0);
 
   typedef std::conditional_t<HOW == kCodes, uint8_t, T> H;
   const H* hk = history_of<H>(a, a.hk, hist, s.index, kh);
@@ -245,11 +239,16 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
         OwnTile x, y;
         x.load(nullptr, static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head, a.k.tok, j0, end, a.dim);
         y.load(nullptr, static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head, a.v.tok, j0, end, a.dim);
+        bool odd = false;
+#pragma unroll
+        for (int n = 0; n < OwnTile::kRegs; ++n) y.r[n] = only_finite<T>(y.r[n], odd);
         __syncthreads();  // the tile before is done with
         x.store(lds[0][0]);
         y.store(lds[0][1]);
-        __syncthreads();
+        odd = any_wave<4>(odd, said);
         if (rw >= rows) continue;
+        if (odd)
+          add_odd_own<T, DH>(a, a.v, s.begin, kh, j0, min(j0 + kRows, end), lo, live ? row.tok : -1, false, o);
         for (int sub = 0; sub < 2; ++sub)
           if (j0 + 32 * sub < end)
             meet_own<T, DH>(lds[0][0], lds[0][1], own_at, 32 * sub, lo, row.tok, j0 + 32 * sub, q, c, o, m, l);
@@ -378,16 +377,22 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
       const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
       for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)) + 32 * wave; j0 < end; j0 += 32 * WAVES) {
         OwnRows::wave_sync();
+        bool odd = false;
         for (int x = 0; x < 2; ++x) {  // one after the other: there are few, and two would not fit the registers
           OwnRows rows_;
           rows_.load(x ? a.v : a.k, s.begin + j0, kh, end - j0, a.dim);
 #pragma unroll
           for (int n = 0; n < kRegs; ++n) {
             const int idx = lane_id<3>() + n * 64;
-            *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = rows_.r[n];
+            bool its = false;
+            const u32x4 fine = only_finite<T>(rows_.r[n], its);
+            if (x) odd |= its;
+            *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = x ? fine : rows_.r[n];
           }
         }
         OwnRows::wave_sync();
+        if (__any(odd))
+          add_odd_own<T, DH>(a, a.v, s.begin, kh, j0, min(j0 + 32, end), lo, live ? row.tok : -1, false, o);
         meet_own<T, DH>(kt, vt, own_at, 0, lo, row.tok, j0, q, c, o, m, l);
       }
     }
@@ -449,12 +454,14 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
   else if (a.lse) a.lse[(int64_t)(h0 + row.g) * a.n_tok + tok] = top * c * kLn2 + logf(sum);
 }
 
-// The sums of a row's parts at their common maximum.  Nothing is read after something else: what is read of parts
-// that are not there is left out.
+// The sums of a row's parts at their common maximum.
 //
-// Few parts: a thread has four columns of a row, all its parts' loads under way at once.
+// A thread has four columns of a row, eight of its parts' loads under way at once.  EAGER, for little data: nothing is
+// read after something else, and what is read of parts that are not there is left out (30 candidates of a request,
+// 4 parts: 3.5 us and 4.5).  Otherwise a row's count comes first, and no part that is not there is read (4516 tokens,
+// 16 heads of 128, up to 8 parts but two on average: 12 us and 19).
 constexpr int kFewParts = 8;
-template <typename T>
+template <typename T, bool EAGER>
 __global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits) {
   const int pieces = a.dim / 4;
   const int64_t total = a.n_tok * a.q_heads, i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / pieces;
@@ -463,28 +470,42 @@ __global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits)
   const float* st = part_of(a, splits);
   const int64_t tok = row / a.q_heads;
   const int qh = (int)(row - tok * a.q_heads), count = *part_count(a, splits, tok, qh);
-  f32x2 stat[kFewParts];
-  f32x4 v[kFewParts];
-#pragma unroll
-  for (int x = 0; x < kFewParts; ++x) {
-    if (x >= splits) break;
-    stat[x] = *reinterpret_cast<const f32x2*>(st + (x * total + row) * 2);
-    v[x] = *reinterpret_cast<const f32x4*>(a.part + (x * total + row) * a.dim + d);
-  }
-  if (count <= 1) return;  // it has its result
+  if (!EAGER && count <= 1) return;  // it has its result
   float top = -kInf, sum = 0.f;
-#pragma unroll
-  for (int x = 0; x < kFewParts; ++x)
-    if (x < count) top = stat[x][0] > top || stat[x][0] != stat[x][0] ? stat[x][0] : top;  // NaN stays
   f32x4 o = {};
+  for (int x0 = 0; x0 < (EAGER ? 1 : count); x0 += kFewParts) {
+    f32x2 stat[kFewParts];
+    f32x4 v[kFewParts];
 #pragma unroll
-  for (int x = 0; x < kFewParts; ++x) {
-    if (x >= count) break;
-    const float by = stat[x][0] == -kInf ? 0.f : stat[x][0] == top ? 1.f : exp2f(stat[x][0] - top);
-    sum += by * stat[x][1];
+    for (int k = 0; k < kFewParts; ++k) {
+      stat[k] = f32x2{-kInf, 0.f};
+      v[k] = f32x4{};
+      if (x0 + k < (EAGER ? splits : count)) {
+        stat[k] = *reinterpret_cast<const f32x2*>(st + ((x0 + k) * total + row) * 2);
+        v[k] = *reinterpret_cast<const f32x4*>(a.part + ((x0 + k) * total + row) * a.dim + d);
+      }
+    }
+    float t = top;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += by * v[x][e];
+    for (int k = 0; k < kFewParts; ++k) {
+      if (EAGER && k >= count) stat[k] = f32x2{-kInf, 0.f};
+      t = stat[k][0] > t || stat[k][0] != stat[k][0] ? stat[k][0] : t;  // NaN stays
+    }
+    const float keep = top == -kInf ? 0.f : top == t ? 1.f : exp2f(top - t);
+    top = t;
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < kFewParts; ++k) {
+      if (x0 + k >= count) break;
+      const float by = stat[k][0] == -kInf ? 0.f : stat[k][0] == t ? 1.f : exp2f(stat[k][0] - t);
+      sum += by * stat[k][1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += by * v[k][e];
+    }
   }
+  if (count <= 1) return;
   if (d == 0 && a.lse) a.lse[qh * a.n_tok + tok] = top * kLn2 + logf(sum);
   typedef T V __attribute__((ext_vector_type(4)));
   const float inv = 1.f / sum;
@@ -493,7 +514,7 @@ __global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits)
   *reinterpret_cast<V*>(static_cast<T*>(a.out.p) + tok * a.out.tok + qh * a.out.head + d) = __builtin_convertvector(o, V);
 }
 
-// Many: a workgroup has a row, and its waves every fourth part.  A lane has one part's maximum and sum (of 64 at a
+// Many parts of few rows: a workgroup has a row, and its waves every fourth part; eager too.  A lane has one part's maximum and sum (of 64 at a
 // time), then two columns, eight parts' loads under way at once.  16 parts of 24 rows 3.5 us, a launch's latency and
 // one of memory; by one wave, its loads one after the other, 7.0.
 constexpr int kJoinAtOnce = 8;
@@ -585,43 +606,47 @@ int64_t slots(const SharedArgs& a, int rows) {
 
 }  // namespace
 
-// How a request's keys are shared out: over so many workgroups that there are about `want`, each of `least` tiles
-// at least.
-static void share_out(SharedPlan& p, int64_t base, int64_t tiles, int64_t most, int64_t want, int64_t least) {
-  if (base >= want) return;
-  p.unit = (int32_t)std::max<int64_t>(least, (base * tiles + want - 1) / want);
-  p.splits = (int32_t)std::min<int64_t>((most + p.unit - 1) / p.unit, 4096);
-}
-
+// How a request's keys are shared out.  us as in by_32_rows().  Of 32 rows, many waves a workgroup rather than a
+// second launch while each has few tiles (1 request of 64 candidates, 1000: 11.2; with a join 12.5).  Of 128 rows, for
+// about 768 workgroups (16 packed histories of up to 6000, 30 candidates, 8 heads of 64: 32; in one part each 94), of
+// 8 tiles at least, 16 where there are many already (12 of up to 5000, 200 candidates, 16 and 4 heads of 64: 46; 8 tiles
+// 54, one part 82).
 SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, int64_t most, bool one) {
-  SharedPlan p{32, 4, 1, 1, 0};
   n_seq = std::max<int64_t>(n_seq, 1);
   const int64_t group = a.q_heads / a.kv_heads, seen = (int64_t)a.window + a.sinks;
-  if (!one && n_tok * group > 48 * n_seq) p.rows = 128;
-  const int64_t slots = one ? n_seq * ((group + 31) / 32) : std::max(n_tok * group / p.rows, n_seq);
-  const int64_t base = std::max<int64_t>(slots * a.kv_heads, 1);
-  auto shared = [&](int64_t keys, int64_t longest) {
+  auto slots = [&](int64_t rows) {
+    const int64_t n = one ? n_seq * ((group + rows - 1) / rows) : std::max(n_tok * group / rows, n_seq);
+    return std::max<int64_t>(n * a.kv_heads, 1);
+  };
+  SharedPlan p{32, 4, 1, 1, 0};
+  // by the whole history: what is enough without a window is enough with one
+  if (!one && !by_32_rows(n_tok * group, n_seq, slots(32), hist)) p.rows = 128;
+  const int64_t base = slots(p.rows);
+  auto shared = [&](SharedPlan& p, int64_t keys, int64_t longest) {
     if (p.rows == 128) {
-      share_out(p, base, (keys + 63) / 64, (longest + 63) / 64, 512, 4);
+      share_out(p, base, (keys + 63) / 64, (longest + 63) / 64, 768, base >= 128 ? 16 : 8);
     } else if (base < 512 && keys > 128) {
       const int waves = a.dim <= 64 ? 16 : 8;
       if (base <= 256 && (base > 128 || keys <= 64 * waves)) p.waves = waves;
       else share_out(p, base, (keys + 31) / 32, (longest + 31) / 32, 1024, 4);
     }
-    return p.splits;
   };
-  SharedPlan none = p;
-  const int32_t whole = shared(hist, most);
-  std::swap(p, none);
-  // what is enough without a window is enough with one
-  p.splits = std::min(shared(std::min(hist, seen), std::min(most, seen)), whole);
+  SharedPlan whole = p;
+  shared(whole, hist, most);
+  shared(p, std::min(hist, seen), std::min(most, seen));
+  p.splits = std::min(p.splits, whole.splits);
   if (p.splits > 1) p.bytes = (size_t)n_tok * a.q_heads * (p.splits * (size_t)(a.dim + 2) + 1) * sizeof(float);
   return p;
 }
 
+// How the parts are joined: eager where all that there could be is little, by workgroups where that is of many parts.
+static bool join_eager(const SharedArgs& a, const SharedPlan& p) {
+  return (int64_t)p.splits * a.n_tok * a.q_heads * a.dim * 4 <= (8 << 20);
+}
+static bool join_by_groups(const SharedArgs& a, const SharedPlan& p) { return p.splits > kFewParts && join_eager(a, p); }
 static int64_t join_threads(const SharedArgs& a, const SharedPlan& p) {
   const int64_t rows = a.n_tok * a.q_heads;
-  return p.splits > kFewParts ? rows * 256 : (rows * (a.dim / 4) + 255) / 256 * 256;
+  return join_by_groups(a, p) ? rows * 256 : (rows * (a.dim / 4) + 255) / 256 * 256;
 }
 // Threads of a call's largest launch.
 int64_t shared_threads(const SharedArgs& a, const SharedPlan& p) {
@@ -666,9 +691,10 @@ hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipS
     });
     e = hipGetLastError();
     if (p.splits > 1 && e == hipSuccess) {
-      const int64_t rows = a.n_tok * a.q_heads, threads = join_threads(a, p);
-      if (p.splits > kFewParts) hipLaunchKernelGGL((shared_join<T>), dim3((unsigned)rows), dim3(256), 0, st, a, p.splits);
-      else hipLaunchKernelGGL((shared_join_few<T>), dim3((unsigned)(threads / 256)), dim3(256), 0, st, a, p.splits);
+      const dim3 join((unsigned)(join_threads(a, p) / 256));
+      if (join_by_groups(a, p)) hipLaunchKernelGGL((shared_join<T>), join, dim3(256), 0, st, a, p.splits);
+      else if (join_eager(a, p)) hipLaunchKernelGGL((shared_join_few<T, true>), join, dim3(256), 0, st, a, p.splits);
+      else hipLaunchKernelGGL((shared_join_few<T, false>), join, dim3(256), 0, st, a, p.splits);
       e = hipGetLastError();
     }
   });

@@ -51,8 +51,8 @@ __device__ __forceinline__ float row_delta(const typename Vec8<T>::t (&out)[DH /
   return swap32_sum(s);
 }
 
-// A tile of 32 keys at row at0 of LDS tiles: dq += ds k.  OWN: of keys j0 on the row sees lo to hi; pairs that do not
-// see each other are left out.  Otherwise the first n are there, and seen.
+// A tile of 32 keys at row at0 of LDS tiles: dq += ds k.  OWN: of keys j0 on the row sees lo to hi.  Otherwise the
+// first n are there, and seen.
 template <typename T, int DH, bool OWN, typename R>
 __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R& at, int at0, int n, int lo, int hi,
                                         int j0, const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int& by,
@@ -67,23 +67,14 @@ __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R&
   f32x16 ds;
 #pragma unroll
   for (int r = 0; r < 16; ++r) ds[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -w.lse)) * (dp[r] - w.delta);
-  uint32_t see = 0;
-  if (OWN) see = hide_outside<3>(lo, hi, j0, ds, 0.f);
+  if (OWN) hide_outside<3>(lo, hi, j0, ds, 0.f);
   else if (n < 32) hide_from(n, 0, ds, 0.f);
   fit_if<T>(ds, dq, by, some);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const V8 b = right_of<T>(ds, 8 * k);
 #pragma unroll
-    for (int db = 0; db < DH / 32; ++db) {
-      const V8 x = left_t<T>(kt, at, at0 + 16 * k, db);
-      if (OWN) {
-        dq[db] = mma(finite_of<T>(x), b, dq[db]);
-        add_odd<T>(dq[db], x, ones<T>(see, 8 * k), V8{});
-      } else {
-        dq[db] = mma(x, b, dq[db]);
-      }
-    }
+    for (int db = 0; db < DH / 32; ++db) dq[db] = mma(left_t<T>(kt, at, at0 + 16 * k, db), b, dq[db]);
   }
 }
 
@@ -93,7 +84,10 @@ __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh
                                         const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int by) {
   const T* kp = static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + tok * a.v.tok + kh * a.v.head;
-  const float s = dot_row<T, DH, 3>(w.q, kp, live, a.dim), dp = dot_row<T, DH, 3>(w.d, vp, live, a.dim);
+  asm volatile("" ::: "memory");  // one row after the other: the registers are full
+  const float s = dot_row<T, DH, 3>(w.q, kp, live, a.dim);
+  asm volatile("" ::: "memory");
+  const float dp = dot_row<T, DH, 3>(w.d, vp, live, a.dim);
   if (!live) return;
   const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -w.lse)), ds = p * (dp - w.delta), x = ldexpf(ds, -by);
   const int64_t at = (int64_t)qh * a.n_tok + tok;
@@ -115,13 +109,17 @@ __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh
 
 // 128 rows a workgroup, 32 a wave, tiles of 64 keys in LDS, as in the forward.
 template <typename T, int DH, bool DIRECT, bool TILES>
-__global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) shared_dq(SharedArgs a) {
+__global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) shared_dq(SharedArgs a, int splits, int unit) {
   typedef TileOf<T, DH, 64, 256, DIRECT> Tile;
   constexpr int kRows = 64, kTile = 128;
   constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
   __shared__ __attribute__((aligned(256))) char lds[2][2][kBytes];
-  const int kh = blockIdx.x % a.kv_heads;
-  const Seq s = find_rows<kTile>(a, blockIdx.x / a.kv_heads);
+  __shared__ uint32_t said[4];
+  int block = blockIdx.x;
+  const int kh = block % a.kv_heads;
+  block /= a.kv_heads;
+  const int split = block % splits;
+  const Seq s = find_rows<kTile>(a, block / splits);
   const int rows = s.len * a.group;
   if (s.tile < 0 || (int64_t)s.tile * kTile >= rows) return;
   const int wave = uniform(threadIdx.x >> 6);
@@ -134,6 +132,8 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   ol.load(a, a.out, s.begin, h0, rw, rows);
   const History hist = history(a, s.index);
   const HistoryTiles<kRows> tiles(hist);
+  const Share share = share_of(tiles.total, splits, unit, split);
+  if (split >= share.count) return;
   const T* hk = history_of<T>(a, a.hk, hist, s.index, kh);
   const T* hv = history_of<T>(a, a.hv, hist, s.index, kh);
   Tile kl, vl;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
     kl.load(to[0], hk, a.hk.tok, tiles.key0(it), tiles.end(it), a.dim);
     vl.load(to[1], hv, a.hv.tok, tiles.key0(it), tiles.end(it), a.dim);
   };
-  if (tiles.total > 0) load(0, lds[0]);
+  if (share.first < share.end) load(share.first, lds[0]);
   const typename Tile::Reads at;
   char* const part = lds[1][wave >> 1];  // a wave's own part of the tiles that the first step does not use
   const int part0 = 32 * (wave & 1);
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
     const int r = rw + (lane_id() & 31);
     const Row row = row_at(a, min(r, last));
     const int64_t stat = (int64_t)(h0 + row.g) * a.n_tok + s.begin + row.tok;
-    if (r < rows && lane_id() < 32) a.delta[stat] = w.delta;
+    if (split == 0 && r < rows && lane_id() < 32) a.delta[stat] = w.delta;
     w.lse = r < rows ? a.lse[stat] * kLog2e : kInf;
   }
   f32x16 dq[DH / 32] = {};
@@ -167,10 +167,10 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   auto meet = [&](int it, char (*now)[kBytes], char (*next)[kBytes]) {
     kl.store(now[0]);
     vl.store(now[1]);
-    if (!DIRECT && it + 1 < tiles.total) load(it + 1, next);
+    if (!DIRECT && it + 1 < share.end) load(it + 1, next);
     Tile::arrived();
     __syncthreads();  // this tile is there, and the other buffer is no longer read
-    if (DIRECT && it + 1 < tiles.total) load(it + 1, next);
+    if (DIRECT && it + 1 < share.end) load(it + 1, next);
     if (rw >= rows) return;
     const int n = tiles.end(it) - tiles.key0(it);
 #pragma unroll
@@ -179,15 +179,17 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
         dq_meet<T, DH, false>(now[0], now[1], at, 32 * sub, n - 32 * sub, 0, 0, 0, w, c, dq, by, some);
   };
   // two tiles a turn, so that the buffers' places are constants
-  for (int it = 0; it < tiles.total; it += 2) {
+  for (int it = share.first; it < share.end; it += 2) {
     meet(it, lds[0], lds[1]);
-    if (it + 1 < tiles.total) meet(it + 1, lds[1], lds[0]);
+    if (it + 1 < share.end) meet(it + 1, lds[1], lds[0]);
   }
 
   const int r = rw + (lane_id<3>() & 31);
   const bool live = r < rows;
   const Row row = row_at(a, live ? r : last);
-  if constexpr (!TILES) {
+  if (split != share.count - 1) {
+    // own tokens are met by the last workgroup of a row
+  } else if constexpr (!TILES) {
     dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
   } else {
     typedef RegisterTile<T, DH, kRows, 256, 3> OwnTile;
@@ -195,14 +197,26 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
     const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
     for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)); j0 < end; j0 += kRows) {
       __syncthreads();  // the tile before is done with
+      bool odd = false;
       for (int x = 0; x < 2; ++x) {  // one after the other: two would not fit the registers
         const EmbHeads& t = x ? a.v : a.k;
         OwnTile tile;
         tile.load(nullptr, static_cast<const T*>(t.p) + s.begin * t.tok + kh * t.head, t.tok, j0, end, a.dim);
+#pragma unroll
+        for (int n = 0; n < OwnTile::kRegs; ++n) {
+          bool its = false;
+          const u32x4 fine = only_finite<T>(tile.r[n], its);
+          if (!x) {
+            tile.r[n] = fine;
+            odd |= its;
+          }
+        }
         tile.store(lds[0][x]);
       }
-      __syncthreads();
+      odd = any_wave<4>(odd, said);
       if (rw >= rows) continue;
+      if (odd)
+        add_odd_own<T, DH>(a, a.k, s.begin, kh, j0, min(j0 + kRows, end), lo, live ? row.tok : -1, true, dq);
       for (int sub = 0; sub < 2; ++sub)
         if (j0 + 32 * sub < end)
           dq_meet<T, DH, true>(lds[0][0], lds[0][1], own_at, 32 * sub, 0, lo, row.tok, j0 + 32 * sub, w, c, dq, by,
@@ -214,24 +228,36 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   if constexpr (std::is_same<T, _Float16>::value) {
     if (some) unfit(dq, by);
   }
+  const int64_t tok = s.begin + row.tok;
+  if (splits > 1 && split == 0 && live && lane_id<3>() < 32) *part_count(a, splits, tok, h0 + row.g) = share.count;
+  if (share.count > 1) {
+    const EmbHeads to{part_of(a, split), 0, (int64_t)a.q_heads * a.dim, a.dim};
+    if (live) store_row<float, DH, 3>(to, tok, h0 + row.g, a.dim, dq, 1.f);
+    return;
+  }
   PackedRows<T, DH, Tile, 3>::store(a, a.dq, s.begin, h0, rw, rows, lds[1][wave >> 1], part0, dq, a.scale);
 }
 
 // 32 rows a workgroup, where a request has few: its four waves take tiles of 32 keys in turn, and their sums meet
 // in LDS.
 template <typename T, int DH, bool TILES>
-__global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
+__global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits, int unit) {
   typedef RegisterTile<T, DH, 32, 64> Tile;
   constexpr int kWaves = 4, kRegs = Tile::kRegs, kPieces = Tile::kPieces;
   __shared__ __attribute__((aligned(256))) char lds[kWaves][2][Tile::kBytes];
-  const int kh = blockIdx.x % a.kv_heads;
-  const Seq s = find_rows<32>(a, blockIdx.x / a.kv_heads);
+  int block = blockIdx.x;
+  const int kh = block % a.kv_heads;
+  block /= a.kv_heads;
+  const int split = block % splits;
+  const Seq s = find_rows<32>(a, block / splits);
   const int rows = s.len * a.group;
   if (s.tile < 0 || (int64_t)s.tile * 32 >= rows) return;
   const int wave = uniform(threadIdx.x >> 6), lane = lane_id();
   const int r0 = s.tile * 32, h0 = kh * a.group, last = min(r0 + 32, rows) - 1;
   const History hist = history(a, s.index);
   const HistoryTiles<32> tiles(hist);
+  const Share share = share_of(tiles.total, splits, unit, split);
+  if (split >= share.count) return;
   const T* hk = history_of<T>(a, a.hk, hist, s.index, kh);
   const T* hv = history_of<T>(a, a.hv, hist, s.index, kh);
   u32x4 kr[kRegs], vr[kRegs];
@@ -264,27 +290,27 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
     x.to_right(kt, 0, at, w.q);
     Rows::W::wave_sync();
   }
-  int it = wave;
-  if (it < tiles.total) load(it);
+  int it = share.first + wave;
+  if (it < share.end) load(it);
   const float c = a.scale * kLog2e;
   {
     const int r = r0 + (lane & 31);
     const Row row = row_at(a, min(r, last));
     const int64_t stat = (int64_t)(h0 + row.g) * a.n_tok + s.begin + row.tok;
-    if (r < rows && threadIdx.x < 32) a.delta[stat] = w.delta;
+    if (split == 0 && r < rows && threadIdx.x < 32) a.delta[stat] = w.delta;
     w.lse = r < rows ? a.lse[stat] * kLog2e : kInf;
   }
   f32x16 dq[DH / 32] = {};
   int by = 0;
   bool some = false;
-  for (; it < tiles.total; it += kWaves) {
+  for (; it < share.end; it += kWaves) {
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
       const int idx = lane + n * 64, to = Tile::at(idx / kPieces, idx % kPieces);
       *reinterpret_cast<u32x4*>(kt + to) = kr[n];
       *reinterpret_cast<u32x4*>(vt + to) = vr[n];
     }
-    if (it + kWaves < tiles.total) load(it + kWaves);
+    if (it + kWaves < share.end) load(it + kWaves);
     WaveRows<T, DH, Tile>::wave_sync();
     dq_meet<T, DH, false>(kt, vt, at, 0, tiles.end(it) - tiles.key0(it), 0, 0, 0, w, c, dq, by, some);
     WaveRows<T, DH, Tile>::wave_sync();
@@ -292,7 +318,9 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
   const int r = r0 + (lane_id<3>() & 31);
   const bool live = r < rows;
   const Row row = row_at(a, live ? r : last);
-  if constexpr (!TILES) {
+  if (split != share.count - 1) {
+    // own tokens are met by the last workgroup of a row
+  } else if constexpr (!TILES) {
     if (wave == 0) dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
   } else {
     typedef WaveRows<T, DH, Tile, 3> OwnRows;
@@ -300,16 +328,22 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
     const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
     for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)) + 32 * wave; j0 < end; j0 += 32 * kWaves) {
       OwnRows::wave_sync();
+      bool odd = false;
       for (int x = 0; x < 2; ++x) {
         OwnRows rows_;
         rows_.load(x ? a.v : a.k, s.begin + j0, kh, end - j0, a.dim);
 #pragma unroll
         for (int n = 0; n < kRegs; ++n) {
           const int idx = lane_id<3>() + n * 64;
-          *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = rows_.r[n];
+          bool its = false;
+          const u32x4 fine = only_finite<T>(rows_.r[n], its);
+          if (!x) odd |= its;
+          *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = x ? rows_.r[n] : fine;
         }
       }
       OwnRows::wave_sync();
+      if (__any(odd))
+        add_odd_own<T, DH>(a, a.k, s.begin, kh, j0, min(j0 + 32, end), lo, live ? row.tok : -1, true, dq);
       dq_meet<T, DH, true>(kt, vt, own_at, 0, 0, lo, row.tok, j0, w, c, dq, by, some);
     }
   }
@@ -338,20 +372,50 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a) {
       for (int e = 0; e < 4; ++e) t[e] += o[e];
     }
     if (!live || d >= a.dim) continue;
+    if (share.count > 1) {
+      *reinterpret_cast<f32x4*>(part_of(a, split) + ((s.begin + row.tok) * a.q_heads + h0 + row.g) * a.dim + d) = t;
+      continue;
+    }
     typedef T V __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int e = 0; e < 4; ++e) t[e] *= a.scale;
     *reinterpret_cast<V*>(row_ptr<T>(a.dq, s.begin, h0, row) + d) = __builtin_convertvector(t, V);
   }
+  if (splits > 1 && split == 0 && live && threadIdx.x < 32)
+    *part_count(a, splits, s.begin + row.tok, h0 + row.g) = share.count;
 }
 
-// dk and dv of tokens that are candidates of their own, from p and ds of their rows with themselves: a thread has
-// eight columns of a token's key/value head and goes over the heads of the group.
-template <typename T>
-__global__ void __launch_bounds__(256) shared_self(SharedArgs a) {
+// What is left when the sums are there, in one launch.  dq of rows that several workgroups shared: a thread adds
+// four columns of their parts, in order.  And dk and dv of tokens that are candidates of their own, from p and ds of
+// their rows with themselves: a thread has eight columns of a token's key/value head and goes over its heads' group.
+template <typename T, bool SELF>
+__global__ void __launch_bounds__(256) shared_finish(SharedArgs a, int splits, int join_blocks) {
   typedef typename Vec8<T>::t V8;
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  if ((int)blockIdx.x < join_blocks) {
+    const int pieces = a.dim / 4;
+    const int64_t total = a.n_tok * a.q_heads, i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / pieces;
+    const int d = (int)(i - row * pieces) * 4;
+    if (row >= total) return;
+    const int64_t tok = row / a.q_heads;
+    const int qh = (int)(row - tok * a.q_heads), count = *part_count(a, splits, tok, qh);
+    if (count <= 1) return;  // it has its gradient
+    f32x4 t = {};
+#pragma unroll 4
+    for (int x = 0; x < count; ++x) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (x * total + row) * a.dim + d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] *= a.scale;
+    *reinterpret_cast<V4*>(static_cast<T*>(a.dq.p) + tok * a.dq.tok + qh * a.dq.head + d) =
+        __builtin_convertvector(t, V4);
+    return;
+  }
+  if (!SELF) return;
   const int pieces = a.dim / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, unit = i / pieces;
+  const int64_t i = (int64_t)(blockIdx.x - join_blocks) * 256 + threadIdx.x, unit = i / pieces;
   const int col = (int)(i - unit * pieces) * 8;
   const int64_t tok = unit / a.kv_heads;
   const int kh = (int)(unit - tok * a.kv_heads);
@@ -377,8 +441,7 @@ __global__ void __launch_bounds__(256) shared_self(SharedArgs a) {
 }
 
 // ---------------------------------------------------------------- dk, dv
-// A workgroup has 128 keys, of a history or of a request's own tokens, for a key/value head and meets the request's
-// rows, 64 a step.  Heads of 64 and less: four waves of 32 keys, which hold them as right operands in registers.
+// A workgroup has 128 keys of a history for a key/value head and meets the request's rows, 64 a step.  Heads of 64 and less: four waves of 32 keys, which hold them as right operands in registers.
 // Heads of 128: eight waves, two to each 32 keys with half of a step's rows, and keys and values in LDS.
 
 // 64 rows (token, head of the group) to LDS.
@@ -420,7 +483,6 @@ struct DkvTiles {
   char q[2][kBytes], d[2][kBytes];
   char k[kWide ? 2 : 0][kBytes], v[kWide ? 2 : 0][kBytes];
   float lse[2][64], delta[2][64];
-  int first[2][64], tok[2][64];  // of a row: its candidate's first token, its own
   __device__ __forceinline__ char* part(int wave) {
     if (kWide) return wave & 2 ? v[0] : k[0];
     return (wave & 2 ? d : q)[1];
@@ -442,8 +504,8 @@ __device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave)
   }
 }
 
-// OWN: keys are the request's tokens j0 to j1 - 1, met by the rows of their candidates.
-template <typename T, int DH, bool DIRECT, bool OWN>
+// Of keys j0 to j1 - 1 of a history: all rows of the request.
+template <typename T, int DH, bool DIRECT>
 __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>& sh, const Seq& s, const History& hist,
                                     int kh, int j0, int j1) {
   typedef typename Vec8<T>::t V8;
@@ -452,77 +514,59 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
   constexpr int kRows = 64;
   const int wave = uniform(threadIdx.x >> 6), h0 = kh * a.group;
   const int jrow = 32 * (wave & 3), jw = j0 + jrow, j = jw + (lane_id() & 31);
-  const int rows = s.len * a.group, row0 = OWN ? j0 * a.group : 0;
-  const EmbHeads &kx = OWN ? a.k : a.hk, &vx = OWN ? a.v : a.hv;
-  const int64_t begin = OWN ? s.begin : hist.row;
+  const int rows = s.len * a.group;
 
-  const typename Tile::Reads at;
-  typedef WaveRows<T, DH, Tile> Rows;
-  V8 k[P::kWide ? 1 : DH / 16], v[P::kWide ? 1 : DH / 16];
-  if constexpr (P::kWide) {
-    const T* kp = static_cast<const T*>(kx.p) + begin * kx.tok + kh * kx.head;
-    const T* vp = static_cast<const T*>(vx.p) + begin * vx.tok + kh * vx.head;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      Tile kl, vl;
-      kl.load(sh.k[x], kp, kx.tok, j0 + kRows * x, j1, a.dim);
-      vl.load(sh.v[x], vp, vx.tok, j0 + kRows * x, j1, a.dim);
-      kl.store(sh.k[x]);
-      vl.store(sh.v[x]);
-    }
-  } else {
-    // through the buffers that the first step does not use
-    Rows kl, vl;
-    kl.load(kx, begin + jw, kh, j1 - jw, a.dim);
-    vl.load(vx, begin + jw, kh, j1 - jw, a.dim);
-    kl.to_right(sh.part(wave), 32 * (wave & 1), at, k);
-    vl.to_right(sh.part(wave), 32 * (wave & 1), at, v);
-  }
-  const float c = a.scale * kLog2e;
   RowsTile<T, DH, P::kThreads, DIRECT> ql, dl;
   float stat = 0.f;  // the first 64 threads: lse of a row; as many after them: its delta
-  int tok = 0, first = 0;
   auto load = [&](int b, int r0) {
     ql.load(sh.q[b], a, a.q, s.begin, h0, r0, rows);
     dl.load(sh.d[b], a, a.dout, s.begin, h0, r0, rows);
     if (threadIdx.x < 2 * kRows) {
       const int r = r0 + (threadIdx.x & (kRows - 1));
       const float* p = threadIdx.x < kRows ? a.lse : a.delta;
-      // a row that is not there gets probabilities of zero, and sees no token
+      // a row that is not there gets probabilities of zero
       stat = threadIdx.x < kRows ? kInf : 0.f;
-      tok = -1;
-      first = 0;
       if (r < rows) {
         const Row x = row_at(a, r);
         stat = p[(int64_t)(h0 + x.g) * a.n_tok + s.begin + x.tok];
-        if (OWN) {
-          tok = x.tok;
-          first = first_of(a, s, x.tok);
-        }
       }
     }
   };
+  if (rows > 0) load(0, 0);
+  const typename Tile::Reads at;
+  typedef WaveRows<T, DH, Tile> Rows;
+  V8 k[P::kWide ? 1 : DH / 16], v[P::kWide ? 1 : DH / 16];
+  if constexpr (P::kWide) {
+    const T* kp = history_of<T>(a, a.hk, hist, 0, kh);
+    const T* vp = history_of<T>(a, a.hv, hist, 0, kh);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      Tile kl, vl;
+      kl.load(sh.k[x], kp, a.hk.tok, j0 + kRows * x, j1, a.dim);
+      vl.load(sh.v[x], vp, a.hv.tok, j0 + kRows * x, j1, a.dim);
+      kl.store(sh.k[x]);
+      vl.store(sh.v[x]);
+    }
+  } else {
+    // through the buffers that the first step does not use
+    Rows kl, vl;
+    kl.load(a.hk, hist.row + jw, kh, j1 - jw, a.dim);
+    vl.load(a.hv, hist.row + jw, kh, j1 - jw, a.dim);
+    kl.to_right(sh.part(wave), 32 * (wave & 1), at, k);
+    vl.to_right(sh.part(wave), 32 * (wave & 1), at, v);
+  }
+  const float c = a.scale * kLog2e;
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
   int by = 0;  // in fp16 dk stands at 2^-by
   bool some = false;
-  if (row0 < rows) load(0, row0);
-  for (int r0 = row0, b = 0; r0 < rows; r0 += kRows, b ^= 1) {
+  for (int r0 = 0, b = 0; r0 < rows; r0 += kRows, b ^= 1) {
     ql.store(sh.q[b]);
     dl.store(sh.d[b]);
-    if (threadIdx.x < kRows) {
-      sh.lse[b][threadIdx.x] = stat * kLog2e;
-      if (OWN) {
-        sh.first[b][threadIdx.x] = first;
-        sh.tok[b][threadIdx.x] = tok;
-      }
-    } else if (threadIdx.x < 2 * kRows) {
-      sh.delta[b][threadIdx.x - kRows] = stat;
-    }
+    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat * kLog2e;
+    else if (threadIdx.x < 2 * kRows) sh.delta[b][threadIdx.x - kRows] = stat;
     if (!DIRECT && r0 + kRows < rows) load(b ^ 1, r0 + kRows);
     Tile::arrived();
     __syncthreads();  // this step's rows are there, and the other buffer is no longer read
-    // candidates from here on begin after the last key
-    if (OWN && sh.first[b][0] >= j1) break;
     if (DIRECT && r0 + kRows < rows) load(b ^ 1, r0 + kRows);
     if (jw >= j1) continue;
 #pragma unroll
@@ -545,7 +589,6 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
         }
       }
       f32x16 p, ds;
-      uint32_t see = 0;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int i = 32 * sub + 8 * g + 4 * (lane_id() >> 5);
@@ -555,10 +598,6 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
         for (int e = 0; e < 4; ++e) {
           p[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -lse[e]));
           ds[4 * g + e] = p[4 * g + e] * (dp[4 * g + e] - delta[e]);
-          if (OWN) {
-            if (j >= sh.first[b][i + e] && j <= sh.tok[b][i + e]) see |= 1u << (4 * g + e);
-            else p[4 * g + e] = ds[4 * g + e] = 0.f;
-          }
         }
       }
       fit_if<T>(ds, dk, by, some);
@@ -567,18 +606,8 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
         const V8 pb = right_of<T>(p, 8 * x), dsb = right_of<T>(ds, 8 * x);
 #pragma unroll
         for (int db = 0; db < DH / 32; ++db) {
-          const V8 dt = left_t<T>(sh.d[b], at, 32 * sub + 16 * x, db);
-          const V8 qt = left_t<T>(sh.q[b], at, 32 * sub + 16 * x, db);
-          if (OWN) {
-            const V8 one = ones<T>(see, 8 * x);
-            dv[db] = mma(finite_of<T>(dt), pb, dv[db]);
-            add_odd<T>(dv[db], dt, one, one);
-            dk[db] = mma(finite_of<T>(qt), dsb, dk[db]);
-            add_odd<T>(dk[db], qt, one, V8{});
-          } else {
-            dv[db] = mma(dt, pb, dv[db]);
-            dk[db] = mma(qt, dsb, dk[db]);
-          }
+          dv[db] = mma(left_t<T>(sh.d[b], at, 32 * sub + 16 * x, db), pb, dv[db]);
+          dk[db] = mma(left_t<T>(sh.q[b], at, 32 * sub + 16 * x, db), dsb, dk[db]);
         }
       }
     }
@@ -586,7 +615,7 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
   if constexpr (std::is_same<T, _Float16>::value) {
     if (some) unfit(dk, by);
   }
-  Tile::arrived();  // of a step that was left early
+  Tile::arrived();  // of keys that no row met
   if (P::kWide) {
     float* fold = reinterpret_cast<float*>(sh.q);
     static_assert(!P::kWide || sizeof(sh.q) + sizeof(sh.d) >= sizeof(float) * 4 * 32 * DH, "room to fold");
@@ -596,14 +625,13 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
     __syncthreads();  // the tiles are done with
   }
   if (wave >= 4) return;
-  // what no row sees, of a history, gets zeros
-  if (!OWN && (rows == 0 || (j < hist.first && j >= hist.sinks))) {
+  // what no row sees gets zeros
+  if (rows == 0 || (j < hist.first && j >= hist.sinks)) {
 #pragma unroll
     for (int db = 0; db < DH / 32; ++db) dk[db] = dv[db] = f32x16{};
   }
-  const EmbHeads &dkx = OWN ? a.dk : a.dhk, &dvx = OWN ? a.dv : a.dhv;
-  Rows::store(dkx, begin + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dk, a.scale, 0);
-  Rows::store(dvx, begin + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dv, 1.f, 0);
+  Rows::store(a.dhk, hist.row + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dk, a.scale, 0);
+  Rows::store(a.dhv, hist.row + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dv, 1.f, 0);
 }
 
 struct HistoryBatch {  // of find_tile
@@ -612,27 +640,142 @@ struct HistoryBatch {  // of find_tile
   int32_t n_seq;
 };
 
-template <typename T, int DH, bool DIRECT, bool OWN>
-__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), 2) shared_dkv(SharedArgs a) {
+// Waves of a SIMD.
+template <int DH>
+constexpr int dkv_waves = DH == 32 ? 3 : 2;
+
+template <typename T, int DH, bool DIRECT>
+__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), (dkv_waves<DH>)) shared_dkv(SharedArgs a) {
   __shared__ __attribute__((aligned(1024))) DkvTiles<T, DH, DIRECT> sh;
   constexpr int kTokens = 128;
   const int kh = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
-  const auto first = [](int64_t t, int b) { return t / kTokens + b; };
-  if constexpr (OWN) {
-    const Seq s = uniform(find_tile(a, slot, first));
-    if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
-    const int j0 = s.tile * kTokens;
-    dkv<T, DH, DIRECT, true>(a, sh, s, History{}, kh, j0, min(j0 + kTokens, s.len));
-  } else {
-    const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot, first));
-    if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
-    const History hist = history(a, h.index);
-    Seq s = uniform(sequence(a, h.index, 0));
-    const int j0 = h.tile * kTokens;
-    // a tile that no row sees has none
-    if (j0 >= hist.sinks && j0 + kTokens <= hist.first) s.len = 0;
-    dkv<T, DH, DIRECT, false>(a, sh, s, hist, kh, j0, min(j0 + kTokens, hist.n));
+  const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot,
+                                  [](int64_t t, int b) { return t / kTokens + b; }));
+  if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
+  const History hist = history(a, h.index);
+  Seq s = uniform(sequence(a, h.index, 0));
+  const int j0 = h.tile * kTokens;
+  // a tile that no row sees has none
+  if (j0 >= hist.sinks && j0 + kTokens <= hist.first) s.len = 0;
+  dkv<T, DH, DIRECT>(a, sh, s, hist, kh, j0, min(j0 + kTokens, hist.n));
+}
+
+// dk and dv of own tokens, where candidates have more than one: a wave has 32 of them for a key/value head and
+// meets the rows from there to the end of the last one's candidate, 32 a step.  Candidates are short, and so is this; a
+// workgroup of four waves, 128 tokens and 64 rows a step took 90 us where this takes TODO (200 requests of up to
+// 120 tokens, candidates of 3, 8 heads of 64).
+template <typename T, int DH>
+__global__ void __launch_bounds__(64, (DH == 128 ? 1 : 2)) shared_dkv_own(SharedArgs a) {
+  typedef typename Vec8<T>::t V8;
+  typedef RegisterTile<T, DH, 32, 64> Tile;
+  typedef PackedRows<T, DH, Tile> Rows;
+  constexpr int kTokens = 32;
+  __shared__ __attribute__((aligned(256))) char lds[2][Tile::kBytes];
+  __shared__ float lses[32], deltas[32];
+  __shared__ int firsts[32], toks[32];
+  const int kh = blockIdx.x % a.kv_heads, h0 = kh * a.group, lane = lane_id();
+  const Seq s = uniform(find_tile(a, blockIdx.x / a.kv_heads, [](int64_t t, int b) { return t / kTokens + b; }));
+  if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
+  const int j0 = s.tile * kTokens, j1 = min(j0 + kTokens, s.len), j = j0 + (lane & 31), rows = s.len * a.group;
+  const typename Tile::Reads at;
+  Rows ql, dl;
+  float lse = kInf, delta = 0.f;
+  int tok = -1, first = 0;
+  auto load = [&](int r0) {
+    ql.load(a, a.q, s.begin, h0, r0, rows);
+    dl.load(a, a.dout, s.begin, h0, r0, rows);
+    const int r = r0 + (lane & 31);
+    // a row that is not there sees no token
+    lse = kInf;
+    delta = 0.f;
+    tok = -1;
+    first = INT32_MAX;
+    if (r < rows) {
+      const Row x = row_at(a, r);
+      const int64_t stat = (int64_t)(h0 + x.g) * a.n_tok + s.begin + x.tok;
+      lse = a.lse[stat] * kLog2e;
+      delta = a.delta[stat];
+      tok = x.tok;
+      first = first_of(a, s, x.tok);
+    }
+  };
+  V8 k[DH / 16], v[DH / 16];
+  {
+    WaveRows<T, DH, Tile> kl;
+    kl.load(a.k, s.begin + j0, kh, j1 - j0, a.dim);
+    kl.to_right(lds[0], 0, at, k);
+    kl.load(a.v, s.begin + j0, kh, j1 - j0, a.dim);
+    kl.to_right(lds[1], 0, at, v);
   }
+  const float c = a.scale * kLog2e;
+  f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
+  int by = 0;
+  bool some = false;
+  // the next step's rows are not loaded ahead: most have one or two, and there is no register over
+  for (int r0 = j0 * a.group; r0 < rows; r0 += 32) {
+    load(r0);
+    if (uniform(first) >= j1) break;  // candidates from here on begin after the last key
+    bool odd = false;
+    Rows::W::wave_sync();
+#pragma unroll
+    for (int n = 0; n < Rows::W::kRegs; ++n) {
+      const int idx = lane + n * 64, to = Tile::at(idx / Tile::kPieces, idx % Tile::kPieces);
+      *reinterpret_cast<u32x4*>(lds[0] + to) = only_finite<T>(ql.r[n], odd);
+      *reinterpret_cast<u32x4*>(lds[1] + to) = only_finite<T>(dl.r[n], odd);
+    }
+    if (lane < 32) {
+      lses[lane] = lse;
+      deltas[lane] = delta;
+      firsts[lane] = first;
+      toks[lane] = tok;
+    }
+    const bool any_odd = __any(odd);
+    Rows::W::wave_sync();
+    if (any_odd) {
+      for (int i = 0; i < min(32, rows - r0); ++i) {
+        const Row x = row_at(a, r0 + i);
+        const bool see = j >= firsts[i] && j <= toks[i];
+        add_odd_row<T, DH>(row_ptr<const T>(a.q, s.begin, h0, x), a.dim, see, true, dk);
+        add_odd_row<T, DH>(row_ptr<const T>(a.dout, s.begin, h0, x), a.dim, see, false, dv);
+      }
+    }
+    f32x16 sc = {}, dp = {};
+#pragma unroll
+    for (int ks = 0; ks < DH / 16; ++ks) {
+      sc = mma(left<T>(lds[0], at, 0, ks), k[ks], sc);
+      dp = mma(left<T>(lds[1], at, 0, ks), v[ks], dp);
+    }
+    f32x16 p, ds;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int i = 8 * g + 4 * (lane >> 5);
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const f32x4 l4 = *reinterpret_cast<const f32x4*>(&lses[i]), d4 = *reinterpret_cast<const f32x4*>(&deltas[i]);
+      const i32x4 f4 = *reinterpret_cast<const i32x4*>(&firsts[i]), t4 = *reinterpret_cast<const i32x4*>(&toks[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -l4[e]));
+        const bool seen = j >= f4[e] && j <= t4[e];
+        p[4 * g + e] = seen ? x : 0.f;
+        ds[4 * g + e] = seen ? x * (dp[4 * g + e] - d4[e]) : 0.f;
+      }
+    }
+    fit_if<T>(ds, dk, by, some);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const V8 pb = right_of<T>(p, 8 * x), dsb = right_of<T>(ds, 8 * x);
+#pragma unroll
+      for (int db = 0; db < DH / 32; ++db) {
+        dv[db] = mma(left_t<T>(lds[1], at, 16 * x, db), pb, dv[db]);
+        dk[db] = mma(left_t<T>(lds[0], at, 16 * x, db), dsb, dk[db]);
+      }
+    }
+  }
+  if constexpr (std::is_same<T, _Float16>::value) {
+    if (some) unfit(dk, by);
+  }
+  Rows::W::store(a.dk, s.begin + j0, kh, j1 - j0, a.dim, lds[0], 0, dk, a.scale, 0);
+  Rows::W::store(a.dv, s.begin + j0, kh, j1 - j0, a.dim, lds[1], 0, dv, 1.f, 0);
 }
 
 // ---------------------------------------------------------------- launches
@@ -645,60 +788,87 @@ bool direct(const SharedArgs& a, int width, std::initializer_list<const EmbHeads
   }
   return a.dim == width;
 }
-// Rows of a request, on average, from which 128 rows a workgroup are the better shape of dq.
-bool few_rows(const SharedArgs& a) { return a.n_tok * a.group <= 48 * (int64_t)a.n_seq; }
-int64_t dq_slots(const SharedArgs& a) { return a.n_tok * a.group / (few_rows(a) ? 32 : 128) + a.n_seq; }
+int64_t dq_slots(const SharedArgs& a, const SharedBwdPlan& p) { return a.n_tok * a.group / p.rows + a.n_seq; }
 int64_t hist_slots(const SharedArgs& a) { return a.n_hist / 128 + a.n_seq; }
-int64_t own_slots(const SharedArgs& a) { return a.n_tok / 128 + a.n_seq; }
-int64_t self_threads(const SharedArgs& a) { return (a.n_tok * a.kv_heads * (a.dim / 8) + 255) / 256 * 256; }
+int64_t own_slots(const SharedArgs& a) { return a.n_tok / 32 + a.n_seq; }
+int64_t join_blocks(const SharedArgs& a, const SharedBwdPlan& p) {
+  return p.splits > 1 ? (a.n_tok * a.q_heads * (a.dim / 4) + 255) / 256 : 0;
+}
+int64_t self_blocks(const SharedArgs& a) {
+  return a.own == kOwnSelf ? (a.n_tok * a.kv_heads * (a.dim / 8) + 255) / 256 : 0;
+}
 
 template <typename T, int DH, bool DIRECT, bool TILES>
-hipError_t go(const SharedArgs& a, hipStream_t st) {
-  if (a.n_tok > 0) {
-    const dim3 grid((unsigned)(dq_slots(a) * a.kv_heads));
-    if (few_rows(a)) hipLaunchKernelGGL((shared_dq_few<T, DH, TILES>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((shared_dq<T, DH, DIRECT, TILES>), grid, dim3(256), 0, st, a);
-  }
+hipError_t go(const SharedArgs& a, const SharedBwdPlan& p, hipStream_t st) {
   // a launch that fails is the last one: what comes after it would read what it did not write
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (a.n_tok > 0) {
+    const dim3 grid((unsigned)(dq_slots(a, p) * a.kv_heads * p.splits));
+    if (p.rows == 32) hipLaunchKernelGGL((shared_dq_few<T, DH, TILES>), grid, dim3(256), 0, st, a, p.splits, p.unit);
+    else hipLaunchKernelGGL((shared_dq<T, DH, DIRECT, TILES>), grid, dim3(256), 0, st, a, p.splits, p.unit);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const dim3 threads(DkvTiles<T, DH, DIRECT>::kThreads);
   if (a.n_hist > 0) {
-    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT, false>), dim3((unsigned)(hist_slots(a) * a.kv_heads)), threads, 0, st,
+    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT>), dim3((unsigned)(hist_slots(a) * a.kv_heads)), threads, 0, st,
                        a);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.n_tok == 0) return e;
   if (TILES) {
-    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT, true>), dim3((unsigned)(own_slots(a) * a.kv_heads)), threads, 0, st, a);
-  } else {
-    hipLaunchKernelGGL((shared_self<T>), dim3((unsigned)(self_threads(a) / 256)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((shared_dkv_own<T, DH>), dim3((unsigned)(own_slots(a) * a.kv_heads)), dim3(64), 0, st, a);
+    e = hipGetLastError();
   }
-  return hipGetLastError();
+  const int64_t join = join_blocks(a, p), self = self_blocks(a);
+  if (e == hipSuccess && join + self > 0) {
+    hipLaunchKernelGGL((shared_finish<T, !TILES>), dim3((unsigned)(join + self)), dim3(256), 0, st, a, p.splits,
+                       (int)join);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
 
-SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_tok) {
+SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t n_hist) {
   SharedBwdPlan p{};
-  p.off_self = ((size_t)n_tok * a.q_heads * sizeof(float) + 255) & ~(size_t)255;
-  p.bytes = p.off_self + 2 * (size_t)n_tok * a.q_heads * sizeof(float);
+  const int64_t group = a.q_heads / a.kv_heads, seen = (int64_t)a.window + a.sinks;
+  n_seq = std::max<int64_t>(n_seq, 1);
+  const int64_t mean = (n_hist + n_seq - 1) / n_seq, most = std::min(4 * mean, n_hist);
+  const auto slots = [&](int64_t rows) {
+    return std::max<int64_t>(std::max(n_tok * group / rows, n_seq) * a.kv_heads, 1);
+  };
+  p.rows = by_32_rows(n_tok * group, n_seq, slots(32), mean) ? 32 : 128;
+  const int64_t base = slots(p.rows), least = p.rows == 128 && base >= 128 ? 16 : 8;
+  const int tile = p.rows == 32 ? 32 : 64;
+  SharedPlan whole{p.rows, 4, 1, 1, 0}, with = whole;
+  share_out(whole, base, (mean + tile - 1) / tile, (most + tile - 1) / tile, 768, least);
+  share_out(with, base, (std::min(mean, seen) + tile - 1) / tile, (std::min(most, seen) + tile - 1) / tile, 768, least);
+  p.splits = std::min(whole.splits, with.splits);  // what is enough without a window is enough with one
+  p.unit = with.unit;
+  const size_t rows = (size_t)n_tok * a.q_heads;
+  const auto room = [](size_t bytes) { return (bytes + 255) & ~(size_t)255; };
+  p.off_self = room(rows * sizeof(float));
+  p.off_part = p.off_self + room(2 * rows * sizeof(float));
+  p.bytes = p.off_part;
+  if (p.splits > 1) p.bytes += rows * (p.splits * (size_t)(a.dim + 2) + 1) * sizeof(float);
   return p;
 }
 
-int64_t shared_bwd_threads(const SharedArgs& a) {
-  const int64_t dkv = std::max(hist_slots(a), own_slots(a)) * a.kv_heads * (a.dim <= 64 ? 256 : 512);
-  return std::max({dq_slots(a) * a.kv_heads * 256, dkv, self_threads(a)});
+int64_t shared_bwd_threads(const SharedArgs& a, const SharedBwdPlan& p) {
+  const int64_t dkv = hist_slots(a) * a.kv_heads * (a.dim <= 64 ? 256 : 512);
+  return std::max({dq_slots(a, p) * a.kv_heads * p.splits * 256, dkv, own_slots(a) * a.kv_heads * 64, (join_blocks(a, p) + self_blocks(a)) * 256});
 }
 
-hipError_t launch_shared_bwd(const SharedArgs& a, hipStream_t st) {
+hipError_t launch_shared_bwd(const SharedArgs& a, const SharedBwdPlan& p, hipStream_t st) {
   auto by_width = [&](auto t) {
     typedef decltype(t) T;
     auto by_tiles = [&](auto d) {
       constexpr int DH = decltype(d)::value;
       const bool straight = direct(a, DH, {&a.q, &a.k, &a.v, &a.dout, &a.hk, &a.hv});
-      if (a.own == kOwnTiles) return straight ? go<T, DH, true, true>(a, st) : go<T, DH, false, true>(a, st);
-      return straight ? go<T, DH, true, false>(a, st) : go<T, DH, false, false>(a, st);
+      if (a.own == kOwnTiles) return straight ? go<T, DH, true, true>(a, p, st) : go<T, DH, false, true>(a, p, st);
+      return straight ? go<T, DH, true, false>(a, p, st) : go<T, DH, false, false>(a, p, st);
     };
     return a.dim <= 32   ? by_tiles(std::integral_constant<int, 32>{})
            : a.dim <= 64 ? by_tiles(std::integral_constant<int, 64>{})

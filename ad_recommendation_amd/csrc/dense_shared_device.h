@@ -2,6 +2,8 @@
 // query rows meet, rows of (token, head of the group), and history in 8 bits.
 #pragma once
 
+#include <algorithm>
+
 #include "dense_attn_device.h"
 
 namespace emb {
@@ -88,6 +90,25 @@ struct HistoryTiles {
 // A request's tiles of keys may go to several workgroups: as many as leave each `unit` tiles, at most `splits`. Their
 // sums go to memory in fp32, [split][token][q head][dim], and a second kernel adds them; a row's count of them
 // follows behind all sums and statistics.
+// Whether 32 rows a workgroup are the better shape: where that is little work in all, or requests have very few
+// rows.  us of the forward, 8 and 2 heads of 64, bf16, caches of up to the last figure: 1 request of 64 candidates,
+// 1000: 11.2 by 32 rows, 13.0 by 128; 64 of up to 16, 1000: 13.9 and 17.2; 8 of up to 64, 4000: 22.5 and 18.5; 256 of
+// up to 16, 400: 20.1 and 17.5, of up to 4, 100: 9.2 and 9.9.
+inline bool by_32_rows(int64_t rows, int64_t n_seq, int64_t groups, int64_t hist) {
+  constexpr int64_t kLittle = 2048;  // tiles of 32 rows and keys
+  return (groups <= 256 && groups * ((hist + 31) / 32) <= kLittle) || (rows <= 16 * n_seq && hist <= 1024);
+}
+// How a request's keys are shared out: over so many workgroups that there are about `want`, each of `least` tiles
+// at least; a request's last part is half one on average.  Not where the longest requests, taken to be of twice the mean,
+// would have hardly fewer tiles a workgroup: the join is a launch.
+inline void share_out(SharedPlan& p, int64_t base, int64_t tiles, int64_t most, int64_t want, int64_t least) {
+  if (base >= want) return;
+  const int64_t parts = want - base / 2, unit = std::max(least, (base * tiles + parts - 1) / parts);
+  if (2 * tiles - unit < 8) return;
+  p.unit = (int32_t)unit;
+  p.splits = (int32_t)std::clamp<int64_t>((most + unit - 1) / unit, 1, 4096);
+}
+
 struct Share {
   int count, first, end;  // workgroups that share; this one's tiles
 };
@@ -116,18 +137,15 @@ __device__ __forceinline__ int first_of(const SharedArgs& a, const Seq& s, int t
   return (int)min(max(f, (int64_t)0), (int64_t)tok);
 }
 
-// Sets x[r] to `hidden` where key j0 + row_of(r) is not one of lo to hi; a bit for each register whose key is.
+// Sets x[r] to `hidden` where key j0 + row_of(r) is not one of lo to hi.
 template <int AGAIN = 0>
-__device__ __forceinline__ uint32_t hide_outside(int lo, int hi, int j0, f32x16& x, float hidden) {
+__device__ __forceinline__ void hide_outside(int lo, int hi, int j0, f32x16& x, float hidden) {
   const int d = j0 + 4 * (lane_id<AGAIN>() >> 5);
-  uint32_t see = 0;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     const int j = d + 8 * (r >> 2) + (r & 3);
-    if (j >= lo && j <= hi) see |= 1u << r;
-    else x[r] = hidden;
+    if (j < lo || j > hi) x[r] = hidden;
   }
-  return see;
 }
 // The same of the keys from `end` on, of which few tiles have any; see hide_keys.
 __device__ __forceinline__ void hide_from(int end, int j0, f32x16& x, float hidden) {
@@ -205,22 +223,44 @@ struct PackedRows : WaveRows<T, DH, TILE, AGAIN> {
   }
 };
 
-// A token's own key or value in the layout of a result's column: four elements at a time.
-template <typename T, int DH, int AGAIN = 0>
-__device__ __forceinline__ void column(const T* p, bool live, int D, f32x16 (&x)[DH / 32]) {
+// What is not finite in tiles of own tokens.  A product adds 0 * x for a pair that does not see each other, which is NaN
+// where x is not finite.  So those elements of the operand whose rows are summed over come to LDS as zeros, and where a
+// tile has any, each of its rows adds them to the sums that see it (a lane has one, as a column): as they are, or as
+// NaN where the weight's sign may be any.  (The scores of such a row are not finite anyway: its lse or delta is not.)
+template <typename T>
+__device__ __forceinline__ u32x4 only_finite(u32x4 x, bool& odd) {
+  const i16x8 o = odd_of<T>(__builtin_bit_cast(typename Vec8<T>::t, x));
+  const u32x4 some = __builtin_bit_cast(u32x4, o);
+  odd |= (some[0] | some[1] | some[2] | some[3]) != 0;
+  return x & ~some;
+}
+template <typename T, int DH>
+__device__ __forceinline__ void add_odd_row(const T* p, int D, bool see, bool nan, f32x16 (&x)[DH / 32]) {
   typedef T V __attribute__((ext_vector_type(4)));
 #pragma unroll
   for (int db = 0; db < DH / 32; ++db) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int col = db * 32 + 8 * g + 4 * (lane_id<AGAIN>() >> 5);
+      const int col = db * 32 + 8 * g + 4 * (lane_id<2>() >> 5);
       f32x4 v = {};
-      if (live && col < D) v = __builtin_convertvector(*reinterpret_cast<const V*>(p + col), f32x4);
+      if (col < D) v = __builtin_convertvector(*reinterpret_cast<const V*>(p + col), f32x4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[db][4 * g + e] = v[e];
+      for (int e = 0; e < 4; ++e)
+        if (see && !(fabsf(v[e]) < kInf)) x[db][4 * g + e] += nan ? __builtin_nanf("") : v[e];
     }
   }
 }
+
+// The same of keys or values of own tokens j0 to j1 - 1, of which a row sees lo to hi.
+template <typename T, int DH>
+__device__ __forceinline__ void add_odd_own(const SharedArgs& a, const EmbHeads& t, int64_t begin, int kh, int j0, int j1,
+                                            int lo, int hi, bool nan, f32x16 (&x)[DH / 32]) {
+  for (int j = j0; j < j1; ++j) {
+    const T* p = static_cast<const T*>(t.p) + (begin + j) * t.tok + kh * t.head;
+    add_odd_row<T, DH>(p, a.dim, j >= lo && j <= hi, nan, x);
+  }
+}
+
 // The product of a lane's row, as right operands, with a row at p; in both halves' lanes.
 template <typename T, int DH, int AGAIN = 0>
 __device__ __forceinline__ float dot_row(const typename Vec8<T>::t (&f)[DH / 16], const T* p, bool live, int D) {
