@@ -53,7 +53,7 @@ template <typename T, int DH>
 __device__ __forceinline__ void meet_self(const SharedArgs& a, int64_t tok, int kh, bool live,
                                           const typename Vec8<T>::t (&q)[DH / 16], float c, f32x16 (&o)[DH / 32],
                                           float& m, float& l) {
-  const float s = dot_row<T, DH, 3>(q, static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head, live, a.dim);
+  const float s = dot_row<T, DH>(q, static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head, live, a.dim);
   if (!live || s == -kInf) return;
   const float mn = fmaxf(m, s), by = m == -kInf ? 0.f : exp2f((m - mn) * c), p = exp2f((s - mn) * c);
   m = mn;
@@ -272,21 +272,67 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
 }
 
 // ---------------------------------------------------------------- 32 rows
-// The waves' tiles come through registers, the next one under way while one is computed.
+// A wave's 32 keys or values on their way to LDS, 16 bytes a load, whole rows next to each other.  (With half a row a
+// lane, which keys could stay in as a left operand, each load meets 32 rows: 256 caches 559 us instead of 355.)
+template <typename T, int DH, bool CODES>
+struct WaveTile {
+  typedef std::conditional_t<CODES, uint8_t, T> H;
+  typedef RegisterTile<T, DH, 32, 64> Tile;
+  static constexpr int kEach = 16 / sizeof(H), kPieces = DH / kEach, kLoads = kPieces / 2;  // 64 lanes, 32 rows
+  u32x4 r[kLoads];
+  __device__ __forceinline__ void load(const H* p, int64_t stride, int row0, int end, int D) {
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int idx = lane_id() + n * 64, row = row0 + idx / kPieces, col = idx % kPieces * kEach;
+      r[n] = u32x4{0, 0, 0, 0};
+      if (row >= end) continue;
+      if (col + kEach <= D) {
+        r[n] = *reinterpret_cast<const u32x4*>(p + row * stride + col);
+      } else if (CODES && col < D) {  // eight columns
+        const u32x2 x = *reinterpret_cast<const u32x2*>(p + row * stride + col);
+        r[n] = u32x4{x[0], x[1], 0, 0};
+      }
+    }
+  }
+  // exp: in 8 bits, the exponent of row (lane % 32); first: the lane that has row 0's.
+  __device__ __forceinline__ void store(char* lds, uint32_t exp, int first) const {
+    typedef typename Vec8<T>::t V8;
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int idx = lane_id() + n * 64, row = idx / kPieces, piece = idx % kPieces;
+      if constexpr (CODES) {
+        const uint32_t e = __builtin_amdgcn_ds_bpermute((first + row) * 4, exp);
+        *reinterpret_cast<V8*>(lds + Tile::at(row, 2 * piece)) = of_codes<T>(u32x2{r[n][0], r[n][1]}, e);
+        *reinterpret_cast<V8*>(lds + Tile::at(row, 2 * piece + 1)) = of_codes<T>(u32x2{r[n][2], r[n][3]}, e);
+      } else {
+        *reinterpret_cast<u32x4*>(lds + Tile::at(row, piece)) = r[n];
+      }
+    }
+  }
+};
+
+// Bound by a wave's chain of loads and products where there are few workgroups, so DEPTH tiles a wave are under way
+// where registers hold two; by reading the cache where there are many: 256 caches of up to 8192 in 8 bits, 32 and 8
+// heads of 128, window 4096: TODO.
 template <typename T, int DH, int WAVES, bool CODES, bool TILES>
-__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow(SharedArgs a, int splits, int unit) {
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow(SharedArgs a, int splits, int unit, int places) {
   typedef typename Vec8<T>::t V8;
   typedef RegisterTile<T, DH, 32, 64> Tile;
-  constexpr int kRegs = Tile::kRegs, kPieces = Tile::kPieces;
+  typedef WaveTile<T, DH, CODES> Wave;
+  constexpr int kDepth = CODES || DH == 32 || (DH == 64 && WAVES == 4) ? 2 : 1;
   __shared__ __attribute__((aligned(16))) char lds[WAVES][2][Tile::kBytes];
   __shared__ float stats[WAVES][2][32];
-  int block = blockIdx.x;
-  const int kh = block % a.kv_heads;
-  block /= a.kv_heads;
-  const int split = block % splits;
-  const Seq s = find_rows<32>(a, block / splits);
+  // A request's heads, which lie next to each other in memory, go to the same one of the GPU's eight parts.
+  const int part = blockIdx.x / 8, kh = part % a.kv_heads, place = part / a.kv_heads * 8 + blockIdx.x % 8;
+  if (place >= places) return;
+  const int split = place % splits;
+  const Seq s = find_rows<32>(a, place / splits);
   const int rows = s.len * a.group;
   if (s.tile < 0 || (int64_t)s.tile * 32 >= rows) return;
+  const History hist = history(a, s.index);
+  const HistoryTiles<32> tiles(hist);
+  const Share share = share_of(tiles.total, splits, unit, split);
+  if (split >= share.count) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
   const int r0 = s.tile * 32, h0 = kh * a.group, last = min(r0 + 32, rows) - 1;
   const int r = r0 + (lane & 31);
@@ -294,41 +340,29 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
   const Row row = row_at(a, live ? r : last);
   const int64_t tok = s.begin + row.tok;
 
-  V8 q[DH / 16];
-  right_row<T, DH>(a.q, tok, h0 + row.g, live && a.scale != 0.f, a.dim, q);
-  const History hist = history(a, s.index);
-  const HistoryTiles<32> tiles(hist);
-  const Share share = share_of(tiles.total, splits, unit, split);
-  if (split >= share.count) return;
-  const int it0 = share.first, it1 = share.end;
-
-  typedef std::conditional_t<CODES, uint8_t, T> H;
-  typedef std::conditional_t<CODES, u32x2, u32x4> Piece;
+  typedef typename Wave::H H;
   const H* hk = history_of<H>(a, a.hk, hist, s.index, kh);
   const H* hv = history_of<H>(a, a.hv, hist, s.index, kh);
   const uint8_t* ke = CODES ? history_of<uint8_t>(a, a.ke, hist, s.index, kh) : nullptr;
   const uint8_t* ve = CODES ? history_of<uint8_t>(a, a.ve, hist, s.index, kh) : nullptr;
-  Piece kr[kRegs], vr[kRegs];
-  uint32_t kx[CODES ? kRegs : 1], vx[CODES ? kRegs : 1];
-  auto load = [&](int it) {
+  Wave kr[kDepth], vr[kDepth];
+  uint32_t exps[kDepth];  // of the lower half's lanes a key's, of the upper's a value's
+  auto load = [&](int it, int n) {
+    if (it >= share.end) return;
     const int j0 = tiles.key0(it), end = tiles.end(it);
-#pragma unroll
-    for (int n = 0; n < kRegs; ++n) {
-      const int idx = lane + n * 64, j = j0 + idx / kPieces, cl = idx % kPieces * 8;
-      kr[n] = vr[n] = Piece{};
-      if (CODES) kx[n] = vx[n] = 0;
-      if (j < end && cl < a.dim) {
-        kr[n] = *reinterpret_cast<const Piece*>(hk + j * a.hk.tok + cl);
-        vr[n] = *reinterpret_cast<const Piece*>(hv + j * a.hv.tok + cl);
-        if (CODES) {
-          kx[n] = ke[j * a.ke.tok];
-          vx[n] = ve[j * a.ve.tok];
-        }
-      }
+    kr[n].load(hk, a.hk.tok, j0, end, a.dim);
+    vr[n].load(hv, a.hv.tok, j0, end, a.dim);
+    if (CODES) {
+      const int j = j0 + (lane & 31);
+      exps[n] = 0;
+      if (j < end) exps[n] = lane < 32 ? ke[j * a.ke.tok] : ve[j * a.ve.tok];
     }
   };
-  int it = it0 + wave;
-  if (it < it1) load(it);
+  const int it0 = share.first + wave;
+#pragma unroll
+  for (int n = 0; n < kDepth; ++n) load(it0 + n * WAVES, n);
+  V8 q[DH / 16];
+  right_row<T, DH>(a.q, tok, h0 + row.g, live && a.scale != 0.f, a.dim, q);
   if (a.scale < 0.f) {
 #pragma unroll
     for (int ks = 0; ks < DH / 16; ++ks) q[ks] = -q[ks];
@@ -337,43 +371,39 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
   f32x16 o[DH / 32] = {};
   float m = -kInf, l = 0.f;
   const typename Tile::Reads at;
-  char* kt = lds[wave][0];
-  char* vt = lds[wave][1];
-  for (; it < it1; it += WAVES) {
-#pragma unroll
-    for (int n = 0; n < kRegs; ++n) {
-      const int idx = lane + n * 64, to = Tile::at(idx / kPieces, idx % kPieces);
-      if constexpr (CODES) {
-        *reinterpret_cast<V8*>(kt + to) = of_codes<T>(kr[n], kx[n]);
-        *reinterpret_cast<V8*>(vt + to) = of_codes<T>(vr[n], vx[n]);
-      } else {
-        *reinterpret_cast<u32x4*>(kt + to) = kr[n];
-        *reinterpret_cast<u32x4*>(vt + to) = vr[n];
-      }
-    }
-    if (it + WAVES < it1) load(it + WAVES);
+  char* const kt = lds[wave][0];
+  char* const vt = lds[wave][1];
+  auto meet = [&](int it, int n) {
+    kr[n].store(kt, exps[n], 0);
+    vr[n].store(vt, exps[n], 32);
+    load(it + kDepth * WAVES, n);
     // the tile is the wave's own: its LDS accesses are carried out in order
     WaveRows<T, DH, Tile>::wave_sync();
     f32x16 sc[1] = {};
 #pragma unroll
     for (int ks = 0; ks < DH / 16; ++ks) sc[0] = mma(left<T>(kt, at, 0, ks), q[ks], sc[0]);
-    const int n = tiles.end(it) - tiles.key0(it);
-    if (n < 32) hide_from(n, 0, sc[0], -kInf);
+    const int keys = tiles.end(it) - tiles.key0(it);
+    if (keys < 32) hide_from(keys, 0, sc[0], -kInf);
     soften(sc, o, m, l, c);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const V8 pb = right_of<T>(sc[0], 8 * k);
+    for (int x = 0; x < 2; ++x) {
+      const V8 pb = right_of<T>(sc[0], 8 * x);
 #pragma unroll
-      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(vt, at, 16 * k, db), pb, o[db]);
+      for (int db = 0; db < DH / 32; ++db) o[db] = mma(left_t<T>(vt, at, 16 * x, db), pb, o[db]);
     }
     WaveRows<T, DH, Tile>::wave_sync();
+  };
+  for (int it = it0; it < share.end; it += kDepth * WAVES) {
+    meet(it, 0);
+    if (kDepth == 2 && it + WAVES < share.end) meet(it + WAVES, kDepth - 1);
   }
   if (split == share.count - 1) {
     if constexpr (!TILES) {
       if (a.own == kOwnSelf && wave == 0) meet_self<T, DH>(a, tok, kh, live, q, c, o, m, l);
     } else {
       typedef WaveRows<T, DH, Tile, 3> OwnRows;
-      const typename RegisterTile<T, DH, 32, 64, 3>::Reads own_at;
+      typedef RegisterTile<T, DH, 32, 64, 3> OwnTile;
+      const typename OwnTile::Reads own_at;
       const int lo = first_of(a, s, row.tok), end = uniform(row_at(a, last).tok) + 1;
       for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)) + 32 * wave; j0 < end; j0 += 32 * WAVES) {
         OwnRows::wave_sync();
@@ -382,12 +412,13 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
           OwnRows rows_;
           rows_.load(x ? a.v : a.k, s.begin + j0, kh, end - j0, a.dim);
 #pragma unroll
-          for (int n = 0; n < kRegs; ++n) {
+          for (int n = 0; n < OwnRows::kRegs; ++n) {
             const int idx = lane_id<3>() + n * 64;
             bool its = false;
             const u32x4 fine = only_finite<T>(rows_.r[n], its);
             if (x) odd |= its;
-            *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = x ? fine : rows_.r[n];
+            *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / Tile::kPieces, idx % Tile::kPieces)) =
+                x ? fine : rows_.r[n];
           }
         }
         OwnRows::wave_sync();
@@ -648,19 +679,24 @@ static int64_t join_threads(const SharedArgs& a, const SharedPlan& p) {
   const int64_t rows = a.n_tok * a.q_heads;
   return join_by_groups(a, p) ? rows * 256 : (rows * (a.dim / 4) + 255) / 256 * 256;
 }
+// Workgroups of 32 rows: places in rounds of eight, each of every key/value head.
+static int64_t narrow_groups(const SharedArgs& a, const SharedPlan& p) {
+  return (slots(a, 32) * p.splits + 7) / 8 * 8 * a.kv_heads;
+}
 // Threads of a call's largest launch.
 int64_t shared_threads(const SharedArgs& a, const SharedPlan& p) {
-  const int64_t groups = slots(a, p.rows) * a.kv_heads * p.splits;
+  const int64_t groups = p.rows == 32 ? narrow_groups(a, p) : slots(a, p.rows) * a.kv_heads * p.splits;
   return std::max(groups * (p.rows == 128 ? 256 : 64 * p.waves), p.splits > 1 ? join_threads(a, p) : 0);
 }
 
 template <typename T, int DH, bool CODES>
-void go_narrow(const SharedArgs& a, const SharedPlan& p, dim3 grid, hipStream_t st) {
+void go_narrow(const SharedArgs& a, const SharedPlan& p, hipStream_t st) {
+  const dim3 grid((unsigned)(narrow_groups(a, p)));
   constexpr int kMost = DH <= 64 ? 16 : 8;
   auto go = [&](auto waves, auto tiles) {
     constexpr int WAVES = decltype(waves)::value;
     hipLaunchKernelGGL((shared_narrow<T, DH, WAVES, CODES, decltype(tiles)::value>), grid, dim3(64 * WAVES), 0, st, a,
-                       p.splits, p.unit);
+                       p.splits, p.unit, (int)(slots(a, 32) * p.splits));
   };
   auto by_own = [&](auto waves) {
     if (a.own == kOwnTiles) go(waves, std::true_type{});
@@ -685,8 +721,8 @@ hipError_t launch_shared(const SharedArgs& a, const SharedPlan& p, bool q8, hipS
         else if (direct(a, DH)) wide(std::integral_constant<int, kDirect>{});
         else wide(std::integral_constant<int, kByRegisters>{});
       } else {
-        if (q8) go_narrow<T, DH, true>(a, p, grid, st);
-        else go_narrow<T, DH, false>(a, p, grid, st);
+        if (q8) go_narrow<T, DH, true>(a, p, st);
+        else go_narrow<T, DH, false>(a, p, st);
       }
     });
     e = hipGetLastError();

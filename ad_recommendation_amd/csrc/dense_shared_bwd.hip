@@ -85,9 +85,9 @@ __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh
   const T* kp = static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + tok * a.v.tok + kh * a.v.head;
   asm volatile("" ::: "memory");  // one row after the other: the registers are full
-  const float s = dot_row<T, DH, 3>(w.q, kp, live, a.dim);
+  const float s = dot_row<T, DH>(w.q, kp, live, a.dim);
   asm volatile("" ::: "memory");
-  const float dp = dot_row<T, DH, 3>(w.d, vp, live, a.dim);
+  const float dp = dot_row<T, DH>(w.d, vp, live, a.dim);
   if (!live) return;
   const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -w.lse)), ds = p * (dp - w.delta), x = ldexpf(ds, -by);
   const int64_t at = (int64_t)qh * a.n_tok + tok;

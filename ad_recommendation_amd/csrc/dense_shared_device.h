@@ -262,12 +262,12 @@ __device__ __forceinline__ void add_odd_own(const SharedArgs& a, const EmbHeads&
 }
 
 // The product of a lane's row, as right operands, with a row at p; in both halves' lanes.
-template <typename T, int DH, int AGAIN = 0>
+template <typename T, int DH>
 __device__ __forceinline__ float dot_row(const typename Vec8<T>::t (&f)[DH / 16], const T* p, bool live, int D) {
   float s = 0.f;
 #pragma unroll
   for (int ks = 0; ks < DH / 16; ++ks) {
-    const int col = ks * 16 + (lane_id<AGAIN>() >> 5) * 8;
+    const int col = ks * 16 + (lane_id<3>() >> 5) * 8;
     typename Vec8<T>::t x = {};
     if (live && col < D) x = *reinterpret_cast<const typename Vec8<T>::t*>(p + col);
 #pragma unroll
