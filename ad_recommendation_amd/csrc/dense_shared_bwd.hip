@@ -644,37 +644,27 @@ struct HistoryBatch {  // of find_tile
 template <int DH>
 constexpr int dkv_waves = DH == 32 ? 3 : 2;
 
-template <typename T, int DH, bool DIRECT>
-__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), (dkv_waves<DH>)) shared_dkv(SharedArgs a) {
-  __shared__ __attribute__((aligned(1024))) DkvTiles<T, DH, DIRECT> sh;
-  constexpr int kTokens = 128;
-  const int kh = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
-  const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot,
-                                  [](int64_t t, int b) { return t / kTokens + b; }));
-  if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
-  const History hist = history(a, h.index);
-  Seq s = uniform(sequence(a, h.index, 0));
-  const int j0 = h.tile * kTokens;
-  // a tile that no row sees has none
-  if (j0 >= hist.sinks && j0 + kTokens <= hist.first) s.len = 0;
-  dkv<T, DH, DIRECT>(a, sh, s, hist, kh, j0, min(j0 + kTokens, hist.n));
-}
-
 // dk and dv of own tokens, where candidates have more than one: a wave has 32 of them for a key/value head and
 // meets the rows from there to the end of the last one's candidate, 32 a step.  Candidates are short, and so is this; a
-// workgroup of four waves, 128 tokens and 64 rows a step took 90 us where this takes TODO (200 requests of up to
-// 120 tokens, candidates of 3, 8 heads of 64).
+// workgroup of four waves, 128 tokens and 64 rows a step took 90 us where this takes 30 (200 requests of up to 120
+// tokens, candidates of 3, 8 heads of 64).
 template <typename T, int DH>
-__global__ void __launch_bounds__(64, (DH == 128 ? 1 : 2)) shared_dkv_own(SharedArgs a) {
+struct OwnTiles {
+  char tile[2][RegisterTile<T, DH, 32, 64>::kBytes];
+  float lse[32], delta[32];
+  int first[32], tok[32];
+};
+template <typename T, int DH>
+__device__ __forceinline__ void dkv_own(const SharedArgs& a, OwnTiles<T, DH>& sh, int kh, int slot) {
   typedef typename Vec8<T>::t V8;
   typedef RegisterTile<T, DH, 32, 64> Tile;
   typedef PackedRows<T, DH, Tile> Rows;
   constexpr int kTokens = 32;
-  __shared__ __attribute__((aligned(256))) char lds[2][Tile::kBytes];
-  __shared__ float lses[32], deltas[32];
-  __shared__ int firsts[32], toks[32];
-  const int kh = blockIdx.x % a.kv_heads, h0 = kh * a.group, lane = lane_id();
-  const Seq s = uniform(find_tile(a, blockIdx.x / a.kv_heads, [](int64_t t, int b) { return t / kTokens + b; }));
+  char(&lds)[2][Tile::kBytes] = sh.tile;
+  float *const lses = sh.lse, *const deltas = sh.delta;
+  int *const firsts = sh.first, *const toks = sh.tok;
+  const int h0 = kh * a.group, lane = lane_id();
+  const Seq s = uniform(find_tile(a, slot, [](int64_t t, int b) { return t / kTokens + b; }));
   if (s.tile < 0 || (int64_t)s.tile * kTokens >= s.len) return;
   const int j0 = s.tile * kTokens, j1 = min(j0 + kTokens, s.len), j = j0 + (lane & 31), rows = s.len * a.group;
   const typename Tile::Reads at;
@@ -778,6 +768,34 @@ __global__ void __launch_bounds__(64, (DH == 128 ? 1 : 2)) shared_dkv_own(Shared
   Rows::W::store(a.dv, s.begin + j0, kh, j1 - j0, a.dim, lds[1], 0, dv, 1.f, 0);
 }
 
+// TILES: the first own_blocks workgroups have own tokens, each wave 32 of its own; one launch, so that those, which
+// wait for memory most of the time, run beside the histories.
+template <typename T, int DH, bool DIRECT, bool TILES>
+__global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), (dkv_waves<DH>))
+    shared_dkv(SharedArgs a, int own_blocks) {
+  typedef DkvTiles<T, DH, DIRECT> P;
+  constexpr int kOwn = TILES ? sizeof(OwnTiles<T, DH>) * P::kWaves : 0;
+  __shared__ __attribute__((aligned(1024))) char lds[kOwn > (int)sizeof(P) ? kOwn : sizeof(P)];
+  constexpr int kTokens = 128;
+  const int kv_heads = a.kv_heads;
+  if (TILES && (int)blockIdx.x < own_blocks) {
+    const int wave = uniform(threadIdx.x >> 6), unit = blockIdx.x * P::kWaves + wave;
+    dkv_own<T, DH>(a, reinterpret_cast<OwnTiles<T, DH>*>(lds)[wave], unit % kv_heads, unit / kv_heads);
+    return;
+  }
+  P& sh = *reinterpret_cast<P*>(lds);
+  const int block = blockIdx.x - own_blocks, kh = block % kv_heads, slot = block / kv_heads;
+  const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot,
+                                  [](int64_t t, int b) { return t / kTokens + b; }));
+  if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
+  const History hist = history(a, h.index);
+  Seq s = uniform(sequence(a, h.index, 0));
+  const int j0 = h.tile * kTokens;
+  // a tile that no row sees has none
+  if (j0 >= hist.sinks && j0 + kTokens <= hist.first) s.len = 0;
+  dkv<T, DH, DIRECT>(a, sh, s, hist, kh, j0, min(j0 + kTokens, hist.n));
+}
+
 // ---------------------------------------------------------------- launches
 // Whether tiles may be loaded straight to LDS: whole rows of the kernel's width, and a tile's rows
 // within 2^31 bytes of one another.
@@ -789,8 +807,10 @@ bool direct(const SharedArgs& a, int width, std::initializer_list<const EmbHeads
   return a.dim == width;
 }
 int64_t dq_slots(const SharedArgs& a, const SharedBwdPlan& p) { return a.n_tok * a.group / p.rows + a.n_seq; }
-int64_t hist_slots(const SharedArgs& a) { return a.n_hist / 128 + a.n_seq; }
-int64_t own_slots(const SharedArgs& a) { return a.n_tok / 32 + a.n_seq; }
+int64_t hist_slots(const SharedArgs& a) { return a.n_hist > 0 ? a.n_hist / 128 + a.n_seq : 0; }
+int64_t own_blocks(const SharedArgs& a, int waves) {
+  return a.n_tok > 0 ? ((a.n_tok / 32 + a.n_seq) * a.kv_heads + waves - 1) / waves : 0;
+}
 int64_t join_blocks(const SharedArgs& a, const SharedBwdPlan& p) {
   return p.splits > 1 ? (a.n_tok * a.q_heads * (a.dim / 4) + 255) / 256 : 0;
 }
@@ -809,17 +829,13 @@ hipError_t go(const SharedArgs& a, const SharedBwdPlan& p, hipStream_t st) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 threads(DkvTiles<T, DH, DIRECT>::kThreads);
-  if (a.n_hist > 0) {
-    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT>), dim3((unsigned)(hist_slots(a) * a.kv_heads)), threads, 0, st,
-                       a);
+  constexpr int kWaves = DkvTiles<T, DH, DIRECT>::kWaves;
+  const int64_t own = TILES ? own_blocks(a, kWaves) : 0, dkv = own + hist_slots(a) * a.kv_heads;
+  if (dkv > 0) {
+    hipLaunchKernelGGL((shared_dkv<T, DH, DIRECT, TILES>), dim3((unsigned)dkv), dim3(64 * kWaves), 0, st, a, (int)own);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.n_tok == 0) return e;
-  if (TILES) {
-    hipLaunchKernelGGL((shared_dkv_own<T, DH>), dim3((unsigned)(own_slots(a) * a.kv_heads)), dim3(64), 0, st, a);
-    e = hipGetLastError();
-  }
   const int64_t join = join_blocks(a, p), self = self_blocks(a);
   if (e == hipSuccess && join + self > 0) {
     hipLaunchKernelGGL((shared_finish<T, !TILES>), dim3((unsigned)(join + self)), dim3(256), 0, st, a, p.splits,
@@ -857,8 +873,10 @@ SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok, in
 }
 
 int64_t shared_bwd_threads(const SharedArgs& a, const SharedBwdPlan& p) {
-  const int64_t dkv = hist_slots(a) * a.kv_heads * (a.dim <= 64 ? 256 : 512);
-  return std::max({dq_slots(a, p) * a.kv_heads * p.splits * 256, dkv, own_slots(a) * a.kv_heads * 64, (join_blocks(a, p) + self_blocks(a)) * 256});
+  const int waves = a.dim <= 64 ? 4 : 8;
+  const int64_t own = a.own == kOwnTiles ? own_blocks(a, waves) : 0;
+  return std::max({dq_slots(a, p) * a.kv_heads * p.splits * 256, (own + hist_slots(a) * a.kv_heads) * 64 * waves,
+                   (join_blocks(a, p) + self_blocks(a)) * 256});
 }
 
 hipError_t launch_shared_bwd(const SharedArgs& a, const SharedBwdPlan& p, hipStream_t st) {
