@@ -145,18 +145,17 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
   int block = blockIdx.x;
   const int kh = block % a.kv_heads;
   block /= a.kv_heads;
-  const int split = block % splits;
-  const Seq s = find_rows<kTile>(a, block / splits);
-  const int rows = s.len * a.group;
-  if (s.tile < 0 || (int64_t)s.tile * kTile >= rows) return;
+  const Unit u = find_unit<kTile, kRows>(a, block, splits, unit);
+  if (u.none) return;
+  const Seq s = u.s;
+  const History hist = u.hist;
+  const Share share = u.share;
+  const int split = u.split, rows = s.len * a.group;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r0 = s.tile * kTile, rw = r0 + wave * 32, h0 = kh * a.group;
   const int last = min(r0 + kTile, rows) - 1;  // of the workgroup's rows
 
-  const History hist = history(a, s.index);
   const HistoryTiles<kRows> tiles(hist);
-  const Share share = share_of(tiles.total, splits, unit, split);
-  if (split >= share.count) return;
   const int it0 = share.first, it1 = share.end;
   typedef PackedRows<T, DH, Tile> Rows;
   Rows ql;
@@ -325,14 +324,13 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
   // A request's heads, which lie next to each other in memory, go to the same one of the GPU's eight parts.
   const int part = blockIdx.x / 8, kh = part % a.kv_heads, place = part / a.kv_heads * 8 + blockIdx.x % 8;
   if (place >= places) return;
-  const int split = place % splits;
-  const Seq s = find_rows<32>(a, place / splits);
-  const int rows = s.len * a.group;
-  if (s.tile < 0 || (int64_t)s.tile * 32 >= rows) return;
-  const History hist = history(a, s.index);
+  const Unit u = find_unit<32, 32>(a, place, splits, unit);
+  if (u.none) return;
+  const Seq s = u.s;
+  const History hist = u.hist;
+  const Share share = u.share;
+  const int split = u.split, rows = s.len * a.group;
   const HistoryTiles<32> tiles(hist);
-  const Share share = share_of(tiles.total, splits, unit, split);
-  if (split >= share.count) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
   const int r0 = s.tile * 32, h0 = kh * a.group, last = min(r0 + 32, rows) - 1;
   const int r = r0 + (lane & 31);

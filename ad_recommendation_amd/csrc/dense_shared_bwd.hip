@@ -118,10 +118,12 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   int block = blockIdx.x;
   const int kh = block % a.kv_heads;
   block /= a.kv_heads;
-  const int split = block % splits;
-  const Seq s = find_rows<kTile>(a, block / splits);
-  const int rows = s.len * a.group;
-  if (s.tile < 0 || (int64_t)s.tile * kTile >= rows) return;
+  const Unit u = find_unit<kTile, kRows>(a, block, splits, unit);
+  if (u.none) return;
+  const Seq s = u.s;
+  const History hist = u.hist;
+  const Share share = u.share;
+  const int split = u.split, rows = s.len * a.group;
   const int wave = uniform(threadIdx.x >> 6);
   const int r0 = s.tile * kTile, rw = r0 + wave * 32, h0 = kh * a.group, last = min(r0 + kTile, rows) - 1;
 
@@ -130,10 +132,7 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   ql.load(a, a.q, s.begin, h0, rw, rows);
   dl.load(a, a.dout, s.begin, h0, rw, rows);
   ol.load(a, a.out, s.begin, h0, rw, rows);
-  const History hist = history(a, s.index);
   const HistoryTiles<kRows> tiles(hist);
-  const Share share = share_of(tiles.total, splits, unit, split);
-  if (split >= share.count) return;
   const T* hk = history_of<T>(a, a.hk, hist, s.index, kh);
   const T* hv = history_of<T>(a, a.hv, hist, s.index, kh);
   Tile kl, vl;
@@ -248,16 +247,15 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
   int block = blockIdx.x;
   const int kh = block % a.kv_heads;
   block /= a.kv_heads;
-  const int split = block % splits;
-  const Seq s = find_rows<32>(a, block / splits);
-  const int rows = s.len * a.group;
-  if (s.tile < 0 || (int64_t)s.tile * 32 >= rows) return;
+  const Unit u = find_unit<32, 32>(a, block, splits, unit);
+  if (u.none) return;
+  const Seq s = u.s;
+  const History hist = u.hist;
+  const Share share = u.share;
+  const int split = u.split, rows = s.len * a.group;
   const int wave = uniform(threadIdx.x >> 6), lane = lane_id();
   const int r0 = s.tile * 32, h0 = kh * a.group, last = min(r0 + 32, rows) - 1;
-  const History hist = history(a, s.index);
   const HistoryTiles<32> tiles(hist);
-  const Share share = share_of(tiles.total, splits, unit, split);
-  if (split >= share.count) return;
   const T* hk = history_of<T>(a, a.hk, hist, s.index, kh);
   const T* hv = history_of<T>(a, a.hv, hist, s.index, kh);
   u32x4 kr[kRegs], vr[kRegs];
@@ -785,12 +783,30 @@ __global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), (dkv_wave
   }
   P& sh = *reinterpret_cast<P*>(lds);
   const int block = blockIdx.x - own_blocks, kh = block % kv_heads, slot = block / kv_heads;
-  const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot,
-                                  [](int64_t t, int b) { return t / kTokens + b; }));
-  if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
-  const History hist = history(a, h.index);
-  Seq s = uniform(sequence(a, h.index, 0));
-  const int j0 = h.tile * kTokens;
+  Seq s;
+  History hist;
+  int tile;
+  if (a.n_seq <= kSorted) {  // as find_unit: those with the most rows first
+    const int b = min(lane_id(), a.n_seq - 1);
+    const int begin = (int)min(max((int64_t)a.off[b], (int64_t)0), a.n_tok);
+    const int len = (int)(min(max((int64_t)a.off[b + 1], (int64_t)begin), a.n_tok) - begin);
+    int row, n;
+    history_place(a, b, row, n);
+    const int x = sorted_place(a.n_seq, slot, (n + kTokens - 1) / kTokens, len, tile);
+    if (x < 0) return;
+    s.index = x;
+    s.begin = __builtin_amdgcn_readlane(begin, x);
+    s.len = __builtin_amdgcn_readlane(len, x);
+    hist = history_of(a, __builtin_amdgcn_readlane(row, x), __builtin_amdgcn_readlane(n, x));
+  } else {
+    const Seq h = uniform(find_tile(HistoryBatch{a.hist, a.n_hist, a.n_seq}, slot,
+                                    [](int64_t t, int b) { return t / kTokens + b; }));
+    if (h.tile < 0 || (int64_t)h.tile * kTokens >= h.len) return;
+    hist = history(a, h.index);
+    s = uniform(sequence(a, h.index, 0));
+    tile = h.tile;
+  }
+  const int j0 = tile * kTokens;
   // a tile that no row sees has none
   if (j0 >= hist.sinks && j0 + kTokens <= hist.first) s.len = 0;
   dkv<T, DH, DIRECT>(a, sh, s, hist, kh, j0, min(j0 + kTokens, hist.n));

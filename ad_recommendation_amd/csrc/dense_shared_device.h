@@ -53,18 +53,28 @@ struct History {
   int64_t row;             // packed: the first event's row
   int n, sinks, first;     // events; of them seen before the window; where the window begins
 };
-__device__ __forceinline__ History history(const SharedArgs& a, int b) {
-  History h;
-  h.row = 0;
-  if (a.packed) {
-    h.row = uniform((int)min(max((int64_t)a.hist[b], (int64_t)0), a.n_hist));  // at most 2^30
-    h.n = uniform((int)(min(max((int64_t)a.hist[b + 1], h.row), a.n_hist) - h.row));
+// Events of request b's history, and where they begin.
+__device__ __forceinline__ void history_place(const SharedArgs& a, int b, int& row, int& n) {
+  row = 0;
+  if (a.packed) {  // at most 2^30
+    row = (int)min(max((int64_t)a.hist[b], (int64_t)0), a.n_hist);
+    n = (int)(min(max((int64_t)a.hist[b + 1], (int64_t)row), a.n_hist) - row);
   } else {
-    h.n = uniform((int)min(max((int64_t)a.hist[b], (int64_t)0), a.n_hist));
+    n = (int)min(max((int64_t)a.hist[b], (int64_t)0), a.n_hist);
   }
-  h.first = max(h.n - a.back, 0);
+}
+__device__ __forceinline__ History history_of(const SharedArgs& a, int row, int n) {
+  History h;
+  h.row = row;
+  h.n = n;
+  h.first = max(n - a.back, 0);
   h.sinks = min(a.sinks, h.first);
   return h;
+}
+__device__ __forceinline__ History history(const SharedArgs& a, int b) {
+  int row, n;
+  history_place(a, b, row, n);
+  return history_of(a, uniform(row), uniform(n));
 }
 template <typename T>
 __device__ __forceinline__ const T* history_of(const SharedArgs& a, const EmbHeads& t, const History& h, int b, int kh) {
@@ -119,6 +129,64 @@ __device__ __forceinline__ Share share_of(int total, int splits, int unit, int s
   s.first = min(split * per, total);
   s.end = min(s.first + per, total);
   return s;
+}
+// What a workgroup has: a tile of ROWS query rows of a request and a share of its tiles of KEYS keys.
+struct Unit {
+  Seq s;
+  History hist;
+  Share share;
+  int split;
+  bool none;
+};
+// Few requests: a lane has one of them, all that their places depend on comes in one load, and those whose workgroups
+// have the most to do come first, with no place in between left empty.
+constexpr int kSorted = 64;
+// The request that place `place` belongs to when each has `units` of them in a row, in the order of `key`, largest first;
+// -1 past the last.  local: which of the request's.
+__device__ __forceinline__ int sorted_place(int n, int place, int units, int key, int& local) {
+  int before = 0;
+  for (int j = 0; j < n; ++j) {
+    const int other = __builtin_amdgcn_readlane(key, j), its = __builtin_amdgcn_readlane(units, j);
+    before += other > key || (other == key && j < lane_id()) ? its : 0;
+  }
+  const uint64_t mine = __ballot(lane_id() < n && place >= before && place - before < units);
+  if (mine == 0) return -1;
+  const int b = __ffsll((unsigned long long)mine) - 1;
+  local = place - __builtin_amdgcn_readlane(before, b);
+  return b;
+}
+template <int ROWS, int KEYS>
+__device__ __forceinline__ Unit find_unit(const SharedArgs& a, int place, int splits, int unit) {
+  Unit u;
+  if (a.off && a.n_seq <= kSorted) {
+    const int b = min(lane_id(), a.n_seq - 1);
+    const int begin = (int)min(max((int64_t)a.off[b], (int64_t)0), a.n_tok);
+    const int len = (int)(min(max((int64_t)a.off[b + 1], (int64_t)begin), a.n_tok) - begin);
+    int row, n;
+    history_place(a, b, row, n);
+    const Share mine = share_of(HistoryTiles<KEYS>(history_of(a, row, n)).total, splits, unit, 0);
+    const int tiles = (int)(((int64_t)len * a.group + ROWS - 1) / ROWS);
+    int local;
+    const int x = sorted_place(a.n_seq, place, tiles * mine.count, mine.end, local);
+    u.none = x < 0;
+    if (u.none) return u;
+    u.s.index = x;
+    u.s.begin = __builtin_amdgcn_readlane(begin, x);
+    u.s.len = __builtin_amdgcn_readlane(len, x);
+    u.hist = history_of(a, __builtin_amdgcn_readlane(row, x), __builtin_amdgcn_readlane(n, x));
+    const int count = __builtin_amdgcn_readlane(mine.count, x);
+    u.s.tile = (uint32_t)local / (uint32_t)count;
+    u.split = local - u.s.tile * count;
+  } else {
+    u.split = place % splits;
+    u.s = find_rows<ROWS>(a, place / splits);
+    u.none = u.s.tile < 0 || (int64_t)u.s.tile * ROWS >= (int64_t)u.s.len * a.group;
+    if (u.none) return u;
+    u.hist = history(a, u.s.index);
+  }
+  u.share = share_of(HistoryTiles<KEYS>(u.hist).total, splits, unit, u.split);
+  u.none = u.split >= u.share.count;
+  return u;
 }
 __device__ __forceinline__ float* part_of(const SharedArgs& a, int split) {
   return a.part + (int64_t)split * a.n_tok * a.q_heads * a.dim;
