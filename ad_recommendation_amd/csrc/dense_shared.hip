@@ -93,7 +93,8 @@ __device__ __forceinline__ void meet_own(const char* kt, const char* vt, const R
 // ---------------------------------------------------------------- 128 rows
 enum { kByRegisters, kDirect, kCodes };  // how tiles of history get to LDS
 
-// Tiles of keys or values in 8 bits through registers: codes are converted on their way to LDS.
+// Tiles of keys or values in 8 bits through registers: codes are converted on their way to LDS.  8 bytes a load, so that
+// a load is one piece of LDS: with 16, whose two pieces meet others in their banks, 64 requests 292 us instead of 278.
 template <typename T, int DH, int ROWS, int THREADS>
 struct CodesTile : RegisterTile<T, DH, ROWS, THREADS> {
   typedef RegisterTile<T, DH, ROWS, THREADS> R;
@@ -637,7 +638,7 @@ int64_t slots(const SharedArgs& a, int rows) {
 
 // How a request's keys are shared out.  us as in by_32_rows().  Of 32 rows, many waves a workgroup rather than a
 // second launch while each has few tiles (1 request of 64 candidates, 1000: 11.2; with a join 12.5).  Of 128 rows, for
-// about 768 workgroups (16 packed histories of up to 6000, 30 candidates, 8 heads of 64: 32; in one part each 94), of
+// about 400 workgroups (16 packed histories of up to 6000, 30 candidates, 8 heads of 64: 32; in one part each 93), of
 // 8 tiles at least, 16 where there are many already (12 of up to 5000, 200 candidates, 16 and 4 heads of 64: 46; 8 tiles
 // 54, one part 82).
 SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, int64_t most, bool one) {
@@ -653,7 +654,7 @@ SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t h
   const int64_t base = slots(p.rows);
   auto shared = [&](SharedPlan& p, int64_t keys, int64_t longest) {
     if (p.rows == 128) {
-      share_out(p, base, (keys + 63) / 64, (longest + 63) / 64, 768, base >= 128 ? 16 : 8);
+      share_out(p, base, (keys + 63) / 64, (longest + 63) / 64, 400, base >= 128 ? 16 : 8);
     } else if (base < 512 && keys > 128) {
       const int waves = a.dim <= 64 ? 16 : 8;
       if (base <= 256 && (base > 128 || keys <= 64 * waves)) p.waves = waves;

@@ -875,8 +875,8 @@ SharedBwdPlan plan_shared_bwd(const EmbAttn& a, int64_t n_seq, int64_t n_tok, in
   const int64_t base = slots(p.rows), least = p.rows == 128 && base >= 128 ? 16 : 8;
   const int tile = p.rows == 32 ? 32 : 64;
   SharedPlan whole{p.rows, 4, 1, 1, 0}, with = whole;
-  share_out(whole, base, (mean + tile - 1) / tile, (most + tile - 1) / tile, 768, least);
-  share_out(with, base, (std::min(mean, seen) + tile - 1) / tile, (std::min(most, seen) + tile - 1) / tile, 768, least);
+  share_out(whole, base, (mean + tile - 1) / tile, (most + tile - 1) / tile, 400, least);
+  share_out(with, base, (std::min(mean, seen) + tile - 1) / tile, (std::min(most, seen) + tile - 1) / tile, 400, least);
   p.splits = std::min(whole.splits, with.splits);  // what is enough without a window is enough with one
   p.unit = with.unit;
   const size_t rows = (size_t)n_tok * a.q_heads;
