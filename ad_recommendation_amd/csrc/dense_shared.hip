@@ -194,19 +194,28 @@ __global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(Shared
 
   f32x16 o[DH / 32] = {};
   float m = -kInf, l = 0.f;  // the maximum that o and l stand at; this lane's half of the sum
+  // Tiles through registers are stored while the one before is computed, between its scores and its
+  // probabilities (64 requests in 8 bits: 275 us; before the barrier, when nothing else is done, 279).
+  auto store = [&](int it, char (*to)[kBytes]) {
+    if (HOW == kDirect || it >= it1) return;
+    kl.store(to[0]);
+    vl.store(to[1]);
+    if (it + 1 < it1) load(it + 1, to);
+  };
+  store(it0, lds[0]);
   auto meet = [&](int it, char (*now)[kBytes], char (*next)[kBytes]) {
-    kl.store(now[0]);
-    vl.store(now[1]);
-    if (HOW != kDirect && it + 1 < it1) load(it + 1, next);
     Tile::arrived();
     __syncthreads();  // this tile is there, and the other buffer is no longer read
     if (HOW == kDirect && it + 1 < it1) load(it + 1, next);
-    if (rw >= rows) return;
     f32x16 sc[2] = {};
+    if (rw < rows) {
 #pragma unroll
-    for (int ks = 0; ks < DH / 16; ++ks)
+      for (int ks = 0; ks < DH / 16; ++ks)
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) sc[sub] = mma(left<T>(now[0], at, 32 * sub, ks), q[ks], sc[sub]);
+        for (int sub = 0; sub < 2; ++sub) sc[sub] = mma(left<T>(now[0], at, 32 * sub, ks), q[ks], sc[sub]);
+    }
+    store(it + 1, next);
+    if (rw >= rows) return;
     const int n = tiles.end(it) - tiles.key0(it);
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
