@@ -110,7 +110,8 @@ int check_launch(int64_t threads) {
 }
 
 // EMB_VALIDATE=1: the offsets (or lengths) as the device holds them.
-int validate_offsets(const int32_t* d, int64_t n_seq, int64_t n_tok, bool lens, hipStream_t st) {
+// whole: the last one has to be n_tok, and not less.
+int validate_offsets(const int32_t* d, int64_t n_seq, int64_t n_tok, bool lens, hipStream_t st, bool whole = true) {
   if (!validate_on()) return EMB_OK;
   try {
     std::vector<int32_t> h((size_t)n_seq + (lens ? 0 : 1));
@@ -125,7 +126,8 @@ int validate_offsets(const int32_t* d, int64_t n_seq, int64_t n_tok, bool lens, 
     DENSE_CHECK(h[0] == 0, EMB_EINVAL, "attention: offsets[0] != 0");
     for (size_t i = 1; i < h.size(); ++i)
       DENSE_CHECK(h[i] >= h[i - 1], EMB_EINVAL, "attention: offsets decrease");
-    DENSE_CHECK(h.back() == n_tok, EMB_EINVAL, "attention: offsets[n_seq] != n_tok");
+    DENSE_CHECK(whole ? h.back() == n_tok : h.back() <= n_tok, EMB_EINVAL,
+                whole ? "attention: offsets[n_seq] != n_tok" : "attention: offsets[n_seq] > n_tok");
   } catch (const std::bad_alloc&) {
     return set_error(EMB_ENOMEM, "attention: host memory");
   }
@@ -255,7 +257,7 @@ int shared_cache(const SharedCall& c, const EmbHeads* hk, const EmbHeads* ke, co
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
   hipStream_t st = static_cast<hipStream_t>(stream);
-  DENSE_TRY(validate_offsets(c.off, c.n_seq, c.n_tok, false, st));
+  DENSE_TRY(validate_offsets(c.off, c.n_seq, c.n_tok, false, st, false));
   DENSE_TRY(validate_offsets(d_lens, c.n_seq, capacity, true, st));
   DENSE_TRY(validate_first(c, st));
   x.out = *out;
@@ -334,7 +336,7 @@ int cache_call(int32_t kv_heads, int32_t dim, int32_t dtype, const EmbHeads* k, 
   x.dim = dim;
   x.dtype = dtype;
   DENSE_TRY(check_launch(cache_threads(x)));
-  if (d_offsets) DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
+  if (d_offsets) DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st, false));
   return done(launch_cache(x, write, st), what);
 }
 
@@ -609,8 +611,8 @@ int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   DENSE_CHECK(p.bytes == 0 || (d_ws && aligned(d_ws, 16)), EMB_EINVAL, "attention: null or misaligned workspace");
   hipStream_t st = static_cast<hipStream_t>(stream);
-  DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
-  DENSE_TRY(validate_offsets(d_hist_offsets, n_seq, n_hist, false, st));
+  DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st, false));
+  DENSE_TRY(validate_offsets(d_hist_offsets, n_seq, n_hist, false, st, false));
   DENSE_TRY(validate_first(c, st));
   x.out = *out;
   x.lse = d_lse;
@@ -675,8 +677,8 @@ int attn_shared_bwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
   DENSE_TRY(check_launch(shared_bwd_threads(x, p)));
   DENSE_CHECK(ws_bytes >= p.bytes, EMB_ENOSPACE, "attention: workspace too small");
   hipStream_t st = static_cast<hipStream_t>(stream);
-  DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st));
-  DENSE_TRY(validate_offsets(d_hist_offsets, n_seq, n_hist, false, st));
+  DENSE_TRY(validate_offsets(d_offsets, n_seq, n_tok, false, st, false));
+  DENSE_TRY(validate_offsets(d_hist_offsets, n_seq, n_hist, false, st, false));
   DENSE_TRY(validate_first(c, st));
   x.out = *out;
   x.lse = const_cast<float*>(d_lse);

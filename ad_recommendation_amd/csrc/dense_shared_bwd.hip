@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(256) shared_finish(SharedArgs a, int splits, i
     const int d = (int)(i - row * pieces) * 4;
     if (row >= total) return;
     const int64_t tok = row / a.q_heads;
-    const int qh = (int)(row - tok * a.q_heads), count = *part_count(a, splits, tok, qh);
-    if (count <= 1) return;  // it has its gradient
+    const int qh = (int)(row - tok * a.q_heads), count = min(*part_count(a, splits, tok, qh), splits);
+    if (count <= 1 || !in_request(a, tok)) return;  // it has its gradient, or is in no request
     f32x4 t = {};
 #pragma unroll 4
     for (int x = 0; x < count; ++x) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(256) shared_finish(SharedArgs a, int splits, i
   const int col = (int)(i - unit * pieces) * 8;
   const int64_t tok = unit / a.kv_heads;
   const int kh = (int)(unit - tok * a.kv_heads);
-  if (tok >= a.n_tok) return;
+  if (tok >= a.n_tok || !in_request(a, tok)) return;
   f32x8 dk = {}, dv = {};
   for (int g = 0; g < a.group; ++g) {
     const int h = kh * a.group + g;

@@ -149,7 +149,7 @@ __device__ __forceinline__ int sorted_place(int n, int place, int units, int key
     const int other = __builtin_amdgcn_readlane(key, j), its = __builtin_amdgcn_readlane(units, j);
     before += other > key || (other == key && j < lane_id()) ? its : 0;
   }
-  const uint64_t mine = __ballot(lane_id() < n && place >= before && place - before < units);
+  const uint64_t mine = __ballot(lane_id() < n && (uint32_t)(place - before) < (uint32_t)units);
   if (mine == 0) return -1;
   const int b = __ffsll((unsigned long long)mine) - 1;
   local = place - __builtin_amdgcn_readlane(before, b);
@@ -194,6 +194,10 @@ __device__ __forceinline__ float* part_of(const SharedArgs& a, int split) {
 // Maximum (in powers of two) and sum.
 __device__ __forceinline__ float* part_stats(const SharedArgs& a, int splits, int split, int64_t tok, int qh) {
   return part_of(a, splits) + (((int64_t)split * a.n_tok + tok) * a.q_heads + qh) * 2;
+}
+// Whether a token is of a request: the tokens of a batch may be fewer than its arrays have rows for.
+__device__ __forceinline__ bool in_request(const SharedArgs& a, int64_t tok) {
+  return !a.off || (tok >= a.off[0] && tok < a.off[a.n_seq]);
 }
 __device__ __forceinline__ int* part_count(const SharedArgs& a, int splits, int64_t tok, int qh) {
   return reinterpret_cast<int*>(part_stats(a, splits, splits, 0, 0)) + tok * a.q_heads + qh;

@@ -156,13 +156,14 @@ int attn_window_decode_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k
  * tokens.  Otherwise as there: scores, softmax, heads that share keys, EmbAttn and its limits.
  *
  * Requests are ragged: request s holds tokens d_offsets[s] to d_offsets[s + 1] - 1 of q, k and v (int32, ascending
- * from 0 to n_tok).  d_first (nullable: every token is a candidate of its own): int32 [n_tok], for each token the
- * first token of its candidate; a candidate's tokens stand together.
+ * from 0 to at most n_tok).  d_first (nullable: every token is a candidate of its own): int32 [n_tok], for each token the
+ * first token of its candidate; a candidate's tokens stand together.  Rows of tokens, or events of a packed
+ * history, past the last offset belong to no request: nothing is written there.
  */
 
 /*
  * Training: histories are packed, request s's are events d_hist_offsets[s] to d_hist_offsets[s + 1] - 1 of hist_k
- * and hist_v (int32, ascending from 0 to n_hist).
+ * and hist_v (int32, ascending from 0 to at most n_hist).
  *   d_lse : nullable; fp32 [q_heads][n_tok], what the backward reads.
  *   d_ws  : 16-byte aligned, at least attn_shared_fwd_workspace_bytes (EMB_ENOSPACE otherwise); null where that is 0.
  * What is not finite reaches only the tokens that see it.  EMB_VALIDATE=1 checks offsets and first (it synchronises
