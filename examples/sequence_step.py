@@ -3,13 +3,16 @@
 Events are keys of the resident embedding table.  A step looks their rows up, runs one block over
 every user's sequence (norm, windowed attention with sinks, gated residual, norm), scores each event,
 and goes back: the dense weights take an AdamW step, the looked-up rows a sparse Adagrad step.  The
-products with weights are plain torch matmuls.  Afterwards the newest event of each user is answered
-from a key/value cache alone and compared with the whole forward.
+products with weights are plain torch matmuls.  With --candidates the batch is of impressions instead:
+each user's candidates are scored as if each were the next event of the history, which all of them share.
+Afterwards the newest event of each user is answered from a key/value cache alone, in 16 and in 8 bits,
+candidates are ranked against the 8-bit cache, and both are compared with the whole forward.
 
-    python examples/sequence_step.py [--steps 60] [--q8] [--window 16]
+    python examples/sequence_step.py [--steps 60] [--q8] [--window 16] [--candidates 12]
 
 The data is synthetic: every item has a hidden value, and an event's label is the sign of the mean over
-the events it sees in its window, so the loss falls far only if attention carries what it read.
+the events it sees in its window, so the loss falls far only if attention carries what it read.  A
+candidate's label is that of an event in its place.
 """
 from __future__ import annotations
 
@@ -59,13 +62,17 @@ class SequenceModel:
         emb.lookup_pool_fwd(self.table.h, keys, self.bags, t, t, x, emb.EMB_F16, self.rowref)
         return x
 
+    def project(self, x):
+        """Norm before the block, and its queries, keys and values."""
+        t = x.shape[0]
+        h = torch.empty_like(x)
+        dense.norm_gate_residual_fwd(x, None, None, None, self.w["pre"], 1.0, EPS, None, h)
+        return h, (h @ self.c["qkv"]).view(t, 3 * HEADS, HEAD).split(HEADS, 1)
+
     def forward(self, keys, offsets):
         t, new = keys.numel(), lambda *s: torch.empty(*s, dtype=HALF, device=DEV)  # noqa: E731
         x = self.lookup(keys)
-        h = new(t, DIM)
-        dense.norm_gate_residual_fwd(x, None, None, None, self.w["pre"], 1.0, EPS, None, h)
-        qkv = (h @ self.c["qkv"]).view(t, 3 * HEADS, HEAD)
-        q, k, v = qkv.split(HEADS, 1)
+        h, (q, k, v) = self.project(x)
         o, lse = new(t, HEADS, HEAD), torch.empty(HEADS, t, device=DEV)
         dense.attn_window_fwd(q, k, v, offsets, self.window, SINKS, self.scale, o, lse)
         y = o.view(t, DIM) @ self.c["out"]
@@ -100,15 +107,63 @@ class SequenceModel:
                                      g["pre"], norm_ws)
         return g, dx
 
-    def train(self, keys, offsets, labels, lr=3e-3, row_lr=0.05):
-        logit = self.forward(keys, offsets)
+    def forward_candidates(self, keys, offsets, hist_offsets):
+        """Scores of candidates: keys are those of the histories' events, then the candidates'.  A candidate
+        is the next event of its user's history and sees nothing of the other candidates."""
+        x = self.lookup(keys)
+        h, qkv = self.project(x)
+        m = keys.numel() - int(offsets[-1])
+        (kh, vh), (q, k, v) = (y[:m] for y in qkv[1:]), (y[m:] for y in qkv)
+        t, new = q.shape[0], lambda *s: torch.empty(*s, dtype=HALF, device=DEV)  # noqa: E731
+        o, lse = new(t, HEADS, HEAD), torch.empty(HEADS, t, device=DEV)
+        nb = dense.attn_shared_fwd_workspace_bytes(t, offsets.numel() - 1, m, HEADS, HEADS, HEAD)
+        ws = torch.empty(nb, dtype=torch.uint8, device=DEV) if nb else None
+        dense.attn_shared_fwd(q, k, v, kh, vh, offsets, None, hist_offsets, self.window, SINKS, self.scale, o, lse, ws)
+        y = o.view(t, DIM) @ self.c["out"]
+        r, h2 = new(t, DIM), new(t, DIM)
+        dense.norm_gate_residual_fwd(x[m:], y, self.c["gate"], self.w["post"], self.w["pre2"], ALPHA, EPS, r, h2)
+        self.saved = x, h, q, k, v, kh, vh, o, lse, y, r, h2
+        return (h2 @ self.c["head"])[:, 0].float()
+
+    def backward_candidates(self, dlogit, offsets, hist_offsets):
+        """The same for candidates; the rows' gradients are of the histories' events, then the candidates'."""
+        x, h, q, k, v, kh, vh, o, lse, y, r, h2 = self.saved
+        t, m, g = q.shape[0], kh.shape[0], {k: torch.empty_like(w) for k, w in self.w.items()}
+        ws = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)  # noqa: E731
+        d = dlogit[:, None].to(HALF)
+        g["head"] = (h2.t().float() @ d.float())
+        dh2 = d @ self.c["head"].t()
+        dx, dy = torch.zeros_like(x), torch.empty_like(y)
+        norm_ws = ws(dense.norm_gate_residual_bwd_workspace_bytes(t + m, DIM))
+        dense.norm_gate_residual_bwd(r, y, self.c["gate"], self.w["post"], self.w["pre2"], ALPHA, EPS, None, dh2,
+                                     dx[m:], dy, g["gate"], g["post"], g["pre2"], norm_ws)
+        g["out"] = (o.view(t, DIM).t() @ dy).float()
+        do = (dy @ self.c["out"].t()).view(t, HEADS, HEAD)
+        # histories have no loss of their own: their events' queries were not used
+        dqkv = torch.zeros(m + t, 3 * HEADS, HEAD, dtype=HALF, device=DEV)
+        dq, dk, dv = dqkv.split(HEADS, 1)
+        n = dense.attn_shared_bwd_workspace_bytes(t, offsets.numel() - 1, m, HEADS, HEADS, HEAD)
+        dense.attn_shared_bwd(q, k, v, kh, vh, offsets, None, hist_offsets, self.window, SINKS, self.scale, o, lse, do,
+                              dq[m:], dk[m:], dv[m:], dk[:m], dv[:m], ws(n))
+        dqkv = dqkv.view(m + t, 3 * DIM)
+        g["qkv"] = (h.t() @ dqkv).float()
+        dh = dqkv @ self.c["qkv"].t()
+        dense.norm_gate_residual_bwd(x, None, None, None, self.w["pre"], 1.0, EPS, dx, dh, dx, None, None, None,
+                                     g["pre"], norm_ws)
+        return g, dx
+
+    def train(self, keys, offsets, labels, hist_offsets=None, lr=3e-3, row_lr=0.05):
+        rest = (offsets,) if hist_offsets is None else (offsets, hist_offsets)
+        forward, backward = ((self.forward, self.backward) if hist_offsets is None else
+                             (self.forward_candidates, self.backward_candidates))
+        logit = forward(keys, *rest)
         loss = torch.nn.functional.binary_cross_entropy_with_logits(logit, labels)
         t = keys.numel()
         # the gradient of the sum, so that half precision holds it; the mean's factor goes to the updates
-        g, dx = self.backward(torch.sigmoid(logit) - labels, offsets)
+        g, dx = backward(torch.sigmoid(logit) - labels, *rest)
         self.step += 1
         args = (self.step, lr, 0.9, 0.99, 1e-8, [0.01 if w.dim() == 2 else 0.0 for w in self.w.values()])
-        more = dict(copies=list(self.c.values()), grad_scale=torch.tensor(1.0 / t, device=DEV))
+        more = dict(copies=list(self.c.values()), grad_scale=torch.tensor(1.0 / labels.numel(), device=DEV))
         if self.q8:
             dense.adamw_step_q8(list(self.w.values()), list(g.values()), *self.state, *args, seed=self.step, **more)
         else:
@@ -126,6 +181,31 @@ class SequenceModel:
         dense.attn_window_decode(q, k_cache, v_cache, lens, self.window, SINKS, self.scale, out, ws)
         return out
 
+    def serve_q8(self, cache, lens, q):
+        """The same against a cache in 8 bits: codes and exponents of keys, then of values."""
+        out = torch.empty_like(q)
+        n, cap = cache[0].shape[:2]
+        nb = dense.attn_window_decode_q8_workspace_bytes(n, cap, HEADS, HEADS, HEAD, self.window, SINKS)
+        ws = torch.empty(nb, dtype=torch.uint8, device=DEV) if nb else None
+        dense.attn_window_decode_q8(q, *cache, lens, self.window, SINKS, self.scale, out, ws)
+        return out
+
+    def rank(self, cache, lens, q, k, v, offsets):
+        """Attention of candidates against the users' 8-bit caches; each sees itself besides."""
+        out = torch.empty_like(q)
+        n, cap = cache[0].shape[:2]
+        nb = dense.attn_shared_cache_workspace_bytes(q.shape[0], n, cap, HEADS, HEADS, HEAD)
+        ws = torch.empty(nb, dtype=torch.uint8, device=DEV) if nb else None
+        dense.attn_shared_cache_q8(q, k, v, *cache, offsets, None, lens, self.window, SINKS, self.scale, out, ws)
+        return out
+
+
+def new_cache(n_seq: int, capacity: int):
+    """An 8-bit cache: codes and exponents of keys, then of values."""
+    codes = [torch.zeros(n_seq, capacity, HEADS, HEAD, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    exps = [torch.zeros(n_seq, HEADS, capacity, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    return codes[0], exps[0], codes[1], exps[1]
+
 
 def batch(rng, values, window: int, n_seq: int = 64, longest: int = 100):
     lens = rng.integers(2, longest, n_seq)
@@ -140,12 +220,27 @@ def batch(rng, values, window: int, n_seq: int = 64, longest: int = 100):
     return to((items + 1).astype(np.int64)), to(off), to(labels)
 
 
+def candidate_batch(rng, values, window: int, n_seq: int = 64, longest: int = 100, most: int = 12):
+    """Histories and candidates: keys (events, then candidates), offsets of both, a label a candidate."""
+    lens, count = rng.integers(0, longest, n_seq), rng.integers(0, most + 1, n_seq)
+    count[0] = max(count[0], 1)
+    hist, off = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (lens, count))
+    items = rng.integers(0, values.size, hist[-1] + off[-1])
+    labels = values[items[hist[-1]:]]
+    for s in range(n_seq):
+        seen = items[max(hist[s], hist[s + 1] - window + 1):hist[s + 1]]  # the candidate has a place in the window
+        labels[off[s]:off[s + 1]] += values[seen].sum()
+    to = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    return to((items + 1).astype(np.int64)), to(off), to((labels > 0).astype(np.float32)), to(hist)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--items", type=int, default=200)
     ap.add_argument("--window", type=int, default=16)
     ap.add_argument("--q8", action="store_true", help="AdamW states in 8 bits")
+    ap.add_argument("--candidates", type=int, default=0, help="train on impressions of up to so many candidates")
     a = ap.parse_args(argv)
     torch.cuda.set_device(0)
     rng = np.random.default_rng(0)
@@ -153,7 +248,9 @@ def main(argv=None):
     m = SequenceModel(a.items, a.window, a.q8)
     losses = []
     for i in range(a.steps):
-        losses.append(m.train(*batch(rng, values, a.window)).item())
+        data = (candidate_batch(rng, values, a.window, most=a.candidates) if a.candidates else
+                batch(rng, values, a.window))
+        losses.append(m.train(*data).item())
         if i % 10 == 0 or i == a.steps - 1:
             print(f"step {i}: loss {losses[-1]:.4f}", flush=True)
 
@@ -170,6 +267,25 @@ def main(argv=None):
     served = m.serve(kc, vc, lens, q[last].contiguous())
     worst = (served.float() - o[last].float()).abs().max().item()
     print(f"newest events from the cache differ from the whole forward by at most {worst:.2g}", flush=True)
+
+    # the same caches in 8 bits: histories written at once but for the newest events, which follow
+    cache = new_cache(lens.numel(), cap)
+    older = torch.ones(k.shape[0], dtype=torch.bool, device=DEV)
+    older[last] = False
+    dense.cache_q8_write(k[older], v[older], off - torch.arange(off.numel(), dtype=torch.int32, device=DEV), None, *cache)
+    dense.cache_q8_write(k[last], v[last], None, lens - 1, *cache)
+    served = m.serve_q8(cache, lens, q[last].contiguous())
+    apart = (served.float() - o[last].float()).abs().max().item()
+    print(f"from the cache in 8 bits by at most {apart:.2g}", flush=True)
+
+    # ranking: every user's candidates against the cache, and against the whole histories in 16 bits
+    keys = torch.cat([keys, torch.from_numpy(rng.integers(1, a.items + 1, 8 * lens.numel())).to(DEV)])
+    c_off = 8 * torch.arange(lens.numel() + 1, dtype=torch.int32, device=DEV)
+    m.forward_candidates(keys, c_off, off)
+    q, k, v, _, _, o = m.saved[2:8]
+    ranked = m.rank(cache, lens, q, k, v, c_off)
+    ranks_apart = (ranked.float() - o.float()).abs().max().item()
+    print(f"candidates against the cache in 8 bits by at most {ranks_apart:.2g}", flush=True)
     m.table.close()
     return losses, worst
 
