@@ -239,21 +239,23 @@ def attn_window_decode(q, k_cache, v_cache, lens, window: int, sinks: int, scale
 
 
 # ------------------------------------------------------------------ caches in 8 bits
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+_U8, _E4M3 = torch.uint8, torch.float8_e4m3fn
+_CACHE_OF = {"k": "k_cache", "v": "v_cache"}
 
 
 def _q8(dev: int, codes, exp, name: str, shape):
     """EmbHeads of codes [sequences, capacity, heads, dim] and of their exponents [sequences, heads, capacity],
     both of any strides but the codes' last, which is 1."""
-    if codes.dtype not in _CODES:
-        raise TypeError(f"{name}_cache: expected uint8 or float8_e4m3fn, got {codes.dtype}")
-    c = _heads(dev, codes, f"{name}_cache", codes.dtype, shape)
-    if exp.dtype is not torch.uint8 or exp.get_device() != dev:
+    t = codes.dtype
+    if t is not _U8 and t is not _E4M3:
+        raise TypeError(f"{name}_cache: expected uint8 or float8_e4m3fn, got {t}")
+    if exp.dtype is not _U8 or exp.get_device() != dev:
         raise TypeError(f"{name}_exp: expected a CUDA tensor of uint8 on the current device, got {exp.dtype} on {exp.device}")
-    if exp.shape != (shape[0], shape[2], shape[1]):
-        raise ValueError(f"{name}_exp: expected shape {(shape[0], shape[2], shape[1])}, got {tuple(exp.shape)}")
+    n_seq, cap, heads, _ = shape
+    if exp.shape != (n_seq, heads, cap):
+        raise ValueError(f"{name}_exp: expected shape {(n_seq, heads, cap)}, got {tuple(exp.shape)}")
     seq, head, tok = exp.stride()
-    return c, _pack_heads(exp.data_ptr(), seq, tok, head)
+    return _heads(dev, codes, _CACHE_OF[name], t, shape), _pack_heads(exp.data_ptr(), seq, tok, head)
 
 
 def _cache(k, v, offsets, start, k_cache):

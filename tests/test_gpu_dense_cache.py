@@ -190,3 +190,30 @@ def test_places_past_32_bits():
     got = [torch.empty_like(k), torch.empty_like(v)]
     dense.cache_q8_read(codes, exp, codes2, exp2, offsets([64]), start, *got)
     assert same_values(got[0], O.values_of(c, e).to(F16))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("dim", [8, 128])
+def test_every_number_of_16_bits(dtype, dim):
+    """All 2^16 patterns, neighbours in a row, under tops from the type's least number to its largest: what is exact,
+    halfway, lost, not finite, and exponents at both ends."""
+    half = torch.float16 if dtype is torch.float16 else torch.bfloat16
+    x = torch.arange(1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(half).view(-1, dim // 2)
+    at = (torch.arange(-24, 16) if dtype is torch.float16 else
+          torch.tensor([-133, -130, -127, -126, -120, -119, -118, -60, -1, 0, 9, 100, 126, 127]))
+    tops = torch.ldexp(torch.ones((), dtype=torch.float64), at)
+    tops = torch.cat([tops, 1.5 * tops[1:], 1.99 * tops[-8:]]).to(half).cuda()
+    rows = torch.cat([x, x], 1).repeat(len(tops), 1).to(dtype)
+    rows[:, 0] = tops.repeat_interleave(len(x)).to(dtype)
+    n = rows.shape[0]
+    k = rows.view(n, 1, dim)
+    got = [torch.zeros(n, 1, 1, dim, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    exps = [torch.zeros(n, 1, 1, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    dense.cache_q8_write(k, k, None, None, got[0], exps[0], got[1], exps[1])
+    codes, exp = O.quantise(k)
+    nan = (codes & 127) == 127
+    for c, e in zip(got, exps):
+        c = c[:, 0]
+        assert torch.equal((c & 127) == 127, nan)
+        assert torch.equal(c[~nan], codes[~nan])
+        assert torch.equal(e[:, 0], exp)
