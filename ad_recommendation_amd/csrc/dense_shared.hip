@@ -132,11 +132,16 @@ struct WideTile {
                                                 RegisterTile<T, DH, kRows, kThreads>>> t;
 };
 
-template <int DH, int HOW>
+// Waves of a SIMD, as many as the registers of 32 rows a wave allow.
+template <int DH>
 constexpr int wide_waves = DH == 128 ? 2 : DH == 64 ? 3 : 4;
 
+// Bound by matrix cores and the vector unit (exponentials), each busy 48 % of the time, and the clock, which falls to 1.9
+// GHz: 16 caches of up to 8192, 1000 candidates, 16 and 4 heads of 128, bf16: 338 us, 930 TFLOP/s.  (Eight waves of 256
+// rows, halves of which take products and exponentials in turn: 406 us.)  In 8 bits the conversion of codes is nearly as
+// much vector work again: 64 of up to 8192, 200 candidates, window 4096: 286 us, 680 TFLOP/s, matrix cores busy 31 %.
 template <typename T, int DH, int HOW>
-__global__ void __launch_bounds__(256, (wide_waves<DH, HOW>)) shared_wide(SharedArgs a, int splits, int unit) {
+__global__ void __launch_bounds__(256, wide_waves<DH>) shared_wide(SharedArgs a, int splits, int unit) {
   typedef typename Vec8<T>::t V8;
   typedef typename WideTile<T, DH, HOW>::t Tile;
   constexpr int kRows = 64, kTile = 128;
@@ -554,9 +559,9 @@ __global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits)
   *reinterpret_cast<V*>(static_cast<T*>(a.out.p) + tok * a.out.tok + qh * a.out.head + d) = __builtin_convertvector(o, V);
 }
 
-// Many parts of few rows: a workgroup has a row, and its waves every fourth part; eager too.  A lane has one part's maximum and sum (of 64 at a
-// time), then two columns, eight parts' loads under way at once.  16 parts of 24 rows 3.5 us, a launch's latency and
-// one of memory; by one wave, its loads one after the other, 7.0.
+// Many parts of few rows: a workgroup has a row, and its waves every fourth part; eager too.  A lane has one part's
+// maximum and sum (of 64 at a time), then two columns, eight parts' loads under way at once.  16 parts of 24 rows 3.5 us,
+// a launch's latency and one of memory; by one wave, its loads one after the other, 7.0.
 constexpr int kJoinAtOnce = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) shared_join(SharedArgs a, int splits) {

@@ -1,7 +1,7 @@
 """Python binding of the library's dense side (include/emb_dense.h): attention over event sequences
-with a sliding window and sinks, attention of candidates that share a history, caches in 8 bits, the gated residual
-norms around a block, and AdamW.  Argument
-marshalling only; the work runs in the library's HIP kernels on the caller's stream.
+with a sliding window and sinks, attention of candidates that share a history, caches in 8 bits, the
+gated residual norms around a block, and AdamW.  Argument marshalling only; the work runs in the
+library's HIP kernels on the caller's stream.
 
 The functions keep the C names and argument order.  Device arguments are torch CUDA tensors on the
 current device; errors raise EmbError (the library's checks) or TypeError/ValueError (the tensors').
