@@ -335,16 +335,16 @@ def test_scores_that_grow_and_dwarf_one_another(c):
 
 @pytest.mark.parametrize("tokens", [1, 4])
 @pytest.mark.parametrize("c", [[6, 11, 4], [150, 210, 90]])
-@pytest.mark.parametrize("d", [32, 128])
-def test_what_is_not_finite_reaches_only_what_sees_it(d, c, tokens):
+@pytest.mark.parametrize("d,hq,dtype", [(32, 2, BF16), (128, 2, BF16), (64, 4, F16), (128, 6, F16)])
+def test_what_is_not_finite_reaches_only_what_sees_it(d, hq, dtype, c, tokens):
     h, window, sinks = [60, 130, 40], 100, 2
-    q, k, v, kh, vh = (x.contiguous() for x in inputs(c, h, 2, 2, d, BF16))
+    q, k, v, kh, vh = (x.contiguous() for x in inputs(c, h, hq, 2, d, dtype))
     off, hoff, first = offsets(c), offsets(h), candidates(c, tokens)
     n = sum(c)
     rest = off, first, hoff, window, sinks, 0.2
     out, lse = fwd(q, k, v, kh, vh, *rest)
     o, l, bo, bl = O.attn_shared_fwd(q, k, v, kh, vh, *rest)
-    dout = rand(n, 2, d, dtype=BF16, seed=7)
+    dout = rand(n, hq, d, dtype=dtype, seed=7)
     want, bound = O.attn_shared_bwd(q, k, v, kh, vh, *rest, out, lse, dout)
     rows = torch.arange(n, device="cuda")
     request = torch.repeat_interleave(torch.arange(3, device="cuda"), torch.tensor(c, device="cuda"))
