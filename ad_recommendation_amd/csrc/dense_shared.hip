@@ -148,10 +148,8 @@ __global__ void __launch_bounds__(256, wide_waves<DH>) shared_wide(SharedArgs a,
   constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
   __shared__ __attribute__((aligned(256))) char lds[2][2][kBytes];
   __shared__ uint32_t said[4];
-  int block = blockIdx.x;
-  const int kh = block % a.kv_heads;
-  block /= a.kv_heads;
-  const Unit u = find_unit<kTile, kRows>(a, block, splits, unit);
+  int kh;
+  const Unit u = find_unit<kTile, kRows, true>(a, blockIdx.x, splits, unit, &kh);
   if (u.none) return;
   const Seq s = u.s;
   const History hist = u.hist;

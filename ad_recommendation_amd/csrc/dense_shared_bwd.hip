@@ -117,10 +117,8 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
   constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
   __shared__ __attribute__((aligned(256))) char lds[2][2][kBytes];
   __shared__ uint32_t said[4];
-  int block = blockIdx.x;
-  const int kh = block % a.kv_heads;
-  block /= a.kv_heads;
-  const Unit u = find_unit<kTile, kRows>(a, block, splits, unit);
+  int kh;
+  const Unit u = find_unit<kTile, kRows, true>(a, blockIdx.x, splits, unit, &kh);
   if (u.none) return;
   const Seq s = u.s;
   const History hist = u.hist;
@@ -798,7 +796,8 @@ __global__ void __launch_bounds__((DkvTiles<T, DH, DIRECT>::kThreads), (dkv_wave
     const int len = (int)(min(max((int64_t)a.off[b + 1], (int64_t)begin), a.n_tok) - begin);
     int row, n;
     history_place(a, b, row, n);
-    const int x = sorted_place(a.n_seq, slot, (n + kTokens - 1) / kTokens, len, tile);
+    const int units = (n + kTokens - 1) / kTokens;
+    const int x = sorted_place(a.n_seq, slot, units, order_of(a.n_seq, units, len), tile);
     if (x < 0) return;
     s.index = x;
     s.begin = __builtin_amdgcn_readlane(begin, x);

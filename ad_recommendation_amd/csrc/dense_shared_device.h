@@ -141,22 +141,41 @@ struct Unit {
 // Few requests: a lane has one of them, all that their places depend on comes in one load, and those whose workgroups
 // have the most to do come first, with no place in between left empty.
 constexpr int kSorted = 64;
-// The request that place `place` belongs to when each has `units` of them in a row, in the order of `key`, largest first;
-// -1 past the last.  local: which of the request's.
-__device__ __forceinline__ int sorted_place(int n, int place, int units, int key, int& local) {
-  int before = 0;
+// Each request has `units` places in a row, in the order of `key`, largest first.
+struct Order {
+  int before, total;  // places before those of the lane's request; all
+};
+__device__ __forceinline__ Order order_of(int n, int units, int key) {
+  Order o{0, 0};
   for (int j = 0; j < n; ++j) {
     const int other = __builtin_amdgcn_readlane(key, j), its = __builtin_amdgcn_readlane(units, j);
-    before += other > key || (other == key && j < lane_id()) ? its : 0;
+    o.before += other > key || (other == key && j < lane_id()) ? its : 0;
+    o.total += its;
   }
-  const uint64_t mine = __ballot(lane_id() < n && (uint32_t)(place - before) < (uint32_t)units);
+  return o;
+}
+// The request that place `place` belongs to, -1 past the last.  local: which of the request's.
+__device__ __forceinline__ int sorted_place(int n, int place, int units, const Order& o, int& local) {
+  const uint64_t mine = __ballot(lane_id() < n && (uint32_t)(place - o.before) < (uint32_t)units);
   if (mine == 0) return -1;
   const int b = __ffsll((unsigned long long)mine) - 1;
-  local = place - __builtin_amdgcn_readlane(before, b);
+  local = place - __builtin_amdgcn_readlane(o.before, b);
   return b;
 }
-template <int ROWS, int KEYS>
-__device__ __forceinline__ Unit find_unit(const SharedArgs& a, int place, int splits, int unit) {
+// Of n workgroups, largest first, the one that workgroup `block` takes over.  Between one and two a unit of the GPU all
+// are there at once, and n - 256 units have two: those of the 256 largest that are the smallest, each with one of what
+// is left, the smallest with the largest.  12 requests of up to 300 candidates and 8191 events, window 4096, 16 and 4
+// heads of 128: 92 us, 100 in the order of their sizes; 6 of up to 500 and 8192: 133 and 139.
+__device__ __forceinline__ int paired(int block, int n) {
+  constexpr int kUnits = 256;
+  const int two = n - kUnits;
+  if (two <= 0 || two > kUnits || block >= n) return block;
+  if (block >= kUnits) return n - 1 - (block - kUnits);
+  return block < two ? kUnits - two + block : block - two;
+}
+// HEADS: `place` is that of a workgroup among those of all key/value heads, and kh becomes its head.
+template <int ROWS, int KEYS, bool HEADS = false>
+__device__ __forceinline__ Unit find_unit(const SharedArgs& a, int place, int splits, int unit, int* kh = nullptr) {
   Unit u;
   if (a.off && a.n_seq <= kSorted) {
     const int b = min(lane_id(), a.n_seq - 1);
@@ -167,7 +186,13 @@ __device__ __forceinline__ Unit find_unit(const SharedArgs& a, int place, int sp
     const Share mine = share_of(HistoryTiles<KEYS>(history_of(a, row, n)).total, splits, unit, 0);
     const int tiles = (int)(((int64_t)len * a.group + ROWS - 1) / ROWS);
     int local;
-    const int x = sorted_place(a.n_seq, place, tiles * mine.count, mine.end, local);
+    const Order order = order_of(a.n_seq, tiles * mine.count, mine.end);
+    if (HEADS) {
+      place = paired(place, order.total * a.kv_heads);
+      *kh = place % a.kv_heads;
+      place /= a.kv_heads;
+    }
+    const int x = sorted_place(a.n_seq, place, tiles * mine.count, order, local);
     u.none = x < 0;
     if (u.none) return u;
     u.s.index = x;
@@ -178,6 +203,10 @@ __device__ __forceinline__ Unit find_unit(const SharedArgs& a, int place, int sp
     u.s.tile = (uint32_t)local / (uint32_t)count;
     u.split = local - u.s.tile * count;
   } else {
+    if (HEADS) {
+      *kh = place % a.kv_heads;
+      place /= a.kv_heads;
+    }
     u.split = place % splits;
     u.s = find_rows<ROWS>(a, place / splits);
     u.none = u.s.tile < 0 || (int64_t)u.s.tile * ROWS >= (int64_t)u.s.len * a.group;
