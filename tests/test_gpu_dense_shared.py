@@ -716,3 +716,36 @@ def test_tensors_of_another_device_are_refused(name, monkeypatch):
     monkeypatch.setattr(dense, "_stream", lambda *a: pytest.fail("a tensor of another device was taken"))
     with pytest.raises(TypeError, match="current device"):
         calls[name]()
+
+
+@pytest.mark.parametrize("n", [22, 30, 44, 64, 65])
+def test_hundreds_of_workgroups_of_unlike_work(n):
+    """Between one and two workgroups a unit of the GPU and past that, requests sorted by their work and not."""
+    gen = torch.Generator().manual_seed(n)
+    c = torch.randint(100, 160, (n,), generator=gen).tolist()
+    h = torch.randint(0, 900, (n,), generator=gen).tolist()
+    for tokens in (1, 3):
+        args = *inputs(c, h, 8, 4, 32, BF16), offsets(c), candidates(c, tokens), offsets(h), 600, 1, 0.2
+        out, lse = fwd(*args)
+        o, l, bo, bl = O.attn_shared_fwd(*args)
+        within(out, o, bo, "out")
+        within(lse, l, bl, "lse")
+        dout = rand(*out.shape, dtype=BF16, seed=5)
+        want, bound = O.attn_shared_bwd(*args, out, lse, dout)
+        for name, g, w, b in zip(NAMES, bwd(*args, out, lse, dout), want, bound):
+            within(g, w, b, name)
+
+
+def test_two_calls_at_once():
+    """Steps on two streams, each with workspaces of its own."""
+    steps = [serve_and_train([200, 30], [5000, 80], F16)[1], serve_and_train([3] * 70, [90] * 70, BF16)[1]]
+    want = [step() for step in steps]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for stream, step in zip(streams, steps):
+            with torch.cuda.stream(stream):
+                got.append(step())
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
