@@ -4,10 +4,11 @@
 // largest in [128, 256), rounded to the nearest e4m3 code (ties to even).  Powers of two lose nothing of a
 // floating-point code, so which scale a row has decides no rounding, and x 2^-k is exact.
 //
-// Memory bound: a lane has eight elements, a row up to 16 lanes whose maximum goes round on the vector unit.  With 16
-// instructions an element the vector unit was as busy as memory; the maximum of bits and a conversion that scales
-// leave about four, and what is rare (numbers that are not finite, exponents at T's ends) goes another way: writing and
-// reading back 64 histories of up to 8191 events, 8 heads of 128, bf16, took 745 us, and takes 694 at 5.2 TB/s.
+// Memory bound: a lane has eight elements, a row up to 16 lanes whose maximum goes round on the vector unit.  With a test
+// of every element, a limit and a scaling of its own the vector unit was as busy as memory; the maximum of bits and a
+// conversion that scales do without in the common case, and what is rare (numbers that are not finite, exponents at T's
+// ends) goes another way: writing and reading back 64 histories of up to 8191 events, 8 heads of 128, bf16, took 745 us,
+// and takes 693 at 5.2 TB/s.
 #include <type_traits>
 
 #include "dense_shared_device.h"
