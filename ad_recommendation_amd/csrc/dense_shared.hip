@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) shared_narrow
   else if (a.lse) a.lse[(int64_t)(h0 + row.g) * a.n_tok + tok] = top * c * kLn2 + logf(sum);
 }
 
-// The sums of a row's parts at their common maximum.
+// The sums of a row's parts at their common maximum.  A row with parts has keys: a sum of 0 is that of scores which are
+// all minus infinity, whose softmax is 0 / 0 here as in one part.
 //
 // A thread has four columns of a row, eight of its parts' loads under way at once.  EAGER, for little data: nothing is
 // read after something else, and what is read of parts that are not there is left out (30 candidates of a request,
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(256) shared_join_few(SharedArgs a, int splits)
   typedef T V __attribute__((ext_vector_type(4)));
   const float inv = 1.f / sum;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = sum == 0.f ? 0.f : o[e] * inv;
+  for (int e = 0; e < 4; ++e) o[e] *= inv;
   *reinterpret_cast<V*>(static_cast<T*>(a.out.p) + tok * a.out.tok + qh * a.out.head + d) = __builtin_convertvector(o, V);
 }
 
@@ -614,10 +615,9 @@ __global__ void __launch_bounds__(256) shared_join(SharedArgs a, int splits) {
   for (int w = 1; w < 4; ++w) o += sums[w][lane];
   if (lane == 0 && a.lse) a.lse[qh * a.n_tok + tok] = top * kLn2 + logf(sum);
   if (d >= a.dim) return;
-  const bool none = sum == 0.f;
   T* out = static_cast<T*>(a.out.p) + tok * a.out.tok + qh * a.out.head + d;
-  out[0] = (T)(none ? 0.f : o[0] / sum);
-  out[1] = (T)(none ? 0.f : o[1] / sum);
+  out[0] = (T)(o[0] / sum);
+  out[1] = (T)(o[1] / sum);
 }
 
 // ---------------------------------------------------------------- launches

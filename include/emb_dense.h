@@ -153,7 +153,9 @@ int attn_window_decode_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k
  * candidate sees the history and its candidate's tokens up to itself; no candidate sees another.  A candidate
  * stands at the place after the history's n events: event j is seen when n - j < window or j < sinks, as the next
  * event of that sequence would see it in attn_window_fwd.  window and sinks say nothing about a candidate's own
- * tokens.  Otherwise as there: scores, softmax, heads that share keys, EmbAttn and its limits.
+ * tokens.  Otherwise as there: scores, softmax, heads that share keys, EmbAttn and its limits.  A score of minus
+ * infinity weighs nothing beside others; where all that a row sees are, its out is NaN and its lse minus infinity, however
+ * many workgroups share the keys.
  *
  * Requests are ragged: request s holds tokens d_offsets[s] to d_offsets[s + 1] - 1 of q, k and v (int32, ascending
  * from 0 to at most n_tok).  d_first (nullable: every token is a candidate of its own): int32 [n_tok], for each token the

@@ -749,3 +749,44 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+# c, h, dim, whether keys are shared out over workgroups: 32 rows a workgroup and 128, joins of each kind
+@pytest.mark.parametrize("c,h,d,shared", [([5, 3], [40, 30], 32, False), ([20], [9000], 64, True), ([400, 200], [90, 60], 64, False),
+                                          ([600], [9000], 64, True), ([3000], [9000], 64, True), ([300, 200], [2000, 700], 64, True)])
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_rows_whose_scores_are_all_minus_infinity(c, h, d, shared, tokens):
+    """Their softmax is NaN, and so is out, however many workgroups share the keys; lse is minus infinity."""
+    hq, hk, n = 4, 2, sum(c)
+    q, k, v, kh, vh = (x.contiguous() for x in inputs(c, h, hq, hk, d, F16))
+    k[..., 0] = kh[..., 0] = 1
+    gone = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+    gone[n - 2, 1:3] = gone[0, 0] = True
+    kept = q.clone()
+    q[..., 0].masked_fill_(gone, -float("inf"))
+    off, hoff, first, scale = offsets(c), offsets(h), candidates(c, tokens), 0.2
+    assert (dense.attn_shared_fwd_workspace_bytes(n, len(c), sum(h), hq, hk, d) > 0) == shared
+    o, l, bo, bl = O.attn_shared_fwd(kept, k, v, kh, vh, off, first, hoff, BIG, 0, scale)
+
+    def check(out, o, bo, gone, what):
+        assert out[gone].isnan().all(), what
+        within(out[~gone], o[~gone], bo[~gone], what)
+    out, lse = fwd(q, k, v, kh, vh, off, first, hoff, BIG, 0, scale)
+    check(out, o, bo, gone, "out")
+    assert (lse.T[gone] == -float("inf")).all()
+    within(lse.T[~gone], l.T[~gone], bl.T[~gone], "lse")
+    cap, lens = max(h) + 3, torch.tensor(h, dtype=torch.int32, device="cuda")
+    kc, vc, got = cached(kh, h, cap), cached(vh, h, cap), torch.full_like(q, 7)
+    nb = dense.attn_shared_cache_workspace_bytes(n, len(c), cap, hq, hk, d)
+    dense.attn_shared_cache(q, k, v, kc, vc, off, first, lens, BIG, 0, scale, got, workspace(nb)[:nb])
+    check(got, o, bo, gone, "out from caches")
+    # the newest event against 8 bits, of which a 1 is one
+    (kq, ke, kv), (vq, ve, vv) = in_8_bits(kc.nan_to_num(0)), in_8_bits(vc.nan_to_num(0))
+    q1, gone1 = kept[:len(c)].clone(), torch.zeros(len(c), hq, dtype=torch.bool, device="cuda")
+    gone1[0, 3] = True
+    o, bo = O.attn_decode(q1, kv, vv, lens, BIG, 0, scale)
+    q1[..., 0].masked_fill_(gone1, -float("inf"))
+    nb = dense.attn_window_decode_q8_workspace_bytes(len(c), cap, hq, hk, d, BIG, 0)
+    got = torch.full_like(q1, 7)
+    dense.attn_window_decode_q8(q1, kq, ke, vq, ve, lens, BIG, 0, scale, got, workspace(nb)[:nb] if nb else None)
+    check(got, o, bo, gone1, "newest")
