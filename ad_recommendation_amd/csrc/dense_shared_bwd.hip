@@ -51,12 +51,13 @@ __device__ __forceinline__ float row_delta(const typename Vec8<T>::t (&out)[DH /
   return swap32_sum(s);
 }
 
-// A tile of 32 keys at row at0 of LDS tiles: dq += ds k.  OWN: of keys j0 on the row sees lo to hi.  Otherwise the
-// first n are there, and seen.
+// A tile of 32 keys at row at0 of LDS tiles: dq += ds k.  OWN: of keys j0 on the row sees lo to hi, and of an `odd`
+// tile, whose keys are not all finite, what is not stays out of the second product.  Otherwise the first n are there, and
+// seen.
 template <typename T, int DH, bool OWN, typename R>
 __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R& at, int at0, int n, int lo, int hi,
                                         int j0, const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int& by,
-                                        bool& some) {
+                                        bool& some, bool odd = false) {
   typedef typename Vec8<T>::t V8;
   f32x16 sc = {}, dp = {};
 #pragma unroll
@@ -74,7 +75,14 @@ __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R&
   for (int k = 0; k < 2; ++k) {
     const V8 b = right_of<T>(ds, 8 * k);
 #pragma unroll
-    for (int db = 0; db < DH / 32; ++db) dq[db] = mma(left_t<T>(kt, at, at0 + 16 * k, db), b, dq[db]);
+    for (int db = 0; db < DH / 32; ++db) {
+      V8 x = left_t<T>(kt, at, at0 + 16 * k, db);
+      if (OWN && odd) {
+        asm volatile("");  // a branch, and not a choice in every tile
+        x = finite_of<T>(x);
+      }
+      dq[db] = mma(x, b, dq[db]);
+    }
   }
 }
 
@@ -107,11 +115,15 @@ __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh
   }
 }
 
+// Waves of a SIMD.  Direct tiles and no token met alone leave 64-wide heads registers for four.
+template <int DH, bool LEAN>
+constexpr int dq_waves = DH == 128 ? 2 : DH == 64 && !LEAN ? 3 : 4;
+
 // 128 rows a workgroup, 32 a wave, tiles of 64 keys in LDS, as in the forward.  8 requests of up to 512 candidates and
 // 4095 events, 16 and 8 heads of 128, bf16: 95 us, matrix cores busy 35 % of the time; 200 of up to 120 tokens and 500
 // events, 8 heads of 64, fp16: 72 us for 197 MB, each workgroup's loads one after the other.
 template <typename T, int DH, bool DIRECT, bool TILES>
-__global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) shared_dq(SharedArgs a, int splits, int unit) {
+__global__ void __launch_bounds__(256, (dq_waves<DH, DIRECT && TILES>)) shared_dq(SharedArgs a, int splits, int unit) {
   typedef TileOf<T, DH, 64, 256, DIRECT> Tile;
   constexpr int kRows = 64, kTile = 128;
   constexpr int kBytes = RegisterTile<T, DH, kRows, 256>::kBytes;
@@ -197,20 +209,15 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
     for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)); j0 < end; j0 += kRows) {
       __syncthreads();  // the tile before is done with
       bool odd = false;
-      for (int x = 0; x < 2; ++x) {  // one after the other: two would not fit the registers
-        const EmbHeads& t = x ? a.v : a.k;
+      {
         OwnTile tile;
-        tile.load(nullptr, static_cast<const T*>(t.p) + s.begin * t.tok + kh * t.head, t.tok, j0, end, a.dim);
+        tile.load(nullptr, static_cast<const T*>(a.k.p) + s.begin * a.k.tok + kh * a.k.head, a.k.tok, j0, end, a.dim);
 #pragma unroll
-        for (int n = 0; n < OwnTile::kRegs; ++n) {
-          bool its = false;
-          const u32x4 fine = only_finite<T>(tile.r[n], its);
-          if (!x) {
-            tile.r[n] = fine;
-            odd |= its;
-          }
-        }
-        tile.store(lds[0][x]);
+        for (int n = 0; n < OwnTile::kRegs; ++n) only_finite<T>(tile.r[n], odd);
+        tile.store(lds[0][0]);
+        asm volatile("" ::: "memory");  // one after the other: two would not fit the registers
+        tile.load(nullptr, static_cast<const T*>(a.v.p) + s.begin * a.v.tok + kh * a.v.head, a.v.tok, j0, end, a.dim);
+        tile.store(lds[0][1]);
       }
       odd = any_wave<4>(odd, said);
       if (rw >= rows) continue;
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(256, (DH == 128 ? 2 : DH == 64 ? 3 : 4)) share
       for (int sub = 0; sub < 2; ++sub)
         if (j0 + 32 * sub < end)
           dq_meet<T, DH, true>(lds[0][0], lds[0][1], own_at, 32 * sub, 0, lo, row.tok, j0 + 32 * sub, w, c, dq, by,
-                               some);
+                               some, odd);
     }
   }
   __syncthreads();  // the tiles are done with
@@ -327,6 +334,7 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
     for (int j0 = uniform(first_of(a, s, row_at(a, r0).tok)) + 32 * wave; j0 < end; j0 += 32 * kWaves) {
       OwnRows::wave_sync();
       bool odd = false;
+#pragma nounroll
       for (int x = 0; x < 2; ++x) {
         OwnRows rows_;
         rows_.load(x ? a.v : a.k, s.begin + j0, kh, end - j0, a.dim);
@@ -334,15 +342,16 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
         for (int n = 0; n < kRegs; ++n) {
           const int idx = lane_id<3>() + n * 64;
           bool its = false;
-          const u32x4 fine = only_finite<T>(rows_.r[n], its);
+          only_finite<T>(rows_.r[n], its);
           if (!x) odd |= its;
-          *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = x ? rows_.r[n] : fine;
+          *reinterpret_cast<u32x4*>(lds[wave][x] + Tile::at(idx / kPieces, idx % kPieces)) = rows_.r[n];
         }
       }
       OwnRows::wave_sync();
-      if (__any(odd))
+      odd = __any(odd);
+      if (odd)
         add_odd_own<T, DH>(a, a.k, s.begin, kh, j0, min(j0 + 32, end), lo, live ? row.tok : -1, true, dq);
-      dq_meet<T, DH, true>(kt, vt, own_at, 0, 0, lo, row.tok, j0, w, c, dq, by, some);
+      dq_meet<T, DH, true>(kt, vt, own_at, 0, 0, lo, row.tok, j0, w, c, dq, by, some, odd);
     }
   }
   if constexpr (std::is_same<T, _Float16>::value) {

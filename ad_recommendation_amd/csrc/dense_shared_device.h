@@ -325,9 +325,12 @@ struct PackedRows : WaveRows<T, DH, TILE, AGAIN> {
 };
 
 // What is not finite in tiles of own tokens.  A product adds 0 * x for a pair that does not see each other, which is NaN
-// where x is not finite.  So those elements of the operand whose rows are summed over come to LDS as zeros, and where a
+// where x is not finite.  So those elements of the operand whose rows are summed over are zeros there, and where a
 // tile has any, each of its rows adds them to the sums that see it (a lane has one, as a column): as they are, or as
-// NaN where the weight's sign may be any.  (The scores of such a row are not finite anyway: its lse or delta is not.)
+// NaN where the weight's sign may be any.  Values (in the forward), queries and gradients are zeros in LDS already: such
+// values are in no score, and of such a query or gradient lse or delta is not finite, nor is what comes of its scores.
+// Keys become zeros only on their way to the second product (finite_of): a score of minus infinity leaves a row's lse
+// finite and has no weight.
 template <typename T>
 __device__ __forceinline__ u32x4 only_finite(u32x4 x, bool& odd) {
   const i16x8 o = odd_of<T>(__builtin_bit_cast(typename Vec8<T>::t, x));

@@ -790,3 +790,51 @@ def test_rows_whose_scores_are_all_minus_infinity(c, h, d, shared, tokens):
     got = torch.full_like(q1, 7)
     dense.attn_window_decode_q8(q1, kq, ke, vq, ve, lens, BIG, 0, scale, got, workspace(nb)[:nb] if nb else None)
     check(got, o, bo, gone1, "newest")
+
+
+@pytest.mark.parametrize("c,h", [([12, 8], [90, 130]), ([160, 140], [90, 230])])
+@pytest.mark.parametrize("d,hq,dtype", [(32, 2, BF16), (128, 4, BF16), (64, 4, F16)])
+def test_gradients_beside_an_own_score_of_minus_infinity(d, hq, dtype, c, h):
+    """A key of a candidate's own, minus infinity in one column, weighs nothing where its score is that: gradients are as
+    without it, but for that column of dq, which is 0 times infinity."""
+    window, sinks, scale, hk, n = 100, 2, 0.2, 2, sum(c)
+    q, k, v, kh, vh = (x.contiguous() for x in inputs(c, h, hq, hk, d, dtype))
+    q[..., 5] = 1
+    off, hoff, first = offsets(c), offsets(h), candidates(c, 4)
+    gone = torch.zeros(n, dtype=torch.bool, device="cuda")
+    gone[torch.tensor([2, c[0] + 6, n - 3], device="cuda")] = True
+    k[gone, :, 5] = -float("inf")
+    args = q, k, v, kh, vh, off, first, hoff, window, sinks, scale
+    out, lse = fwd(*args)
+    assert out.isfinite().all() and lse.isfinite().all()
+    dout = rand(n, hq, d, dtype=dtype, seed=7)
+    got = bwd(*args, out, lse, dout)
+    u, tiny, g = O.U[dtype], O.TINY[dtype], hq // hk
+    want, bound = ([torch.zeros(x.shape, dtype=torch.float64, device="cuda") for x in (q, k, v, kh, vh)] for _ in range(2))
+    odd = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for a, z, b, y in zip(off.tolist()[:-1], off.tolist()[1:], hoff.tolist()[:-1], hoff.tolist()[1:]):
+        see = O.shared_sees(y - b, first[a:z].long() - a, window, sinks, "cuda")
+        odd[a:z] = (see[:, y - b:] & gone[a:z]).any(1)
+        see = see & ~torch.cat([torch.zeros(y - b, dtype=torch.bool, device="cuda"), gone[a:z]])
+        for i in range(hq):
+            x = i // g
+            kk = torch.cat([kh[b:y, x], k[a:z, x]]).double().nan_to_num(0, 0, 0)
+            vv, qq, do, oo = torch.cat([vh[b:y, x], v[a:z, x]]).double(), q[a:z, i].double(), dout[a:z, i].double(), out[a:z, i].double()
+            s, rel = O._head(qq, kk, scale)
+            rel += (8 * lse[i, a:z].abs().max().item() + len(kk)) * O.F32
+            p = torch.exp(s - lse[i, a:z].double()[:, None]).masked_fill(~see, 0.0)
+            delta, both = (do * oo).sum(1, keepdim=True), (do * oo).abs().sum(1, keepdim=True)
+            ds = p * (do @ vv.T - delta)
+            # as the oracle's: dp and delta are fp32 sums, p and ds are rounded to 16 bits
+            e = p * (d + 8) * O.F32 * (do.abs() @ vv.abs().T + both) + ((u + 2 * rel) * ds.abs() + tiny) * see * (1 + u)
+            ep = ((u + 2 * rel) * p + tiny) * see
+            want[0][a:z, i], bound[0][a:z, i] = ds @ kk * scale, e @ kk.abs() * scale
+            for to, y_ in ((want, (ds.T @ qq * scale, p.T @ do)), (bound, (e.T @ qq.abs() * scale, ep.T @ do.abs()))):
+                for own, hist, t in ((1, 3, y_[0]), (2, 4, y_[1])):
+                    to[hist][b:y, x] += t[:y - b]
+                    to[own][a:z, x] += t[y - b:]
+    assert got[0][odd][..., 5].isnan().all() and odd.any()
+    got[0][..., 5].masked_fill_(odd[:, None], 0)
+    want[0][..., 5].masked_fill_(odd[:, None], 0)
+    for name, x, w, b in zip(NAMES, got, want, bound):
+        within(x, w, b * (1 + u) + u * w.abs() + tiny, name)
