@@ -8,8 +8,9 @@
 // own tokens by tiles of them, or, where every token is a candidate, one element at a time from p and ds of the row
 // with itself.
 //
-// In fp16 a score's gradient past 65504 does not fit the second product: sums then go on at a power of two below
-// (fit), looked for in every tile by one more maximum.
+// In fp16 a score's gradient past 65504 does not fit the second product, and below 2^-14 loses bits there: of thousands
+// of events and a small dout all of them are.  So each query's, or key's, stand at a power of two of their own (Fit), and
+// probabilities, for dv, at one for all.
 #include <algorithm>
 #include <initializer_list>
 
@@ -19,19 +20,51 @@ namespace emb {
 
 namespace {
 
-// Gradients of 32 x 32 scores into 16 bits' range; `some`: whether sums of the wave stand at a power of two by now.
-template <typename T, int N>
-__device__ __forceinline__ void fit_if(f32x16& x, f32x16 (&sums)[N], int& by, bool& some) {
-  if constexpr (std::is_same<T, _Float16>::value) {
-    float top = 0.f;
+// Where score gradients stand in fp16: at f, a power of two, and so do sums of their products; bf16 has the range of fp32.
+// They begin at 2^12, where those of most calls have their largest between 2^-6 and 65504.  What comes past that brings all
+// to a largest of 2^8, with room to grow, and the sums after it, as a running maximum does; and so does a first largest
+// below 2^-6.  So where fp16 has fewer bits, below 2^-14, a score's gradient is off by 2^-37 or 2^-19 of the largest at most.
+// A lane has a query or a key, and f is of the two lanes that share it.  300 short requests' backward, 8 and 4 heads of 128,
+// takes 161 us so, and 156 with gradients as they come; 200 of candidates of 3 tokens, 8 heads of 64, 112 and 113.
+template <typename T>
+struct Fit {
+  static constexpr bool kOn = std::is_same<T, _Float16>::value;
+  float f;
+  bool set = false;  // whether there was one of kLeast or more
+  static constexpr float kLeast = 1.f / 64;
+  __device__ __forceinline__ explicit Fit(float at) : f(kOn ? at : 1.f) {}
+  // x stands at f already
+  template <int N>
+  __device__ __forceinline__ void look(f32x16& x, f32x16 (&sums)[N]) {
+    if constexpr (kOn) {
+      float top = 0.f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
-    if (some || __any(top > 65504.f)) {
-      some = true;
-      fit<T>(x, sums, by);
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
+      set |= top >= kLeast;
+      if (__builtin_expect(__any(top > 65504.f || (!set && top > 0.f)), 0)) move(x, sums, top);
     }
   }
-}
+  template <int N>
+  __device__ __forceinline__ void move(f32x16& x, f32x16 (&sums)[N], float top) {
+    top = fminf(swap32_max(top), 0x1p127f);  // of what is not finite the sums are not either
+    set |= top >= kLeast;
+    // not past 2^64, so that f times any product of fp16's numbers is finite
+    const int most = 65 - __builtin_amdgcn_frexp_expf(f), to = 9 - __builtin_amdgcn_frexp_expf(top);
+    const float by = top > 65504.f || (!set && top > 0.f) ? ldexpf(1.f, min(to, most)) : 1.f;
+    f *= by;
+    set |= top > 0.f;
+    x *= by;
+#pragma unroll
+    for (int n = 0; n < N; ++n) sums[n] *= by;
+  }
+  // What sums that stand at f, and at 2^raised besides, are multiplied by.
+  __device__ __forceinline__ float back(int raised = 0) const {
+    return kOn ? ldexpf(1.f, 1 - __builtin_amdgcn_frexp_expf(f) - raised) : 1.f;
+  }
+};
+constexpr int kRaised = 12;
+// Probabilities of the products for dv stand there in fp16, so that they have all their bits down to 2^-26.
+template <typename T> constexpr int kRaisedP = Fit<T>::kOn ? kRaised : 0;
 
 // ---------------------------------------------------------------- dq
 // What a lane's row has throughout: its operands, delta and lse; also writes delta.
@@ -56,8 +89,8 @@ __device__ __forceinline__ float row_delta(const typename Vec8<T>::t (&out)[DH /
 // seen.
 template <typename T, int DH, bool OWN, typename R>
 __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R& at, int at0, int n, int lo, int hi,
-                                        int j0, const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int& by,
-                                        bool& some, bool odd = false) {
+                                        int j0, const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], Fit<T>& fit,
+                                        bool odd = false) {
   typedef typename Vec8<T>::t V8;
   f32x16 sc = {}, dp = {};
 #pragma unroll
@@ -67,10 +100,13 @@ __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R&
   }
   f32x16 ds;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) ds[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -w.lse)) * (dp[r] - w.delta);
+  for (int r = 0; r < 16; ++r) {
+    const float x = Fit<T>::kOn ? fmaf(dp[r], fit.f, -w.delta * fit.f) : dp[r] - w.delta;
+    ds[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -w.lse)) * x;
+  }
   if (OWN) hide_outside<3>(lo, hi, j0, ds, 0.f);
   else if (n < 32) hide_from(n, 0, ds, 0.f);
-  fit_if<T>(ds, dq, by, some);
+  fit.look(ds, dq);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const V8 b = right_of<T>(ds, 8 * k);
@@ -89,7 +125,7 @@ __device__ __forceinline__ void dq_meet(const char* kt, const char* vt, const R&
 // The row's own token alone, on the vector unit; p and ds go to a.self for that token's dk and dv.
 template <typename T, int DH>
 __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh, int qh, bool live,
-                                        const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], int by) {
+                                        const QueryRow<T, DH>& w, float c, f32x16 (&dq)[DH / 32], float f) {
   const T* kp = static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head;
   const T* vp = static_cast<const T*>(a.v.p) + tok * a.v.tok + kh * a.v.head;
   asm volatile("" ::: "memory");  // one row after the other: the registers are full
@@ -97,7 +133,7 @@ __device__ __forceinline__ void dq_self(const SharedArgs& a, int64_t tok, int kh
   asm volatile("" ::: "memory");
   const float dp = dot_row<T, DH>(w.d, vp, live, a.dim);
   if (!live) return;
-  const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -w.lse)), ds = p * (dp - w.delta), x = ldexpf(ds, -by);
+  const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -w.lse)), ds = p * (dp - w.delta), x = ds * f;
   const int64_t at = (int64_t)qh * a.n_tok + tok;
   if (lane_id<3>() < 32) a.self[at] = p;
   else a.self[(int64_t)a.q_heads * a.n_tok + at] = ds;
@@ -173,8 +209,7 @@ __global__ void __launch_bounds__(256, (dq_waves<DH, DIRECT && TILES>)) shared_d
     w.lse = r < rows ? a.lse[stat] * kLog2e : kInf;
   }
   f32x16 dq[DH / 32] = {};
-  int by = 0;  // in fp16 dq stands at 2^-by
-  bool some = false;
+  Fit<T> fit(1 << kRaised);  // of dq
   auto meet = [&](int it, char (*now)[kBytes], char (*next)[kBytes]) {
     kl.store(now[0]);
     vl.store(now[1]);
@@ -187,7 +222,7 @@ __global__ void __launch_bounds__(256, (dq_waves<DH, DIRECT && TILES>)) shared_d
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
       if (32 * sub < n)
-        dq_meet<T, DH, false>(now[0], now[1], at, 32 * sub, n - 32 * sub, 0, 0, 0, w, c, dq, by, some);
+        dq_meet<T, DH, false>(now[0], now[1], at, 32 * sub, n - 32 * sub, 0, 0, 0, w, c, dq, fit);
   };
   // two tiles a turn, so that the buffers' places are constants
   for (int it = share.first; it < share.end; it += 2) {
@@ -201,7 +236,7 @@ __global__ void __launch_bounds__(256, (dq_waves<DH, DIRECT && TILES>)) shared_d
   if (split != share.count - 1) {
     // own tokens are met by the last workgroup of a row
   } else if constexpr (!TILES) {
-    dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
+    dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, fit.f);
   } else {
     typedef RegisterTile<T, DH, kRows, 256, 3> OwnTile;
     const typename OwnTile::Reads own_at;
@@ -225,23 +260,21 @@ __global__ void __launch_bounds__(256, (dq_waves<DH, DIRECT && TILES>)) shared_d
         add_odd_own<T, DH>(a, a.k, s.begin, kh, j0, min(j0 + kRows, end), lo, live ? row.tok : -1, true, dq);
       for (int sub = 0; sub < 2; ++sub)
         if (j0 + 32 * sub < end)
-          dq_meet<T, DH, true>(lds[0][0], lds[0][1], own_at, 32 * sub, 0, lo, row.tok, j0 + 32 * sub, w, c, dq, by,
-                               some, odd);
+          dq_meet<T, DH, true>(lds[0][0], lds[0][1], own_at, 32 * sub, 0, lo, row.tok, j0 + 32 * sub, w, c, dq, fit,
+                               odd);
     }
   }
   __syncthreads();  // the tiles are done with
   if (rw >= rows) return;
-  if constexpr (std::is_same<T, _Float16>::value) {
-    if (some) unfit(dq, by);
-  }
+  const float by = fit.back();
   const int64_t tok = s.begin + row.tok;
   if (splits > 1 && split == 0 && live && lane_id<3>() < 32) *part_count(a, splits, tok, h0 + row.g) = share.count;
   if (share.count > 1) {
     const EmbHeads to{part_of(a, split), 0, (int64_t)a.q_heads * a.dim, a.dim};
-    if (live) store_row<float, DH, 3>(to, tok, h0 + row.g, a.dim, dq, 1.f);
+    if (live) store_row<float, DH, 3>(to, tok, h0 + row.g, a.dim, dq, by);
     return;
   }
-  PackedRows<T, DH, Tile, 3>::store(a, a.dq, s.begin, h0, rw, rows, lds[1][wave >> 1], part0, dq, a.scale);
+  PackedRows<T, DH, Tile, 3>::store(a, a.dq, s.begin, h0, rw, rows, lds[1][wave >> 1], part0, dq, by * a.scale);
 }
 
 // 32 rows a workgroup, where a request has few: its four waves take tiles of 32 keys in turn, and their sums meet
@@ -306,8 +339,7 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
     w.lse = r < rows ? a.lse[stat] * kLog2e : kInf;
   }
   f32x16 dq[DH / 32] = {};
-  int by = 0;
-  bool some = false;
+  Fit<T> fit(1 << kRaised);
   for (; it < share.end; it += kWaves) {
 #pragma unroll
     for (int n = 0; n < kRegs; ++n) {
@@ -317,7 +349,7 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
     }
     if (it + kWaves < share.end) load(it + kWaves);
     WaveRows<T, DH, Tile>::wave_sync();
-    dq_meet<T, DH, false>(kt, vt, at, 0, tiles.end(it) - tiles.key0(it), 0, 0, 0, w, c, dq, by, some);
+    dq_meet<T, DH, false>(kt, vt, at, 0, tiles.end(it) - tiles.key0(it), 0, 0, 0, w, c, dq, fit);
     WaveRows<T, DH, Tile>::wave_sync();
   }
   const int r = r0 + (lane_id<3>() & 31);
@@ -326,7 +358,7 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
   if (split != share.count - 1) {
     // own tokens are met by the last workgroup of a row
   } else if constexpr (!TILES) {
-    if (wave == 0) dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, by);
+    if (wave == 0) dq_self<T, DH>(a, s.begin + row.tok, kh, h0 + row.g, live, w, c, dq, fit.f);
   } else {
     typedef WaveRows<T, DH, Tile, 3> OwnRows;
     const typename RegisterTile<T, DH, 32, 64, 3>::Reads own_at;
@@ -351,12 +383,10 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
       odd = __any(odd);
       if (odd)
         add_odd_own<T, DH>(a, a.k, s.begin, kh, j0, min(j0 + 32, end), lo, live ? row.tok : -1, true, dq);
-      dq_meet<T, DH, true>(kt, vt, own_at, 0, 0, lo, row.tok, j0, w, c, dq, by, some, odd);
+      dq_meet<T, DH, true>(kt, vt, own_at, 0, 0, lo, row.tok, j0, w, c, dq, fit, odd);
     }
   }
-  if constexpr (std::is_same<T, _Float16>::value) {
-    if (some) unfit(dq, by);
-  }
+  const float by = fit.back();
   // the waves meet, as in the forward
   static_assert(sizeof(lds[0]) >= sizeof(float) * 32 * DH, "a wave's sums take its tiles' place");
   f32x4* mine = reinterpret_cast<f32x4*>(lds[wave]);
@@ -365,7 +395,7 @@ __global__ void __launch_bounds__(256, 2) shared_dq_few(SharedArgs a, int splits
   for (int x = 0; x < DH / 8; ++x) {
     const f32x16 t = dq[x >> 2];
     const int e = (x & 3) * 4;
-    mine[x * 64 + lane] = f32x4{t[e], t[e + 1], t[e + 2], t[e + 3]};
+    mine[x * 64 + lane] = f32x4{t[e] * by, t[e + 1] * by, t[e + 2] * by, t[e + 3] * by};
   }
   __syncthreads();
 #pragma unroll
@@ -500,18 +530,18 @@ struct DkvTiles {
   }
 };
 
-// Adds the sums of the upper half of eight waves to those of the lower half, through LDS.
+// Adds the sums of the upper half of eight waves to those of the lower half, through LDS; each times its `by`.
 template <int N>
-__device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave) {
+__device__ __forceinline__ void fold_waves(f32x16 (&x)[N], float* lds, int wave, float by) {
   __syncthreads();
   if (wave >= 4) {
 #pragma unroll
-    for (int k = 0; k < N * 16; ++k) lds[((wave - 4) * N * 16 + k) * 64 + lane_id()] = x[k >> 4][k & 15];
+    for (int k = 0; k < N * 16; ++k) lds[((wave - 4) * N * 16 + k) * 64 + lane_id()] = x[k >> 4][k & 15] * by;
   }
   __syncthreads();
   if (wave < 4) {
 #pragma unroll
-    for (int k = 0; k < N * 16; ++k) x[k >> 4][k & 15] += lds[(wave * N * 16 + k) * 64 + lane_id()];
+    for (int k = 0; k < N * 16; ++k) x[k >> 4][k & 15] = fmaf(x[k >> 4][k & 15], by, lds[(wave * N * 16 + k) * 64 + lane_id()]);
   }
 }
 
@@ -568,12 +598,11 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
   }
   const float c = a.scale * kLog2e;
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
-  int by = 0;  // in fp16 dk stands at 2^-by
-  bool some = false;
+  Fit<T> fit(1.f);  // of dk, beside the probabilities'
   for (int r0 = 0, b = 0; r0 < rows; r0 += kRows, b ^= 1) {
     ql.store(sh.q[b]);
     dl.store(sh.d[b]);
-    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat * kLog2e;
+    if (threadIdx.x < kRows) sh.lse[b][threadIdx.x] = stat * kLog2e - kRaisedP<T>;
     else if (threadIdx.x < 2 * kRows) sh.delta[b][threadIdx.x - kRows] = stat;
     if (!DIRECT && r0 + kRows < rows) load(b ^ 1, r0 + kRows);
     Tile::arrived();
@@ -608,10 +637,10 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           p[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -lse[e]));
-          ds[4 * g + e] = p[4 * g + e] * (dp[4 * g + e] - delta[e]);
+          ds[4 * g + e] = p[4 * g + e] * (dp[4 * g + e] - delta[e]) * (Fit<T>::kOn ? fit.f : 1.f);
         }
       }
-      fit_if<T>(ds, dk, by, some);
+      fit.look(ds, dk);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const V8 pb = right_of<T>(p, 8 * x), dsb = right_of<T>(ds, 8 * x);
@@ -623,15 +652,14 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
       }
     }
   }
-  if constexpr (std::is_same<T, _Float16>::value) {
-    if (some) unfit(dk, by);
-  }
+  float by = fit.back(kRaisedP<T>);
   Tile::arrived();  // of keys that no row met
   if (P::kWide) {
     float* fold = reinterpret_cast<float*>(sh.q);
     static_assert(!P::kWide || sizeof(sh.q) + sizeof(sh.d) >= sizeof(float) * 4 * 32 * DH, "room to fold");
-    fold_waves(dk, fold, wave);
-    fold_waves(dv, fold, wave);
+    fold_waves(dk, fold, wave, by);
+    fold_waves(dv, fold, wave, 1.f);
+    by = 1.f;
   } else {
     __syncthreads();  // the tiles are done with
   }
@@ -641,8 +669,8 @@ __device__ __forceinline__ void dkv(const SharedArgs& a, DkvTiles<T, DH, DIRECT>
 #pragma unroll
     for (int db = 0; db < DH / 32; ++db) dk[db] = dv[db] = f32x16{};
   }
-  Rows::store(a.dhk, hist.row + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dk, a.scale, 0);
-  Rows::store(a.dhv, hist.row + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dv, 1.f, 0);
+  Rows::store(a.dhk, hist.row + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dk, by * a.scale, 0);
+  Rows::store(a.dhv, hist.row + jw, kh, j1 - jw, a.dim, sh.part(wave), 32 * (wave & 1), dv, 1.f / (1 << kRaisedP<T>), 0);
 }
 
 struct HistoryBatch {  // of find_tile
@@ -694,7 +722,7 @@ __device__ __forceinline__ void dkv_own(const SharedArgs& a, OwnTiles<T, DH>& sh
     if (r < rows) {
       const Row x = row_at(a, r);
       const int64_t stat = (int64_t)(h0 + x.g) * a.n_tok + s.begin + x.tok;
-      lse = a.lse[stat] * kLog2e;
+      lse = a.lse[stat] * kLog2e - kRaisedP<T>;
       delta = a.delta[stat];
       tok = x.tok;
       first = first_of(a, s, x.tok);
@@ -710,8 +738,7 @@ __device__ __forceinline__ void dkv_own(const SharedArgs& a, OwnTiles<T, DH>& sh
   }
   const float c = a.scale * kLog2e;
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
-  int by = 0;
-  bool some = false;
+  Fit<T> fit(1.f);
   // the next step's rows are not loaded ahead: most have one or two, and there is no register over
   for (int r0 = j0 * a.group; r0 < rows; r0 += 32) {
     load(r0);
@@ -758,10 +785,10 @@ __device__ __forceinline__ void dkv_own(const SharedArgs& a, OwnTiles<T, DH>& sh
         const float x = __builtin_amdgcn_exp2f(fmaf(sc[4 * g + e], c, -l4[e]));
         const bool seen = j >= f4[e] && j <= t4[e];
         p[4 * g + e] = seen ? x : 0.f;
-        ds[4 * g + e] = seen ? x * (dp[4 * g + e] - d4[e]) : 0.f;
+        ds[4 * g + e] = seen ? x * (dp[4 * g + e] - d4[e]) * (Fit<T>::kOn ? fit.f : 1.f) : 0.f;
       }
     }
-    fit_if<T>(ds, dk, by, some);
+    fit.look(ds, dk);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const V8 pb = right_of<T>(p, 8 * x), dsb = right_of<T>(ds, 8 * x);
@@ -772,11 +799,8 @@ __device__ __forceinline__ void dkv_own(const SharedArgs& a, OwnTiles<T, DH>& sh
       }
     }
   }
-  if constexpr (std::is_same<T, _Float16>::value) {
-    if (some) unfit(dk, by);
-  }
-  Rows::W::store(a.dk, s.begin + j0, kh, j1 - j0, a.dim, lds[0], 0, dk, a.scale, 0);
-  Rows::W::store(a.dv, s.begin + j0, kh, j1 - j0, a.dim, lds[1], 0, dv, 1.f, 0);
+  Rows::W::store(a.dk, s.begin + j0, kh, j1 - j0, a.dim, lds[0], 0, dk, fit.back(kRaisedP<T>) * a.scale, 0);
+  Rows::W::store(a.dv, s.begin + j0, kh, j1 - j0, a.dim, lds[1], 0, dv, 1.f / (1 << kRaisedP<T>), 0);
 }
 
 // TILES: the first own_blocks workgroups have own tokens, each wave 32 of its own; one launch, so that those, which

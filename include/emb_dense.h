@@ -181,7 +181,8 @@ int attn_shared_fwd(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k, cons
 /*
  * The backward: gradients with respect to q, k, v and the history, from the forward's inputs, out and lse and the
  * gradient of out.  The history's are summed over the request's tokens and the query heads that share a head; events
- * that no token sees get zeros.  In EMB_F16 gradients of scores over 65504 do no harm.
+ * that no token sees get zeros.  In EMB_F16 score gradients are brought to where 16 bits hold them, so that neither those
+ * over 65504 nor small ones (of a small dout, or many events) cost the results bits that these have.
  * d_ws (16-byte aligned): at least attn_shared_bwd_workspace_bytes (EMB_ENOSPACE otherwise).
  */
 int attn_shared_bwd_workspace_bytes(const EmbAttn* a, int64_t n_seq, int64_t n_tok, int64_t n_hist, size_t* bytes);

@@ -838,3 +838,55 @@ def test_gradients_beside_an_own_score_of_minus_infinity(d, hq, dtype, c, h):
     want[0][..., 5].masked_fill_(odd[:, None], 0)
     for name, x, w, b in zip(NAMES, got, want, bound):
         within(x, w, b * (1 + u) + u * w.abs() + tiny, name)
+
+
+@pytest.mark.parametrize("grow", [2.0 ** -10, 2.0 ** -14, 2.0 ** -18])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("c,tokens", [([20], 1), ([20], 3), ([300], 1), ([300], 50)])
+def test_small_gradients_of_scores_in_fp16(c, tokens, d, grow):
+    """Of thousands of events and a small dout they lie at 2^-19, 2^-23 and 2^-27, where fp16 has few bits left or none, and
+    results where it has more."""
+    h = [4000]
+    q, k, v, kh, vh = inputs(c, h, 2, 1, d, F16)
+    q, k, kh, scale = q * 2.0 ** -8, k * 2.0 ** -8, kh * 2.0 ** -8, 2.0 ** 20 / d
+    args = q, k, v, kh, vh, offsets(c), candidates(c, tokens), offsets(h), BIG, 0, scale
+    out, lse = fwd(*args)
+    dout = rand(*out.shape, dtype=F16, seed=5) * grow
+    # Gradients are linear in dout, and the bounds of those of one `more` times as large allow for 2^-25 lost of a score's
+    # gradient.  Standing at 2^12, one loses 2^-37; where a row's largest, or a key's, is below 2^-6 there all are brought
+    # to a largest of 2^8, and lose 2^-33 of one below 2^-18.
+    more = 2.0 ** 12
+    want, bound = O.attn_shared_bwd(*args, out, lse, dout.double() * more)
+    got = bwd(*args, out, lse, dout)
+    for i, (name, g, w, b) in enumerate(zip(NAMES, got, want, bound)):
+        w, b = w / more, b / more
+        if i == 0 or i == 3 and grow > 2.0 ** -18:
+            assert w.abs().max() > 2.0 ** -14, name  # past fp16's lower end there is nothing to see
+        within(g, w, b + O.TINY[F16], name)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("c,tokens", [([300], 1), ([40, 30], 3)])
+def test_small_probabilities_in_fp16(c, tokens, d):
+    """60000 events of equal weight: each probability is rounded the same way, and a sum of them is off by as much."""
+    h = [60000] + [40000] * (len(c) - 1)
+    q, k, v, kh, vh = inputs(c, h, 1, 1, d, F16)
+    q = torch.zeros_like(q)
+    args = q, k, v, kh, vh, offsets(c), candidates(c, tokens), offsets(h), BIG, 0, 0.2
+    out, lse = fwd(*args)
+    dout = torch.full_like(out, 64)
+    got = bwd(*args, out, lse, dout)
+    for own in (2, 4):
+        for s, (n, m) in enumerate(zip(c, h)):
+            if own == 4:
+                total, at = n / (m + 1), slice(sum(h[:s]), sum(h[:s + 1]))
+                if tokens > 1:  # a candidate's tokens see one, two, ... of its own
+                    first = candidates(c, tokens)[sum(c[:s]):sum(c[:s + 1])] - sum(c[:s])
+                    total = (1 / (m + 1 + torch.arange(n, device="cuda") - first).double()).sum().item()
+                # a rounding of each probability, of the result, and fp32's of the exponent, at most about 16 + 15, and sums
+                rel = 2.0 ** -11 * 2 + (2 * 32 + 64 + n) * O.F32
+                err = (got[4][at].double() / 64 - total).abs().max().item()
+                assert err <= rel * total, (d, err / total)
+            elif tokens == 1:
+                err = (got[2][sum(c[:s]):sum(c[:s + 1])].double() / 64 - 1 / (m + 1)).abs().max().item()
+                assert err <= (2.0 ** -11 + 256 * O.F32) / (m + 1), (d, err * (m + 1))
