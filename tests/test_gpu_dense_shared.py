@@ -890,3 +890,60 @@ def test_small_probabilities_in_fp16(c, tokens, d):
             elif tokens == 1:
                 err = (got[2][sum(c[:s]):sum(c[:s + 1])].double() / 64 - 1 / (m + 1)).abs().max().item()
                 assert err <= (2.0 ** -11 + 256 * O.F32) / (m + 1), (d, err * (m + 1))
+
+
+# requests whose keys are shared out, more of them than are sorted: by 128 rows a workgroup, and by 32
+@pytest.mark.parametrize("c,h,hq,hk,d,tokens", [(140, 6000, 2, 1, 64, 1), (140, 6000, 1, 1, 128, 5), (3, 4000, 2, 1, 64, 1),
+                                                (4, 3000, 3, 1, 32, 2)])
+@pytest.mark.parametrize("n", [65, 100])
+def test_many_requests_whose_keys_are_shared_out(n, c, h, hq, hk, d, tokens):
+    gen = torch.Generator().manual_seed(n + c)
+    c, h = (torch.randint(0, x + 1, (n,), generator=gen).tolist() for x in (c, h))
+    c[0], c[-1], h[1], window, sinks, scale = 0, 0, 0, 2500, 3, 1.3 * d ** -0.5
+    q, k, v, kh, vh = inputs([sum(c) + 5], h, hq, hk, d, BF16)  # tokens of no request behind the last
+    off, hoff, first = offsets(c), offsets(h), candidates(c + [5], tokens)
+    m = sum(c)
+    for f in (dense.attn_shared_fwd_workspace_bytes, dense.attn_shared_cache_workspace_bytes):
+        assert f(m + 5, n, sum(h) if f is dense.attn_shared_fwd_workspace_bytes else max(h), hq, hk, d) > 0
+    rest = off, first, hoff, window, sinks, scale
+    out, lse = fwd(q, k, v, kh, vh, *rest)
+    assert (out[m:] == 7).all() and (lse[:, m:] == 7).all()
+    cut = q[:m], k[:m], v[:m], kh, vh, off, None if first is None else first[:m], *rest[2:]
+    o, l, bo, bl = O.attn_shared_fwd(*cut)
+    within(out[:m], o, bo, "out")
+    within(lse[:, :m], l, bl, "lse")
+    dout = rand(m + 5, hq, d, dtype=BF16, seed=9)
+    want, bound = O.attn_shared_bwd(*cut, out[:m], lse[:, :m], dout[:m])
+    for name, g, w, b in zip(NAMES, bwd(q, k, v, kh, vh, *rest, out, lse, dout), want, bound):
+        assert (g[w.shape[0]:] == 7).all()
+        within(g[:w.shape[0]], w, b, name)
+    # against caches, in 16 bits and in 8
+    cap, lens = max(h), torch.tensor(h, dtype=torch.int32, device="cuda")
+    nb, got = dense.attn_shared_cache_workspace_bytes(m + 5, n, cap, hq, hk, d), torch.full_like(out, 7)
+    ws = workspace(nb)
+    dense.attn_shared_cache(q, k, v, cached(kh, h, cap), cached(vh, h, cap), off, first, lens, window, sinks, scale, got, ws[:nb])
+    assert (ws[nb:] == 0xFF).all() and (got[m:] == 7).all()
+    within(got[:m], o, bo, "out from caches")
+    cache = [torch.full((n, cap, hk, d) if x % 2 == 0 else (n, hk, cap), 0x7F, dtype=U8, device="cuda") for x in range(4)]
+    dense.cache_q8_write(kh, vh, hoff, None, *cache)
+    kv, vv = (O.values_of(*O.quantise(x)).to(BF16) for x in (kh, vh))
+    o, _, bo, _ = O.attn_shared_fwd(*cut[:3], kv, vv, *cut[5:])
+    ws = workspace(nb)
+    dense.attn_shared_cache_q8(q, k, v, *cache, off, first, lens, window, sinks, scale, got, ws[:nb])
+    assert (ws[nb:] == 0xFF).all() and (got[m:] == 7).all()
+    within(got[:m], o, bo, "out from 8 bits")
+
+
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("c,pad", [(20, 3), (600, 40)])
+def test_shared_out_backward_with_rows_behind_the_last(c, pad, tokens):
+    q, k, v, kh, vh = inputs([c + pad], [9000], 4, 2, 64, F16)
+    first = candidates([c, pad], tokens)
+    rest = offsets([c]), first, offsets([9000]), BIG, 0, 0.125
+    out, lse = fwd(q, k, v, kh, vh, *rest)
+    dout = rand(c + pad, 4, 64, dtype=F16, seed=9)
+    cut = q[:c], k[:c], v[:c], kh, vh, rest[0], None if first is None else first[:c], *rest[2:]
+    want, bound = O.attn_shared_bwd(*cut, out[:c], lse[:, :c], dout[:c])
+    for name, g, w, b in zip(NAMES, bwd(q, k, v, kh, vh, *rest, out, lse, dout), want, bound):
+        assert (g[w.shape[0]:] == 7).all()
+        within(g[:w.shape[0]], w, b, name)
