@@ -207,6 +207,19 @@ def new_cache(n_seq: int, capacity: int):
     return codes[0], exps[0], codes[1], exps[1]
 
 
+def history_cache(k, v, offsets):
+    """An 8-bit cache of whole histories, written at once but for the newest events, which follow."""
+    lens = offsets[1:] - offsets[:-1]
+    cache = new_cache(lens.numel(), int(lens.max()))
+    last = (offsets[1:] - 1).long()
+    older = torch.ones(k.shape[0], dtype=torch.bool, device=DEV)
+    older[last] = False
+    dense.cache_q8_write(k[older], v[older], offsets - torch.arange(offsets.numel(), dtype=torch.int32, device=DEV), None,
+                         *cache)
+    dense.cache_q8_write(k[last], v[last], None, lens - 1, *cache)
+    return cache
+
+
 def batch(rng, values, window: int, n_seq: int = 64, longest: int = 100):
     lens = rng.integers(2, longest, n_seq)
     off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
@@ -268,12 +281,8 @@ def main(argv=None):
     worst = (served.float() - o[last].float()).abs().max().item()
     print(f"newest events from the cache differ from the whole forward by at most {worst:.2g}", flush=True)
 
-    # the same caches in 8 bits: histories written at once but for the newest events, which follow
-    cache = new_cache(lens.numel(), cap)
-    older = torch.ones(k.shape[0], dtype=torch.bool, device=DEV)
-    older[last] = False
-    dense.cache_q8_write(k[older], v[older], off - torch.arange(off.numel(), dtype=torch.int32, device=DEV), None, *cache)
-    dense.cache_q8_write(k[last], v[last], None, lens - 1, *cache)
+    # the same caches in 8 bits
+    cache = history_cache(k, v, off)
     served = m.serve_q8(cache, lens, q[last].contiguous())
     apart = (served.float() - o[last].float()).abs().max().item()
     print(f"from the cache in 8 bits by at most {apart:.2g}", flush=True)
