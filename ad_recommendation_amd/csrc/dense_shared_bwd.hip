@@ -40,14 +40,14 @@ struct Fit {
       float top = 0.f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
+      top = swap32_max(top);  // both lanes decide by the same
       set |= top >= kLeast;
       if (__builtin_expect(__any(top > 65504.f || (!set && top > 0.f)), 0)) move(x, sums, top);
     }
   }
   template <int N>
   __device__ __forceinline__ void move(f32x16& x, f32x16 (&sums)[N], float top) {
-    top = fminf(swap32_max(top), 0x1p127f);  // of what is not finite the sums are not either
-    set |= top >= kLeast;
+    top = fminf(top, 0x1p127f);  // of what is not finite the sums are not either
     // not past 2^64, so that f times any product of fp16's numbers is finite
     const int most = 65 - __builtin_amdgcn_frexp_expf(f), to = 9 - __builtin_amdgcn_frexp_expf(top);
     const float by = top > 65504.f || (!set && top > 0.f) ? ldexpf(1.f, min(to, most)) : 1.f;

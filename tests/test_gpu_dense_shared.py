@@ -947,3 +947,30 @@ def test_shared_out_backward_with_rows_behind_the_last(c, pad, tokens):
     for name, g, w, b in zip(NAMES, bwd(q, k, v, kh, vh, *rest, out, lse, dout), want, bound):
         assert (g[w.shape[0]:] == 7).all()
         within(g[:w.shape[0]], w, b, name)
+
+
+@pytest.mark.parametrize("d,hq,hk", [(32, 2, 2), (64, 2, 1), (128, 4, 2)])
+@pytest.mark.parametrize("c,h,tokens", [([20], [900], 1), ([20], [900], 3), ([300, 40], [700, 90], 1), ([300, 40], [700, 90], 3),
+                                        ([12, 40, 0, 25], [300, 90, 7, 0], 3), ([150], [64], 50), ([150, 90], [3, 2], 3)])
+@pytest.mark.parametrize("few", [False, True])
+def test_score_gradients_of_many_magnitudes_in_fp16(c, h, tokens, few, d, hq, hk):
+    """Tokens' douts from 2^-3 down to 2^-17, in any order, and weights from one to e^-20: large and small ones come one
+    after the other for each query and each key.  few: every 32nd token's alone is small, which other tiles' rows meet
+    among large ones."""
+    q, k, v, kh, vh = inputs(c, h, hq, hk, d, F16)
+    args = q, k, v, kh, vh, offsets(c), candidates(c, tokens), offsets(h), BIG, 0, 4 * d ** -0.5
+    out, lse = fwd(*args)
+    gen = torch.Generator(device="cuda").manual_seed(d + len(c))
+    down = torch.randint(3, 18, (sum(c), 1, 1), generator=gen, device="cuda")
+    if few:
+        down = torch.where(torch.arange(sum(c), device="cuda") % 32 == 0, 17, 3)[:, None, None]
+    dout = (rand(*out.shape, dtype=torch.float32, seed=5) * 0.5 ** down).half()
+    # as above: standing at 2^12 at least a score's gradient loses 2^-37, while none is past 16, where they would move down
+    more = 2.0 ** 12
+    want, bound = O.attn_shared_bwd(*args, out, lse, dout.double() * more)
+    for t, _, i, _, see, qq, kk, vv in O._requests(*args[:9], 0):
+        p = torch.exp(qq @ kk.T * args[10] - lse[i, t].double()[:, None]).masked_fill(~see, 0.0)
+        do = dout[t, i].double()
+        assert (p * (do @ vv.T - (do * out[t, i].double()).sum(1, keepdim=True))).abs().max() < 16
+    for name, g, w, b in zip(NAMES, bwd(*args, out, lse, dout), want, bound):
+        within(g, w / more, b / more + O.TINY[F16], name)
