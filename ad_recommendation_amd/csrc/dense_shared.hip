@@ -48,14 +48,15 @@ __device__ __forceinline__ void soften(f32x16 (&sc)[N], f32x16 (&o)[DB], float& 
 // history and share no address with it (AGAIN, see lane_id), so that it keeps its registers.
 //
 // A token alone: its score and value on the vector unit, so nothing that is not finite reaches another row.  A
-// score of minus infinity has no weight beside others; one that is not finite otherwise makes the sum NaN.
+// score of minus infinity has a weight of 0; one that is not finite otherwise makes the sum NaN.
 template <typename T, int DH>
 __device__ __forceinline__ void meet_self(const SharedArgs& a, int64_t tok, int kh, bool live,
                                           const typename Vec8<T>::t (&q)[DH / 16], float c, f32x16 (&o)[DH / 32],
                                           float& m, float& l) {
   const float s = dot_row<T, DH>(q, static_cast<const T*>(a.k.p) + tok * a.k.tok + kh * a.k.head, live, a.dim);
-  if (!live || s == -kInf) return;
-  const float mn = fmaxf(m, s), by = m == -kInf ? 0.f : exp2f((m - mn) * c), p = exp2f((s - mn) * c);
+  if (!live) return;
+  const float mn = fmaxf(m, s), by = m == -kInf ? 0.f : exp2f((m - mn) * c);
+  const float p = s == -kInf ? 0.f : exp2f((s - mn) * c);
   m = mn;
   l = l * by + (lane_id<3>() < 32 ? p : 0.f);
   typedef T V __attribute__((ext_vector_type(4)));

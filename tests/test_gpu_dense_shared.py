@@ -974,3 +974,29 @@ def test_score_gradients_of_many_magnitudes_in_fp16(c, h, tokens, few, d, hq, hk
         assert (p * (do @ vv.T - (do * out[t, i].double()).sum(1, keepdim=True))).abs().max() < 16
     for name, g, w, b in zip(NAMES, bwd(*args, out, lse, dout), want, bound):
         within(g, w / more, b / more + O.TINY[F16], name)
+
+
+@pytest.mark.parametrize("c,h", [([12, 8], [90, 130]), ([160, 140], [90, 230])])
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_value_that_is_not_finite_shows_beside_a_score_of_minus_infinity(bad, tokens, c, h):
+    """0 times it is NaN, of an own token as of an event of the history; other columns do not change."""
+    q, k, v, kh, vh = (x.contiguous() for x in inputs(c, h, 2, 1, 64, F16))
+    q[..., 5] = 1
+    own, event = c[0] + 4, h[0] + 3
+    k[own, 0, 5] = kh[event, 0, 5] = -float("inf")
+    off, hoff, first = offsets(c), offsets(h), candidates(c, tokens)
+    rest = off, first, hoff, BIG, 0, 0.2
+    want, lse = fwd(q, k, v, kh, vh, *rest)
+    assert want.isfinite().all() and lse.isfinite().all()
+    rows = torch.arange(sum(c), device="cuda")
+    start = rows if first is None else first.long()
+    for x, at, seeing in ((v, own, (start == start[own]) & (rows >= own)), (vh, event, rows >= c[0])):
+        keep = x[at, 0, 7].clone()
+        x[at, 0, 7] = bad
+        got, l = fwd(q, k, v, kh, vh, *rest)
+        assert not got[seeing][..., 7].isfinite().any()
+        got[..., 7].masked_fill_(seeing[:, None], 0)
+        assert torch.equal(got, torch.where(seeing[:, None, None] & (torch.arange(64, device="cuda") == 7), 0, want))
+        assert torch.equal(l, lse)
+        x[at, 0, 7] = keep
