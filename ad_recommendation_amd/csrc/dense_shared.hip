@@ -95,7 +95,7 @@ __device__ __forceinline__ void meet_own(const char* kt, const char* vt, const R
 enum { kByRegisters, kDirect, kCodes };  // how tiles of history get to LDS
 
 // Tiles of keys or values in 8 bits through registers: codes are converted on their way to LDS.  8 bytes a load, so that
-// a load is one piece of LDS: with 16, whose two pieces meet others in their banks, 64 requests 292 us instead of 278.
+// a load is one piece of LDS: with 16, whose two pieces meet others in their banks, 64 requests take 5 % longer.
 template <typename T, int DH, int ROWS, int THREADS>
 struct CodesTile : RegisterTile<T, DH, ROWS, THREADS> {
   typedef RegisterTile<T, DH, ROWS, THREADS> R;
@@ -138,9 +138,9 @@ template <int DH>
 constexpr int wide_waves = DH == 128 ? 2 : DH == 64 ? 3 : 4;
 
 // Bound by matrix cores and the vector unit (exponentials), each busy 48 % of the time, and the clock, which falls to 1.9
-// GHz: 16 caches of up to 8192, 1000 candidates, 16 and 4 heads of 128, bf16: 338 us, 930 TFLOP/s.  (Eight waves of 256
+// GHz: 16 caches of up to 8192, 1000 candidates, 16 and 4 heads of 128, bf16: 340 us, 930 TFLOP/s.  (Eight waves of 256
 // rows, halves of which take products and exponentials in turn: 406 us.)  In 8 bits the conversion of codes is nearly as
-// much vector work again: 64 of up to 8192, 200 candidates, window 4096: 286 us, 680 TFLOP/s, matrix cores busy 31 %.
+// much vector work again: 64 of up to 8192, 200 candidates, window 4096: 284 us, 685 TFLOP/s, matrix cores busy 31 %.
 template <typename T, int DH, int HOW>
 __global__ void __launch_bounds__(256, wide_waves<DH>) shared_wide(SharedArgs a, int splits, int unit) {
   typedef typename Vec8<T>::t V8;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(256, wide_waves<DH>) shared_wide(SharedArgs a,
   f32x16 o[DH / 32] = {};
   float m = -kInf, l = 0.f;  // the maximum that o and l stand at; this lane's half of the sum
   // Tiles through registers are stored while the one before is computed, between its scores and its
-  // probabilities (64 requests in 8 bits: 275 us; before the barrier, when nothing else is done, 279).
+  // probabilities (before the barrier, when nothing else is done, 64 requests in 8 bits take 1.5 % longer).
   auto store = [&](int it, char (*to)[kBytes]) {
     if (HOW == kDirect || it >= it1) return;
     kl.store(to[0]);
@@ -652,9 +652,10 @@ int64_t slots(const SharedArgs& a, int rows) {
 
 // How a request's keys are shared out.  us as in by_32_rows().  Of 32 rows, many waves a workgroup rather than a
 // second launch while each has few tiles (1 request of 64 candidates, 1000: 11.2; with a join 12.5).  Of 128 rows, for
-// about 400 workgroups (16 packed histories of up to 6000, 30 candidates, 8 heads of 64: 32; in one part each 93), of
-// 8 tiles at least, 16 where there are many already (12 of up to 5000, 200 candidates, 16 and 4 heads of 64: 46; 8 tiles
-// 54, one part 82).
+// about 400 workgroups (16 packed histories of up to 6000, 30 candidates, 8 heads of 64: 32; in one part each 93; 350, 450
+// and 500 are 2.5 % better than 400 in the mean of 16 batches, and up to 20 % better or worse in each), of 8 tiles at least
+// (with fewer what the parts write passes 8 MB sooner, and the join takes its longer way: see join_eager()), 16 where there
+// are many already (12 of up to 5000, 200 candidates, 16 and 4 heads of 64: 46; 8 tiles 54, one part 82).
 SharedPlan plan_shared(const EmbAttn& a, int64_t n_seq, int64_t n_tok, int64_t hist, int64_t most, bool one) {
   n_seq = std::max<int64_t>(n_seq, 1);
   const int64_t group = a.q_heads / a.kv_heads, seen = (int64_t)a.window + a.sinks;

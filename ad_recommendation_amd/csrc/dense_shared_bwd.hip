@@ -157,7 +157,7 @@ constexpr int dq_waves = DH == 128 ? 2 : DH == 64 && !LEAN ? 3 : 4;
 
 // 128 rows a workgroup, 32 a wave, tiles of 64 keys in LDS, as in the forward.  8 requests of up to 512 candidates and
 // 4095 events, 16 and 8 heads of 128, bf16: 95 us, matrix cores busy 35 % of the time; 200 of up to 120 tokens and 500
-// events, 8 heads of 64, fp16: 72 us for 197 MB, each workgroup's loads one after the other.
+// events, 8 heads of 64, fp16: 68 us for 197 MB, each workgroup's loads one after the other.
 template <typename T, int DH, bool DIRECT, bool TILES>
 __global__ void __launch_bounds__(256, (dq_waves<DH, DIRECT && TILES>)) shared_dq(SharedArgs a, int splits, int unit) {
   typedef TileOf<T, DH, 64, 256, DIRECT> Tile;

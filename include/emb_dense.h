@@ -67,7 +67,8 @@ typedef struct {
  *   d_lse : nullable; fp32 [q_heads][n_tok], what the backward reads.
  * A key or value that is not finite reaches only the queries that see it (and in the backward, a
  * query or gradient only the keys it sees).  Sums that are not finite, in EMB_F16 also those of score gradients
- * over 65504, are computed once more: such a call takes a few times as long.
+ * over 65504, are computed once more: such a call takes a few times as long.  In EMB_F16 score gradients, and the
+ * backward's probabilities, keep the bits that type has for them: fewer below 2^-14.
  * EMB_VALIDATE=1 checks the offsets first (it synchronises the stream); without it malformed
  * offsets give wrong results but no access outside the n_tok tokens.
  * Errors: EMB_EINVAL for a null pointer, a bad descriptor, alignment or stride; EMB_ERANGE for
@@ -153,9 +154,10 @@ int attn_window_decode_q8(const EmbAttn* a, const EmbHeads* q, const EmbHeads* k
  * candidate sees the history and its candidate's tokens up to itself; no candidate sees another.  A candidate
  * stands at the place after the history's n events: event j is seen when n - j < window or j < sinks, as the next
  * event of that sequence would see it in attn_window_fwd.  window and sinks say nothing about a candidate's own
- * tokens.  Otherwise as there: scores, softmax, heads that share keys, EmbAttn and its limits.  A score of minus
- * infinity weighs nothing beside others; where all that a row sees are, its out is NaN and its lse minus infinity, however
- * many workgroups share the keys.
+ * tokens: all of them see the same events, so under a window shorter than the history the later tokens of a candidate see
+ * a few events more than they would if the earlier ones had been appended to the sequence.  Otherwise as there: scores, softmax, heads that share keys, EmbAttn and its limits.  A score of minus
+ * infinity weighs nothing beside others, and 0 times a value that is not finite is NaN; where all that a row sees are such
+ * scores, its out is NaN and its lse minus infinity, however many workgroups share the keys.
  *
  * Requests are ragged: request s holds tokens d_offsets[s] to d_offsets[s + 1] - 1 of q, k and v (int32, ascending
  * from 0 to at most n_tok).  d_first (nullable: every token is a candidate of its own): int32 [n_tok], for each token the
